@@ -400,6 +400,210 @@ int fp8_linear_bwd_noalloc(const void* dY, int64_t M, int64_t N, int64_t K,
                            const fp8_recipe_t* recipe, const fp8_linear_state_t* state,
                            void* dX, float* dW, int accumulate_dW, void* stream);
 
+/* ------------------------------------------- between the linears of a block
+ *
+ * The operators that stand between the FP8 linears of a feed-forward or
+ * expert block: the norms around it with its gate and residual scale, the
+ * GEMM with activation and residual in its epilogue (dense, or one product
+ * per expert), and the sort of tokens by expert and back.  The conventions
+ * above hold.  Sums, statistics and everything else between an input and an
+ * output are FP32, each output is rounded once, and every sum runs in a fixed
+ * order: equal calls on one device give equal bits.  (The pages have no
+ * counterpart: they name these parts of a model as the ones kept out of FP8.)
+ * The structs are read during the call only. */
+
+typedef enum { FP8_NORM_RMS = 0, FP8_NORM_LAYER = 1 } fp8_norm_t;
+typedef enum {
+    FP8_ACT_NONE = 0,      /* z                                               */
+    FP8_ACT_RELU = 1,      /* max(z, 0)                                       */
+    FP8_ACT_SILU = 2,      /* z / (1 + exp(-z))                               */
+    FP8_ACT_GELU = 3,      /* z Phi(z)                                        */
+    FP8_ACT_GELU_TANH = 4  /* z/2 (1 + tanh(sqrt(2/pi)(z + 0.044715 z^3)))    */
+} fp8_act_t;
+
+/* The norms before and after a block, its gate and the residual scale:
+ *   p  = post_norm ? N(h; w_post, b_post) : h
+ *   x' = alpha x + gate * p
+ *   y  = N(x'; w_pre, b_pre)
+ *   N(v; w, b) = w (v - m) r + b, r = 1 / sqrt(mean((v - m)^2) + eps),
+ *   m = mean(v) (FP8_NORM_LAYER) or 0 (FP8_NORM_RMS, which takes no b). */
+typedef struct {
+    int64_t rows;          /* tokens, >= 0                                    */
+    int64_t width;         /* 1..16384, any; multiples of 8 move in 16-byte   */
+                           /*   pieces                                        */
+    int32_t kind;          /* fp8_norm_t, of both norms                       */
+    int32_t stream_type;   /* fp8_out_t of x and x_out                        */
+    float   eps;           /* >= 0                                            */
+    float   alpha;         /* the residual's scale                            */
+    const void* x;         /* [rows][width], nullable: 0                      */
+    const void* h;         /* [rows][width] bf16, nullable: x' = alpha x      */
+    const void* gate;      /* [gate_rows][width] bf16, nullable: 1            */
+    int64_t gate_rows;     /* divides rows: row r takes gate row r /          */
+                           /*   (rows / gate_rows) -- 1: a vector, rows: a    */
+                           /*   gate per token; 0 without a gate              */
+    int32_t post_norm;     /* 0 or 1                                          */
+    const float* w_post;   /* [width], nullable: 1                            */
+    const float* b_post;   /* [width], nullable: 0                            */
+    const float* w_pre;    /* [width], nullable: 1                            */
+    const float* b_pre;    /* [width], nullable: 0                            */
+    void* x_out;           /* [rows][width] x', nullable; may be x itself     */
+    void* y;               /* [rows][width] bf16, nullable                    */
+    uint8_t* q;            /* [rows][width] FP8 codes of y, nullable          */
+    int32_t q_format;      /* fp8_format_t                                    */
+    int32_t q_granularity; /* FP8_GRAN_TENSOR: codes of y * q_scale[0];       */
+                           /* FP8_GRAN_ROW: each row's own scale, by          */
+                           /*   fp8_quantize's per-row rule                   */
+    int32_t pow2;          /* per row: scales rounded down to powers of two   */
+    const float* q_scale;  /* [1] (FP8_GRAN_TENSOR)                           */
+    float* q_scale_inv;    /* [rows] 1 / scale (FP8_GRAN_ROW)                 */
+    float* amax;           /* [1] max|y|, nullable (FP8_GRAN_TENSOR)          */
+    float* stats;          /* [4][rows] m_post, r_post, m_pre, r_pre for the  */
+                           /*   backward pass, nullable; 0 where there is none*/
+} fp8_norm_fwd_args_t;
+
+/* The codes are those of the FP32 y, which is rounded once (a cast of the
+ * bf16 y would round twice). */
+int fp8_norm_fwd(const fp8_norm_fwd_args_t* args, void* stream);
+
+/* Gradients of fp8_norm_fwd.  dX = dx_out + (gradient of y through N) is the
+ * gradient of x'; dx = alpha dX; through the gate and the post norm it gives
+ * dh.  The gradients of vectors are FP32 sums over the rows (of a gate row's
+ * group), overwritten or, with accumulate, added to. */
+typedef struct {
+    int64_t rows, width;
+    int32_t kind, stream_type;
+    float   alpha;
+    const void* dy;        /* [rows][width] bf16, nullable: 0                 */
+    const void* x_out;     /* [rows][width] x' as the forward wrote it        */
+    const void* dx_out;    /* [rows][width] stream_type, the gradient that x' */
+                           /*   gets from its other use, nullable: 0          */
+    const void* h;         /* as in the forward                               */
+    const void* gate;
+    int64_t gate_rows;
+    int32_t post_norm;
+    const float* w_post;
+    const float* b_post;   /* read for dgate                                  */
+    const float* w_pre;
+    const float* stats;    /* [4][rows] of the forward                        */
+    void* dx;              /* [rows][width] stream_type, nullable; may be     */
+                           /*   dx_out itself                                 */
+    void* dh;              /* [rows][width] bf16, nullable                    */
+    float* dw_pre;         /* [width], each nullable                          */
+    float* db_pre;
+    float* dw_post;
+    float* db_post;
+    float* dgate;          /* [gate_rows][width], nullable                    */
+    int32_t accumulate;
+} fp8_norm_bwd_args_t;
+
+/* Bytes of workspace of fp8_norm_bwd on the current device (partial sums);
+ * gate_rows = 0 without a gate.  0 for arguments that the call refuses. */
+size_t fp8_norm_bwd_workspace_size(int64_t rows, int64_t width, int64_t gate_rows);
+int fp8_norm_bwd(const fp8_norm_bwd_args_t* args, void* workspace, size_t workspace_bytes,
+                 void* stream);
+
+/* FP8 GEMM with bias, activation and residual in its epilogue:
+ *   z[m][n] = sa sb sum_k A[m][k] B[n][k] + bias[n]
+ *   v = act(z), or gated: v[m][n] = act(z[m][n]) z[m][N + n] -- B's first N
+ *       rows are the gate's, the next N the up product's
+ *   D = v + residual
+ * with per-tensor or per-row factors as in fp8_gemm (block factors:
+ * FP8_ERR_UNSUPPORTED), K-contiguous operands.
+ * With `offsets` there is one product per expert: rows offsets[e] ..
+ * offsets[e + 1] of A (and of residual, z, d, q) take B's and bias's part e.
+ * The offsets are what fp8_moe_plan writes with an align that is a multiple
+ * of 32, in device memory; rows past offsets[experts] are left as they are
+ * (z, d, q) or unread. */
+typedef struct {
+    const uint8_t* A;      /* [M][K] codes, 16-byte aligned                   */
+    const uint8_t* B;      /* [experts][N or 2N][K] codes, 16-byte aligned    */
+    int32_t fa, fb;        /* fp8_format_t                                    */
+    int64_t M, N, K;       /* M >= 0; N, K positive multiples of 16           */
+    int32_t ga, gb;        /* FP8_GRAN_TENSOR: scale_inv_a[0], scale_inv_b    */
+                           /*   [experts]; FP8_GRAN_ROW: scale_inv_a [M],     */
+                           /*   scale_inv_b [experts][N or 2N]                */
+    const float* scale_inv_a;
+    const float* scale_inv_b;
+    int32_t act;           /* fp8_act_t                                       */
+    int32_t gated;         /* 0 or 1                                          */
+    const void* bias;      /* bf16 [experts][N or 2N], 16-byte aligned,       */
+                           /*   nullable                                      */
+    const void* residual;  /* bf16 [M][N], nullable                           */
+    void* z;               /* bf16 [M][N or 2N], for the backward pass,       */
+                           /*   nullable                                      */
+    void* d;               /* bf16 [M][N], nullable when q is set             */
+    uint8_t* q;            /* [M][N] codes of D * q_scale[0], nullable        */
+    int32_t q_format;
+    const float* q_scale;  /* [1], with q                                     */
+    float* amax;           /* [1] max|D| over the written rows, nullable,     */
+                           /*   with q                                        */
+    const int32_t* offsets;/* [experts + 1], nullable                         */
+    int32_t experts;       /* 1..256; 1 without offsets                       */
+} fp8_gemm_act_args_t;
+
+int fp8_gemm_act(const fp8_gemm_act_args_t* args, void* stream);
+
+/* Gradient of the epilogue, from z as the forward wrote it (the gradient of
+ * the residual is dD itself):
+ *   dz = dD act'(z); gated: dz_gate = dD z_up act'(z_gate), dz_up = dD act(z_gate)
+ * as bf16 and / or as FP8 codes of dz * q_scale[0] (for the dgrad and wgrad
+ * GEMMs), with the bias gradient dbias[n] (+)= sum_m dz[m][n].  ReLU's
+ * derivative at 0 is 0. */
+typedef struct {
+    int64_t M, N;          /* N a positive multiple of 16                     */
+    int32_t act, gated;
+    const void* dD;        /* bf16 [M][N]                                     */
+    const void* z;         /* bf16 [M][N or 2N]                               */
+    void* dz;              /* bf16 [M][N or 2N], nullable                     */
+    uint8_t* q;            /* [M][N or 2N], nullable                          */
+    int32_t q_format;
+    const float* q_scale;  /* [1], with q                                     */
+    float* amax;           /* [1] max|dz|, nullable, with q                   */
+    float* dbias;          /* FP32 [N or 2N], nullable                        */
+    int32_t accumulate;    /* add to dbias                                    */
+} fp8_act_bwd_args_t;
+
+/* Bytes of workspace that fp8_act_bwd needs for dbias. */
+size_t fp8_act_bwd_workspace_size(int64_t M, int64_t N, int gated);
+int fp8_act_bwd(const fp8_act_bwd_args_t* args, void* workspace, size_t workspace_bytes,
+                void* stream);
+
+/* Tokens sorted by expert.  ids [tokens][slots] holds each token's experts;
+ * an id outside 0..experts-1 is a dropped slot.  Expert e's rows are
+ * offsets[e] .. offsets[e] + counts[e], in the order of (token, slot), padded
+ * to a multiple of align up to offsets[e + 1].
+ *   offsets [experts + 1], counts [experts]
+ *   row_of  [tokens][slots]  the slot's row, or -1
+ *   src     [rows]           the row's token * slots + slot, or -1 (pad rows
+ *                            and rows past offsets[experts])
+ * rows: at least fp8_moe_rows(), which no routing exceeds.  experts 1..1024,
+ * slots 1..64, align 1..4096; tokens * slots and rows below 2^31. */
+int64_t fp8_moe_rows(int64_t tokens, int slots, int experts, int align);   /* -1: out of range */
+size_t fp8_moe_workspace_size(int64_t tokens, int slots, int experts);
+int fp8_moe_plan(const int32_t* ids, int64_t tokens, int slots, int experts, int align,
+                 int32_t* offsets, int32_t* counts, int32_t* row_of, int32_t* src, int64_t rows,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* xs[row_of[t][j]] = x[t], zeros in the rows without a source.  A row is
+ * row_bytes bytes of any type (bf16, FP32, FP8 codes); scale (nullable, with
+ * scale_s): one float a token (codes' per-row factors) that goes along. */
+int fp8_moe_permute(const void* x, const float* scale, int64_t tokens, int slots, int64_t row_bytes,
+                    const int32_t* row_of, const int32_t* src, int64_t rows, void* xs,
+                    float* scale_s, void* stream);
+
+/* y[t] = sum_j weights[t][j] ys[row_of[t][j]], j ascending; dropped slots add
+ * nothing.  weights NULL: 1, which is also the gradient of fp8_moe_permute.
+ * type: fp8_out_t of ys and y. */
+int fp8_moe_unpermute(const void* ys, int type, const int32_t* row_of, const float* weights,
+                      int64_t tokens, int slots, int64_t width, int64_t rows, void* y, void* stream);
+
+/* Gradient of fp8_moe_unpermute: dys[row_of[t][j]] = weights[t][j] dy[t],
+ * zeros in the rows without a source; dweights[t][j] = <dy[t], ys[row]>
+ * (nullable), 0 for a dropped slot. */
+int fp8_moe_unpermute_bwd(const void* dy, const void* ys, int type, const int32_t* row_of,
+                          const int32_t* src, const float* weights, int64_t tokens, int slots,
+                          int64_t width, int64_t rows, void* dys, float* dweights, void* stream);
+
 /* Message of the last failing call on this host thread ("" if none). */
 const char* fp8_last_error(void);
 

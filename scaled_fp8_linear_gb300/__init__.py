@@ -508,3 +508,10 @@ class Fp8Linear:
     def load_state_dict(self, sd: dict) -> None:
         for k, v in sd.items():
             getattr(self, k).copy_(v)
+
+
+# The operators between the linears (needs the names above).
+from . import block_ops as _block_ops   # noqa: E402
+from .block_ops import *                # noqa: E402,F401,F403
+
+__all__ += _block_ops.__all__

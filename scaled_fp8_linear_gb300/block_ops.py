@@ -1,0 +1,452 @@
+"""The operators between the FP8 linears of a feed-forward or expert block.
+
+Like the package's other calls these only marshal arguments to the C-ABI
+library (include/fp8linear.h has the formulas): outputs that are not given
+are allocated on the inputs' device, everything runs in the library's
+kernels on the current (or the given) stream.
+
+  fp8_norm_fwd, fp8_norm_bwd      norms before and after a block, gate, residual scale
+  fp8_gemm_act, fp8_act_bwd       FP8 GEMM with bias, activation and residual in its epilogue
+  fp8_moe_plan, fp8_moe_permute, fp8_moe_unpermute, fp8_moe_unpermute_bwd
+                                  tokens sorted by expert and back
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import (_U8, _check, _ptr, _stream, _vp, E4M3, GRAN_ROW, GRAN_TENSOR, OUT_BF16, OUT_F32)
+from . import lib as _base_lib
+
+__all__ = [
+    "NORM_RMS", "NORM_LAYER", "ACT_NONE", "ACT_RELU", "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH",
+    "NormFwd", "NormBwd", "GemmAct", "ActBwd", "MoePlan",
+    "fp8_norm_fwd", "fp8_norm_bwd", "fp8_norm_bwd_workspace_size", "fp8_gemm_act", "fp8_act_bwd",
+    "fp8_act_bwd_workspace_size", "fp8_moe_rows", "fp8_moe_workspace_size", "fp8_moe_plan",
+    "fp8_moe_permute", "fp8_moe_unpermute", "fp8_moe_unpermute_bwd",
+]
+
+NORM_RMS, NORM_LAYER = 0, 1
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3, 4
+
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_OUT = {_BF16: OUT_BF16, _F32: OUT_F32}
+_i32, _i64, _f32, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+
+
+class NormFwdArgsC(ctypes.Structure):
+    """fp8_norm_fwd_args_t"""
+    _fields_ = [("rows", _i64), ("width", _i64), ("kind", _i32), ("stream_type", _i32),
+                ("eps", _f32), ("alpha", _f32), ("x", _vp), ("h", _vp), ("gate", _vp),
+                ("gate_rows", _i64), ("post_norm", _i32), ("w_post", _vp), ("b_post", _vp),
+                ("w_pre", _vp), ("b_pre", _vp), ("x_out", _vp), ("y", _vp), ("q", _vp),
+                ("q_format", _i32), ("q_granularity", _i32), ("pow2", _i32), ("q_scale", _vp),
+                ("q_scale_inv", _vp), ("amax", _vp), ("stats", _vp)]
+
+
+class NormBwdArgsC(ctypes.Structure):
+    """fp8_norm_bwd_args_t"""
+    _fields_ = [("rows", _i64), ("width", _i64), ("kind", _i32), ("stream_type", _i32),
+                ("alpha", _f32), ("dy", _vp), ("x_out", _vp), ("dx_out", _vp), ("h", _vp),
+                ("gate", _vp), ("gate_rows", _i64), ("post_norm", _i32), ("w_post", _vp),
+                ("b_post", _vp), ("w_pre", _vp), ("stats", _vp), ("dx", _vp), ("dh", _vp),
+                ("dw_pre", _vp), ("db_pre", _vp), ("dw_post", _vp), ("db_post", _vp),
+                ("dgate", _vp), ("accumulate", _i32)]
+
+
+class GemmActArgsC(ctypes.Structure):
+    """fp8_gemm_act_args_t"""
+    _fields_ = [("A", _vp), ("B", _vp), ("fa", _i32), ("fb", _i32), ("M", _i64), ("N", _i64),
+                ("K", _i64), ("ga", _i32), ("gb", _i32), ("scale_inv_a", _vp),
+                ("scale_inv_b", _vp), ("act", _i32), ("gated", _i32), ("bias", _vp),
+                ("residual", _vp), ("z", _vp), ("d", _vp), ("q", _vp), ("q_format", _i32),
+                ("q_scale", _vp), ("amax", _vp), ("offsets", _vp), ("experts", _i32)]
+
+
+class ActBwdArgsC(ctypes.Structure):
+    """fp8_act_bwd_args_t"""
+    _fields_ = [("M", _i64), ("N", _i64), ("act", _i32), ("gated", _i32), ("dD", _vp), ("z", _vp),
+                ("dz", _vp), ("q", _vp), ("q_format", _i32), ("q_scale", _vp), ("amax", _vp),
+                ("dbias", _vp), ("accumulate", _i32)]
+
+
+class NormFwd(NamedTuple):
+    x_out: Optional[torch.Tensor]
+    y: Optional[torch.Tensor]
+    q: Optional[torch.Tensor]
+    q_scale_inv: Optional[torch.Tensor]
+    amax: Optional[torch.Tensor]
+    stats: Optional[torch.Tensor]
+
+
+class NormBwd(NamedTuple):
+    dx: Optional[torch.Tensor]
+    dh: Optional[torch.Tensor]
+    dw_pre: Optional[torch.Tensor]
+    db_pre: Optional[torch.Tensor]
+    dw_post: Optional[torch.Tensor]
+    db_post: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+
+
+class GemmAct(NamedTuple):
+    d: Optional[torch.Tensor]
+    z: Optional[torch.Tensor]
+    q: Optional[torch.Tensor]
+    amax: Optional[torch.Tensor]
+
+
+class ActBwd(NamedTuple):
+    dz: Optional[torch.Tensor]
+    q: Optional[torch.Tensor]
+    amax: Optional[torch.Tensor]
+    dbias: Optional[torch.Tensor]
+
+
+class MoePlan(NamedTuple):
+    offsets: torch.Tensor
+    counts: torch.Tensor
+    row_of: torch.Tensor
+    src: torch.Tensor
+
+
+_ready = None
+
+
+def _lib():
+    """The library with these calls' signatures declared."""
+    global _ready
+    if _ready is None:
+        L = _base_lib()
+        i, P = ctypes.c_int, ctypes.POINTER
+        L.fp8_norm_fwd.argtypes = [P(NormFwdArgsC), _vp]
+        L.fp8_norm_bwd.argtypes = [P(NormBwdArgsC), _vp, _sz, _vp]
+        L.fp8_norm_bwd_workspace_size.argtypes = [_i64, _i64, _i64]
+        L.fp8_norm_bwd_workspace_size.restype = _sz
+        L.fp8_gemm_act.argtypes = [P(GemmActArgsC), _vp]
+        L.fp8_act_bwd.argtypes = [P(ActBwdArgsC), _vp, _sz, _vp]
+        L.fp8_act_bwd_workspace_size.argtypes = [_i64, _i64, i]
+        L.fp8_act_bwd_workspace_size.restype = _sz
+        L.fp8_moe_rows.argtypes = [_i64, i, i, i]
+        L.fp8_moe_rows.restype = _i64
+        L.fp8_moe_workspace_size.argtypes = [_i64, i, i]
+        L.fp8_moe_workspace_size.restype = _sz
+        L.fp8_moe_plan.argtypes = [_vp, _i64, i, i, i, _vp, _vp, _vp, _vp, _i64, _vp, _sz, _vp]
+        L.fp8_moe_permute.argtypes = [_vp, _vp, _i64, i, _i64, _vp, _vp, _i64, _vp, _vp, _vp]
+        L.fp8_moe_unpermute.argtypes = [_vp, i, _vp, _vp, _i64, i, _i64, _i64, _vp, _vp]
+        L.fp8_moe_unpermute_bwd.argtypes = [_vp, _vp, i, _vp, _vp, _vp, _i64, i, _i64, _i64, _vp,
+                                            _vp, _vp]
+        for name in ("fp8_norm_fwd", "fp8_norm_bwd", "fp8_gemm_act", "fp8_act_bwd", "fp8_moe_plan",
+                     "fp8_moe_permute", "fp8_moe_unpermute", "fp8_moe_unpermute_bwd"):
+            getattr(L, name).restype = i
+        _ready = L
+    return _ready
+
+
+def _given(t, what, dtype, shape):
+    """The address of a given tensor of this shape, None for none."""
+    if t is None:
+        return None
+    p = _ptr(t, what, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return p
+
+
+def _rows(t, what):
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be 2-D")
+    return t.shape
+
+
+def _workspace(workspace, need, device):
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    return _ptr(workspace, "workspace", torch.uint8), workspace.numel(), workspace
+
+
+# ------------------------------------------------------------------ norms
+
+def fp8_norm_fwd(x, h=None, kind: int = NORM_RMS, eps: float = 1e-5, alpha: float = 1.0, gate=None,
+                 post_norm: bool = False, w_post=None, b_post=None, w_pre=None, b_pre=None,
+                 want_y: bool = True, want_stats: bool = False, q_fmt: int | None = None,
+                 q_gran: int = GRAN_TENSOR, q_scale=None, pow2: bool = False,
+                 want_amax: bool = False, x_out=None, y=None, q=None, q_scale_inv=None, amax=None,
+                 stats=None, want_x_out: bool = True, stream=None) -> NormFwd:
+    """x' = alpha x + gate * p with p = N(h; w_post, b_post) (post_norm) or h,
+    then y = N(x'; w_pre, b_pre).  x [T, C] bf16 or fp32 (None: 0), h [T, C]
+    bf16 (None: x' = alpha x), gate [G, C] bf16 with G dividing T.  y comes as
+    bf16 (want_y) and, with q_fmt, as FP8 codes: per tensor with q_scale (and
+    max|y|, want_amax) or per row (GRAN_ROW, q_scale_inv [T]).  stats [4, T]
+    (want_stats) is what fp8_norm_bwd needs.  x_out may be x."""
+    ref = x if x is not None else h
+    if ref is None:
+        raise ValueError("x and h are None")
+    T, C = _rows(ref, "x")
+    dev = ref.device
+    dt = x.dtype if x is not None else (x_out.dtype if x_out is not None else _BF16)
+    if dt not in _OUT:
+        raise TypeError(f"x: dtype {dt}, expected bfloat16 or float32")
+    if x_out is None and want_x_out:
+        x_out = torch.empty(T, C, dtype=dt, device=dev)
+    if y is None and want_y:
+        y = torch.empty(T, C, dtype=_BF16, device=dev)
+    if q_fmt is not None and q is None:
+        q = torch.empty(T, C, dtype=torch.uint8, device=dev)
+    if q_fmt is not None and q_gran == GRAN_ROW and q_scale_inv is None:
+        q_scale_inv = torch.empty(T, dtype=_F32, device=dev)
+    if want_amax and amax is None:
+        amax = torch.empty(1, dtype=_F32, device=dev)
+    if want_stats and stats is None:
+        stats = torch.empty(4, T, dtype=_F32, device=dev)
+    gate_rows = 0 if gate is None else _rows(gate, "gate")[0]
+    a = NormFwdArgsC(
+        T, C, kind, _OUT[dt], eps, alpha, _given(x, "x", dt, (T, C)), _given(h, "h", _BF16, (T, C)),
+        _given(gate, "gate", _BF16, (gate_rows, C)), gate_rows, bool(post_norm),
+        _given(w_post, "w_post", _F32, (C,)), _given(b_post, "b_post", _F32, (C,)),
+        _given(w_pre, "w_pre", _F32, (C,)), _given(b_pre, "b_pre", _F32, (C,)),
+        _given(x_out, "x_out", dt, (T, C)), _given(y, "y", _BF16, (T, C)),
+        _given(q, "q", _U8, (T, C)), E4M3 if q_fmt is None else q_fmt, q_gran, bool(pow2),
+        _given(q_scale, "q_scale", _F32, (1,)), _given(q_scale_inv, "q_scale_inv", _F32, (T,)),
+        _given(amax, "amax", _F32, (1,)), _given(stats, "stats", _F32, (4, T)))
+    _check(_lib().fp8_norm_fwd(ctypes.byref(a), _stream(stream)))
+    return NormFwd(x_out, y, q, q_scale_inv, amax, stats)
+
+
+def fp8_norm_bwd_workspace_size(rows: int, width: int, gate_rows: int = 0) -> int:
+    return int(_lib().fp8_norm_bwd_workspace_size(rows, width, gate_rows))
+
+
+def fp8_norm_bwd(dy, x_out, stats, dx_out=None, h=None, kind: int = NORM_RMS, alpha: float = 1.0,
+                 gate=None, post_norm: bool = False, w_post=None, b_post=None, w_pre=None,
+                 b_pre=None, dx=None, dh=None, dw_pre=None, db_pre=None, dw_post=None,
+                 db_post=None, dgate=None, accumulate: bool = False, workspace=None,
+                 stream=None) -> NormBwd:
+    """Gradients of fp8_norm_fwd from dy (None: 0) and dx_out, the gradient
+    that x' gets from its other use (None: 0; the stream's type).  x_out and
+    stats are the forward's.  dx and dh come where their inputs were; the
+    vectors' gradients (fp32) where the vectors were given, added to the given
+    outputs with accumulate.  dx may be dx_out."""
+    ref = next((t for t in (x_out, dx_out, dy) if t is not None), None)
+    if ref is None:
+        raise ValueError("dy and dx_out are None")
+    T, C = _rows(ref, "x_out")
+    dev = ref.device
+    dt = x_out.dtype if x_out is not None else dx_out.dtype if dx_out is not None else _BF16
+    if dt not in _OUT:
+        raise TypeError(f"x_out: dtype {dt}, expected bfloat16 or float32")
+    if accumulate and any(v is not None and o is None for v, o in (
+            (w_pre, dw_pre), (b_pre, db_pre), (w_post, dw_post), (b_post, db_post), (gate, dgate))):
+        raise ValueError("accumulate adds to given outputs")
+
+    def vec(out, of, shape):
+        return torch.empty(shape, dtype=_F32, device=dev) if out is None and of is not None else out
+
+    if dx is None:
+        dx = torch.empty(T, C, dtype=dt, device=dev)
+    if dh is None and h is not None:
+        dh = torch.empty(T, C, dtype=_BF16, device=dev)
+    gate_rows = 0 if gate is None else _rows(gate, "gate")[0]
+    if dy is not None:
+        dw_pre, db_pre = vec(dw_pre, w_pre, (C,)), vec(db_pre, b_pre, (C,))
+    dw_post, db_post = vec(dw_post, w_post, (C,)), vec(db_post, b_post, (C,))
+    dgate = vec(dgate, gate, (gate_rows, C))
+    need = fp8_norm_bwd_workspace_size(T, C, gate_rows)
+    ws, ws_bytes, workspace = _workspace(workspace, need, dev)
+    a = NormBwdArgsC(
+        T, C, kind, _OUT[dt], alpha, _given(dy, "dy", _BF16, (T, C)),
+        _given(x_out, "x_out", dt, (T, C)), _given(dx_out, "dx_out", dt, (T, C)),
+        _given(h, "h", _BF16, (T, C)), _given(gate, "gate", _BF16, (gate_rows, C)), gate_rows,
+        bool(post_norm), _given(w_post, "w_post", _F32, (C,)), _given(b_post, "b_post", _F32, (C,)),
+        _given(w_pre, "w_pre", _F32, (C,)), _given(stats, "stats", _F32, (4, T)),
+        _given(dx, "dx", dt, (T, C)), _given(dh, "dh", _BF16, (T, C)),
+        _given(dw_pre, "dw_pre", _F32, (C,)), _given(db_pre, "db_pre", _F32, (C,)),
+        _given(dw_post, "dw_post", _F32, (C,)), _given(db_post, "db_post", _F32, (C,)),
+        _given(dgate, "dgate", _F32, (gate_rows, C)), bool(accumulate))
+    _check(_lib().fp8_norm_bwd(ctypes.byref(a), ws, ws_bytes, _stream(stream)))
+    return NormBwd(dx, dh, dw_pre, db_pre, dw_post, db_post, dgate)
+
+
+# ------------------------------------------------------------------ GEMM with an epilogue
+
+def fp8_gemm_act(A, fa: int, B, fb: int, scale_inv_a, scale_inv_b, ga: int = GRAN_TENSOR,
+                 gb: int = GRAN_TENSOR, act: int = ACT_NONE, gated: bool = False, bias=None,
+                 residual=None, want_z: bool = False, want_d: bool = True, q_fmt: int | None = None,
+                 q_scale=None, want_amax: bool = False, z=None, d=None, q=None, amax=None,
+                 offsets=None, stream=None) -> GemmAct:
+    """D = act(z) + residual with z = s_a s_b A . B^T + bias, or, gated, D =
+    act(z[:, :N]) z[:, N:] + residual (B's first N rows are the gate's).  A
+    [M, K] and B [N or 2N, K] are FP8 codes.  D comes as bf16 (want_d) and,
+    with q_fmt, as FP8 codes of D * q_scale; z (bf16, want_z) is what
+    fp8_act_bwd needs.  With offsets [E + 1] (fp8_moe_plan's, align a multiple
+    of 32) B is [E, N or 2N, K] and each expert's rows of A take their part of
+    B, scale_inv_b and bias."""
+    M, K = _rows(A, "A")
+    E = 1
+    if offsets is not None:
+        if B.dim() != 3:
+            raise ValueError("B must be [experts, N or 2N, K] with offsets")
+        E = B.shape[0]
+    elif B.dim() != 2:
+        raise ValueError("B must be 2-D")
+    rows = B.shape[-2]
+    if B.shape[-1] != K:
+        raise ValueError("A and B disagree on K")
+    if gated and rows % 2:
+        raise ValueError("a gated B has an even number of rows")
+    N = rows // 2 if gated else rows
+    dev = A.device
+    if d is None and want_d:
+        d = torch.empty(M, N, dtype=_BF16, device=dev)
+    if z is None and want_z:
+        z = torch.empty(M, rows, dtype=_BF16, device=dev)
+    if q is None and q_fmt is not None:
+        q = torch.empty(M, N, dtype=torch.uint8, device=dev)
+    if amax is None and want_amax:
+        amax = torch.empty(1, dtype=_F32, device=dev)
+    per_b = (E,) if offsets is not None else (1,)
+    per_row = (E, rows) if offsets is not None else (rows,)
+    a = GemmActArgsC(
+        _ptr(A, "A", _U8), _ptr(B, "B", _U8), fa, fb, M, N, K, ga, gb,
+        _given(scale_inv_a, "scale_inv_a", _F32, (M,) if ga == GRAN_ROW else (1,)),
+        _given(scale_inv_b, "scale_inv_b", _F32, per_row if gb == GRAN_ROW else per_b), act,
+        bool(gated), _given(bias, "bias", _BF16, per_row), _given(residual, "residual", _BF16, (M, N)),
+        _given(z, "z", _BF16, (M, rows)), _given(d, "d", _BF16, (M, N)), _given(q, "q", _U8, (M, N)),
+        E4M3 if q_fmt is None else q_fmt, _given(q_scale, "q_scale", _F32, (1,)),
+        _given(amax, "amax", _F32, (1,)), _given(offsets, "offsets", _I32, (E + 1,)), E)
+    _check(_lib().fp8_gemm_act(ctypes.byref(a), _stream(stream)))
+    return GemmAct(d, z, q, amax)
+
+
+def fp8_act_bwd_workspace_size(M: int, N: int, gated: bool) -> int:
+    return int(_lib().fp8_act_bwd_workspace_size(M, N, int(bool(gated))))
+
+
+def fp8_act_bwd(dD, z, act: int, gated: bool = False, want_dz: bool = True, q_fmt: int | None = None,
+                q_scale=None, want_amax: bool = False, want_dbias: bool = False, dz=None, q=None,
+                amax=None, dbias=None, accumulate: bool = False, workspace=None,
+                stream=None) -> ActBwd:
+    """dz = dD act'(z) (gated: both halves) from fp8_gemm_act's z, as bf16
+    (want_dz) and, with q_fmt, as FP8 codes of dz * q_scale; dbias (fp32,
+    want_dbias) is dz's column sum, added to a given one with accumulate."""
+    M, N = _rows(dD, "dD")
+    rows = 2 * N if gated else N
+    dev = dD.device
+    if accumulate and dbias is None:
+        raise ValueError("accumulate adds to a given dbias")
+    if dz is None and want_dz:
+        dz = torch.empty(M, rows, dtype=_BF16, device=dev)
+    if q is None and q_fmt is not None:
+        q = torch.empty(M, rows, dtype=torch.uint8, device=dev)
+    if amax is None and want_amax:
+        amax = torch.empty(1, dtype=_F32, device=dev)
+    if dbias is None and want_dbias:
+        dbias = torch.empty(rows, dtype=_F32, device=dev)
+    ws = ws_bytes = None
+    if dbias is not None:
+        ws, ws_bytes, workspace = _workspace(workspace, fp8_act_bwd_workspace_size(M, N, gated), dev)
+    a = ActBwdArgsC(
+        M, N, act, bool(gated), _given(dD, "dD", _BF16, (M, N)), _given(z, "z", _BF16, (M, rows)),
+        _given(dz, "dz", _BF16, (M, rows)), _given(q, "q", _U8, (M, rows)),
+        E4M3 if q_fmt is None else q_fmt, _given(q_scale, "q_scale", _F32, (1,)),
+        _given(amax, "amax", _F32, (1,)), _given(dbias, "dbias", _F32, (rows,)), bool(accumulate))
+    _check(_lib().fp8_act_bwd(ctypes.byref(a), ws, ws_bytes or 0, _stream(stream)))
+    return ActBwd(dz, q, amax, dbias)
+
+
+# ------------------------------------------------------------------ tokens by expert
+
+def fp8_moe_rows(tokens: int, slots: int, experts: int, align: int = 1) -> int:
+    """Rows that hold any routing of this size."""
+    r = int(_lib().fp8_moe_rows(tokens, slots, experts, align))
+    if r < 0:
+        raise ValueError("fp8_moe_rows: slots 1..64, experts 1..1024, align 1..4096, tokens < 2^31")
+    return r
+
+
+def fp8_moe_workspace_size(tokens: int, slots: int, experts: int) -> int:
+    return int(_lib().fp8_moe_workspace_size(tokens, slots, experts))
+
+
+def fp8_moe_plan(ids, experts: int, align: int = 1, rows: int | None = None, offsets=None,
+                 counts=None, row_of=None, src=None, workspace=None, stream=None) -> MoePlan:
+    """Sort the slots of ids [T, k] (int32; outside 0..experts-1: dropped) by
+    expert: offsets [E + 1] and counts [E] of the experts' rows, row_of [T, k]
+    the slot's row or -1, src [rows] the row's slot (t * k + j) or -1.  Each
+    expert's rows are padded to a multiple of align."""
+    T, k = _rows(ids, "ids")
+    dev = ids.device
+    if rows is None:
+        rows = fp8_moe_rows(T, k, experts, align) if src is None else src.numel()
+    if offsets is None:
+        offsets = torch.empty(experts + 1, dtype=_I32, device=dev)
+    if counts is None:
+        counts = torch.empty(experts, dtype=_I32, device=dev)
+    if row_of is None:
+        row_of = torch.empty(T, k, dtype=_I32, device=dev)
+    if src is None:
+        src = torch.empty(rows, dtype=_I32, device=dev)
+    ws, ws_bytes, need = None, 0, fp8_moe_workspace_size(T, k, experts)
+    if need:
+        ws, ws_bytes, workspace = _workspace(workspace, need, dev)
+    _check(_lib().fp8_moe_plan(
+        _ptr(ids, "ids", _I32), T, k, experts, align, _given(offsets, "offsets", _I32, (experts + 1,)),
+        _given(counts, "counts", _I32, (experts,)), _given(row_of, "row_of", _I32, (T, k)),
+        _given(src, "src", _I32, (rows,)), rows, ws, ws_bytes, _stream(stream)))
+    return MoePlan(offsets, counts, row_of, src)
+
+
+def fp8_moe_permute(x, row_of, src, scale=None, xs=None, scale_s=None, stream=None):
+    """xs [rows, C] = x's rows in the plan's order, zeros where there is no
+    source; x is of any type (codes go with their per-row factors, scale [T]).
+    Returns (xs, scale_s or None)."""
+    T, C = _rows(x, "x")
+    k, rows = _rows(row_of, "row_of")[1], src.numel()
+    if xs is None:
+        xs = torch.empty(rows, C, dtype=x.dtype, device=x.device)
+    if scale is not None and scale_s is None:
+        scale_s = torch.empty(rows, dtype=_F32, device=x.device)
+    _check(_lib().fp8_moe_permute(
+        _ptr(x, "x"), _given(scale, "scale", _F32, (T,)), T, k, C * x.element_size(),
+        _given(row_of, "row_of", _I32, (T, k)), _given(src, "src", _I32, (rows,)), rows,
+        _given(xs, "xs", x.dtype, (rows, C)), _given(scale_s, "scale_s", _F32, (rows,)),
+        _stream(stream)))
+    return xs, scale_s
+
+
+def fp8_moe_unpermute(ys, row_of, weights=None, y=None, stream=None) -> torch.Tensor:
+    """y [T, C] = the weighted sum of each token's rows of ys [rows, C] (bf16
+    or fp32); weights [T, k] fp32, None: 1 (the gradient of the permutation)."""
+    rows, C = _rows(ys, "ys")
+    T, k = _rows(row_of, "row_of")
+    if ys.dtype not in _OUT:
+        raise TypeError(f"ys: dtype {ys.dtype}, expected bfloat16 or float32")
+    if y is None:
+        y = torch.empty(T, C, dtype=ys.dtype, device=ys.device)
+    _check(_lib().fp8_moe_unpermute(
+        _ptr(ys, "ys"), _OUT[ys.dtype], _ptr(row_of, "row_of", _I32),
+        _given(weights, "weights", _F32, (T, k)), T, k, C, rows, _given(y, "y", ys.dtype, (T, C)),
+        _stream(stream)))
+    return y
+
+
+def fp8_moe_unpermute_bwd(dy, ys, row_of, src, weights=None, dys=None, dweights=None, stream=None):
+    """Gradients of fp8_moe_unpermute: (dys [rows, C], dweights [T, k] or None
+    without weights)."""
+    rows, C = _rows(ys, "ys")
+    T, k = _rows(row_of, "row_of")
+    if ys.dtype not in _OUT:
+        raise TypeError(f"ys: dtype {ys.dtype}, expected bfloat16 or float32")
+    if dys is None:
+        dys = torch.empty(rows, C, dtype=ys.dtype, device=ys.device)
+    if dweights is None and weights is not None:
+        dweights = torch.empty(T, k, dtype=_F32, device=ys.device)
+    _check(_lib().fp8_moe_unpermute_bwd(
+        _given(dy, "dy", ys.dtype, (T, C)), _ptr(ys, "ys"), _OUT[ys.dtype],
+        _ptr(row_of, "row_of", _I32), _given(src, "src", _I32, (rows,)),
+        _given(weights, "weights", _F32, (T, k)), T, k, C, rows,
+        _given(dys, "dys", ys.dtype, (rows, C)), _given(dweights, "dweights", _F32, (T, k)),
+        _stream(stream)))
+    return dys, dweights

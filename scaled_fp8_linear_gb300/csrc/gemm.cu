@@ -1610,8 +1610,8 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// Tensor map of a K-contiguous FP8 matrix [rows x K]: boxes of 128 bytes of K
-// by box_rows rows, 128-byte swizzle, zero fill outside the matrix.
+}  // namespace
+
 int make_kmajor_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t K,
                     uint32_t box_rows) {
     EncodeTiledFn fn = encode_fn();
@@ -1630,6 +1630,26 @@ int make_kmajor_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t K,
                          static_cast<long long>(K));
     return FP8_OK;
 }
+
+int make_output_map(CUtensorMap* map, void* ptr, int64_t rows, int64_t cols, int64_t row_bytes,
+                    CUtensorMapDataType type, uint32_t box_cols, CUtensorMapSwizzle swizzle) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return set_error(FP8_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+    const cuuint32_t box[2] = {box_cols, 32};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = fn(map, type, 2, ptr, dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return set_error(FP8_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for output [%lld x %lld]",
+                         static_cast<int>(r), static_cast<long long>(rows),
+                         static_cast<long long>(cols));
+    return FP8_OK;
+}
+
+namespace {
 
 // Tensor map of an MN-contiguous FP8 matrix stored [K x MN] (the transpose of
 // a K-major operand): boxes of 128 elements of MN by BK rows of K, 128-byte

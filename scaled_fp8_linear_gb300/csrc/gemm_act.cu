@@ -1,0 +1,830 @@
+// gemm_act.cu -- FP8 GEMM with bias, activation and residual in its epilogue,
+// dense or one product per expert, and the gradient of that epilogue.
+//
+//   z = s_a s_b A . B^T + bias;  v = act(z), or act(z_gate) z_up;  D = v + residual
+//
+// The products run as in gemm.cu: TMA tiles into a shared-memory ring, one
+// thread issuing tcgen05.mma into one of two TMEM accumulators, epilogue
+// warps on the other.  What is different here:
+//   - gated: the accumulator's left half holds a tile of the gate's product
+//     and the right half the same tile of the up product (the B rows of the
+//     two are loaded side by side), so an epilogue thread has both in its row
+//     and z_up never goes through memory;
+//   - per expert: a unit of work is a tile of one expert's rows; the experts'
+//     row offsets are read on the device, so no count comes to the host.  A
+//     tile's rows past its expert's end are computed and not written: offsets
+//     are multiples of 32, the height of a stored box;
+//   - eight epilogue warps: an activation costs more than a scale.
+// z stays in fp32 from the accumulator to D; D, z and the codes are each
+// rounded once.
+#include <cstdint>
+#include <mutex>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/fp8linear.h"
+#include "internal.h"
+#include "ptx.cuh"
+#include "rowops.cuh"
+
+namespace fp8 {
+namespace {
+
+constexpr int BK = 128;       // FP8 elements of K per stage
+constexpr int UMMA_K = 32;    // K of one kind::f8f6f4 instruction
+constexpr int kMaxGemmExperts = 256;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = (4 + kEpiWarps) * 32;
+
+struct ActParams {
+    int64_t M, N, K;
+    int num_n, num_kb;
+    int fa, fb, ga, gb;
+    const float* sa;
+    const float* sb;
+    int act;
+    const __nv_bfloat16* bias;
+    const __nv_bfloat16* residual;
+    int has_z, has_d, has_q, q_fmt;
+    const float* q_scale;
+    float* amax;
+    const int32_t* offsets;   // null: one product over all rows
+    int experts;
+    int group;                // raster group (row blocks)
+    unsigned* status;
+};
+
+// ------------------------------------------------------------------ activations
+
+__device__ __forceinline__ float sigmoid_scaled(float num, float x) {   // num / (1 + exp(-x))
+    return __fdividef(num, 1.0f + __expf(-x));
+}
+
+constexpr float kGeluC = 0.7978845608028654f, kGeluA = 0.044715f;   // sqrt(2 / pi)
+constexpr float kSqrtHalf = 0.7071067811865476f, kInvSqrt2Pi = 0.3989422804014327f;
+
+template <int ACT>
+__device__ __forceinline__ float act_of(float z) {
+    if constexpr (ACT == FP8_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
+    if constexpr (ACT == FP8_ACT_SILU) return sigmoid_scaled(z, z);
+    if constexpr (ACT == FP8_ACT_GELU) return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
+    // 1 + tanh(u) = 2 / (1 + exp(-2u))
+    if constexpr (ACT == FP8_ACT_GELU_TANH)
+        return sigmoid_scaled(z, 2.0f * kGeluC * (z + kGeluA * z * z * z));
+    return z;
+}
+
+// act(z) and its derivative.
+template <int ACT>
+__device__ __forceinline__ void act_and_grad(float z, float& a, float& g) {
+    if constexpr (ACT == FP8_ACT_RELU) {
+        a = z > 0.0f ? z : (z != z ? z : 0.0f);
+        g = z > 0.0f ? 1.0f : 0.0f;
+    } else if constexpr (ACT == FP8_ACT_SILU) {
+        const float s = sigmoid_scaled(1.0f, z);
+        a = z * s;
+        g = s * (1.0f + z * (1.0f - s));
+    } else if constexpr (ACT == FP8_ACT_GELU) {
+        const float cdf = 0.5f * (1.0f + erff(z * kSqrtHalf));
+        a = z * cdf;
+        g = cdf + z * kInvSqrt2Pi * __expf(-0.5f * z * z);
+    } else if constexpr (ACT == FP8_ACT_GELU_TANH) {
+        const float s = sigmoid_scaled(1.0f, 2.0f * kGeluC * (z + kGeluA * z * z * z));
+        a = z * s;
+        g = s + a * (1.0f - s) * 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
+    } else {
+        a = z;
+        g = 1.0f;
+    }
+}
+
+template <int ACT, int N>
+__device__ __forceinline__ void act_all(float (&v)[N]) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = act_of<ACT>(v[j]);
+}
+
+template <int N>
+__device__ __forceinline__ void apply_act(int act, float (&v)[N]) {
+    switch (act) {   // uniform over the grid
+        case FP8_ACT_RELU: act_all<FP8_ACT_RELU>(v); break;
+        case FP8_ACT_SILU: act_all<FP8_ACT_SILU>(v); break;
+        case FP8_ACT_GELU: act_all<FP8_ACT_GELU>(v); break;
+        case FP8_ACT_GELU_TANH: act_all<FP8_ACT_GELU_TANH>(v); break;
+        default: break;
+    }
+}
+
+// ------------------------------------------------------------------ units of work
+
+// The experts' rows and tiles, in shared memory: expert e has rows off[e] ..
+// off[e + 1] and units first[e] .. first[e + 1].  Without offsets: one entry.
+struct Units {
+    int off[kMaxGemmExperts + 1];
+    int first[kMaxGemmExperts + 1];
+};
+
+// Fills `u` (every thread of the CTA; ends with a barrier).  Offsets are held
+// to 0 .. M and made never to fall, so whatever they are no unit reaches
+// outside and there are no more units than the rows allow.
+__device__ __forceinline__ void make_units(Units* u, const ActParams& p, int rows_per_tile) {
+    const int t = static_cast<int>(threadIdx.x);
+    const int M = static_cast<int>(p.M);
+    if (p.offsets) {
+        for (int e = t; e <= p.experts; e += blockDim.x)
+            u->off[e] = min(max(p.offsets[e], 0), M);
+    } else if (t <= 1) {
+        u->off[t] = t ? M : 0;
+    }
+    __syncthreads();
+    if (t < 32) {   // one warp: exclusive sum of the experts' tile counts
+        int run = 0, high = 0;
+        for (int base = 0; base <= p.experts; base += 32) {   // never falling
+            const int e = base + t;
+            int v = max(e <= p.experts ? u->off[e] : 0, high);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int w = __shfl_up_sync(row::kAll, v, o);
+                if (t >= o) v = max(v, w);
+            }
+            if (e <= p.experts) u->off[e] = v;
+            high = __shfl_sync(row::kAll, v, 31);
+        }
+        __syncwarp();
+        for (int base = 0; base < p.experts; base += 32) {
+            const int e = base + t;
+            int n = 0;
+            if (e < p.experts) {
+                const int rows = u->off[e + 1] - u->off[e];
+                n = (rows + rows_per_tile - 1) / rows_per_tile * p.num_n;
+            }
+            int incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(row::kAll, incl, o);
+                if (t >= o) incl += v;
+            }
+            if (e < p.experts) u->first[e] = run + incl - n;
+            run += __shfl_sync(row::kAll, incl, 31);
+        }
+        if (t == 0) u->first[p.experts] = run;
+    }
+    __syncthreads();
+}
+
+struct Tile {
+    int expert;
+    int row0, row_end;   // first row, end of the expert's rows
+    int n_blk;
+};
+
+__device__ __forceinline__ Tile tile_of(int unit, const Units* u, const ActParams& p,
+                                        int rows_per_tile) {
+    int lo = 0, hi = p.experts;   // the last expert that starts at or before the unit
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (u->first[mid] <= unit) lo = mid;
+        else hi = mid;
+    }
+    const int local = unit - u->first[lo];
+    const int num_m = (u->off[lo + 1] - u->off[lo] + rows_per_tile - 1) / rows_per_tile;
+    // grouped raster: `group` row blocks down each column block, so that the
+    // CTAs at work share A and B panels in L2
+    const int per_group = p.group * p.num_n;
+    const int g = local / per_group;
+    const int size = min(num_m - g * p.group, p.group);
+    const int in_g = local - g * per_group;
+    Tile t;
+    t.expert = lo;
+    t.row0 = u->off[lo] + (g * p.group + in_g % size) * rows_per_tile;
+    t.row_end = u->off[lo + 1];
+    t.n_blk = in_g / size;
+    return t;
+}
+
+// ------------------------------------------------------------------ the epilogue
+
+// Writes one box of 32 rows from `slot` (this warp's, filled through `fill`).
+template <typename Fill>
+__device__ __forceinline__ void emit(uint8_t* slot, const CUtensorMap* map, int64_t x, int64_t y,
+                                     bool in_range, Fill fill) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) ptx::bulk_wait_group_read<0>();   // the slot's last box has been read
+    __syncwarp();
+    fill();
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        if (in_range)
+            ptx::tma_store_2d(map, ptx::smem_u32(slot), static_cast<int32_t>(x), static_cast<int32_t>(y));
+        ptx::bulk_commit_group();
+    }
+}
+
+// 32 columns of this thread's row as bf16: 64 bytes, in the TMA's 64-byte
+// swizzle (piece j of row r at j ^ ((r >> 1) & 3)), which spreads the banks.
+__device__ __forceinline__ void emit_bf16(uint8_t* slot, const float (&v)[32], const CUtensorMap* map,
+                                          int64_t x, int64_t y, bool in_range) {
+    emit(slot, map, x, y, in_range, [&] {
+        const int lane = threadIdx.x & 31, swz = (lane >> 1) & 3;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint4 w = make_uint4(row::pack_bf16(v[8 * j], v[8 * j + 1]),
+                                       row::pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                                       row::pack_bf16(v[8 * j + 4], v[8 * j + 5]),
+                                       row::pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+            *reinterpret_cast<uint4*>(slot + lane * 64 + 16 * (j ^ swz)) = w;
+        }
+    });
+}
+
+__device__ __forceinline__ void emit_codes(uint8_t* slot, const float (&v)[32], int fmt, float s,
+                                           const CUtensorMap* map, int64_t x, int64_t y,
+                                           bool in_range) {
+    emit(slot, map, x, y, in_range, [&] {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float* c = v + 16 * j + 4 * e;
+                w[e] = row::cvt_pair(fmt, __fmul_rn(c[0], s), __fmul_rn(c[1], s)) |
+                       (row::cvt_pair(fmt, __fmul_rn(c[2], s), __fmul_rn(c[3], s)) << 16);
+            }
+            *reinterpret_cast<uint4*>(slot + lane * 32 + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    });
+}
+
+// z of 32 columns: accumulator times factors plus bias.  fa: the row's
+// factor; `base`: where this expert's factors and bias of column n0 start.
+// Columns at n_left and past are not read.
+__device__ __forceinline__ void dequant(float (&z)[32], const uint32_t (&r)[32], float fa,
+                                        int64_t base, int n_left, const ActParams& p, float sb0) {
+    if (p.gb == FP8_GRAN_ROW) {
+        const int lane = threadIdx.x & 31;
+        const float sbv = lane < n_left ? p.sb[base + lane] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            z[j] = __fmul_rn(__uint_as_float(r[j]), __fmul_rn(fa, __shfl_sync(row::kAll, sbv, j)));
+    } else {
+        const float f = __fmul_rn(fa, sb0);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) z[j] = __fmul_rn(__uint_as_float(r[j]), f);
+    }
+    if (p.bias) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+            if (j < n_left) {   // n_left is a multiple of 16
+                float b[8];
+                row::unpack8(b, __ldg(reinterpret_cast<const uint4*>(p.bias + base + j)));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) z[j + e] = __fadd_rn(z[j + e], b[e]);
+            }
+        }
+    }
+}
+
+struct OutMaps {
+    CUtensorMap z, z_up, d, q;
+};
+
+// The epilogue of a warp: 32 rows x COLS output columns of one tile, from
+// TMEM column `tcol` (gated: the up product UP columns further on).
+template <bool GATED, int UP, int COLS>
+__device__ __forceinline__ void epilogue(uint8_t* slot, uint32_t tcol, const Tile& t, int64_t m0,
+                                         int64_t n_first, const ActParams& p, const OutMaps& maps,
+                                         uint32_t& top) {
+    const int lane = threadIdx.x & 31;
+    const int64_t m = m0 + lane;
+    const bool live = m < t.row_end;
+    const bool in_rows = m0 < t.row_end;
+    const int64_t b_rows = GATED ? 2 * p.N : p.N;
+    const float fa = p.ga == FP8_GRAN_ROW ? p.sa[live ? m : p.M - 1] : p.sa[0];
+    const float sb0 = p.gb == FP8_GRAN_ROW ? 0.0f : p.sb[t.expert];
+    const float qs = p.has_q ? p.q_scale[0] : 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < COLS / 32; ++c) {
+        const int64_t n0 = n_first + c * 32;
+        const int n_left = static_cast<int>(min(p.N - n0, static_cast<int64_t>(32)));
+        const bool in_range = in_rows && n_left > 0;
+        float z[32];
+        {
+            uint32_t r[32];
+            ptx::tmem_ld_32x32b_x32(tcol + c * 32, r);
+            ptx::tmem_wait_ld();
+            dequant(z, r, fa, t.expert * b_rows + n0, n_left, p, sb0);
+        }
+        if (p.has_z) emit_bf16(slot, z, &maps.z, n0, m0, in_range);
+        apply_act(p.act, z);
+        if constexpr (GATED) {
+            float up[32];
+            uint32_t r[32];
+            ptx::tmem_ld_32x32b_x32(tcol + UP + c * 32, r);
+            ptx::tmem_wait_ld();
+            dequant(up, r, fa, t.expert * b_rows + p.N + n0, n_left, p, sb0);
+            if (p.has_z) emit_bf16(slot, up, &maps.z_up, n0, m0, in_range);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) z[j] *= up[j];
+        }
+        if (p.residual && live) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+                if (j < n_left) {
+                    float v[8];
+                    row::unpack8(v, row::ld_stream(p.residual + m * p.N + n0 + j));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) z[j + e] += v[e];
+                }
+            }
+        }
+        if (p.has_d) emit_bf16(slot, z, &maps.d, n0, m0, in_range);
+        if (p.has_q) {
+            emit_codes(slot, z, p.q_fmt, qs, &maps.q, n0, m0, in_range);
+            if (p.amax && live) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (j < n_left) top = max(top, row::abs_bits(z[j]));
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ CTA-pair kernel
+
+// A cluster of two CTAs per 256-row tile of 256 accumulator columns (gated:
+// 128 output columns; the even CTA holds their gate rows of B and the odd
+// one their up rows, which is how cta_group::2 splits B).  Roles and
+// barriers as in gemm.cu's pair kernel.
+constexpr int kPairStages = 6;
+constexpr int kHalf = 128;
+constexpr int kPairTile = 256;
+constexpr int kPairStageBytes = 2 * kHalf * BK;
+constexpr int kSlotBytes = 2048;
+constexpr int kPairSmem = kPairStages * kPairStageBytes + kEpiWarps * kSlotBytes + 256 +
+                          static_cast<int>(sizeof(Units)) + 1024;
+
+template <bool GATED>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    gemm_act_pair_kernel(const __grid_constant__ CUtensorMap tmA,
+                         const __grid_constant__ CUtensorMap tmB,
+                         const __grid_constant__ OutMaps maps, const __grid_constant__ ActParams p) {
+    ptx::griddep_launch_dependents();
+    constexpr int TN = GATED ? kHalf : kPairTile;   // output columns of a tile
+    constexpr uint32_t TMEM_COLS = 2 * kPairTile;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* slots = ring + kPairStages * kPairStageBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(slots + kEpiWarps * kSlotBytes);
+    uint64_t* empty = full + kPairStages;
+    uint64_t* tfull = empty + kPairStages;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* done = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+    Units* units = reinterpret_cast<Units*>(reinterpret_cast<uint8_t*>(full) + 256);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_ctarank();
+    const bool leader = rank == 0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            ptx::mbar_init(&full[s], 1);
+            ptx::mbar_init(&empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            ptx::mbar_init(&tfull[a], 1);
+            ptx::mbar_init(&tempty[a], 2 * kEpiWarps);   // both CTAs' epilogue warps
+        }
+        ptx::mbar_init(done, 1);
+        *abort_flag = 0;
+        ptx::fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        ptx::tma_prefetch_desc(&tmA);
+        ptx::tma_prefetch_desc(&tmB);
+    }
+    if (warp == 2) {
+        ptx::tmem_alloc_pair(tmem_slot, TMEM_COLS);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::griddep_wait();
+    make_units(units, p, kPairTile);
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int num_units = units->first[p.experts];
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0;
+            int64_t issued = 0;
+            bool ok = true;
+            for (int u = pair; ok && u < num_units; u += npairs) {
+                const Tile t = tile_of(u, units, p, kPairTile);
+                const int ya = t.row0 + static_cast<int>(rank) * kHalf;
+                const int64_t yb64 =
+                    GATED ? (2 * static_cast<int64_t>(t.expert) + rank) * p.N + t.n_blk * TN
+                          : t.expert * p.N + t.n_blk * TN + rank * kHalf;
+                const int yb = static_cast<int>(yb64);
+                for (int kb = 0; kb < p.num_kb; ++kb) {
+                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
+                    uint8_t* sa = ring + stage * kPairStageBytes;
+                    const uint32_t bar = ptx::cluster_addr(&full[stage], 0);
+                    if (leader) ptx::mbar_arrive_expect_tx(&full[stage], 2 * kPairStageBytes);
+                    ptx::tma_load_2d_pair(sa, &tmA, bar, kb * BK, ya);
+                    ptx::tma_load_2d_pair(sa + kHalf * BK, &tmB, bar, kb * BK, yb);
+                    ++issued;
+                    if (++stage == kPairStages) { stage = 0; phase ^= 1u; }
+                }
+            }
+            uint32_t never = 0;
+            if (leader) {
+                // drain: the last copies into each slot (both CTAs' bytes) have landed
+                for (int s = 0; s < kPairStages; ++s) {
+                    if (issued <= s && issued < kPairStages) break;
+                    const uint32_t par = (static_cast<uint32_t>(s) < stage) ? phase : (phase ^ 1u);
+                    ptx::mbar_wait(&full[s], par, &never);
+                }
+            } else if (!ok) {
+                // copies signal the peer's barriers: after an abort, give those in
+                // flight a bounded time to land before this CTA moves on
+                const uint64_t t0 = ptx::globaltimer();
+                while (ptx::globaltimer() - t0 < 1000000ull) {
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            const uint32_t idesc = ptx::idesc_f8f6f4(p.fa, p.fb, kPairTile, kPairTile);
+            const uint64_t tmpl = ptx::sdesc_kmajor_sw128(0);
+            uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+            bool ok = true;
+            for (int u = pair; ok && u < num_units; u += npairs) {
+                if (!ptx::mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag)) break;
+                ptx::tc_fence_after();
+                const uint32_t d = tmem_base + acc * kPairTile;
+                for (int kb = 0; kb < p.num_kb; ++kb) {
+                    if (!ptx::mbar_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
+                    ptx::tc_fence_after();
+                    uint8_t* sa = ring + stage * kPairStageBytes;
+                    const uint64_t ad = tmpl | ((ptx::smem_u32(sa) & 0x3FFFFu) >> 4);
+                    const uint64_t bd = tmpl | ((ptx::smem_u32(sa + kHalf * BK) & 0x3FFFFu) >> 4);
+#pragma unroll
+                    for (int k = 0; k < BK / UMMA_K; ++k)
+                        ptx::mma_f8f6f4_pair(d, ad + k * (UMMA_K >> 4), bd + k * (UMMA_K >> 4), idesc,
+                                             (kb | k) != 0);
+                    ptx::mma_commit_pair(&empty[stage], 0x3);
+                    if (++stage == kPairStages) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                ptx::mma_commit_pair(&tfull[acc], 0x3);
+                acc ^= 1u;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+            uint32_t never = 0;
+            ptx::mma_commit_pair(done, 0x1);
+            ptx::mbar_wait(done, 0, &never);
+        }
+    } else if (warp >= 4) {
+        const int qd = warp & 3, side = (warp - 4) >> 2;   // TMEM lanes, half of the columns
+        uint8_t* slot = slots + (warp - 4) * kSlotBytes;
+        uint32_t acc = 0, acc_phase = 0, top = 0;
+        for (int u = pair; u < num_units; u += npairs) {
+            const Tile t = tile_of(u, units, p, kPairTile);
+            bool ok = (lane == 0) ? ptx::mbar_wait(&tfull[acc], acc_phase, abort_flag) : false;
+            ok = __shfl_sync(row::kAll, ok, 0);
+            if (!ok) break;
+            __syncwarp();
+            ptx::tc_fence_after();
+            const uint32_t tcol = tmem_base + (static_cast<uint32_t>(qd * 32) << 16) +
+                                  acc * kPairTile + side * (TN / 2);
+            epilogue<GATED, kHalf, TN / 2>(slot, tcol, t, t.row0 + rank * kHalf + qd * 32,
+                                           static_cast<int64_t>(t.n_blk) * TN + side * (TN / 2), p,
+                                           maps, top);
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::cluster_addr(&tempty[acc], 0));
+            acc ^= 1u;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+        if (lane == 0) ptx::bulk_wait_group_all();   // every TMA store has completed
+        top = __reduce_max_sync(row::kAll, top);
+        if (p.amax && lane == 0) row::raise_amax(p.amax, top);
+        __syncwarp();
+    }
+
+    ptx::tc_fence_before();
+    ptx::cluster_sync();   // the pair's MMAs, copies and remote arrivals are all done
+    if (warp == 2) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    }
+    if (threadIdx.x == 0 && *abort_flag && p.status) atomicOr(p.status, 1u);
+}
+
+// ------------------------------------------------------------------ gradient of the epilogue
+
+constexpr int kBwdRows = 64;   // rows a CTA: 8 passes of 8 rows x 256 columns
+
+struct ActBwd {
+    const __nv_bfloat16* d;
+    const __nv_bfloat16* z;
+    __nv_bfloat16* dz;
+    uint8_t* q;
+    const float* q_scale;
+    float* amax;
+    float* part;      // [row blocks][N or 2N] partial column sums, or null
+    int64_t M, N;
+    int64_t col_blocks;
+    int q_fmt;
+};
+
+// Elementwise, HBM-bound: D's gradient and z are read once, dz is written
+// once.  Column sums stay in registers over the CTA's rows.
+template <int ACT, bool GATED>
+__global__ void __launch_bounds__(256) act_bwd_kernel(const __grid_constant__ ActBwd p) {
+    ptx::griddep_launch_dependents();
+    __shared__ float sums[8][256];
+    ptx::griddep_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t block_row = blockIdx.x / p.col_blocks;
+    const int64_t c0 = (blockIdx.x % p.col_blocks) * 256, c = c0 + lane * 8;
+    const int64_t width = GATED ? 2 * p.N : p.N;
+    const bool on = c < p.N;   // N is a multiple of 16
+    const float qs = p.q ? p.q_scale[0] : 0.0f;
+    float s0[8] = {}, s1[8] = {};
+    uint32_t top = 0;
+    auto put = [&](const float (&v)[8], int64_t at) {
+        if (p.dz) *reinterpret_cast<uint4*>(p.dz + at) = row::pack8(v);
+        if (p.q) {
+            *reinterpret_cast<uint2*>(p.q + at) = row::cvt8(p.q_fmt, v, qs);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = max(top, row::abs_bits(v[e]));
+        }
+    };
+    if (on) {
+#pragma unroll 2
+        for (int i = 0; i < kBwdRows / 8; ++i) {
+            const int64_t m = block_row * kBwdRows + i * 8 + warp;
+            if (m >= p.M) break;
+            float d[8], z[8], u[8];
+            row::unpack8(d, row::ld_stream(p.d + m * p.N + c));
+            row::unpack8(z, row::ld_stream(p.z + m * width + c));
+            if constexpr (GATED) row::unpack8(u, row::ld_stream(p.z + m * width + p.N + c));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float a, g;
+                act_and_grad<ACT>(z[e], a, g);
+                if constexpr (GATED) {
+                    z[e] = d[e] * u[e] * g;
+                    u[e] = d[e] * a;
+                    s1[e] += u[e];
+                } else {
+                    z[e] = d[e] * g;
+                }
+                s0[e] += z[e];
+            }
+            put(z, m * width + c);
+            if constexpr (GATED) put(u, m * width + p.N + c);
+        }
+    }
+    if (p.part) {
+#pragma unroll
+        for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sums[warp][lane * 8 + e] = h ? s1[e] : s0[e];
+            __syncthreads();
+            if (c0 + threadIdx.x < p.N) {
+                float s = 0.0f;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) s += sums[w][threadIdx.x];
+                p.part[block_row * width + h * p.N + c0 + threadIdx.x] = s;
+            }
+        }
+    }
+    if (p.amax) {
+        top = __reduce_max_sync(row::kAll, top);
+        if (lane == 0) row::raise_amax(p.amax, top);
+    }
+}
+
+template <int ACT>
+void launch_act_bwd(const ActBwd& p, bool gated, unsigned ctas, cudaStream_t st) {
+    if (gated) launch_pdl(act_bwd_kernel<ACT, true>, dim3(ctas), dim3(256), 0, st, p);
+    else launch_pdl(act_bwd_kernel<ACT, false>, dim3(ctas), dim3(256), 0, st, p);
+}
+
+// ------------------------------------------------------------------ host side
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
+
+int launch_status(const char* what) {
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? FP8_OK : set_error(FP8_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+// The kernel's dynamic shared memory allowed once per device, and how many of
+// its clusters (or CTAs) run at once.
+template <typename Kernel>
+int kernel_slots(Kernel k, int id, int smem, int cluster, int* out) {
+    static std::mutex mu;
+    static int cache[64][8] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
+    int uncached = 0;
+    std::lock_guard<std::mutex> lock(mu);
+    int& c = dev >= 0 && dev < 64 ? cache[dev][id] : uncached;
+    if (c == 0) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess)
+            return set_error(FP8_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        int n = num_sms() / cluster;
+        if (cluster > 1) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(2 * 1024);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = smem;
+            int got = 0;
+            if (cudaOccupancyMaxActiveClusters(&got, k, &cfg) == cudaSuccess && got > 0) n = got;
+            else (void)cudaGetLastError();
+        }
+        c = n;
+    }
+    *out = c;
+    return FP8_OK;
+}
+
+// Raster group: the group's A panels (256 rows by K bytes each) stay in L2
+// beside the B panels in flight, as in gemm.cu.
+int raster_group(int64_t K) {
+    int g = 16;
+    while (g > 4 && g * 256 * K > (int64_t{64} << 20)) g >>= 1;
+    return g;
+}
+
+template <bool GATED>
+int launch_pair(const fp8_gemm_act_args_t* a, ActParams& p, const OutMaps& maps, cudaStream_t st) {
+    const int64_t b_rows = a->gated ? 2 * a->N : a->N;
+    CUtensorMap tmA, tmB;
+    int r = make_kmajor_map(&tmA, a->A, a->M, a->K, kHalf);
+    if (r == FP8_OK) r = make_kmajor_map(&tmB, a->B, b_rows * a->experts, a->K, kHalf);
+    int clusters = 0;
+    auto k = gemm_act_pair_kernel<GATED>;
+    if (r == FP8_OK) r = kernel_slots(k, GATED, kPairSmem, 2, &clusters);
+    if (r != FP8_OK) return r;
+    p.num_n = static_cast<int>((a->N + (GATED ? kHalf : kPairTile) - 1) / (GATED ? kHalf : kPairTile));
+    // at most this many tiles, however the experts' rows are cut
+    const int64_t tiles = ((a->M + kPairTile - 1) / kPairTile + a->experts - 1) * p.num_n;
+    const unsigned grid = 2 * static_cast<unsigned>(tiles < clusters ? tiles : clusters);
+    launch_pdl(k, dim3(grid), dim3(kThreads), kPairSmem, st, tmA, tmB, maps, p);
+    return launch_status("fp8_gemm_act");
+}
+
+}  // namespace
+}  // namespace fp8
+
+using namespace fp8;
+
+extern "C" {
+
+int fp8_gemm_act(const fp8_gemm_act_args_t* a, void* stream) {
+    const char* what = "fp8_gemm_act";
+    if (!a) return set_error(FP8_ERR_INVALID_ARG, "%s: args is NULL", what);
+    if ((a->fa != FP8_E4M3 && a->fa != FP8_E5M2) || (a->fb != FP8_E4M3 && a->fb != FP8_E5M2) ||
+        (a->q && a->q_format != FP8_E4M3 && a->q_format != FP8_E5M2))
+        return set_error(FP8_ERR_INVALID_ARG, "%s: unknown FP8 format", what);
+    for (int g : {a->ga & ~FP8_SCALE_POW2, a->gb & ~FP8_SCALE_POW2}) {
+        if (g < FP8_GRAN_TENSOR || g > FP8_GRAN_ROW)
+            return set_error(FP8_ERR_INVALID_ARG, "%s: unknown scale granularity", what);
+        if (g != FP8_GRAN_TENSOR && g != FP8_GRAN_ROW)
+            return set_error(FP8_ERR_UNSUPPORTED, "%s: built for per-tensor and per-row scales", what);
+    }
+    if ((a->ga | a->gb) & FP8_SCALE_POW2)
+        return set_error(FP8_ERR_INVALID_ARG, "%s: FP8_SCALE_POW2 is for block scales", what);
+    if (a->act < FP8_ACT_NONE || a->act > FP8_ACT_GELU_TANH)
+        return set_error(FP8_ERR_INVALID_ARG, "%s: unknown activation %d", what, a->act);
+    if (a->M < 0 || a->N < 16 || a->K < 16 || a->N % 16 || a->K % 16)
+        return set_error(FP8_ERR_SHAPE, "%s: M must be >= 0, N and K positive multiples of 16", what);
+    if (a->experts < 1 || a->experts > kMaxGemmExperts || (!a->offsets && a->experts != 1))
+        return set_error(FP8_ERR_SHAPE, "%s: experts in 1..%d, 1 without offsets", what, kMaxGemmExperts);
+    const int64_t b_rows = a->gated ? 2 * a->N : a->N;
+    const int64_t limit = (int64_t{1} << 31) - 1024;   // coordinates and units are 32-bit
+    if (a->M > limit || b_rows > limit / a->experts || a->K > limit ||
+        (a->M / 128 + a->experts) * (a->N / 32 + 1) > limit)
+        return set_error(FP8_ERR_SHAPE, "%s: dimensions out of range", what);
+    if (!a->scale_inv_a || !a->scale_inv_b || !a->B || (!a->A && a->M))
+        return set_error(FP8_ERR_INVALID_ARG, "%s: NULL pointer", what);
+    if (!a->d && !a->q && a->M) return set_error(FP8_ERR_INVALID_ARG, "%s: d and q are NULL", what);
+    if (a->q ? !a->q_scale : (a->M && (a->q_scale || a->amax)))
+        return set_error(FP8_ERR_INVALID_ARG, "%s: q and q_scale go together, amax with them", what);
+    for (const void* t : {static_cast<const void*>(a->A), static_cast<const void*>(a->B), a->bias,
+                          a->residual, static_cast<const void*>(a->z), static_cast<const void*>(a->d),
+                          static_cast<const void*>(a->q)})
+        if (!aligned(t, 16)) return set_error(FP8_ERR_ALIGN, "%s: tensors must be 16-byte aligned", what);
+    for (const void* t : {static_cast<const void*>(a->scale_inv_a), static_cast<const void*>(a->scale_inv_b),
+                          static_cast<const void*>(a->q_scale), static_cast<const void*>(a->amax),
+                          static_cast<const void*>(a->offsets)})
+        if (!aligned(t, 4)) return set_error(FP8_ERR_ALIGN, "%s: scales and offsets must be 4-byte aligned", what);
+    cudaStream_t st = as_stream(stream);
+    if (a->amax) launch_zero_words(a->amax, 1, st);
+    if (a->M == 0) return launch_status(what);
+
+    ActParams p{};
+    p.M = a->M; p.N = a->N; p.K = a->K;
+    p.num_kb = static_cast<int>((a->K + BK - 1) / BK);
+    p.fa = a->fa; p.fb = a->fb; p.ga = a->ga; p.gb = a->gb;
+    p.sa = a->scale_inv_a; p.sb = a->scale_inv_b;
+    p.act = a->act;
+    p.bias = static_cast<const __nv_bfloat16*>(a->bias);
+    p.residual = static_cast<const __nv_bfloat16*>(a->residual);
+    p.has_z = a->z != nullptr; p.has_d = a->d != nullptr; p.has_q = a->q != nullptr;
+    p.q_fmt = a->q_format; p.q_scale = a->q_scale; p.amax = a->amax;
+    p.offsets = a->offsets; p.experts = a->experts;
+    p.group = raster_group(a->K);
+    p.status = device_status_word();
+    OutMaps maps{};
+    int r = FP8_OK;
+    const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const auto sw = CU_TENSOR_MAP_SWIZZLE_64B;
+    if (a->z) r = make_output_map(&maps.z, a->z, a->M, a->N, b_rows * 2, bf, 32, sw);
+    if (r == FP8_OK && a->z && a->gated)
+        r = make_output_map(&maps.z_up, static_cast<__nv_bfloat16*>(a->z) + a->N, a->M, a->N,
+                            b_rows * 2, bf, 32, sw);
+    if (r == FP8_OK && a->d) r = make_output_map(&maps.d, a->d, a->M, a->N, a->N * 2, bf, 32, sw);
+    if (r == FP8_OK && a->q)
+        r = make_output_map(&maps.q, a->q, a->M, a->N, a->N, CU_TENSOR_MAP_DATA_TYPE_UINT8, 32,
+                            CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (r != FP8_OK) return r;
+    return a->gated ? launch_pair<true>(a, p, maps, st) : launch_pair<false>(a, p, maps, st);
+}
+
+size_t fp8_act_bwd_workspace_size(int64_t M, int64_t N, int gated) {
+    if (M < 0 || N < 16 || N % 16) return 0;
+    return static_cast<size_t>((M + kBwdRows - 1) / kBwdRows) * static_cast<size_t>(gated ? 2 * N : N) * 4;
+}
+
+int fp8_act_bwd(const fp8_act_bwd_args_t* a, void* workspace, size_t workspace_bytes, void* stream) {
+    const char* what = "fp8_act_bwd";
+    if (!a) return set_error(FP8_ERR_INVALID_ARG, "%s: args is NULL", what);
+    if (a->act < FP8_ACT_NONE || a->act > FP8_ACT_GELU_TANH)
+        return set_error(FP8_ERR_INVALID_ARG, "%s: unknown activation %d", what, a->act);
+    if (a->M < 0 || a->N < 16 || a->N % 16 || a->N > (int64_t{1} << 30))
+        return set_error(FP8_ERR_SHAPE, "%s: M must be >= 0, N a positive multiple of 16", what);
+    const int64_t col_blocks = (a->N + 255) / 256, row_blocks = (a->M + kBwdRows - 1) / kBwdRows;
+    if (a->M > (int64_t{1} << 31) || row_blocks * col_blocks >= (int64_t{1} << 31))
+        return set_error(FP8_ERR_SHAPE, "%s: dimensions out of range", what);
+    if ((!a->dD || !a->z) && a->M) return set_error(FP8_ERR_INVALID_ARG, "%s: NULL pointer", what);
+    if (!a->dz && !a->q && !a->dbias && a->M)
+        return set_error(FP8_ERR_INVALID_ARG, "%s: no output", what);
+    if (a->q && a->q_format != FP8_E4M3 && a->q_format != FP8_E5M2)
+        return set_error(FP8_ERR_INVALID_ARG, "%s: unknown FP8 format", what);
+    if (a->q ? !a->q_scale : (a->M && (a->q_scale || a->amax)))
+        return set_error(FP8_ERR_INVALID_ARG, "%s: q and q_scale go together, amax with them", what);
+    const size_t need = a->dbias ? fp8_act_bwd_workspace_size(a->M, a->N, a->gated) : 0;
+    if (need && (!workspace || workspace_bytes < need))
+        return set_error(FP8_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", what,
+                         workspace ? workspace_bytes : size_t{0}, need);
+    for (const void* t : {a->dD, a->z, static_cast<const void*>(a->dz), static_cast<const void*>(a->q),
+                          static_cast<const void*>(need ? workspace : nullptr)})
+        if (!aligned(t, 16))
+            return set_error(FP8_ERR_ALIGN, "%s: tensors and workspace must be 16-byte aligned", what);
+    for (const void* t : {static_cast<const void*>(a->q_scale), static_cast<const void*>(a->amax),
+                          static_cast<const void*>(a->dbias)})
+        if (!aligned(t, 4)) return set_error(FP8_ERR_ALIGN, "%s: q_scale, amax and dbias must be 4-byte aligned", what);
+    cudaStream_t st = as_stream(stream);
+    const int64_t width = a->gated ? 2 * a->N : a->N;
+    if (a->amax) launch_zero_words(a->amax, 1, st);
+    if (a->M) {
+        ActBwd p{};
+        p.d = static_cast<const __nv_bfloat16*>(a->dD);
+        p.z = static_cast<const __nv_bfloat16*>(a->z);
+        p.dz = static_cast<__nv_bfloat16*>(a->dz);
+        p.q = a->q; p.q_scale = a->q_scale; p.q_fmt = a->q_format; p.amax = a->amax;
+        p.part = a->dbias ? static_cast<float*>(workspace) : nullptr;
+        p.M = a->M; p.N = a->N; p.col_blocks = col_blocks;
+        const unsigned ctas = static_cast<unsigned>(row_blocks * col_blocks);
+        const bool gated = a->gated != 0;
+        switch (a->act) {
+            case FP8_ACT_RELU: launch_act_bwd<FP8_ACT_RELU>(p, gated, ctas, st); break;
+            case FP8_ACT_SILU: launch_act_bwd<FP8_ACT_SILU>(p, gated, ctas, st); break;
+            case FP8_ACT_GELU: launch_act_bwd<FP8_ACT_GELU>(p, gated, ctas, st); break;
+            case FP8_ACT_GELU_TANH: launch_act_bwd<FP8_ACT_GELU_TANH>(p, gated, ctas, st); break;
+            default: launch_act_bwd<FP8_ACT_NONE>(p, gated, ctas, st); break;
+        }
+    }
+    if (a->dbias)
+        launch_column_sums(static_cast<const float*>(workspace), row_blocks, width, a->dbias,
+                           a->accumulate, st);
+    return launch_status(what);
+}
+
+}  // extern "C"

@@ -39,6 +39,23 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 int make_bf16_box_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols,
                       uint32_t box_cols, uint32_t box_rows);
 
+// Tensor map of a K-contiguous FP8 matrix [rows x K]: boxes of 128 bytes of K
+// by box_rows rows, 128-byte swizzle, zero fill outside the matrix.
+int make_kmajor_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t K, uint32_t box_rows);
+
+// Tensor map of an output [rows x cols] with rows row_bytes apart, for TMA
+// stores of boxes of 32 rows x box_cols columns.
+int make_output_map(CUtensorMap* map, void* ptr, int64_t rows, int64_t cols, int64_t row_bytes,
+                    CUtensorMapDataType type, uint32_t box_cols, CUtensorMapSwizzle swizzle);
+
+// out[c] (+)= sum over i < n of part[i][c], c < width, in a fixed order.
+void launch_column_sums(const float* part, int64_t n, int64_t width, float* out, int accumulate,
+                        cudaStream_t stream);
+
+// One launch that sets n (small) 32-bit words to zero, e.g. an amax before the
+// kernel that raises it.
+void launch_zero_words(void* p, int n, cudaStream_t stream);
+
 // Number of SMs of the current device (cached per device).
 int num_sms();
 

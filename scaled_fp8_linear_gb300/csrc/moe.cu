@@ -1,0 +1,549 @@
+// moe.cu -- tokens sorted by expert and back, around the experts' linears.
+//
+//   plan         a stable counting sort of the (token, slot) pairs by expert:
+//                row(t, j) = offset[e] + #{pairs before (t, j) with expert e}
+//   permute      xs[row] = x[token]                    (pad rows zero)
+//   unpermute    y[t] = sum_j w[t, j] ys[row(t, j)]    (fp32, j ascending)
+//   its gradient dys[row] = w[t, j] dy[t],  dw[t, j] = <dy[t], ys[row]>
+//
+// All of them move rows: the bound is HBM.  The copies go token by token, so
+// that a token's row is read once for its k copies, and every sum runs in a
+// fixed order, so that equal calls give equal bits.
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/fp8linear.h"
+#include "internal.h"
+#include "ptx.cuh"
+#include "rowops.cuh"
+
+namespace fp8 {
+namespace {
+
+constexpr int kPlanThreads = 256, kPlanWarps = kPlanThreads / 32;
+constexpr int kMaxExperts = 1024, kMaxSlots = 64;
+// One CTA ranks up to this many pairs: past it the per-CTA histograms of a
+// first launch cost less than the walk of one CTA over all pairs.
+constexpr int kPlanOneCta = 2048;
+constexpr int kPlanChunk = 1024;   // pairs a CTA at least
+constexpr int kPlanMaxCtas = 128;  // so that summing the CTAs' histograms stays short
+
+struct PlanGrid {
+    int ctas, chunk;
+};
+
+PlanGrid plan_grid(int64_t n) {
+    if (n <= kPlanOneCta) return {1, static_cast<int>((n + 31) / 32 * 32)};
+    int64_t chunk = (n + kPlanMaxCtas - 1) / kPlanMaxCtas;
+    if (chunk < kPlanChunk) chunk = kPlanChunk;
+    chunk = (chunk + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
+    return {static_cast<int>((n + chunk - 1) / chunk), static_cast<int>(chunk)};
+}
+
+// hist[cta][e]: how many of the CTA's pairs go to expert e.
+__global__ void __launch_bounds__(kPlanThreads)
+    moe_hist_kernel(const int32_t* __restrict__ ids, int n, int experts, int chunk,
+                    int32_t* __restrict__ hist) {
+    ptx::griddep_launch_dependents();
+    __shared__ int h[kMaxExperts];
+    for (int e = threadIdx.x; e < experts; e += kPlanThreads) h[e] = 0;
+    __syncthreads();
+    ptx::griddep_wait();
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * chunk;
+    for (int i = threadIdx.x; i < chunk; i += kPlanThreads) {
+        const int64_t at = first + i;
+        if (at < n) {
+            const int e = ids[at];
+            if (e >= 0 && e < experts) atomicAdd(&h[e], 1);   // integers: any order
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < experts; e += kPlanThreads)
+        hist[static_cast<int64_t>(blockIdx.x) * experts + e] = h[e];
+}
+
+// Ranks and writes the CTA's chunk of pairs.  Each warp owns a contiguous
+// part of the chunk: it counts its pairs per expert (lanes with the same
+// expert find one another with a match), the counts become starting rows by
+// a sum over the CTAs and warps before it, and a second walk hands the rows
+// out in order.  Every CTA sums all CTAs' histograms itself (ctas x experts
+// words from L2), which saves a launch.
+__global__ void __launch_bounds__(kPlanThreads)
+    moe_place_kernel(const int32_t* __restrict__ ids, int n, int experts, int align, int chunk,
+                     const int32_t* __restrict__ hist, int32_t* __restrict__ offsets,
+                     int32_t* __restrict__ counts, int32_t* __restrict__ row_of,
+                     int32_t* __restrict__ src, int rows) {
+    ptx::griddep_launch_dependents();
+    __shared__ int cnt[kPlanWarps][kMaxExperts];   // counts, then next rows
+    __shared__ int total[kMaxExperts + 1], start[kMaxExperts + 1];
+    __shared__ int warp_tot[kPlanWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int e = lane; e < experts; e += 32) cnt[warp][e] = 0;
+    __syncwarp();
+    ptx::griddep_wait();
+    const int per_warp = (chunk + kPlanWarps * 32 - 1) / (kPlanWarps * 32) * 32;
+    const int64_t cta_first = static_cast<int64_t>(blockIdx.x) * chunk;
+    const int64_t cta_end = cta_first + chunk < n ? cta_first + chunk : n;
+    const int64_t first = cta_first + static_cast<int64_t>(warp) * per_warp;
+    const int64_t end = first + per_warp < cta_end ? first + per_warp : cta_end;
+    const uint32_t below = (1u << lane) - 1u;
+
+    for (int64_t i = first; i < end; i += 32) {
+        const int64_t at = i + lane;
+        int e = at < end ? ids[at] : -1;
+        if (e >= experts) e = -1;
+        const uint32_t same = __match_any_sync(row::kAll, e);
+        if (e >= 0 && (same & below) == 0) cnt[warp][e] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    // per expert: pairs in the CTAs before this one, and in all
+    for (int e = threadIdx.x; e < experts; e += kPlanThreads) {
+        int own = 0;
+#pragma unroll
+        for (int w = 0; w < kPlanWarps; ++w) own += cnt[w][e];
+        int before = 0, all = own;
+        if (hist) {
+            all = 0;
+#pragma unroll 8
+            for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
+                const int h = hist[static_cast<int64_t>(b) * experts + e];
+                all += h;
+                before += b < static_cast<int>(blockIdx.x) ? h : 0;
+            }
+        }
+        total[e] = all;
+        start[e] = before;
+    }
+    __syncthreads();
+    // offsets: the exclusive sum of the padded totals, four experts a thread
+    constexpr int kPer = kMaxExperts / kPlanThreads;
+    int pad[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = static_cast<int>(threadIdx.x) * kPer + i;
+        pad[i] = e < experts ? (total[e] + align - 1) / align * align : 0;
+        sum += pad[i];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(row::kAll, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_tot[warp] = incl;
+    __syncthreads();
+    int run = incl - sum;
+    for (int w = 0; w < warp; ++w) run += warp_tot[w];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = static_cast<int>(threadIdx.x) * kPer + i;
+        if (e < experts) {
+            if (blockIdx.x == 0) {
+                offsets[e] = run;
+                counts[e] = total[e];
+            }
+            // pad rows of the experts that this CTA is dealt
+            if (e % static_cast<int>(gridDim.x) == static_cast<int>(blockIdx.x))
+                for (int r = run + total[e]; r < run + pad[i]; ++r) src[r] = -1;
+            int next = run + start[e];
+            for (int w = 0; w < kPlanWarps; ++w) {
+                const int c = cnt[w][e];
+                cnt[w][e] = next;
+                next += c;
+            }
+        }
+        run += pad[i];
+        if (e == experts - 1) {
+            start[experts] = run;
+            if (blockIdx.x == 0) offsets[experts] = run;
+        }
+    }
+    __syncthreads();
+    for (int64_t r = start[experts] + static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x;
+         r < rows; r += static_cast<int64_t>(gridDim.x) * kPlanThreads)
+        src[r] = -1;
+    for (int64_t i = first; i < end; i += 32) {
+        const int64_t at = i + lane;
+        int e = at < end ? ids[at] : -1;
+        if (e >= experts) e = -1;
+        const uint32_t same = __match_any_sync(row::kAll, e);
+        int r = -1;
+        if (e >= 0) r = cnt[warp][e] + __popc(same & below);
+        __syncwarp();
+        if (e >= 0 && (same & below) == 0) cnt[warp][e] += __popc(same);
+        __syncwarp();
+        if (at < end) {
+            row_of[at] = r;
+            if (r >= 0) src[r] = static_cast<int32_t>(at);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ row copies
+
+// How a CTA of 256 threads is dealt to rows: `lanes` threads a row (a power
+// of two), 256 / lanes rows at a time.
+constexpr int kRowThreads = 256;
+
+int lanes_for(int64_t pieces) {
+    int l = 8;
+    while (l < kRowThreads && l < pieces) l <<= 1;
+    return l;
+}
+
+// xs[row_of[t, j]] = x[t] for every slot j; V is the copied unit.  CTAs past
+// the tokens' set the pad rows (src < 0) to zero.
+template <typename V>
+__global__ void __launch_bounds__(kRowThreads)
+    moe_permute_kernel(const V* __restrict__ x, const float* __restrict__ scale, int64_t tokens,
+                       int slots, int64_t units, const int32_t* __restrict__ row_of,
+                       const int32_t* __restrict__ src, int64_t rows, V* __restrict__ xs,
+                       float* __restrict__ scale_s, int lanes, int64_t token_ctas) {
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const int sub = threadIdx.x / lanes, lane = threadIdx.x % lanes, per = kRowThreads / lanes;
+    if (blockIdx.x < token_ctas) {
+        const int64_t t = static_cast<int64_t>(blockIdx.x) * per + sub;
+        if (t >= tokens) return;
+        const int32_t* to = row_of + t * slots;
+        for (int64_t u = lane; u < units; u += lanes) {
+            const V v = x[t * units + u];
+            for (int j = 0; j < slots; ++j) {
+                const int64_t r = to[j];
+                if (r >= 0 && r < rows) xs[r * units + u] = v;
+            }
+        }
+        if (scale && lane == 0)
+            for (int j = 0; j < slots; ++j)
+                if (to[j] >= 0 && to[j] < rows) scale_s[to[j]] = scale[t];
+    } else {
+        const V zero{};
+        for (int64_t r = (blockIdx.x - token_ctas) * per + sub; r < rows;
+             r += (gridDim.x - token_ctas) * per) {
+            if (src[r] >= 0) continue;
+            for (int64_t u = lane; u < units; u += lanes) xs[r * units + u] = zero;
+            if (scale && lane == 0) scale_s[r] = 0.0f;
+        }
+    }
+}
+
+// Elements of type T (bf16 or fp32) as fp32, N at a time.
+template <typename T, int N>
+struct Piece;
+template <>
+struct Piece<__nv_bfloat16, 8> {
+    static __device__ __forceinline__ void load(float (&v)[8], const __nv_bfloat16* p) {
+        row::unpack8(v, row::ld_stream(p));
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[8]) {
+        *reinterpret_cast<uint4*>(p) = row::pack8(v);
+    }
+};
+template <>
+struct Piece<float, 4> {
+    static __device__ __forceinline__ void load(float (&v)[4], const float* p) {
+        const uint4 w = row::ld_stream(p);
+        v[0] = __uint_as_float(w.x); v[1] = __uint_as_float(w.y);
+        v[2] = __uint_as_float(w.z); v[3] = __uint_as_float(w.w);
+    }
+    static __device__ __forceinline__ void store(float* p, const float (&v)[4]) {
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+};
+template <>
+struct Piece<__nv_bfloat16, 1> {
+    static __device__ __forceinline__ void load(float (&v)[1], const __nv_bfloat16* p) {
+        v[0] = __bfloat162float(*p);
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[1]) {
+        *p = __float2bfloat16_rn(v[0]);
+    }
+};
+template <>
+struct Piece<float, 1> {
+    static __device__ __forceinline__ void load(float (&v)[1], const float* p) { v[0] = *p; }
+    static __device__ __forceinline__ void store(float* p, const float (&v)[1]) { *p = v[0]; }
+};
+
+// y[t] = sum_j w[t, j] ys[row_of[t, j]] (w null: 1), fp32 in the order of j,
+// rounded once.
+template <typename T, int N>
+__global__ void __launch_bounds__(kRowThreads)
+    moe_unpermute_kernel(const T* __restrict__ ys, const int32_t* __restrict__ row_of,
+                         const float* __restrict__ w, int64_t tokens, int slots, int64_t width,
+                         int64_t rows, T* __restrict__ y, int lanes) {
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const int sub = threadIdx.x / lanes, lane = threadIdx.x % lanes, per = kRowThreads / lanes;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * per + sub;
+    if (t >= tokens) return;
+    const int32_t* from = row_of + t * slots;
+    for (int64_t c = static_cast<int64_t>(lane) * N; c < width; c += static_cast<int64_t>(lanes) * N) {
+        float acc[N] = {};
+        for (int j = 0; j < slots; ++j) {
+            const int64_t r = from[j];
+            if (r < 0 || r >= rows) continue;
+            float v[N];
+            Piece<T, N>::load(v, ys + r * width + c);
+            const float f = w ? w[t * slots + j] : 1.0f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) acc[e] = fmaf(f, v[e], acc[e]);
+        }
+        Piece<T, N>::store(y + t * width + c, acc);
+    }
+}
+
+// The gradient of the weighted sum, token by token: dys[row] = w dy[t] and
+// dw[t, j] = <dy[t], ys[row]>, so dy is read once for its k rows.  A CTA is a
+// token; CTAs past the tokens set the pad rows to zero.
+template <typename T, int N>
+__global__ void __launch_bounds__(kRowThreads)
+    moe_unpermute_bwd_kernel(const T* __restrict__ dy, const T* __restrict__ ys,
+                             const int32_t* __restrict__ row_of, const int32_t* __restrict__ src,
+                             const float* __restrict__ w, int64_t tokens, int slots, int64_t width,
+                             int64_t rows, T* __restrict__ dys, float* __restrict__ dw) {
+    ptx::griddep_launch_dependents();
+    __shared__ float part[kRowThreads / 32][kMaxSlots];
+    ptx::griddep_wait();
+    if (blockIdx.x >= tokens) {
+        const float zero[N] = {};
+        for (int64_t r = blockIdx.x - tokens; r < rows; r += gridDim.x - tokens) {
+            if (src[r] >= 0) continue;
+            for (int64_t c = static_cast<int64_t>(threadIdx.x) * N; c < width; c += kRowThreads * N)
+                Piece<T, N>::store(dys + r * width + c, zero);
+        }
+        return;
+    }
+    const int64_t t = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t* to = row_of + t * slots;
+    for (int j = 0; j < slots; ++j) {
+        const int64_t r = to[j];
+        const float f = w ? w[t * slots + j] : 1.0f;
+        float dot = 0.0f;
+        if (r >= 0 && r < rows) {
+            for (int64_t c = static_cast<int64_t>(threadIdx.x) * N; c < width; c += kRowThreads * N) {
+                float g[N], v[N], o[N];
+                Piece<T, N>::load(g, dy + t * width + c);
+                Piece<T, N>::load(v, ys + r * width + c);
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    dot = fmaf(g[e], v[e], dot);
+                    o[e] = f * g[e];
+                }
+                Piece<T, N>::store(dys + r * width + c, o);
+            }
+        }
+        dot = row::warp_sum(dot);
+        if (lane == 0) part[warp][j] = dot;
+    }
+    __syncthreads();
+    if (dw && static_cast<int>(threadIdx.x) < slots) {
+        float s = 0.0f;
+        for (int i = 0; i < kRowThreads / 32; ++i) s += part[i][threadIdx.x];
+        dw[t * slots + threadIdx.x] = s;
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
+
+int launch_status(const char* what) {
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? FP8_OK : set_error(FP8_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+int check_routing(const char* what, int64_t tokens, int slots, int64_t rows) {
+    if (tokens < 0 || slots < 1 || slots > kMaxSlots || rows < 0)
+        return set_error(FP8_ERR_SHAPE, "%s: tokens and rows must be >= 0, slots in 1..%d", what,
+                         kMaxSlots);
+    if (tokens * slots >= (int64_t{1} << 31) || rows >= (int64_t{1} << 31))
+        return set_error(FP8_ERR_SHAPE, "%s: tokens x slots and rows must be below 2^31", what);
+    return FP8_OK;
+}
+
+template <typename V>
+void launch_permute(const void* x, const float* scale, int64_t tokens, int slots, int64_t row_bytes,
+                    const int32_t* row_of, const int32_t* src, int64_t rows, void* xs,
+                    float* scale_s, cudaStream_t st) {
+    const int64_t units = row_bytes / static_cast<int64_t>(sizeof(V));
+    const int lanes = lanes_for(units), per = kRowThreads / lanes;
+    const int64_t token_ctas = (tokens + per - 1) / per;
+    const int64_t want = (rows + per * 16 - 1) / (per * 16);
+    const int64_t pad_ctas = want < 1 ? 1 : (want > 8 * num_sms() ? 8 * num_sms() : want);
+    launch_pdl(moe_permute_kernel<V>, dim3(static_cast<unsigned>(token_ctas + pad_ctas)),
+               dim3(kRowThreads), 0, st, static_cast<const V*>(x), scale, tokens, slots, units,
+               row_of, src, rows, static_cast<V*>(xs), scale_s, lanes, token_ctas);
+}
+
+template <typename T, int N>
+void launch_unpermute(const void* ys, const int32_t* row_of, const float* w, int64_t tokens,
+                      int slots, int64_t width, int64_t rows, void* y, cudaStream_t st) {
+    const int lanes = lanes_for((width + N - 1) / N), per = kRowThreads / lanes;
+    launch_pdl(moe_unpermute_kernel<T, N>, dim3(static_cast<unsigned>((tokens + per - 1) / per)),
+               dim3(kRowThreads), 0, st, static_cast<const T*>(ys), row_of, w, tokens, slots, width, rows,
+               static_cast<T*>(y), lanes);
+}
+
+template <typename T, int N>
+void launch_unpermute_bwd(const void* dy, const void* ys, const int32_t* row_of, const int32_t* src,
+                          const float* w, int64_t tokens, int slots, int64_t width, int64_t rows,
+                          void* dys, float* dw, cudaStream_t st) {
+    const int64_t want = (rows + 15) / 16;
+    const int64_t pad_ctas = want < 1 ? 1 : (want > 8 * num_sms() ? 8 * num_sms() : want);
+    launch_pdl(moe_unpermute_bwd_kernel<T, N>, dim3(static_cast<unsigned>(tokens + pad_ctas)),
+               dim3(kRowThreads), 0, st, static_cast<const T*>(dy), static_cast<const T*>(ys), row_of,
+               src, w, tokens, slots, width, rows, static_cast<T*>(dys), dw);
+}
+
+}  // namespace
+}  // namespace fp8
+
+using namespace fp8;
+
+extern "C" {
+
+int64_t fp8_moe_rows(int64_t tokens, int slots, int experts, int align) {
+    if (tokens < 0 || slots < 1 || slots > kMaxSlots || experts < 1 || experts > kMaxExperts ||
+        align < 1 || align > 4096 || tokens >= (int64_t{1} << 31))
+        return -1;
+    const int64_t n = tokens * slots;
+    return n + (n < experts ? n : experts) * (align - 1);
+}
+
+size_t fp8_moe_workspace_size(int64_t tokens, int slots, int experts) {
+    if (fp8_moe_rows(tokens, slots, experts, 1) < 0) return 0;
+    const PlanGrid g = plan_grid(tokens * slots);
+    return g.ctas > 1 ? static_cast<size_t>(g.ctas) * experts * sizeof(int32_t) : 0;
+}
+
+int fp8_moe_plan(const int32_t* ids, int64_t tokens, int slots, int experts, int align,
+                 int32_t* offsets, int32_t* counts, int32_t* row_of, int32_t* src, int64_t rows,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+    const int st = check_routing("fp8_moe_plan", tokens, slots, rows);
+    if (st != FP8_OK) return st;
+    if (experts < 1 || experts > kMaxExperts)
+        return set_error(FP8_ERR_SHAPE, "fp8_moe_plan: experts %d outside 1..%d", experts, kMaxExperts);
+    if (align < 1 || align > 4096)
+        return set_error(FP8_ERR_SHAPE, "fp8_moe_plan: align %d outside 1..4096", align);
+    const int64_t need_rows = fp8_moe_rows(tokens, slots, experts, align);
+    if (need_rows >= (int64_t{1} << 31) || rows < need_rows)
+        return set_error(FP8_ERR_SHAPE, "fp8_moe_plan: %lld rows, %lld needed (fp8_moe_rows)",
+                         static_cast<long long>(rows), static_cast<long long>(need_rows));
+    if (!offsets || !counts || ((!ids || !row_of) && tokens) || (!src && rows))
+        return set_error(FP8_ERR_INVALID_ARG, "fp8_moe_plan: NULL pointer");
+    if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(counts, 4) || !aligned(row_of, 4) ||
+        !aligned(src, 4) || !aligned(workspace, 4))
+        return set_error(FP8_ERR_ALIGN, "fp8_moe_plan: pointers must be 4-byte aligned");
+    const int n = static_cast<int>(tokens * slots);
+    const PlanGrid g = plan_grid(n);
+    const size_t need = fp8_moe_workspace_size(tokens, slots, experts);
+    if (need && (!workspace || workspace_bytes < need))
+        return set_error(FP8_ERR_INVALID_ARG, "fp8_moe_plan: workspace of %zu bytes, %zu needed",
+                         workspace ? workspace_bytes : size_t{0}, need);
+    int32_t* hist = nullptr;
+    if (g.ctas > 1) {
+        hist = static_cast<int32_t*>(workspace);
+        launch_pdl(moe_hist_kernel, dim3(g.ctas), dim3(kPlanThreads), 0, as_stream(stream), ids, n,
+                   experts, g.chunk, hist);
+    }
+    launch_pdl(moe_place_kernel, dim3(g.ctas), dim3(kPlanThreads), 0, as_stream(stream), ids, n,
+               experts, align, g.chunk, static_cast<const int32_t*>(hist), offsets, counts, row_of,
+               src, static_cast<int>(rows));
+    return launch_status("fp8_moe_plan");
+}
+
+int fp8_moe_permute(const void* x, const float* scale, int64_t tokens, int slots, int64_t row_bytes,
+                    const int32_t* row_of, const int32_t* src, int64_t rows, void* xs,
+                    float* scale_s, void* stream) {
+    const int st = check_routing("fp8_moe_permute", tokens, slots, rows);
+    if (st != FP8_OK) return st;
+    if (row_bytes < 1 || row_bytes > (int64_t{1} << 24))
+        return set_error(FP8_ERR_SHAPE, "fp8_moe_permute: row of %lld bytes outside 1..2^24",
+                         static_cast<long long>(row_bytes));
+    if (((!x || !row_of) && tokens) || ((!xs || !src) && rows))
+        return set_error(FP8_ERR_INVALID_ARG, "fp8_moe_permute: NULL pointer");
+    if ((scale != nullptr) != (scale_s != nullptr) && tokens && rows)
+        return set_error(FP8_ERR_INVALID_ARG, "fp8_moe_permute: scale and scale_s go together");
+    if (!aligned(x, 16) || !aligned(xs, 16) || !aligned(row_of, 4) || !aligned(src, 4) ||
+        !aligned(scale, 4) || !aligned(scale_s, 4))
+        return set_error(FP8_ERR_ALIGN,
+                         "fp8_moe_permute: x and xs must be 16-byte aligned, the rest 4-byte");
+    if (!rows) return FP8_OK;
+    // the widest unit that the row's length lets every row start on
+    if (row_bytes % 16 == 0)
+        launch_permute<uint4>(x, scale, tokens, slots, row_bytes, row_of, src, rows, xs, scale_s, as_stream(stream));
+    else if (row_bytes % 4 == 0)
+        launch_permute<uint32_t>(x, scale, tokens, slots, row_bytes, row_of, src, rows, xs, scale_s, as_stream(stream));
+    else if (row_bytes % 2 == 0)
+        launch_permute<uint16_t>(x, scale, tokens, slots, row_bytes, row_of, src, rows, xs, scale_s, as_stream(stream));
+    else
+        launch_permute<uint8_t>(x, scale, tokens, slots, row_bytes, row_of, src, rows, xs, scale_s, as_stream(stream));
+    return launch_status("fp8_moe_permute");
+}
+
+int fp8_moe_unpermute(const void* ys, int type, const int32_t* row_of, const float* weights,
+                      int64_t tokens, int slots, int64_t width, int64_t rows, void* y, void* stream) {
+    const int st = check_routing("fp8_moe_unpermute", tokens, slots, rows);
+    if (st != FP8_OK) return st;
+    if (type != FP8_OUT_BF16 && type != FP8_OUT_F32)
+        return set_error(FP8_ERR_INVALID_ARG, "fp8_moe_unpermute: unknown type %d", type);
+    if (width < 0 || width > (int64_t{1} << 22))
+        return set_error(FP8_ERR_SHAPE, "fp8_moe_unpermute: width outside 0..2^22");
+    if ((!row_of || (!y && width)) && tokens)
+        return set_error(FP8_ERR_INVALID_ARG, "fp8_moe_unpermute: NULL pointer");
+    if (!ys && tokens && rows && width)
+        return set_error(FP8_ERR_INVALID_ARG, "fp8_moe_unpermute: NULL pointer");
+    if (!aligned(ys, 16) || !aligned(y, 16) || !aligned(row_of, 4) || !aligned(weights, 4))
+        return set_error(FP8_ERR_ALIGN,
+                         "fp8_moe_unpermute: ys and y must be 16-byte aligned, the rest 4-byte");
+    if (!tokens || !width) return FP8_OK;
+    if (type == FP8_OUT_BF16) {
+        if (width % 8 == 0)
+            launch_unpermute<__nv_bfloat16, 8>(ys, row_of, weights, tokens, slots, width, rows, y, as_stream(stream));
+        else
+            launch_unpermute<__nv_bfloat16, 1>(ys, row_of, weights, tokens, slots, width, rows, y, as_stream(stream));
+    } else if (width % 4 == 0) {
+        launch_unpermute<float, 4>(ys, row_of, weights, tokens, slots, width, rows, y, as_stream(stream));
+    } else {
+        launch_unpermute<float, 1>(ys, row_of, weights, tokens, slots, width, rows, y, as_stream(stream));
+    }
+    return launch_status("fp8_moe_unpermute");
+}
+
+int fp8_moe_unpermute_bwd(const void* dy, const void* ys, int type, const int32_t* row_of,
+                          const int32_t* src, const float* weights, int64_t tokens, int slots,
+                          int64_t width, int64_t rows, void* dys, float* dweights, void* stream) {
+    const int st = check_routing("fp8_moe_unpermute_bwd", tokens, slots, rows);
+    if (st != FP8_OK) return st;
+    if (type != FP8_OUT_BF16 && type != FP8_OUT_F32)
+        return set_error(FP8_ERR_INVALID_ARG, "fp8_moe_unpermute_bwd: unknown type %d", type);
+    if (width < 0 || width > (int64_t{1} << 22))
+        return set_error(FP8_ERR_SHAPE, "fp8_moe_unpermute_bwd: width outside 0..2^22");
+    if (((!dy && width) || !row_of) && tokens)
+        return set_error(FP8_ERR_INVALID_ARG, "fp8_moe_unpermute_bwd: NULL pointer");
+    if ((!src || ((!ys || !dys) && width)) && rows)
+        return set_error(FP8_ERR_INVALID_ARG, "fp8_moe_unpermute_bwd: NULL pointer");
+    if (!aligned(dy, 16) || !aligned(ys, 16) || !aligned(dys, 16) || !aligned(row_of, 4) ||
+        !aligned(src, 4) || !aligned(weights, 4) || !aligned(dweights, 4))
+        return set_error(FP8_ERR_ALIGN, "fp8_moe_unpermute_bwd: dy, ys and dys must be 16-byte "
+                                        "aligned, the rest 4-byte");
+    if (!tokens && !rows) return FP8_OK;
+    if (type == FP8_OUT_BF16) {
+        if (width % 8 == 0)
+            launch_unpermute_bwd<__nv_bfloat16, 8>(dy, ys, row_of, src, weights, tokens, slots, width, rows, dys, dweights, as_stream(stream));
+        else
+            launch_unpermute_bwd<__nv_bfloat16, 1>(dy, ys, row_of, src, weights, tokens, slots, width, rows, dys, dweights, as_stream(stream));
+    } else if (width % 4 == 0) {
+        launch_unpermute_bwd<float, 4>(dy, ys, row_of, src, weights, tokens, slots, width, rows, dys, dweights, as_stream(stream));
+    } else {
+        launch_unpermute_bwd<float, 1>(dy, ys, row_of, src, weights, tokens, slots, width, rows, dys, dweights, as_stream(stream));
+    }
+    return launch_status("fp8_moe_unpermute_bwd");
+}
+
+}  // extern "C"

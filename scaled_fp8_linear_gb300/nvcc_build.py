@@ -16,7 +16,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libfp8linear.so")
-SOURCES = ["quantize.cu", "gemm.cu", "api.cu", "noalloc.cu"]
+SOURCES = ["quantize.cu", "gemm.cu", "api.cu", "noalloc.cu", "norm.cu", "moe.cu",
+           "gemm_act.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
