@@ -13,11 +13,14 @@ kernels on the current (or the given) stream.
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 from typing import NamedTuple, Optional
 
 import torch
 
-from . import (_U8, _check, _ptr, _stream, _vp, E4M3, GRAN_ROW, GRAN_TENSOR, OUT_BF16, OUT_F32)
+from . import (_U8, _ptr, _stream, _vp, E4M3, Fp8Error, GRAN_ROW, GRAN_TENSOR, OUT_BF16, OUT_F32,
+               fp8_last_error)
 from . import lib as _base_lib
 
 __all__ = [
@@ -31,7 +34,7 @@ __all__ = [
 NORM_RMS, NORM_LAYER = 0, 1
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3, 4
 
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_BF16, _F32, _I32, _BYTE = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 _OUT = {_BF16: OUT_BF16, _F32: OUT_F32}
 _i32, _i64, _f32, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 
@@ -70,6 +73,19 @@ class ActBwdArgsC(ctypes.Structure):
     _fields_ = [("M", _i64), ("N", _i64), ("act", _i32), ("gated", _i32), ("dD", _vp), ("z", _vp),
                 ("dz", _vp), ("q", _vp), ("q_format", _i32), ("q_scale", _vp), ("amax", _vp),
                 ("dbias", _vp), ("accumulate", _i32)]
+
+
+# A call's arguments are packed to the C struct's bytes in one go, which takes
+# a third of the time of filling a ctypes.Structure field by field.
+_CODE = {_i32: "i", _i64: "q", _f32: "f", _vp: "P"}
+
+
+def _packer(args):
+    return struct.Struct("@" + "".join(_CODE[t] for _, t in args._fields_)).pack
+
+
+_pack_norm_fwd, _pack_norm_bwd = _packer(NormFwdArgsC), _packer(NormBwdArgsC)
+_pack_gemm_act, _pack_act_bwd = _packer(GemmActArgsC), _packer(ActBwdArgsC)
 
 
 class NormFwd(NamedTuple):
@@ -115,18 +131,23 @@ class MoePlan(NamedTuple):
 _ready = None
 
 
+def _check(status):
+    if status:
+        raise Fp8Error(status, fp8_last_error())
+
+
 def _lib():
     """The library with these calls' signatures declared."""
     global _ready
     if _ready is None:
         L = _base_lib()
-        i, P = ctypes.c_int, ctypes.POINTER
-        L.fp8_norm_fwd.argtypes = [P(NormFwdArgsC), _vp]
-        L.fp8_norm_bwd.argtypes = [P(NormBwdArgsC), _vp, _sz, _vp]
+        i = ctypes.c_int
+        L.fp8_norm_fwd.argtypes = [_vp, _vp]
+        L.fp8_norm_bwd.argtypes = [_vp, _vp, _sz, _vp]
         L.fp8_norm_bwd_workspace_size.argtypes = [_i64, _i64, _i64]
         L.fp8_norm_bwd_workspace_size.restype = _sz
-        L.fp8_gemm_act.argtypes = [P(GemmActArgsC), _vp]
-        L.fp8_act_bwd.argtypes = [P(ActBwdArgsC), _vp, _sz, _vp]
+        L.fp8_gemm_act.argtypes = [_vp, _vp]
+        L.fp8_act_bwd.argtypes = [_vp, _vp, _sz, _vp]
         L.fp8_act_bwd_workspace_size.argtypes = [_i64, _i64, i]
         L.fp8_act_bwd_workspace_size.restype = _sz
         L.fp8_moe_rows.argtypes = [_i64, i, i, i]
@@ -146,10 +167,13 @@ def _lib():
 
 
 def _given(t, what, dtype, shape):
-    """The address of a given tensor of this shape, None for none."""
+    """The address of a given tensor of this type and shape, 0 for none."""
     if t is None:
-        return None
-    p = _ptr(t, what, dtype)
+        return 0
+    if t.__class__ is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_cuda \
+            and t.is_contiguous():
+        return t.data_ptr()
+    p = _ptr(t, what, _U8 if dtype is torch.uint8 else dtype)   # says what is wrong
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     return p
@@ -190,9 +214,10 @@ def fp8_norm_fwd(x, h=None, kind: int = NORM_RMS, eps: float = 1e-5, alpha: floa
     if dt not in _OUT:
         raise TypeError(f"x: dtype {dt}, expected bfloat16 or float32")
     if x_out is None and want_x_out:
-        x_out = torch.empty(T, C, dtype=dt, device=dev)
+        x_out = torch.empty_like(x) if x is not None else torch.empty(T, C, dtype=dt, device=dev)
     if y is None and want_y:
-        y = torch.empty(T, C, dtype=_BF16, device=dev)
+        y = (torch.empty_like(h) if h is not None else torch.empty_like(x) if dt is _BF16 else
+             torch.empty(T, C, dtype=_BF16, device=dev))
     if q_fmt is not None and q is None:
         q = torch.empty(T, C, dtype=torch.uint8, device=dev)
     if q_fmt is not None and q_gran == GRAN_ROW and q_scale_inv is None:
@@ -202,16 +227,16 @@ def fp8_norm_fwd(x, h=None, kind: int = NORM_RMS, eps: float = 1e-5, alpha: floa
     if want_stats and stats is None:
         stats = torch.empty(4, T, dtype=_F32, device=dev)
     gate_rows = 0 if gate is None else _rows(gate, "gate")[0]
-    a = NormFwdArgsC(
+    a = _pack_norm_fwd(
         T, C, kind, _OUT[dt], eps, alpha, _given(x, "x", dt, (T, C)), _given(h, "h", _BF16, (T, C)),
-        _given(gate, "gate", _BF16, (gate_rows, C)), gate_rows, bool(post_norm),
+        _given(gate, "gate", _BF16, (gate_rows, C)), gate_rows, int(bool(post_norm)),
         _given(w_post, "w_post", _F32, (C,)), _given(b_post, "b_post", _F32, (C,)),
         _given(w_pre, "w_pre", _F32, (C,)), _given(b_pre, "b_pre", _F32, (C,)),
         _given(x_out, "x_out", dt, (T, C)), _given(y, "y", _BF16, (T, C)),
-        _given(q, "q", _U8, (T, C)), E4M3 if q_fmt is None else q_fmt, q_gran, bool(pow2),
+        _given(q, "q", _BYTE, (T, C)), E4M3 if q_fmt is None else q_fmt, q_gran, int(bool(pow2)),
         _given(q_scale, "q_scale", _F32, (1,)), _given(q_scale_inv, "q_scale_inv", _F32, (T,)),
         _given(amax, "amax", _F32, (1,)), _given(stats, "stats", _F32, (4, T)))
-    _check(_lib().fp8_norm_fwd(ctypes.byref(a), _stream(stream)))
+    _check(_lib().fp8_norm_fwd(a, _stream(stream)))
     return NormFwd(x_out, y, q, q_scale_inv, amax, stats)
 
 
@@ -255,17 +280,17 @@ def fp8_norm_bwd(dy, x_out, stats, dx_out=None, h=None, kind: int = NORM_RMS, al
     dgate = vec(dgate, gate, (gate_rows, C))
     need = fp8_norm_bwd_workspace_size(T, C, gate_rows)
     ws, ws_bytes, workspace = _workspace(workspace, need, dev)
-    a = NormBwdArgsC(
+    a = _pack_norm_bwd(
         T, C, kind, _OUT[dt], alpha, _given(dy, "dy", _BF16, (T, C)),
         _given(x_out, "x_out", dt, (T, C)), _given(dx_out, "dx_out", dt, (T, C)),
         _given(h, "h", _BF16, (T, C)), _given(gate, "gate", _BF16, (gate_rows, C)), gate_rows,
-        bool(post_norm), _given(w_post, "w_post", _F32, (C,)), _given(b_post, "b_post", _F32, (C,)),
+        int(bool(post_norm)), _given(w_post, "w_post", _F32, (C,)), _given(b_post, "b_post", _F32, (C,)),
         _given(w_pre, "w_pre", _F32, (C,)), _given(stats, "stats", _F32, (4, T)),
         _given(dx, "dx", dt, (T, C)), _given(dh, "dh", _BF16, (T, C)),
         _given(dw_pre, "dw_pre", _F32, (C,)), _given(db_pre, "db_pre", _F32, (C,)),
         _given(dw_post, "dw_post", _F32, (C,)), _given(db_post, "db_post", _F32, (C,)),
-        _given(dgate, "dgate", _F32, (gate_rows, C)), bool(accumulate))
-    _check(_lib().fp8_norm_bwd(ctypes.byref(a), ws, ws_bytes, _stream(stream)))
+        _given(dgate, "dgate", _F32, (gate_rows, C)), int(bool(accumulate)))
+    _check(_lib().fp8_norm_bwd(a, ws, ws_bytes, _stream(stream)))
     return NormBwd(dx, dh, dw_pre, db_pre, dw_post, db_post, dgate)
 
 
@@ -308,15 +333,15 @@ def fp8_gemm_act(A, fa: int, B, fb: int, scale_inv_a, scale_inv_b, ga: int = GRA
         amax = torch.empty(1, dtype=_F32, device=dev)
     per_b = (E,) if offsets is not None else (1,)
     per_row = (E, rows) if offsets is not None else (rows,)
-    a = GemmActArgsC(
-        _ptr(A, "A", _U8), _ptr(B, "B", _U8), fa, fb, M, N, K, ga, gb,
+    a = _pack_gemm_act(
+        _given(A, "A", _BYTE, (M, K)), _given(B, "B", _BYTE, B.shape), fa, fb, M, N, K, ga, gb,
         _given(scale_inv_a, "scale_inv_a", _F32, (M,) if ga == GRAN_ROW else (1,)),
         _given(scale_inv_b, "scale_inv_b", _F32, per_row if gb == GRAN_ROW else per_b), act,
-        bool(gated), _given(bias, "bias", _BF16, per_row), _given(residual, "residual", _BF16, (M, N)),
-        _given(z, "z", _BF16, (M, rows)), _given(d, "d", _BF16, (M, N)), _given(q, "q", _U8, (M, N)),
+        int(bool(gated)), _given(bias, "bias", _BF16, per_row), _given(residual, "residual", _BF16, (M, N)),
+        _given(z, "z", _BF16, (M, rows)), _given(d, "d", _BF16, (M, N)), _given(q, "q", _BYTE, (M, N)),
         E4M3 if q_fmt is None else q_fmt, _given(q_scale, "q_scale", _F32, (1,)),
         _given(amax, "amax", _F32, (1,)), _given(offsets, "offsets", _I32, (E + 1,)), E)
-    _check(_lib().fp8_gemm_act(ctypes.byref(a), _stream(stream)))
+    _check(_lib().fp8_gemm_act(a, _stream(stream)))
     return GemmAct(d, z, q, amax)
 
 
@@ -347,17 +372,18 @@ def fp8_act_bwd(dD, z, act: int, gated: bool = False, want_dz: bool = True, q_fm
     ws = ws_bytes = None
     if dbias is not None:
         ws, ws_bytes, workspace = _workspace(workspace, fp8_act_bwd_workspace_size(M, N, gated), dev)
-    a = ActBwdArgsC(
-        M, N, act, bool(gated), _given(dD, "dD", _BF16, (M, N)), _given(z, "z", _BF16, (M, rows)),
-        _given(dz, "dz", _BF16, (M, rows)), _given(q, "q", _U8, (M, rows)),
+    a = _pack_act_bwd(
+        M, N, act, int(bool(gated)), _given(dD, "dD", _BF16, (M, N)), _given(z, "z", _BF16, (M, rows)),
+        _given(dz, "dz", _BF16, (M, rows)), _given(q, "q", _BYTE, (M, rows)),
         E4M3 if q_fmt is None else q_fmt, _given(q_scale, "q_scale", _F32, (1,)),
-        _given(amax, "amax", _F32, (1,)), _given(dbias, "dbias", _F32, (rows,)), bool(accumulate))
-    _check(_lib().fp8_act_bwd(ctypes.byref(a), ws, ws_bytes or 0, _stream(stream)))
+        _given(amax, "amax", _F32, (1,)), _given(dbias, "dbias", _F32, (rows,)), int(bool(accumulate)))
+    _check(_lib().fp8_act_bwd(a, ws, ws_bytes or 0, _stream(stream)))
     return ActBwd(dz, q, amax, dbias)
 
 
 # ------------------------------------------------------------------ tokens by expert
 
+@functools.lru_cache(maxsize=256)
 def fp8_moe_rows(tokens: int, slots: int, experts: int, align: int = 1) -> int:
     """Rows that hold any routing of this size."""
     r = int(_lib().fp8_moe_rows(tokens, slots, experts, align))
@@ -366,6 +392,7 @@ def fp8_moe_rows(tokens: int, slots: int, experts: int, align: int = 1) -> int:
     return r
 
 
+@functools.lru_cache(maxsize=256)
 def fp8_moe_workspace_size(tokens: int, slots: int, experts: int) -> int:
     return int(_lib().fp8_moe_workspace_size(tokens, slots, experts))
 
@@ -392,7 +419,7 @@ def fp8_moe_plan(ids, experts: int, align: int = 1, rows: int | None = None, off
     if need:
         ws, ws_bytes, workspace = _workspace(workspace, need, dev)
     _check(_lib().fp8_moe_plan(
-        _ptr(ids, "ids", _I32), T, k, experts, align, _given(offsets, "offsets", _I32, (experts + 1,)),
+        _given(ids, "ids", _I32, (T, k)), T, k, experts, align, _given(offsets, "offsets", _I32, (experts + 1,)),
         _given(counts, "counts", _I32, (experts,)), _given(row_of, "row_of", _I32, (T, k)),
         _given(src, "src", _I32, (rows,)), rows, ws, ws_bytes, _stream(stream)))
     return MoePlan(offsets, counts, row_of, src)
@@ -409,7 +436,7 @@ def fp8_moe_permute(x, row_of, src, scale=None, xs=None, scale_s=None, stream=No
     if scale is not None and scale_s is None:
         scale_s = torch.empty(rows, dtype=_F32, device=x.device)
     _check(_lib().fp8_moe_permute(
-        _ptr(x, "x"), _given(scale, "scale", _F32, (T,)), T, k, C * x.element_size(),
+        _given(x, "x", x.dtype, (T, C)), _given(scale, "scale", _F32, (T,)), T, k, C * x.element_size(),
         _given(row_of, "row_of", _I32, (T, k)), _given(src, "src", _I32, (rows,)), rows,
         _given(xs, "xs", x.dtype, (rows, C)), _given(scale_s, "scale_s", _F32, (rows,)),
         _stream(stream)))
@@ -426,7 +453,7 @@ def fp8_moe_unpermute(ys, row_of, weights=None, y=None, stream=None) -> torch.Te
     if y is None:
         y = torch.empty(T, C, dtype=ys.dtype, device=ys.device)
     _check(_lib().fp8_moe_unpermute(
-        _ptr(ys, "ys"), _OUT[ys.dtype], _ptr(row_of, "row_of", _I32),
+        _given(ys, "ys", ys.dtype, (rows, C)), _OUT[ys.dtype], _given(row_of, "row_of", _I32, (T, k)),
         _given(weights, "weights", _F32, (T, k)), T, k, C, rows, _given(y, "y", ys.dtype, (T, C)),
         _stream(stream)))
     return y
@@ -444,8 +471,8 @@ def fp8_moe_unpermute_bwd(dy, ys, row_of, src, weights=None, dys=None, dweights=
     if dweights is None and weights is not None:
         dweights = torch.empty(T, k, dtype=_F32, device=ys.device)
     _check(_lib().fp8_moe_unpermute_bwd(
-        _given(dy, "dy", ys.dtype, (T, C)), _ptr(ys, "ys"), _OUT[ys.dtype],
-        _ptr(row_of, "row_of", _I32), _given(src, "src", _I32, (rows,)),
+        _given(dy, "dy", ys.dtype, (T, C)), _given(ys, "ys", ys.dtype, (rows, C)), _OUT[ys.dtype],
+        _given(row_of, "row_of", _I32, (T, k)), _given(src, "src", _I32, (rows,)),
         _given(weights, "weights", _F32, (T, k)), T, k, C, rows,
         _given(dys, "dys", ys.dtype, (rows, C)), _given(dweights, "dweights", _F32, (T, k)),
         _stream(stream)))

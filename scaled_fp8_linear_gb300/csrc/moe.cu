@@ -9,6 +9,7 @@
 // All of them move rows: the bound is HBM.  The copies go token by token, so
 // that a token's row is read once for its k copies, and every sum runs in a
 // fixed order, so that equal calls give equal bits.
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -229,11 +230,128 @@ __global__ void __launch_bounds__(kRowThreads)
     }
 }
 
+// The same for rows of at least 1 KB in 16-byte units, by bulk copies alone:
+// a warp takes a token's row (or a piece of a long one) into a slot of shared
+// memory and each lane sends it to one of the slots' rows; no register or
+// load unit touches the data.  Three slots a warp: one being filled, one
+// being sent, one whose copies are being waited for.
+constexpr int kBulkSlots = 3;
+constexpr int kBulkSlotBytes = 16384;        // at most; longer rows go in pieces
+constexpr int kBulkSmem = 200 * 1024;
+
+struct BulkRows {
+    const uint8_t* x;
+    const float* scale;
+    const int32_t* row_of;
+    const int32_t* src;
+    uint8_t* xs;
+    float* scale_s;
+    unsigned* status;
+    int64_t tokens, rows, row_bytes;
+    int slots, slot_bytes, pieces;           // pieces a row
+};
+
+__global__ void __launch_bounds__(256)
+    moe_permute_bulk_kernel(const __grid_constant__ BulkRows p) {
+    ptx::griddep_launch_dependents();
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t full[8 * kBulkSlots];
+    __shared__ volatile uint32_t gave_up;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    uint8_t* zeros = smem + nw * kBulkSlots * p.slot_bytes;
+    uint8_t* mine = smem + warp * kBulkSlots * p.slot_bytes;
+    uint64_t* bar = full + warp * kBulkSlots;
+    if (lane == 0)
+        for (int i = 0; i < kBulkSlots; ++i) ptx::mbar_init(&bar[i], 1);
+    if (threadIdx.x == 0) gave_up = 0;
+    ptx::fence_barrier_init();
+    for (int i = threadIdx.x * 16; i < p.slot_bytes; i += blockDim.x * 16)
+        *reinterpret_cast<uint4*>(zeros + i) = make_uint4(0, 0, 0, 0);
+    ptx::fence_proxy_async_smem();   // the zeros are read by bulk copies
+    __syncthreads();
+    ptx::griddep_wait();
+    const int64_t step = static_cast<int64_t>(gridDim.x) * nw;
+    const int64_t first = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
+    const int64_t items = p.tokens * p.pieces;
+    auto bytes_of = [&](int64_t piece) {
+        const int64_t left = p.row_bytes - piece * p.slot_bytes;
+        return static_cast<uint32_t>(left < p.slot_bytes ? left : p.slot_bytes);
+    };
+    uint32_t issued = 0;
+    auto fill = [&](int64_t item) {   // lane 0
+        const int64_t t = item / p.pieces, piece = item - t * p.pieces;
+        uint64_t* b = &bar[issued % kBulkSlots];
+        ptx::mbar_arrive_expect_tx(b, bytes_of(piece));
+        ptx::bulk_load(mine + issued % kBulkSlots * p.slot_bytes,
+                       p.x + t * p.row_bytes + piece * p.slot_bytes, bytes_of(piece), b);
+    };
+    // the first rows on their way, and the first token's destinations
+    for (int i = 0; i < kBulkSlots - 1; ++i) {
+        if (first + i * step >= items) break;
+        if (lane == 0) fill(first + i * step);
+        ++issued;
+    }
+    auto dest = [&](int64_t item, int j) -> int64_t {
+        if (item >= items || j >= p.slots) return -1;
+        const int64_t r = p.row_of[item / p.pieces * p.slots + j];
+        return r < p.rows ? r : -1;
+    };
+    int64_t to0 = dest(first, lane), to1 = dest(first, lane + 32);
+    uint32_t done = 0;
+    bool ok = true;
+    for (int64_t item = first; item < items; item += step) {
+        const int64_t r0 = to0, r1 = to1;
+        to0 = dest(item + step, lane);
+        to1 = dest(item + step, lane + 32);
+        const int64_t t = item / p.pieces, piece = item - t * p.pieces;
+        const uint32_t n = bytes_of(piece);
+        ok = ptx::mbar_wait(&bar[done % kBulkSlots], done / kBulkSlots & 1u, &gave_up);
+        ok = __all_sync(row::kAll, ok);
+        if (!ok) break;
+        const uint8_t* from = mine + done % kBulkSlots * p.slot_bytes;
+        if (r0 >= 0) ptx::bulk_store(p.xs + r0 * p.row_bytes + piece * p.slot_bytes, from, n);
+        if (r1 >= 0) ptx::bulk_store(p.xs + r1 * p.row_bytes + piece * p.slot_bytes, from, n);
+        ptx::bulk_commit_group();
+        if (p.scale && piece == 0) {
+            if (r0 >= 0) p.scale_s[r0] = p.scale[t];
+            if (r1 >= 0) p.scale_s[r1] = p.scale[t];
+        }
+        ++done;
+        // the next fill takes the slot of the item before this one
+        const int64_t next = item + (kBulkSlots - 1) * step;
+        if (next < items) {
+            ptx::bulk_wait_group_read<1>();
+            __syncwarp();
+            if (lane == 0) fill(next);
+            ++issued;
+        }
+    }
+    if (ok) {   // pad rows, 32 at a look
+        const int64_t blocks = (p.rows + 31) / 32;
+        for (int64_t b = first; b < blocks; b += step) {
+            const int64_t r = b * 32 + lane;
+            if (r < p.rows && p.src[r] < 0) {
+                for (int64_t piece = 0; piece < p.pieces; ++piece)
+                    ptx::bulk_store(p.xs + r * p.row_bytes + piece * p.slot_bytes, zeros, bytes_of(piece));
+                if (p.scale) p.scale_s[r] = 0.0f;
+            }
+        }
+        ptx::bulk_commit_group();
+    } else if (lane == 0) {
+        // fills may still be on their way into this CTA's shared memory
+        uint32_t never = 0;
+        for (; done < issued; ++done) ptx::mbar_wait(&bar[done % kBulkSlots], done / kBulkSlots & 1u, &never);
+        if (p.status) atomicOr(p.status, 1u);
+    }
+    ptx::bulk_wait_group_all();
+}
+
 // Elements of type T (bf16 or fp32) as fp32, N at a time.
 template <typename T, int N>
 struct Piece;
 template <>
 struct Piece<__nv_bfloat16, 8> {
+    static __device__ __forceinline__ void open(float (&v)[8], const uint4& w) { row::unpack8(v, w); }
     static __device__ __forceinline__ void load(float (&v)[8], const __nv_bfloat16* p) {
         row::unpack8(v, row::ld_stream(p));
     }
@@ -243,10 +361,12 @@ struct Piece<__nv_bfloat16, 8> {
 };
 template <>
 struct Piece<float, 4> {
-    static __device__ __forceinline__ void load(float (&v)[4], const float* p) {
-        const uint4 w = row::ld_stream(p);
+    static __device__ __forceinline__ void open(float (&v)[4], const uint4& w) {
         v[0] = __uint_as_float(w.x); v[1] = __uint_as_float(w.y);
         v[2] = __uint_as_float(w.z); v[3] = __uint_as_float(w.w);
+    }
+    static __device__ __forceinline__ void load(float (&v)[4], const float* p) {
+        open(v, row::ld_stream(p));
     }
     static __device__ __forceinline__ void store(float* p, const float (&v)[4]) {
         *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
@@ -282,14 +402,23 @@ __global__ void __launch_bounds__(kRowThreads)
     const int32_t* from = row_of + t * slots;
     for (int64_t c = static_cast<int64_t>(lane) * N; c < width; c += static_cast<int64_t>(lanes) * N) {
         float acc[N] = {};
-        for (int j = 0; j < slots; ++j) {
-            const int64_t r = from[j];
-            if (r < 0 || r >= rows) continue;
-            float v[N];
-            Piece<T, N>::load(v, ys + r * width + c);
-            const float f = w ? w[t * slots + j] : 1.0f;
+        for (int j = 0; j < slots; j += 4) {   // four rows' loads in flight, added in order
+            float v[4][N], f[4];
+            bool here[4];
 #pragma unroll
-            for (int e = 0; e < N; ++e) acc[e] = fmaf(f, v[e], acc[e]);
+            for (int i = 0; i < 4; ++i) {
+                const int64_t r = j + i < slots ? from[j + i] : -1;
+                here[i] = r >= 0 && r < rows;
+                if (!here[i]) continue;
+                f[i] = w ? w[t * slots + j + i] : 1.0f;
+                Piece<T, N>::load(v[i], ys + r * width + c);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (!here[i]) continue;
+#pragma unroll
+                for (int e = 0; e < N; ++e) acc[e] = fmaf(f[i], v[i][e], acc[e]);
+            }
         }
         Piece<T, N>::store(y + t * width + c, acc);
     }
@@ -347,6 +476,90 @@ __global__ void __launch_bounds__(kRowThreads)
     }
 }
 
+// The same for rows that the CTA's registers hold (VPT pieces a thread): dy is
+// read once, and the next slot's piece of ys is loaded while this one's is
+// used.
+template <typename T, int N, int VPT>
+__global__ void __launch_bounds__(kRowThreads)
+    moe_unpermute_bwd_held_kernel(const T* __restrict__ dy, const T* __restrict__ ys,
+                                  const int32_t* __restrict__ row_of, const int32_t* __restrict__ src,
+                                  const float* __restrict__ w, int64_t tokens, int slots,
+                                  int64_t width, int64_t rows, T* __restrict__ dys,
+                                  float* __restrict__ dw) {
+    ptx::griddep_launch_dependents();
+    __shared__ float part[kRowThreads / 32][kMaxSlots];
+    __shared__ int to[kMaxSlots];
+    __shared__ float wt[kMaxSlots];
+    ptx::griddep_wait();
+    const int threads = static_cast<int>(blockDim.x);
+    if (blockIdx.x >= tokens) {
+        const float zero[N] = {};
+        for (int64_t r = blockIdx.x - tokens; r < rows; r += gridDim.x - tokens) {
+            if (src[r] >= 0) continue;
+            for (int64_t c = static_cast<int64_t>(threadIdx.x) * N; c < width; c += threads * N)
+                Piece<T, N>::store(dys + r * width + c, zero);
+        }
+        return;
+    }
+    const int64_t t = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int j = threadIdx.x; j < slots; j += threads) {
+        const int r = row_of[t * slots + j];
+        to[j] = r >= 0 && r < rows ? r : -1;
+        wt[j] = w ? w[t * slots + j] : 1.0f;
+    }
+    bool live[VPT];
+    uint4 g[VPT], a[VPT], b[VPT];   // dy; ys of this slot and of the next
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int64_t c = static_cast<int64_t>(threadIdx.x + i * threads) * N;
+        live[i] = c < width;
+        g[i] = live[i] ? row::ld_stream(dy + t * width + c) : make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    auto fetch = [&](uint4 (&v)[VPT], int j) {
+        const int64_t r = j < slots ? to[j] : -1;
+        if (r < 0) return;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (live[i])
+                v[i] = row::ld_stream(ys + r * width + static_cast<int64_t>(threadIdx.x + i * threads) * N);
+    };
+    fetch(b, 0);
+    for (int j = 0; j < slots; ++j) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) a[i] = b[i];
+        fetch(b, j + 1);
+        const int64_t r = to[j];
+        float dot = 0.0f;
+        if (r >= 0) {
+            const float f = wt[j];
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                if (!live[i]) continue;
+                float x[N], y[N], o[N];
+                Piece<T, N>::open(x, g[i]);
+                Piece<T, N>::open(y, a[i]);
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    dot = fmaf(x[e], y[e], dot);
+                    o[e] = f * x[e];
+                }
+                Piece<T, N>::store(dys + r * width + static_cast<int64_t>(threadIdx.x + i * threads) * N, o);
+            }
+        }
+        dot = row::warp_sum(dot);
+        if (lane == 0) part[warp][j] = dot;
+    }
+    if (!dw) return;
+    __syncthreads();
+    for (int j = threadIdx.x; j < slots; j += threads) {
+        float s = 0.0f;
+        for (int i = 0; i < threads / 32; ++i) s += part[i][j];
+        dw[t * slots + j] = s;
+    }
+}
+
 // ------------------------------------------------------------------ host side
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -380,6 +593,38 @@ void launch_permute(const void* x, const float* scale, int64_t tokens, int slots
                row_of, src, rows, static_cast<V*>(xs), scale_s, lanes, token_ctas);
 }
 
+int launch_permute_bulk(const void* x, const float* scale, int64_t tokens, int slots,
+                        int64_t row_bytes, const int32_t* row_of, const int32_t* src, int64_t rows,
+                        void* xs, float* scale_s, cudaStream_t st) {
+    BulkRows p{};
+    p.x = static_cast<const uint8_t*>(x); p.scale = scale; p.row_of = row_of; p.src = src;
+    p.xs = static_cast<uint8_t*>(xs); p.scale_s = scale_s; p.status = device_status_word();
+    p.tokens = tokens; p.rows = rows; p.row_bytes = row_bytes; p.slots = slots;
+    p.slot_bytes = static_cast<int>(row_bytes < kBulkSlotBytes ? (row_bytes + 127) / 128 * 128 : kBulkSlotBytes);
+    p.pieces = static_cast<int>((row_bytes + p.slot_bytes - 1) / p.slot_bytes);
+    int warps = (kBulkSmem - p.slot_bytes) / (kBulkSlots * p.slot_bytes);
+    if (warps > 8) warps = 8;
+    static std::atomic<bool> allowed[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
+    if (dev < 0 || dev >= 64 || !allowed[dev].load(std::memory_order_relaxed)) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            moe_permute_bulk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBulkSmem);
+        if (e != cudaSuccess)
+            return set_error(FP8_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        if (dev >= 0 && dev < 64) allowed[dev].store(true, std::memory_order_relaxed);
+    }
+    const int smem = (warps * kBulkSlots + 1) * p.slot_bytes;
+    // small rows leave room for more CTAs on an SM
+    int per_sm = kBulkSmem / smem;
+    if (per_sm > 8) per_sm = 8;
+    const int64_t work = tokens * p.pieces + (rows + 31) / 32;
+    const int64_t most = static_cast<int64_t>(num_sms()) * per_sm;
+    launch_pdl(moe_permute_bulk_kernel, dim3(static_cast<unsigned>(work < most ? work : most)),
+               dim3(warps * 32), smem, st, p);
+    return FP8_OK;
+}
+
 template <typename T, int N>
 void launch_unpermute(const void* ys, const int32_t* row_of, const float* w, int64_t tokens,
                       int slots, int64_t width, int64_t rows, void* y, cudaStream_t st) {
@@ -395,9 +640,21 @@ void launch_unpermute_bwd(const void* dy, const void* ys, const int32_t* row_of,
                           void* dys, float* dw, cudaStream_t st) {
     const int64_t want = (rows + 15) / 16;
     const int64_t pad_ctas = want < 1 ? 1 : (want > 8 * num_sms() ? 8 * num_sms() : want);
-    launch_pdl(moe_unpermute_bwd_kernel<T, N>, dim3(static_cast<unsigned>(tokens + pad_ctas)),
-               dim3(kRowThreads), 0, st, static_cast<const T*>(dy), static_cast<const T*>(ys), row_of,
-               src, w, tokens, slots, width, rows, static_cast<T*>(dys), dw);
+    const dim3 grid(static_cast<unsigned>(tokens + pad_ctas));
+    auto go = [&](auto kernel, int threads) {
+        launch_pdl(kernel, grid, dim3(threads), 0, st, static_cast<const T*>(dy),
+                   static_cast<const T*>(ys), row_of, src, w, tokens, slots, width, rows,
+                   static_cast<T*>(dys), dw);
+    };
+    if constexpr (N > 1) {
+        const int64_t pieces = width / N;
+        if (pieces <= kRowThreads)   // a width of 0 still writes dw
+            return go(moe_unpermute_bwd_held_kernel<T, N, 1>,
+                      pieces < 32 ? 32 : static_cast<int>((pieces + 31) / 32 * 32));
+        if (pieces <= 2 * kRowThreads) return go(moe_unpermute_bwd_held_kernel<T, N, 2>, kRowThreads);
+        if (pieces <= 4 * kRowThreads) return go(moe_unpermute_bwd_held_kernel<T, N, 4>, kRowThreads);
+    }
+    go(moe_unpermute_bwd_kernel<T, N>, kRowThreads);
 }
 
 }  // namespace
@@ -474,8 +731,13 @@ int fp8_moe_permute(const void* x, const float* scale, int64_t tokens, int slots
         return set_error(FP8_ERR_ALIGN,
                          "fp8_moe_permute: x and xs must be 16-byte aligned, the rest 4-byte");
     if (!rows) return FP8_OK;
+    // rows of 1 KB and more in bulk copies; shorter ones through registers, in
     // the widest unit that the row's length lets every row start on
-    if (row_bytes % 16 == 0)
+    if (row_bytes % 16 == 0 && row_bytes >= 1024) {
+        const int r = launch_permute_bulk(x, scale, tokens, slots, row_bytes, row_of, src, rows, xs,
+                                          scale_s, as_stream(stream));
+        if (r != FP8_OK) return r;
+    } else if (row_bytes % 16 == 0)
         launch_permute<uint4>(x, scale, tokens, slots, row_bytes, row_of, src, rows, xs, scale_s, as_stream(stream));
     else if (row_bytes % 4 == 0)
         launch_permute<uint32_t>(x, scale, tokens, slots, row_bytes, row_of, src, rows, xs, scale_s, as_stream(stream));

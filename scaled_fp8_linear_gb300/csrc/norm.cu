@@ -12,6 +12,7 @@
 // and the stores is fp32: y comes from the unrounded x', and each output is
 // rounded once.  The variance is the mean of squared distances from the mean
 // (a second reduction over the registers), which does not cancel.
+#include <atomic>
 #include <cfloat>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -80,6 +81,16 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, float* part, int& turn) 
         ++turn;
     }
     return v;
+}
+
+// A row's scale from the bits of its largest magnitude, by the per-row cast's
+// rule: 1 for a row that is all zero or not finite.
+__device__ __forceinline__ float row_scale(uint32_t top, int fmt, int pow2) {
+    const float a = __uint_as_float(top);
+    if (!(a > 0.0f && a <= FLT_MAX)) return 1.0f;
+    float s = __fdiv_rn(fmt == FP8_E4M3 ? 448.0f : 57344.0f, a);
+    s = fminf(fmaxf(s, FLT_MIN), FLT_MAX);
+    return pow2 ? __uint_as_float(__float_as_uint(s) & 0xFF800000u) : s;
 }
 
 // Eight elements from p; VEC: 16-byte pieces, all eight present.  Otherwise
@@ -201,7 +212,7 @@ __device__ __forceinline__ void apply_norm(float (&v)[8], const float* w, const 
 
 template <typename S, int VPT, bool WARP, bool VEC, bool LAYER, int THREADS>
 __global__ void __launch_bounds__(THREADS)
-    norm_fwd_kernel(const __grid_constant__ NormFwd p) {
+    norm_fwd_any_kernel(const __grid_constant__ NormFwd p) {
     ptx::griddep_launch_dependents();
     __shared__ float part[128];
     ptx::griddep_wait();
@@ -273,13 +284,7 @@ __global__ void __launch_bounds__(THREADS)
     float s = 1.0f;
     if (p.q_rows || p.amax) top = row_max<WARP>(top, part, turn);
     if (p.q_rows) {
-        // the per-row cast's rule: 1 for a row that is all zero or not finite
-        const float a = __uint_as_float(top);
-        if (a > 0.0f && a <= FLT_MAX) {
-            s = __fdiv_rn(p.q_fmt == FP8_E4M3 ? 448.0f : 57344.0f, a);
-            s = fminf(fmaxf(s, FLT_MIN), FLT_MAX);
-            if (p.pow2) s = __uint_as_float(__float_as_uint(s) & 0xFF800000u);
-        }
+        s = row_scale(top, p.q_fmt, p.pow2);
         if (at == 0) p.q_scale_inv[r] = __fdiv_rn(1.0f, s);
     } else {
         s = p.q_scale[0];
@@ -299,26 +304,257 @@ __global__ void __launch_bounds__(THREADS)
     }
 }
 
-template <typename S, bool VEC, bool LAYER>
+// The forward for rows in 16-byte pieces up to kFastWidth columns: CTAs stay
+// on the SM and walk the rows, each thread on its own columns, with the
+// vectors of those columns in registers (RMS norm) and the next row's pieces
+// loaded while the current row is reduced -- a row's loads cover the two
+// reductions' latency.  WARP: a warp a row, else the CTA.
+template <typename S, int VPT, bool WARP, bool LAYER, int THREADS>
+__global__ void __launch_bounds__(THREADS)
+    norm_fwd_kernel(const __grid_constant__ NormFwd p) {
+    using row::f2;
+    ptx::griddep_launch_dependents();
+    // sums: two buffers of 16 warps' values; the row maximum has its own
+    __shared__ __align__(16) float part[2][16];
+    __shared__ float part_max[128];
+    constexpr bool KEEP = !LAYER;
+    if (!WARP && threadIdx.x < 32) part[threadIdx.x >> 4][threadIdx.x & 15] = 0.0f;
+    if (!WARP) __syncthreads();
+    const int lanes = WARP ? 32 : static_cast<int>(blockDim.x);
+    const int at = WARP ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
+    const int64_t stride = WARP ? static_cast<int64_t>(gridDim.x) * (THREADS / 32) : gridDim.x;
+    int64_t r = WARP ? static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5)
+                     : blockIdx.x;
+    ptx::griddep_wait();
+    if (r >= p.rows) return;
+    int turn = 0, turn_max = 0;
+    auto sum = [&](float (&s)[1]) {
+        if constexpr (WARP) {
+            s[0] = row::warp_sum(s[0]);
+        } else {
+            row::block_sum16<1>(s, part[turn]);
+            turn ^= 1;
+        }
+    };
+    const float inv_c = 1.0f / static_cast<float>(p.width);
+    const S* xin = static_cast<const S*>(p.x);
+    bool live[VPT];
+    int col[VPT];
+    row::Raw8<__nv_bfloat16> hn[VPT];
+    row::Raw8<S> xn[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        col[i] = 8 * (at + i * lanes);
+        live[i] = col[i] < p.width;
+        hn[i].zero();
+        xn[i].zero();
+        if (live[i]) {
+            if (p.h) hn[i].load(p.h + r * p.width + col[i]);
+            if (xin) xn[i].load(xin + r * p.width + col[i]);
+        }
+    }
+    f2 wg[KEEP ? VPT : 1][4], wp[VPT][4], bp[KEEP ? 1 : VPT][4];   // w_post * gate, w_pre, b_pre
+    int64_t group = 0, group_end = 0;   // the gate row in use and the row after its last
+    const bool scaled = p.w_post || p.gate;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        if (!live[i]) continue;
+        if (p.w_pre) row::shared_pairs(wp[i], p.w_pre + col[i]);
+        if constexpr (LAYER) {
+            if (p.b_pre) row::shared_pairs(bp[i], p.b_pre + col[i]);
+        }
+    }
+    const f2 alpha = row::all2(p.alpha);
+    for (; r < p.rows; r += stride) {
+        const int64_t base = r * p.width;
+        if (r >= group_end) {
+            group = r / p.rows_per_gate;
+            group_end = (group + 1) * p.rows_per_gate;
+            if (KEEP && scaled) {
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
+                    if (!live[i]) continue;
+                    if (p.w_post) row::shared_pairs(wg[KEEP ? i : 0], p.w_post + col[i]);
+                    if (p.gate) {
+                        f2 t[4];
+                        row::shared_pairs(t, p.gate + group * p.width + col[i]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) wg[i][e] = p.w_post ? row::mul2(wg[i][e], t[e]) : t[e];
+                    }
+                }
+            }
+        }
+        f2 v[VPT][4];
+        row::Raw8<S> x[VPT];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            hn[i].pairs(v[i]);
+            x[i] = xn[i];
+        }
+        if (r + stride < p.rows) {
+            const int64_t next = base + stride * p.width;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                if (!live[i]) continue;
+                if (p.h) hn[i].load(p.h + next + col[i]);
+                if (xin) xn[i].load(xin + next + col[i]);
+            }
+        }
+        auto stats = [&](float& mean, float& rstd) {
+            mean = 0.0f;
+            if constexpr (LAYER) {
+                f2 a = 0;
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) a = row::add2(a, v[i][e]);
+                float s[1] = {row::lo2(a) + row::hi2(a)};
+                sum(s);
+                mean = s[0] * inv_c;
+            }
+            f2 a = 0;
+            const f2 m = row::all2(-mean);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                f2 b = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const f2 d = LAYER ? row::add2(v[i][e], m) : v[i][e];
+                    b = row::fma2(d, d, b);
+                }
+                if (!LAYER || live[i]) a = row::add2(a, b);   // past the row v is 0, v - mean is not
+            }
+            float s[1] = {row::lo2(a) + row::hi2(a)};
+            sum(s);
+            rstd = rsqrtf(s[0] * inv_c + p.eps);
+        };
+        float mean_post = 0.0f, rstd_post = 0.0f, mean_pre = 0.0f, rstd_pre = 0.0f;
+        if (p.post) stats(mean_post, rstd_post);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            f2 xs[4];
+            x[i].pairs(xs);
+            if (!live[i]) continue;
+            if constexpr (KEEP) {
+                const f2 rs = row::all2(p.post ? rstd_post : 1.0f);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (scaled) v[i][e] = row::mul2(v[i][e], wg[i][e]);
+                    v[i][e] = row::fma2(v[i][e], rs, row::mul2(xs[e], alpha));
+                }
+            } else {
+                f2 t[4];
+                if (p.post) {
+                    const f2 m = row::all2(-mean_post), rs = row::all2(rstd_post);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[i][e] = row::mul2(row::add2(v[i][e], m), rs);
+                    if (p.w_post) {
+                        row::shared_pairs(t, p.w_post + col[i]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[i][e] = row::mul2(v[i][e], t[e]);
+                    }
+                    if (p.b_post) {
+                        row::shared_pairs(t, p.b_post + col[i]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[i][e] = row::add2(v[i][e], t[e]);
+                    }
+                }
+                if (p.gate) {
+                    row::shared_pairs(t, p.gate + group * p.width + col[i]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[i][e] = row::mul2(v[i][e], t[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[i][e] = row::fma2(xs[e], alpha, v[i][e]);
+            }
+            if (p.x_out) row::store_pairs(static_cast<S*>(p.x_out) + base + col[i], v[i]);
+        }
+        if (p.y || p.q || p.stats) stats(mean_pre, rstd_pre);
+        if (p.stats && at == 0) {
+            p.stats[r] = mean_post;
+            p.stats[p.rows + r] = rstd_post;
+            p.stats[2 * p.rows + r] = mean_pre;
+            p.stats[3 * p.rows + r] = rstd_pre;
+        }
+        if (!p.y && !p.q) continue;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            if (!live[i]) continue;
+            const f2 rs = row::all2(rstd_pre), m = row::all2(-mean_pre);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (LAYER) v[i][e] = row::add2(v[i][e], m);
+                v[i][e] = row::mul2(v[i][e], rs);
+                if (p.w_pre) v[i][e] = row::mul2(v[i][e], wp[i][e]);
+                if constexpr (LAYER) {
+                    if (p.b_pre) v[i][e] = row::add2(v[i][e], bp[i][e]);
+                }
+            }
+            if (p.y) row::store_pairs(p.y + base + col[i], v[i]);
+        }
+        if (!p.q) continue;
+        float s = 1.0f;
+        if (p.q_rows || p.amax) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                if (!live[i]) continue;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    top = max(top, max(row::abs_bits(row::lo2(v[i][e])), row::abs_bits(row::hi2(v[i][e]))));
+            }
+            top = row_max<WARP>(top, part_max, turn_max);
+            if (p.q_rows) {
+                s = row_scale(top, p.q_fmt, p.pow2);
+                if (at == 0) p.q_scale_inv[r] = __fdiv_rn(1.0f, s);
+            } else if (at == 0) {
+                row::raise_amax(p.amax, top);
+            }
+        }
+        if (!p.q_rows) s = p.q_scale[0];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            if (!live[i]) continue;
+            float t[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                t[2 * e] = row::lo2(v[i][e]);
+                t[2 * e + 1] = row::hi2(v[i][e]);
+            }
+            *reinterpret_cast<uint2*>(p.q + base + col[i]) = row::cvt8(p.q_fmt, t, s);
+        }
+    }
+}
+
+// Rows in 16-byte pieces up to here take the resident kernels: 512 threads
+// with two pieces each, 128 registers a thread.
+constexpr int64_t kFastWidth = 8192;
+
+template <typename S, bool LAYER>
 void launch_fwd(const NormFwd& p, cudaStream_t st) {
     const int64_t pieces = (p.width + 7) / 8;
-    // up to 1024 columns a warp holds a row: no CTA barrier, eight rows a CTA
-    if (pieces <= 128) {
-        const dim3 grid(static_cast<unsigned>((p.rows + 7) / 8));
-        if (pieces <= 32)
-            launch_pdl(norm_fwd_kernel<S, 1, true, VEC, LAYER, 256>, grid, dim3(256), 0, st, p);
-        else if (pieces <= 64)
-            launch_pdl(norm_fwd_kernel<S, 2, true, VEC, LAYER, 256>, grid, dim3(256), 0, st, p);
-        else
-            launch_pdl(norm_fwd_kernel<S, 4, true, VEC, LAYER, 256>, grid, dim3(256), 0, st, p);
+    const int threads = static_cast<int>(((pieces + 1) / 2 + 31) / 32 * 32);
+    if (p.width % 8 == 0 && p.width <= kFastWidth) {
+        // up to 512 columns a warp holds a row, without a CTA barrier
+        const bool warp = pieces <= 64;
+        const int64_t per_sm = warp ? 2 : 512 / threads;
+        const int64_t want = warp ? (p.rows + 7) / 8 : p.rows, most = num_sms() * per_sm;
+        const dim3 grid(static_cast<unsigned>(want < most ? want : most));
+        if (pieces <= 32) launch_pdl(norm_fwd_kernel<S, 1, true, LAYER, 256>, grid, dim3(256), 0, st, p);
+        else if (warp) launch_pdl(norm_fwd_kernel<S, 2, true, LAYER, 256>, grid, dim3(256), 0, st, p);
+        else launch_pdl(norm_fwd_kernel<S, 2, false, LAYER, 512>, grid, dim3(threads), 0, st, p);
         return;
     }
-    const int threads = static_cast<int>(((pieces + 1) / 2 + 31) / 32 * 32);
-    const dim3 grid(static_cast<unsigned>(p.rows));
-    if (threads <= 512)
-        launch_pdl(norm_fwd_kernel<S, 2, false, VEC, LAYER, 512>, grid, dim3(threads), 0, st, p);
-    else
-        launch_pdl(norm_fwd_kernel<S, 2, false, VEC, LAYER, 1024>, grid, dim3(threads), 0, st, p);
+    if (p.width % 8 == 0) {
+        launch_pdl(norm_fwd_any_kernel<S, 2, false, true, LAYER, 1024>,
+                   dim3(static_cast<unsigned>(p.rows)), dim3(threads), 0, st, p);
+    } else if (pieces <= 64) {
+        launch_pdl(norm_fwd_any_kernel<S, 2, true, false, LAYER, 256>,
+                   dim3(static_cast<unsigned>((p.rows + 7) / 8)), dim3(256), 0, st, p);
+    } else {
+        launch_pdl(norm_fwd_any_kernel<S, 2, false, false, LAYER, 1024>,
+                   dim3(static_cast<unsigned>(p.rows)), dim3(threads), 0, st, p);
+    }
 }
 
 // ------------------------------------------------------------------ backward
@@ -349,11 +585,12 @@ struct NormBwd {
     int64_t rows, width, groups, parts;
     float alpha;
     int post, add_dgate;
+    unsigned* status;
 };
 
 struct BwdPlan {
     bool warp;
-    int vpt, threads, ctas;
+    int vpt, threads, per_sm, ctas;
     int64_t groups, parts;
     size_t dw_floats, dgate_floats;
 };
@@ -366,8 +603,8 @@ BwdPlan bwd_plan(int64_t rows, int64_t width, int64_t gate_rows) {
     b.warp = pieces <= 64;
     b.vpt = pieces <= 32 ? 1 : 2;
     b.threads = b.warp ? 256 : static_cast<int>(((pieces + 1) / 2 + 31) / 32 * 32);
-    const int64_t per_sm = b.warp ? 2 : (b.threads >= 512 ? 1 : 512 / b.threads);
-    const int64_t target = num_sms() * per_sm;
+    b.per_sm = b.warp ? 2 : (b.threads >= 512 ? 1 : 512 / b.threads);
+    const int64_t target = num_sms() * b.per_sm;
     b.groups = gate_rows > 0 ? gate_rows : 1;
     const int64_t in_group = rows / b.groups;
     b.parts = b.groups >= target ? 1 : target / b.groups;
@@ -420,7 +657,7 @@ __device__ __forceinline__ void flush(float (&acc)[VPT][8], const int (&n)[VPT],
 
 template <typename S, int VPT, bool WARP, bool VEC, bool LAYER, int THREADS>
 __global__ void __launch_bounds__(THREADS)
-    norm_bwd_kernel(const __grid_constant__ NormBwd p) {
+    norm_bwd_any_kernel(const __grid_constant__ NormBwd p) {
     ptx::griddep_launch_dependents();
     __shared__ float part[128];
     __shared__ float buf[WARP ? 8 * 512 : 1];
@@ -601,6 +838,371 @@ __global__ void __launch_bounds__(THREADS)
     }
 }
 
+// The backward for rows in 16-byte pieces up to kFastWidth columns.  The rows
+// come through a ring of shared-memory stages, filled by bulk copies one or
+// two batches ahead (a batch is a row, or the eight rows of a CTA's warps:
+// consecutive in memory, so four copies), because the column sums leave no
+// registers to hold a row ahead.  A stage is read piece by piece as the row
+// needs it, and filled again once every thread is past its last read.
+// The gate is one row within a chunk, so with A = sum dX hh and B = sum dX over
+// the chunk's rows  dgate = w_post A + b_post B,  dw_post = sum of gate A  and
+// db_post = sum of gate B  over the chunks: one pair of running sums serves
+// the gate's and the post norm's gradients.
+struct BwdRing {
+    int stages;
+    uint32_t x_at, dxo_at, h_at, stage_bytes;   // dy at 0
+};
+
+template <typename S, int VPT, bool WARP, bool LAYER, int THREADS>
+__global__ void __launch_bounds__(THREADS)
+    norm_bwd_kernel(const __grid_constant__ NormBwd p, const __grid_constant__ BwdRing ring) {
+    using row::f2;
+    ptx::griddep_launch_dependents();
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(16) float part[2][32];
+    __shared__ float buf[WARP ? 8 * 512 : 1];
+    __shared__ uint64_t full[8];
+    __shared__ volatile uint32_t gave_up;
+    constexpr int BATCH = WARP ? 8 : 1;   // rows
+    const int lanes = WARP ? 32 : static_cast<int>(blockDim.x);
+    const int at = WARP ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
+    const int own = WARP ? static_cast<int>(threadIdx.x >> 5) : 0;   // this thread's row of a batch
+    if (threadIdx.x < 64) part[threadIdx.x >> 5][threadIdx.x & 31] = 0.0f;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ring.stages; ++i) ptx::mbar_init(&full[i], 1);
+        gave_up = 0;
+        ptx::fence_barrier_init();
+    }
+    __syncthreads();
+    ptx::griddep_wait();
+
+    const int chunks = static_cast<int>(p.groups * p.parts);
+    const int parts = static_cast<int>(p.parts), in_group = static_cast<int>(p.rows / p.groups);
+    // the CTA's batches in order: rows [r, end) of chunk k (no chunk is empty)
+    struct Walk {
+        int k, r, end;
+    };
+    auto enter = [&](Walk& w) {
+        if (w.k >= chunks) return;
+        const int g = w.k / parts, i = w.k - g * parts;
+        w.r = g * in_group + static_cast<int>(static_cast<int64_t>(i) * in_group / parts);
+        w.end = g * in_group + static_cast<int>(static_cast<int64_t>(i + 1) * in_group / parts);
+    };
+    auto next = [&](Walk& w) {
+        w.r += BATCH;
+        if (w.r >= w.end) {
+            w.k += gridDim.x;
+            enter(w);
+        }
+    };
+    Walk ahead{static_cast<int>(blockIdx.x), 0, 0};
+    uint32_t issued = 0;
+    auto fill = [&]() {   // thread 0: copy the next batch of rows into its stage
+        const uint32_t n = static_cast<uint32_t>(min(ahead.end - ahead.r, BATCH)) * static_cast<uint32_t>(p.width);
+        uint8_t* to = smem + (issued % ring.stages) * ring.stage_bytes;
+        uint64_t* bar = &full[issued % ring.stages];
+        const int64_t first = static_cast<int64_t>(ahead.r) * p.width;
+        const uint32_t bytes = (p.dy ? n * (2 + sizeof(S)) : 0) + (p.dx_out ? n * sizeof(S) : 0) + (p.h ? n * 2 : 0);
+        ptx::mbar_arrive_expect_tx(bar, bytes);
+        if (p.dy) {
+            ptx::bulk_load(to, p.dy + first, n * 2, bar);
+            ptx::bulk_load(to + ring.x_at, static_cast<const S*>(p.x_out) + first, n * sizeof(S), bar);
+        }
+        if (p.dx_out)
+            ptx::bulk_load(to + ring.dxo_at, static_cast<const S*>(p.dx_out) + first, n * sizeof(S), bar);
+        if (p.h) ptx::bulk_load(to + ring.h_at, p.h + first, n * 2, bar);
+        ++issued;
+        next(ahead);
+    };
+    if (threadIdx.x == 0) {
+        enter(ahead);
+        for (int i = 0; i < ring.stages && ahead.k < chunks; ++i) fill();
+    }
+
+    int turn = 0;
+    auto sum = [&](float (&v)[2]) {
+        if constexpr (WARP) {
+            v[0] = row::warp_sum(v[0]);
+            if constexpr (LAYER) v[1] = row::warp_sum(v[1]);
+        } else if constexpr (LAYER) {
+            row::block_sum16<2>(v, part[turn]);
+        } else {
+            float t[1] = {v[0]};
+            row::block_sum16<1>(t, part[turn]);
+            v[0] = t[0];
+        }
+        turn ^= 1;
+    };
+    const float inv_c = 1.0f / static_cast<float>(p.width);
+    f2 dw_pre[VPT][4], sum_a[VPT][4];
+    f2 db_pre[LAYER ? VPT : 1][4], sum_b[LAYER ? VPT : 1][4];
+    int col[VPT];
+    bool live[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        col[i] = 8 * (at + i * lanes);
+        live[i] = col[i] < p.width;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            dw_pre[i][e] = sum_a[i][e] = 0;
+            if constexpr (LAYER) db_pre[i][e] = sum_b[i][e] = 0;
+        }
+    }
+    auto out_sums = [&](const f2 (&acc)[VPT][4], float* out, bool add) {
+        float v[VPT][8];
+        int n[VPT];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            n[i] = live[i] ? 8 : 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[i][2 * e] = row::lo2(acc[i][e]);
+                v[i][2 * e + 1] = row::hi2(acc[i][e]);
+            }
+        }
+        flush<VPT, WARP, true>(v, n, at, lanes, p.width, out, add, buf);
+    };
+    const int64_t rows_of = static_cast<int64_t>(gridDim.x) * p.width;
+    float* const my_sums = p.dw_part + static_cast<int64_t>(blockIdx.x) * p.width;
+    // the end of a chunk: its part of dgate, and of the post norm's sums
+    auto end_chunk = [&](const __nv_bfloat16* gate, int64_t k, bool first) {
+        f2 t[VPT][4], w[4];
+        if (p.dgate_part) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) t[i][e] = sum_a[i][e];
+                if (!live[i] || !p.post) continue;
+                if (p.w_post) {
+                    row::shared_pairs(w, p.w_post + col[i]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) t[i][e] = row::mul2(t[i][e], w[e]);
+                }
+                if constexpr (LAYER) {
+                    if (p.b_post) {
+                        row::shared_pairs(w, p.b_post + col[i]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) t[i][e] = row::fma2(sum_b[i][e], w[e], t[i][e]);
+                    }
+                }
+            }
+            out_sums(t, p.dgate_part + k * p.width, p.add_dgate != 0);
+        }
+        if (p.post) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                if (!live[i]) continue;
+                row::shared_pairs(w, gate + col[i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sum_a[i][e] = row::mul2(sum_a[i][e], w[e]);
+                    if constexpr (LAYER) sum_b[i][e] = row::mul2(sum_b[i][e], w[e]);
+                }
+            }
+            out_sums(sum_a, my_sums + 2 * rows_of, !first);
+            if constexpr (LAYER) out_sums(sum_b, my_sums + 3 * rows_of, !first);
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sum_a[i][e] = 0;
+                if constexpr (LAYER) sum_b[i][e] = 0;
+            }
+    };
+
+    const f2 alpha = row::all2(p.alpha);
+    Walk now{static_cast<int>(blockIdx.x), 0, 0};
+    enter(now);
+    // a row's statistics do not come through the ring: loaded a batch ahead
+    float next_stat[4];
+    auto load_stats = [&](const Walk& w) {
+        next_stat[0] = next_stat[2] = 0.0f;
+        next_stat[1] = next_stat[3] = 1.0f;
+        const int64_t r = w.r + own;
+        if (w.k >= chunks || r >= w.end || !p.stats) return;
+        if (p.post) {
+            if constexpr (LAYER) next_stat[0] = p.stats[r];
+            next_stat[1] = p.stats[p.rows + r];
+        }
+        if constexpr (LAYER) next_stat[2] = p.stats[2 * p.rows + r];
+        next_stat[3] = p.stats[3 * p.rows + r];
+    };
+    load_stats(now);
+    uint32_t stage = 0, phase = 0;
+    while (now.k < chunks) {
+        const __nv_bfloat16* gate = p.gate ? p.gate + now.k / parts * p.width : nullptr;
+        const int k = now.k;
+        for (; now.k == k; next(now)) {
+            const int64_t r = now.r + own;
+            const bool has_row = !WARP || r < now.end;
+            const float m_post = next_stat[0], r_post = next_stat[1];
+            const float m_pre = next_stat[2], r_pre = next_stat[3];
+            Walk then = now;
+            next(then);
+            load_stats(then);
+            ptx::mbar_wait(&full[stage], phase, &gave_up);
+            const uint8_t* st = smem + stage * ring.stage_bytes;
+            const int64_t base = r * p.width, in = static_cast<int64_t>(own) * p.width;
+            if (has_row) {
+                f2 d[VPT][4], u[VPT][4];
+                if (p.dy) {
+                    f2 s0 = 0, s1 = 0;
+                    const f2 rs = row::all2(r_pre), mr = row::all2(-m_pre * r_pre);
+#pragma unroll
+                    for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) d[i][e] = u[i][e] = 0;
+                        if (!live[i]) continue;
+                        row::Raw8<__nv_bfloat16> a;
+                        row::Raw8<S> b;
+                        a.load_shared(reinterpret_cast<const __nv_bfloat16*>(st) + in + col[i]);
+                        b.load_shared(reinterpret_cast<const S*>(st + ring.x_at) + in + col[i]);
+                        a.pairs(d[i]);
+                        b.pairs(u[i]);
+                        f2 w[4];
+                        if (p.w_pre) row::shared_pairs(w, p.w_pre + col[i]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            u[i][e] = LAYER ? row::fma2(u[i][e], rs, mr) : row::mul2(u[i][e], rs);
+                            dw_pre[i][e] = row::fma2(d[i][e], u[i][e], dw_pre[i][e]);
+                            if constexpr (LAYER) db_pre[i][e] = row::add2(db_pre[i][e], d[i][e]);
+                            if (p.w_pre) d[i][e] = row::mul2(d[i][e], w[e]);
+                            s0 = row::fma2(d[i][e], u[i][e], s0);
+                            if constexpr (LAYER) s1 = row::add2(s1, d[i][e]);
+                        }
+                    }
+                    float s[2] = {row::lo2(s0) + row::hi2(s0), row::lo2(s1) + row::hi2(s1)};
+                    sum(s);
+                    // dX = dx' + r (g - mean(g) - u mean(g u))
+                    const f2 cu = row::all2(-r_pre * (s[0] * inv_c));
+                    const f2 cg = row::all2(-r_pre * (s[1] * inv_c));
+#pragma unroll
+                    for (int i = 0; i < VPT; ++i) {
+                        if (!live[i]) continue;
+                        f2 o[4];
+                        if (p.dx_out) {
+                            row::Raw8<S> a;
+                            a.load_shared(reinterpret_cast<const S*>(st + ring.dxo_at) + in + col[i]);
+                            a.pairs(o);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[e] = 0;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if constexpr (LAYER) o[e] = row::add2(o[e], cg);
+                            d[i][e] = row::fma2(d[i][e], rs, row::fma2(u[i][e], cu, o[e]));
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) d[i][e] = 0;
+                        if (!live[i] || !p.dx_out) continue;
+                        row::Raw8<S> a;
+                        a.load_shared(reinterpret_cast<const S*>(st + ring.dxo_at) + in + col[i]);
+                        a.pairs(d[i]);
+                    }
+                }
+                // d is dX; u becomes the block's output, normed
+                f2 s0 = 0, s1 = 0;
+                const f2 rs = row::all2(r_post), mr = row::all2(-m_post * r_post);
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
+                    if (!live[i]) continue;
+                    if (p.dx) {
+                        f2 o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[e] = row::mul2(d[i][e], alpha);
+                        row::store_pairs(static_cast<S*>(p.dx) + base + col[i], o);
+                    }
+                    if (!p.h) continue;
+                    row::Raw8<__nv_bfloat16> a;
+                    a.load_shared(reinterpret_cast<const __nv_bfloat16*>(st + ring.h_at) + in + col[i]);
+                    a.pairs(u[i]);
+                    f2 w[4];
+                    if (p.post) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            u[i][e] = LAYER ? row::fma2(u[i][e], rs, mr) : row::mul2(u[i][e], rs);
+                        if (p.w_post) row::shared_pairs(w, p.w_post + col[i]);
+                    }
+                    if (gate) {
+                        f2 gt[4];
+                        row::shared_pairs(gt, gate + col[i]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            sum_a[i][e] = row::fma2(d[i][e], u[i][e], sum_a[i][e]);
+                            if constexpr (LAYER) sum_b[i][e] = row::add2(sum_b[i][e], d[i][e]);
+                            d[i][e] = row::mul2(d[i][e], gt[e]);
+                        }
+                    } else if (p.post) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            sum_a[i][e] = row::fma2(d[i][e], u[i][e], sum_a[i][e]);
+                            if constexpr (LAYER) sum_b[i][e] = row::add2(sum_b[i][e], d[i][e]);
+                        }
+                    }
+                    if (p.post) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (p.w_post) d[i][e] = row::mul2(d[i][e], w[e]);
+                            s0 = row::fma2(d[i][e], u[i][e], s0);
+                            if constexpr (LAYER) s1 = row::add2(s1, d[i][e]);
+                        }
+                    }
+                }
+                if (p.h) {
+                    f2 ch = 0, cq = 0, scale = row::all2(1.0f);
+                    if (p.post) {
+                        float s[2] = {row::lo2(s0) + row::hi2(s0), row::lo2(s1) + row::hi2(s1)};
+                        sum(s);
+                        scale = rs;
+                        ch = row::all2(-r_post * (s[0] * inv_c));
+                        cq = row::all2(-r_post * (s[1] * inv_c));
+                    }
+                    if (p.dh) {
+#pragma unroll
+                        for (int i = 0; i < VPT; ++i) {
+                            if (!live[i]) continue;
+                            if (p.post) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const f2 t = LAYER ? row::fma2(u[i][e], ch, cq) : row::mul2(u[i][e], ch);
+                                    d[i][e] = row::fma2(d[i][e], scale, t);
+                                }
+                            }
+                            row::store_pairs(p.dh + base + col[i], d[i]);
+                        }
+                    }
+                }
+            }
+            if (++stage == static_cast<uint32_t>(ring.stages)) { stage = 0; phase ^= 1u; }
+            // with a post norm over the CTA its sum's barrier is past the last read
+            if (WARP || !(p.post && p.h)) __syncthreads();
+            if (threadIdx.x == 0 && ahead.k < chunks) fill();
+        }
+        if (gate) end_chunk(gate, k, k == static_cast<int>(blockIdx.x));
+    }
+    out_sums(dw_pre, my_sums, false);
+    if constexpr (LAYER) out_sums(db_pre, my_sums + rows_of, false);
+    if (!p.gate) {
+        out_sums(sum_a, my_sums + 2 * rows_of, false);
+        if constexpr (LAYER) out_sums(sum_b, my_sums + 3 * rows_of, false);
+    }
+    if (threadIdx.x == 0 && gave_up) {
+        // copies may still be on their way into this CTA's shared memory
+        uint32_t never = 0;
+        for (uint32_t i = 0; i < issued && i < static_cast<uint32_t>(ring.stages); ++i) {
+            const uint32_t last = issued - 1 - i;   // the newest copy into each stage
+            ptx::mbar_wait(&full[last % ring.stages], last / ring.stages & 1u, &never);
+        }
+        if (p.status) atomicOr(p.status, 1u);
+    }
+}
+
 // Sums of partial rows: job j < 4 adds dw_part[j][0 .. ctas), job 4 + g the
 // `parts` rows of group g.  A CTA takes 32 columns: 32 slices of the rows
 // first, then the slices, both in a fixed order.
@@ -640,15 +1242,59 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const __grid_constant__
     }
 }
 
-template <typename S, bool VEC, bool LAYER>
-void launch_bwd(const NormBwd& p, const BwdPlan& b, cudaStream_t st) {
+// Shared memory for the ring of one CTA: what an SM has, less what L1 needs
+// for the vectors (14 bytes a column at most), over the CTAs on it.
+constexpr int kRingBytesPerSm = 160 * 1024;
+
+template <typename S, int VPT, bool WARP, bool LAYER, int THREADS>
+int launch_bwd_ring(const NormBwd& p, const BwdPlan& b, cudaStream_t st) {
+    BwdRing ring;
+    const uint32_t n = static_cast<uint32_t>(p.width * (WARP ? 8 : 1));
+    auto up = [](uint32_t v) { return (v + 127) / 128 * 128; };
+    ring.x_at = up(n * 2);
+    ring.dxo_at = ring.x_at + up(n * sizeof(S));
+    ring.h_at = ring.dxo_at + up(n * sizeof(S));
+    ring.stage_bytes = ring.h_at + up(n * 2);
+    const uint32_t room = static_cast<uint32_t>(kRingBytesPerSm / b.per_sm);
+    ring.stages = static_cast<int>(room / ring.stage_bytes);
+    if (ring.stages > 4) ring.stages = 4;
+    if (ring.stages < 2) ring.stages = 2;
+    const uint32_t bytes = ring.stages * ring.stage_bytes;
+    auto k = norm_bwd_kernel<S, VPT, WARP, LAYER, THREADS>;
+    // per device and instance; setting it again is harmless
+    static std::atomic<uint32_t> allowed[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
+    if (dev < 0 || dev >= 64 || allowed[dev].load(std::memory_order_relaxed) < bytes) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(bytes));
+        if (e != cudaSuccess)
+            return set_error(FP8_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        if (dev >= 0 && dev < 64) {
+            uint32_t was = allowed[dev].load(std::memory_order_relaxed);
+            while (was < bytes && !allowed[dev].compare_exchange_weak(was, bytes)) {
+            }
+        }
+    }
+    launch_pdl(k, dim3(b.ctas), dim3(b.threads), bytes, st, p, ring);
+    return FP8_OK;
+}
+
+template <typename S, bool LAYER>
+int launch_bwd(const NormBwd& p, const BwdPlan& b, cudaStream_t st) {
     const dim3 grid(b.ctas), block(b.threads);
-    if (b.warp && b.vpt == 1) launch_pdl(norm_bwd_kernel<S, 1, true, VEC, LAYER, 256>, grid, block, 0, st, p);
-    else if (b.warp) launch_pdl(norm_bwd_kernel<S, 2, true, VEC, LAYER, 256>, grid, block, 0, st, p);
-    else if (b.threads <= 512)
-        launch_pdl(norm_bwd_kernel<S, 2, false, VEC, LAYER, 512>, grid, block, 0, st, p);
+    if (p.width % 8 == 0 && p.width <= kFastWidth) {
+        if (b.warp && b.vpt == 1) return launch_bwd_ring<S, 1, true, LAYER, 256>(p, b, st);
+        if (b.warp) return launch_bwd_ring<S, 2, true, LAYER, 256>(p, b, st);
+        return launch_bwd_ring<S, 2, false, LAYER, 512>(p, b, st);
+    }
+    if (p.width % 8 == 0)
+        launch_pdl(norm_bwd_any_kernel<S, 2, false, true, LAYER, 1024>, grid, block, 0, st, p);
+    else if (b.warp)
+        launch_pdl(norm_bwd_any_kernel<S, 2, true, false, LAYER, 256>, grid, block, 0, st, p);
     else
-        launch_pdl(norm_bwd_kernel<S, 2, false, VEC, LAYER, 1024>, grid, block, 0, st, p);
+        launch_pdl(norm_bwd_any_kernel<S, 2, false, false, LAYER, 1024>, grid, block, 0, st, p);
+    return FP8_OK;
 }
 
 }  // namespace
@@ -752,18 +1398,15 @@ int fp8_norm_fwd(const fp8_norm_fwd_args_t* a, void* stream) {
     p.q = a->q; p.q_scale = a->q_scale; p.q_scale_inv = a->q_scale_inv; p.amax = a->amax;
     p.stats = a->stats;
     p.rows = a->rows; p.width = a->width;
-    p.rows_per_gate = a->gate ? a->rows / a->gate_rows : 1;
+    p.rows_per_gate = a->gate ? a->rows / a->gate_rows : a->rows;
     p.alpha = a->alpha; p.eps = a->eps; p.post = a->post_norm != 0;
     p.q_fmt = a->q_format; p.q_rows = a->q_granularity == FP8_GRAN_ROW; p.pow2 = a->pow2 != 0;
-    const bool vec = a->width % 8 == 0, layer = a->kind == FP8_NORM_LAYER;
+    const bool layer = a->kind == FP8_NORM_LAYER;
     cudaStream_t s = as_stream(stream);
-    if (a->stream_type == FP8_OUT_F32) {
-        if (vec) layer ? launch_fwd<float, true, true>(p, s) : launch_fwd<float, true, false>(p, s);
-        else layer ? launch_fwd<float, false, true>(p, s) : launch_fwd<float, false, false>(p, s);
-    } else {
-        if (vec) layer ? launch_fwd<__nv_bfloat16, true, true>(p, s) : launch_fwd<__nv_bfloat16, true, false>(p, s);
-        else layer ? launch_fwd<__nv_bfloat16, false, true>(p, s) : launch_fwd<__nv_bfloat16, false, false>(p, s);
-    }
+    if (a->stream_type == FP8_OUT_F32)
+        layer ? launch_fwd<float, true>(p, s) : launch_fwd<float, false>(p, s);
+    else
+        layer ? launch_fwd<__nv_bfloat16, true>(p, s) : launch_fwd<__nv_bfloat16, false>(p, s);
     return launch_status(what);
 }
 
@@ -836,14 +1479,13 @@ int fp8_norm_bwd(const fp8_norm_bwd_args_t* a, void* workspace, size_t workspace
     p.add_dgate = direct && a->accumulate;
     p.rows = a->rows; p.width = a->width; p.groups = b.groups; p.parts = b.parts;
     p.alpha = a->alpha; p.post = a->post_norm != 0;
-    const bool vec = a->width % 8 == 0, layer = a->kind == FP8_NORM_LAYER;
-    if (a->stream_type == FP8_OUT_F32) {
-        if (vec) layer ? launch_bwd<float, true, true>(p, b, s) : launch_bwd<float, true, false>(p, b, s);
-        else layer ? launch_bwd<float, false, true>(p, b, s) : launch_bwd<float, false, false>(p, b, s);
-    } else {
-        if (vec) layer ? launch_bwd<__nv_bfloat16, true, true>(p, b, s) : launch_bwd<__nv_bfloat16, true, false>(p, b, s);
-        else layer ? launch_bwd<__nv_bfloat16, false, true>(p, b, s) : launch_bwd<__nv_bfloat16, false, false>(p, b, s);
-    }
+    p.status = device_status_word();
+    const bool layer = a->kind == FP8_NORM_LAYER;
+    if (a->stream_type == FP8_OUT_F32)
+        st = layer ? launch_bwd<float, true>(p, b, s) : launch_bwd<float, false>(p, b, s);
+    else
+        st = layer ? launch_bwd<__nv_bfloat16, true>(p, b, s) : launch_bwd<__nv_bfloat16, false>(p, b, s);
+    if (st != FP8_OK) return st;
     NormSums q{};
     q.dw_part = p.dw_part;
     q.dgate_part = p.dw_part + b.dw_floats;

@@ -47,6 +47,85 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
                       pack_bf16(v[6], v[7]));
 }
 
+// ------------------------------------------------ pairs of fp32 in one register pair
+// Packed instructions do two elements at a time: the norms' kernels are near
+// the issue limit without them.
+
+using f2 = uint64_t;
+
+__device__ __forceinline__ f2 mk2(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ f2 all2(float v) { return mk2(v, v); }
+__device__ __forceinline__ float lo2(f2 v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi2(f2 v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) { return ptx::fmul2(a, b); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) { return ptx::ffma2(a, b, c); }
+__device__ __forceinline__ f2 bf2(uint32_t w) { return mk2(bf_lo(w), bf_hi(w)); }
+__device__ __forceinline__ uint32_t pack_bf16(f2 v) { return pack_bf16(lo2(v), hi2(v)); }
+
+// Eight elements, as loaded (bf16: one 16-byte word, fp32: two) and as pairs.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 w;
+    __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = ld_stream(p); }
+    __device__ __forceinline__ void load_shared(const __nv_bfloat16* p) {
+        w = *reinterpret_cast<const uint4*>(p);
+    }
+    __device__ __forceinline__ void pairs(f2 (&v)[4]) const {
+        v[0] = bf2(w.x); v[1] = bf2(w.y); v[2] = bf2(w.z); v[3] = bf2(w.w);
+    }
+};
+template <>
+struct Raw8<float> {
+    uint4 a, b;
+    __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void load(const float* p) {
+        a = ld_stream(p);
+        b = ld_stream(p + 4);
+    }
+    __device__ __forceinline__ void load_shared(const float* p) {
+        a = *reinterpret_cast<const uint4*>(p);
+        b = *reinterpret_cast<const uint4*>(p + 4);
+    }
+    __device__ __forceinline__ void pairs(f2 (&v)[4]) const {
+        v[0] = mk2(__uint_as_float(a.x), __uint_as_float(a.y));
+        v[1] = mk2(__uint_as_float(a.z), __uint_as_float(a.w));
+        v[2] = mk2(__uint_as_float(b.x), __uint_as_float(b.y));
+        v[3] = mk2(__uint_as_float(b.z), __uint_as_float(b.w));
+    }
+};
+
+__device__ __forceinline__ void store_pairs(__nv_bfloat16* p, const f2 (&v)[4]) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_bf16(v[0]), pack_bf16(v[1]), pack_bf16(v[2]), pack_bf16(v[3]));
+}
+__device__ __forceinline__ void store_pairs(float* p, const f2 (&v)[4]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(lo2(v[0]), hi2(v[0]), lo2(v[1]), hi2(v[1]));
+    reinterpret_cast<float4*>(p)[1] = make_float4(lo2(v[2]), hi2(v[2]), lo2(v[3]), hi2(v[3]));
+}
+
+// Eight elements of a vector that every row shares, through L1.
+__device__ __forceinline__ void shared_pairs(f2 (&v)[4], const float* p) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = mk2(a.x, a.y); v[1] = mk2(a.z, a.w); v[2] = mk2(b.x, b.y); v[3] = mk2(b.z, b.w);
+}
+__device__ __forceinline__ void shared_pairs(f2 (&v)[4], const __nv_bfloat16* p) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+    v[0] = bf2(w.x); v[1] = bf2(w.y); v[2] = bf2(w.z); v[3] = bf2(w.w);
+}
+
 // Two fp32 -> two FP8 codes (the first in the low byte), round to nearest
 // even, saturating.
 template <int FMT>
@@ -97,6 +176,28 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float* part) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < nw ? part[i * 32 + lane] : 0.0f);
+}
+
+// The same for CTAs of at most 16 warps: every thread adds the warps' values
+// itself, four at a load, which is a third of a second shuffle tree's
+// latency.  `part`: N x 16 floats, zero past the CTA's warps.
+template <int N>
+__device__ __forceinline__ void block_sum16(float (&v)[N], float* part) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        v[i] = warp_sum(v[i]);
+        if (lane == 0) part[i * 16 + warp] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float4* q = reinterpret_cast<const float4*>(part + i * 16);
+        const float4 a = q[0], b = q[1], c = q[2], d = q[3];
+        const f2 s = add2(add2(add2(mk2(a.x, a.y), mk2(a.z, a.w)), add2(mk2(b.x, b.y), mk2(b.z, b.w))),
+                          add2(add2(mk2(c.x, c.y), mk2(c.z, c.w)), add2(mk2(d.x, d.y), mk2(d.z, d.w))));
+        v[i] = lo2(s) + hi2(s);
+    }
 }
 
 }  // namespace row
