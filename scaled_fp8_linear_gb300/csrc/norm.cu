@@ -848,12 +848,20 @@ __global__ void __launch_bounds__(THREADS)
 // the chunk's rows  dgate = w_post A + b_post B,  dw_post = sum of gate A  and
 // db_post = sum of gate B  over the chunks: one pair of running sums serves
 // the gate's and the post norm's gradients.
+//
+// HAS says at compile time which parts there are, for the usual calls: a row
+// is then one stretch of code in which loads move ahead of their uses, where
+// tests between them would hold them back.  0: all tested as the kernel runs.
+constexpr int kHasAll = 1;    // dy, x', dx', h, dx, dh, w_pre; the other parts by bits
+constexpr int kHasPost = 2;   // with w_post
+constexpr int kHasGate = 4;
+
 struct BwdRing {
     int stages;
     uint32_t x_at, dxo_at, h_at, stage_bytes;   // dy at 0
 };
 
-template <typename S, int VPT, bool WARP, bool LAYER, int THREADS>
+template <typename S, int VPT, bool WARP, bool LAYER, int THREADS, int HAS>
 __global__ void __launch_bounds__(THREADS)
     norm_bwd_kernel(const __grid_constant__ NormBwd p, const __grid_constant__ BwdRing ring) {
     using row::f2;
@@ -864,6 +872,12 @@ __global__ void __launch_bounds__(THREADS)
     __shared__ uint64_t full[8];
     __shared__ volatile uint32_t gave_up;
     constexpr int BATCH = WARP ? 8 : 1;   // rows
+    constexpr bool ALL = (HAS & kHasAll) != 0;
+    const bool has_dy = ALL || p.dy, has_dxo = ALL || p.dx_out, has_h = ALL || p.h;
+    const bool has_dx = ALL || p.dx, has_dh = ALL || p.dh, has_w_pre = ALL || p.w_pre;
+    const bool post = ALL ? (HAS & kHasPost) != 0 : p.post != 0;
+    const bool has_w_post = ALL ? (HAS & kHasPost) != 0 : p.w_post != nullptr;
+    const bool gated = ALL ? (HAS & kHasGate) != 0 : p.gate != nullptr;
     const int lanes = WARP ? 32 : static_cast<int>(blockDim.x);
     const int at = WARP ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
     const int own = WARP ? static_cast<int>(threadIdx.x >> 5) : 0;   // this thread's row of a batch
@@ -902,15 +916,15 @@ __global__ void __launch_bounds__(THREADS)
         uint8_t* to = smem + (issued % ring.stages) * ring.stage_bytes;
         uint64_t* bar = &full[issued % ring.stages];
         const int64_t first = static_cast<int64_t>(ahead.r) * p.width;
-        const uint32_t bytes = (p.dy ? n * (2 + sizeof(S)) : 0) + (p.dx_out ? n * sizeof(S) : 0) + (p.h ? n * 2 : 0);
+        const uint32_t bytes = (has_dy ? n * (2 + sizeof(S)) : 0) + (has_dxo ? n * sizeof(S) : 0) + (has_h ? n * 2 : 0);
         ptx::mbar_arrive_expect_tx(bar, bytes);
-        if (p.dy) {
+        if (has_dy) {
             ptx::bulk_load(to, p.dy + first, n * 2, bar);
             ptx::bulk_load(to + ring.x_at, static_cast<const S*>(p.x_out) + first, n * sizeof(S), bar);
         }
-        if (p.dx_out)
+        if (has_dxo)
             ptx::bulk_load(to + ring.dxo_at, static_cast<const S*>(p.dx_out) + first, n * sizeof(S), bar);
-        if (p.h) ptx::bulk_load(to + ring.h_at, p.h + first, n * 2, bar);
+        if (has_h) ptx::bulk_load(to + ring.h_at, p.h + first, n * 2, bar);
         ++issued;
         next(ahead);
     };
@@ -972,8 +986,8 @@ __global__ void __launch_bounds__(THREADS)
             for (int i = 0; i < VPT; ++i) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) t[i][e] = sum_a[i][e];
-                if (!live[i] || !p.post) continue;
-                if (p.w_post) {
+                if (!live[i] || !post) continue;
+                if (has_w_post) {
                     row::shared_pairs(w, p.w_post + col[i]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) t[i][e] = row::mul2(t[i][e], w[e]);
@@ -988,7 +1002,7 @@ __global__ void __launch_bounds__(THREADS)
             }
             out_sums(t, p.dgate_part + k * p.width, p.add_dgate != 0);
         }
-        if (p.post) {
+        if (post) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 if (!live[i]) continue;
@@ -1020,8 +1034,8 @@ __global__ void __launch_bounds__(THREADS)
         next_stat[0] = next_stat[2] = 0.0f;
         next_stat[1] = next_stat[3] = 1.0f;
         const int64_t r = w.r + own;
-        if (w.k >= chunks || r >= w.end || !p.stats) return;
-        if (p.post) {
+        if (w.k >= chunks || r >= w.end || (!ALL && !p.stats)) return;
+        if (post) {
             if constexpr (LAYER) next_stat[0] = p.stats[r];
             next_stat[1] = p.stats[p.rows + r];
         }
@@ -1031,7 +1045,7 @@ __global__ void __launch_bounds__(THREADS)
     load_stats(now);
     uint32_t stage = 0, phase = 0;
     while (now.k < chunks) {
-        const __nv_bfloat16* gate = p.gate ? p.gate + now.k / parts * p.width : nullptr;
+        const __nv_bfloat16* gate = gated ? p.gate + now.k / parts * p.width : nullptr;
         const int k = now.k;
         for (; now.k == k; next(now)) {
             const int64_t r = now.r + own;
@@ -1046,7 +1060,7 @@ __global__ void __launch_bounds__(THREADS)
             const int64_t base = r * p.width, in = static_cast<int64_t>(own) * p.width;
             if (has_row) {
                 f2 d[VPT][4], u[VPT][4];
-                if (p.dy) {
+                if (has_dy) {
                     f2 s0 = 0, s1 = 0;
                     const f2 rs = row::all2(r_pre), mr = row::all2(-m_pre * r_pre);
 #pragma unroll
@@ -1061,13 +1075,13 @@ __global__ void __launch_bounds__(THREADS)
                         a.pairs(d[i]);
                         b.pairs(u[i]);
                         f2 w[4];
-                        if (p.w_pre) row::shared_pairs(w, p.w_pre + col[i]);
+                        if (has_w_pre) row::shared_pairs(w, p.w_pre + col[i]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             u[i][e] = LAYER ? row::fma2(u[i][e], rs, mr) : row::mul2(u[i][e], rs);
                             dw_pre[i][e] = row::fma2(d[i][e], u[i][e], dw_pre[i][e]);
                             if constexpr (LAYER) db_pre[i][e] = row::add2(db_pre[i][e], d[i][e]);
-                            if (p.w_pre) d[i][e] = row::mul2(d[i][e], w[e]);
+                            if (has_w_pre) d[i][e] = row::mul2(d[i][e], w[e]);
                             s0 = row::fma2(d[i][e], u[i][e], s0);
                             if constexpr (LAYER) s1 = row::add2(s1, d[i][e]);
                         }
@@ -1081,7 +1095,7 @@ __global__ void __launch_bounds__(THREADS)
                     for (int i = 0; i < VPT; ++i) {
                         if (!live[i]) continue;
                         f2 o[4];
-                        if (p.dx_out) {
+                        if (has_dxo) {
                             row::Raw8<S> a;
                             a.load_shared(reinterpret_cast<const S*>(st + ring.dxo_at) + in + col[i]);
                             a.pairs(o);
@@ -1100,7 +1114,7 @@ __global__ void __launch_bounds__(THREADS)
                     for (int i = 0; i < VPT; ++i) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) d[i][e] = 0;
-                        if (!live[i] || !p.dx_out) continue;
+                        if (!live[i] || !has_dxo) continue;
                         row::Raw8<S> a;
                         a.load_shared(reinterpret_cast<const S*>(st + ring.dxo_at) + in + col[i]);
                         a.pairs(d[i]);
@@ -1112,24 +1126,24 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) {
                     if (!live[i]) continue;
-                    if (p.dx) {
+                    if (has_dx) {
                         f2 o[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[e] = row::mul2(d[i][e], alpha);
                         row::store_pairs(static_cast<S*>(p.dx) + base + col[i], o);
                     }
-                    if (!p.h) continue;
+                    if (!has_h) continue;
                     row::Raw8<__nv_bfloat16> a;
                     a.load_shared(reinterpret_cast<const __nv_bfloat16*>(st + ring.h_at) + in + col[i]);
                     a.pairs(u[i]);
                     f2 w[4];
-                    if (p.post) {
+                    if (post) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             u[i][e] = LAYER ? row::fma2(u[i][e], rs, mr) : row::mul2(u[i][e], rs);
-                        if (p.w_post) row::shared_pairs(w, p.w_post + col[i]);
+                        if (has_w_post) row::shared_pairs(w, p.w_post + col[i]);
                     }
-                    if (gate) {
+                    if (gated) {
                         f2 gt[4];
                         row::shared_pairs(gt, gate + col[i]);
 #pragma unroll
@@ -1138,36 +1152,36 @@ __global__ void __launch_bounds__(THREADS)
                             if constexpr (LAYER) sum_b[i][e] = row::add2(sum_b[i][e], d[i][e]);
                             d[i][e] = row::mul2(d[i][e], gt[e]);
                         }
-                    } else if (p.post) {
+                    } else if (post) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             sum_a[i][e] = row::fma2(d[i][e], u[i][e], sum_a[i][e]);
                             if constexpr (LAYER) sum_b[i][e] = row::add2(sum_b[i][e], d[i][e]);
                         }
                     }
-                    if (p.post) {
+                    if (post) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            if (p.w_post) d[i][e] = row::mul2(d[i][e], w[e]);
+                            if (has_w_post) d[i][e] = row::mul2(d[i][e], w[e]);
                             s0 = row::fma2(d[i][e], u[i][e], s0);
                             if constexpr (LAYER) s1 = row::add2(s1, d[i][e]);
                         }
                     }
                 }
-                if (p.h) {
+                if (has_h) {
                     f2 ch = 0, cq = 0, scale = row::all2(1.0f);
-                    if (p.post) {
+                    if (post) {
                         float s[2] = {row::lo2(s0) + row::hi2(s0), row::lo2(s1) + row::hi2(s1)};
                         sum(s);
                         scale = rs;
                         ch = row::all2(-r_post * (s[0] * inv_c));
                         cq = row::all2(-r_post * (s[1] * inv_c));
                     }
-                    if (p.dh) {
+                    if (has_dh) {
 #pragma unroll
                         for (int i = 0; i < VPT; ++i) {
                             if (!live[i]) continue;
-                            if (p.post) {
+                            if (post) {
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
                                     const f2 t = LAYER ? row::fma2(u[i][e], ch, cq) : row::mul2(u[i][e], ch);
@@ -1181,14 +1195,14 @@ __global__ void __launch_bounds__(THREADS)
             }
             if (++stage == static_cast<uint32_t>(ring.stages)) { stage = 0; phase ^= 1u; }
             // with a post norm over the CTA its sum's barrier is past the last read
-            if (WARP || !(p.post && p.h)) __syncthreads();
+            if (WARP || !(post && has_h)) __syncthreads();
             if (threadIdx.x == 0 && ahead.k < chunks) fill();
         }
-        if (gate) end_chunk(gate, k, k == static_cast<int>(blockIdx.x));
+        if (gated) end_chunk(gate, k, k == static_cast<int>(blockIdx.x));
     }
     out_sums(dw_pre, my_sums, false);
     if constexpr (LAYER) out_sums(db_pre, my_sums + rows_of, false);
-    if (!p.gate) {
+    if (!gated) {
         out_sums(sum_a, my_sums + 2 * rows_of, false);
         if constexpr (LAYER) out_sums(sum_b, my_sums + 3 * rows_of, false);
     }
@@ -1246,7 +1260,7 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const __grid_constant__
 // for the vectors (14 bytes a column at most), over the CTAs on it.
 constexpr int kRingBytesPerSm = 160 * 1024;
 
-template <typename S, int VPT, bool WARP, bool LAYER, int THREADS>
+template <typename S, int VPT, bool WARP, bool LAYER, int THREADS, int HAS>
 int launch_bwd_ring(const NormBwd& p, const BwdPlan& b, cudaStream_t st) {
     BwdRing ring;
     const uint32_t n = static_cast<uint32_t>(p.width * (WARP ? 8 : 1));
@@ -1260,7 +1274,7 @@ int launch_bwd_ring(const NormBwd& p, const BwdPlan& b, cudaStream_t st) {
     if (ring.stages > 4) ring.stages = 4;
     if (ring.stages < 2) ring.stages = 2;
     const uint32_t bytes = ring.stages * ring.stage_bytes;
-    auto k = norm_bwd_kernel<S, VPT, WARP, LAYER, THREADS>;
+    auto k = norm_bwd_kernel<S, VPT, WARP, LAYER, THREADS, HAS>;
     // per device and instance; setting it again is harmless
     static std::atomic<uint32_t> allowed[64] = {};
     int dev = 0;
@@ -1284,9 +1298,17 @@ template <typename S, bool LAYER>
 int launch_bwd(const NormBwd& p, const BwdPlan& b, cudaStream_t st) {
     const dim3 grid(b.ctas), block(b.threads);
     if (p.width % 8 == 0 && p.width <= kFastWidth) {
-        if (b.warp && b.vpt == 1) return launch_bwd_ring<S, 1, true, LAYER, 256>(p, b, st);
-        if (b.warp) return launch_bwd_ring<S, 2, true, LAYER, 256>(p, b, st);
-        return launch_bwd_ring<S, 2, false, LAYER, 512>(p, b, st);
+        if (b.warp && b.vpt == 1) return launch_bwd_ring<S, 1, true, LAYER, 256, 0>(p, b, st);
+        if (b.warp) return launch_bwd_ring<S, 2, true, LAYER, 256, 0>(p, b, st);
+        if (p.dy && p.x_out && p.dx_out && p.h && p.dx && p.dh && p.w_pre && (!p.post || p.w_post)) {
+            constexpr int A = kHasAll, P = kHasPost, G = kHasGate;
+            if (p.post)
+                return p.gate ? launch_bwd_ring<S, 2, false, LAYER, 512, A | P | G>(p, b, st)
+                              : launch_bwd_ring<S, 2, false, LAYER, 512, A | P>(p, b, st);
+            return p.gate ? launch_bwd_ring<S, 2, false, LAYER, 512, A | G>(p, b, st)
+                          : launch_bwd_ring<S, 2, false, LAYER, 512, A>(p, b, st);
+        }
+        return launch_bwd_ring<S, 2, false, LAYER, 512, 0>(p, b, st);
     }
     if (p.width % 8 == 0)
         launch_pdl(norm_bwd_any_kernel<S, 2, false, true, LAYER, 1024>, grid, block, 0, st, p);
