@@ -304,12 +304,21 @@ __global__ void __launch_bounds__(THREADS)
     }
 }
 
+// HAS of the resident kernels says at compile time which parts there are, for the usual calls: a row
+// is then one stretch of code in which loads move ahead of their uses, where
+// tests between them would hold them back.  0: all tested as the kernel runs.
+constexpr int kHasAll = 1;    // forward: x, h, x', w_pre; backward: dy, x', dx', h, dx,
+                              // dh, w_pre; whole rows (every thread's pieces
+                              // lie within the row); the other parts by bits
+constexpr int kHasPost = 2;   // with w_post
+constexpr int kHasGate = 4;
+
 // The forward for rows in 16-byte pieces up to kFastWidth columns: CTAs stay
 // on the SM and walk the rows, each thread on its own columns, with the
 // vectors of those columns in registers (RMS norm) and the next row's pieces
 // loaded while the current row is reduced -- a row's loads cover the two
 // reductions' latency.  WARP: a warp a row, else the CTA.
-template <typename S, int VPT, bool WARP, bool LAYER, int THREADS>
+template <typename S, int VPT, bool WARP, bool LAYER, int THREADS, int HAS>
 __global__ void __launch_bounds__(THREADS)
     norm_fwd_kernel(const __grid_constant__ NormFwd p) {
     using row::f2;
@@ -318,6 +327,12 @@ __global__ void __launch_bounds__(THREADS)
     __shared__ __align__(16) float part[2][16];
     __shared__ float part_max[128];
     constexpr bool KEEP = !LAYER;
+    constexpr bool ALL = (HAS & kHasAll) != 0;
+    const bool has_h = ALL || p.h, has_x = ALL || p.x, has_x_out = ALL || p.x_out;
+    const bool has_w_pre = ALL || p.w_pre;
+    const bool post = ALL ? (HAS & kHasPost) != 0 : p.post != 0;
+    const bool has_w_post = ALL ? (HAS & kHasPost) != 0 : p.w_post != nullptr;
+    const bool gated = ALL ? (HAS & kHasGate) != 0 : p.gate != nullptr;
     if (!WARP && threadIdx.x < 32) part[threadIdx.x >> 4][threadIdx.x & 15] = 0.0f;
     if (!WARP) __syncthreads();
     const int lanes = WARP ? 32 : static_cast<int>(blockDim.x);
@@ -345,21 +360,21 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         col[i] = 8 * (at + i * lanes);
-        live[i] = col[i] < p.width;
+        live[i] = ALL || col[i] < p.width;
         hn[i].zero();
         xn[i].zero();
         if (live[i]) {
-            if (p.h) hn[i].load(p.h + r * p.width + col[i]);
-            if (xin) xn[i].load(xin + r * p.width + col[i]);
+            if (has_h) hn[i].load(p.h + r * p.width + col[i]);
+            if (has_x) xn[i].load(xin + r * p.width + col[i]);
         }
     }
     f2 wg[KEEP ? VPT : 1][4], wp[VPT][4], bp[KEEP ? 1 : VPT][4];   // w_post * gate, w_pre, b_pre
     int64_t group = 0, group_end = 0;   // the gate row in use and the row after its last
-    const bool scaled = p.w_post || p.gate;
+    const bool scaled = has_w_post || gated;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         if (!live[i]) continue;
-        if (p.w_pre) row::shared_pairs(wp[i], p.w_pre + col[i]);
+        if (has_w_pre) row::shared_pairs(wp[i], p.w_pre + col[i]);
         if constexpr (LAYER) {
             if (p.b_pre) row::shared_pairs(bp[i], p.b_pre + col[i]);
         }
@@ -374,12 +389,12 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) {
                     if (!live[i]) continue;
-                    if (p.w_post) row::shared_pairs(wg[KEEP ? i : 0], p.w_post + col[i]);
-                    if (p.gate) {
+                    if (has_w_post) row::shared_pairs(wg[KEEP ? i : 0], p.w_post + col[i]);
+                    if (gated) {
                         f2 t[4];
                         row::shared_pairs(t, p.gate + group * p.width + col[i]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) wg[i][e] = p.w_post ? row::mul2(wg[i][e], t[e]) : t[e];
+                        for (int e = 0; e < 4; ++e) wg[i][e] = has_w_post ? row::mul2(wg[i][e], t[e]) : t[e];
                     }
                 }
             }
@@ -396,8 +411,8 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 if (!live[i]) continue;
-                if (p.h) hn[i].load(p.h + next + col[i]);
-                if (xin) xn[i].load(xin + next + col[i]);
+                if (has_h) hn[i].load(p.h + next + col[i]);
+                if (has_x) xn[i].load(xin + next + col[i]);
             }
         }
         auto stats = [&](float& mean, float& rstd) {
@@ -429,14 +444,14 @@ __global__ void __launch_bounds__(THREADS)
             rstd = rsqrtf(s[0] * inv_c + p.eps);
         };
         float mean_post = 0.0f, rstd_post = 0.0f, mean_pre = 0.0f, rstd_pre = 0.0f;
-        if (p.post) stats(mean_post, rstd_post);
+        if (post) stats(mean_post, rstd_post);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             f2 xs[4];
             x[i].pairs(xs);
             if (!live[i]) continue;
             if constexpr (KEEP) {
-                const f2 rs = row::all2(p.post ? rstd_post : 1.0f);
+                const f2 rs = row::all2(post ? rstd_post : 1.0f);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     if (scaled) v[i][e] = row::mul2(v[i][e], wg[i][e]);
@@ -444,11 +459,11 @@ __global__ void __launch_bounds__(THREADS)
                 }
             } else {
                 f2 t[4];
-                if (p.post) {
+                if (post) {
                     const f2 m = row::all2(-mean_post), rs = row::all2(rstd_post);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[i][e] = row::mul2(row::add2(v[i][e], m), rs);
-                    if (p.w_post) {
+                    if (has_w_post) {
                         row::shared_pairs(t, p.w_post + col[i]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) v[i][e] = row::mul2(v[i][e], t[e]);
@@ -459,7 +474,7 @@ __global__ void __launch_bounds__(THREADS)
                         for (int e = 0; e < 4; ++e) v[i][e] = row::add2(v[i][e], t[e]);
                     }
                 }
-                if (p.gate) {
+                if (gated) {
                     row::shared_pairs(t, p.gate + group * p.width + col[i]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[i][e] = row::mul2(v[i][e], t[e]);
@@ -467,7 +482,7 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[i][e] = row::fma2(xs[e], alpha, v[i][e]);
             }
-            if (p.x_out) row::store_pairs(static_cast<S*>(p.x_out) + base + col[i], v[i]);
+            if (has_x_out) row::store_pairs(static_cast<S*>(p.x_out) + base + col[i], v[i]);
         }
         if (p.y || p.q || p.stats) stats(mean_pre, rstd_pre);
         if (p.stats && at == 0) {
@@ -485,7 +500,7 @@ __global__ void __launch_bounds__(THREADS)
             for (int e = 0; e < 4; ++e) {
                 if constexpr (LAYER) v[i][e] = row::add2(v[i][e], m);
                 v[i][e] = row::mul2(v[i][e], rs);
-                if (p.w_pre) v[i][e] = row::mul2(v[i][e], wp[i][e]);
+                if (has_w_pre) v[i][e] = row::mul2(v[i][e], wp[i][e]);
                 if constexpr (LAYER) {
                     if (p.b_pre) v[i][e] = row::add2(v[i][e], bp[i][e]);
                 }
@@ -540,9 +555,27 @@ void launch_fwd(const NormFwd& p, cudaStream_t st) {
         const int64_t per_sm = warp ? 2 : 512 / threads;
         const int64_t want = warp ? (p.rows + 7) / 8 : p.rows, most = num_sms() * per_sm;
         const dim3 grid(static_cast<unsigned>(want < most ? want : most));
-        if (pieces <= 32) launch_pdl(norm_fwd_kernel<S, 1, true, LAYER, 256>, grid, dim3(256), 0, st, p);
-        else if (warp) launch_pdl(norm_fwd_kernel<S, 2, true, LAYER, 256>, grid, dim3(256), 0, st, p);
-        else launch_pdl(norm_fwd_kernel<S, 2, false, LAYER, 512>, grid, dim3(threads), 0, st, p);
+        if (pieces <= 32) {
+            launch_pdl(norm_fwd_kernel<S, 1, true, LAYER, 256, 0>, grid, dim3(256), 0, st, p);
+            return;
+        }
+        if (warp) {
+            launch_pdl(norm_fwd_kernel<S, 2, true, LAYER, 256, 0>, grid, dim3(256), 0, st, p);
+            return;
+        }
+        if (p.x && p.h && p.x_out && p.w_pre && (!p.post || p.w_post) && p.width == 16 * threads) {
+            constexpr int A = kHasAll, P = kHasPost, G = kHasGate;
+            if (p.post && p.gate)
+                launch_pdl(norm_fwd_kernel<S, 2, false, LAYER, 512, A | P | G>, grid, dim3(threads), 0, st, p);
+            else if (p.post)
+                launch_pdl(norm_fwd_kernel<S, 2, false, LAYER, 512, A | P>, grid, dim3(threads), 0, st, p);
+            else if (p.gate)
+                launch_pdl(norm_fwd_kernel<S, 2, false, LAYER, 512, A | G>, grid, dim3(threads), 0, st, p);
+            else
+                launch_pdl(norm_fwd_kernel<S, 2, false, LAYER, 512, A>, grid, dim3(threads), 0, st, p);
+            return;
+        }
+        launch_pdl(norm_fwd_kernel<S, 2, false, LAYER, 512, 0>, grid, dim3(threads), 0, st, p);
         return;
     }
     if (p.width % 8 == 0) {
@@ -848,14 +881,6 @@ __global__ void __launch_bounds__(THREADS)
 // the chunk's rows  dgate = w_post A + b_post B,  dw_post = sum of gate A  and
 // db_post = sum of gate B  over the chunks: one pair of running sums serves
 // the gate's and the post norm's gradients.
-//
-// HAS says at compile time which parts there are, for the usual calls: a row
-// is then one stretch of code in which loads move ahead of their uses, where
-// tests between them would hold them back.  0: all tested as the kernel runs.
-constexpr int kHasAll = 1;    // dy, x', dx', h, dx, dh, w_pre; the other parts by bits
-constexpr int kHasPost = 2;   // with w_post
-constexpr int kHasGate = 4;
-
 struct BwdRing {
     int stages;
     uint32_t x_at, dxo_at, h_at, stage_bytes;   // dy at 0
@@ -955,7 +980,7 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         col[i] = 8 * (at + i * lanes);
-        live[i] = col[i] < p.width;
+        live[i] = ALL || col[i] < p.width;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             dw_pre[i][e] = sum_a[i][e] = 0;
@@ -1300,7 +1325,8 @@ int launch_bwd(const NormBwd& p, const BwdPlan& b, cudaStream_t st) {
     if (p.width % 8 == 0 && p.width <= kFastWidth) {
         if (b.warp && b.vpt == 1) return launch_bwd_ring<S, 1, true, LAYER, 256, 0>(p, b, st);
         if (b.warp) return launch_bwd_ring<S, 2, true, LAYER, 256, 0>(p, b, st);
-        if (p.dy && p.x_out && p.dx_out && p.h && p.dx && p.dh && p.w_pre && (!p.post || p.w_post)) {
+        if (p.dy && p.x_out && p.dx_out && p.h && p.dx && p.dh && p.w_pre && (!p.post || p.w_post) &&
+            p.width == 16 * b.threads) {
             constexpr int A = kHasAll, P = kHasPost, G = kHasGate;
             if (p.post)
                 return p.gate ? launch_bwd_ring<S, 2, false, LAYER, 512, A | P | G>(p, b, st)
