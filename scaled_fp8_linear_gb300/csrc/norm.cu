@@ -93,20 +93,22 @@ __device__ __forceinline__ float row_scale(uint32_t top, int fmt, int pow2) {
     return pow2 ? __uint_as_float(__float_as_uint(s) & 0xFF800000u) : s;
 }
 
-// Eight elements from p; VEC: 16-byte pieces, all eight present.  Otherwise
-// the first n, zeros after them.
+// A thread's eight elements of a piece: VEC, the 16 bytes at p (fp32: 32).
+// Otherwise, for rows that do not start on 16 bytes, the n elements at p,
+// p + step, ... (step: the threads of a row, so that a warp's loads are
+// contiguous), zeros after them.
 template <bool VEC>
-__device__ __forceinline__ void load8(float (&v)[8], const __nv_bfloat16* p, int n) {
+__device__ __forceinline__ void load8(float (&v)[8], const __nv_bfloat16* p, int n, int step) {
     if constexpr (VEC) {
         row::unpack8(v, row::ld_stream(p));
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = e < n ? __bfloat162float(p[e]) : 0.0f;
+        for (int e = 0; e < 8; ++e) v[e] = e < n ? __bfloat162float(p[e * step]) : 0.0f;
     }
 }
 
 template <bool VEC>
-__device__ __forceinline__ void load8(float (&v)[8], const float* p, int n) {
+__device__ __forceinline__ void load8(float (&v)[8], const float* p, int n, int step) {
     if constexpr (VEC) {
         const uint4 a = row::ld_stream(p), b = row::ld_stream(p + 4);
         v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
@@ -115,52 +117,64 @@ __device__ __forceinline__ void load8(float (&v)[8], const float* p, int n) {
         v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = e < n ? p[e] : 0.0f;
+        for (int e = 0; e < 8; ++e) v[e] = e < n ? p[e * step] : 0.0f;
+    }
+}
+
+// The same where `on`, zeros elsewhere.
+template <bool VEC, typename T>
+__device__ __forceinline__ void load8(float (&v)[8], const T* p, int n, int step, bool on) {
+    if (on) {
+        load8<VEC>(v, p, n, step);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
     }
 }
 
 // The same through L1, for the vectors that every row shares.
-template <bool VEC>
-__device__ __forceinline__ void shared8(float (&v)[8], const float* p, int n) {
+template <bool VEC, typename T>
+__device__ __forceinline__ void shared8(float (&v)[8], const T* p, int n, int step) {
     if constexpr (VEC) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-        const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        row::f2 t[4];
+        row::shared_pairs(t, p);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = row::lo2(t[e]);
+            v[2 * e + 1] = row::hi2(t[e]);
+        }
     } else {
-        load8<false>(v, p, n);
+        load8<false>(v, p, n, step);
     }
 }
 
-template <bool VEC>
-__device__ __forceinline__ void shared8(float (&v)[8], const __nv_bfloat16* p, int n) {
-    if constexpr (VEC)
-        row::unpack8(v, __ldg(reinterpret_cast<const uint4*>(p)));
-    else
-        load8<false>(v, p, n);
-}
+__device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 
-template <bool VEC>
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8], int n) {
+template <bool VEC, typename T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8], int n, int step) {
     if constexpr (VEC) {
-        *reinterpret_cast<uint4*>(p) = row::pack8(v);
+        const row::f2 t[4] = {row::mk2(v[0], v[1]), row::mk2(v[2], v[3]), row::mk2(v[4], v[5]),
+                              row::mk2(v[6], v[7])};
+        row::store_pairs(p, t);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (e < n) p[e] = __float2bfloat16_rn(v[e]);
+            if (e < n) store1(p + e * step, v[e]);
     }
 }
 
+// First column of piece i of thread `at` of a row's `lanes` threads, and how
+// many of its elements lie in the row.
 template <bool VEC>
-__device__ __forceinline__ void store8(float* p, const float (&v)[8], int n) {
-    if constexpr (VEC) {
-        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < n) p[e] = v[e];
-    }
+__device__ __forceinline__ int piece_col(int at, int i, int lanes) {
+    return VEC ? 8 * (at + i * lanes) : at + 8 * i * lanes;
+}
+template <bool VEC>
+__device__ __forceinline__ int piece_len(int col, int lanes, int64_t width) {
+    const int left = static_cast<int>(width) - col;
+    if (left <= 0) return 0;
+    return min(8, VEC ? left : (left + lanes - 1) / lanes);
 }
 
 // Mean (layer norm) and 1/sqrt(variance + eps) of the row whose pieces the
@@ -193,18 +207,18 @@ __device__ __forceinline__ void row_stats(const float (&v)[VPT][8], const int (&
 
 // v = w (v - mean) rstd + b on one piece.
 template <bool VEC>
-__device__ __forceinline__ void apply_norm(float (&v)[8], const float* w, const float* b, int64_t c,
-                                           int n, float mean, float rstd) {
+__device__ __forceinline__ void apply_norm(float (&v)[8], const float* w, const float* b, int c,
+                                           int n, int step, float mean, float rstd) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = (v[e] - mean) * rstd;
     float s[8];
     if (w) {
-        shared8<VEC>(s, w + c, n);
+        shared8<VEC>(s, w + c, n, step);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= s[e];
     }
     if (b) {
-        shared8<VEC>(s, b + c, n);
+        shared8<VEC>(s, b + c, n, step);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += s[e];
     }
@@ -230,13 +244,13 @@ __global__ void __launch_bounds__(THREADS)
     int n[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int64_t c = 8 * static_cast<int64_t>(at + i * lanes);
-        n[i] = static_cast<int>(p.width - c < 0 ? 0 : (p.width - c < 8 ? p.width - c : 8));
+        const int c = piece_col<VEC>(at, i, lanes);
+        n[i] = piece_len<VEC>(c, lanes, p.width);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[i][e] = x[i][e] = 0.0f;
         if (n[i] > 0) {
-            if (p.h) load8<VEC>(v[i], p.h + base + c, n[i]);
-            if (xin) load8<VEC>(x[i], xin + base + c, n[i]);
+            if (p.h) load8<VEC>(v[i], p.h + base + c, n[i], lanes);
+            if (xin) load8<VEC>(x[i], xin + base + c, n[i], lanes);
         }
     }
     float mean_post = 0.0f, rstd_post = 0.0f, mean_pre = 0.0f, rstd_pre = 0.0f;
@@ -246,19 +260,19 @@ __global__ void __launch_bounds__(THREADS)
         p.gate ? p.gate + (r / p.rows_per_gate) * p.width : nullptr;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int64_t c = 8 * static_cast<int64_t>(at + i * lanes);
+        const int c = piece_col<VEC>(at, i, lanes);
         if (n[i] <= 0) continue;
-        if (p.post) apply_norm<VEC>(v[i], p.w_post, p.b_post, c, n[i], mean_post, rstd_post);
+        if (p.post) apply_norm<VEC>(v[i], p.w_post, p.b_post, c, n[i], lanes, mean_post, rstd_post);
         if (gate) {
             float g[8];
-            shared8<VEC>(g, gate + c, n[i]);
+            shared8<VEC>(g, gate + c, n[i], lanes);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[i][e] *= g[e];
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             v[i][e] = VEC || e < n[i] ? fmaf(p.alpha, x[i][e], v[i][e]) : 0.0f;
-        if (p.x_out) store8<VEC>(static_cast<S*>(p.x_out) + base + c, v[i], n[i]);
+        if (p.x_out) store8<VEC>(static_cast<S*>(p.x_out) + base + c, v[i], n[i], lanes);
     }
     if (p.y || p.q || p.stats)
         row_stats<VPT, WARP, VEC, LAYER>(v, n, inv_c, p.eps, part, turn, mean_pre, rstd_pre);
@@ -272,10 +286,10 @@ __global__ void __launch_bounds__(THREADS)
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int64_t c = 8 * static_cast<int64_t>(at + i * lanes);
+        const int c = piece_col<VEC>(at, i, lanes);
         if (n[i] <= 0) continue;
-        apply_norm<VEC>(v[i], p.w_pre, p.b_pre, c, n[i], mean_pre, rstd_pre);
-        if (p.y) store8<VEC>(p.y + base + c, v[i], n[i]);
+        apply_norm<VEC>(v[i], p.w_pre, p.b_pre, c, n[i], lanes, mean_pre, rstd_pre);
+        if (p.y) store8<VEC>(p.y + base + c, v[i], n[i], lanes);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             if (VEC || e < n[i]) top = max(top, row::abs_bits(v[i][e]));
@@ -292,14 +306,16 @@ __global__ void __launch_bounds__(THREADS)
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int64_t c = 8 * static_cast<int64_t>(at + i * lanes);
+        const int c = piece_col<VEC>(at, i, lanes);
         if (n[i] <= 0) continue;
         const uint2 code = row::cvt8(p.q_fmt, v[i], s);
         if constexpr (VEC) {
             *reinterpret_cast<uint2*>(p.q + base + c) = code;
         } else {
-            for (int e = 0; e < n[i]; ++e)
-                p.q[base + c + e] = static_cast<uint8_t>((e < 4 ? code.x : code.y) >> (8 * (e & 3)));
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < n[i])
+                    p.q[base + c + e * lanes] = static_cast<uint8_t>((e < 4 ? code.x : code.y) >> (8 * (e & 3)));
         }
     }
 }
@@ -584,6 +600,9 @@ void launch_fwd(const NormFwd& p, cudaStream_t st) {
     } else if (pieces <= 64) {
         launch_pdl(norm_fwd_any_kernel<S, 2, true, false, LAYER, 256>,
                    dim3(static_cast<unsigned>((p.rows + 7) / 8)), dim3(256), 0, st, p);
+    } else if (threads <= 512) {
+        launch_pdl(norm_fwd_any_kernel<S, 2, false, false, LAYER, 512>,
+                   dim3(static_cast<unsigned>(p.rows)), dim3(threads), 0, st, p);
     } else {
         launch_pdl(norm_fwd_any_kernel<S, 2, false, false, LAYER, 1024>,
                    dim3(static_cast<unsigned>(p.rows)), dim3(threads), 0, st, p);
@@ -654,15 +673,16 @@ BwdPlan bwd_plan(int64_t rows, int64_t width, int64_t gate_rows) {
 // Adds the CTA's rows of one accumulator (WARP: its eight warps' first) and
 // writes the result to `out`; `add` adds to what is there.
 template <int VPT, bool WARP, bool VEC>
-__device__ __forceinline__ void flush(float (&acc)[VPT][8], const int (&n)[VPT], int at, int lanes,
-                                      int64_t width, float* out, bool add, float* buf) {
+__device__ __forceinline__ void flush(const float (&acc)[VPT][8], const int (&n)[VPT], int at,
+                                      int lanes, int64_t width, float* out, bool add, float* buf) {
     if constexpr (WARP) {
         const int warp = threadIdx.x >> 5;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) buf[warp * 512 + 8 * (at + i * 32) + e] = acc[i][e];
+            for (int e = 0; e < 8; ++e)
+                buf[warp * 512 + piece_col<VEC>(at, i, 32) + (VEC ? e : e * 32)] = acc[i][e];
         __syncthreads();
         for (int64_t c = threadIdx.x; c < width; c += blockDim.x) {
             float s = 0.0f;
@@ -671,23 +691,26 @@ __device__ __forceinline__ void flush(float (&acc)[VPT][8], const int (&n)[VPT],
             out[c] = add ? out[c] + s : s;
         }
     } else {
+        const int step = VEC ? 1 : lanes;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (n[i] <= 0) continue;
-            float* o = out + 8 * static_cast<int64_t>(at + i * lanes);
+            float* o = out + piece_col<VEC>(at, i, lanes);
             if (add) {
-                for (int e = 0; e < n[i]; ++e) o[e] += acc[i][e];
+                for (int e = 0; e < n[i]; ++e) o[e * step] += acc[i][e];
             } else {
-                store8<VEC>(o, acc[i], n[i]);
+                store8<VEC>(o, acc[i], n[i], lanes);
             }
         }
     }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[i][e] = 0.0f;
 }
 
+// The gate is one row within a chunk, so with A = sum dX hh and B = sum dX over
+// the chunk's rows  dgate = w_post A + b_post B,  dw_post = sum of gate A  and
+// db_post = sum of gate B  over the chunks: one pair of running sums serves
+// the gate's and the post norm's gradients.
+//
+// This kernel takes any width; the resident one below takes the usual ones.
 template <typename S, int VPT, bool WARP, bool VEC, bool LAYER, int THREADS>
 __global__ void __launch_bounds__(THREADS)
     norm_bwd_any_kernel(const __grid_constant__ NormBwd p) {
@@ -702,19 +725,30 @@ __global__ void __launch_bounds__(THREADS)
     const float inv_c = 1.0f / static_cast<float>(p.width);
     int turn = 0;
 
-    float dw_pre[VPT][8], dw_post[VPT][8], dg[VPT][8];
-    float db_pre[LAYER ? VPT : 1][8], db_post[LAYER ? VPT : 1][8];
-    int n[VPT];
+    float dw_pre[VPT][8], sum_a[VPT][8], db_pre[LAYER ? VPT : 1][8], sum_b[LAYER ? VPT : 1][8];
+    int n[VPT], col[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int64_t c = 8 * static_cast<int64_t>(at + i * lanes);
-        n[i] = static_cast<int>(p.width - c < 0 ? 0 : (p.width - c < 8 ? p.width - c : 8));
+        col[i] = piece_col<VEC>(at, i, lanes);
+        n[i] = piece_len<VEC>(col[i], lanes, p.width);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            dw_pre[i][e] = dw_post[i][e] = dg[i][e] = 0.0f;
-            if constexpr (LAYER) db_pre[i][e] = db_post[i][e] = 0.0f;
+            dw_pre[i][e] = sum_a[i][e] = 0.0f;
+            if constexpr (LAYER) db_pre[i][e] = sum_b[i][e] = 0.0f;
         }
     }
+    auto sum = [&](float (&s)[2]) {
+        if constexpr (LAYER) {
+            row_sum<WARP>(s, part, turn);
+        } else {
+            float t[1] = {s[0]};
+            row_sum<WARP>(t, part, turn);
+            s[0] = t[0];
+            s[1] = 0.0f;
+        }
+    };
+    const int64_t rows_of = static_cast<int64_t>(gridDim.x) * p.width;
+    float* const my_sums = p.dw_part + static_cast<int64_t>(blockIdx.x) * p.width;
 
     const int64_t chunks = p.groups * p.parts, in_group = p.rows / p.groups;
     for (int64_t k = blockIdx.x; k < chunks; k += gridDim.x) {
@@ -724,150 +758,166 @@ __global__ void __launch_bounds__(THREADS)
         const __nv_bfloat16* gate = p.gate ? p.gate + group * p.width : nullptr;
         for (int64_t r = begin + first; r < end; r += step) {
             const int64_t base = r * p.width;
-            float d[VPT][8], u[VPT][8], hv[VPT][8];
+            float d[VPT][8], u[VPT][8];
             float m_post = 0.0f, r_post = 1.0f;
             if (p.post) {
                 m_post = LAYER ? p.stats[r] : 0.0f;
                 r_post = p.stats[p.rows + r];
             }
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                const int64_t c = 8 * static_cast<int64_t>(at + i * lanes);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) d[i][e] = hv[i][e] = 0.0f;
-                if (n[i] > 0) {
-                    if (p.dx_out) load8<VEC>(d[i], static_cast<const S*>(p.dx_out) + base + c, n[i]);
-                    if (p.h) load8<VEC>(hv[i], p.h + base + c, n[i]);
-                }
-            }
             if (p.dy) {
                 const float m_pre = LAYER ? p.stats[2 * p.rows + r] : 0.0f;
                 const float r_pre = p.stats[3 * p.rows + r];
-                float g[VPT][8], s[2] = {0.0f, 0.0f};
+                float s[2] = {0.0f, 0.0f};
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) {
-                    const int64_t c = 8 * static_cast<int64_t>(at + i * lanes);
+                    load8<VEC>(d[i], p.dy + base + col[i], n[i], lanes, n[i] > 0);
+                    load8<VEC>(u[i], static_cast<const S*>(p.x_out) + base + col[i], n[i], lanes, n[i] > 0);
+                }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) g[i][e] = u[i][e] = 0.0f;
+                for (int i = 0; i < VPT; ++i) {
                     if (n[i] <= 0) continue;
-                    load8<VEC>(g[i], p.dy + base + c, n[i]);
-                    load8<VEC>(u[i], static_cast<const S*>(p.x_out) + base + c, n[i]);
                     float w[8];
-                    if (p.w_pre) shared8<VEC>(w, p.w_pre + c, n[i]);
+                    if (p.w_pre) shared8<VEC>(w, p.w_pre + col[i], n[i], lanes);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        u[i][e] = (u[i][e] - m_pre) * r_pre;
-                        if (!VEC && e >= n[i]) u[i][e] = 0.0f;
-                        dw_pre[i][e] = fmaf(g[i][e], u[i][e], dw_pre[i][e]);
-                        if constexpr (LAYER) db_pre[i][e] += g[i][e];
-                        if (p.w_pre) g[i][e] *= w[e];
-                        s[0] = fmaf(g[i][e], u[i][e], s[0]);
-                        s[1] += g[i][e];
+                        u[i][e] = VEC || e < n[i] ? (u[i][e] - m_pre) * r_pre : 0.0f;
+                        dw_pre[i][e] = fmaf(d[i][e], u[i][e], dw_pre[i][e]);
+                        if constexpr (LAYER) db_pre[i][e] += d[i][e];
+                        if (p.w_pre) d[i][e] *= w[e];
+                        s[0] = fmaf(d[i][e], u[i][e], s[0]);
+                        s[1] += d[i][e];
                     }
                 }
-                if constexpr (LAYER) {
-                    row_sum<WARP>(s, part, turn);
-                } else {
-                    float t[1] = {s[0]};
-                    row_sum<WARP>(t, part, turn);
-                    s[0] = t[0];
-                    s[1] = 0.0f;
-                }
+                float o[VPT][8];   // on its way while the row is summed
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    load8<VEC>(o[i], static_cast<const S*>(p.dx_out) + base + col[i], n[i], lanes,
+                               p.dx_out && n[i] > 0);
+                sum(s);
                 const float su = s[0] * inv_c, sg = s[1] * inv_c;
 #pragma unroll
                 for (int i = 0; i < VPT; ++i)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        d[i][e] = fmaf(r_pre, g[i][e] - sg - u[i][e] * su, d[i][e]);
+                        d[i][e] = fmaf(r_pre, d[i][e] - sg - u[i][e] * su, o[i][e]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    load8<VEC>(d[i], static_cast<const S*>(p.dx_out) + base + col[i], n[i], lanes,
+                               p.dx_out && n[i] > 0);
             }
-            // from here d is dX; columns past the row hold values that no one uses
+            // d is dX (columns past the row hold values that no one uses); u
+            // becomes the block's output, normed
+            if (p.h) {
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    load8<VEC>(u[i], p.h + base + col[i], n[i], lanes, n[i] > 0);
+            }
             float s[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int64_t c = 8 * static_cast<int64_t>(at + i * lanes);
                 if (n[i] <= 0) continue;
                 if (p.dx) {
                     float o[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) o[e] = p.alpha * d[i][e];
-                    store8<VEC>(static_cast<S*>(p.dx) + base + c, o, n[i]);
+                    store8<VEC>(static_cast<S*>(p.dx) + base + col[i], o, n[i], lanes);
                 }
                 if (!p.h) continue;
+                if (p.post) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) u[i][e] = (u[i][e] - m_post) * r_post;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    sum_a[i][e] = fmaf(d[i][e], u[i][e], sum_a[i][e]);
+                    if constexpr (LAYER) sum_b[i][e] += d[i][e];
+                }
                 float w[8];
-                if (p.post) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) hv[i][e] = (hv[i][e] - m_post) * r_post;
-                    if (p.w_post) shared8<VEC>(w, p.w_post + c, n[i]);
-                }
                 if (gate) {
-                    float gt[8], pv[8];
-                    shared8<VEC>(gt, gate + c, n[i]);
+                    shared8<VEC>(w, gate + col[i], n[i], lanes);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) pv[e] = p.post && p.w_post ? hv[i][e] * w[e] : hv[i][e];
-                    if (LAYER && p.post && p.b_post) {
-                        float b[8];
-                        shared8<VEC>(b, p.b_post + c, n[i]);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) pv[e] += b[e];
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        dg[i][e] = fmaf(d[i][e], pv[e], dg[i][e]);
-                        d[i][e] *= gt[e];
-                    }
+                    for (int e = 0; e < 8; ++e) d[i][e] *= w[e];
                 }
                 if (p.post) {
+                    if (p.w_post) shared8<VEC>(w, p.w_post + col[i], n[i], lanes);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        if (!VEC && e >= n[i]) {
-                            d[i][e] = 0.0f;
-                            continue;
-                        }
-                        dw_post[i][e] = fmaf(d[i][e], hv[i][e], dw_post[i][e]);
-                        if constexpr (LAYER) db_post[i][e] += d[i][e];
                         if (p.w_post) d[i][e] *= w[e];
-                        s[0] = fmaf(d[i][e], hv[i][e], s[0]);
+                        if (!VEC && e >= n[i]) d[i][e] = 0.0f;
+                        s[0] = fmaf(d[i][e], u[i][e], s[0]);
                         s[1] += d[i][e];
                     }
                 }
             }
             if (!p.h) continue;
-            if (p.post) {
-                if constexpr (LAYER) {
-                    row_sum<WARP>(s, part, turn);
-                } else {
-                    float t[1] = {s[0]};
-                    row_sum<WARP>(t, part, turn);
-                    s[0] = t[0];
-                    s[1] = 0.0f;
-                }
-            }
+            if (p.post) sum(s);
             const float sh = s[0] * inv_c, sq = s[1] * inv_c;
             if (p.dh) {
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) {
-                    const int64_t c = 8 * static_cast<int64_t>(at + i * lanes);
                     if (n[i] <= 0) continue;
                     if (p.post) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            d[i][e] = r_post * (d[i][e] - sq - hv[i][e] * sh);
+                            d[i][e] = r_post * (d[i][e] - sq - u[i][e] * sh);
                     }
-                    store8<VEC>(p.dh + base + c, d[i], n[i]);
+                    store8<VEC>(p.dh + base + col[i], d[i], n[i], lanes);
                 }
             }
         }
-        if (gate && p.dgate_part)
-            flush<VPT, WARP, VEC>(dg, n, at, lanes, p.width, p.dgate_part + k * p.width,
+        if (!gate) continue;
+        // the end of a chunk: its part of dgate, and of the post norm's sums
+        if (p.dgate_part) {
+            float t[VPT][8];
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                float w[8], b[8];
+                const bool on = n[i] > 0 && p.post;
+                if (on && p.w_post) shared8<VEC>(w, p.w_post + col[i], n[i], lanes);
+                if (on && p.b_post) shared8<VEC>(b, p.b_post + col[i], n[i], lanes);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    t[i][e] = on && p.w_post ? sum_a[i][e] * w[e] : sum_a[i][e];
+                    if constexpr (LAYER) {
+                        if (on && p.b_post) t[i][e] = fmaf(sum_b[i][e], b[e], t[i][e]);
+                    }
+                }
+            }
+            flush<VPT, WARP, VEC>(t, n, at, lanes, p.width, p.dgate_part + k * p.width,
                                   p.add_dgate != 0, buf);
+        }
+        if (p.post) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                if (n[i] <= 0) continue;
+                float w[8];
+                shared8<VEC>(w, gate + col[i], n[i], lanes);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    sum_a[i][e] *= w[e];
+                    if constexpr (LAYER) sum_b[i][e] *= w[e];
+                }
+            }
+            const bool add = k != blockIdx.x;
+            flush<VPT, WARP, VEC>(sum_a, n, at, lanes, p.width, my_sums + 2 * rows_of, add, buf);
+            if constexpr (LAYER)
+                flush<VPT, WARP, VEC>(sum_b, n, at, lanes, p.width, my_sums + 3 * rows_of, add, buf);
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                sum_a[i][e] = 0.0f;
+                if constexpr (LAYER) sum_b[i][e] = 0.0f;
+            }
     }
-    const int64_t rows_of = static_cast<int64_t>(gridDim.x) * p.width;
-    float* out = p.dw_part + static_cast<int64_t>(blockIdx.x) * p.width;
-    flush<VPT, WARP, VEC>(dw_pre, n, at, lanes, p.width, out, false, buf);
-    flush<VPT, WARP, VEC>(dw_post, n, at, lanes, p.width, out + 2 * rows_of, false, buf);
-    if constexpr (LAYER) {
-        flush<VPT, WARP, VEC>(db_pre, n, at, lanes, p.width, out + rows_of, false, buf);
-        flush<VPT, WARP, VEC>(db_post, n, at, lanes, p.width, out + 3 * rows_of, false, buf);
+    flush<VPT, WARP, VEC>(dw_pre, n, at, lanes, p.width, my_sums, false, buf);
+    if constexpr (LAYER) flush<VPT, WARP, VEC>(db_pre, n, at, lanes, p.width, my_sums + rows_of, false, buf);
+    if (!p.gate) {
+        flush<VPT, WARP, VEC>(sum_a, n, at, lanes, p.width, my_sums + 2 * rows_of, false, buf);
+        if constexpr (LAYER)
+            flush<VPT, WARP, VEC>(sum_b, n, at, lanes, p.width, my_sums + 3 * rows_of, false, buf);
     }
 }
 
@@ -877,10 +927,6 @@ __global__ void __launch_bounds__(THREADS)
 // consecutive in memory, so four copies), because the column sums leave no
 // registers to hold a row ahead.  A stage is read piece by piece as the row
 // needs it, and filled again once every thread is past its last read.
-// The gate is one row within a chunk, so with A = sum dX hh and B = sum dX over
-// the chunk's rows  dgate = w_post A + b_post B,  dw_post = sum of gate A  and
-// db_post = sum of gate B  over the chunks: one pair of running sums serves
-// the gate's and the post norm's gradients.
 struct BwdRing {
     int stages;
     uint32_t x_at, dxo_at, h_at, stage_bytes;   // dy at 0
@@ -1340,6 +1386,8 @@ int launch_bwd(const NormBwd& p, const BwdPlan& b, cudaStream_t st) {
         launch_pdl(norm_bwd_any_kernel<S, 2, false, true, LAYER, 1024>, grid, block, 0, st, p);
     else if (b.warp)
         launch_pdl(norm_bwd_any_kernel<S, 2, true, false, LAYER, 256>, grid, block, 0, st, p);
+    else if (b.threads <= 512)
+        launch_pdl(norm_bwd_any_kernel<S, 2, false, false, LAYER, 512>, grid, block, 0, st, p);
     else
         launch_pdl(norm_bwd_any_kernel<S, 2, false, false, LAYER, 1024>, grid, block, 0, st, p);
     return FP8_OK;
