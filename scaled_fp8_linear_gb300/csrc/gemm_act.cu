@@ -58,52 +58,87 @@ struct ActParams {
 
 // ------------------------------------------------------------------ activations
 
-__device__ __forceinline__ float sigmoid_scaled(float num, float x) {   // num / (1 + exp(-x))
-    return __fdividef(num, 1.0f + __expf(-x));
+using row::f2;
+
+__device__ __forceinline__ float ex2(float x) {   // 2^x
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluC = 0.7978845608028654f, kGeluA = 0.044715f;   // sqrt(2 / pi)
 constexpr float kSqrtHalf = 0.7071067811865476f, kInvSqrt2Pi = 0.3989422804014327f;
 
+// 1 / (1 + exp(-k x)) for a pair, `scale` = -k log2(e).  Far out, 2^x runs to
+// infinity or zero and the result to 0 or 1.
+__device__ __forceinline__ f2 sigmoid2(f2 x, float scale) {
+    const f2 t = row::mul2(x, row::all2(scale));
+    return row::mk2(rcp(1.0f + ex2(row::lo2(t))), rcp(1.0f + ex2(row::hi2(t))));
+}
+
+// The argument of GELU's tanh form: z + 0.044715 z^3; 1 + tanh(u) = 2 / (1 + exp(-2u)).
+__device__ __forceinline__ f2 gelu_arg2(f2 z) {
+    return row::mul2(z, row::fma2(row::mul2(z, z), row::all2(kGeluA), row::all2(1.0f)));
+}
+
+__device__ __forceinline__ f2 normal_cdf2(f2 z) {
+    const f2 t = row::mul2(z, row::all2(kSqrtHalf));
+    return row::fma2(row::mk2(erff(row::lo2(t)), erff(row::hi2(t))), row::all2(0.5f), row::all2(0.5f));
+}
+
+__device__ __forceinline__ float relu(float z) { return z > 0.0f ? z : (z != z ? z : 0.0f); }
+
 template <int ACT>
-__device__ __forceinline__ float act_of(float z) {
-    if constexpr (ACT == FP8_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
-    if constexpr (ACT == FP8_ACT_SILU) return sigmoid_scaled(z, z);
-    if constexpr (ACT == FP8_ACT_GELU) return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
-    // 1 + tanh(u) = 2 / (1 + exp(-2u))
+__device__ __forceinline__ f2 act2(f2 z) {
+    if constexpr (ACT == FP8_ACT_RELU) return row::mk2(relu(row::lo2(z)), relu(row::hi2(z)));
+    if constexpr (ACT == FP8_ACT_SILU) return row::mul2(z, sigmoid2(z, -kLog2e));
+    if constexpr (ACT == FP8_ACT_GELU) return row::mul2(z, normal_cdf2(z));
     if constexpr (ACT == FP8_ACT_GELU_TANH)
-        return sigmoid_scaled(z, 2.0f * kGeluC * (z + kGeluA * z * z * z));
+        return row::mul2(z, sigmoid2(gelu_arg2(z), -2.0f * kGeluC * kLog2e));
     return z;
 }
 
 // act(z) and its derivative.
 template <int ACT>
-__device__ __forceinline__ void act_and_grad(float z, float& a, float& g) {
+__device__ __forceinline__ void act_and_grad2(f2 z, f2& a, f2& g) {
+    const f2 one = row::all2(1.0f), minus = row::all2(-1.0f);
     if constexpr (ACT == FP8_ACT_RELU) {
-        a = z > 0.0f ? z : (z != z ? z : 0.0f);
-        g = z > 0.0f ? 1.0f : 0.0f;
+        a = act2<ACT>(z);
+        g = row::mk2(row::lo2(z) > 0.0f ? 1.0f : 0.0f, row::hi2(z) > 0.0f ? 1.0f : 0.0f);
     } else if constexpr (ACT == FP8_ACT_SILU) {
-        const float s = sigmoid_scaled(1.0f, z);
-        a = z * s;
-        g = s * (1.0f + z * (1.0f - s));
+        const f2 s = sigmoid2(z, -kLog2e);
+        a = row::mul2(z, s);
+        g = row::fma2(a, row::fma2(s, minus, one), s);   // s + z s (1 - s)
     } else if constexpr (ACT == FP8_ACT_GELU) {
-        const float cdf = 0.5f * (1.0f + erff(z * kSqrtHalf));
-        a = z * cdf;
-        g = cdf + z * kInvSqrt2Pi * __expf(-0.5f * z * z);
+        const f2 cdf = normal_cdf2(z);
+        const f2 e = row::mul2(row::mul2(z, z), row::all2(-0.5f * kLog2e));
+        a = row::mul2(z, cdf);
+        g = row::fma2(row::mul2(z, row::all2(kInvSqrt2Pi)), row::mk2(ex2(row::lo2(e)), ex2(row::hi2(e))), cdf);
     } else if constexpr (ACT == FP8_ACT_GELU_TANH) {
-        const float s = sigmoid_scaled(1.0f, 2.0f * kGeluC * (z + kGeluA * z * z * z));
-        a = z * s;
-        g = s + a * (1.0f - s) * 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
+        const f2 s = sigmoid2(gelu_arg2(z), -2.0f * kGeluC * kLog2e);
+        const f2 du = row::fma2(row::mul2(z, z), row::all2(6.0f * kGeluC * kGeluA), row::all2(2.0f * kGeluC));
+        a = row::mul2(z, s);
+        g = row::fma2(row::mul2(a, du), row::fma2(s, minus, one), s);
     } else {
         a = z;
-        g = 1.0f;
+        g = one;
     }
 }
 
 template <int ACT, int N>
 __device__ __forceinline__ void act_all(float (&v)[N]) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = act_of<ACT>(v[j]);
+    for (int j = 0; j < N; j += 2) {
+        const f2 a = act2<ACT>(row::mk2(v[j], v[j + 1]));
+        v[j] = row::lo2(a);
+        v[j + 1] = row::hi2(a);
+    }
 }
 
 template <int N>
@@ -206,14 +241,30 @@ __device__ __forceinline__ Tile tile_of(int unit, const Units* u, const ActParam
 
 // ------------------------------------------------------------------ the epilogue
 
-// Writes one box of 32 rows from `slot` (this warp's, filled through `fill`).
-template <typename Fill>
-__device__ __forceinline__ void emit(uint8_t* slot, const CUtensorMap* map, int64_t x, int64_t y,
+// A warp's output staging: SLOTS boxes of 2 KB in turn, so that a box is filled
+// while the copies of the ones before it read theirs.
+constexpr int kSlotBytes = 2048;
+
+template <int SLOTS>
+struct Staging {
+    uint8_t* base;
+    uint32_t turn = 0;
+    __device__ __forceinline__ uint8_t* next() {
+        uint8_t* s = base + turn * kSlotBytes;
+        turn = turn + 1 == SLOTS ? 0 : turn + 1;
+        return s;
+    }
+};
+
+// Writes one box of 32 rows from the warp's next slot, filled through `fill`.
+template <int SLOTS, typename Fill>
+__device__ __forceinline__ void emit(Staging<SLOTS>& staging, const CUtensorMap* map, int64_t x, int64_t y,
                                      bool in_range, Fill fill) {
     const int lane = threadIdx.x & 31;
-    if (lane == 0) ptx::bulk_wait_group_read<0>();   // the slot's last box has been read
+    uint8_t* slot = staging.next();
+    if (lane == 0) ptx::bulk_wait_group_read<SLOTS - 1>();   // the slot's last box has been read
     __syncwarp();
-    fill();
+    fill(slot);
     ptx::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
@@ -225,9 +276,10 @@ __device__ __forceinline__ void emit(uint8_t* slot, const CUtensorMap* map, int6
 
 // 32 columns of this thread's row as bf16: 64 bytes, in the TMA's 64-byte
 // swizzle (piece j of row r at j ^ ((r >> 1) & 3)), which spreads the banks.
-__device__ __forceinline__ void emit_bf16(uint8_t* slot, const float (&v)[32], const CUtensorMap* map,
+template <int SLOTS>
+__device__ __forceinline__ void emit_bf16(Staging<SLOTS>& staging, const float (&v)[32], const CUtensorMap* map,
                                           int64_t x, int64_t y, bool in_range) {
-    emit(slot, map, x, y, in_range, [&] {
+    emit(staging, map, x, y, in_range, [&](uint8_t* slot) {
         const int lane = threadIdx.x & 31, swz = (lane >> 1) & 3;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -240,10 +292,11 @@ __device__ __forceinline__ void emit_bf16(uint8_t* slot, const float (&v)[32], c
     });
 }
 
-__device__ __forceinline__ void emit_codes(uint8_t* slot, const float (&v)[32], int fmt, float s,
+template <int SLOTS>
+__device__ __forceinline__ void emit_codes(Staging<SLOTS>& staging, const float (&v)[32], int fmt, float s,
                                            const CUtensorMap* map, int64_t x, int64_t y,
                                            bool in_range) {
-    emit(slot, map, x, y, in_range, [&] {
+    emit(staging, map, x, y, in_range, [&](uint8_t* slot) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -292,12 +345,64 @@ struct OutMaps {
     CUtensorMap z, z_up, d, q;
 };
 
+// The residual of a warp's 32 rows x 32 columns, as four coalesced loads a
+// thread (four lanes a row: 64 bytes, eight rows a load).  Loaded by the rows'
+// own threads instead, every 16 bytes would be a line of its own: 88 us
+// against 37 for an 8192 x 4096 x 1024 product.
+struct Residual {
+    uint4 w[4];
+    __device__ __forceinline__ void load(const ActParams& p, int64_t m0, int row_end, int64_t n0) {
+        if (!p.residual) return;
+        const int lane = threadIdx.x & 31;
+        const int64_t n = n0 + 8 * (lane & 3);
+        if (n >= p.N) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t m = m0 + 8 * i + (lane >> 2);
+            if (m < row_end) w[i] = row::ld_stream(p.residual + m * p.N + n);
+        }
+    }
+};
+
+// D of 32 columns: adds the residual to v (handed to the rows' threads through
+// the slot that D's box leaves from) and, where D is wanted, writes the box.
+template <int SLOTS>
+__device__ __forceinline__ void emit_d(Staging<SLOTS>& staging, float (&v)[32], const Residual& res,
+                                       const ActParams& p, const CUtensorMap* map, int64_t x, int64_t y,
+                                       bool in_range) {
+    emit(staging, map, x, y, in_range && p.has_d, [&](uint8_t* slot) {
+        const int lane = threadIdx.x & 31, swz = (lane >> 1) & 3;
+        uint8_t* own = slot + lane * 64;
+        if (p.residual) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 8 * i + (lane >> 2);
+                *reinterpret_cast<uint4*>(slot + r * 64 + 16 * ((lane & 3) ^ ((r >> 1) & 3))) = res.w[i];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float t[8];
+                row::unpack8(t, *reinterpret_cast<const uint4*>(own + 16 * (j ^ swz)));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[8 * j + e] += t[e];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(own + 16 * (j ^ swz)) =
+                make_uint4(row::pack_bf16(v[8 * j], v[8 * j + 1]), row::pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                           row::pack_bf16(v[8 * j + 4], v[8 * j + 5]), row::pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+    });
+}
+
 // The epilogue of a warp: 32 rows x COLS output columns of one tile, from
-// TMEM column `tcol` (gated: the up product UP columns further on).
-template <bool GATED, int UP, int COLS>
-__device__ __forceinline__ void epilogue(uint8_t* slot, uint32_t tcol, const Tile& t, int64_t m0,
-                                         int64_t n_first, const ActParams& p, const OutMaps& maps,
-                                         uint32_t& top) {
+// TMEM column `tcol` (gated: the up product UP columns further on).  `res`
+// holds the first chunk's residual; each later one is loaded a chunk ahead.
+template <bool GATED, int UP, int COLS, int SLOTS>
+__device__ __forceinline__ void epilogue(Staging<SLOTS>& staging, Residual& res, uint32_t tcol, const Tile& t,
+                                         int64_t m0, int64_t n_first, const ActParams& p,
+                                         const OutMaps& maps, float& top) {
     const int lane = threadIdx.x & 31;
     const int64_t m = m0 + lane;
     const bool live = m < t.row_end;
@@ -312,42 +417,31 @@ __device__ __forceinline__ void epilogue(uint8_t* slot, uint32_t tcol, const Til
         const int n_left = static_cast<int>(min(p.N - n0, static_cast<int64_t>(32)));
         const bool in_range = in_rows && n_left > 0;
         float z[32];
-        {
-            uint32_t r[32];
-            ptx::tmem_ld_32x32b_x32(tcol + c * 32, r);
-            ptx::tmem_wait_ld();
-            dequant(z, r, fa, t.expert * b_rows + n0, n_left, p, sb0);
-        }
-        if (p.has_z) emit_bf16(slot, z, &maps.z, n0, m0, in_range);
+        uint32_t r[32], r_up[GATED ? 32 : 1];
+        ptx::tmem_ld_32x32b_x32(tcol + c * 32, r);
+        if constexpr (GATED) ptx::tmem_ld_32x32b_x32(tcol + UP + c * 32, r_up);
+        ptx::tmem_wait_ld();
+        dequant(z, r, fa, t.expert * b_rows + n0, n_left, p, sb0);
+        if (p.has_z) emit_bf16(staging, z, &maps.z, n0, m0, in_range);
         apply_act(p.act, z);
         if constexpr (GATED) {
             float up[32];
-            uint32_t r[32];
-            ptx::tmem_ld_32x32b_x32(tcol + UP + c * 32, r);
-            ptx::tmem_wait_ld();
-            dequant(up, r, fa, t.expert * b_rows + p.N + n0, n_left, p, sb0);
-            if (p.has_z) emit_bf16(slot, up, &maps.z_up, n0, m0, in_range);
+            dequant(up, r_up, fa, t.expert * b_rows + p.N + n0, n_left, p, sb0);
+            if (p.has_z) emit_bf16(staging, up, &maps.z_up, n0, m0, in_range);
 #pragma unroll
             for (int j = 0; j < 32; ++j) z[j] *= up[j];
         }
-        if (p.residual && live) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-                if (j < n_left) {
-                    float v[8];
-                    row::unpack8(v, row::ld_stream(p.residual + m * p.N + n0 + j));
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) z[j + e] += v[e];
-                }
-            }
-        }
-        if (p.has_d) emit_bf16(slot, z, &maps.d, n0, m0, in_range);
+        if (p.has_d || p.residual) emit_d(staging, z, res, p, &maps.d, n0, m0, in_range);
+        if (c + 1 < COLS / 32) res.load(p, m0, t.row_end, n0 + 32);
         if (p.has_q) {
-            emit_codes(slot, z, p.q_fmt, qs, &maps.q, n0, m0, in_range);
+            emit_codes(staging, z, p.q_fmt, qs, &maps.q, n0, m0, in_range);
             if (p.amax && live) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (j < n_left) top = max(top, row::abs_bits(z[j]));
+                for (int j = 0; j < 32; j += 16) {   // n_left is a multiple of 16
+                    if (j >= n_left) continue;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) top = row::max_abs(top, z[j + e]);
+                }
             }
         }
     }
@@ -359,12 +453,11 @@ __device__ __forceinline__ void epilogue(uint8_t* slot, uint32_t tcol, const Til
 // 128 output columns; the even CTA holds their gate rows of B and the odd
 // one their up rows, which is how cta_group::2 splits B).  Roles and
 // barriers as in gemm.cu's pair kernel.
-constexpr int kPairStages = 6;
+constexpr int kPairStages = 5, kPairSlots = 3;
 constexpr int kHalf = 128;
 constexpr int kPairTile = 256;
 constexpr int kPairStageBytes = 2 * kHalf * BK;
-constexpr int kSlotBytes = 2048;
-constexpr int kPairSmem = kPairStages * kPairStageBytes + kEpiWarps * kSlotBytes + 256 +
+constexpr int kPairSmem = kPairStages * kPairStageBytes + kEpiWarps * kPairSlots * kSlotBytes + 256 +
                           static_cast<int>(sizeof(Units)) + 1024;
 
 template <bool GATED>
@@ -379,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint8_t* ring = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* slots = ring + kPairStages * kPairStageBytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(slots + kEpiWarps * kSlotBytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(slots + kEpiWarps * kPairSlots * kSlotBytes);
     uint64_t* empty = full + kPairStages;
     uint64_t* tfull = empty + kPairStages;
     uint64_t* tempty = tfull + 2;
@@ -494,10 +587,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= 4) {
         const int qd = warp & 3, side = (warp - 4) >> 2;   // TMEM lanes, half of the columns
-        uint8_t* slot = slots + (warp - 4) * kSlotBytes;
-        uint32_t acc = 0, acc_phase = 0, top = 0;
+        Staging<kPairSlots> staging{slots + (warp - 4) * kPairSlots * kSlotBytes};
+        Residual res;
+        uint32_t acc = 0, acc_phase = 0;
+        float top = 0.0f;
         for (int u = pair; u < num_units; u += npairs) {
             const Tile t = tile_of(u, units, p, kPairTile);
+            const int64_t m0 = t.row0 + rank * kHalf + qd * 32;
+            const int64_t n0 = static_cast<int64_t>(t.n_blk) * TN + side * (TN / 2);
+            res.load(p, m0, t.row_end, n0);
             bool ok = (lane == 0) ? ptx::mbar_wait(&tfull[acc], acc_phase, abort_flag) : false;
             ok = __shfl_sync(row::kAll, ok, 0);
             if (!ok) break;
@@ -505,9 +603,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ptx::tc_fence_after();
             const uint32_t tcol = tmem_base + (static_cast<uint32_t>(qd * 32) << 16) +
                                   acc * kPairTile + side * (TN / 2);
-            epilogue<GATED, kHalf, TN / 2>(slot, tcol, t, t.row0 + rank * kHalf + qd * 32,
-                                           static_cast<int64_t>(t.n_blk) * TN + side * (TN / 2), p,
-                                           maps, top);
+            epilogue<GATED, kHalf, TN / 2>(staging, res, tcol, t, m0, n0, p, maps, top);
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::cluster_addr(&tempty[acc], 0));
@@ -515,8 +611,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (acc == 0) acc_phase ^= 1u;
         }
         if (lane == 0) ptx::bulk_wait_group_all();   // every TMA store has completed
-        top = __reduce_max_sync(row::kAll, top);
-        if (p.amax && lane == 0) row::raise_amax(p.amax, top);
+        const uint32_t bits = __reduce_max_sync(row::kAll, row::abs_bits(top));
+        if (p.amax && lane == 0) row::raise_amax(p.amax, bits);
         __syncwarp();
     }
 
@@ -529,9 +625,181 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && *abort_flag && p.status) atomicOr(p.status, 1u);
 }
 
+// ------------------------------------------------------------------ single-CTA kernel
+
+// 128 rows by BN accumulator columns (gated: BN / 2 of the gate's product and
+// BN / 2 of the up product).  For problems whose tiles fit the SMs at once,
+// where a tile's own latency is the cost (BN 64 or 128), and for experts with
+// few rows each, where 256-row tiles would multiply too many absent rows.
+template <int BN>
+struct TileLayout {
+    static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 5 : 6;
+    static constexpr int SLOTS = BN == 256 ? 1 : 3;
+
+    static constexpr int A_BYTES = kHalf * BK, B_BYTES = BN * BK;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int SMEM = STAGES * STAGE_BYTES + kEpiWarps * SLOTS * kSlotBytes + 256 +
+                                static_cast<int>(sizeof(Units)) + 1024;
+};
+
+template <int BN, bool GATED>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_act_tile_kernel(const __grid_constant__ CUtensorMap tmA,
+                         const __grid_constant__ CUtensorMap tmB,
+                         const __grid_constant__ OutMaps maps, const __grid_constant__ ActParams p) {
+    ptx::griddep_launch_dependents();
+    using L = TileLayout<BN>;
+    constexpr int STAGES = L::STAGES, SLOTS = L::SLOTS;
+    constexpr int TN = GATED ? BN / 2 : BN;           // output columns of a tile
+    constexpr int COLS = TN >= 64 ? TN / 2 : 32;      // of an epilogue warp
+    constexpr int SIDES = TN / COLS;
+    constexpr uint32_t TMEM_COLS = 2 * BN;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* slots = ring + STAGES * L::STAGE_BYTES;
+    uint64_t* full = reinterpret_cast<uint64_t*>(slots + kEpiWarps * SLOTS * kSlotBytes);
+    uint64_t* empty = full + STAGES;
+    uint64_t* tfull = empty + STAGES;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* done = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+    Units* units = reinterpret_cast<Units*>(reinterpret_cast<uint8_t*>(full) + 256);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(&full[s], 1);
+            ptx::mbar_init(&empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            ptx::mbar_init(&tfull[a], 1);
+            ptx::mbar_init(&tempty[a], 4 * SIDES);
+        }
+        ptx::mbar_init(done, 1);
+        *abort_flag = 0;
+        ptx::fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        ptx::tma_prefetch_desc(&tmA);
+        ptx::tma_prefetch_desc(&tmB);
+    }
+    if (warp == 2) {
+        ptx::tmem_alloc(tmem_slot, TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    ptx::griddep_wait();
+    ptx::tc_fence_before();
+    make_units(units, p, kHalf);   // its barriers also cover the set-up above
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int num_units = units->first[p.experts];
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0;
+            int64_t issued = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; ok && u < num_units; u += gridDim.x) {
+                const Tile t = tile_of(u, units, p, kHalf);
+                const int64_t yb64 = static_cast<int64_t>(t.expert) * (GATED ? 2 : 1) * p.N + t.n_blk * TN;
+                const int yb = static_cast<int>(yb64), yu = static_cast<int>(yb64 + p.N);
+                for (int kb = 0; kb < p.num_kb; ++kb) {
+                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
+                    uint8_t* sa = ring + stage * L::STAGE_BYTES;
+                    ptx::mbar_arrive_expect_tx(&full[stage], L::STAGE_BYTES);
+                    ptx::tma_load_2d(sa, &tmA, &full[stage], kb * BK, t.row0);
+                    ptx::tma_load_2d(sa + L::A_BYTES, &tmB, &full[stage], kb * BK, yb);
+                    if constexpr (GATED)
+                        ptx::tma_load_2d(sa + L::A_BYTES + L::B_BYTES / 2, &tmB, &full[stage], kb * BK, yu);
+                    ++issued;
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+            }
+            // drain: the last copies into each slot have landed
+            uint32_t never = 0;
+            for (int s = 0; s < STAGES; ++s) {
+                if (issued <= s && issued < STAGES) break;
+                const uint32_t par = (static_cast<uint32_t>(s) < stage) ? phase : (phase ^ 1u);
+                ptx::mbar_wait(&full[s], par, &never);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = ptx::idesc_f8f6f4(p.fa, p.fb, kHalf, BN);
+            const uint64_t tmpl = ptx::sdesc_kmajor_sw128(0);
+            uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; ok && u < num_units; u += gridDim.x) {
+                if (!ptx::mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag)) break;
+                ptx::tc_fence_after();
+                const uint32_t d = tmem_base + acc * BN;
+                for (int kb = 0; kb < p.num_kb; ++kb) {
+                    if (!ptx::mbar_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
+                    ptx::tc_fence_after();
+                    uint8_t* sa = ring + stage * L::STAGE_BYTES;
+                    const uint64_t ad = tmpl | ((ptx::smem_u32(sa) & 0x3FFFFu) >> 4);
+                    const uint64_t bd = tmpl | ((ptx::smem_u32(sa + L::A_BYTES) & 0x3FFFFu) >> 4);
+#pragma unroll
+                    for (int k = 0; k < BK / UMMA_K; ++k)
+                        ptx::mma_f8f6f4(d, ad + k * (UMMA_K >> 4), bd + k * (UMMA_K >> 4), idesc,
+                                        (kb | k) != 0);
+                    ptx::mma_commit(&empty[stage]);
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                ptx::mma_commit(&tfull[acc]);
+                acc ^= 1u;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+            // every MMA issued by this thread must finish before TMEM is released
+            uint32_t never = 0;
+            ptx::mma_commit(done);
+            ptx::mbar_wait(done, 0, &never);
+        }
+    } else if (warp >= 4 && (warp - 4) >> 2 < SIDES) {
+        const int qd = warp & 3, side = (warp - 4) >> 2;
+        Staging<SLOTS> staging{slots + (warp - 4) * SLOTS * kSlotBytes};
+        Residual res;
+        uint32_t acc = 0, acc_phase = 0;
+        float top = 0.0f;
+        for (int u = blockIdx.x; u < num_units; u += gridDim.x) {
+            const Tile t = tile_of(u, units, p, kHalf);
+            const int64_t m0 = t.row0 + qd * 32;
+            const int64_t n0 = static_cast<int64_t>(t.n_blk) * TN + side * COLS;
+            res.load(p, m0, t.row_end, n0);
+            bool ok = (lane == 0) ? ptx::mbar_wait(&tfull[acc], acc_phase, abort_flag) : false;
+            ok = __shfl_sync(row::kAll, ok, 0);
+            if (!ok) break;
+            __syncwarp();
+            ptx::tc_fence_after();
+            const uint32_t tcol = tmem_base + (static_cast<uint32_t>(qd * 32) << 16) + acc * BN + side * COLS;
+            epilogue<GATED, BN / 2, COLS>(staging, res, tcol, t, m0, n0, p, maps, top);
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&tempty[acc]);
+            acc ^= 1u;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+        if (lane == 0) ptx::bulk_wait_group_all();   // every TMA store has completed
+        const uint32_t bits = __reduce_max_sync(row::kAll, row::abs_bits(top));
+        if (p.amax && lane == 0) row::raise_amax(p.amax, bits);
+        __syncwarp();
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem_base, TMEM_COLS);
+    }
+    if (threadIdx.x == 0 && *abort_flag && p.status) atomicOr(p.status, 1u);
+}
+
 // ------------------------------------------------------------------ gradient of the epilogue
 
-constexpr int kBwdRows = 64;   // rows a CTA: 8 passes of 8 rows x 256 columns
+constexpr int kBwdRows = 64;   // rows a CTA: 8 warps, 8 rows each
 
 struct ActBwd {
     const __nv_bfloat16* d;
@@ -540,67 +808,83 @@ struct ActBwd {
     uint8_t* q;
     const float* q_scale;
     float* amax;
-    float* part;      // [row blocks][N or 2N] partial column sums, or null
+    float* part;      // [row blocks][N or 2N] partial column sums (BIAS)
     int64_t M, N;
     int64_t col_blocks;
     int q_fmt;
 };
 
 // Elementwise, HBM-bound: D's gradient and z are read once, dz is written
-// once.  Column sums stay in registers over the CTA's rows.
-template <int ACT, bool GATED>
+// once, 256 columns a warp.  The pairs' packed instructions keep it off the
+// issue limit.  BIAS: column sums stay in registers over the CTA's rows.
+template <int ACT, bool GATED, bool BIAS>
 __global__ void __launch_bounds__(256) act_bwd_kernel(const __grid_constant__ ActBwd p) {
     ptx::griddep_launch_dependents();
-    __shared__ float sums[8][256];
+    __shared__ float sums[BIAS ? 8 : 1][256];
     ptx::griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t block_row = blockIdx.x / p.col_blocks;
-    const int64_t c0 = (blockIdx.x % p.col_blocks) * 256, c = c0 + lane * 8;
+    const int64_t c0 = (blockIdx.x - block_row * p.col_blocks) * 256, c = c0 + lane * 8;
     const int64_t width = GATED ? 2 * p.N : p.N;
     const bool on = c < p.N;   // N is a multiple of 16
-    const float qs = p.q ? p.q_scale[0] : 0.0f;
-    float s0[8] = {}, s1[8] = {};
-    uint32_t top = 0;
-    auto put = [&](const float (&v)[8], int64_t at) {
-        if (p.dz) *reinterpret_cast<uint4*>(p.dz + at) = row::pack8(v);
+    const f2 qs = row::all2(p.q ? p.q_scale[0] : 0.0f);
+    f2 s0[4] = {}, s1[4] = {};
+    float top = 0.0f;
+    auto put = [&](const f2 (&v)[4], int64_t at) {
+        if (p.dz) row::store_pairs(p.dz + at, v);
         if (p.q) {
-            *reinterpret_cast<uint2*>(p.q + at) = row::cvt8(p.q_fmt, v, qs);
+            uint32_t code[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) top = max(top, row::abs_bits(v[e]));
+            for (int e = 0; e < 4; ++e) {
+                const f2 t = row::mul2(v[e], qs);
+                code[e] = row::cvt_pair(p.q_fmt, row::lo2(t), row::hi2(t));
+                top = row::max_abs(row::max_abs(top, row::lo2(v[e])), row::hi2(v[e]));
+            }
+            *reinterpret_cast<uint2*>(p.q + at) = make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
         }
     };
     if (on) {
-#pragma unroll 2
+        const int64_t m0 = block_row * kBwdRows + warp;
+        // one row at a time: many warps hide its loads (116 us a pass with four
+        // rows' loads in flight, 117 with one, 131 with two)
+#pragma unroll 1
         for (int i = 0; i < kBwdRows / 8; ++i) {
-            const int64_t m = block_row * kBwdRows + i * 8 + warp;
+            const int64_t m = m0 + i * 8;
             if (m >= p.M) break;
-            float d[8], z[8], u[8];
-            row::unpack8(d, row::ld_stream(p.d + m * p.N + c));
-            row::unpack8(z, row::ld_stream(p.z + m * width + c));
-            if constexpr (GATED) row::unpack8(u, row::ld_stream(p.z + m * width + p.N + c));
+            row::Raw8<__nv_bfloat16> rd, rz, ru;
+            rd.load(p.d + m * p.N + c);
+            rz.load(p.z + m * width + c);
+            if constexpr (GATED) ru.load(p.z + m * width + p.N + c);
+            f2 d[4], z[4], u[4];
+            rd.pairs(d);
+            rz.pairs(z);
+            if constexpr (GATED) ru.pairs(u);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float a, g;
-                act_and_grad<ACT>(z[e], a, g);
+            for (int e = 0; e < 4; ++e) {
+                f2 a, g;
+                act_and_grad2<ACT>(z[e], a, g);
                 if constexpr (GATED) {
-                    z[e] = d[e] * u[e] * g;
-                    u[e] = d[e] * a;
-                    s1[e] += u[e];
+                    z[e] = row::mul2(row::mul2(d[e], u[e]), g);
+                    u[e] = row::mul2(d[e], a);
+                    if constexpr (BIAS) s1[e] = row::add2(s1[e], u[e]);
                 } else {
-                    z[e] = d[e] * g;
+                    z[e] = row::mul2(d[e], g);
                 }
-                s0[e] += z[e];
+                if constexpr (BIAS) s0[e] = row::add2(s0[e], z[e]);
             }
             put(z, m * width + c);
             if constexpr (GATED) put(u, m * width + p.N + c);
         }
     }
-    if (p.part) {
+    if constexpr (BIAS) {
 #pragma unroll
         for (int h = 0; h < (GATED ? 2 : 1); ++h) {
             __syncthreads();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sums[warp][lane * 8 + e] = h ? s1[e] : s0[e];
+            for (int e = 0; e < 4; ++e) {
+                sums[warp][lane * 8 + 2 * e] = row::lo2(h ? s1[e] : s0[e]);
+                sums[warp][lane * 8 + 2 * e + 1] = row::hi2(h ? s1[e] : s0[e]);
+            }
             __syncthreads();
             if (c0 + threadIdx.x < p.N) {
                 float s = 0.0f;
@@ -611,15 +895,20 @@ __global__ void __launch_bounds__(256) act_bwd_kernel(const __grid_constant__ Ac
         }
     }
     if (p.amax) {
-        top = __reduce_max_sync(row::kAll, top);
-        if (lane == 0) row::raise_amax(p.amax, top);
+        const uint32_t bits = __reduce_max_sync(row::kAll, row::abs_bits(top));
+        if (lane == 0) row::raise_amax(p.amax, bits);
     }
 }
 
 template <int ACT>
 void launch_act_bwd(const ActBwd& p, bool gated, unsigned ctas, cudaStream_t st) {
-    if (gated) launch_pdl(act_bwd_kernel<ACT, true>, dim3(ctas), dim3(256), 0, st, p);
-    else launch_pdl(act_bwd_kernel<ACT, false>, dim3(ctas), dim3(256), 0, st, p);
+    if (gated) {
+        if (p.part) launch_pdl(act_bwd_kernel<ACT, true, true>, dim3(ctas), dim3(256), 0, st, p);
+        else launch_pdl(act_bwd_kernel<ACT, true, false>, dim3(ctas), dim3(256), 0, st, p);
+    } else {
+        if (p.part) launch_pdl(act_bwd_kernel<ACT, false, true>, dim3(ctas), dim3(256), 0, st, p);
+        else launch_pdl(act_bwd_kernel<ACT, false, false>, dim3(ctas), dim3(256), 0, st, p);
+    }
 }
 
 // ------------------------------------------------------------------ host side
@@ -671,9 +960,16 @@ int raster_group(int64_t K) {
     return g;
 }
 
+// At most this many tiles of `rows` rows and `cols` output columns, however
+// the experts' rows are cut.
+int64_t most_tiles(const fp8_gemm_act_args_t* a, int rows, int cols) {
+    return ((a->M + rows - 1) / rows + a->experts - 1) * ((a->N + cols - 1) / cols);
+}
+
 template <bool GATED>
 int launch_pair(const fp8_gemm_act_args_t* a, ActParams& p, const OutMaps& maps, cudaStream_t st) {
-    const int64_t b_rows = a->gated ? 2 * a->N : a->N;
+    constexpr int TN = GATED ? kHalf : kPairTile;
+    const int64_t b_rows = GATED ? 2 * a->N : a->N;
     CUtensorMap tmA, tmB;
     int r = make_kmajor_map(&tmA, a->A, a->M, a->K, kHalf);
     if (r == FP8_OK) r = make_kmajor_map(&tmB, a->B, b_rows * a->experts, a->K, kHalf);
@@ -681,12 +977,58 @@ int launch_pair(const fp8_gemm_act_args_t* a, ActParams& p, const OutMaps& maps,
     auto k = gemm_act_pair_kernel<GATED>;
     if (r == FP8_OK) r = kernel_slots(k, GATED, kPairSmem, 2, &clusters);
     if (r != FP8_OK) return r;
-    p.num_n = static_cast<int>((a->N + (GATED ? kHalf : kPairTile) - 1) / (GATED ? kHalf : kPairTile));
-    // at most this many tiles, however the experts' rows are cut
-    const int64_t tiles = ((a->M + kPairTile - 1) / kPairTile + a->experts - 1) * p.num_n;
+    p.num_n = static_cast<int>((a->N + TN - 1) / TN);
+    const int64_t tiles = most_tiles(a, kPairTile, TN);
     const unsigned grid = 2 * static_cast<unsigned>(tiles < clusters ? tiles : clusters);
     launch_pdl(k, dim3(grid), dim3(kThreads), kPairSmem, st, tmA, tmB, maps, p);
     return launch_status("fp8_gemm_act");
+}
+
+template <int BN, bool GATED>
+int launch_tile(const fp8_gemm_act_args_t* a, ActParams& p, const OutMaps& maps, cudaStream_t st) {
+    constexpr int TN = GATED ? BN / 2 : BN, SMEM = TileLayout<BN>::SMEM;
+    const int64_t b_rows = GATED ? 2 * a->N : a->N;
+    CUtensorMap tmA, tmB;
+    int r = make_kmajor_map(&tmA, a->A, a->M, a->K, kHalf);
+    if (r == FP8_OK) r = make_kmajor_map(&tmB, a->B, b_rows * a->experts, a->K, TN);
+    int ctas = 0;
+    auto k = gemm_act_tile_kernel<BN, GATED>;
+    constexpr int id = 2 + (BN == 64 ? 0 : BN == 128 ? 2 : 4) + GATED;
+    if (r == FP8_OK) r = kernel_slots(k, id, SMEM, 1, &ctas);
+    if (r != FP8_OK) return r;
+    p.num_n = static_cast<int>((a->N + TN - 1) / TN);
+    const int64_t tiles = most_tiles(a, kHalf, TN);
+    const unsigned grid = static_cast<unsigned>(tiles < ctas ? tiles : ctas);
+    launch_pdl(k, dim3(grid), dim3(kThreads), SMEM, st, tmA, tmB, maps, p);
+    return launch_status("fp8_gemm_act");
+}
+
+template <bool GATED>
+int launch_gemm_act(const fp8_gemm_act_args_t* a, ActParams& p, const OutMaps& maps, cudaStream_t st) {
+    // The tile shape that finishes first: rounds over the SMs times a tile's
+    // time, in units of a 128 x 256 tile's.  A CTA pair's 256 x 256 tile takes
+    // 0.92 of it (half the B bytes an SM): 1177 against 1270 us for a gated
+    // 4096 x 28672 x 8192 product; but its rows come in 256s, and a product of
+    // 4099 x 8192 x 28672 takes 692 us in pairs and 640 us in 128 rows.  128 x 128
+    // takes 0.67 and 128 x 64 0.60 (the A bytes are the same): 547 and 983 us
+    // against 406 for gated products of 16384 x 4096 x 4096 over 16 experts, but
+    // 8.9 and 6.8 us against 11.6 for 256 x 512 x 512.  An expert's last tile
+    // is taken as half full, with no whole rounds.
+    const int sms = num_sms();
+    auto cost = [&](int rows, int acc_cols, int slots, double time) {
+        const int64_t cols = GATED ? acc_cols / 2 : acc_cols;
+        const double n = static_cast<double>((a->N + cols - 1) / cols);
+        if (a->offsets)
+            return (static_cast<double>(a->M) / rows + 0.5 * a->experts) * n / slots * time;
+        const int64_t tiles = most_tiles(a, rows, static_cast<int>(cols));
+        return static_cast<double>((tiles + slots - 1) / slots) * time;
+    };
+    const double c64 = cost(kHalf, 64, sms, 0.60), c128 = cost(kHalf, 128, sms, 0.67);
+    const double c256 = cost(kHalf, 256, sms, 1.0), pair = cost(kPairTile, kPairTile, sms / 2, 0.92);
+    if (c64 <= c128 && c64 <= c256 && c64 <= pair) return launch_tile<64, GATED>(a, p, maps, st);
+    if (c128 <= c256 && c128 <= pair) return launch_tile<128, GATED>(a, p, maps, st);
+    if (c256 < pair) return launch_tile<256, GATED>(a, p, maps, st);
+    return launch_pair<GATED>(a, p, maps, st);
 }
 
 }  // namespace
@@ -764,7 +1106,7 @@ int fp8_gemm_act(const fp8_gemm_act_args_t* a, void* stream) {
         r = make_output_map(&maps.q, a->q, a->M, a->N, a->N, CU_TENSOR_MAP_DATA_TYPE_UINT8, 32,
                             CU_TENSOR_MAP_SWIZZLE_NONE);
     if (r != FP8_OK) return r;
-    return a->gated ? launch_pair<true>(a, p, maps, st) : launch_pair<false>(a, p, maps, st);
+    return a->gated ? launch_gemm_act<true>(a, p, maps, st) : launch_gemm_act<false>(a, p, maps, st);
 }
 
 size_t fp8_act_bwd_workspace_size(int64_t M, int64_t N, int gated) {

@@ -99,23 +99,31 @@ __global__ void __launch_bounds__(kPlanThreads)
         __syncwarp();
     }
     __syncthreads();
-    // per expert: pairs in the CTAs before this one, and in all
+    // per expert: pairs in the CTAs before this one, and in all.  With few
+    // experts several threads share one's column of the histograms.
     for (int e = threadIdx.x; e < experts; e += kPlanThreads) {
         int own = 0;
 #pragma unroll
         for (int w = 0; w < kPlanWarps; ++w) own += cnt[w][e];
-        int before = 0, all = own;
-        if (hist) {
-            all = 0;
+        total[e] = hist ? 0 : own;
+        start[e] = 0;
+    }
+    if (hist) {
+        __syncthreads();
+        const int ctas = static_cast<int>(gridDim.x);
+        const int parts = experts < kPlanThreads ? kPlanThreads / experts : 1;
+        for (int i = threadIdx.x; i < experts * parts; i += kPlanThreads) {
+            const int e = i % experts, part = i / experts;
+            int before = 0, all = 0;
 #pragma unroll 8
-            for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
+            for (int b = part; b < ctas; b += parts) {
                 const int h = hist[static_cast<int64_t>(b) * experts + e];
                 all += h;
                 before += b < static_cast<int>(blockIdx.x) ? h : 0;
             }
+            atomicAdd(&total[e], all);      // integers: any order
+            atomicAdd(&start[e], before);
         }
-        total[e] = all;
-        start[e] = before;
     }
     __syncthreads();
     // offsets: the exclusive sum of the padded totals, four experts a thread
@@ -238,6 +246,7 @@ __global__ void __launch_bounds__(kRowThreads)
 constexpr int kBulkSlots = 3;
 constexpr int kBulkSlotBytes = 16384;        // at most; longer rows go in pieces
 constexpr int kBulkSmem = 200 * 1024;
+constexpr int64_t kBulkLeast = 4 << 20;      // bytes of xs
 
 struct BulkRows {
     const uint8_t* x;
@@ -731,9 +740,10 @@ int fp8_moe_permute(const void* x, const float* scale, int64_t tokens, int slots
         return set_error(FP8_ERR_ALIGN,
                          "fp8_moe_permute: x and xs must be 16-byte aligned, the rest 4-byte");
     if (!rows) return FP8_OK;
-    // rows of 1 KB and more in bulk copies; shorter ones through registers, in
-    // the widest unit that the row's length lets every row start on
-    if (row_bytes % 16 == 0 && row_bytes >= 1024) {
+    // rows of 1 KB and more in bulk copies, where there are enough of them to
+    // fill their pipelines; others through registers, in the widest unit that
+    // the row's length lets every row start on
+    if (row_bytes % 16 == 0 && row_bytes >= 1024 && rows * row_bytes >= kBulkLeast) {
         const int r = launch_permute_bulk(x, scale, tokens, slots, row_bytes, row_of, src, rows, xs,
                                           scale_s, as_stream(stream));
         if (r != FP8_OK) return r;

@@ -526,15 +526,15 @@ __global__ void __launch_bounds__(THREADS)
         if (!p.q) continue;
         float s = 1.0f;
         if (p.q_rows || p.amax) {
-            uint32_t top = 0;
+            float m = 0.0f;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 if (!live[i]) continue;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    top = max(top, max(row::abs_bits(row::lo2(v[i][e])), row::abs_bits(row::hi2(v[i][e]))));
+                    m = row::max_abs(row::max_abs(m, row::lo2(v[i][e])), row::hi2(v[i][e]));
             }
-            top = row_max<WARP>(top, part_max, turn_max);
+            const uint32_t top = row_max<WARP>(row::abs_bits(m), part_max, turn_max);
             if (p.q_rows) {
                 s = row_scale(top, p.q_fmt, p.pow2);
                 if (at == 0) p.q_scale_inv[r] = __fdiv_rn(1.0f, s);

@@ -149,6 +149,13 @@ __device__ __forceinline__ uint2 cvt8(int fmt, const float (&v)[8], float s) {
 // |v| as an unsigned integer that orders like the magnitude, NaN above all.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
+// max(top, |v|), NaN if either is: abs_bits() of the result orders above all.
+__device__ __forceinline__ float max_abs(float top, float v) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(top), "f"(fabsf(v)));
+    return m;
+}
+
 // Raise *amax (fp32, non-negative) to the magnitude with these bits.  Most
 // callers find it already higher and save the atomic.
 __device__ __forceinline__ void raise_amax(float* amax, uint32_t bits) {
