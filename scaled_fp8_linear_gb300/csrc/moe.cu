@@ -52,12 +52,16 @@ __global__ void __launch_bounds__(kPlanThreads)
     __syncthreads();
     ptx::griddep_wait();
     const int64_t first = static_cast<int64_t>(blockIdx.x) * chunk;
-    for (int i = threadIdx.x; i < chunk; i += kPlanThreads) {
-        const int64_t at = first + i;
-        if (at < n) {
-            const int e = ids[at];
-            if (e >= 0 && e < experts) atomicAdd(&h[e], 1);   // integers: any order
+    for (int i = threadIdx.x; i < chunk; i += 4 * kPlanThreads) {
+        int e[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {   // chunk is a multiple of kPlanThreads
+            const int64_t at = first + i + k * kPlanThreads;
+            e[k] = i + k * kPlanThreads < chunk && at < n ? ids[at] : -1;
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (e[k] >= 0 && e[k] < experts) atomicAdd(&h[e[k]], 1);   // integers: any order
     }
     __syncthreads();
     for (int e = threadIdx.x; e < experts; e += kPlanThreads)
@@ -90,39 +94,51 @@ __global__ void __launch_bounds__(kPlanThreads)
     const int64_t end = first + per_warp < cta_end ? first + per_warp : cta_end;
     const uint32_t below = (1u << lane) - 1u;
 
-    for (int64_t i = first; i < end; i += 32) {
-        const int64_t at = i + lane;
-        int e = at < end ? ids[at] : -1;
-        if (e >= experts) e = -1;
-        const uint32_t same = __match_any_sync(row::kAll, e);
-        if (e >= 0 && (same & below) == 0) cnt[warp][e] += __popc(same);
-        __syncwarp();
+    constexpr int kAhead = 8;   // looks of 32 pairs loaded together
+    int e[kAhead];
+    auto load = [&](int64_t i) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t at = i + 32 * k + lane;
+            e[k] = at < end ? ids[at] : -1;
+            if (e[k] >= experts) e[k] = -1;
+        }
+    };
+    for (int64_t i = first; i < end; i += 32 * kAhead) {
+        load(i);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (i + 32 * k >= end) break;
+            const uint32_t same = __match_any_sync(row::kAll, e[k]);
+            if (e[k] >= 0 && (same & below) == 0) cnt[warp][e[k]] += __popc(same);
+            __syncwarp();
+        }
     }
     __syncthreads();
     // per expert: pairs in the CTAs before this one, and in all.  With few
     // experts several threads share one's column of the histograms.
-    for (int e = threadIdx.x; e < experts; e += kPlanThreads) {
+    for (int x = threadIdx.x; x < experts; x += kPlanThreads) {
         int own = 0;
 #pragma unroll
-        for (int w = 0; w < kPlanWarps; ++w) own += cnt[w][e];
-        total[e] = hist ? 0 : own;
-        start[e] = 0;
+        for (int w = 0; w < kPlanWarps; ++w) own += cnt[w][x];
+        total[x] = hist ? 0 : own;
+        start[x] = 0;
     }
     if (hist) {
         __syncthreads();
         const int ctas = static_cast<int>(gridDim.x);
         const int parts = experts < kPlanThreads ? kPlanThreads / experts : 1;
         for (int i = threadIdx.x; i < experts * parts; i += kPlanThreads) {
-            const int e = i % experts, part = i / experts;
+            const int x = i % experts, part = i / experts;
             int before = 0, all = 0;
 #pragma unroll 8
             for (int b = part; b < ctas; b += parts) {
-                const int h = hist[static_cast<int64_t>(b) * experts + e];
+                const int h = hist[static_cast<int64_t>(b) * experts + x];
                 all += h;
                 before += b < static_cast<int>(blockIdx.x) ? h : 0;
             }
-            atomicAdd(&total[e], all);      // integers: any order
-            atomicAdd(&start[e], before);
+            atomicAdd(&total[x], all);      // integers: any order
+            atomicAdd(&start[x], before);
         }
     }
     __syncthreads();
@@ -131,8 +147,8 @@ __global__ void __launch_bounds__(kPlanThreads)
     int pad[kPer], sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int e = static_cast<int>(threadIdx.x) * kPer + i;
-        pad[i] = e < experts ? (total[e] + align - 1) / align * align : 0;
+        const int x = static_cast<int>(threadIdx.x) * kPer + i;
+        pad[i] = x < experts ? (total[x] + align - 1) / align * align : 0;
         sum += pad[i];
     }
     int incl = sum;
@@ -147,24 +163,24 @@ __global__ void __launch_bounds__(kPlanThreads)
     for (int w = 0; w < warp; ++w) run += warp_tot[w];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int e = static_cast<int>(threadIdx.x) * kPer + i;
-        if (e < experts) {
+        const int x = static_cast<int>(threadIdx.x) * kPer + i;
+        if (x < experts) {
             if (blockIdx.x == 0) {
-                offsets[e] = run;
-                counts[e] = total[e];
+                offsets[x] = run;
+                counts[x] = total[x];
             }
             // pad rows of the experts that this CTA is dealt
-            if (e % static_cast<int>(gridDim.x) == static_cast<int>(blockIdx.x))
-                for (int r = run + total[e]; r < run + pad[i]; ++r) src[r] = -1;
-            int next = run + start[e];
+            if (x % static_cast<int>(gridDim.x) == static_cast<int>(blockIdx.x))
+                for (int r = run + total[x]; r < run + pad[i]; ++r) src[r] = -1;
+            int next = run + start[x];
             for (int w = 0; w < kPlanWarps; ++w) {
-                const int c = cnt[w][e];
-                cnt[w][e] = next;
+                const int c = cnt[w][x];
+                cnt[w][x] = next;
                 next += c;
             }
         }
         run += pad[i];
-        if (e == experts - 1) {
+        if (x == experts - 1) {
             start[experts] = run;
             if (blockIdx.x == 0) offsets[experts] = run;
         }
@@ -173,19 +189,22 @@ __global__ void __launch_bounds__(kPlanThreads)
     for (int64_t r = start[experts] + static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x;
          r < rows; r += static_cast<int64_t>(gridDim.x) * kPlanThreads)
         src[r] = -1;
-    for (int64_t i = first; i < end; i += 32) {
-        const int64_t at = i + lane;
-        int e = at < end ? ids[at] : -1;
-        if (e >= experts) e = -1;
-        const uint32_t same = __match_any_sync(row::kAll, e);
-        int r = -1;
-        if (e >= 0) r = cnt[warp][e] + __popc(same & below);
-        __syncwarp();
-        if (e >= 0 && (same & below) == 0) cnt[warp][e] += __popc(same);
-        __syncwarp();
-        if (at < end) {
-            row_of[at] = r;
-            if (r >= 0) src[r] = static_cast<int32_t>(at);
+    for (int64_t i = first; i < end; i += 32 * kAhead) {
+        if (end - first > 32 * kAhead) load(i);   // else still there from the count
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t at = i + 32 * k + lane;
+            if (i + 32 * k >= end) break;
+            const uint32_t same = __match_any_sync(row::kAll, e[k]);
+            int r = -1;
+            if (e[k] >= 0) r = cnt[warp][e[k]] + __popc(same & below);
+            __syncwarp();
+            if (e[k] >= 0 && (same & below) == 0) cnt[warp][e[k]] += __popc(same);
+            __syncwarp();
+            if (at < end) {
+                row_of[at] = r;
+                if (r >= 0) src[r] = static_cast<int32_t>(at);
+            }
         }
     }
 }
@@ -238,6 +257,80 @@ __global__ void __launch_bounds__(kRowThreads)
     }
 }
 
+// The same for rows that do not start on 16 bytes: a CTA brings a token's row
+// into shared memory, each byte at its place modulo 16, and writes every copy
+// in aligned 16-byte pieces put together from two neighbouring words at a
+// time; single bytes only at a copy's two ends.
+constexpr int kImageBytes = 32768;   // of a row at a time
+
+__global__ void __launch_bounds__(kRowThreads)
+    moe_permute_bytes_kernel(const uint8_t* __restrict__ x, const float* __restrict__ scale,
+                             int64_t tokens, int slots, int64_t row_bytes,
+                             const int32_t* __restrict__ row_of, const int32_t* __restrict__ src,
+                             int64_t rows, uint8_t* __restrict__ xs, float* __restrict__ scale_s) {
+    ptx::griddep_launch_dependents();
+    __shared__ __align__(16) uint8_t image[kImageBytes + 64];
+    __shared__ int to[kMaxSlots];
+    ptx::griddep_wait();
+    const int tid = threadIdx.x;
+    // bytes [0, n) of a row go to `out` from image + at (null: zeros)
+    auto write = [&](uint8_t* out, int n, int at, bool zeros) {
+        const int head = min(n, static_cast<int>(-reinterpret_cast<uintptr_t>(out) & 15));
+        const int body = (n - head) / 16;
+        for (int i = tid; i < body; i += kRowThreads) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (!zeros) {
+                const int b = at + head + 16 * i;
+                const uint32_t* q = reinterpret_cast<const uint32_t*>(image + (b & ~3));
+                const int s = 8 * (b & 3);
+                const uint32_t w0 = q[0], w1 = q[1], w2 = q[2], w3 = q[3], w4 = q[4];
+                v = make_uint4(__funnelshift_r(w0, w1, s), __funnelshift_r(w1, w2, s),
+                               __funnelshift_r(w2, w3, s), __funnelshift_r(w3, w4, s));
+            }
+            *reinterpret_cast<uint4*>(out + head + 16 * i) = v;
+        }
+        const int tail = n - head - 16 * body;
+        if (tid < head) out[tid] = zeros ? uint8_t{0} : image[at + tid];
+        else if (tid >= 32 && tid - 32 < tail) {
+            const int i = head + 16 * body + tid - 32;
+            out[i] = zeros ? uint8_t{0} : image[at + i];
+        }
+    };
+    if (blockIdx.x < tokens) {
+        const int64_t t = blockIdx.x;
+        if (tid < slots) {
+            const int r = row_of[t * slots + tid];
+            to[tid] = r >= 0 && r < rows ? r : -1;
+            if (scale && to[tid] >= 0) scale_s[to[tid]] = scale[t];
+        }
+        for (int64_t first = 0; first < row_bytes; first += kImageBytes) {
+            const int n = static_cast<int>(row_bytes - first < kImageBytes ? row_bytes - first : kImageBytes);
+            const uint8_t* in = x + t * row_bytes + first;
+            const int at = static_cast<int>(reinterpret_cast<uintptr_t>(in) & 15);
+            const int head = min(n, (16 - at) & 15), body = (n - head) / 16;
+            __syncthreads();   // the image before this one has been read
+            for (int i = tid; i < body; i += kRowThreads)
+                *reinterpret_cast<uint4*>(image + at + head + 16 * i) = row::ld_stream(in + head + 16 * i);
+            const int tail = n - head - 16 * body;
+            if (tid < head) image[at + tid] = in[tid];
+            else if (tid >= 32 && tid - 32 < tail)
+                image[at + head + 16 * body + tid - 32] = in[head + 16 * body + tid - 32];
+            __syncthreads();
+            for (int j = 0; j < slots; ++j)
+                if (to[j] >= 0) write(xs + static_cast<int64_t>(to[j]) * row_bytes + first, n, at, false);
+        }
+    } else {
+        for (int64_t r = blockIdx.x - tokens; r < rows; r += gridDim.x - tokens) {
+            if (src[r] >= 0) continue;
+            for (int64_t first = 0; first < row_bytes; first += kImageBytes)
+                write(xs + r * row_bytes + first,
+                      static_cast<int>(row_bytes - first < kImageBytes ? row_bytes - first : kImageBytes),
+                      0, true);
+            if (scale && tid == 0) scale_s[r] = 0.0f;
+        }
+    }
+}
+
 // The same for rows of at least 1 KB in 16-byte units, by bulk copies alone:
 // a warp takes a token's row (or a piece of a long one) into a slot of shared
 // memory and each lane sends it to one of the slots' rows; no register or
@@ -246,7 +339,6 @@ __global__ void __launch_bounds__(kRowThreads)
 constexpr int kBulkSlots = 3;
 constexpr int kBulkSlotBytes = 16384;        // at most; longer rows go in pieces
 constexpr int kBulkSmem = 200 * 1024;
-constexpr int64_t kBulkLeast = 4 << 20;      // bytes of xs
 
 struct BulkRows {
     const uint8_t* x;
@@ -360,6 +452,8 @@ template <typename T, int N>
 struct Piece;
 template <>
 struct Piece<__nv_bfloat16, 8> {
+    using Raw = uint4;
+    static __device__ __forceinline__ Raw raw(const __nv_bfloat16* p) { return row::ld_stream(p); }
     static __device__ __forceinline__ void open(float (&v)[8], const uint4& w) { row::unpack8(v, w); }
     static __device__ __forceinline__ void load(float (&v)[8], const __nv_bfloat16* p) {
         row::unpack8(v, row::ld_stream(p));
@@ -370,6 +464,8 @@ struct Piece<__nv_bfloat16, 8> {
 };
 template <>
 struct Piece<float, 4> {
+    using Raw = uint4;
+    static __device__ __forceinline__ Raw raw(const float* p) { return row::ld_stream(p); }
     static __device__ __forceinline__ void open(float (&v)[4], const uint4& w) {
         v[0] = __uint_as_float(w.x); v[1] = __uint_as_float(w.y);
         v[2] = __uint_as_float(w.z); v[3] = __uint_as_float(w.w);
@@ -383,6 +479,11 @@ struct Piece<float, 4> {
 };
 template <>
 struct Piece<__nv_bfloat16, 1> {
+    using Raw = uint16_t;
+    static __device__ __forceinline__ Raw raw(const __nv_bfloat16* p) {
+        return __ldg(reinterpret_cast<const uint16_t*>(p));
+    }
+    static __device__ __forceinline__ void open(float (&v)[1], Raw w) { v[0] = row::bf_lo(w); }
     static __device__ __forceinline__ void load(float (&v)[1], const __nv_bfloat16* p) {
         v[0] = __bfloat162float(*p);
     }
@@ -392,41 +493,53 @@ struct Piece<__nv_bfloat16, 1> {
 };
 template <>
 struct Piece<float, 1> {
+    using Raw = float;
+    static __device__ __forceinline__ Raw raw(const float* p) { return __ldg(p); }
+    static __device__ __forceinline__ void open(float (&v)[1], Raw w) { v[0] = w; }
     static __device__ __forceinline__ void load(float (&v)[1], const float* p) { v[0] = *p; }
     static __device__ __forceinline__ void store(float* p, const float (&v)[1]) { *p = v[0]; }
 };
 
 // y[t] = sum_j w[t, j] ys[row_of[t, j]] (w null: 1), fp32 in the order of j,
-// rounded once.
+// rounded once.  A CTA takes 256 / lanes tokens; their rows and weights first,
+// in shared memory (a dropped slot as -1), then the pieces of eight slots at
+// a time, so that a thread has eight loads in flight.
 template <typename T, int N>
 __global__ void __launch_bounds__(kRowThreads)
     moe_unpermute_kernel(const T* __restrict__ ys, const int32_t* __restrict__ row_of,
                          const float* __restrict__ w, int64_t tokens, int slots, int64_t width,
                          int64_t rows, T* __restrict__ y, int lanes) {
     ptx::griddep_launch_dependents();
+    __shared__ int from[kRowThreads / 8 * kMaxSlots];
+    __shared__ float wt[kRowThreads / 8 * kMaxSlots];
     ptx::griddep_wait();
     const int sub = threadIdx.x / lanes, lane = threadIdx.x % lanes, per = kRowThreads / lanes;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * per + sub;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * per, t = t0 + sub;
+    for (int i = threadIdx.x; i < per * slots && t0 * slots + i < tokens * slots; i += kRowThreads) {
+        const int r = row_of[t0 * slots + i];
+        from[i] = r >= 0 && r < rows ? r : -1;
+        wt[i] = w ? w[t0 * slots + i] : 1.0f;
+    }
+    __syncthreads();
     if (t >= tokens) return;
-    const int32_t* from = row_of + t * slots;
     for (int64_t c = static_cast<int64_t>(lane) * N; c < width; c += static_cast<int64_t>(lanes) * N) {
         float acc[N] = {};
-        for (int j = 0; j < slots; j += 4) {   // four rows' loads in flight, added in order
-            float v[4][N], f[4];
-            bool here[4];
+        for (int j = 0; j < slots; j += 8) {
+            typename Piece<T, N>::Raw v[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t r = j + i < slots ? from[j + i] : -1;
-                here[i] = r >= 0 && r < rows;
-                if (!here[i]) continue;
-                f[i] = w ? w[t * slots + j + i] : 1.0f;
-                Piece<T, N>::load(v[i], ys + r * width + c);
+            for (int i = 0; i < 8; ++i) {
+                const int r = j + i < slots ? from[sub * slots + j + i] : -1;
+                v[i] = r >= 0 ? Piece<T, N>::raw(ys + static_cast<int64_t>(r) * width + c)
+                              : typename Piece<T, N>::Raw{};
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (!here[i]) continue;
+            for (int i = 0; i < 8; ++i) {
+                if (j + i >= slots || from[sub * slots + j + i] < 0) continue;
+                float x[N];
+                Piece<T, N>::open(x, v[i]);
+                const float f = wt[sub * slots + j + i];
 #pragma unroll
-                for (int e = 0; e < N; ++e) acc[e] = fmaf(f[i], v[i][e], acc[e]);
+                for (int e = 0; e < N; ++e) acc[e] = fmaf(f, x[e], acc[e]);
             }
         }
         Piece<T, N>::store(y + t * width + c, acc);
@@ -602,6 +715,16 @@ void launch_permute(const void* x, const float* scale, int64_t tokens, int slots
                row_of, src, rows, static_cast<V*>(xs), scale_s, lanes, token_ctas);
 }
 
+void launch_permute_bytes(const void* x, const float* scale, int64_t tokens, int slots,
+                          int64_t row_bytes, const int32_t* row_of, const int32_t* src, int64_t rows,
+                          void* xs, float* scale_s, cudaStream_t st) {
+    const int64_t want = (rows + 15) / 16;
+    const int64_t pad_ctas = want > 8 * num_sms() ? 8 * num_sms() : want;
+    launch_pdl(moe_permute_bytes_kernel, dim3(static_cast<unsigned>(tokens + pad_ctas)),
+               dim3(kRowThreads), 0, st, static_cast<const uint8_t*>(x), scale, tokens, slots,
+               row_bytes, row_of, src, rows, static_cast<uint8_t*>(xs), scale_s);
+}
+
 int launch_permute_bulk(const void* x, const float* scale, int64_t tokens, int slots,
                         int64_t row_bytes, const int32_t* row_of, const int32_t* src, int64_t rows,
                         void* xs, float* scale_s, cudaStream_t st) {
@@ -740,15 +863,17 @@ int fp8_moe_permute(const void* x, const float* scale, int64_t tokens, int slots
         return set_error(FP8_ERR_ALIGN,
                          "fp8_moe_permute: x and xs must be 16-byte aligned, the rest 4-byte");
     if (!rows) return FP8_OK;
-    // rows of 1 KB and more in bulk copies, where there are enough of them to
-    // fill their pipelines; others through registers, in the widest unit that
-    // the row's length lets every row start on
-    if (row_bytes % 16 == 0 && row_bytes >= 1024 && rows * row_bytes >= kBulkLeast) {
+    // Rows of whole 16-byte pieces: in bulk copies, short ones (where a copy's
+    // fixed cost shows) through registers.  Others: put together from shared
+    // memory, short ones in the widest unit that every row starts on.
+    if (row_bytes % 16 == 0 && row_bytes >= 1024) {
         const int r = launch_permute_bulk(x, scale, tokens, slots, row_bytes, row_of, src, rows, xs,
                                           scale_s, as_stream(stream));
         if (r != FP8_OK) return r;
     } else if (row_bytes % 16 == 0)
         launch_permute<uint4>(x, scale, tokens, slots, row_bytes, row_of, src, rows, xs, scale_s, as_stream(stream));
+    else if (row_bytes >= 512)
+        launch_permute_bytes(x, scale, tokens, slots, row_bytes, row_of, src, rows, xs, scale_s, as_stream(stream));
     else if (row_bytes % 4 == 0)
         launch_permute<uint32_t>(x, scale, tokens, slots, row_bytes, row_of, src, rows, xs, scale_s, as_stream(stream));
     else if (row_bytes % 2 == 0)
