@@ -19,7 +19,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import (_U8, _ptr, _stream, _vp, E4M3, Fp8Error, GRAN_ROW, GRAN_TENSOR, OUT_BF16, OUT_F32,
+from . import (_U8, _ptr, _raw_stream, _stream, _vp, E4M3, Fp8Error, GRAN_ROW, GRAN_TENSOR, OUT_BF16, OUT_F32,
                fp8_last_error)
 from . import lib as _base_lib
 
@@ -179,6 +179,13 @@ def _given(t, what, dtype, shape):
     return p
 
 
+def _on(stream, t):
+    """The stream's handle: the given one, or the current one of t's device."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return _stream(stream)
+
+
 def _rows(t, what):
     if t.dim() != 2:
         raise ValueError(f"{what} must be 2-D")
@@ -208,35 +215,53 @@ def fp8_norm_fwd(x, h=None, kind: int = NORM_RMS, eps: float = 1e-5, alpha: floa
     ref = x if x is not None else h
     if ref is None:
         raise ValueError("x and h are None")
-    T, C = _rows(ref, "x")
+    T, C = shape = _rows(ref, "x")
     dev = ref.device
     dt = x.dtype if x is not None else (x_out.dtype if x_out is not None else _BF16)
     if dt not in _OUT:
         raise TypeError(f"x: dtype {dt}, expected bfloat16 or float32")
-    if x_out is None and want_x_out:
+    p_xo = p_y = p_q = p_inv = p_amax = p_stats = 0
+    if x_out is not None:
+        p_xo = _given(x_out, "x_out", dt, shape)
+    elif want_x_out:
         x_out = torch.empty_like(x) if x is not None else torch.empty(T, C, dtype=dt, device=dev)
-    if y is None and want_y:
+        p_xo = x_out.data_ptr()
+    if y is not None:
+        p_y = _given(y, "y", _BF16, shape)
+    elif want_y:
         y = (torch.empty_like(h) if h is not None else torch.empty_like(x) if dt is _BF16 else
              torch.empty(T, C, dtype=_BF16, device=dev))
-    if q_fmt is not None and q is None:
-        q = torch.empty(T, C, dtype=torch.uint8, device=dev)
-    if q_fmt is not None and q_gran == GRAN_ROW and q_scale_inv is None:
-        q_scale_inv = torch.empty(T, dtype=_F32, device=dev)
+        p_y = y.data_ptr()
+    if q_fmt is not None or q is not None:
+        if q is None:
+            q = torch.empty(T, C, dtype=torch.uint8, device=dev)
+        p_q = _given(q, "q", _BYTE, shape)
+        if q_gran == GRAN_ROW and q_scale_inv is None:
+            q_scale_inv = torch.empty(T, dtype=_F32, device=dev)
+    if q_scale_inv is not None:
+        p_inv = _given(q_scale_inv, "q_scale_inv", _F32, (T,))
     if want_amax and amax is None:
         amax = torch.empty(1, dtype=_F32, device=dev)
-    if want_stats and stats is None:
+    if amax is not None:
+        p_amax = _given(amax, "amax", _F32, (1,))
+    if stats is not None:
+        p_stats = _given(stats, "stats", _F32, (4, T))
+    elif want_stats:
         stats = torch.empty(4, T, dtype=_F32, device=dev)
+        p_stats = stats.data_ptr()
     gate_rows = 0 if gate is None else _rows(gate, "gate")[0]
+    vec = (C,)
     a = _pack_norm_fwd(
-        T, C, kind, _OUT[dt], eps, alpha, _given(x, "x", dt, (T, C)), _given(h, "h", _BF16, (T, C)),
-        _given(gate, "gate", _BF16, (gate_rows, C)), gate_rows, int(bool(post_norm)),
-        _given(w_post, "w_post", _F32, (C,)), _given(b_post, "b_post", _F32, (C,)),
-        _given(w_pre, "w_pre", _F32, (C,)), _given(b_pre, "b_pre", _F32, (C,)),
-        _given(x_out, "x_out", dt, (T, C)), _given(y, "y", _BF16, (T, C)),
-        _given(q, "q", _BYTE, (T, C)), E4M3 if q_fmt is None else q_fmt, q_gran, int(bool(pow2)),
-        _given(q_scale, "q_scale", _F32, (1,)), _given(q_scale_inv, "q_scale_inv", _F32, (T,)),
-        _given(amax, "amax", _F32, (1,)), _given(stats, "stats", _F32, (4, T)))
-    _check(_lib().fp8_norm_fwd(a, _stream(stream)))
+        T, C, kind, _OUT[dt], eps, alpha, 0 if x is None else _given(x, "x", dt, shape),
+        0 if h is None else _given(h, "h", _BF16, shape),
+        0 if gate is None else _given(gate, "gate", _BF16, (gate_rows, C)), gate_rows,
+        1 if post_norm else 0, 0 if w_post is None else _given(w_post, "w_post", _F32, vec),
+        0 if b_post is None else _given(b_post, "b_post", _F32, vec),
+        0 if w_pre is None else _given(w_pre, "w_pre", _F32, vec),
+        0 if b_pre is None else _given(b_pre, "b_pre", _F32, vec), p_xo, p_y, p_q,
+        E4M3 if q_fmt is None else q_fmt, q_gran, 1 if pow2 else 0,
+        0 if q_scale is None else _given(q_scale, "q_scale", _F32, (1,)), p_inv, p_amax, p_stats)
+    _check(_lib().fp8_norm_fwd(a, _on(stream, ref)))
     return NormFwd(x_out, y, q, q_scale_inv, amax, stats)
 
 
@@ -290,7 +315,7 @@ def fp8_norm_bwd(dy, x_out, stats, dx_out=None, h=None, kind: int = NORM_RMS, al
         _given(dw_pre, "dw_pre", _F32, (C,)), _given(db_pre, "db_pre", _F32, (C,)),
         _given(dw_post, "dw_post", _F32, (C,)), _given(db_post, "db_post", _F32, (C,)),
         _given(dgate, "dgate", _F32, (gate_rows, C)), int(bool(accumulate)))
-    _check(_lib().fp8_norm_bwd(a, ws, ws_bytes, _stream(stream)))
+    _check(_lib().fp8_norm_bwd(a, ws, ws_bytes, _on(stream, ref)))
     return NormBwd(dx, dh, dw_pre, db_pre, dw_post, db_post, dgate)
 
 
@@ -323,25 +348,40 @@ def fp8_gemm_act(A, fa: int, B, fb: int, scale_inv_a, scale_inv_b, ga: int = GRA
         raise ValueError("a gated B has an even number of rows")
     N = rows // 2 if gated else rows
     dev = A.device
-    if d is None and want_d:
+    out = (M, N)
+    p_d = p_z = p_q = p_amax = 0
+    if d is not None:
+        p_d = _given(d, "d", _BF16, out)
+    elif want_d:
         d = torch.empty(M, N, dtype=_BF16, device=dev)
-    if z is None and want_z:
+        p_d = d.data_ptr()
+    if z is not None:
+        p_z = _given(z, "z", _BF16, (M, rows))
+    elif want_z:
         z = torch.empty(M, rows, dtype=_BF16, device=dev)
-    if q is None and q_fmt is not None:
+        p_z = z.data_ptr()
+    if q is not None:
+        p_q = _given(q, "q", _BYTE, out)
+    elif q_fmt is not None:
         q = torch.empty(M, N, dtype=torch.uint8, device=dev)
-    if amax is None and want_amax:
+        p_q = q.data_ptr()
+    if amax is not None:
+        p_amax = _given(amax, "amax", _F32, (1,))
+    elif want_amax:
         amax = torch.empty(1, dtype=_F32, device=dev)
-    per_b = (E,) if offsets is not None else (1,)
+        p_amax = amax.data_ptr()
+    per_b = (E,)
     per_row = (E, rows) if offsets is not None else (rows,)
     a = _pack_gemm_act(
         _given(A, "A", _BYTE, (M, K)), _given(B, "B", _BYTE, B.shape), fa, fb, M, N, K, ga, gb,
         _given(scale_inv_a, "scale_inv_a", _F32, (M,) if ga == GRAN_ROW else (1,)),
         _given(scale_inv_b, "scale_inv_b", _F32, per_row if gb == GRAN_ROW else per_b), act,
-        int(bool(gated)), _given(bias, "bias", _BF16, per_row), _given(residual, "residual", _BF16, (M, N)),
-        _given(z, "z", _BF16, (M, rows)), _given(d, "d", _BF16, (M, N)), _given(q, "q", _BYTE, (M, N)),
-        E4M3 if q_fmt is None else q_fmt, _given(q_scale, "q_scale", _F32, (1,)),
-        _given(amax, "amax", _F32, (1,)), _given(offsets, "offsets", _I32, (E + 1,)), E)
-    _check(_lib().fp8_gemm_act(a, _stream(stream)))
+        1 if gated else 0, 0 if bias is None else _given(bias, "bias", _BF16, per_row),
+        0 if residual is None else _given(residual, "residual", _BF16, out), p_z, p_d, p_q,
+        E4M3 if q_fmt is None else q_fmt,
+        0 if q_scale is None else _given(q_scale, "q_scale", _F32, (1,)), p_amax,
+        0 if offsets is None else _given(offsets, "offsets", _I32, (E + 1,)), E)
+    _check(_lib().fp8_gemm_act(a, _on(stream, A)))
     return GemmAct(d, z, q, amax)
 
 
@@ -377,7 +417,7 @@ def fp8_act_bwd(dD, z, act: int, gated: bool = False, want_dz: bool = True, q_fm
         _given(dz, "dz", _BF16, (M, rows)), _given(q, "q", _BYTE, (M, rows)),
         E4M3 if q_fmt is None else q_fmt, _given(q_scale, "q_scale", _F32, (1,)),
         _given(amax, "amax", _F32, (1,)), _given(dbias, "dbias", _F32, (rows,)), int(bool(accumulate)))
-    _check(_lib().fp8_act_bwd(a, ws, ws_bytes or 0, _stream(stream)))
+    _check(_lib().fp8_act_bwd(a, ws, ws_bytes or 0, _on(stream, dD)))
     return ActBwd(dz, q, amax, dbias)
 
 
@@ -408,20 +448,21 @@ def fp8_moe_plan(ids, experts: int, align: int = 1, rows: int | None = None, off
     if rows is None:
         rows = fp8_moe_rows(T, k, experts, align) if src is None else src.numel()
     if offsets is None:
-        offsets = torch.empty(experts + 1, dtype=_I32, device=dev)
+        offsets = ids.new_empty(experts + 1)
     if counts is None:
-        counts = torch.empty(experts, dtype=_I32, device=dev)
+        counts = ids.new_empty(experts)
     if row_of is None:
-        row_of = torch.empty(T, k, dtype=_I32, device=dev)
+        row_of = torch.empty_like(ids)
     if src is None:
-        src = torch.empty(rows, dtype=_I32, device=dev)
+        src = ids.new_empty(rows)
     ws, ws_bytes, need = None, 0, fp8_moe_workspace_size(T, k, experts)
     if need:
         ws, ws_bytes, workspace = _workspace(workspace, need, dev)
     _check(_lib().fp8_moe_plan(
-        _given(ids, "ids", _I32, (T, k)), T, k, experts, align, _given(offsets, "offsets", _I32, (experts + 1,)),
-        _given(counts, "counts", _I32, (experts,)), _given(row_of, "row_of", _I32, (T, k)),
-        _given(src, "src", _I32, (rows,)), rows, ws, ws_bytes, _stream(stream)))
+        _given(ids, "ids", _I32, (T, k)), T, k, experts, align,
+        _given(offsets, "offsets", _I32, (experts + 1,)), _given(counts, "counts", _I32, (experts,)),
+        _given(row_of, "row_of", _I32, (T, k)), _given(src, "src", _I32, (rows,)), rows, ws, ws_bytes,
+        _on(stream, ids)))
     return MoePlan(offsets, counts, row_of, src)
 
 
@@ -432,14 +473,14 @@ def fp8_moe_permute(x, row_of, src, scale=None, xs=None, scale_s=None, stream=No
     T, C = _rows(x, "x")
     k, rows = _rows(row_of, "row_of")[1], src.numel()
     if xs is None:
-        xs = torch.empty(rows, C, dtype=x.dtype, device=x.device)
+        xs = x.new_empty(rows, C)
     if scale is not None and scale_s is None:
         scale_s = torch.empty(rows, dtype=_F32, device=x.device)
     _check(_lib().fp8_moe_permute(
-        _given(x, "x", x.dtype, (T, C)), _given(scale, "scale", _F32, (T,)), T, k, C * x.element_size(),
-        _given(row_of, "row_of", _I32, (T, k)), _given(src, "src", _I32, (rows,)), rows,
-        _given(xs, "xs", x.dtype, (rows, C)), _given(scale_s, "scale_s", _F32, (rows,)),
-        _stream(stream)))
+        _given(x, "x", x.dtype, (T, C)), 0 if scale is None else _given(scale, "scale", _F32, (T,)), T, k,
+        C * x.element_size(), _given(row_of, "row_of", _I32, (T, k)), _given(src, "src", _I32, (rows,)),
+        rows, _given(xs, "xs", x.dtype, (rows, C)),
+        0 if scale_s is None else _given(scale_s, "scale_s", _F32, (rows,)), _on(stream, x)))
     return xs, scale_s
 
 
@@ -455,7 +496,7 @@ def fp8_moe_unpermute(ys, row_of, weights=None, y=None, stream=None) -> torch.Te
     _check(_lib().fp8_moe_unpermute(
         _given(ys, "ys", ys.dtype, (rows, C)), _OUT[ys.dtype], _given(row_of, "row_of", _I32, (T, k)),
         _given(weights, "weights", _F32, (T, k)), T, k, C, rows, _given(y, "y", ys.dtype, (T, C)),
-        _stream(stream)))
+        _on(stream, ys)))
     return y
 
 
@@ -475,5 +516,5 @@ def fp8_moe_unpermute_bwd(dy, ys, row_of, src, weights=None, dys=None, dweights=
         _given(row_of, "row_of", _I32, (T, k)), _given(src, "src", _I32, (rows,)),
         _given(weights, "weights", _F32, (T, k)), T, k, C, rows,
         _given(dys, "dys", ys.dtype, (rows, C)), _given(dweights, "dweights", _F32, (T, k)),
-        _stream(stream)))
+        _on(stream, ys)))
     return dys, dweights

@@ -334,9 +334,10 @@ __global__ void __launch_bounds__(kRowThreads)
 // The same for rows of at least 1 KB in 16-byte units, by bulk copies alone:
 // a warp takes a token's row (or a piece of a long one) into a slot of shared
 // memory and each lane sends it to one of the slots' rows; no register or
-// load unit touches the data.  Three slots a warp: one being filled, one
-// being sent, one whose copies are being waited for.
-constexpr int kBulkSlots = 3;
+// load unit touches the data.  Two slots a warp: one filled while the other
+// is sent (8192 tokens to 8 of 64 experts, rows of 8 KB: 117 us with two, 122
+// with three or four, for 106 us of copies in either).
+constexpr int kBulkSlots = 2;
 constexpr int kBulkSlotBytes = 16384;        // at most; longer rows go in pieces
 constexpr int kBulkSmem = 200 * 1024;
 
@@ -427,11 +428,13 @@ __global__ void __launch_bounds__(256)
             ++issued;
         }
     }
-    if (ok) {   // pad rows, 32 at a look
-        const int64_t blocks = (p.rows + 31) / 32;
-        for (int64_t b = first; b < blocks; b += step) {
-            const int64_t r = b * 32 + lane;
-            if (r < p.rows && p.src[r] < 0) {
+    if (ok) {
+        // pad rows, up to 32 at a look: with few rows they spread over the warps
+        const int64_t share = (p.rows + step - 1) / step;
+        const int look = static_cast<int>(share < 32 ? share : 32);
+        for (int64_t r0 = first * look; r0 < p.rows; r0 += step * look) {
+            const int64_t r = r0 + lane;
+            if (lane < look && r < p.rows && p.src[r] < 0) {
                 for (int64_t piece = 0; piece < p.pieces; ++piece)
                     ptx::bulk_store(p.xs + r * p.row_bytes + piece * p.slot_bytes, zeros, bytes_of(piece));
                 if (p.scale) p.scale_s[r] = 0.0f;
@@ -750,7 +753,7 @@ int launch_permute_bulk(const void* x, const float* scale, int64_t tokens, int s
     // small rows leave room for more CTAs on an SM
     int per_sm = kBulkSmem / smem;
     if (per_sm > 8) per_sm = 8;
-    const int64_t work = tokens * p.pieces + (rows + 31) / 32;
+    const int64_t work = tokens * p.pieces + rows / 8 + 1;
     const int64_t most = static_cast<int64_t>(num_sms()) * per_sm;
     launch_pdl(moe_permute_bulk_kernel, dim3(static_cast<unsigned>(work < most ? work : most)),
                dim3(warps * 32), smem, st, p);
