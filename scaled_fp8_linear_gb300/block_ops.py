@@ -192,10 +192,17 @@ def _rows(t, what):
     return t.shape
 
 
-def _workspace(workspace, need, device):
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    return _ptr(workspace, "workspace", torch.uint8), workspace.numel(), workspace
+def _workspace(workspace, need, device, stream):
+    """(address, bytes, tensor) of the given workspace or of a new one.  A new
+    one is freed when the call returns: on a stream of the caller's own it is
+    kept from torch's allocator until that stream is past the call."""
+    if workspace is not None:
+        return _given(workspace, "workspace", _BYTE, workspace.shape), workspace.numel(), workspace
+    workspace = torch.empty(need if need > 16 else 16, dtype=_BYTE, device=device)
+    if stream is not None:
+        workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                                else torch.cuda.ExternalStream(int(stream), device=device))
+    return workspace.data_ptr(), workspace.numel(), workspace
 
 
 # ------------------------------------------------------------------ norms
@@ -279,42 +286,56 @@ def fp8_norm_bwd(dy, x_out, stats, dx_out=None, h=None, kind: int = NORM_RMS, al
     stats are the forward's.  dx and dh come where their inputs were; the
     vectors' gradients (fp32) where the vectors were given, added to the given
     outputs with accumulate.  dx may be dx_out."""
-    ref = next((t for t in (x_out, dx_out, dy) if t is not None), None)
+    ref = x_out if x_out is not None else dx_out if dx_out is not None else dy
     if ref is None:
         raise ValueError("dy and dx_out are None")
-    T, C = _rows(ref, "x_out")
+    T, C = shape = _rows(ref, "x_out")
     dev = ref.device
     dt = x_out.dtype if x_out is not None else dx_out.dtype if dx_out is not None else _BF16
     if dt not in _OUT:
         raise TypeError(f"x_out: dtype {dt}, expected bfloat16 or float32")
-    if accumulate and any(v is not None and o is None for v, o in (
-            (w_pre, dw_pre), (b_pre, db_pre), (w_post, dw_post), (b_post, db_post), (gate, dgate))):
+    want = [dw_pre is None and w_pre is not None and dy is not None,
+            db_pre is None and b_pre is not None and dy is not None,
+            dw_post is None and w_post is not None, db_post is None and b_post is not None]
+    if accumulate and (any(want) or (dgate is None and gate is not None)):
         raise ValueError("accumulate adds to given outputs")
-
-    def vec(out, of, shape):
-        return torch.empty(shape, dtype=_F32, device=dev) if out is None and of is not None else out
-
+    vec = (C,)
     if dx is None:
-        dx = torch.empty(T, C, dtype=dt, device=dev)
+        dx = torch.empty_like(ref) if ref.dtype is dt else torch.empty(T, C, dtype=dt, device=dev)
     if dh is None and h is not None:
-        dh = torch.empty(T, C, dtype=_BF16, device=dev)
+        dh = torch.empty_like(h)
     gate_rows = 0 if gate is None else _rows(gate, "gate")[0]
-    if dy is not None:
-        dw_pre, db_pre = vec(dw_pre, w_pre, (C,)), vec(db_pre, b_pre, (C,))
-    dw_post, db_post = vec(dw_post, w_post, (C,)), vec(db_post, b_post, (C,))
-    dgate = vec(dgate, gate, (gate_rows, C))
-    need = fp8_norm_bwd_workspace_size(T, C, gate_rows)
-    ws, ws_bytes, workspace = _workspace(workspace, need, dev)
+    n = sum(want)
+    if n:   # the vectors' gradients in one allocation, each row 16-byte aligned
+        step = (C + 3) // 4 * 4
+        rows = torch.empty(n, step, dtype=_F32, device=dev).unbind(0)
+        if step != C:
+            rows = [r[:C] for r in rows]
+        rows = iter(rows)
+        dw_pre = next(rows) if want[0] else dw_pre
+        db_pre = next(rows) if want[1] else db_pre
+        dw_post = next(rows) if want[2] else dw_post
+        db_post = next(rows) if want[3] else db_post
+    if dgate is None and gate is not None:
+        dgate = torch.empty(gate_rows, C, dtype=_F32, device=dev)
+    ws, ws_bytes, workspace = _workspace(workspace, fp8_norm_bwd_workspace_size(T, C, gate_rows), dev,
+                                         stream)
     a = _pack_norm_bwd(
-        T, C, kind, _OUT[dt], alpha, _given(dy, "dy", _BF16, (T, C)),
-        _given(x_out, "x_out", dt, (T, C)), _given(dx_out, "dx_out", dt, (T, C)),
-        _given(h, "h", _BF16, (T, C)), _given(gate, "gate", _BF16, (gate_rows, C)), gate_rows,
-        int(bool(post_norm)), _given(w_post, "w_post", _F32, (C,)), _given(b_post, "b_post", _F32, (C,)),
-        _given(w_pre, "w_pre", _F32, (C,)), _given(stats, "stats", _F32, (4, T)),
-        _given(dx, "dx", dt, (T, C)), _given(dh, "dh", _BF16, (T, C)),
-        _given(dw_pre, "dw_pre", _F32, (C,)), _given(db_pre, "db_pre", _F32, (C,)),
-        _given(dw_post, "dw_post", _F32, (C,)), _given(db_post, "db_post", _F32, (C,)),
-        _given(dgate, "dgate", _F32, (gate_rows, C)), int(bool(accumulate)))
+        T, C, kind, _OUT[dt], alpha, 0 if dy is None else _given(dy, "dy", _BF16, shape),
+        0 if x_out is None else _given(x_out, "x_out", dt, shape),
+        0 if dx_out is None else _given(dx_out, "dx_out", dt, shape),
+        0 if h is None else _given(h, "h", _BF16, shape),
+        0 if gate is None else _given(gate, "gate", _BF16, (gate_rows, C)), gate_rows,
+        1 if post_norm else 0, 0 if w_post is None else _given(w_post, "w_post", _F32, vec),
+        0 if b_post is None else _given(b_post, "b_post", _F32, vec),
+        0 if w_pre is None else _given(w_pre, "w_pre", _F32, vec),
+        0 if stats is None else _given(stats, "stats", _F32, (4, T)), _given(dx, "dx", dt, shape),
+        0 if dh is None else _given(dh, "dh", _BF16, shape),
+        0 if dw_pre is None else _given(dw_pre, "dw_pre", _F32, vec),
+        0 if db_pre is None else _given(db_pre, "db_pre", _F32, vec),
+        0 if dw_post is None else _given(dw_post, "dw_post", _F32, vec),
+        0 if db_post is None else _given(db_post, "db_post", _F32, vec),
+        0 if dgate is None else _given(dgate, "dgate", _F32, (gate_rows, C)), 1 if accumulate else 0)
     _check(_lib().fp8_norm_bwd(a, ws, ws_bytes, _on(stream, ref)))
     return NormBwd(dx, dh, dw_pre, db_pre, dw_post, db_post, dgate)
 
@@ -385,6 +406,7 @@ def fp8_gemm_act(A, fa: int, B, fb: int, scale_inv_a, scale_inv_b, ga: int = GRA
     return GemmAct(d, z, q, amax)
 
 
+@functools.lru_cache(maxsize=256)
 def fp8_act_bwd_workspace_size(M: int, N: int, gated: bool) -> int:
     return int(_lib().fp8_act_bwd_workspace_size(M, N, int(bool(gated))))
 
@@ -401,23 +423,36 @@ def fp8_act_bwd(dD, z, act: int, gated: bool = False, want_dz: bool = True, q_fm
     dev = dD.device
     if accumulate and dbias is None:
         raise ValueError("accumulate adds to a given dbias")
-    if dz is None and want_dz:
+    out = (M, rows)
+    p_dz = p_q = p_amax = p_db = 0
+    if dz is not None:
+        p_dz = _given(dz, "dz", _BF16, out)
+    elif want_dz:
         dz = torch.empty(M, rows, dtype=_BF16, device=dev)
-    if q is None and q_fmt is not None:
-        q = torch.empty(M, rows, dtype=torch.uint8, device=dev)
-    if amax is None and want_amax:
+        p_dz = dz.data_ptr()
+    if q is not None:
+        p_q = _given(q, "q", _BYTE, out)
+    elif q_fmt is not None:
+        q = torch.empty(M, rows, dtype=_BYTE, device=dev)
+        p_q = q.data_ptr()
+    if amax is not None:
+        p_amax = _given(amax, "amax", _F32, (1,))
+    elif want_amax:
         amax = torch.empty(1, dtype=_F32, device=dev)
+        p_amax = amax.data_ptr()
     if dbias is None and want_dbias:
         dbias = torch.empty(rows, dtype=_F32, device=dev)
-    ws = ws_bytes = None
+    ws, ws_bytes = None, 0
     if dbias is not None:
-        ws, ws_bytes, workspace = _workspace(workspace, fp8_act_bwd_workspace_size(M, N, gated), dev)
+        p_db = _given(dbias, "dbias", _F32, (rows,))
+        ws, ws_bytes, workspace = _workspace(workspace, fp8_act_bwd_workspace_size(M, N, gated), dev,
+                                             stream)
     a = _pack_act_bwd(
-        M, N, act, int(bool(gated)), _given(dD, "dD", _BF16, (M, N)), _given(z, "z", _BF16, (M, rows)),
-        _given(dz, "dz", _BF16, (M, rows)), _given(q, "q", _BYTE, (M, rows)),
-        E4M3 if q_fmt is None else q_fmt, _given(q_scale, "q_scale", _F32, (1,)),
-        _given(amax, "amax", _F32, (1,)), _given(dbias, "dbias", _F32, (rows,)), int(bool(accumulate)))
-    _check(_lib().fp8_act_bwd(a, ws, ws_bytes or 0, _on(stream, dD)))
+        M, N, act, 1 if gated else 0, _given(dD, "dD", _BF16, (M, N)), _given(z, "z", _BF16, out),
+        p_dz, p_q, E4M3 if q_fmt is None else q_fmt,
+        0 if q_scale is None else _given(q_scale, "q_scale", _F32, (1,)), p_amax, p_db,
+        1 if accumulate else 0)
+    _check(_lib().fp8_act_bwd(a, ws, ws_bytes, _on(stream, dD)))
     return ActBwd(dz, q, amax, dbias)
 
 
@@ -448,16 +483,16 @@ def fp8_moe_plan(ids, experts: int, align: int = 1, rows: int | None = None, off
     if rows is None:
         rows = fp8_moe_rows(T, k, experts, align) if src is None else src.numel()
     if offsets is None:
-        offsets = ids.new_empty(experts + 1)
+        offsets = torch.empty(experts + 1, dtype=_I32, device=dev)
     if counts is None:
-        counts = ids.new_empty(experts)
+        counts = torch.empty(experts, dtype=_I32, device=dev)
     if row_of is None:
         row_of = torch.empty_like(ids)
     if src is None:
-        src = ids.new_empty(rows)
+        src = torch.empty(rows, dtype=_I32, device=dev)
     ws, ws_bytes, need = None, 0, fp8_moe_workspace_size(T, k, experts)
     if need:
-        ws, ws_bytes, workspace = _workspace(workspace, need, dev)
+        ws, ws_bytes, workspace = _workspace(workspace, need, dev, stream)
     _check(_lib().fp8_moe_plan(
         _given(ids, "ids", _I32, (T, k)), T, k, experts, align,
         _given(offsets, "offsets", _I32, (experts + 1,)), _given(counts, "counts", _I32, (experts,)),
@@ -473,7 +508,7 @@ def fp8_moe_permute(x, row_of, src, scale=None, xs=None, scale_s=None, stream=No
     T, C = _rows(x, "x")
     k, rows = _rows(row_of, "row_of")[1], src.numel()
     if xs is None:
-        xs = x.new_empty(rows, C)
+        xs = torch.empty(rows, C, dtype=x.dtype, device=x.device)
     if scale is not None and scale_s is None:
         scale_s = torch.empty(rows, dtype=_F32, device=x.device)
     _check(_lib().fp8_moe_permute(
