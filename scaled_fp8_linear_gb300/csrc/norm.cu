@@ -1288,43 +1288,73 @@ __global__ void __launch_bounds__(THREADS)
     }
 }
 
-// Sums of partial rows: job j < 4 adds dw_part[j][0 .. ctas), job 4 + g the
-// `parts` rows of group g.  A CTA takes 32 columns: 32 slices of the rows
-// first, then the slices, both in a fixed order.
+// Sums of partial rows: job j < dws adds the `ctas` rows of dw_part[which[j]],
+// job dws + g the `parts` rows of group g of the gate.  A CTA takes 16 x V
+// columns: 16 slices of the rows first, then the slices, in a fixed order.
+// Small CTAs with eight loads in flight a thread: the kernel is latency.
 struct NormSums {
     const float* dw_part;
     const float* dgate_part;
     float* out[4];
     float* dgate;
+    int which[4];
+    int dws;
     int64_t ctas, parts, width;
     int accumulate;
 };
 
-__global__ void __launch_bounds__(1024) norm_sums_kernel(const __grid_constant__ NormSums p) {
+template <int V>
+__global__ void __launch_bounds__(256) norm_sums_kernel(const __grid_constant__ NormSums p) {
     ptx::griddep_launch_dependents();
-    __shared__ float part[32][33];
+    __shared__ float part[16][16 * V + 1];
     ptx::griddep_wait();
-    const int64_t job = blockIdx.y;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31);
-    const int slice = threadIdx.x >> 5;
-    float* out = job < 4 ? p.out[job] : p.dgate + (job - 4) * p.width;
-    if (!out || (job >= 4 && !p.dgate)) return;
-    const int64_t n = job < 4 ? p.ctas : p.parts;
-    const float* in = job < 4 ? p.dw_part + job * p.ctas * p.width
-                              : p.dgate_part + (job - 4) * p.parts * p.width;
-    float s = 0.0f;
-    if (c < p.width) {
-#pragma unroll 4
-        for (int64_t i = slice; i < n; i += 32) s += in[i * p.width + c];
+    const int job = blockIdx.y, slice = threadIdx.x >> 4, lane = threadIdx.x & 15;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 16 * V + lane * V;
+    const bool gate = job >= p.dws;
+    const int64_t group = job - p.dws;
+    const int64_t n = gate ? p.parts : p.ctas;
+    const float* in = gate ? p.dgate_part + group * p.parts * p.width
+                           : p.dw_part + p.which[job] * p.ctas * p.width;
+    float s[V] = {};
+    if (c < p.width) {   // with V = 4 the width is a multiple of 4
+#pragma unroll 8
+        for (int64_t i = slice; i < n; i += 16) {
+            if constexpr (V == 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(in + i * p.width + c));
+                s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
+            } else {
+                s[0] += __ldcg(in + i * p.width + c);
+            }
+        }
     }
-    part[slice][threadIdx.x & 31] = s;
+#pragma unroll
+    for (int e = 0; e < V; ++e) part[slice][lane * V + e] = s[e];
     __syncthreads();
-    if (slice == 0 && c < p.width) {
+    if (threadIdx.x < 16 * V) {
+        const int64_t o = static_cast<int64_t>(blockIdx.x) * 16 * V + threadIdx.x;
         float t = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) t += part[i][threadIdx.x];
-        out[c] = p.accumulate ? out[c] + t : t;
+        for (int i = 0; i < 16; ++i) t += part[i][threadIdx.x];
+        if (o < p.width) {
+            float* out = gate ? p.dgate + group * p.width : p.out[p.which[job]];
+            out[o] = p.accumulate ? out[o] + t : t;
+        }
     }
+}
+
+// Launches the jobs whose outputs are set; `groups`: of dgate.
+void launch_sums(NormSums q, int64_t groups, cudaStream_t stream) {
+    q.dws = 0;
+    for (int j = 0; j < 4; ++j)
+        if (q.out[j]) q.which[q.dws++] = j;
+    const unsigned jobs = static_cast<unsigned>(q.dws + (q.dgate ? groups : 0));
+    if (!jobs) return;
+    if (q.width % 4 == 0)
+        launch_pdl(norm_sums_kernel<4>, dim3(static_cast<unsigned>((q.width + 63) / 64), jobs), dim3(256),
+                   0, stream, q);
+    else
+        launch_pdl(norm_sums_kernel<1>, dim3(static_cast<unsigned>((q.width + 15) / 16), jobs), dim3(256),
+                   0, stream, q);
 }
 
 // Shared memory for the ring of one CTA: what an SM has, less what L1 needs
@@ -1403,8 +1433,7 @@ void launch_column_sums(const float* part, int64_t n, int64_t width, float* out,
     q.ctas = n;
     q.width = width;
     q.accumulate = accumulate;
-    launch_pdl(norm_sums_kernel, dim3(static_cast<unsigned>((width + 31) / 32)), dim3(1024), 0,
-               stream, q);
+    launch_sums(q, 0, stream);
 }
 
 namespace {
@@ -1589,12 +1618,7 @@ int fp8_norm_bwd(const fp8_norm_bwd_args_t* a, void* workspace, size_t workspace
     q.dgate = direct ? nullptr : a->dgate;
     q.ctas = b.ctas; q.parts = b.parts; q.width = a->width;
     q.accumulate = a->accumulate != 0;
-    if (q.out[0] || q.out[1] || q.out[2] || q.out[3] || q.dgate) {
-        // several parts a group: fewer groups than CTAs
-        const unsigned jobs = static_cast<unsigned>(4 + (q.dgate ? b.groups : 0));
-        launch_pdl(norm_sums_kernel, dim3(static_cast<unsigned>((a->width + 31) / 32), jobs),
-                   dim3(1024), 0, s, q);
-    }
+    launch_sums(q, b.groups, s);   // several parts a group: fewer groups than CTAs
     return launch_status(what);
 }
 
