@@ -258,10 +258,10 @@ __global__ void __launch_bounds__(kRowThreads)
 }
 
 // The same for rows that do not start on 16 bytes: a CTA brings a token's row
-// into shared memory, each byte at its place modulo 16, and writes every copy
-// in aligned 16-byte pieces put together from two neighbouring words at a
-// time; single bytes only at a copy's two ends.
-constexpr int kImageBytes = 32768;   // of a row at a time
+// into shared memory, each byte at its place modulo 16, and writes the copies
+// in aligned 16-byte pieces put together from neighbouring words; single
+// bytes only at a copy's two ends.
+constexpr int kImageBytes = 32768;   // of a row at a time, at most
 
 __global__ void __launch_bounds__(kRowThreads)
     moe_permute_bytes_kernel(const uint8_t* __restrict__ x, const float* __restrict__ scale,
@@ -269,42 +269,51 @@ __global__ void __launch_bounds__(kRowThreads)
                              const int32_t* __restrict__ row_of, const int32_t* __restrict__ src,
                              int64_t rows, uint8_t* __restrict__ xs, float* __restrict__ scale_s) {
     ptx::griddep_launch_dependents();
-    __shared__ __align__(16) uint8_t image[kImageBytes + 64];
+    extern __shared__ __align__(16) uint8_t image[];   // the row's part, 64 bytes over
     __shared__ int to[kMaxSlots];
     ptx::griddep_wait();
     const int tid = threadIdx.x;
-    // bytes [0, n) of a row go to `out` from image + at (null: zeros)
-    auto write = [&](uint8_t* out, int n, int at, bool zeros) {
-        const int head = min(n, static_cast<int>(-reinterpret_cast<uintptr_t>(out) & 15));
-        const int body = (n - head) / 16;
-        for (int i = tid; i < body; i += kRowThreads) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (!zeros) {
-                const int b = at + head + 16 * i;
-                const uint32_t* q = reinterpret_cast<const uint32_t*>(image + (b & ~3));
-                const int s = 8 * (b & 3);
-                const uint32_t w0 = q[0], w1 = q[1], w2 = q[2], w3 = q[3], w4 = q[4];
-                v = make_uint4(__funnelshift_r(w0, w1, s), __funnelshift_r(w1, w2, s),
-                               __funnelshift_r(w2, w3, s), __funnelshift_r(w3, w4, s));
+    const bool pad = blockIdx.x >= tokens;   // CTAs past the tokens: zeros into pad rows
+    const int64_t t = blockIdx.x;
+    if (!pad && tid < slots) {
+        const int r = row_of[t * slots + tid];
+        to[tid] = r >= 0 && r < rows ? r : -1;
+        if (scale && to[tid] >= 0) scale_s[to[tid]] = scale[t];
+    }
+    // copies of `n` bytes, from image + at (pad: zeros), to `count` rows
+    auto write = [&](int count, int64_t pad_row, int64_t first, int n, int at) {
+        const int most = n / 16 + 1;   // aligned pieces, and one more turn for the ends
+        for (int k = tid; k < count * (most + 1); k += kRowThreads) {
+            const int j = k / (most + 1), i = k - j * (most + 1);
+            const int64_t r = pad ? pad_row : to[j];
+            if (r < 0) continue;
+            uint8_t* out = xs + r * row_bytes + first;
+            const int head = min(n, static_cast<int>(-reinterpret_cast<uintptr_t>(out) & 15));
+            const int body = (n - head) / 16;
+            if (i < body) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (!pad) {
+                    const int b = at + head + 16 * i;
+                    const uint32_t* q = reinterpret_cast<const uint32_t*>(image + (b & ~3));
+                    const int s = 8 * (b & 3);
+                    const uint32_t w0 = q[0], w1 = q[1], w2 = q[2], w3 = q[3], w4 = q[4];
+                    v = make_uint4(__funnelshift_r(w0, w1, s), __funnelshift_r(w1, w2, s),
+                                   __funnelshift_r(w2, w3, s), __funnelshift_r(w3, w4, s));
+                }
+                __stcs(reinterpret_cast<uint4*>(out + head + 16 * i), v);
+            } else if (i == most - 1) {
+                for (int e = 0; e < head; ++e) out[e] = pad ? uint8_t{0} : image[at + e];
+            } else if (i == most) {
+                for (int e = head + 16 * body; e < n; ++e) out[e] = pad ? uint8_t{0} : image[at + e];
             }
-            *reinterpret_cast<uint4*>(out + head + 16 * i) = v;
-        }
-        const int tail = n - head - 16 * body;
-        if (tid < head) out[tid] = zeros ? uint8_t{0} : image[at + tid];
-        else if (tid >= 32 && tid - 32 < tail) {
-            const int i = head + 16 * body + tid - 32;
-            out[i] = zeros ? uint8_t{0} : image[at + i];
         }
     };
-    if (blockIdx.x < tokens) {
-        const int64_t t = blockIdx.x;
-        if (tid < slots) {
-            const int r = row_of[t * slots + tid];
-            to[tid] = r >= 0 && r < rows ? r : -1;
-            if (scale && to[tid] >= 0) scale_s[to[tid]] = scale[t];
-        }
+    auto part = [&](int64_t first) {
+        return static_cast<int>(row_bytes - first < kImageBytes ? row_bytes - first : kImageBytes);
+    };
+    if (!pad) {
         for (int64_t first = 0; first < row_bytes; first += kImageBytes) {
-            const int n = static_cast<int>(row_bytes - first < kImageBytes ? row_bytes - first : kImageBytes);
+            const int n = part(first);
             const uint8_t* in = x + t * row_bytes + first;
             const int at = static_cast<int>(reinterpret_cast<uintptr_t>(in) & 15);
             const int head = min(n, (16 - at) & 15), body = (n - head) / 16;
@@ -316,16 +325,12 @@ __global__ void __launch_bounds__(kRowThreads)
             else if (tid >= 32 && tid - 32 < tail)
                 image[at + head + 16 * body + tid - 32] = in[head + 16 * body + tid - 32];
             __syncthreads();
-            for (int j = 0; j < slots; ++j)
-                if (to[j] >= 0) write(xs + static_cast<int64_t>(to[j]) * row_bytes + first, n, at, false);
+            write(slots, 0, first, n, at);
         }
     } else {
         for (int64_t r = blockIdx.x - tokens; r < rows; r += gridDim.x - tokens) {
             if (src[r] >= 0) continue;
-            for (int64_t first = 0; first < row_bytes; first += kImageBytes)
-                write(xs + r * row_bytes + first,
-                      static_cast<int>(row_bytes - first < kImageBytes ? row_bytes - first : kImageBytes),
-                      0, true);
+            for (int64_t first = 0; first < row_bytes; first += kImageBytes) write(1, r, first, part(first), 0);
             if (scale && tid == 0) scale_s[r] = 0.0f;
         }
     }
@@ -725,8 +730,9 @@ void launch_permute_bytes(const void* x, const float* scale, int64_t tokens, int
     const int64_t want = (rows + 15) / 16;
     const int64_t pad_ctas = want > 8 * num_sms() ? 8 * num_sms() : want;
     launch_pdl(moe_permute_bytes_kernel, dim3(static_cast<unsigned>(tokens + pad_ctas)),
-               dim3(kRowThreads), 0, st, static_cast<const uint8_t*>(x), scale, tokens, slots,
-               row_bytes, row_of, src, rows, static_cast<uint8_t*>(xs), scale_s);
+               dim3(kRowThreads), 64 + (row_bytes < kImageBytes ? (row_bytes + 15) / 16 * 16 : kImageBytes),
+               st, static_cast<const uint8_t*>(x), scale, tokens, slots, row_bytes, row_of, src, rows,
+               static_cast<uint8_t*>(xs), scale_s);
 }
 
 int launch_permute_bulk(const void* x, const float* scale, int64_t tokens, int slots,

@@ -74,6 +74,34 @@ def test_permute(C, dtype):
         assert torch.equal(ss.cpu(), scale[src.clamp_min(0) // k] * (src >= 0))
 
 
+@pytest.mark.parametrize("C,dtype", [(40001, torch.uint8), (40000, torch.uint8), (16385, BF), (20000, torch.float32)])
+def test_permute_long_rows(C, dtype):
+    """Rows that a kernel takes in several parts."""
+    ids = _ids(9, 2, 4, 1)
+    x = (torch.randn(9, C, generator=torch.Generator().manual_seed(2)) * 50).to(dtype)
+    p = F.fp8_moe_plan(ids.to(DEV), 4, align=4)
+    xs, _ = F.fp8_moe_permute(x.to(DEV), p.row_of, p.src)
+    src = p.src.cpu().long()
+    assert torch.equal(xs.cpu(), x[src.clamp_min(0) // 2] * (src >= 0)[:, None].to(dtype))
+
+
+@pytest.mark.parametrize("C", [12000, 20001])
+def test_wide_weighted_sum(C):
+    """Rows past what a CTA's registers hold."""
+    ids = _ids(5, 3, 4, 1)
+    g = torch.Generator().manual_seed(3)
+    p = F.fp8_moe_plan(ids.to(DEV), 4, align=4)
+    row = p.row_of.cpu().long()
+    ys, dy = torch.randn(p.src.numel(), C, generator=g).to(BF), torch.randn(5, C, generator=g).to(BF)
+    w = torch.rand(5, 3, generator=g)
+    v = ys[row.clamp_min(0)].to(F64) * (row >= 0)[..., None]
+    R.check(F.fp8_moe_unpermute(ys.to(DEV), p.row_of, weights=w.to(DEV)), (v * w.to(F64)[..., None]).sum(1),
+            (v * w.to(F64)[..., None]).abs().sum(1), "y")
+    _, dw = F.fp8_moe_unpermute_bwd(dy.to(DEV), ys.to(DEV), p.row_of, p.src, w.to(DEV))
+    t = v * dy.to(F64)[:, None, :]
+    R.check(dw, t.sum(2), t.abs().sum(2), "dweights")
+
+
 @pytest.mark.parametrize("dtype", [BF, torch.float32])
 @pytest.mark.parametrize("C", WIDTHS)
 @pytest.mark.parametrize("k", [1, 2, 8, 13])
