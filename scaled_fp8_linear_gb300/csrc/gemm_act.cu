@@ -38,6 +38,11 @@ constexpr int kMaxGemmExperts = 256;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (4 + kEpiWarps) * 32;
 
+// A launch's share of each product's rows.  A product whose last 256-row block
+// is at most half full can leave that remainder to a second launch in 128-row
+// tiles, which starts on the SMs as the first launch's CTAs run out of tiles.
+enum { kAllRows = 0, kWholeBlocks = 1, kRemainder = 2 };
+
 struct ActParams {
     int64_t M, N, K;
     int num_n, num_kb;
@@ -53,6 +58,7 @@ struct ActParams {
     const int32_t* offsets;   // null: one product over all rows
     int experts;
     int group;                // raster group (row blocks)
+    int part;                 // kAllRows, or which part of each product's rows
     unsigned* status;
 };
 
@@ -154,10 +160,10 @@ __device__ __forceinline__ void apply_act(int act, float (&v)[N]) {
 
 // ------------------------------------------------------------------ units of work
 
-// The experts' rows and tiles, in shared memory: expert e has rows off[e] ..
-// off[e + 1] and units first[e] .. first[e + 1].  Without offsets: one entry.
+// The products' rows and tiles, in shared memory: product e has rows begin[e]
+// .. end[e] and units first[e] .. first[e + 1].  One product without offsets.
 struct Units {
-    int off[kMaxGemmExperts + 1];
+    int begin[kMaxGemmExperts], end[kMaxGemmExperts];
     int first[kMaxGemmExperts + 1];
 };
 
@@ -167,41 +173,38 @@ struct Units {
 __device__ __forceinline__ void make_units(Units* u, const ActParams& p, int rows_per_tile) {
     const int t = static_cast<int>(threadIdx.x);
     const int M = static_cast<int>(p.M);
-    if (p.offsets) {
-        for (int e = t; e <= p.experts; e += blockDim.x)
-            u->off[e] = min(max(p.offsets[e], 0), M);
-    } else if (t <= 1) {
-        u->off[t] = t ? M : 0;
-    }
-    __syncthreads();
-    if (t < 32) {   // one warp: exclusive sum of the experts' tile counts
-        int run = 0, high = 0;
-        for (int base = 0; base <= p.experts; base += 32) {   // never falling
-            const int e = base + t;
-            int v = max(e <= p.experts ? u->off[e] : 0, high);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int w = __shfl_up_sync(row::kAll, v, o);
-                if (t >= o) v = max(v, w);
-            }
-            if (e <= p.experts) u->off[e] = v;
-            high = __shfl_sync(row::kAll, v, 31);
-        }
-        __syncwarp();
+    if (t < 32) {   // one warp, 32 products at a time
+        int run = 0, high = p.offsets ? min(max(p.offsets[0], 0), M) : 0;
         for (int base = 0; base < p.experts; base += 32) {
             const int e = base + t;
-            int n = 0;
-            if (e < p.experts) {
-                const int rows = u->off[e + 1] - u->off[e];
-                n = (rows + rows_per_tile - 1) / rows_per_tile * p.num_n;
+            const bool on = e < p.experts;
+            // the row after this product's last: the largest offset up to its own
+            int end = high;
+            if (on) end = max(high, p.offsets ? min(max(p.offsets[e + 1], 0), M) : M);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int w = __shfl_up_sync(row::kAll, end, o);
+                if (t >= o) end = max(end, w);
             }
+            int begin = __shfl_up_sync(row::kAll, end, 1);
+            if (t == 0) begin = high;
+            high = __shfl_sync(row::kAll, end, 31);
+            const int rest = (end - begin) % 256;
+            const int left = rest <= 128 ? rest : 0;   // what a second launch takes
+            if (p.part == kWholeBlocks) end -= left;
+            if (p.part == kRemainder) begin = end - left;
+            const int n = on ? (end - begin + rows_per_tile - 1) / rows_per_tile * p.num_n : 0;
             int incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(row::kAll, incl, o);
-                if (t >= o) incl += v;
+                const int w = __shfl_up_sync(row::kAll, incl, o);
+                if (t >= o) incl += w;
             }
-            if (e < p.experts) u->first[e] = run + incl - n;
+            if (on) {
+                u->begin[e] = begin;
+                u->end[e] = end;
+                u->first[e] = run + incl - n;
+            }
             run += __shfl_sync(row::kAll, incl, 31);
         }
         if (t == 0) u->first[p.experts] = run;
@@ -224,7 +227,7 @@ __device__ __forceinline__ Tile tile_of(int unit, const Units* u, const ActParam
         else hi = mid;
     }
     const int local = unit - u->first[lo];
-    const int num_m = (u->off[lo + 1] - u->off[lo] + rows_per_tile - 1) / rows_per_tile;
+    const int num_m = (u->end[lo] - u->begin[lo] + rows_per_tile - 1) / rows_per_tile;
     // grouped raster: `group` row blocks down each column block, so that the
     // CTAs at work share A and B panels in L2
     const int per_group = p.group * p.num_n;
@@ -233,8 +236,8 @@ __device__ __forceinline__ Tile tile_of(int unit, const Units* u, const ActParam
     const int in_g = local - g * per_group;
     Tile t;
     t.expert = lo;
-    t.row0 = u->off[lo] + (g * p.group + in_g % size) * rows_per_tile;
-    t.row_end = u->off[lo + 1];
+    t.row0 = u->begin[lo] + (g * p.group + in_g % size) * rows_per_tile;
+    t.row_end = u->end[lo];
     t.n_blk = in_g / size;
     return t;
 }
@@ -465,7 +468,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_act_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                          const __grid_constant__ CUtensorMap tmB,
                          const __grid_constant__ OutMaps maps, const __grid_constant__ ActParams p) {
-    ptx::griddep_launch_dependents();
     constexpr int TN = GATED ? kHalf : kPairTile;   // output columns of a tile
     constexpr uint32_t TMEM_COLS = 2 * kPairTile;
     extern __shared__ uint8_t smem_raw[];
@@ -506,6 +508,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ptx::tmem_relinquish_pair();
     }
     ptx::griddep_wait();
+    // only now: a remainder's launch does not wait for this one before it reads
+    ptx::griddep_launch_dependents();
     make_units(units, p, kPairTile);
     ptx::tc_fence_before();
     ptx::cluster_sync();
@@ -689,7 +693,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_alloc(tmem_slot, TMEM_COLS);
         ptx::tmem_relinquish();
     }
-    ptx::griddep_wait();
+    // A remainder's launch runs beside the whole blocks' launch: that one's CTAs
+    // have all waited for what came before, and the two write different rows.
+    // It waits at its end, so that what follows it follows both.
+    if (p.part != kRemainder) ptx::griddep_wait();
     ptx::tc_fence_before();
     make_units(units, p, kHalf);   // its barriers also cover the set-up above
     ptx::tc_fence_after();
@@ -795,6 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_dealloc(tmem_base, TMEM_COLS);
     }
     if (threadIdx.x == 0 && *abort_flag && p.status) atomicOr(p.status, 1u);
+    if (p.part == kRemainder) ptx::griddep_wait();
 }
 
 // ------------------------------------------------------------------ gradient of the epilogue
@@ -997,7 +1005,8 @@ int launch_tile(const fp8_gemm_act_args_t* a, ActParams& p, const OutMaps& maps,
     if (r == FP8_OK) r = kernel_slots(k, id, SMEM, 1, &ctas);
     if (r != FP8_OK) return r;
     p.num_n = static_cast<int>((a->N + TN - 1) / TN);
-    const int64_t tiles = most_tiles(a, kHalf, TN);
+    const int64_t tiles = p.part == kRemainder ? static_cast<int64_t>(a->experts) * p.num_n
+                                               : most_tiles(a, kHalf, TN);
     const unsigned grid = static_cast<unsigned>(tiles < ctas ? tiles : ctas);
     launch_pdl(k, dim3(grid), dim3(kThreads), SMEM, st, tmA, tmB, maps, p);
     return launch_status("fp8_gemm_act");
@@ -1025,8 +1034,28 @@ int launch_gemm_act(const fp8_gemm_act_args_t* a, ActParams& p, const OutMaps& m
     };
     const double c64 = cost(kHalf, 64, sms, 0.60), c128 = cost(kHalf, 128, sms, 0.67);
     const double c256 = cost(kHalf, 256, sms, 1.0), pair = cost(kPairTile, kPairTile, sms / 2, 0.92);
-    if (c64 <= c128 && c64 <= c256 && c64 <= pair) return launch_tile<64, GATED>(a, p, maps, st);
-    if (c128 <= c256 && c128 <= pair) return launch_tile<128, GATED>(a, p, maps, st);
+    // one product's whole blocks in pairs, its remainder in 128 x 256 tiles
+    // beside them (4099 x 8192 x 28672: 632 us, against 686 for 128 x 256 alone;
+    // experts' remainders, launched so, were 6% slower than all in 128 x 256)
+    double split = 1e30;
+    const int64_t rest = a->M % kPairTile;
+    if (!a->offsets && a->M > kPairTile && rest > 0 && rest <= kHalf) {
+        const int64_t n = (a->N + (GATED ? 127 : 255)) / (GATED ? 128 : 256);
+        const int64_t blocks = a->M / kPairTile * n, slots = sms / 2;
+        const double rounds = static_cast<double>((blocks + slots - 1) / slots) * 0.92;
+        const double even = (static_cast<double>(blocks) * 2 * 0.92 + static_cast<double>(n)) / sms;
+        split = even > rounds ? even : rounds;
+    }
+    if (c64 <= c128 && c64 <= c256 && c64 <= pair && c64 <= split)
+        return launch_tile<64, GATED>(a, p, maps, st);
+    if (c128 <= c256 && c128 <= pair && c128 <= split) return launch_tile<128, GATED>(a, p, maps, st);
+    if (split < c256 && split < pair) {
+        p.part = kWholeBlocks;
+        const int r = launch_pair<GATED>(a, p, maps, st);
+        if (r != FP8_OK) return r;
+        p.part = kRemainder;
+        return launch_tile<256, GATED>(a, p, maps, st);
+    }
     if (c256 < pair) return launch_tile<256, GATED>(a, p, maps, st);
     return launch_pair<GATED>(a, p, maps, st);
 }
