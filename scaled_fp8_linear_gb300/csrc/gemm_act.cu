@@ -17,6 +17,11 @@
 //   - eight epilogue warps: an activation costs more than a scale.
 // z stays in fp32 from the accumulator to D; D, z and the codes are each
 // rounded once.
+// Measured on a GB300: gated 4096 x 28672 x 8192 with z kept 1.18 ms (3.27
+// PFLOP/s, 0.86 of twice the bf16 cuBLAS burst rate), 4099 x 8192 x 28672 onto a
+// residual 0.64 ms (3.0; the power limit sets the clock), 32 experts' gated
+// products of 2048 x 4096 over 8192 rows to codes 138 us (2.0; 0.6 GB of weights,
+// tiles bound by the 64 bytes a cycle that an SM takes in).
 #include <cstdint>
 #include <mutex>
 
@@ -824,7 +829,8 @@ struct ActBwd {
 
 // Elementwise, HBM-bound: D's gradient and z are read once, dz is written
 // once, 256 columns a warp.  The pairs' packed instructions keep it off the
-// issue limit.  BIAS: column sums stay in registers over the CTA's rows.
+// issue limit: 8192 x 11008 gated to codes 111 us (6.5 TB/s; 138 with scalar
+// ones).  BIAS: column sums stay in registers over the CTA's rows.
 template <int ACT, bool GATED, bool BIAS>
 __global__ void __launch_bounds__(256) act_bwd_kernel(const __grid_constant__ ActBwd p) {
     ptx::griddep_launch_dependents();
