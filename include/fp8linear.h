@@ -428,7 +428,7 @@ typedef enum {
  *   N(v; w, b) = w (v - m) r + b, r = 1 / sqrt(mean((v - m)^2) + eps),
  *   m = mean(v) (FP8_NORM_LAYER) or 0 (FP8_NORM_RMS, which takes no b). */
 typedef struct {
-    int64_t rows;          /* tokens, >= 0                                    */
+    int64_t rows;          /* tokens, 0..2^31-1025                            */
     int64_t width;         /* 1..16384, any; multiples of 8 move in 16-byte   */
                            /*   pieces                                        */
     int32_t kind;          /* fp8_norm_t, of both norms                       */
@@ -511,9 +511,10 @@ int fp8_norm_bwd(const fp8_norm_bwd_args_t* args, void* workspace, size_t worksp
  * FP8_ERR_UNSUPPORTED), K-contiguous operands.
  * With `offsets` there is one product per expert: rows offsets[e] ..
  * offsets[e + 1] of A (and of residual, z, d, q) take B's and bias's part e.
- * The offsets are what fp8_moe_plan writes with an align that is a multiple
- * of 32, in device memory; rows past offsets[experts] are left as they are
- * (z, d, q) or unread. */
+ * The offsets are what fp8_moe_plan writes, in device memory, with any align
+ * (32 lets every row leave in a TMA box); rows past offsets[experts] are left
+ * as they are (z, d, q) or unread.  Offsets outside 0..M are held to it, and
+ * one below its predecessor counts as equal to it. */
 typedef struct {
     const uint8_t* A;      /* [M][K] codes, 16-byte aligned                   */
     const uint8_t* B;      /* [experts][N or 2N][K] codes, 16-byte aligned    */
@@ -528,7 +529,7 @@ typedef struct {
     int32_t gated;         /* 0 or 1                                          */
     const void* bias;      /* bf16 [experts][N or 2N], 16-byte aligned,       */
                            /*   nullable                                      */
-    const void* residual;  /* bf16 [M][N], nullable                           */
+    const void* residual;  /* bf16 [M][N], nullable; may be d itself          */
     void* z;               /* bf16 [M][N or 2N], for the backward pass,       */
                            /*   nullable                                      */
     void* d;               /* bf16 [M][N], nullable when q is set             */
@@ -577,7 +578,7 @@ int fp8_act_bwd(const fp8_act_bwd_args_t* args, void* workspace, size_t workspac
  *   src     [rows]           the row's token * slots + slot, or -1 (pad rows
  *                            and rows past offsets[experts])
  * rows: at least fp8_moe_rows(), which no routing exceeds.  experts 1..1024,
- * slots 1..64, align 1..4096; tokens * slots and rows below 2^31. */
+ * slots 1..64, align 1..4096; tokens * slots and rows at most 2^30. */
 int64_t fp8_moe_rows(int64_t tokens, int slots, int experts, int align);   /* -1: out of range */
 size_t fp8_moe_workspace_size(int64_t tokens, int slots, int experts);
 int fp8_moe_plan(const int32_t* ids, int64_t tokens, int slots, int experts, int align,

@@ -351,9 +351,9 @@ def fp8_gemm_act(A, fa: int, B, fb: int, scale_inv_a, scale_inv_b, ga: int = GRA
     act(z[:, :N]) z[:, N:] + residual (B's first N rows are the gate's).  A
     [M, K] and B [N or 2N, K] are FP8 codes.  D comes as bf16 (want_d) and,
     with q_fmt, as FP8 codes of D * q_scale; z (bf16, want_z) is what
-    fp8_act_bwd needs.  With offsets [E + 1] (fp8_moe_plan's, align a multiple
-    of 32) B is [E, N or 2N, K] and each expert's rows of A take their part of
-    B, scale_inv_b and bias."""
+    fp8_act_bwd needs.  With offsets [E + 1] (fp8_moe_plan's) B is
+    [E, N or 2N, K] and each expert's rows of A take their part of B,
+    scale_inv_b and bias.  d may be residual."""
     M, K = _rows(A, "A")
     E = 1
     if offsets is not None:
@@ -463,7 +463,7 @@ def fp8_moe_rows(tokens: int, slots: int, experts: int, align: int = 1) -> int:
     """Rows that hold any routing of this size."""
     r = int(_lib().fp8_moe_rows(tokens, slots, experts, align))
     if r < 0:
-        raise ValueError("fp8_moe_rows: slots 1..64, experts 1..1024, align 1..4096, tokens < 2^31")
+        raise ValueError("fp8_moe_rows: slots 1..64, experts 1..1024, align 1..4096, tokens * slots <= 2^30")
     return r
 
 

@@ -12,8 +12,8 @@
 //     and z_up never goes through memory;
 //   - per expert: a unit of work is a tile of one expert's rows; the experts'
 //     row offsets are read on the device, so no count comes to the host.  A
-//     tile's rows past its expert's end are computed and not written: offsets
-//     are multiples of 32, the height of a stored box;
+//     tile's rows past its expert's end are computed and not written; where
+//     an expert ends within a stored box, the rows are stored one by one;
 //   - eight epilogue warps: an activation costs more than a scale.
 // z stays in fp32 from the accumulator to D; D, z and the codes are each
 // rounded once.
@@ -57,7 +57,10 @@ struct ActParams {
     int act;
     const __nv_bfloat16* bias;
     const __nv_bfloat16* residual;
-    int has_z, has_d, has_q, q_fmt;
+    void* z;
+    void* d;
+    uint8_t* q;
+    int q_fmt;
     const float* q_scale;
     float* amax;
     const int32_t* offsets;   // null: one product over all rows
@@ -264,10 +267,16 @@ struct Staging {
     }
 };
 
-// Writes one box of 32 rows from the warp's next slot, filled through `fill`.
+// A warp's 32 rows of one tile: how a box of theirs is written.  kCopy: by the
+// TMA, which leaves out rows and columns past the matrix.  kByRow: the product
+// ends within the box and another's rows follow, so each row's thread stores
+// its own.  kNone: nothing there to write.
+enum class BoxMode { kNone, kCopy, kByRow };
+
+// Fills the warp's next slot through `fill` and, in kCopy, sends its box.
 template <int SLOTS, typename Fill>
 __device__ __forceinline__ void emit(Staging<SLOTS>& staging, const CUtensorMap* map, int64_t x, int64_t y,
-                                     bool in_range, Fill fill) {
+                                     BoxMode mode, Fill fill) {
     const int lane = threadIdx.x & 31;
     uint8_t* slot = staging.next();
     if (lane == 0) ptx::bulk_wait_group_read<SLOTS - 1>();   // the slot's last box has been read
@@ -276,48 +285,56 @@ __device__ __forceinline__ void emit(Staging<SLOTS>& staging, const CUtensorMap*
     ptx::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-        if (in_range)
+        if (mode == BoxMode::kCopy)
             ptx::tma_store_2d(map, ptx::smem_u32(slot), static_cast<int32_t>(x), static_cast<int32_t>(y));
         ptx::bulk_commit_group();
     }
 }
 
+// One row's 32 columns (n_left of them in the matrix, a multiple of 16).
+__device__ __forceinline__ void store_row(void* row0, int64_t pitch, int64_t m, int64_t n0, int n_left,
+                                          const uint4 (&w)[4]) {
+    uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(row0) + m * pitch + n0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (8 * j < n_left) out[j] = w[j];
+}
+
+__device__ __forceinline__ void pack32(uint4 (&w)[4], const float (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        w[j] = make_uint4(row::pack_bf16(v[8 * j], v[8 * j + 1]), row::pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                          row::pack_bf16(v[8 * j + 4], v[8 * j + 5]),
+                          row::pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+}
+
 // 32 columns of this thread's row as bf16: 64 bytes, in the TMA's 64-byte
 // swizzle (piece j of row r at j ^ ((r >> 1) & 3)), which spreads the banks.
 template <int SLOTS>
-__device__ __forceinline__ void emit_bf16(Staging<SLOTS>& staging, const float (&v)[32], const CUtensorMap* map,
-                                          int64_t x, int64_t y, bool in_range) {
-    emit(staging, map, x, y, in_range, [&](uint8_t* slot) {
+__device__ __forceinline__ void emit_bf16(Staging<SLOTS>& staging, const float (&v)[32],
+                                          const CUtensorMap* map, int64_t x, int64_t y, BoxMode mode) {
+    emit(staging, map, x, y, mode, [&](uint8_t* slot) {
         const int lane = threadIdx.x & 31, swz = (lane >> 1) & 3;
+        uint4 w[4];
+        pack32(w, v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint4 w = make_uint4(row::pack_bf16(v[8 * j], v[8 * j + 1]),
-                                       row::pack_bf16(v[8 * j + 2], v[8 * j + 3]),
-                                       row::pack_bf16(v[8 * j + 4], v[8 * j + 5]),
-                                       row::pack_bf16(v[8 * j + 6], v[8 * j + 7]));
-            *reinterpret_cast<uint4*>(slot + lane * 64 + 16 * (j ^ swz)) = w;
-        }
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(slot + lane * 64 + 16 * (j ^ swz)) = w[j];
     });
 }
 
-template <int SLOTS>
-__device__ __forceinline__ void emit_codes(Staging<SLOTS>& staging, const float (&v)[32], int fmt, float s,
-                                           const CUtensorMap* map, int64_t x, int64_t y,
-                                           bool in_range) {
-    emit(staging, map, x, y, in_range, [&](uint8_t* slot) {
-        const int lane = threadIdx.x & 31;
+// The codes of 32 columns: 32 bytes.
+__device__ __forceinline__ void codes32(uint4 (&w)[2], const float (&v)[32], int fmt, float s) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            uint32_t w[4];
+    for (int j = 0; j < 2; ++j) {
+        uint32_t c[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float* c = v + 16 * j + 4 * e;
-                w[e] = row::cvt_pair(fmt, __fmul_rn(c[0], s), __fmul_rn(c[1], s)) |
-                       (row::cvt_pair(fmt, __fmul_rn(c[2], s), __fmul_rn(c[3], s)) << 16);
-            }
-            *reinterpret_cast<uint4*>(slot + lane * 32 + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int e = 0; e < 4; ++e) {
+            const float* t = v + 16 * j + 4 * e;
+            c[e] = row::cvt_pair(fmt, __fmul_rn(t[0], s), __fmul_rn(t[1], s)) |
+                   (row::cvt_pair(fmt, __fmul_rn(t[2], s), __fmul_rn(t[3], s)) << 16);
         }
-    });
+        w[j] = make_uint4(c[0], c[1], c[2], c[3]);
+    }
 }
 
 // z of 32 columns: accumulator times factors plus bias.  fa: the row's
@@ -377,8 +394,8 @@ struct Residual {
 template <int SLOTS>
 __device__ __forceinline__ void emit_d(Staging<SLOTS>& staging, float (&v)[32], const Residual& res,
                                        const ActParams& p, const CUtensorMap* map, int64_t x, int64_t y,
-                                       bool in_range) {
-    emit(staging, map, x, y, in_range && p.has_d, [&](uint8_t* slot) {
+                                       BoxMode mode) {
+    emit(staging, map, x, y, p.d ? mode : BoxMode::kNone, [&](uint8_t* slot) {
         const int lane = threadIdx.x & 31, swz = (lane >> 1) & 3;
         uint8_t* own = slot + lane * 64;
         if (p.residual) {
@@ -396,11 +413,10 @@ __device__ __forceinline__ void emit_d(Staging<SLOTS>& staging, float (&v)[32], 
                 for (int e = 0; e < 8; ++e) v[8 * j + e] += t[e];
             }
         }
+        uint4 w[4];
+        pack32(w, v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(own + 16 * (j ^ swz)) =
-                make_uint4(row::pack_bf16(v[8 * j], v[8 * j + 1]), row::pack_bf16(v[8 * j + 2], v[8 * j + 3]),
-                           row::pack_bf16(v[8 * j + 4], v[8 * j + 5]), row::pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(own + 16 * (j ^ swz)) = w[j];
     });
 }
 
@@ -414,35 +430,65 @@ __device__ __forceinline__ void epilogue(Staging<SLOTS>& staging, Residual& res,
     const int lane = threadIdx.x & 31;
     const int64_t m = m0 + lane;
     const bool live = m < t.row_end;
-    const bool in_rows = m0 < t.row_end;
     const int64_t b_rows = GATED ? 2 * p.N : p.N;
     const float fa = p.ga == FP8_GRAN_ROW ? p.sa[live ? m : p.M - 1] : p.sa[0];
     const float sb0 = p.gb == FP8_GRAN_ROW ? 0.0f : p.sb[t.expert];
-    const float qs = p.has_q ? p.q_scale[0] : 0.0f;
+    const float qs = p.q ? p.q_scale[0] : 0.0f;
 #pragma unroll 1
     for (int c = 0; c < COLS / 32; ++c) {
         const int64_t n0 = n_first + c * 32;
         const int n_left = static_cast<int>(min(p.N - n0, static_cast<int64_t>(32)));
-        const bool in_range = in_rows && n_left > 0;
+        const BoxMode mode = m0 >= t.row_end || n_left <= 0 ? BoxMode::kNone
+                             : m0 + 32 > t.row_end && t.row_end < p.M ? BoxMode::kByRow : BoxMode::kCopy;
+        const bool by_row = mode == BoxMode::kByRow && live;
+        uint4 w[4];
         float z[32];
         uint32_t r[32], r_up[GATED ? 32 : 1];
         ptx::tmem_ld_32x32b_x32(tcol + c * 32, r);
         if constexpr (GATED) ptx::tmem_ld_32x32b_x32(tcol + UP + c * 32, r_up);
         ptx::tmem_wait_ld();
         dequant(z, r, fa, t.expert * b_rows + n0, n_left, p, sb0);
-        if (p.has_z) emit_bf16(staging, z, &maps.z, n0, m0, in_range);
+        if (p.z) {
+            emit_bf16(staging, z, &maps.z, n0, m0, mode);
+            if (by_row) {
+                pack32(w, z);
+                store_row(p.z, b_rows, m, n0, n_left, w);
+            }
+        }
         apply_act(p.act, z);
         if constexpr (GATED) {
             float up[32];
             dequant(up, r_up, fa, t.expert * b_rows + p.N + n0, n_left, p, sb0);
-            if (p.has_z) emit_bf16(staging, up, &maps.z_up, n0, m0, in_range);
+            if (p.z) {
+                emit_bf16(staging, up, &maps.z_up, n0, m0, mode);
+                if (by_row) {
+                    pack32(w, up);
+                    store_row(p.z, b_rows, m, p.N + n0, n_left, w);
+                }
+            }
 #pragma unroll
             for (int j = 0; j < 32; ++j) z[j] *= up[j];
         }
-        if (p.has_d || p.residual) emit_d(staging, z, res, p, &maps.d, n0, m0, in_range);
+        if (p.d || p.residual) {
+            emit_d(staging, z, res, p, &maps.d, n0, m0, mode);
+            if (p.d && by_row) {
+                pack32(w, z);
+                store_row(p.d, p.N, m, n0, n_left, w);
+            }
+        }
         if (c + 1 < COLS / 32) res.load(p, m0, t.row_end, n0 + 32);
-        if (p.has_q) {
-            emit_codes(staging, z, p.q_fmt, qs, &maps.q, n0, m0, in_range);
+        if (p.q) {
+            uint4 codes[2];
+            codes32(codes, z, p.q_fmt, qs);
+            emit(staging, &maps.q, n0, m0, mode, [&](uint8_t* slot) {
+                reinterpret_cast<uint4*>(slot + lane * 32)[0] = codes[0];
+                reinterpret_cast<uint4*>(slot + lane * 32)[1] = codes[1];
+            });
+            if (by_row) {
+                uint4* out = reinterpret_cast<uint4*>(p.q + m * p.N + n0);
+                out[0] = codes[0];
+                if (n_left > 16) out[1] = codes[1];
+            }
             if (p.amax && live) {
 #pragma unroll
                 for (int j = 0; j < 32; j += 16) {   // n_left is a multiple of 16
@@ -1123,7 +1169,7 @@ int fp8_gemm_act(const fp8_gemm_act_args_t* a, void* stream) {
     p.act = a->act;
     p.bias = static_cast<const __nv_bfloat16*>(a->bias);
     p.residual = static_cast<const __nv_bfloat16*>(a->residual);
-    p.has_z = a->z != nullptr; p.has_d = a->d != nullptr; p.has_q = a->q != nullptr;
+    p.z = a->z; p.d = a->d; p.q = a->q;
     p.q_fmt = a->q_format; p.q_scale = a->q_scale; p.amax = a->amax;
     p.offsets = a->offsets; p.experts = a->experts;
     p.group = raster_group(a->K);

@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kPlanThreads = 256, kPlanWarps = kPlanThreads / 32;
 constexpr int kMaxExperts = 1024, kMaxSlots = 64;
+constexpr int64_t kMost = int64_t{1} << 30;   // pairs and rows: 32-bit numbers and grids
 // One CTA ranks up to this many pairs: past it the per-CTA histograms of a
 // first launch cost less than the walk of one CTA over all pairs.
 constexpr int kPlanOneCta = 2048;
@@ -709,8 +710,8 @@ int check_routing(const char* what, int64_t tokens, int slots, int64_t rows) {
     if (tokens < 0 || slots < 1 || slots > kMaxSlots || rows < 0)
         return set_error(FP8_ERR_SHAPE, "%s: tokens and rows must be >= 0, slots in 1..%d", what,
                          kMaxSlots);
-    if (tokens * slots >= (int64_t{1} << 31) || rows >= (int64_t{1} << 31))
-        return set_error(FP8_ERR_SHAPE, "%s: tokens x slots and rows must be below 2^31", what);
+    if (tokens > kMost || tokens * slots > kMost || rows > kMost)
+        return set_error(FP8_ERR_SHAPE, "%s: tokens x slots and rows must be at most 2^30", what);
     return FP8_OK;
 }
 
@@ -812,7 +813,7 @@ extern "C" {
 
 int64_t fp8_moe_rows(int64_t tokens, int slots, int experts, int align) {
     if (tokens < 0 || slots < 1 || slots > kMaxSlots || experts < 1 || experts > kMaxExperts ||
-        align < 1 || align > 4096 || tokens >= (int64_t{1} << 31))
+        align < 1 || align > 4096 || tokens > kMost || tokens * slots > kMost)
         return -1;
     const int64_t n = tokens * slots;
     return n + (n < experts ? n : experts) * (align - 1);
@@ -834,7 +835,7 @@ int fp8_moe_plan(const int32_t* ids, int64_t tokens, int slots, int experts, int
     if (align < 1 || align > 4096)
         return set_error(FP8_ERR_SHAPE, "fp8_moe_plan: align %d outside 1..4096", align);
     const int64_t need_rows = fp8_moe_rows(tokens, slots, experts, align);
-    if (need_rows >= (int64_t{1} << 31) || rows < need_rows)
+    if (need_rows < 0 || need_rows > kMost || rows < need_rows)
         return set_error(FP8_ERR_SHAPE, "fp8_moe_plan: %lld rows, %lld needed (fp8_moe_rows)",
                          static_cast<long long>(rows), static_cast<long long>(need_rows));
     if (!offsets || !counts || ((!ids || !row_of) && tokens) || (!src && rows))

@@ -39,6 +39,7 @@ void launch_zero_words(void* p, int n, cudaStream_t stream) {
 namespace {
 
 constexpr int64_t kMaxWidth = 16384;   // a row in the registers of 1024 threads
+constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1025;   // row numbers, and a batch more, in 32 bits
 
 struct NormFwd {
     const void* x;
@@ -1454,8 +1455,8 @@ int launch_status(const char* what) {
 
 int check_shape(const char* what, int64_t rows, int64_t width, const void* gate, int64_t gate_rows,
                 int kind, int type) {
-    if (rows < 0 || width < 1 || rows >= (int64_t{1} << 31))
-        return set_error(FP8_ERR_SHAPE, "%s: rows must be in 0..2^31-1, width at least 1", what);
+    if (rows < 0 || width < 1 || rows > kMaxRows)
+        return set_error(FP8_ERR_SHAPE, "%s: rows must be in 0..2^31-1025, width at least 1", what);
     if (width > kMaxWidth)
         return set_error(FP8_ERR_UNSUPPORTED, "%s: width %lld, built up to %lld", what,
                          static_cast<long long>(width), static_cast<long long>(kMaxWidth));
@@ -1540,7 +1541,7 @@ int fp8_norm_fwd(const fp8_norm_fwd_args_t* a, void* stream) {
 }
 
 size_t fp8_norm_bwd_workspace_size(int64_t rows, int64_t width, int64_t gate_rows) {
-    if (rows < 0 || width < 1 || width > kMaxWidth || gate_rows < 0 ||
+    if (rows < 0 || rows > kMaxRows || width < 1 || width > kMaxWidth || gate_rows < 0 ||
         (gate_rows > 0 && rows % gate_rows))
         return 0;
     const BwdPlan b = bwd_plan(rows, width, gate_rows);

@@ -16,10 +16,11 @@ namespace row {
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 // 16-byte streaming load: read once, so it is not kept in L1, where the rows'
-// shared vectors (norm weights, gates) live.
+// shared vectors (norm weights, gates) live.  A plain load, not one of the
+// read-only path: some outputs may be an input itself.
 __device__ __forceinline__ uint4 ld_stream(const void* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;

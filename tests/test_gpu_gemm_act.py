@@ -28,7 +28,7 @@ def _val(q):
     return q.to(torch.float32).to(F64)
 
 
-def _case(M, N, K, act, gated, bias, res, gran, experts, q_fmt, seed=0, z=True):
+def _case(M, N, K, act, gated, bias, res, gran, experts, q_fmt, seed=0, z=True, align=32):
     g = torch.Generator().manual_seed(seed)
     rows = 2 * N if gated else N
     E = experts or 1
@@ -36,7 +36,7 @@ def _case(M, N, K, act, gated, bias, res, gran, experts, q_fmt, seed=0, z=True):
     if experts:
         off, at = [0], 0
         for e in range(E):               # ragged shares, expert 1 empty
-            at = min(M, at + (0 if e == 1 else 32 * int(torch.randint(0, 2 * M // (32 * E) + 2, (1,), generator=g))))
+            at = min(M, at + (0 if e == 1 else align * int(torch.randint(0, 2 * M // (align * E) + 2, (1,), generator=g))))
             off.append(at)
         off[-1] = max(off[-1], min(M, 32)) if E > 2 else off[-1]
     a, b = _codes(g, M, K), _codes(g, E, rows, K)
@@ -108,6 +108,41 @@ def test_epilogues(M, act, gated, bias, res, gran, q_fmt):
     (320, 48, 64, 256, True, F.GRAN_TENSOR)])
 def test_experts(M, N, K, E, gated, gran):
     _case(M, N, K, F.ACT_SILU, gated, True, True, gran, E, F.E4M3, seed=E)
+
+
+@pytest.mark.parametrize("align", [1, 16])
+@pytest.mark.parametrize("M,N,K,E,gated", [(300, 48, 64, 20, True), (1500, 272, 256, 6, False),
+                                           (2000, 528, 128, 17, True), (333, 16, 32, 256, False)])
+def test_experts_any_offsets(M, N, K, E, gated, align):
+    """Experts that end within a stored box of 32 rows."""
+    _case(M, N, K, F.ACT_GELU_TANH, gated, True, True, F.GRAN_ROW, E, F.E4M3, seed=M, align=align)
+
+
+def test_remainder_beside_pairs():
+    """A product whose last rows leave in a launch of their own: the same as
+    the row-wise product (700 = 2 x 256 + 188 has none, 600 and 4099 do)."""
+    for M, N, K in ((600, 8192, 512), (4099, 4096, 256)):
+        _case(M, N, K, F.ACT_SILU, False, True, True, F.GRAN_ROW, 0, F.E4M3, seed=M)
+
+
+def test_residual_in_place():
+    g = torch.Generator().manual_seed(3)
+    a, b = _codes(g, 700, 256).view(torch.uint8).to(DEV), _codes(g, 512, 256).view(torch.uint8).to(DEV)
+    one, res = torch.ones(1, device=DEV), torch.randn(700, 512, generator=g).to(BF).to(DEV)
+    want = F.fp8_gemm_act(a, F.E4M3, b, F.E4M3, one, one, act=F.ACT_GELU, residual=res).d
+    F.fp8_gemm_act(a, F.E4M3, b, F.E4M3, one, one, act=F.ACT_GELU, residual=res, d=res)
+    assert torch.equal(res, want)
+
+
+@pytest.mark.parametrize("fa,fb", [(F.E5M2, F.E4M3), (F.E4M3, F.E5M2), (F.E5M2, F.E5M2)])
+def test_formats(fa, fb):
+    """Small integers are exact in either format."""
+    g = torch.Generator().manual_seed(4)
+    a, b = (torch.randint(-3, 4, s, generator=g).float() for s in ((300, 128), (272, 128)))
+    q = lambda t, f: t.to(torch.float8_e5m2 if f == F.E5M2 else torch.float8_e4m3fn).view(torch.uint8).to(DEV)
+    one = torch.ones(1, device=DEV)
+    o = F.fp8_gemm_act(q(a, fa), fa, q(b, fb), fb, one, one)
+    assert torch.equal(o.d.cpu(), (a @ b.t()).to(BF))
 
 
 def test_experts_leave_other_rows():
