@@ -167,13 +167,13 @@ def _lib():
 
 
 def _given(t, what, dtype, shape):
-    """The address of a given tensor of this type and shape, 0 for none."""
-    if t is None:
-        return 0
-    if t.__class__ is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_cuda \
-            and t.is_contiguous():
-        return t.data_ptr()
-    p = _ptr(t, what, _U8 if dtype is torch.uint8 else dtype)   # says what is wrong
+    """The address of a tensor that has to be of this type and shape."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    p = _ptr(t, what, _U8 if dtype is _BYTE else dtype)   # says what is wrong
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     return p
@@ -187,9 +187,10 @@ def _on(stream, t):
 
 
 def _rows(t, what):
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{what} must be 2-D")
-    return t.shape
+    return shape
 
 
 def _workspace(workspace, need, device, stream):
@@ -268,12 +269,12 @@ def fp8_norm_fwd(x, h=None, kind: int = NORM_RMS, eps: float = 1e-5, alpha: floa
         0 if b_pre is None else _given(b_pre, "b_pre", _F32, vec), p_xo, p_y, p_q,
         E4M3 if q_fmt is None else q_fmt, q_gran, 1 if pow2 else 0,
         0 if q_scale is None else _given(q_scale, "q_scale", _F32, (1,)), p_inv, p_amax, p_stats)
-    _check(_lib().fp8_norm_fwd(a, _on(stream, ref)))
+    _check((_ready or _lib()).fp8_norm_fwd(a, _on(stream, ref)))
     return NormFwd(x_out, y, q, q_scale_inv, amax, stats)
 
 
 def fp8_norm_bwd_workspace_size(rows: int, width: int, gate_rows: int = 0) -> int:
-    return int(_lib().fp8_norm_bwd_workspace_size(rows, width, gate_rows))
+    return int((_ready or _lib()).fp8_norm_bwd_workspace_size(rows, width, gate_rows))
 
 
 def fp8_norm_bwd(dy, x_out, stats, dx_out=None, h=None, kind: int = NORM_RMS, alpha: float = 1.0,
@@ -336,7 +337,7 @@ def fp8_norm_bwd(dy, x_out, stats, dx_out=None, h=None, kind: int = NORM_RMS, al
         0 if dw_post is None else _given(dw_post, "dw_post", _F32, vec),
         0 if db_post is None else _given(db_post, "db_post", _F32, vec),
         0 if dgate is None else _given(dgate, "dgate", _F32, (gate_rows, C)), 1 if accumulate else 0)
-    _check(_lib().fp8_norm_bwd(a, ws, ws_bytes, _on(stream, ref)))
+    _check((_ready or _lib()).fp8_norm_bwd(a, ws, ws_bytes, _on(stream, ref)))
     return NormBwd(dx, dh, dw_pre, db_pre, dw_post, db_post, dgate)
 
 
@@ -402,13 +403,13 @@ def fp8_gemm_act(A, fa: int, B, fb: int, scale_inv_a, scale_inv_b, ga: int = GRA
         E4M3 if q_fmt is None else q_fmt,
         0 if q_scale is None else _given(q_scale, "q_scale", _F32, (1,)), p_amax,
         0 if offsets is None else _given(offsets, "offsets", _I32, (E + 1,)), E)
-    _check(_lib().fp8_gemm_act(a, _on(stream, A)))
+    _check((_ready or _lib()).fp8_gemm_act(a, _on(stream, A)))
     return GemmAct(d, z, q, amax)
 
 
 @functools.lru_cache(maxsize=256)
 def fp8_act_bwd_workspace_size(M: int, N: int, gated: bool) -> int:
-    return int(_lib().fp8_act_bwd_workspace_size(M, N, int(bool(gated))))
+    return int((_ready or _lib()).fp8_act_bwd_workspace_size(M, N, int(bool(gated))))
 
 
 def fp8_act_bwd(dD, z, act: int, gated: bool = False, want_dz: bool = True, q_fmt: int | None = None,
@@ -452,7 +453,7 @@ def fp8_act_bwd(dD, z, act: int, gated: bool = False, want_dz: bool = True, q_fm
         p_dz, p_q, E4M3 if q_fmt is None else q_fmt,
         0 if q_scale is None else _given(q_scale, "q_scale", _F32, (1,)), p_amax, p_db,
         1 if accumulate else 0)
-    _check(_lib().fp8_act_bwd(a, ws, ws_bytes, _on(stream, dD)))
+    _check((_ready or _lib()).fp8_act_bwd(a, ws, ws_bytes, _on(stream, dD)))
     return ActBwd(dz, q, amax, dbias)
 
 
@@ -461,7 +462,7 @@ def fp8_act_bwd(dD, z, act: int, gated: bool = False, want_dz: bool = True, q_fm
 @functools.lru_cache(maxsize=256)
 def fp8_moe_rows(tokens: int, slots: int, experts: int, align: int = 1) -> int:
     """Rows that hold any routing of this size."""
-    r = int(_lib().fp8_moe_rows(tokens, slots, experts, align))
+    r = int((_ready or _lib()).fp8_moe_rows(tokens, slots, experts, align))
     if r < 0:
         raise ValueError("fp8_moe_rows: slots 1..64, experts 1..1024, align 1..4096, tokens * slots <= 2^30")
     return r
@@ -469,7 +470,7 @@ def fp8_moe_rows(tokens: int, slots: int, experts: int, align: int = 1) -> int:
 
 @functools.lru_cache(maxsize=256)
 def fp8_moe_workspace_size(tokens: int, slots: int, experts: int) -> int:
-    return int(_lib().fp8_moe_workspace_size(tokens, slots, experts))
+    return int((_ready or _lib()).fp8_moe_workspace_size(tokens, slots, experts))
 
 
 def fp8_moe_plan(ids, experts: int, align: int = 1, rows: int | None = None, offsets=None,
@@ -484,20 +485,27 @@ def fp8_moe_plan(ids, experts: int, align: int = 1, rows: int | None = None, off
         rows = fp8_moe_rows(T, k, experts, align) if src is None else src.numel()
     if offsets is None:
         offsets = torch.empty(experts + 1, dtype=_I32, device=dev)
+        p_off = offsets.data_ptr()
+    else:
+        p_off = _given(offsets, "offsets", _I32, (experts + 1,))
     if counts is None:
         counts = torch.empty(experts, dtype=_I32, device=dev)
+        p_cnt = counts.data_ptr()
+    else:
+        p_cnt = _given(counts, "counts", _I32, (experts,))
     if row_of is None:
         row_of = torch.empty_like(ids)
     if src is None:
         src = torch.empty(rows, dtype=_I32, device=dev)
+        p_src = src.data_ptr()
+    else:
+        p_src = _given(src, "src", _I32, (rows,))
     ws, ws_bytes, need = None, 0, fp8_moe_workspace_size(T, k, experts)
     if need:
         ws, ws_bytes, workspace = _workspace(workspace, need, dev, stream)
-    _check(_lib().fp8_moe_plan(
-        _given(ids, "ids", _I32, (T, k)), T, k, experts, align,
-        _given(offsets, "offsets", _I32, (experts + 1,)), _given(counts, "counts", _I32, (experts,)),
-        _given(row_of, "row_of", _I32, (T, k)), _given(src, "src", _I32, (rows,)), rows, ws, ws_bytes,
-        _on(stream, ids)))
+    _check((_ready or _lib()).fp8_moe_plan(
+        _given(ids, "ids", _I32, (T, k)), T, k, experts, align, p_off, p_cnt,
+        _given(row_of, "row_of", _I32, (T, k)), p_src, rows, ws, ws_bytes, _on(stream, ids)))
     return MoePlan(offsets, counts, row_of, src)
 
 
@@ -509,13 +517,20 @@ def fp8_moe_permute(x, row_of, src, scale=None, xs=None, scale_s=None, stream=No
     k, rows = _rows(row_of, "row_of")[1], src.numel()
     if xs is None:
         xs = torch.empty(rows, C, dtype=x.dtype, device=x.device)
-    if scale is not None and scale_s is None:
-        scale_s = torch.empty(rows, dtype=_F32, device=x.device)
-    _check(_lib().fp8_moe_permute(
-        _given(x, "x", x.dtype, (T, C)), 0 if scale is None else _given(scale, "scale", _F32, (T,)), T, k,
-        C * x.element_size(), _given(row_of, "row_of", _I32, (T, k)), _given(src, "src", _I32, (rows,)),
-        rows, _given(xs, "xs", x.dtype, (rows, C)),
-        0 if scale_s is None else _given(scale_s, "scale_s", _F32, (rows,)), _on(stream, x)))
+        p_xs = xs.data_ptr()
+    else:
+        p_xs = _given(xs, "xs", x.dtype, (rows, C))
+    p_sc = p_ss = 0
+    if scale is not None:
+        if scale_s is None:
+            scale_s = torch.empty(rows, dtype=_F32, device=x.device)
+        p_sc = _given(scale, "scale", _F32, (T,))
+    if scale_s is not None:
+        p_ss = _given(scale_s, "scale_s", _F32, (rows,))
+    _check((_ready or _lib()).fp8_moe_permute(
+        _given(x, "x", x.dtype, (T, C)), p_sc, T, k, C * x.element_size(),
+        _given(row_of, "row_of", _I32, (T, k)), _given(src, "src", _I32, (rows,)), rows, p_xs, p_ss,
+        _on(stream, x)))
     return xs, scale_s
 
 
@@ -528,9 +543,9 @@ def fp8_moe_unpermute(ys, row_of, weights=None, y=None, stream=None) -> torch.Te
         raise TypeError(f"ys: dtype {ys.dtype}, expected bfloat16 or float32")
     if y is None:
         y = torch.empty(T, C, dtype=ys.dtype, device=ys.device)
-    _check(_lib().fp8_moe_unpermute(
+    _check((_ready or _lib()).fp8_moe_unpermute(
         _given(ys, "ys", ys.dtype, (rows, C)), _OUT[ys.dtype], _given(row_of, "row_of", _I32, (T, k)),
-        _given(weights, "weights", _F32, (T, k)), T, k, C, rows, _given(y, "y", ys.dtype, (T, C)),
+        0 if weights is None else _given(weights, "weights", _F32, (T, k)), T, k, C, rows, _given(y, "y", ys.dtype, (T, C)),
         _on(stream, ys)))
     return y
 
@@ -546,10 +561,10 @@ def fp8_moe_unpermute_bwd(dy, ys, row_of, src, weights=None, dys=None, dweights=
         dys = torch.empty(rows, C, dtype=ys.dtype, device=ys.device)
     if dweights is None and weights is not None:
         dweights = torch.empty(T, k, dtype=_F32, device=ys.device)
-    _check(_lib().fp8_moe_unpermute_bwd(
+    _check((_ready or _lib()).fp8_moe_unpermute_bwd(
         _given(dy, "dy", ys.dtype, (T, C)), _given(ys, "ys", ys.dtype, (rows, C)), _OUT[ys.dtype],
         _given(row_of, "row_of", _I32, (T, k)), _given(src, "src", _I32, (rows,)),
-        _given(weights, "weights", _F32, (T, k)), T, k, C, rows,
-        _given(dys, "dys", ys.dtype, (rows, C)), _given(dweights, "dweights", _F32, (T, k)),
+        0 if weights is None else _given(weights, "weights", _F32, (T, k)), T, k, C, rows,
+        _given(dys, "dys", ys.dtype, (rows, C)), 0 if dweights is None else _given(dweights, "dweights", _F32, (T, k)),
         _on(stream, ys)))
     return dys, dweights
