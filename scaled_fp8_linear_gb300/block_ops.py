@@ -306,17 +306,14 @@ def fp8_norm_bwd(dy, x_out, stats, dx_out=None, h=None, kind: int = NORM_RMS, al
     if dh is None and h is not None:
         dh = torch.empty_like(h)
     gate_rows = 0 if gate is None else _rows(gate, "gate")[0]
-    n = sum(want)
-    if n:   # the vectors' gradients in one allocation, each row 16-byte aligned
-        step = (C + 3) // 4 * 4
-        rows = torch.empty(n, step, dtype=_F32, device=dev).unbind(0)
-        if step != C:
-            rows = [r[:C] for r in rows]
-        rows = iter(rows)
-        dw_pre = next(rows) if want[0] else dw_pre
-        db_pre = next(rows) if want[1] else db_pre
-        dw_post = next(rows) if want[2] else dw_post
-        db_post = next(rows) if want[3] else db_post
+    if want[0]:
+        dw_pre = torch.empty(C, dtype=_F32, device=dev)
+    if want[1]:
+        db_pre = torch.empty(C, dtype=_F32, device=dev)
+    if want[2]:
+        dw_post = torch.empty(C, dtype=_F32, device=dev)
+    if want[3]:
+        db_post = torch.empty(C, dtype=_F32, device=dev)
     if dgate is None and gate is not None:
         dgate = torch.empty(gate_rows, C, dtype=_F32, device=dev)
     ws, ws_bytes, workspace = _workspace(workspace, fp8_norm_bwd_workspace_size(T, C, gate_rows), dev,
