@@ -180,7 +180,7 @@ __device__ __forceinline__ int piece_len(int col, int lanes, int64_t width) {
 
 // Mean (layer norm) and 1/sqrt(variance + eps) of the row whose pieces the
 // threads hold; elements past the row are zero in v and left out of the sums.
-template <int VPT, bool WARP, bool VEC, bool LAYER>
+template <int VPT, bool WARP, bool LAYER>
 __device__ __forceinline__ void row_stats(const float (&v)[VPT][8], const int (&n)[VPT], float inv_c,
                                           float eps, float* part, int& turn, float& mean,
                                           float& rstd) {
@@ -200,32 +200,32 @@ __device__ __forceinline__ void row_stats(const float (&v)[VPT][8], const int (&
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float d = v[i][e] - mean;
-            if (VEC ? n[i] > 0 : e < n[i]) s[0] = fmaf(d, d, s[0]);
+            if (e < n[i]) s[0] = fmaf(d, d, s[0]);
         }
     row_sum<WARP>(s, part, turn);
     rstd = 1.0f / sqrtf(s[0] * inv_c + eps);
 }
 
 // v = w (v - mean) rstd + b on one piece.
-template <bool VEC>
 __device__ __forceinline__ void apply_norm(float (&v)[8], const float* w, const float* b, int c,
                                            int n, int step, float mean, float rstd) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = (v[e] - mean) * rstd;
     float s[8];
     if (w) {
-        shared8<VEC>(s, w + c, n, step);
+        shared8<false>(s, w + c, n, step);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= s[e];
     }
     if (b) {
-        shared8<VEC>(s, b + c, n, step);
+        shared8<false>(s, b + c, n, step);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += s[e];
     }
 }
 
-template <typename S, int VPT, bool WARP, bool VEC, bool LAYER, int THREADS>
+// The forward for rows that do not start on 16 bytes.
+template <typename S, int VPT, bool WARP, bool LAYER, int THREADS>
 __global__ void __launch_bounds__(THREADS)
     norm_fwd_any_kernel(const __grid_constant__ NormFwd p) {
     ptx::griddep_launch_dependents();
@@ -245,38 +245,38 @@ __global__ void __launch_bounds__(THREADS)
     int n[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = piece_col<VEC>(at, i, lanes);
-        n[i] = piece_len<VEC>(c, lanes, p.width);
+        const int c = piece_col<false>(at, i, lanes);
+        n[i] = piece_len<false>(c, lanes, p.width);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[i][e] = x[i][e] = 0.0f;
         if (n[i] > 0) {
-            if (p.h) load8<VEC>(v[i], p.h + base + c, n[i], lanes);
-            if (xin) load8<VEC>(x[i], xin + base + c, n[i], lanes);
+            if (p.h) load8<false>(v[i], p.h + base + c, n[i], lanes);
+            if (xin) load8<false>(x[i], xin + base + c, n[i], lanes);
         }
     }
     float mean_post = 0.0f, rstd_post = 0.0f, mean_pre = 0.0f, rstd_pre = 0.0f;
     if (p.post)
-        row_stats<VPT, WARP, VEC, LAYER>(v, n, inv_c, p.eps, part, turn, mean_post, rstd_post);
+        row_stats<VPT, WARP, LAYER>(v, n, inv_c, p.eps, part, turn, mean_post, rstd_post);
     const __nv_bfloat16* gate =
         p.gate ? p.gate + (r / p.rows_per_gate) * p.width : nullptr;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = piece_col<VEC>(at, i, lanes);
+        const int c = piece_col<false>(at, i, lanes);
         if (n[i] <= 0) continue;
-        if (p.post) apply_norm<VEC>(v[i], p.w_post, p.b_post, c, n[i], lanes, mean_post, rstd_post);
+        if (p.post) apply_norm(v[i], p.w_post, p.b_post, c, n[i], lanes, mean_post, rstd_post);
         if (gate) {
             float g[8];
-            shared8<VEC>(g, gate + c, n[i], lanes);
+            shared8<false>(g, gate + c, n[i], lanes);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[i][e] *= g[e];
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            v[i][e] = VEC || e < n[i] ? fmaf(p.alpha, x[i][e], v[i][e]) : 0.0f;
-        if (p.x_out) store8<VEC>(static_cast<S*>(p.x_out) + base + c, v[i], n[i], lanes);
+            v[i][e] = e < n[i] ? fmaf(p.alpha, x[i][e], v[i][e]) : 0.0f;
+        if (p.x_out) store8<false>(static_cast<S*>(p.x_out) + base + c, v[i], n[i], lanes);
     }
     if (p.y || p.q || p.stats)
-        row_stats<VPT, WARP, VEC, LAYER>(v, n, inv_c, p.eps, part, turn, mean_pre, rstd_pre);
+        row_stats<VPT, WARP, LAYER>(v, n, inv_c, p.eps, part, turn, mean_pre, rstd_pre);
     if (p.stats && at == 0) {
         p.stats[r] = mean_post;
         p.stats[p.rows + r] = rstd_post;
@@ -287,13 +287,13 @@ __global__ void __launch_bounds__(THREADS)
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = piece_col<VEC>(at, i, lanes);
+        const int c = piece_col<false>(at, i, lanes);
         if (n[i] <= 0) continue;
-        apply_norm<VEC>(v[i], p.w_pre, p.b_pre, c, n[i], lanes, mean_pre, rstd_pre);
-        if (p.y) store8<VEC>(p.y + base + c, v[i], n[i], lanes);
+        apply_norm(v[i], p.w_pre, p.b_pre, c, n[i], lanes, mean_pre, rstd_pre);
+        if (p.y) store8<false>(p.y + base + c, v[i], n[i], lanes);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (VEC || e < n[i]) top = max(top, row::abs_bits(v[i][e]));
+            if (e < n[i]) top = max(top, row::abs_bits(v[i][e]));
     }
     if (!p.q) return;
     float s = 1.0f;
@@ -307,17 +307,13 @@ __global__ void __launch_bounds__(THREADS)
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = piece_col<VEC>(at, i, lanes);
+        const int c = piece_col<false>(at, i, lanes);
         if (n[i] <= 0) continue;
         const uint2 code = row::cvt8(p.q_fmt, v[i], s);
-        if constexpr (VEC) {
-            *reinterpret_cast<uint2*>(p.q + base + c) = code;
-        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < n[i])
-                    p.q[base + c + e * lanes] = static_cast<uint8_t>((e < 4 ? code.x : code.y) >> (8 * (e & 3)));
-        }
+        for (int e = 0; e < 8; ++e)
+            if (e < n[i])
+                p.q[base + c + e * lanes] = static_cast<uint8_t>((e < 4 ? code.x : code.y) >> (8 * (e & 3)));
     }
 }
 
@@ -330,7 +326,7 @@ constexpr int kHasAll = 1;    // forward: x, h, x', w_pre; backward: dy, x', dx'
 constexpr int kHasPost = 2;   // with w_post
 constexpr int kHasGate = 4;
 
-// The forward for rows in 16-byte pieces up to kFastWidth columns: CTAs stay
+// The forward for rows in 16-byte pieces: CTAs stay
 // on the SM and walk the rows, each thread on its own columns, with the
 // vectors of those columns in registers (RMS norm) and the next row's pieces
 // loaded while the current row is reduced -- a row's loads cover the two
@@ -343,7 +339,8 @@ __global__ void __launch_bounds__(THREADS)
     // sums: two buffers of 16 warps' values; the row maximum has its own
     __shared__ __align__(16) float part[2][16];
     __shared__ float part_max[128];
-    constexpr bool KEEP = !LAYER;
+    constexpr bool KEEP = !LAYER && VPT <= 2;   // the vectors before the second norm
+    constexpr bool KEEP_PRE = VPT <= 2;         // and its own
     constexpr bool ALL = (HAS & kHasAll) != 0;
     const bool has_h = ALL || p.h, has_x = ALL || p.x, has_x_out = ALL || p.x_out;
     const bool has_w_pre = ALL || p.w_pre;
@@ -385,15 +382,16 @@ __global__ void __launch_bounds__(THREADS)
             if (has_x) xn[i].load(xin + r * p.width + col[i]);
         }
     }
-    f2 wg[KEEP ? VPT : 1][4], wp[VPT][4], bp[KEEP ? 1 : VPT][4];   // w_post * gate, w_pre, b_pre
+    f2 wg[KEEP ? VPT : 1][4];   // w_post * gate
+    f2 wp[KEEP_PRE ? VPT : 1][4], bp[KEEP_PRE && LAYER ? VPT : 1][4];   // w_pre, b_pre
     int64_t group = 0, group_end = 0;   // the gate row in use and the row after its last
     const bool scaled = has_w_post || gated;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        if (!live[i]) continue;
-        if (has_w_pre) row::shared_pairs(wp[i], p.w_pre + col[i]);
+        if (!KEEP_PRE || !live[i]) continue;
+        if (has_w_pre) row::shared_pairs(wp[KEEP_PRE ? i : 0], p.w_pre + col[i]);
         if constexpr (LAYER) {
-            if (p.b_pre) row::shared_pairs(bp[i], p.b_pre + col[i]);
+            if (p.b_pre) row::shared_pairs(bp[KEEP_PRE ? i : 0], p.b_pre + col[i]);
         }
     }
     const f2 alpha = row::all2(p.alpha);
@@ -513,13 +511,18 @@ __global__ void __launch_bounds__(THREADS)
         for (int i = 0; i < VPT; ++i) {
             if (!live[i]) continue;
             const f2 rs = row::all2(rstd_pre), m = row::all2(-mean_pre);
+            const int kept = KEEP_PRE ? i : 0;
+            if constexpr (!KEEP_PRE) {
+                if (has_w_pre) row::shared_pairs(wp[0], p.w_pre + col[i]);
+                if (LAYER && p.b_pre) row::shared_pairs(bp[0], p.b_pre + col[i]);
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if constexpr (LAYER) v[i][e] = row::add2(v[i][e], m);
                 v[i][e] = row::mul2(v[i][e], rs);
-                if (has_w_pre) v[i][e] = row::mul2(v[i][e], wp[i][e]);
+                if (has_w_pre) v[i][e] = row::mul2(v[i][e], wp[kept][e]);
                 if constexpr (LAYER) {
-                    if (p.b_pre) v[i][e] = row::add2(v[i][e], bp[i][e]);
+                    if (p.b_pre) v[i][e] = row::add2(v[i][e], bp[kept][e]);
                 }
             }
             if (p.y) row::store_pairs(p.y + base + col[i], v[i]);
@@ -558,8 +561,8 @@ __global__ void __launch_bounds__(THREADS)
     }
 }
 
-// Rows in 16-byte pieces up to here take the resident kernels: 512 threads
-// with two pieces each, 128 registers a thread.
+// Rows in 16-byte pieces up to here: 512 threads with two pieces each and 128
+// registers a thread.
 constexpr int64_t kFastWidth = 8192;
 
 template <typename S, bool LAYER>
@@ -596,16 +599,18 @@ void launch_fwd(const NormFwd& p, cudaStream_t st) {
         return;
     }
     if (p.width % 8 == 0) {
-        launch_pdl(norm_fwd_any_kernel<S, 2, false, true, LAYER, 1024>,
-                   dim3(static_cast<unsigned>(p.rows)), dim3(threads), 0, st, p);
+        // wider rows: four pieces a thread, all vectors through L1
+        const int t4 = static_cast<int>(((pieces + 3) / 4 + 31) / 32 * 32);
+        const dim3 grid(static_cast<unsigned>(p.rows < num_sms() ? p.rows : num_sms()));
+        launch_pdl(norm_fwd_kernel<S, 4, false, LAYER, 512, 0>, grid, dim3(t4), 0, st, p);
     } else if (pieces <= 64) {
-        launch_pdl(norm_fwd_any_kernel<S, 2, true, false, LAYER, 256>,
+        launch_pdl(norm_fwd_any_kernel<S, 2, true, LAYER, 256>,
                    dim3(static_cast<unsigned>((p.rows + 7) / 8)), dim3(256), 0, st, p);
     } else if (threads <= 512) {
-        launch_pdl(norm_fwd_any_kernel<S, 2, false, false, LAYER, 512>,
+        launch_pdl(norm_fwd_any_kernel<S, 2, false, LAYER, 512>,
                    dim3(static_cast<unsigned>(p.rows)), dim3(threads), 0, st, p);
     } else {
-        launch_pdl(norm_fwd_any_kernel<S, 2, false, false, LAYER, 1024>,
+        launch_pdl(norm_fwd_any_kernel<S, 2, false, LAYER, 1024>,
                    dim3(static_cast<unsigned>(p.rows)), dim3(threads), 0, st, p);
     }
 }
