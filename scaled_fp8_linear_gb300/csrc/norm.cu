@@ -14,7 +14,9 @@
 // (a second reduction over the registers), which does not cancel.
 #include <atomic>
 #include <cfloat>
+#include <climits>
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -716,19 +718,16 @@ __device__ __forceinline__ void flush(const float (&acc)[VPT][8], const int (&n)
 // db_post = sum of gate B  over the chunks: one pair of running sums serves
 // the gate's and the post norm's gradients.
 //
-// This kernel takes any width (8192 x 4095: 336 us; 4096 x 16384: 288 us, its
-// sums spill at 64 registers a thread); the resident one below takes the usual ones.
-template <typename S, int VPT, bool WARP, bool VEC, bool LAYER, int THREADS>
-__global__ void __launch_bounds__(THREADS)
+// This kernel takes rows wider than kFastWidth (4096 x 16384: 288 us; its sums
+// spill at 64 registers a thread), the resident one below the others.
+template <typename S, bool VEC, bool LAYER>
+__global__ void __launch_bounds__(1024)
     norm_bwd_any_kernel(const __grid_constant__ NormBwd p) {
     ptx::griddep_launch_dependents();
     __shared__ float part[128];
-    __shared__ float buf[WARP ? 8 * 512 : 1];
     ptx::griddep_wait();
-    const int lanes = WARP ? 32 : static_cast<int>(blockDim.x);
-    const int at = WARP ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
-    const int64_t first = WARP ? threadIdx.x >> 5 : 0;
-    const int64_t step = WARP ? blockDim.x >> 5 : 1;
+    constexpr int VPT = 2;
+    const int lanes = static_cast<int>(blockDim.x), at = static_cast<int>(threadIdx.x);
     const float inv_c = 1.0f / static_cast<float>(p.width);
     int turn = 0;
 
@@ -746,10 +745,10 @@ __global__ void __launch_bounds__(THREADS)
     }
     auto sum = [&](float (&s)[2]) {
         if constexpr (LAYER) {
-            row_sum<WARP>(s, part, turn);
+            row_sum<false>(s, part, turn);
         } else {
             float t[1] = {s[0]};
-            row_sum<WARP>(t, part, turn);
+            row_sum<false>(t, part, turn);
             s[0] = t[0];
             s[1] = 0.0f;
         }
@@ -763,7 +762,7 @@ __global__ void __launch_bounds__(THREADS)
         const int64_t begin = group * in_group + part_no * in_group / p.parts;
         const int64_t end = group * in_group + (part_no + 1) * in_group / p.parts;
         const __nv_bfloat16* gate = p.gate ? p.gate + group * p.width : nullptr;
-        for (int64_t r = begin + first; r < end; r += step) {
+        for (int64_t r = begin; r < end; ++r) {
             const int64_t base = r * p.width;
             float d[VPT][8], u[VPT][8];
             float m_post = 0.0f, r_post = 1.0f;
@@ -891,8 +890,8 @@ __global__ void __launch_bounds__(THREADS)
                     }
                 }
             }
-            flush<VPT, WARP, VEC>(t, n, at, lanes, p.width, p.dgate_part + k * p.width,
-                                  p.add_dgate != 0, buf);
+            flush<VPT, false, VEC>(t, n, at, lanes, p.width, p.dgate_part + k * p.width,
+                                  p.add_dgate != 0, nullptr);
         }
         if (p.post) {
 #pragma unroll
@@ -907,9 +906,9 @@ __global__ void __launch_bounds__(THREADS)
                 }
             }
             const bool add = k != blockIdx.x;
-            flush<VPT, WARP, VEC>(sum_a, n, at, lanes, p.width, my_sums + 2 * rows_of, add, buf);
+            flush<VPT, false, VEC>(sum_a, n, at, lanes, p.width, my_sums + 2 * rows_of, add, nullptr);
             if constexpr (LAYER)
-                flush<VPT, WARP, VEC>(sum_b, n, at, lanes, p.width, my_sums + 3 * rows_of, add, buf);
+                flush<VPT, false, VEC>(sum_b, n, at, lanes, p.width, my_sums + 3 * rows_of, add, nullptr);
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
@@ -919,29 +918,32 @@ __global__ void __launch_bounds__(THREADS)
                 if constexpr (LAYER) sum_b[i][e] = 0.0f;
             }
     }
-    flush<VPT, WARP, VEC>(dw_pre, n, at, lanes, p.width, my_sums, false, buf);
-    if constexpr (LAYER) flush<VPT, WARP, VEC>(db_pre, n, at, lanes, p.width, my_sums + rows_of, false, buf);
+    flush<VPT, false, VEC>(dw_pre, n, at, lanes, p.width, my_sums, false, nullptr);
+    if constexpr (LAYER) flush<VPT, false, VEC>(db_pre, n, at, lanes, p.width, my_sums + rows_of, false, nullptr);
     if (!p.gate) {
-        flush<VPT, WARP, VEC>(sum_a, n, at, lanes, p.width, my_sums + 2 * rows_of, false, buf);
+        flush<VPT, false, VEC>(sum_a, n, at, lanes, p.width, my_sums + 2 * rows_of, false, nullptr);
         if constexpr (LAYER)
-            flush<VPT, WARP, VEC>(sum_b, n, at, lanes, p.width, my_sums + 3 * rows_of, false, buf);
+            flush<VPT, false, VEC>(sum_b, n, at, lanes, p.width, my_sums + 3 * rows_of, false, nullptr);
     }
 }
 
-// The backward for rows in 16-byte pieces up to kFastWidth columns.  The rows
-// come through a ring of shared-memory stages, filled by bulk copies one or
+// The backward up to kFastWidth columns.  The rows come
+// through a ring of shared-memory stages, filled by bulk copies one or
 // two batches ahead (a batch is a row, or the eight rows of a CTA's warps:
 // consecutive in memory, so four copies), because the column sums leave no
 // registers to hold a row ahead.  8192 x 4096 bf16 with both norms and a gate
 // per sequence: 67 us (6.0 TB/s) and 8 us for the sums' kernel; loads straight
 // into registers took 146.  A stage is read piece by piece as the row
 // needs it, and filled again once every thread is past its last read.
+// VEC: rows in 16-byte pieces.  Others start anywhere: a copy takes the 16-byte
+// pieces around them (cut at the tensor's end, whose last elements are then
+// read from global memory), and a thread's columns are a row's threads apart.
 struct BwdRing {
     int stages;
     uint32_t x_at, dxo_at, h_at, stage_bytes;   // dy at 0
 };
 
-template <typename S, int VPT, bool WARP, bool LAYER, int THREADS, int HAS>
+template <typename S, int VPT, bool WARP, bool VEC, bool LAYER, int THREADS, int HAS>
 __global__ void __launch_bounds__(THREADS)
     norm_bwd_kernel(const __grid_constant__ NormBwd p, const __grid_constant__ BwdRing ring) {
     using row::f2;
@@ -995,16 +997,26 @@ __global__ void __launch_bounds__(THREADS)
         const uint32_t n = static_cast<uint32_t>(min(ahead.end - ahead.r, BATCH)) * static_cast<uint32_t>(p.width);
         uint8_t* to = smem + (issued % ring.stages) * ring.stage_bytes;
         uint64_t* bar = &full[issued % ring.stages];
-        const int64_t first = static_cast<int64_t>(ahead.r) * p.width;
-        const uint32_t bytes = (has_dy ? n * (2 + sizeof(S)) : 0) + (has_dxo ? n * sizeof(S) : 0) + (has_h ? n * 2 : 0);
-        ptx::mbar_arrive_expect_tx(bar, bytes);
+        const int64_t first = static_cast<int64_t>(ahead.r) * p.width, all = p.rows * p.width;
+        // the bytes of n elements of `size` from the first on, in whole pieces
+        auto from = [&](uint32_t size) { return first * size & (VEC ? ~int64_t{0} : ~int64_t{15}); };
+        auto bytes = [&](uint32_t size) -> uint32_t {
+            if (VEC) return n * size;
+            int64_t end = ((first + n) * size + 15) & ~int64_t{15};
+            if (end > all * size) end = all * size & ~int64_t{15};
+            return end > from(size) ? static_cast<uint32_t>(end - from(size)) : 0u;
+        };
+        const uint32_t b2 = bytes(2), bs = bytes(sizeof(S));
+        ptx::mbar_arrive_expect_tx(bar, (has_dy ? b2 + bs : 0) + (has_dxo ? bs : 0) + (has_h ? b2 : 0));
+        auto load = [&](uint32_t at, const void* t, uint32_t size, uint32_t count) {
+            if (count) ptx::bulk_load(to + at, static_cast<const uint8_t*>(t) + from(size), count, bar);
+        };
         if (has_dy) {
-            ptx::bulk_load(to, p.dy + first, n * 2, bar);
-            ptx::bulk_load(to + ring.x_at, static_cast<const S*>(p.x_out) + first, n * sizeof(S), bar);
+            load(0, p.dy, 2, b2);
+            load(ring.x_at, p.x_out, sizeof(S), bs);
         }
-        if (has_dxo)
-            ptx::bulk_load(to + ring.dxo_at, static_cast<const S*>(p.dx_out) + first, n * sizeof(S), bar);
-        if (has_h) ptx::bulk_load(to + ring.h_at, p.h + first, n * 2, bar);
+        if (has_dxo) load(ring.dxo_at, p.dx_out, sizeof(S), bs);
+        if (has_h) load(ring.h_at, p.h, 2, b2);
         ++issued;
         next(ahead);
     };
@@ -1030,31 +1042,72 @@ __global__ void __launch_bounds__(THREADS)
     const float inv_c = 1.0f / static_cast<float>(p.width);
     f2 dw_pre[VPT][4], sum_a[VPT][4];
     f2 db_pre[LAYER ? VPT : 1][4], sum_b[LAYER ? VPT : 1][4];
-    int col[VPT];
+    int col[VPT], len[VPT];
     bool live[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        col[i] = 8 * (at + i * lanes);
-        live[i] = ALL || col[i] < p.width;
+        col[i] = piece_col<VEC>(at, i, lanes);
+        len[i] = ALL && VEC ? 8 : piece_len<VEC>(col[i], lanes, p.width);
+        live[i] = len[i] > 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             dw_pre[i][e] = sum_a[i][e] = 0;
             if constexpr (LAYER) db_pre[i][e] = sum_b[i][e] = 0;
         }
     }
+    // piece i of a vector that every row shares
+    auto vec = [&](f2 (&v)[4], const auto* t, int i) {
+        if constexpr (VEC) {
+            row::shared_pairs(v, t + col[i]);
+        } else {
+            float x[8];
+            load8<false>(x, t + col[i], len[i], lanes);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = row::mk2(x[2 * e], x[2 * e + 1]);
+        }
+    };
+    // piece i of this thread's row of a batch: `part` is the batch's place in
+    // the stage, `in` the row's first element there; elements from `safe` on
+    // were not copied and come from `t`, the batch in global memory
+    auto piece = [&](f2 (&v)[4], const auto* part, const auto* t, int in, int safe, int i) {
+        using T = std::remove_cv_t<std::remove_pointer_t<decltype(part)>>;
+        if constexpr (VEC) {
+            row::Raw8<T> a;
+            a.load_shared(part + in + col[i]);
+            a.pairs(v);
+        } else {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int at_e = in + col[i] + e * lanes;
+                x[e] = e >= len[i] ? 0.0f : static_cast<float>(at_e < safe ? part[at_e] : t[at_e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = row::mk2(x[2 * e], x[2 * e + 1]);
+        }
+    };
+    auto put = [&](auto* t, const f2 (&v)[4], int i) {
+        if constexpr (VEC) {
+            row::store_pairs(t + col[i], v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < len[i]) store1(t + col[i] + e * lanes, e & 1 ? row::hi2(v[e / 2]) : row::lo2(v[e / 2]));
+        }
+    };
     auto out_sums = [&](const f2 (&acc)[VPT][4], float* out, bool add) {
         float v[VPT][8];
         int n[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            n[i] = live[i] ? 8 : 0;
+            n[i] = len[i];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 v[i][2 * e] = row::lo2(acc[i][e]);
                 v[i][2 * e + 1] = row::hi2(acc[i][e]);
             }
         }
-        flush<VPT, WARP, true>(v, n, at, lanes, p.width, out, add, buf);
+        flush<VPT, WARP, VEC>(v, n, at, lanes, p.width, out, add, buf);
     };
     const int64_t rows_of = static_cast<int64_t>(gridDim.x) * p.width;
     float* const my_sums = p.dw_part + static_cast<int64_t>(blockIdx.x) * p.width;
@@ -1068,13 +1121,13 @@ __global__ void __launch_bounds__(THREADS)
                 for (int e = 0; e < 4; ++e) t[i][e] = sum_a[i][e];
                 if (!live[i] || !post) continue;
                 if (has_w_post) {
-                    row::shared_pairs(w, p.w_post + col[i]);
+                    vec(w, p.w_post, i);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) t[i][e] = row::mul2(t[i][e], w[e]);
                 }
                 if constexpr (LAYER) {
                     if (p.b_post) {
-                        row::shared_pairs(w, p.b_post + col[i]);
+                        vec(w, p.b_post, i);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) t[i][e] = row::fma2(sum_b[i][e], w[e], t[i][e]);
                     }
@@ -1086,7 +1139,7 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 if (!live[i]) continue;
-                row::shared_pairs(w, gate + col[i]);
+                vec(w, gate, i);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     sum_a[i][e] = row::mul2(sum_a[i][e], w[e]);
@@ -1137,7 +1190,24 @@ __global__ void __launch_bounds__(THREADS)
             load_stats(then);
             ptx::mbar_wait(&full[stage], phase, &gave_up);
             const uint8_t* st = smem + stage * ring.stage_bytes;
-            const int64_t base = r * p.width, in = static_cast<int64_t>(own) * p.width;
+            const int64_t base = r * p.width;
+            const int in = own * static_cast<int>(p.width);
+            // the batch in the stage and in global memory
+            const int64_t batch = VEC ? 0 : static_cast<int64_t>(now.r) * p.width, all = p.rows * p.width;
+            // elements of the batch before the tensor's last whole 16-byte piece ends
+            auto copied = [&](int64_t piece_len16) {
+                const int64_t n = (all & ~(piece_len16 - 1)) - batch;
+                return n < INT_MAX ? static_cast<int>(n) : INT_MAX;
+            };
+            const int safe2 = VEC ? 0 : copied(8), safes = VEC ? 0 : copied(16 / sizeof(S));
+            const int shift2 = VEC ? 0 : static_cast<int>(batch * 2 & 15);
+            const int shifts = VEC ? 0 : static_cast<int>(batch * sizeof(S) & 15);
+            const auto* s_dy = reinterpret_cast<const __nv_bfloat16*>(st + shift2);
+            const auto* s_x = reinterpret_cast<const S*>(st + ring.x_at + shifts);
+            const auto* s_dxo = reinterpret_cast<const S*>(st + ring.dxo_at + shifts);
+            const auto* s_h = reinterpret_cast<const __nv_bfloat16*>(st + ring.h_at + shift2);
+            const S* g_x = static_cast<const S*>(p.x_out) + batch;
+            const S* g_dxo = static_cast<const S*>(p.dx_out) + batch;
             if (has_row) {
                 f2 d[VPT][4], u[VPT][4];
                 if (has_dy) {
@@ -1148,14 +1218,10 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) d[i][e] = u[i][e] = 0;
                         if (!live[i]) continue;
-                        row::Raw8<__nv_bfloat16> a;
-                        row::Raw8<S> b;
-                        a.load_shared(reinterpret_cast<const __nv_bfloat16*>(st) + in + col[i]);
-                        b.load_shared(reinterpret_cast<const S*>(st + ring.x_at) + in + col[i]);
-                        a.pairs(d[i]);
-                        b.pairs(u[i]);
+                        piece(d[i], s_dy, p.dy + batch, in, safe2, i);
+                        piece(u[i], s_x, g_x, in, safes, i);
                         f2 w[4];
-                        if (has_w_pre) row::shared_pairs(w, p.w_pre + col[i]);
+                        if (has_w_pre) vec(w, p.w_pre, i);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             u[i][e] = LAYER ? row::fma2(u[i][e], rs, mr) : row::mul2(u[i][e], rs);
@@ -1176,9 +1242,7 @@ __global__ void __launch_bounds__(THREADS)
                         if (!live[i]) continue;
                         f2 o[4];
                         if (has_dxo) {
-                            row::Raw8<S> a;
-                            a.load_shared(reinterpret_cast<const S*>(st + ring.dxo_at) + in + col[i]);
-                            a.pairs(o);
+                            piece(o, s_dxo, g_dxo, in, safes, i);
                         } else {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) o[e] = 0;
@@ -1195,9 +1259,7 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) d[i][e] = 0;
                         if (!live[i] || !has_dxo) continue;
-                        row::Raw8<S> a;
-                        a.load_shared(reinterpret_cast<const S*>(st + ring.dxo_at) + in + col[i]);
-                        a.pairs(d[i]);
+                        piece(d[i], s_dxo, g_dxo, in, safes, i);
                     }
                 }
                 // d is dX; u becomes the block's output, normed
@@ -1206,26 +1268,30 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) {
                     if (!live[i]) continue;
+                    if constexpr (!VEC) {   // elements past the row add to no sum
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            d[i][e] = row::mk2(2 * e < len[i] ? row::lo2(d[i][e]) : 0.0f,
+                                               2 * e + 1 < len[i] ? row::hi2(d[i][e]) : 0.0f);
+                    }
                     if (has_dx) {
                         f2 o[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[e] = row::mul2(d[i][e], alpha);
-                        row::store_pairs(static_cast<S*>(p.dx) + base + col[i], o);
+                        put(static_cast<S*>(p.dx) + base, o, i);
                     }
                     if (!has_h) continue;
-                    row::Raw8<__nv_bfloat16> a;
-                    a.load_shared(reinterpret_cast<const __nv_bfloat16*>(st + ring.h_at) + in + col[i]);
-                    a.pairs(u[i]);
+                    piece(u[i], s_h, p.h + batch, in, safe2, i);
                     f2 w[4];
                     if (post) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             u[i][e] = LAYER ? row::fma2(u[i][e], rs, mr) : row::mul2(u[i][e], rs);
-                        if (has_w_post) row::shared_pairs(w, p.w_post + col[i]);
+                        if (has_w_post) vec(w, p.w_post, i);
                     }
                     if (gated) {
                         f2 gt[4];
-                        row::shared_pairs(gt, gate + col[i]);
+                        vec(gt, gate, i);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             sum_a[i][e] = row::fma2(d[i][e], u[i][e], sum_a[i][e]);
@@ -1268,7 +1334,7 @@ __global__ void __launch_bounds__(THREADS)
                                     d[i][e] = row::fma2(d[i][e], scale, t);
                                 }
                             }
-                            row::store_pairs(p.dh + base + col[i], d[i]);
+                            put(p.dh + base, d[i], i);
                         }
                     }
                 }
@@ -1371,11 +1437,11 @@ void launch_sums(NormSums q, int64_t groups, cudaStream_t stream) {
 // for the vectors (14 bytes a column at most), over the CTAs on it.
 constexpr int kRingBytesPerSm = 160 * 1024;
 
-template <typename S, int VPT, bool WARP, bool LAYER, int THREADS, int HAS>
+template <typename S, int VPT, bool WARP, bool VEC, bool LAYER, int THREADS, int HAS>
 int launch_bwd_ring(const NormBwd& p, const BwdPlan& b, cudaStream_t st) {
     BwdRing ring;
     const uint32_t n = static_cast<uint32_t>(p.width * (WARP ? 8 : 1));
-    auto up = [](uint32_t v) { return (v + 127) / 128 * 128; };
+    auto up = [](uint32_t v) { return (v + (VEC ? 0 : 32) + 127) / 128 * 128; };
     ring.x_at = up(n * 2);
     ring.dxo_at = ring.x_at + up(n * sizeof(S));
     ring.h_at = ring.dxo_at + up(n * sizeof(S));
@@ -1385,7 +1451,7 @@ int launch_bwd_ring(const NormBwd& p, const BwdPlan& b, cudaStream_t st) {
     if (ring.stages > 4) ring.stages = 4;
     if (ring.stages < 2) ring.stages = 2;
     const uint32_t bytes = ring.stages * ring.stage_bytes;
-    auto k = norm_bwd_kernel<S, VPT, WARP, LAYER, THREADS, HAS>;
+    auto k = norm_bwd_kernel<S, VPT, WARP, VEC, LAYER, THREADS, HAS>;
     // per device and instance; setting it again is harmless
     static std::atomic<uint32_t> allowed[64] = {};
     int dev = 0;
@@ -1405,31 +1471,30 @@ int launch_bwd_ring(const NormBwd& p, const BwdPlan& b, cudaStream_t st) {
     return FP8_OK;
 }
 
+template <typename S, bool LAYER, bool VEC>
+int launch_bwd_resident(const NormBwd& p, const BwdPlan& b, cudaStream_t st) {
+    if (b.warp && b.vpt == 1) return launch_bwd_ring<S, 1, true, VEC, LAYER, 256, 0>(p, b, st);
+    if (b.warp) return launch_bwd_ring<S, 2, true, VEC, LAYER, 256, 0>(p, b, st);
+    if (p.dy && p.x_out && p.dx_out && p.h && p.dx && p.dh && p.w_pre && (!p.post || p.w_post) &&
+        (!VEC || p.width == 16 * b.threads)) {
+        constexpr int A = kHasAll, P = kHasPost, G = kHasGate;
+        if (p.post && p.gate) return launch_bwd_ring<S, 2, false, VEC, LAYER, 512, A | P | G>(p, b, st);
+        if (!p.post && !p.gate) return launch_bwd_ring<S, 2, false, VEC, LAYER, 512, A>(p, b, st);
+        if constexpr (VEC)
+            return p.post ? launch_bwd_ring<S, 2, false, true, LAYER, 512, A | P>(p, b, st)
+                          : launch_bwd_ring<S, 2, false, true, LAYER, 512, A | G>(p, b, st);
+    }
+    return launch_bwd_ring<S, 2, false, VEC, LAYER, 512, 0>(p, b, st);
+}
+
 template <typename S, bool LAYER>
 int launch_bwd(const NormBwd& p, const BwdPlan& b, cudaStream_t st) {
+    const bool vec = p.width % 8 == 0;
+    if (p.width <= kFastWidth)
+        return vec ? launch_bwd_resident<S, LAYER, true>(p, b, st) : launch_bwd_resident<S, LAYER, false>(p, b, st);
     const dim3 grid(b.ctas), block(b.threads);
-    if (p.width % 8 == 0 && p.width <= kFastWidth) {
-        if (b.warp && b.vpt == 1) return launch_bwd_ring<S, 1, true, LAYER, 256, 0>(p, b, st);
-        if (b.warp) return launch_bwd_ring<S, 2, true, LAYER, 256, 0>(p, b, st);
-        if (p.dy && p.x_out && p.dx_out && p.h && p.dx && p.dh && p.w_pre && (!p.post || p.w_post) &&
-            p.width == 16 * b.threads) {
-            constexpr int A = kHasAll, P = kHasPost, G = kHasGate;
-            if (p.post)
-                return p.gate ? launch_bwd_ring<S, 2, false, LAYER, 512, A | P | G>(p, b, st)
-                              : launch_bwd_ring<S, 2, false, LAYER, 512, A | P>(p, b, st);
-            return p.gate ? launch_bwd_ring<S, 2, false, LAYER, 512, A | G>(p, b, st)
-                          : launch_bwd_ring<S, 2, false, LAYER, 512, A>(p, b, st);
-        }
-        return launch_bwd_ring<S, 2, false, LAYER, 512, 0>(p, b, st);
-    }
-    if (p.width % 8 == 0)
-        launch_pdl(norm_bwd_any_kernel<S, 2, false, true, LAYER, 1024>, grid, block, 0, st, p);
-    else if (b.warp)
-        launch_pdl(norm_bwd_any_kernel<S, 2, true, false, LAYER, 256>, grid, block, 0, st, p);
-    else if (b.threads <= 512)
-        launch_pdl(norm_bwd_any_kernel<S, 2, false, false, LAYER, 512>, grid, block, 0, st, p);
-    else
-        launch_pdl(norm_bwd_any_kernel<S, 2, false, false, LAYER, 1024>, grid, block, 0, st, p);
+    if (vec) launch_pdl(norm_bwd_any_kernel<S, true, LAYER>, grid, block, 0, st, p);
+    else launch_pdl(norm_bwd_any_kernel<S, false, LAYER>, grid, block, 0, st, p);
     return FP8_OK;
 }
 
