@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kRowThreads)
 // memory and each lane sends it to one of the slots' rows; no register or
 // load unit touches the data.  Two slots a warp: one filled while the other
 // is sent (8192 tokens to 8 of 64 experts, rows of 8 KB: 117 us with two, 122
-// with three or four).  The copies run at 5.3 TB/s, a write of one stream of
+// with three or four).  The copies run at 5.8 TB/s, a write of one stream of
 // the same size at 7.5: the scattered rows are the bound, not the copy engine
 // (through registers they took 10% longer).
 constexpr int kBulkSlots = 2;
