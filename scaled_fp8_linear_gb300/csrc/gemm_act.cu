@@ -30,6 +30,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/fp8linear.h"
+#include "hostops.h"
 #include "internal.h"
 #include "ptx.cuh"
 #include "rowops.cuh"
@@ -973,13 +974,6 @@ void launch_act_bwd(const ActBwd& p, bool gated, unsigned ctas, cudaStream_t st)
 
 // ------------------------------------------------------------------ host side
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
-
-int launch_status(const char* what) {
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? FP8_OK : set_error(FP8_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
 
 // The kernel's dynamic shared memory allowed once per device, and how many of
 // its clusters (or CTAs) run at once.
@@ -1041,7 +1035,7 @@ int launch_pair(const fp8_gemm_act_args_t* a, ActParams& p, const OutMaps& maps,
     const int64_t tiles = most_tiles(a, kPairTile, TN);
     const unsigned grid = 2 * static_cast<unsigned>(tiles < clusters ? tiles : clusters);
     launch_pdl(k, dim3(grid), dim3(kThreads), kPairSmem, st, tmA, tmB, maps, p);
-    return launch_status("fp8_gemm_act");
+    return host::launch_status("fp8_gemm_act");
 }
 
 template <int BN, bool GATED>
@@ -1061,7 +1055,7 @@ int launch_tile(const fp8_gemm_act_args_t* a, ActParams& p, const OutMaps& maps,
                                                : most_tiles(a, kHalf, TN);
     const unsigned grid = static_cast<unsigned>(tiles < ctas ? tiles : ctas);
     launch_pdl(k, dim3(grid), dim3(kThreads), SMEM, st, tmA, tmB, maps, p);
-    return launch_status("fp8_gemm_act");
+    return host::launch_status("fp8_gemm_act");
 }
 
 template <bool GATED>
@@ -1116,6 +1110,7 @@ int launch_gemm_act(const fp8_gemm_act_args_t* a, ActParams& p, const OutMaps& m
 }  // namespace fp8
 
 using namespace fp8;
+using namespace fp8::host;
 
 extern "C" {
 

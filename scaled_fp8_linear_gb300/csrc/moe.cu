@@ -9,12 +9,12 @@
 // All of them move rows: the bound is HBM.  The copies go token by token, so
 // that a token's row is read once for its k copies, and every sum runs in a
 // fixed order, so that equal calls give equal bits.
-#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "../../include/fp8linear.h"
+#include "hostops.h"
 #include "internal.h"
 #include "ptx.cuh"
 #include "rowops.cuh"
@@ -698,13 +698,6 @@ __global__ void __launch_bounds__(kRowThreads)
 
 // ------------------------------------------------------------------ host side
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
-
-int launch_status(const char* what) {
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? FP8_OK : set_error(FP8_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
 
 int check_routing(const char* what, int64_t tokens, int slots, int64_t rows) {
     if (tokens < 0 || slots < 1 || slots > kMaxSlots || rows < 0)
@@ -751,16 +744,9 @@ int launch_permute_bulk(const void* x, const float* scale, int64_t tokens, int s
     p.pieces = static_cast<int>((row_bytes + p.slot_bytes - 1) / p.slot_bytes);
     int warps = (kBulkSmem - p.slot_bytes) / (kBulkSlots * p.slot_bytes);
     if (warps > 8) warps = 8;
-    static std::atomic<bool> allowed[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
-    if (dev < 0 || dev >= 64 || !allowed[dev].load(std::memory_order_relaxed)) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            moe_permute_bulk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBulkSmem);
-        if (e != cudaSuccess)
-            return set_error(FP8_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-        if (dev >= 0 && dev < 64) allowed[dev].store(true, std::memory_order_relaxed);
-    }
+    static host::SmemAllowance allowed;
+    const int r = host::allow_smem(moe_permute_bulk_kernel, kBulkSmem, allowed);
+    if (r != FP8_OK) return r;
     const int smem = (warps * kBulkSlots + 1) * p.slot_bytes;
     // small rows leave room for more CTAs on an SM
     int per_sm = kBulkSmem / smem;
@@ -808,6 +794,7 @@ void launch_unpermute_bwd(const void* dy, const void* ys, const int32_t* row_of,
 }  // namespace fp8
 
 using namespace fp8;
+using namespace fp8::host;
 
 extern "C" {
 

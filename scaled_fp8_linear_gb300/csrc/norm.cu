@@ -12,7 +12,6 @@
 // and the stores is fp32: y comes from the unrounded x', and each output is
 // rounded once.  The variance is the mean of squared distances from the mean
 // (a second reduction over the registers), which does not cancel.
-#include <atomic>
 #include <cfloat>
 #include <climits>
 #include <cstdint>
@@ -21,6 +20,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/fp8linear.h"
+#include "hostops.h"
 #include "internal.h"
 #include "ptx.cuh"
 #include "rowops.cuh"
@@ -1452,31 +1452,26 @@ int launch_bwd_ring(const NormBwd& p, const BwdPlan& b, cudaStream_t st) {
     if (ring.stages < 2) ring.stages = 2;
     const uint32_t bytes = ring.stages * ring.stage_bytes;
     auto k = norm_bwd_kernel<S, VPT, WARP, VEC, LAYER, THREADS, HAS>;
-    // per device and instance; setting it again is harmless
-    static std::atomic<uint32_t> allowed[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
-    if (dev < 0 || dev >= 64 || allowed[dev].load(std::memory_order_relaxed) < bytes) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(bytes));
-        if (e != cudaSuccess)
-            return set_error(FP8_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-        if (dev >= 0 && dev < 64) {
-            uint32_t was = allowed[dev].load(std::memory_order_relaxed);
-            while (was < bytes && !allowed[dev].compare_exchange_weak(was, bytes)) {
-            }
-        }
-    }
+    static host::SmemAllowance allowed;   // of this instance
+    const int r = host::allow_smem(k, static_cast<int>(bytes), allowed);
+    if (r != FP8_OK) return r;
     launch_pdl(k, dim3(b.ctas), dim3(b.threads), bytes, st, p, ring);
     return FP8_OK;
 }
 
 template <typename S, bool LAYER, bool VEC>
 int launch_bwd_resident(const NormBwd& p, const BwdPlan& b, cudaStream_t st) {
-    if (b.warp && b.vpt == 1) return launch_bwd_ring<S, 1, true, VEC, LAYER, 256, 0>(p, b, st);
-    if (b.warp) return launch_bwd_ring<S, 2, true, VEC, LAYER, 256, 0>(p, b, st);
-    if (p.dy && p.x_out && p.dx_out && p.h && p.dx && p.dh && p.w_pre && (!p.post || p.w_post) &&
-        (!VEC || p.width == 16 * b.threads)) {
+    const bool all = p.dy && p.x_out && p.dx_out && p.h && p.dx && p.dh && p.w_pre && (!p.post || p.w_post);
+    if (b.warp) {
+        if constexpr (VEC) {
+            if (all && !p.post && !p.gate && p.width == 256 * b.vpt)
+                return b.vpt == 1 ? launch_bwd_ring<S, 1, true, true, LAYER, 256, kHasAll>(p, b, st)
+                                  : launch_bwd_ring<S, 2, true, true, LAYER, 256, kHasAll>(p, b, st);
+        }
+        return b.vpt == 1 ? launch_bwd_ring<S, 1, true, VEC, LAYER, 256, 0>(p, b, st)
+                          : launch_bwd_ring<S, 2, true, VEC, LAYER, 256, 0>(p, b, st);
+    }
+    if (all && (!VEC || p.width == 16 * b.threads)) {
         constexpr int A = kHasAll, P = kHasPost, G = kHasGate;
         if (p.post && p.gate) return launch_bwd_ring<S, 2, false, VEC, LAYER, 512, A | P | G>(p, b, st);
         if (!p.post && !p.gate) return launch_bwd_ring<S, 2, false, VEC, LAYER, 512, A>(p, b, st);
@@ -1515,13 +1510,6 @@ namespace {
 
 // ------------------------------------------------------------------ host side
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
-
-int launch_status(const char* what) {
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? FP8_OK : set_error(FP8_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
 
 int check_shape(const char* what, int64_t rows, int64_t width, const void* gate, int64_t gate_rows,
                 int kind, int type) {
@@ -1543,6 +1531,7 @@ int check_shape(const char* what, int64_t rows, int64_t width, const void* gate,
 }  // namespace fp8
 
 using namespace fp8;
+using namespace fp8::host;
 
 extern "C" {
 
