@@ -22,13 +22,14 @@
 namespace fp8 {
 namespace {
 
-constexpr int kPlanThreads = 256, kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32;
 constexpr int kMaxExperts = 1024, kMaxSlots = 64;
 constexpr int64_t kMost = int64_t{1} << 30;   // pairs and rows: 32-bit numbers and grids
-// One CTA ranks up to this many pairs: past it the per-CTA histograms of a
-// first launch cost less than the walk of one CTA over all pairs.
+// One CTA ranks up to this many pairs; past it the per-CTA histograms of a first
+// launch cost less than the walk of one CTA over all of them (4000 pairs, 256
+// experts: 13 us by one CTA, 6 by two launches; 32 pairs: 3.3 us by one CTA).
 constexpr int kPlanOneCta = 2048;
-constexpr int kPlanChunk = 1024;   // pairs a CTA at least
+constexpr int kPlanChunk = 512;    // pairs a CTA at least: one look of 32 a warp
 constexpr int kPlanMaxCtas = 128;  // so that summing the CTAs' histograms stays short
 
 struct PlanGrid {
@@ -74,18 +75,20 @@ __global__ void __launch_bounds__(kPlanThreads)
 // expert find one another with a match), the counts become starting rows by
 // a sum over the CTAs and warps before it, and a second walk hands the rows
 // out in order.  Every CTA sums all CTAs' histograms itself (ctas x experts
-// words from L2), which saves a launch.
+// words from L2), which saves a launch.  65536 pairs to 64 experts: 7.6 us with
+// the histograms' launch.
 __global__ void __launch_bounds__(kPlanThreads)
     moe_place_kernel(const int32_t* __restrict__ ids, int n, int experts, int align, int chunk,
                      const int32_t* __restrict__ hist, int32_t* __restrict__ offsets,
                      int32_t* __restrict__ counts, int32_t* __restrict__ row_of,
                      int32_t* __restrict__ src, int rows) {
     ptx::griddep_launch_dependents();
-    __shared__ int cnt[kPlanWarps][kMaxExperts];   // counts, then next rows
+    extern __shared__ int counters[];   // [warps][experts]: counts, then next rows
     __shared__ int total[kMaxExperts + 1], start[kMaxExperts + 1];
     __shared__ int warp_tot[kPlanWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int e = lane; e < experts; e += 32) cnt[warp][e] = 0;
+    auto cnt = [&](int w, int e) -> int& { return counters[w * experts + e]; };
+    for (int e = lane; e < experts; e += 32) cnt(warp, e) = 0;
     __syncwarp();
     ptx::griddep_wait();
     const int per_warp = (chunk + kPlanWarps * 32 - 1) / (kPlanWarps * 32) * 32;
@@ -111,7 +114,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         for (int k = 0; k < kAhead; ++k) {
             if (i + 32 * k >= end) break;
             const uint32_t same = __match_any_sync(row::kAll, e[k]);
-            if (e[k] >= 0 && (same & below) == 0) cnt[warp][e[k]] += __popc(same);
+            if (e[k] >= 0 && (same & below) == 0) cnt(warp, e[k]) += __popc(same);
             __syncwarp();
         }
     }
@@ -121,7 +124,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     for (int x = threadIdx.x; x < experts; x += kPlanThreads) {
         int own = 0;
 #pragma unroll
-        for (int w = 0; w < kPlanWarps; ++w) own += cnt[w][x];
+        for (int w = 0; w < kPlanWarps; ++w) own += cnt(w, x);
         total[x] = hist ? 0 : own;
         start[x] = 0;
     }
@@ -175,8 +178,8 @@ __global__ void __launch_bounds__(kPlanThreads)
                 for (int r = run + total[x]; r < run + pad[i]; ++r) src[r] = -1;
             int next = run + start[x];
             for (int w = 0; w < kPlanWarps; ++w) {
-                const int c = cnt[w][x];
-                cnt[w][x] = next;
+                const int c = cnt(w, x);
+                cnt(w, x) = next;
                 next += c;
             }
         }
@@ -198,9 +201,9 @@ __global__ void __launch_bounds__(kPlanThreads)
             if (i + 32 * k >= end) break;
             const uint32_t same = __match_any_sync(row::kAll, e[k]);
             int r = -1;
-            if (e[k] >= 0) r = cnt[warp][e[k]] + __popc(same & below);
+            if (e[k] >= 0) r = cnt(warp, e[k]) + __popc(same & below);
             __syncwarp();
-            if (e[k] >= 0 && (same & below) == 0) cnt[warp][e[k]] += __popc(same);
+            if (e[k] >= 0 && (same & below) == 0) cnt(warp, e[k]) += __popc(same);
             __syncwarp();
             if (at < end) {
                 row_of[at] = r;
@@ -842,7 +845,11 @@ int fp8_moe_plan(const int32_t* ids, int64_t tokens, int slots, int experts, int
         launch_pdl(moe_hist_kernel, dim3(g.ctas), dim3(kPlanThreads), 0, as_stream(stream), ids, n,
                    experts, g.chunk, hist);
     }
-    launch_pdl(moe_place_kernel, dim3(g.ctas), dim3(kPlanThreads), 0, as_stream(stream), ids, n,
+    static host::SmemAllowance allowed;
+    const int smem = kPlanWarps * experts * static_cast<int>(sizeof(int));
+    const int r = smem > 32768 ? host::allow_smem(moe_place_kernel, smem, allowed) : FP8_OK;
+    if (r != FP8_OK) return r;
+    launch_pdl(moe_place_kernel, dim3(g.ctas), dim3(kPlanThreads), smem, as_stream(stream), ids, n,
                experts, align, g.chunk, static_cast<const int32_t*>(hist), offsets, counts, row_of,
                src, static_cast<int>(rows));
     return launch_status("fp8_moe_plan");
