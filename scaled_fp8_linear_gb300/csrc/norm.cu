@@ -549,17 +549,16 @@ __global__ void __launch_bounds__(THREADS)
             }
         }
         if (!p.q_rows) s = p.q_scale[0];
+        const f2 ss = row::all2(s);
+        // the format is tested once: a test a pair would convert to both
+        auto codes = [&](auto fmt) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if (!live[i]) continue;
-            float t[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                t[2 * e] = row::lo2(v[i][e]);
-                t[2 * e + 1] = row::hi2(v[i][e]);
-            }
-            *reinterpret_cast<uint2*>(p.q + base + col[i]) = row::cvt8(p.q_fmt, t, s);
-        }
+            for (int i = 0; i < VPT; ++i)
+                if (live[i])
+                    *reinterpret_cast<uint2*>(p.q + base + col[i]) = row::cvt8<decltype(fmt)::value>(v[i], ss);
+        };
+        if (p.q_fmt == FP8_E4M3) codes(std::integral_constant<int, 0>{});
+        else codes(std::integral_constant<int, 1>{});
     }
 }
 

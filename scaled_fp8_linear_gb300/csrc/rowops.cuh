@@ -139,11 +139,28 @@ __device__ __forceinline__ uint32_t cvt_pair(int fmt, float lo, float hi) {
     return fmt == 0 ? cvt_pair<0>(lo, hi) : cvt_pair<1>(lo, hi);
 }
 
-__device__ __forceinline__ uint2 cvt8(int fmt, const float (&v)[8], float s) {
+template <int FMT>
+__device__ __forceinline__ uint2 cvt8(const float (&v)[8], float s) {
     uint32_t c[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-        c[e] = cvt_pair(fmt, __fmul_rn(v[2 * e], s), __fmul_rn(v[2 * e + 1], s));
+        c[e] = cvt_pair<FMT>(__fmul_rn(v[2 * e], s), __fmul_rn(v[2 * e + 1], s));
+    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+__device__ __forceinline__ uint2 cvt8(int fmt, const float (&v)[8], float s) {
+    return fmt == 0 ? cvt8<0>(v, s) : cvt8<1>(v, s);
+}
+
+// Codes of eight pairs-packed values.
+template <int FMT>
+__device__ __forceinline__ uint2 cvt8(const f2 (&v)[4], f2 s) {
+    uint32_t c[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const f2 t = mul2(v[e], s);
+        c[e] = cvt_pair<FMT>(lo2(t), hi2(t));
+    }
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
