@@ -56,6 +56,18 @@ def test_activation_gradient_against_differences(act):
 
 
 
+@pytest.mark.parametrize("args", [B.NormFwdArgsC, B.NormBwdArgsC, B.GemmActArgsC, B.ActBwdArgsC])
+def test_packed_arguments_have_the_struct_layout(args):
+    """Each field lands where the C struct has it."""
+    pack = B._packer(args)
+    for i, (name, kind) in enumerate(args._fields_):
+        values = [0] * len(args._fields_)
+        values[i] = 1.5 if kind is ctypes.c_float else 77
+        got = args.from_buffer_copy(pack(*values).ljust(ctypes.sizeof(args), b"\0"))
+        for j, (other, _) in enumerate(args._fields_):
+            assert (getattr(got, other) or 0) == values[j], (name, other)
+
+
 def test_norm_refusals():
     L = B._lib()
     p = FAKE

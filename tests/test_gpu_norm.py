@@ -189,3 +189,24 @@ def test_another_stream_and_a_graph():
     x.mul_(2)
     graph.replay()
     assert torch.equal(y2, F.fp8_norm_fwd(x, h, w_pre=w2).y)
+
+
+def test_binding_refusals_of_tensors():
+    """Strided, misaligned and host tensors, and other types, before a launch."""
+    x = torch.randn(64, 64, device=DEV).to(BF)
+    with pytest.raises(ValueError, match="contiguous"):
+        F.fp8_norm_fwd(x.t())
+    with pytest.raises(ValueError, match="CUDA"):
+        F.fp8_norm_fwd(x, x.cpu())
+    with pytest.raises(TypeError):
+        F.fp8_norm_fwd(x, w_pre=torch.ones(64, device=DEV, dtype=BF))
+    with pytest.raises(ValueError, match="shape"):
+        F.fp8_norm_fwd(x, w_pre=torch.ones(65, device=DEV))
+    with pytest.raises(F.Fp8Error) as e:
+        F.fp8_norm_fwd(x.view(-1)[4:4 + 63 * 64].view(63, 64))
+    assert e.value.status == -3
+    ids = torch.zeros(4, 2, device=DEV, dtype=torch.int64)
+    with pytest.raises(TypeError):
+        F.fp8_moe_plan(ids, 4)
+    with pytest.raises(TypeError):
+        F.fp8_gemm_act(x, 0, x, 0, torch.ones(1, device=DEV), torch.ones(1, device=DEV))
