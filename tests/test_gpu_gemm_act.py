@@ -125,6 +125,37 @@ def test_remainder_beside_pairs():
         _case(M, N, K, F.ACT_SILU, False, True, True, F.GRAN_ROW, 0, F.E4M3, seed=M)
 
 
+def test_remainder_is_ordered():
+    """Between a cast that writes its operand and a norm that reads its result,
+    back to back and from a graph: the same bits as with a wait between them."""
+    g = torch.Generator(device=DEV).manual_seed(7)
+    M, N, K = 600, 8192, 512
+    xs = [torch.randn(M, K, generator=g, device=DEV).to(BF) for _ in range(8)]
+    w = torch.randint(0, 0x70, (N, K), generator=g, device=DEV, dtype=torch.uint8)
+    one, inv = torch.ones(1, device=DEV), torch.full((1,), 2.0 ** -8, device=DEV)
+    q = torch.empty(M, K, dtype=torch.uint8, device=DEV)
+
+    def chain(x, wait=lambda: None):
+        F.fp8_quantize(x, F.E4M3, scale=one, q=q)
+        wait()
+        d = F.fp8_gemm_act(q, F.E4M3, w, F.E4M3, one, inv, act=F.ACT_SILU).d
+        wait()
+        return d, F.fp8_norm_fwd(d, want_x_out=False).y
+
+    want = [chain(x, torch.cuda.synchronize) for x in xs]
+    for _ in range(4):
+        got = [chain(x) for x in xs]
+        assert all(torch.equal(a, b) for p, r in zip(got, want) for a, b in zip(p, r))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [chain(x) for x in xs]
+    for _ in range(4):
+        for p in got:
+            p[0].zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for p, r in zip(got, want) for a, b in zip(p, r))
+
+
 def test_residual_in_place():
     g = torch.Generator().manual_seed(3)
     a, b = _codes(g, 700, 256).view(torch.uint8).to(DEV), _codes(g, 512, 256).view(torch.uint8).to(DEV)
@@ -218,3 +249,20 @@ def test_gradient(M, N, act, gated):
     more = o.dbias.clone()
     F.fp8_act_bwd(d.to(DEV), z.to(DEV), act, gated=gated, dbias=more, accumulate=True, want_dz=False)
     R.check(more, 2 * want.sum(0), 2 * mag.sum(0), "dbias added")
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements of D and z: the last rows equal the same rows alone."""
+    M, N, K = (1 << 18) + 40, 8192, 32
+    g = torch.Generator(device=DEV).manual_seed(1)
+    code = lambda *s: torch.randint(0, 0x70, s, generator=g, device=DEV, dtype=torch.uint8)
+    a, b = code(M, K), code(N, K)
+    sa, sb = torch.rand(M, device=DEV) * 2 ** -9, torch.rand(N, device=DEV)
+    res = torch.empty(M, N, dtype=BF, device=DEV)
+    res.normal_(generator=g)
+    run = lambda a, sa, res: F.fp8_gemm_act(a, F.E4M3, b, F.E4M3, sa, sb, ga=F.GRAN_ROW, gb=F.GRAN_ROW,
+                                            act=F.ACT_SILU, residual=res, want_z=True)
+    o, t = run(a, sa, res), run(a[-40:].contiguous(), sa[-40:].contiguous(), res[-40:].contiguous())
+    assert torch.equal(o.d[-40:], t.d) and torch.equal(o.z[-40:], t.z)
+    q = F.fp8_act_bwd(res, o.z, F.ACT_SILU).dz[-40:]
+    assert torch.equal(q, F.fp8_act_bwd(res[-40:].contiguous(), t.z, F.ACT_SILU).dz)

@@ -210,3 +210,20 @@ def test_binding_refusals_of_tensors():
         F.fp8_moe_plan(ids, 4)
     with pytest.raises(TypeError):
         F.fp8_gemm_act(x, 0, x, 0, torch.ones(1, device=DEV), torch.ones(1, device=DEV))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last rows equal the same rows alone."""
+    T, C = (1 << 18) + 5, 8192
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.empty(T, C, dtype=BF, device=DEV)
+    x.normal_(generator=g)
+    w = 1 + 0.1 * torch.randn(C, device=DEV)
+    f = F.fp8_norm_fwd(x, x, w_pre=w, want_stats=True)
+    tail = x[-7:].contiguous()
+    ft = F.fp8_norm_fwd(tail, tail, w_pre=w, want_stats=True)
+    assert torch.equal(f.y[-7:], ft.y) and torch.equal(f.x_out[-7:], ft.x_out)
+    assert torch.equal(f.stats[:, -7:], ft.stats)
+    b = F.fp8_norm_bwd(f.y, f.x_out, f.stats, dx_out=x, h=x, w_pre=w)
+    bt = F.fp8_norm_bwd(ft.y, ft.x_out, ft.stats, dx_out=tail, h=tail, w_pre=w)
+    assert torch.equal(b.dx[-7:], bt.dx) and torch.equal(b.dh[-7:], bt.dh)
