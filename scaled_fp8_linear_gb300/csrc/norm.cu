@@ -703,8 +703,17 @@ __device__ __forceinline__ void flush(const float (&acc)[VPT][8], const int (&n)
         for (int i = 0; i < VPT; ++i) {
             if (n[i] <= 0) continue;
             float* o = out + piece_col<VEC>(at, i, lanes);
-            if (add) {
-                for (int e = 0; e < n[i]; ++e) o[e * step] += acc[i][e];
+            if (VEC && add) {
+                float4* q = reinterpret_cast<float4*>(o);
+                float4 a = q[0], b = q[1];
+                a.x += acc[i][0]; a.y += acc[i][1]; a.z += acc[i][2]; a.w += acc[i][3];
+                b.x += acc[i][4]; b.y += acc[i][5]; b.z += acc[i][6]; b.w += acc[i][7];
+                q[0] = a;
+                q[1] = b;
+            } else if (add) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e < n[i]) o[e * step] += acc[i][e];
             } else {
                 store8<VEC>(o, acc[i], n[i], lanes);
             }
@@ -940,6 +949,7 @@ __global__ void __launch_bounds__(1024)
 struct BwdRing {
     int stages;
     uint32_t x_at, dxo_at, h_at, stage_bytes;   // dy at 0
+    uint32_t sums_at;   // the post norm's running sums behind the stages, or 0: in dw_part
 };
 
 template <typename S, int VPT, bool WARP, bool VEC, bool LAYER, int THREADS, int HAS>
@@ -1110,6 +1120,10 @@ __global__ void __launch_bounds__(THREADS)
     };
     const int64_t rows_of = static_cast<int64_t>(gridDim.x) * p.width;
     float* const my_sums = p.dw_part + static_cast<int64_t>(blockIdx.x) * p.width;
+    // where the chunks' shares of the post norm's sums meet: a CTA with many
+    // chunks (a gate per token) adds them up in shared memory
+    float* const post_w = ring.sums_at ? reinterpret_cast<float*>(smem + ring.sums_at) : my_sums + 2 * rows_of;
+    float* const post_b = ring.sums_at ? post_w + p.width : my_sums + 3 * rows_of;
     // the end of a chunk: its part of dgate, and of the post norm's sums
     auto end_chunk = [&](const __nv_bfloat16* gate, int64_t k, bool first) {
         f2 t[VPT][4], w[4];
@@ -1145,8 +1159,8 @@ __global__ void __launch_bounds__(THREADS)
                     if constexpr (LAYER) sum_b[i][e] = row::mul2(sum_b[i][e], w[e]);
                 }
             }
-            out_sums(sum_a, my_sums + 2 * rows_of, !first);
-            if constexpr (LAYER) out_sums(sum_b, my_sums + 3 * rows_of, !first);
+            out_sums(sum_a, post_w, !first);
+            if constexpr (LAYER) out_sums(sum_b, post_b, !first);
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
@@ -1347,6 +1361,13 @@ __global__ void __launch_bounds__(THREADS)
     }
     out_sums(dw_pre, my_sums, false);
     if constexpr (LAYER) out_sums(db_pre, my_sums + rows_of, false);
+    if (gated && post && ring.sums_at) {
+        __syncthreads();
+        for (int64_t c = threadIdx.x; c < p.width; c += blockDim.x) {
+            my_sums[2 * rows_of + c] = post_w[c];
+            if constexpr (LAYER) my_sums[3 * rows_of + c] = post_b[c];
+        }
+    }
     if (!gated) {
         out_sums(sum_a, my_sums + 2 * rows_of, false);
         if constexpr (LAYER) out_sums(sum_b, my_sums + 3 * rows_of, false);
@@ -1435,6 +1456,7 @@ void launch_sums(NormSums q, int64_t groups, cudaStream_t stream) {
 // Shared memory for the ring of one CTA: what an SM has, less what L1 needs
 // for the vectors (14 bytes a column at most), over the CTAs on it.
 constexpr int kRingBytesPerSm = 160 * 1024;
+constexpr uint32_t kRingMost = 208 * 1024;   // of one CTA, beside its static shared memory
 
 template <typename S, int VPT, bool WARP, bool VEC, bool LAYER, int THREADS, int HAS>
 int launch_bwd_ring(const NormBwd& p, const BwdPlan& b, cudaStream_t st) {
@@ -1449,7 +1471,13 @@ int launch_bwd_ring(const NormBwd& p, const BwdPlan& b, cudaStream_t st) {
     ring.stages = static_cast<int>(room / ring.stage_bytes);
     if (ring.stages > 4) ring.stages = 4;
     if (ring.stages < 2) ring.stages = 2;
-    const uint32_t bytes = ring.stages * ring.stage_bytes;
+    uint32_t bytes = ring.stages * ring.stage_bytes;
+    ring.sums_at = 0;
+    const uint32_t sums = static_cast<uint32_t>(p.width) * (LAYER ? 8 : 4);
+    if (p.gate && p.post && b.groups * b.parts > b.ctas && bytes + sums <= kRingMost) {
+        ring.sums_at = bytes;
+        bytes += sums;
+    }
     auto k = norm_bwd_kernel<S, VPT, WARP, VEC, LAYER, THREADS, HAS>;
     static host::SmemAllowance allowed;   // of this instance
     const int r = host::allow_smem(k, static_cast<int>(bytes), allowed);

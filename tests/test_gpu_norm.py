@@ -125,7 +125,8 @@ def test_no_rows():
 @pytest.mark.parametrize("kind", [F.NORM_RMS, F.NORM_LAYER])
 @pytest.mark.parametrize("stream", [BF, torch.float32])
 @pytest.mark.parametrize("T,C,G", SHAPES + [(700, 128, 1), (641, 512, 641), (400, 2048, 4), (512, 640, 128),
-                                            (200, 3, 100), (67, 1, 67), (1000, 13, 4), (333, 333, 3), (90, 4001, 30)])
+                                            (200, 3, 100), (67, 1, 67), (1000, 13, 4), (333, 333, 3), (90, 4001, 30),
+                                            (640, 4096, 640), (320, 8192, 160), (320, 4097, 320)])
 def test_backward(T, C, G, stream, kind):
     x, h, gate, w1, b1, w2, b2 = _inputs(T, C, kind, stream, G, seed=1)
     g = _g(9)
