@@ -616,10 +616,12 @@ __global__ void __launch_bounds__(kRowThreads)
 
 // The same for rows that the CTA's registers hold (VPT pieces a thread): dy is
 // read once, and the next slot's piece of ys is loaded while this one's is
-// used.  8191 tokens' 8 rows of 14 KB: 371 us (5.7 TB/s; 446 reading dy again
-// for each slot, most of it from HBM).
+// used.  8191 tokens' 8 rows of 14 KB: 364 us (5.8 TB/s; 446 reading dy again
+// for each slot, most of it from HBM).  Two and four pieces are held to 64
+// registers, for four CTAs an SM (373 us with three), one piece to 32, for
+// eight (8192 tokens' 8 rows of 2 KB: 52 us, 62 with five).
 template <typename T, int N, int VPT>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, VPT == 1 ? 8 : 4)
     moe_unpermute_bwd_held_kernel(const T* __restrict__ dy, const T* __restrict__ ys,
                                   const int32_t* __restrict__ row_of, const int32_t* __restrict__ src,
                                   const float* __restrict__ w, int64_t tokens, int slots,
