@@ -158,10 +158,13 @@ __device__ __forceinline__ void act_and_grad2(f2 z, f2& a, f2& g) {
         a = row::mul2(z, cdf);
         g = row::fma2(row::mul2(z, row::all2(kInvSqrt2Pi)), e, cdf);
     } else if constexpr (ACT == FP8_ACT_GELU_TANH) {
+        // s + z s (1 - s) u', u' = 2 sqrt(2/pi) (1 + 3 0.044715 z^2).  Past |z| = 100
+        // s (1 - s) is 0 in fp32, so z stays there: 0 times z^2's overflow is NaN.
         const f2 s = sigmoid2(gelu_arg2(z), -2.0f * kGeluC * kLog2e);
-        const f2 du = row::fma2(row::mul2(z, z), row::all2(6.0f * kGeluC * kGeluA), row::all2(2.0f * kGeluC));
         a = row::mul2(z, s);
-        g = row::fma2(row::mul2(a, du), row::fma2(s, minus, one), s);
+        const f2 c = row::mk2(fminf(fmaxf(row::lo2(z), -100.0f), 100.0f), fminf(fmaxf(row::hi2(z), -100.0f), 100.0f));
+        const f2 du = row::fma2(row::mul2(c, c), row::all2(6.0f * kGeluC * kGeluA), row::all2(2.0f * kGeluC));
+        g = row::fma2(row::mul2(row::mul2(c, s), du), row::fma2(s, minus, one), s);
     } else {
         a = z;
         g = one;

@@ -66,3 +66,23 @@ def test_whole_range(act):
     z = torch.linspace(-8, 8, 1025)
     a = z.to(F64) * _gates(z.to(F64), act)[0]
     R.check(_forward(z, act), a, a.abs(), "act, forward", U * a.abs())
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_largest_values(act):
+    """Up to the largest bf16 and fp32 values, finite and right; from 1e5 on
+    every activation is z (or 0, on its negative side) and its derivative 1
+    (or 0), exactly."""
+    z = torch.tensor([40.0, 1e5, 1e10, 2e19, 1e20, 1e30, 3e38]).to(BF)
+    for sign in (1.0, -1.0):
+        on = float(sign > 0 or act == F.ACT_NONE)
+        s, ds = _gates(sign * z.to(F64), act)
+        g, a = _backward(sign * z, act)
+        d = _forward((sign * z).float(), act)
+        m = s + (z.to(F64) * ds).abs()
+        R.check(g, s + sign * z.to(F64) * ds, m, "derivative", U * m)
+        R.check(a, sign * z.to(F64) * s, z.to(F64) * s, "act, backward", U * z.to(F64) * s)
+        R.check(d, sign * z.to(F64) * s, z.to(F64) * s, "act, forward", U * z.to(F64) * s)
+        assert torch.equal(g.cpu()[1:], torch.full_like(z[1:], on)), (act, sign)
+        assert torch.equal(a.cpu()[1:], on * sign * z[1:]), (act, sign)
+        assert torch.equal(d.cpu()[1:], on * sign * z[1:]), (act, sign)
