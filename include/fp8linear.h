@@ -512,9 +512,10 @@ int fp8_norm_bwd(const fp8_norm_bwd_args_t* args, void* workspace, size_t worksp
  * With `offsets` there is one product per expert: rows offsets[e] ..
  * offsets[e + 1] of A (and of residual, z, d, q) take B's and bias's part e.
  * The offsets are what fp8_moe_plan writes, in device memory, with any align
- * (32 lets every row leave in a TMA box); rows past offsets[experts] are left
- * as they are (z, d, q) or unread.  Offsets outside 0..M are held to it, and
- * one below its predecessor counts as equal to it. */
+ * (32 lets every row leave in a TMA box); rows before offsets[0] and past
+ * offsets[experts] are left as they are (z, d, q) or unread: what follows has
+ * to leave them out too (fp8_act_bwd by the same offsets).  Offsets outside
+ * 0..M are held to it, and one below its predecessor counts as equal to it. */
 typedef struct {
     const uint8_t* A;      /* [M][K] codes, 16-byte aligned                   */
     const uint8_t* B;      /* [experts][N or 2N][K] codes, 16-byte aligned    */
@@ -549,7 +550,10 @@ int fp8_gemm_act(const fp8_gemm_act_args_t* args, void* stream);
  *   dz = dD act'(z); gated: dz_gate = dD z_up act'(z_gate), dz_up = dD act(z_gate)
  * as bf16 and / or as FP8 codes of dz * q_scale[0] (for the dgrad and wgrad
  * GEMMs), with the bias gradient dbias[n] (+)= sum_m dz[m][n].  ReLU's
- * derivative at 0 is 0. */
+ * derivative at 0 is 0.
+ * After a product with offsets, give them here as well: the other rows, which
+ * that product left as they were, are then neither read nor written nor
+ * counted, and dbias is one sum an expert. */
 typedef struct {
     int64_t M, N;          /* N a positive multiple of 16                     */
     int32_t act, gated;
@@ -560,12 +564,17 @@ typedef struct {
     int32_t q_format;
     const float* q_scale;  /* [1], with q                                     */
     float* amax;           /* [1] max|dz|, nullable, with q                   */
-    float* dbias;          /* FP32 [N or 2N], nullable                        */
+    float* dbias;          /* FP32 [N or 2N], with offsets [experts][N or 2N],*/
+                           /*   nullable                                      */
     int32_t accumulate;    /* add to dbias                                    */
+    const int32_t* offsets;/* [experts + 1] as in fp8_gemm_act, nullable      */
+    int32_t experts;       /* 1..256, read with offsets only                  */
 } fp8_act_bwd_args_t;
 
-/* Bytes of workspace that fp8_act_bwd needs for dbias. */
+/* Bytes of workspace that fp8_act_bwd needs for dbias, without offsets and
+ * with them. */
 size_t fp8_act_bwd_workspace_size(int64_t M, int64_t N, int gated);
+size_t fp8_act_bwd_experts_workspace_size(int64_t M, int64_t N, int gated, int experts);
 int fp8_act_bwd(const fp8_act_bwd_args_t* args, void* workspace, size_t workspace_bytes,
                 void* stream);
 

@@ -72,7 +72,7 @@ class ActBwdArgsC(ctypes.Structure):
     """fp8_act_bwd_args_t"""
     _fields_ = [("M", _i64), ("N", _i64), ("act", _i32), ("gated", _i32), ("dD", _vp), ("z", _vp),
                 ("dz", _vp), ("q", _vp), ("q_format", _i32), ("q_scale", _vp), ("amax", _vp),
-                ("dbias", _vp), ("accumulate", _i32)]
+                ("dbias", _vp), ("accumulate", _i32), ("offsets", _vp), ("experts", _i32)]
 
 
 # A call's arguments are packed to the C struct's bytes in one go, which takes
@@ -150,6 +150,8 @@ def _lib():
         L.fp8_act_bwd.argtypes = [_vp, _vp, _sz, _vp]
         L.fp8_act_bwd_workspace_size.argtypes = [_i64, _i64, i]
         L.fp8_act_bwd_workspace_size.restype = _sz
+        L.fp8_act_bwd_experts_workspace_size.argtypes = [_i64, _i64, i, i]
+        L.fp8_act_bwd_experts_workspace_size.restype = _sz
         L.fp8_moe_rows.argtypes = [_i64, i, i, i]
         L.fp8_moe_rows.restype = _i64
         L.fp8_moe_workspace_size.argtypes = [_i64, i, i]
@@ -351,7 +353,9 @@ def fp8_gemm_act(A, fa: int, B, fb: int, scale_inv_a, scale_inv_b, ga: int = GRA
     with q_fmt, as FP8 codes of D * q_scale; z (bf16, want_z) is what
     fp8_act_bwd needs.  With offsets [E + 1] (fp8_moe_plan's) B is
     [E, N or 2N, K] and each expert's rows of A take their part of B,
-    scale_inv_b and bias.  d may be residual."""
+    scale_inv_b and bias; rows that no expert has (past the last offset) are
+    left as they are in d, z and q -- of a new tensor, whatever its memory
+    held -- so give fp8_act_bwd the same offsets.  d may be residual."""
     M, K = _rows(A, "A")
     E = 1
     if offsets is not None:
@@ -405,17 +409,23 @@ def fp8_gemm_act(A, fa: int, B, fb: int, scale_inv_a, scale_inv_b, ga: int = GRA
 
 
 @functools.lru_cache(maxsize=256)
-def fp8_act_bwd_workspace_size(M: int, N: int, gated: bool) -> int:
-    return int((_ready or _lib()).fp8_act_bwd_workspace_size(M, N, int(bool(gated))))
+def fp8_act_bwd_workspace_size(M: int, N: int, gated: bool, experts: int = 0) -> int:
+    """Bytes for dbias; experts: their number, with offsets (0: without)."""
+    L = _ready or _lib()
+    if experts:
+        return int(L.fp8_act_bwd_experts_workspace_size(M, N, int(bool(gated)), experts))
+    return int(L.fp8_act_bwd_workspace_size(M, N, int(bool(gated))))
 
 
 def fp8_act_bwd(dD, z, act: int, gated: bool = False, want_dz: bool = True, q_fmt: int | None = None,
                 q_scale=None, want_amax: bool = False, want_dbias: bool = False, dz=None, q=None,
                 amax=None, dbias=None, accumulate: bool = False, workspace=None,
-                stream=None) -> ActBwd:
+                stream=None, offsets=None) -> ActBwd:
     """dz = dD act'(z) (gated: both halves) from fp8_gemm_act's z, as bf16
     (want_dz) and, with q_fmt, as FP8 codes of dz * q_scale; dbias (fp32,
-    want_dbias) is dz's column sum, added to a given one with accumulate."""
+    want_dbias) is dz's column sum, added to a given one with accumulate.
+    With the offsets [E + 1] that fp8_gemm_act had, rows that no expert has are
+    neither read nor written nor counted in amax, and dbias is [E, N or 2N]."""
     M, N = _rows(dD, "dD")
     rows = 2 * N if gated else N
     dev = dD.device
@@ -438,18 +448,25 @@ def fp8_act_bwd(dD, z, act: int, gated: bool = False, want_dz: bool = True, q_fm
     elif want_amax:
         amax = torch.empty(1, dtype=_F32, device=dev)
         p_amax = amax.data_ptr()
+    p_off, E = 0, 0
+    if offsets is not None:
+        E = offsets.numel() - 1
+        if E < 1:
+            raise ValueError("offsets must hold one number an expert and the end")
+        p_off = _given(offsets, "offsets", _I32, (E + 1,))
+    per_col = (rows,) if offsets is None else (E, rows)
     if dbias is None and want_dbias:
-        dbias = torch.empty(rows, dtype=_F32, device=dev)
+        dbias = torch.empty(per_col, dtype=_F32, device=dev)
     ws, ws_bytes = None, 0
     if dbias is not None:
-        p_db = _given(dbias, "dbias", _F32, (rows,))
-        ws, ws_bytes, workspace = _workspace(workspace, fp8_act_bwd_workspace_size(M, N, gated), dev,
+        p_db = _given(dbias, "dbias", _F32, per_col)
+        ws, ws_bytes, workspace = _workspace(workspace, fp8_act_bwd_workspace_size(M, N, gated, E), dev,
                                              stream)
     a = _pack_act_bwd(
         M, N, act, 1 if gated else 0, _given(dD, "dD", _BF16, (M, N)), _given(z, "z", _BF16, out),
         p_dz, p_q, E4M3 if q_fmt is None else q_fmt,
         0 if q_scale is None else _given(q_scale, "q_scale", _F32, (1,)), p_amax, p_db,
-        1 if accumulate else 0)
+        1 if accumulate else 0, p_off, E)
     _check((_ready or _lib()).fp8_act_bwd(a, ws, ws_bytes, _on(stream, dD)))
     return ActBwd(dz, q, amax, dbias)
 

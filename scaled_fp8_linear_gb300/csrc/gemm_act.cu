@@ -204,17 +204,17 @@ struct Units {
 // Fills `u` (every thread of the CTA; ends with a barrier).  Offsets are held
 // to 0 .. M and made never to fall, so whatever they are no unit reaches
 // outside and there are no more units than the rows allow.
-__device__ __forceinline__ void make_units(Units* u, const ActParams& p, int rows_per_tile) {
+__device__ __forceinline__ void make_units(Units* u, int M, const int32_t* offsets, int experts, int num_n,
+                                           int part, int rows_per_tile) {
     const int t = static_cast<int>(threadIdx.x);
-    const int M = static_cast<int>(p.M);
     if (t < 32) {   // one warp, 32 products at a time
-        int run = 0, high = p.offsets ? min(max(p.offsets[0], 0), M) : 0;
-        for (int base = 0; base < p.experts; base += 32) {
+        int run = 0, high = offsets ? min(max(offsets[0], 0), M) : 0;
+        for (int base = 0; base < experts; base += 32) {
             const int e = base + t;
-            const bool on = e < p.experts;
+            const bool on = e < experts;
             // the row after this product's last: the largest offset up to its own
             int end = high;
-            if (on) end = max(high, p.offsets ? min(max(p.offsets[e + 1], 0), M) : M);
+            if (on) end = max(high, offsets ? min(max(offsets[e + 1], 0), M) : M);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int w = __shfl_up_sync(row::kAll, end, o);
@@ -225,9 +225,9 @@ __device__ __forceinline__ void make_units(Units* u, const ActParams& p, int row
             high = __shfl_sync(row::kAll, end, 31);
             const int rest = (end - begin) % 256;
             const int left = rest <= 128 ? rest : 0;   // what a second launch takes
-            if (p.part == kWholeBlocks) end -= left;
-            if (p.part == kRemainder) begin = end - left;
-            const int n = on ? (end - begin + rows_per_tile - 1) / rows_per_tile * p.num_n : 0;
+            if (part == kWholeBlocks) end -= left;
+            if (part == kRemainder) begin = end - left;
+            const int n = on ? (end - begin + rows_per_tile - 1) / rows_per_tile * num_n : 0;
             int incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -241,9 +241,24 @@ __device__ __forceinline__ void make_units(Units* u, const ActParams& p, int row
             }
             run += __shfl_sync(row::kAll, incl, 31);
         }
-        if (t == 0) u->first[p.experts] = run;
+        if (t == 0) u->first[experts] = run;
     }
     __syncthreads();
+}
+
+__device__ __forceinline__ void make_units(Units* u, const ActParams& p, int rows_per_tile) {
+    make_units(u, static_cast<int>(p.M), p.offsets, p.experts, p.num_n, p.part, rows_per_tile);
+}
+
+// The product that a unit belongs to: the last that starts at or before it.
+__device__ __forceinline__ int expert_of(int unit, const Units* u, int experts) {
+    int lo = 0, hi = experts;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (u->first[mid] <= unit) lo = mid;
+        else hi = mid;
+    }
+    return lo;
 }
 
 struct Tile {
@@ -254,12 +269,7 @@ struct Tile {
 
 __device__ __forceinline__ Tile tile_of(int unit, const Units* u, const ActParams& p,
                                         int rows_per_tile) {
-    int lo = 0, hi = p.experts;   // the last expert that starts at or before the unit
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (u->first[mid] <= unit) lo = mid;
-        else hi = mid;
-    }
+    const int lo = expert_of(unit, u, p.experts);
     const int local = unit - u->first[lo];
     const int num_m = (u->end[lo] - u->begin[lo] + rows_per_tile - 1) / rows_per_tile;
     // grouped raster: `group` row blocks down each column block, so that the
@@ -899,13 +909,18 @@ struct ActBwd {
     int64_t M, N;
     int64_t col_blocks;
     int q_fmt;
+    const int32_t* offsets;   // EXPERTS: row blocks are cut within an expert's rows
+    int experts;
+    int32_t* first;           // EXPERTS and BIAS: [experts + 1] each expert's first row block, written here
 };
 
 // Elementwise, HBM-bound: D's gradient and z are read once, dz is written
 // once, 256 columns a warp.  The pairs' packed instructions keep it off the
 // issue limit: 8192 x 11008 gated to codes 111 us (6.5 TB/s; 138 with scalar
-// ones).  BIAS: column sums stay in registers over the CTA's rows.
-template <int ACT, bool GATED, bool BIAS>
+// ones).  BIAS: column sums stay in registers over the CTA's rows.  EXPERTS:
+// only rows of the experts; a CTA's rows belong to one of them, and CTAs past
+// the experts' row blocks have nothing to do.
+template <int ACT, bool GATED, bool BIAS, bool EXPERTS>
 __global__ void __launch_bounds__(256) act_bwd_kernel(const __grid_constant__ ActBwd p) {
     ptx::griddep_launch_dependents();
     __shared__ float sums[BIAS ? 8 : 1][256];
@@ -913,6 +928,17 @@ __global__ void __launch_bounds__(256) act_bwd_kernel(const __grid_constant__ Ac
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t block_row = blockIdx.x / p.col_blocks;
     const int64_t c0 = (blockIdx.x - block_row * p.col_blocks) * 256, c = c0 + lane * 8;
+    int64_t row0 = block_row * kBwdRows, row_end = p.M;
+    if constexpr (EXPERTS) {
+        __shared__ Units units;
+        make_units(&units, static_cast<int>(p.M), p.offsets, p.experts, 1, kAllRows, kBwdRows);
+        if (BIAS && blockIdx.x == 0)
+            for (int e = threadIdx.x; e <= p.experts; e += 256) p.first[e] = units.first[e];
+        if (block_row >= units.first[p.experts]) return;
+        const int e = expert_of(static_cast<int>(block_row), &units, p.experts);
+        row0 = units.begin[e] + (block_row - units.first[e]) * kBwdRows;
+        row_end = units.end[e];
+    }
     const int64_t width = GATED ? 2 * p.N : p.N;
     const bool on = c < p.N;   // N is a multiple of 16
     const f2 qs = row::all2(p.q ? p.q_scale[0] : 0.0f);
@@ -932,13 +958,13 @@ __global__ void __launch_bounds__(256) act_bwd_kernel(const __grid_constant__ Ac
         }
     };
     if (on) {
-        const int64_t m0 = block_row * kBwdRows + warp;
+        const int64_t m0 = row0 + warp;
         // one row at a time: many warps hide its loads (116 us a pass with four
         // rows' loads in flight, 117 with one, 131 with two)
 #pragma unroll 1
         for (int i = 0; i < kBwdRows / 8; ++i) {
             const int64_t m = m0 + i * 8;
-            if (m >= p.M) break;
+            if (m >= row_end) break;
             row::Raw8<__nv_bfloat16> rd, rz, ru;
             rd.load(p.d + m * p.N + c);
             rz.load(p.z + m * width + c);
@@ -988,15 +1014,47 @@ __global__ void __launch_bounds__(256) act_bwd_kernel(const __grid_constant__ Ac
     }
 }
 
-template <int ACT>
+// dbias[e][c] (+)= the sum of expert e's row blocks' partial sums: eight slices
+// of the blocks first, then the slices, in a fixed order.
+__global__ void __launch_bounds__(256)
+    expert_bias_kernel(const float* part, const int32_t* first, int64_t width, float* dbias, int accumulate) {
+    ptx::griddep_launch_dependents();
+    __shared__ float sums[8][32];
+    ptx::griddep_wait();
+    const int e = blockIdx.y, slice = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;   // width is a multiple of 16
+    const int end = first[e + 1];
+    float s = 0.0f;
+    if (c < width) {
+#pragma unroll 4
+        for (int i = first[e] + slice; i < end; i += 8) s += part[i * width + c];
+    }
+    sums[slice][lane] = s;
+    __syncthreads();
+    if (slice == 0 && c < width) {
+        float t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t += sums[i][lane];
+        float* out = dbias + e * width + c;
+        *out = accumulate ? *out + t : t;
+    }
+}
+
+template <int ACT, bool EXPERTS>
 void launch_act_bwd(const ActBwd& p, bool gated, unsigned ctas, cudaStream_t st) {
     if (gated) {
-        if (p.part) launch_pdl(act_bwd_kernel<ACT, true, true>, dim3(ctas), dim3(256), 0, st, p);
-        else launch_pdl(act_bwd_kernel<ACT, true, false>, dim3(ctas), dim3(256), 0, st, p);
+        if (p.part) launch_pdl(act_bwd_kernel<ACT, true, true, EXPERTS>, dim3(ctas), dim3(256), 0, st, p);
+        else launch_pdl(act_bwd_kernel<ACT, true, false, EXPERTS>, dim3(ctas), dim3(256), 0, st, p);
     } else {
-        if (p.part) launch_pdl(act_bwd_kernel<ACT, false, true>, dim3(ctas), dim3(256), 0, st, p);
-        else launch_pdl(act_bwd_kernel<ACT, false, false>, dim3(ctas), dim3(256), 0, st, p);
+        if (p.part) launch_pdl(act_bwd_kernel<ACT, false, true, EXPERTS>, dim3(ctas), dim3(256), 0, st, p);
+        else launch_pdl(act_bwd_kernel<ACT, false, false, EXPERTS>, dim3(ctas), dim3(256), 0, st, p);
     }
+}
+
+template <int ACT>
+void launch_act_bwd(const ActBwd& p, bool gated, unsigned ctas, cudaStream_t st) {
+    if (p.offsets) launch_act_bwd<ACT, true>(p, gated, ctas, st);
+    else launch_act_bwd<ACT, false>(p, gated, ctas, st);
 }
 
 // ------------------------------------------------------------------ host side
@@ -1041,10 +1099,12 @@ int raster_group(int64_t K) {
     return g;
 }
 
-// At most this many tiles of `rows` rows and `cols` output columns, however
-// the experts' rows are cut.
+// At most this many blocks of `rows` rows, however the experts' rows are cut.
+int64_t most_blocks(int64_t M, int rows, int experts) { return (M + rows - 1) / rows + experts - 1; }
+
+// The same for tiles of `rows` rows and `cols` output columns.
 int64_t most_tiles(const fp8_gemm_act_args_t* a, int rows, int cols) {
-    return ((a->M + rows - 1) / rows + a->experts - 1) * ((a->N + cols - 1) / cols);
+    return most_blocks(a->M, rows, a->experts) * ((a->N + cols - 1) / cols);
 }
 
 template <bool GATED>
@@ -1214,7 +1274,13 @@ int fp8_gemm_act(const fp8_gemm_act_args_t* a, void* stream) {
 
 size_t fp8_act_bwd_workspace_size(int64_t M, int64_t N, int gated) {
     if (M < 0 || N < 16 || N % 16) return 0;
-    return static_cast<size_t>((M + kBwdRows - 1) / kBwdRows) * static_cast<size_t>(gated ? 2 * N : N) * 4;
+    return static_cast<size_t>(most_blocks(M, kBwdRows, 1)) * static_cast<size_t>(gated ? 2 * N : N) * 4;
+}
+
+size_t fp8_act_bwd_experts_workspace_size(int64_t M, int64_t N, int gated, int experts) {
+    if (M < 1 || N < 16 || N % 16 || experts < 1 || experts > kMaxGemmExperts) return 0;
+    return static_cast<size_t>(most_blocks(M, kBwdRows, experts)) * static_cast<size_t>(gated ? 2 * N : N) * 4 +
+           static_cast<size_t>(experts + 1) * 4;
 }
 
 int fp8_act_bwd(const fp8_act_bwd_args_t* a, void* workspace, size_t workspace_bytes, void* stream) {
@@ -1224,8 +1290,13 @@ int fp8_act_bwd(const fp8_act_bwd_args_t* a, void* workspace, size_t workspace_b
         return set_error(FP8_ERR_INVALID_ARG, "%s: unknown activation %d", what, a->act);
     if (a->M < 0 || a->N < 16 || a->N % 16 || a->N > (int64_t{1} << 30))
         return set_error(FP8_ERR_SHAPE, "%s: M must be >= 0, N a positive multiple of 16", what);
-    const int64_t col_blocks = (a->N + 255) / 256, row_blocks = (a->M + kBwdRows - 1) / kBwdRows;
-    if (a->M > (int64_t{1} << 31) || row_blocks * col_blocks >= (int64_t{1} << 31))
+    if (a->offsets && (a->experts < 1 || a->experts > kMaxGemmExperts))
+        return set_error(FP8_ERR_SHAPE, "%s: experts in 1..%d", what, kMaxGemmExperts);
+    const int64_t limit = a->offsets ? (int64_t{1} << 31) - 1024 : int64_t{1} << 31;   // offsets are 32-bit
+    if (a->M > limit) return set_error(FP8_ERR_SHAPE, "%s: dimensions out of range", what);
+    const int64_t col_blocks = (a->N + 255) / 256;
+    const int64_t row_blocks = most_blocks(a->M, kBwdRows, a->offsets ? a->experts : 1);
+    if (row_blocks * col_blocks >= (int64_t{1} << 31))
         return set_error(FP8_ERR_SHAPE, "%s: dimensions out of range", what);
     if ((!a->dD || !a->z) && a->M) return set_error(FP8_ERR_INVALID_ARG, "%s: NULL pointer", what);
     if (!a->dz && !a->q && !a->dbias && a->M)
@@ -1234,7 +1305,9 @@ int fp8_act_bwd(const fp8_act_bwd_args_t* a, void* workspace, size_t workspace_b
         return set_error(FP8_ERR_INVALID_ARG, "%s: unknown FP8 format", what);
     if (a->q ? !a->q_scale : (a->M && (a->q_scale || a->amax)))
         return set_error(FP8_ERR_INVALID_ARG, "%s: q and q_scale go together, amax with them", what);
-    const size_t need = a->dbias ? fp8_act_bwd_workspace_size(a->M, a->N, a->gated) : 0;
+    const size_t need = !a->dbias ? 0
+                        : a->offsets ? fp8_act_bwd_experts_workspace_size(a->M, a->N, a->gated, a->experts)
+                                     : fp8_act_bwd_workspace_size(a->M, a->N, a->gated);
     if (need && (!workspace || workspace_bytes < need))
         return set_error(FP8_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", what,
                          workspace ? workspace_bytes : size_t{0}, need);
@@ -1243,8 +1316,9 @@ int fp8_act_bwd(const fp8_act_bwd_args_t* a, void* workspace, size_t workspace_b
         if (!aligned(t, 16))
             return set_error(FP8_ERR_ALIGN, "%s: tensors and workspace must be 16-byte aligned", what);
     for (const void* t : {static_cast<const void*>(a->q_scale), static_cast<const void*>(a->amax),
-                          static_cast<const void*>(a->dbias)})
-        if (!aligned(t, 4)) return set_error(FP8_ERR_ALIGN, "%s: q_scale, amax and dbias must be 4-byte aligned", what);
+                          static_cast<const void*>(a->dbias), static_cast<const void*>(a->offsets)})
+        if (!aligned(t, 4))
+            return set_error(FP8_ERR_ALIGN, "%s: q_scale, amax, dbias and offsets must be 4-byte aligned", what);
     cudaStream_t st = as_stream(stream);
     const int64_t width = a->gated ? 2 * a->N : a->N;
     if (a->amax) launch_zero_words(a->amax, 1, st);
@@ -1256,6 +1330,8 @@ int fp8_act_bwd(const fp8_act_bwd_args_t* a, void* workspace, size_t workspace_b
         p.q = a->q; p.q_scale = a->q_scale; p.q_fmt = a->q_format; p.amax = a->amax;
         p.part = a->dbias ? static_cast<float*>(workspace) : nullptr;
         p.M = a->M; p.N = a->N; p.col_blocks = col_blocks;
+        p.offsets = a->offsets; p.experts = a->experts;
+        if (p.part && a->offsets) p.first = reinterpret_cast<int32_t*>(p.part + row_blocks * width);
         const unsigned ctas = static_cast<unsigned>(row_blocks * col_blocks);
         const bool gated = a->gated != 0;
         switch (a->act) {
@@ -1266,9 +1342,18 @@ int fp8_act_bwd(const fp8_act_bwd_args_t* a, void* workspace, size_t workspace_b
             default: launch_act_bwd<FP8_ACT_NONE>(p, gated, ctas, st); break;
         }
     }
-    if (a->dbias)
+    if (a->dbias && !a->offsets) {
         launch_column_sums(static_cast<const float*>(workspace), row_blocks, width, a->dbias,
                            a->accumulate, st);
+    } else if (a->dbias && a->M) {
+        const float* part = static_cast<const float*>(workspace);
+        launch_pdl(expert_bias_kernel, dim3(static_cast<unsigned>((width + 31) / 32), a->experts), dim3(256), 0,
+                   st, part, reinterpret_cast<const int32_t*>(part + row_blocks * width), width, a->dbias,
+                   a->accumulate != 0 ? 1 : 0);
+    } else if (a->dbias && !a->accumulate) {   // no rows: zeros
+        const cudaError_t e = cudaMemsetAsync(a->dbias, 0, static_cast<size_t>(a->experts) * width * 4, st);
+        if (e != cudaSuccess) return set_error(FP8_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    }
     return launch_status(what);
 }
 
