@@ -26,6 +26,12 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import scaled_fp8_linear_gb300 as F   # noqa: E402
 
 
+def scale_for(top, x):
+    """The scale that takes x's largest magnitude to `top`; finite for a
+    tensor of zeros."""
+    return top / F.fp8_amax(x).clamp_min(1e-20)
+
+
 def weight_codes(w):
     """E4M3 codes of w [E, N, K] with one factor per expert, and transposed."""
     E, N, K = w.shape
@@ -33,7 +39,7 @@ def weight_codes(w):
         torch.empty(E, K, N, dtype=torch.uint8, device=w.device)
     inv = torch.empty(E, device=w.device)
     for e in range(E):
-        scale = 448.0 / F.fp8_amax(w[e])
+        scale = scale_for(448.0, w[e])
         F.fp8_quantize(w[e], F.E4M3, scale=scale, q=q[e], q_t=q_t[e])
         inv[e] = 1.0 / scale[0]
     return q, q_t, inv
@@ -91,20 +97,20 @@ class ExpertBlock:
         g.update(w_next=n.dw_pre, w_post=n.dw_post, gate=n.dgate)
         do, g["w"] = F.fp8_moe_unpermute_bwd(n.dh, s["o"], plan.row_of, plan.src, s["w"])
         # the second product: codes of its gradient, dgrad per expert, wgrad per expert
-        do_scale = 57344.0 / F.fp8_amax(do)
+        do_scale = scale_for(57344.0, do)
         do_q = F.fp8_quantize(do, F.E5M2, scale=do_scale)[0]
         do_inv = 1.0 / do_scale
         dh = F.fp8_gemm_act(do_q, F.E5M2, self.out_qt, F.E4M3, do_inv, self.out_inv,
                             offsets=plan.offsets).d
         g["w_out"] = self._wgrad(do_q, do_inv, s["up"].q, 1.0 / self.h_scale, off)
         # the epilogue's gradient, as codes
-        dz_scale = 2048.0 / F.fp8_amax(dh[:off[-1]]).clamp_min(1e-20)
+        dz_scale = scale_for(2048.0, dh[:off[-1]])
         a = F.fp8_act_bwd(dh, s["up"].z, F.ACT_SILU, gated=True, want_dz=False, q_fmt=F.E5M2,
                           q_scale=dz_scale, offsets=plan.offsets)
         dxs = F.fp8_gemm_act(a.q, F.E5M2, self.in_qt, F.E4M3, 1.0 / dz_scale, self.in_inv,
                              offsets=plan.offsets).d
         ys = s["pre"].y   # the wgrad reads the tokens' rows with one factor
-        y_scale = 448.0 / F.fp8_amax(ys)
+        y_scale = scale_for(448.0, ys)
         y_q = F.fp8_moe_permute(F.fp8_quantize(ys, F.E4M3, scale=y_scale)[0], plan.row_of, plan.src)[0]
         g["w_in"] = self._wgrad(a.q, 1.0 / dz_scale, y_q, 1.0 / y_scale, off)
         dy = F.fp8_moe_unpermute(dxs, plan.row_of)
