@@ -3,7 +3,9 @@
 Like the package's other calls these only marshal arguments to the C-ABI
 library (include/fp8linear.h has the formulas): outputs that are not given
 are allocated on the inputs' device, everything runs in the library's
-kernels on the current (or the given) stream.
+kernels on the current stream.  With stream= (torch's object or a raw handle)
+a call is what it is under torch.cuda.stream(stream): its outputs are of that
+stream's memory, and a use on another stream waits as for any other tensor.
 
   fp8_norm_fwd, fp8_norm_bwd      norms before and after a block, gate, residual scale
   fp8_gemm_act, fp8_act_bwd       FP8 GEMM with bias, activation and residual in its epilogue
@@ -181,11 +183,35 @@ def _given(t, what, dtype, shape):
     return p
 
 
-def _on(stream, t):
-    """The stream's handle: the given one, or the current one of t's device."""
-    if stream is None and _raw_stream is not None:
-        return _raw_stream(t.get_device())
-    return _stream(stream)
+def _on(t):
+    """The handle of the current stream of t's device."""
+    return _raw_stream(t.get_device()) if _raw_stream is not None else _stream(None)
+
+
+def _is_current(stream):
+    """Whether this is the current stream of the current device."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream.device_index == torch.cuda.current_device() and stream.cuda_stream == _stream(None)
+    return int(stream) == _stream(None)
+
+
+def _stream_context(stream):
+    """torch's context for a stream given as its object or as a raw handle."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _under(stream, call, args):
+    """call(**args) with the given stream as the current one.  So all that the
+    call allocates comes from this stream's memory: a block of the caller's
+    stream may still be in use by work there that this stream does not wait
+    for, however long ago its tensor was freed."""
+    args["stream"] = None
+    if _is_current(stream):
+        return call(**args)
+    with _stream_context(stream):
+        return call(**args)
 
 
 def _rows(t, what):
@@ -195,16 +221,11 @@ def _rows(t, what):
     return shape
 
 
-def _workspace(workspace, need, device, stream):
-    """(address, bytes, tensor) of the given workspace or of a new one.  A new
-    one is freed when the call returns: on a stream of the caller's own it is
-    kept from torch's allocator until that stream is past the call."""
+def _workspace(workspace, need, device):
+    """(address, bytes, tensor) of the given workspace or of a new one."""
     if workspace is not None:
         return _given(workspace, "workspace", _BYTE, workspace.shape), workspace.numel(), workspace
     workspace = torch.empty(need if need > 16 else 16, dtype=_BYTE, device=device)
-    if stream is not None:
-        workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                else torch.cuda.ExternalStream(int(stream), device=device))
     return workspace.data_ptr(), workspace.numel(), workspace
 
 
@@ -222,6 +243,8 @@ def fp8_norm_fwd(x, h=None, kind: int = NORM_RMS, eps: float = 1e-5, alpha: floa
     bf16 (want_y) and, with q_fmt, as FP8 codes: per tensor with q_scale (and
     max|y|, want_amax) or per row (GRAN_ROW, q_scale_inv [T]).  stats [4, T]
     (want_stats) is what fp8_norm_bwd needs.  x_out may be x."""
+    if stream is not None:
+        return _under(stream, fp8_norm_fwd, locals())
     ref = x if x is not None else h
     if ref is None:
         raise ValueError("x and h are None")
@@ -271,7 +294,7 @@ def fp8_norm_fwd(x, h=None, kind: int = NORM_RMS, eps: float = 1e-5, alpha: floa
         0 if b_pre is None else _given(b_pre, "b_pre", _F32, vec), p_xo, p_y, p_q,
         E4M3 if q_fmt is None else q_fmt, q_gran, 1 if pow2 else 0,
         0 if q_scale is None else _given(q_scale, "q_scale", _F32, (1,)), p_inv, p_amax, p_stats)
-    _check((_ready or _lib()).fp8_norm_fwd(a, _on(stream, ref)))
+    _check((_ready or _lib()).fp8_norm_fwd(a, _on(ref)))
     return NormFwd(x_out, y, q, q_scale_inv, amax, stats)
 
 
@@ -289,6 +312,8 @@ def fp8_norm_bwd(dy, x_out, stats, dx_out=None, h=None, kind: int = NORM_RMS, al
     stats are the forward's.  dx and dh come where their inputs were; the
     vectors' gradients (fp32) where the vectors were given, added to the given
     outputs with accumulate.  dx may be dx_out."""
+    if stream is not None:
+        return _under(stream, fp8_norm_bwd, locals())
     ref = x_out if x_out is not None else dx_out if dx_out is not None else dy
     if ref is None:
         raise ValueError("dy and dx_out are None")
@@ -318,8 +343,7 @@ def fp8_norm_bwd(dy, x_out, stats, dx_out=None, h=None, kind: int = NORM_RMS, al
         db_post = torch.empty(C, dtype=_F32, device=dev)
     if dgate is None and gate is not None:
         dgate = torch.empty(gate_rows, C, dtype=_F32, device=dev)
-    ws, ws_bytes, workspace = _workspace(workspace, fp8_norm_bwd_workspace_size(T, C, gate_rows), dev,
-                                         stream)
+    ws, ws_bytes, workspace = _workspace(workspace, fp8_norm_bwd_workspace_size(T, C, gate_rows), dev)
     a = _pack_norm_bwd(
         T, C, kind, _OUT[dt], alpha, 0 if dy is None else _given(dy, "dy", _BF16, shape),
         0 if x_out is None else _given(x_out, "x_out", dt, shape),
@@ -336,7 +360,7 @@ def fp8_norm_bwd(dy, x_out, stats, dx_out=None, h=None, kind: int = NORM_RMS, al
         0 if dw_post is None else _given(dw_post, "dw_post", _F32, vec),
         0 if db_post is None else _given(db_post, "db_post", _F32, vec),
         0 if dgate is None else _given(dgate, "dgate", _F32, (gate_rows, C)), 1 if accumulate else 0)
-    _check((_ready or _lib()).fp8_norm_bwd(a, ws, ws_bytes, _on(stream, ref)))
+    _check((_ready or _lib()).fp8_norm_bwd(a, ws, ws_bytes, _on(ref)))
     return NormBwd(dx, dh, dw_pre, db_pre, dw_post, db_post, dgate)
 
 
@@ -356,6 +380,8 @@ def fp8_gemm_act(A, fa: int, B, fb: int, scale_inv_a, scale_inv_b, ga: int = GRA
     scale_inv_b and bias; rows that no expert has (past the last offset) are
     left as they are in d, z and q -- of a new tensor, whatever its memory
     held -- so give fp8_act_bwd the same offsets.  d may be residual."""
+    if stream is not None:
+        return _under(stream, fp8_gemm_act, locals())
     M, K = _rows(A, "A")
     E = 1
     if offsets is not None:
@@ -404,7 +430,7 @@ def fp8_gemm_act(A, fa: int, B, fb: int, scale_inv_a, scale_inv_b, ga: int = GRA
         E4M3 if q_fmt is None else q_fmt,
         0 if q_scale is None else _given(q_scale, "q_scale", _F32, (1,)), p_amax,
         0 if offsets is None else _given(offsets, "offsets", _I32, (E + 1,)), E)
-    _check((_ready or _lib()).fp8_gemm_act(a, _on(stream, A)))
+    _check((_ready or _lib()).fp8_gemm_act(a, _on(A)))
     return GemmAct(d, z, q, amax)
 
 
@@ -426,6 +452,8 @@ def fp8_act_bwd(dD, z, act: int, gated: bool = False, want_dz: bool = True, q_fm
     want_dbias) is dz's column sum, added to a given one with accumulate.
     With the offsets [E + 1] that fp8_gemm_act had, rows that no expert has are
     neither read nor written nor counted in amax, and dbias is [E, N or 2N]."""
+    if stream is not None:
+        return _under(stream, fp8_act_bwd, locals())
     M, N = _rows(dD, "dD")
     rows = 2 * N if gated else N
     dev = dD.device
@@ -460,14 +488,13 @@ def fp8_act_bwd(dD, z, act: int, gated: bool = False, want_dz: bool = True, q_fm
     ws, ws_bytes = None, 0
     if dbias is not None:
         p_db = _given(dbias, "dbias", _F32, per_col)
-        ws, ws_bytes, workspace = _workspace(workspace, fp8_act_bwd_workspace_size(M, N, gated, E), dev,
-                                             stream)
+        ws, ws_bytes, workspace = _workspace(workspace, fp8_act_bwd_workspace_size(M, N, gated, E), dev)
     a = _pack_act_bwd(
         M, N, act, 1 if gated else 0, _given(dD, "dD", _BF16, (M, N)), _given(z, "z", _BF16, out),
         p_dz, p_q, E4M3 if q_fmt is None else q_fmt,
         0 if q_scale is None else _given(q_scale, "q_scale", _F32, (1,)), p_amax, p_db,
         1 if accumulate else 0, p_off, E)
-    _check((_ready or _lib()).fp8_act_bwd(a, ws, ws_bytes, _on(stream, dD)))
+    _check((_ready or _lib()).fp8_act_bwd(a, ws, ws_bytes, _on(dD)))
     return ActBwd(dz, q, amax, dbias)
 
 
@@ -493,6 +520,8 @@ def fp8_moe_plan(ids, experts: int, align: int = 1, rows: int | None = None, off
     expert: offsets [E + 1] and counts [E] of the experts' rows, row_of [T, k]
     the slot's row or -1, src [rows] the row's slot (t * k + j) or -1.  Each
     expert's rows are padded to a multiple of align."""
+    if stream is not None:
+        return _under(stream, fp8_moe_plan, locals())
     T, k = _rows(ids, "ids")
     dev = ids.device
     if rows is None:
@@ -516,10 +545,10 @@ def fp8_moe_plan(ids, experts: int, align: int = 1, rows: int | None = None, off
         p_src = _given(src, "src", _I32, (rows,))
     ws, ws_bytes, need = None, 0, fp8_moe_workspace_size(T, k, experts)
     if need:
-        ws, ws_bytes, workspace = _workspace(workspace, need, dev, stream)
+        ws, ws_bytes, workspace = _workspace(workspace, need, dev)
     _check((_ready or _lib()).fp8_moe_plan(
         _given(ids, "ids", _I32, (T, k)), T, k, experts, align, p_off, p_cnt,
-        _given(row_of, "row_of", _I32, (T, k)), p_src, rows, ws, ws_bytes, _on(stream, ids)))
+        _given(row_of, "row_of", _I32, (T, k)), p_src, rows, ws, ws_bytes, _on(ids)))
     return MoePlan(offsets, counts, row_of, src)
 
 
@@ -527,6 +556,8 @@ def fp8_moe_permute(x, row_of, src, scale=None, xs=None, scale_s=None, stream=No
     """xs [rows, C] = x's rows in the plan's order, zeros where there is no
     source; x is of any type (codes go with their per-row factors, scale [T]).
     Returns (xs, scale_s or None)."""
+    if stream is not None:
+        return _under(stream, fp8_moe_permute, locals())
     T, C = _rows(x, "x")
     k, rows = _rows(row_of, "row_of")[1], src.numel()
     if xs is None:
@@ -544,13 +575,15 @@ def fp8_moe_permute(x, row_of, src, scale=None, xs=None, scale_s=None, stream=No
     _check((_ready or _lib()).fp8_moe_permute(
         _given(x, "x", x.dtype, (T, C)), p_sc, T, k, C * x.element_size(),
         _given(row_of, "row_of", _I32, (T, k)), _given(src, "src", _I32, (rows,)), rows, p_xs, p_ss,
-        _on(stream, x)))
+        _on(x)))
     return xs, scale_s
 
 
 def fp8_moe_unpermute(ys, row_of, weights=None, y=None, stream=None) -> torch.Tensor:
     """y [T, C] = the weighted sum of each token's rows of ys [rows, C] (bf16
     or fp32); weights [T, k] fp32, None: 1 (the gradient of the permutation)."""
+    if stream is not None:
+        return _under(stream, fp8_moe_unpermute, locals())
     rows, C = _rows(ys, "ys")
     T, k = _rows(row_of, "row_of")
     if ys.dtype not in _OUT:
@@ -560,13 +593,15 @@ def fp8_moe_unpermute(ys, row_of, weights=None, y=None, stream=None) -> torch.Te
     _check((_ready or _lib()).fp8_moe_unpermute(
         _given(ys, "ys", ys.dtype, (rows, C)), _OUT[ys.dtype], _given(row_of, "row_of", _I32, (T, k)),
         0 if weights is None else _given(weights, "weights", _F32, (T, k)), T, k, C, rows, _given(y, "y", ys.dtype, (T, C)),
-        _on(stream, ys)))
+        _on(ys)))
     return y
 
 
 def fp8_moe_unpermute_bwd(dy, ys, row_of, src, weights=None, dys=None, dweights=None, stream=None):
     """Gradients of fp8_moe_unpermute: (dys [rows, C], dweights [T, k] or None
     without weights)."""
+    if stream is not None:
+        return _under(stream, fp8_moe_unpermute_bwd, locals())
     rows, C = _rows(ys, "ys")
     T, k = _rows(row_of, "row_of")
     if ys.dtype not in _OUT:
@@ -580,5 +615,5 @@ def fp8_moe_unpermute_bwd(dy, ys, row_of, src, weights=None, dys=None, dweights=
         _given(row_of, "row_of", _I32, (T, k)), _given(src, "src", _I32, (rows,)),
         0 if weights is None else _given(weights, "weights", _F32, (T, k)), T, k, C, rows,
         _given(dys, "dys", ys.dtype, (rows, C)), 0 if dweights is None else _given(dweights, "dweights", _F32, (T, k)),
-        _on(stream, ys)))
+        _on(ys)))
     return dys, dweights
