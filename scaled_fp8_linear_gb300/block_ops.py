@@ -3,7 +3,8 @@
 Like the package's other calls these only marshal arguments to the C-ABI
 library (include/fp8linear.h has the formulas): outputs that are not given
 are allocated on the inputs' device, everything runs in the library's
-kernels on the current stream.  With stream= (torch's object or a raw handle)
+kernels on the current device, where all tensors have to be, and its current
+stream.  With stream= (torch's object or a raw handle)
 a call is what it is under torch.cuda.stream(stream): its outputs are of that
 stream's memory, and a use on another stream waits as for any other tensor.
 
@@ -170,22 +171,44 @@ def _lib():
     return _ready
 
 
-def _given(t, what, dtype, shape):
-    """The address of a tensor that has to be of this type and shape."""
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_devices = None   # how many there are; of one, no tensor's number is asked for (0.1 us each)
+
+
+def _here(t):
+    """The number of t's device, which has to be the current one: the library
+    launches there.  None where there is no other device."""
+    global _devices
+    if _devices is None:
+        _devices = torch.cuda.device_count()
+    if _devices == 1:
+        return None
+    n = t.get_device()
+    if n >= 0 and n != _current_device():
+        raise ValueError(f"tensors on cuda:{n}, but the current device is cuda:{_current_device()}")
+    return n
+
+
+def _given(t, what, dtype, shape, on):
+    """The address of a tensor that has to be of this type and shape and on
+    the device that _here() gave."""
     try:
-        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        if (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()
+                and (on is None or t.get_device() == on)):
             return t.data_ptr()
     except AttributeError:
         pass
     p = _ptr(t, what, _U8 if dtype is _BYTE else dtype)   # says what is wrong
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if on is not None and t.get_device() != on:
+        raise ValueError(f"{what}: on cuda:{t.get_device()}, not where the other tensors are")
     return p
 
 
-def _on(t):
-    """The handle of the current stream of t's device."""
-    return _raw_stream(t.get_device()) if _raw_stream is not None else _stream(None)
+def _on(device):
+    """The handle of the current stream of the device that _here() gave."""
+    return _raw_stream(device or 0) if _raw_stream is not None else _stream(None)
 
 
 def _is_current(stream):
@@ -221,10 +244,10 @@ def _rows(t, what):
     return shape
 
 
-def _workspace(workspace, need, device):
+def _workspace(workspace, need, device, on):
     """(address, bytes, tensor) of the given workspace or of a new one."""
     if workspace is not None:
-        return _given(workspace, "workspace", _BYTE, workspace.shape), workspace.numel(), workspace
+        return _given(workspace, "workspace", _BYTE, workspace.shape, on), workspace.numel(), workspace
     workspace = torch.empty(need if need > 16 else 16, dtype=_BYTE, device=device)
     return workspace.data_ptr(), workspace.numel(), workspace
 
@@ -249,18 +272,18 @@ def fp8_norm_fwd(x, h=None, kind: int = NORM_RMS, eps: float = 1e-5, alpha: floa
     if ref is None:
         raise ValueError("x and h are None")
     T, C = shape = _rows(ref, "x")
-    dev = ref.device
+    dev, on = ref.device, _here(ref)
     dt = x.dtype if x is not None else (x_out.dtype if x_out is not None else _BF16)
     if dt not in _OUT:
         raise TypeError(f"x: dtype {dt}, expected bfloat16 or float32")
     p_xo = p_y = p_q = p_inv = p_amax = p_stats = 0
     if x_out is not None:
-        p_xo = _given(x_out, "x_out", dt, shape)
+        p_xo = _given(x_out, "x_out", dt, shape, on)
     elif want_x_out:
         x_out = torch.empty_like(x) if x is not None else torch.empty(T, C, dtype=dt, device=dev)
         p_xo = x_out.data_ptr()
     if y is not None:
-        p_y = _given(y, "y", _BF16, shape)
+        p_y = _given(y, "y", _BF16, shape, on)
     elif want_y:
         y = (torch.empty_like(h) if h is not None else torch.empty_like(x) if dt is _BF16 else
              torch.empty(T, C, dtype=_BF16, device=dev))
@@ -268,33 +291,33 @@ def fp8_norm_fwd(x, h=None, kind: int = NORM_RMS, eps: float = 1e-5, alpha: floa
     if q_fmt is not None or q is not None:
         if q is None:
             q = torch.empty(T, C, dtype=torch.uint8, device=dev)
-        p_q = _given(q, "q", _BYTE, shape)
+        p_q = _given(q, "q", _BYTE, shape, on)
         if q_gran == GRAN_ROW and q_scale_inv is None:
             q_scale_inv = torch.empty(T, dtype=_F32, device=dev)
     if q_scale_inv is not None:
-        p_inv = _given(q_scale_inv, "q_scale_inv", _F32, (T,))
+        p_inv = _given(q_scale_inv, "q_scale_inv", _F32, (T,), on)
     if want_amax and amax is None:
         amax = torch.empty(1, dtype=_F32, device=dev)
     if amax is not None:
-        p_amax = _given(amax, "amax", _F32, (1,))
+        p_amax = _given(amax, "amax", _F32, (1,), on)
     if stats is not None:
-        p_stats = _given(stats, "stats", _F32, (4, T))
+        p_stats = _given(stats, "stats", _F32, (4, T), on)
     elif want_stats:
         stats = torch.empty(4, T, dtype=_F32, device=dev)
         p_stats = stats.data_ptr()
     gate_rows = 0 if gate is None else _rows(gate, "gate")[0]
     vec = (C,)
     a = _pack_norm_fwd(
-        T, C, kind, _OUT[dt], eps, alpha, 0 if x is None else _given(x, "x", dt, shape),
-        0 if h is None else _given(h, "h", _BF16, shape),
-        0 if gate is None else _given(gate, "gate", _BF16, (gate_rows, C)), gate_rows,
-        1 if post_norm else 0, 0 if w_post is None else _given(w_post, "w_post", _F32, vec),
-        0 if b_post is None else _given(b_post, "b_post", _F32, vec),
-        0 if w_pre is None else _given(w_pre, "w_pre", _F32, vec),
-        0 if b_pre is None else _given(b_pre, "b_pre", _F32, vec), p_xo, p_y, p_q,
+        T, C, kind, _OUT[dt], eps, alpha, 0 if x is None else _given(x, "x", dt, shape, on),
+        0 if h is None else _given(h, "h", _BF16, shape, on),
+        0 if gate is None else _given(gate, "gate", _BF16, (gate_rows, C), on), gate_rows,
+        1 if post_norm else 0, 0 if w_post is None else _given(w_post, "w_post", _F32, vec, on),
+        0 if b_post is None else _given(b_post, "b_post", _F32, vec, on),
+        0 if w_pre is None else _given(w_pre, "w_pre", _F32, vec, on),
+        0 if b_pre is None else _given(b_pre, "b_pre", _F32, vec, on), p_xo, p_y, p_q,
         E4M3 if q_fmt is None else q_fmt, q_gran, 1 if pow2 else 0,
-        0 if q_scale is None else _given(q_scale, "q_scale", _F32, (1,)), p_inv, p_amax, p_stats)
-    _check((_ready or _lib()).fp8_norm_fwd(a, _on(ref)))
+        0 if q_scale is None else _given(q_scale, "q_scale", _F32, (1,), on), p_inv, p_amax, p_stats)
+    _check((_ready or _lib()).fp8_norm_fwd(a, _on(on)))
     return NormFwd(x_out, y, q, q_scale_inv, amax, stats)
 
 
@@ -318,7 +341,7 @@ def fp8_norm_bwd(dy, x_out, stats, dx_out=None, h=None, kind: int = NORM_RMS, al
     if ref is None:
         raise ValueError("dy and dx_out are None")
     T, C = shape = _rows(ref, "x_out")
-    dev = ref.device
+    dev, on = ref.device, _here(ref)
     dt = x_out.dtype if x_out is not None else dx_out.dtype if dx_out is not None else _BF16
     if dt not in _OUT:
         raise TypeError(f"x_out: dtype {dt}, expected bfloat16 or float32")
@@ -343,24 +366,24 @@ def fp8_norm_bwd(dy, x_out, stats, dx_out=None, h=None, kind: int = NORM_RMS, al
         db_post = torch.empty(C, dtype=_F32, device=dev)
     if dgate is None and gate is not None:
         dgate = torch.empty(gate_rows, C, dtype=_F32, device=dev)
-    ws, ws_bytes, workspace = _workspace(workspace, fp8_norm_bwd_workspace_size(T, C, gate_rows), dev)
+    ws, ws_bytes, workspace = _workspace(workspace, fp8_norm_bwd_workspace_size(T, C, gate_rows), dev, on)
     a = _pack_norm_bwd(
-        T, C, kind, _OUT[dt], alpha, 0 if dy is None else _given(dy, "dy", _BF16, shape),
-        0 if x_out is None else _given(x_out, "x_out", dt, shape),
-        0 if dx_out is None else _given(dx_out, "dx_out", dt, shape),
-        0 if h is None else _given(h, "h", _BF16, shape),
-        0 if gate is None else _given(gate, "gate", _BF16, (gate_rows, C)), gate_rows,
-        1 if post_norm else 0, 0 if w_post is None else _given(w_post, "w_post", _F32, vec),
-        0 if b_post is None else _given(b_post, "b_post", _F32, vec),
-        0 if w_pre is None else _given(w_pre, "w_pre", _F32, vec),
-        0 if stats is None else _given(stats, "stats", _F32, (4, T)), _given(dx, "dx", dt, shape),
-        0 if dh is None else _given(dh, "dh", _BF16, shape),
-        0 if dw_pre is None else _given(dw_pre, "dw_pre", _F32, vec),
-        0 if db_pre is None else _given(db_pre, "db_pre", _F32, vec),
-        0 if dw_post is None else _given(dw_post, "dw_post", _F32, vec),
-        0 if db_post is None else _given(db_post, "db_post", _F32, vec),
-        0 if dgate is None else _given(dgate, "dgate", _F32, (gate_rows, C)), 1 if accumulate else 0)
-    _check((_ready or _lib()).fp8_norm_bwd(a, ws, ws_bytes, _on(ref)))
+        T, C, kind, _OUT[dt], alpha, 0 if dy is None else _given(dy, "dy", _BF16, shape, on),
+        0 if x_out is None else _given(x_out, "x_out", dt, shape, on),
+        0 if dx_out is None else _given(dx_out, "dx_out", dt, shape, on),
+        0 if h is None else _given(h, "h", _BF16, shape, on),
+        0 if gate is None else _given(gate, "gate", _BF16, (gate_rows, C), on), gate_rows,
+        1 if post_norm else 0, 0 if w_post is None else _given(w_post, "w_post", _F32, vec, on),
+        0 if b_post is None else _given(b_post, "b_post", _F32, vec, on),
+        0 if w_pre is None else _given(w_pre, "w_pre", _F32, vec, on),
+        0 if stats is None else _given(stats, "stats", _F32, (4, T), on), _given(dx, "dx", dt, shape, on),
+        0 if dh is None else _given(dh, "dh", _BF16, shape, on),
+        0 if dw_pre is None else _given(dw_pre, "dw_pre", _F32, vec, on),
+        0 if db_pre is None else _given(db_pre, "db_pre", _F32, vec, on),
+        0 if dw_post is None else _given(dw_post, "dw_post", _F32, vec, on),
+        0 if db_post is None else _given(db_post, "db_post", _F32, vec, on),
+        0 if dgate is None else _given(dgate, "dgate", _F32, (gate_rows, C), on), 1 if accumulate else 0)
+    _check((_ready or _lib()).fp8_norm_bwd(a, ws, ws_bytes, _on(on)))
     return NormBwd(dx, dh, dw_pre, db_pre, dw_post, db_post, dgate)
 
 
@@ -396,41 +419,41 @@ def fp8_gemm_act(A, fa: int, B, fb: int, scale_inv_a, scale_inv_b, ga: int = GRA
     if gated and rows % 2:
         raise ValueError("a gated B has an even number of rows")
     N = rows // 2 if gated else rows
-    dev = A.device
+    dev, on = A.device, _here(A)
     out = (M, N)
     p_d = p_z = p_q = p_amax = 0
     if d is not None:
-        p_d = _given(d, "d", _BF16, out)
+        p_d = _given(d, "d", _BF16, out, on)
     elif want_d:
         d = torch.empty(M, N, dtype=_BF16, device=dev)
         p_d = d.data_ptr()
     if z is not None:
-        p_z = _given(z, "z", _BF16, (M, rows))
+        p_z = _given(z, "z", _BF16, (M, rows), on)
     elif want_z:
         z = torch.empty(M, rows, dtype=_BF16, device=dev)
         p_z = z.data_ptr()
     if q is not None:
-        p_q = _given(q, "q", _BYTE, out)
+        p_q = _given(q, "q", _BYTE, out, on)
     elif q_fmt is not None:
         q = torch.empty(M, N, dtype=torch.uint8, device=dev)
         p_q = q.data_ptr()
     if amax is not None:
-        p_amax = _given(amax, "amax", _F32, (1,))
+        p_amax = _given(amax, "amax", _F32, (1,), on)
     elif want_amax:
         amax = torch.empty(1, dtype=_F32, device=dev)
         p_amax = amax.data_ptr()
     per_b = (E,)
     per_row = (E, rows) if offsets is not None else (rows,)
     a = _pack_gemm_act(
-        _given(A, "A", _BYTE, (M, K)), _given(B, "B", _BYTE, B.shape), fa, fb, M, N, K, ga, gb,
-        _given(scale_inv_a, "scale_inv_a", _F32, (M,) if ga == GRAN_ROW else (1,)),
-        _given(scale_inv_b, "scale_inv_b", _F32, per_row if gb == GRAN_ROW else per_b), act,
-        1 if gated else 0, 0 if bias is None else _given(bias, "bias", _BF16, per_row),
-        0 if residual is None else _given(residual, "residual", _BF16, out), p_z, p_d, p_q,
+        _given(A, "A", _BYTE, (M, K), on), _given(B, "B", _BYTE, B.shape, on), fa, fb, M, N, K, ga, gb,
+        _given(scale_inv_a, "scale_inv_a", _F32, (M,) if ga == GRAN_ROW else (1,), on),
+        _given(scale_inv_b, "scale_inv_b", _F32, per_row if gb == GRAN_ROW else per_b, on), act,
+        1 if gated else 0, 0 if bias is None else _given(bias, "bias", _BF16, per_row, on),
+        0 if residual is None else _given(residual, "residual", _BF16, out, on), p_z, p_d, p_q,
         E4M3 if q_fmt is None else q_fmt,
-        0 if q_scale is None else _given(q_scale, "q_scale", _F32, (1,)), p_amax,
-        0 if offsets is None else _given(offsets, "offsets", _I32, (E + 1,)), E)
-    _check((_ready or _lib()).fp8_gemm_act(a, _on(A)))
+        0 if q_scale is None else _given(q_scale, "q_scale", _F32, (1,), on), p_amax,
+        0 if offsets is None else _given(offsets, "offsets", _I32, (E + 1,), on), E)
+    _check((_ready or _lib()).fp8_gemm_act(a, _on(on)))
     return GemmAct(d, z, q, amax)
 
 
@@ -456,23 +479,23 @@ def fp8_act_bwd(dD, z, act: int, gated: bool = False, want_dz: bool = True, q_fm
         return _under(stream, fp8_act_bwd, locals())
     M, N = _rows(dD, "dD")
     rows = 2 * N if gated else N
-    dev = dD.device
+    dev, on = dD.device, _here(dD)
     if accumulate and dbias is None:
         raise ValueError("accumulate adds to a given dbias")
     out = (M, rows)
     p_dz = p_q = p_amax = p_db = 0
     if dz is not None:
-        p_dz = _given(dz, "dz", _BF16, out)
+        p_dz = _given(dz, "dz", _BF16, out, on)
     elif want_dz:
         dz = torch.empty(M, rows, dtype=_BF16, device=dev)
         p_dz = dz.data_ptr()
     if q is not None:
-        p_q = _given(q, "q", _BYTE, out)
+        p_q = _given(q, "q", _BYTE, out, on)
     elif q_fmt is not None:
         q = torch.empty(M, rows, dtype=_BYTE, device=dev)
         p_q = q.data_ptr()
     if amax is not None:
-        p_amax = _given(amax, "amax", _F32, (1,))
+        p_amax = _given(amax, "amax", _F32, (1,), on)
     elif want_amax:
         amax = torch.empty(1, dtype=_F32, device=dev)
         p_amax = amax.data_ptr()
@@ -481,20 +504,20 @@ def fp8_act_bwd(dD, z, act: int, gated: bool = False, want_dz: bool = True, q_fm
         E = offsets.numel() - 1
         if E < 1:
             raise ValueError("offsets must hold one number an expert and the end")
-        p_off = _given(offsets, "offsets", _I32, (E + 1,))
+        p_off = _given(offsets, "offsets", _I32, (E + 1,), on)
     per_col = (rows,) if offsets is None else (E, rows)
     if dbias is None and want_dbias:
         dbias = torch.empty(per_col, dtype=_F32, device=dev)
     ws, ws_bytes = None, 0
     if dbias is not None:
-        p_db = _given(dbias, "dbias", _F32, per_col)
-        ws, ws_bytes, workspace = _workspace(workspace, fp8_act_bwd_workspace_size(M, N, gated, E), dev)
+        p_db = _given(dbias, "dbias", _F32, per_col, on)
+        ws, ws_bytes, workspace = _workspace(workspace, fp8_act_bwd_workspace_size(M, N, gated, E), dev, on)
     a = _pack_act_bwd(
-        M, N, act, 1 if gated else 0, _given(dD, "dD", _BF16, (M, N)), _given(z, "z", _BF16, out),
+        M, N, act, 1 if gated else 0, _given(dD, "dD", _BF16, (M, N), on), _given(z, "z", _BF16, out, on),
         p_dz, p_q, E4M3 if q_fmt is None else q_fmt,
-        0 if q_scale is None else _given(q_scale, "q_scale", _F32, (1,)), p_amax, p_db,
+        0 if q_scale is None else _given(q_scale, "q_scale", _F32, (1,), on), p_amax, p_db,
         1 if accumulate else 0, p_off, E)
-    _check((_ready or _lib()).fp8_act_bwd(a, ws, ws_bytes, _on(dD)))
+    _check((_ready or _lib()).fp8_act_bwd(a, ws, ws_bytes, _on(on)))
     return ActBwd(dz, q, amax, dbias)
 
 
@@ -523,32 +546,32 @@ def fp8_moe_plan(ids, experts: int, align: int = 1, rows: int | None = None, off
     if stream is not None:
         return _under(stream, fp8_moe_plan, locals())
     T, k = _rows(ids, "ids")
-    dev = ids.device
+    dev, on = ids.device, _here(ids)
     if rows is None:
         rows = fp8_moe_rows(T, k, experts, align) if src is None else src.numel()
     if offsets is None:
         offsets = torch.empty(experts + 1, dtype=_I32, device=dev)
         p_off = offsets.data_ptr()
     else:
-        p_off = _given(offsets, "offsets", _I32, (experts + 1,))
+        p_off = _given(offsets, "offsets", _I32, (experts + 1,), on)
     if counts is None:
         counts = torch.empty(experts, dtype=_I32, device=dev)
         p_cnt = counts.data_ptr()
     else:
-        p_cnt = _given(counts, "counts", _I32, (experts,))
+        p_cnt = _given(counts, "counts", _I32, (experts,), on)
     if row_of is None:
         row_of = torch.empty_like(ids)
     if src is None:
         src = torch.empty(rows, dtype=_I32, device=dev)
         p_src = src.data_ptr()
     else:
-        p_src = _given(src, "src", _I32, (rows,))
+        p_src = _given(src, "src", _I32, (rows,), on)
     ws, ws_bytes, need = None, 0, fp8_moe_workspace_size(T, k, experts)
     if need:
-        ws, ws_bytes, workspace = _workspace(workspace, need, dev)
+        ws, ws_bytes, workspace = _workspace(workspace, need, dev, on)
     _check((_ready or _lib()).fp8_moe_plan(
-        _given(ids, "ids", _I32, (T, k)), T, k, experts, align, p_off, p_cnt,
-        _given(row_of, "row_of", _I32, (T, k)), p_src, rows, ws, ws_bytes, _on(ids)))
+        _given(ids, "ids", _I32, (T, k), on), T, k, experts, align, p_off, p_cnt,
+        _given(row_of, "row_of", _I32, (T, k), on), p_src, rows, ws, ws_bytes, _on(on)))
     return MoePlan(offsets, counts, row_of, src)
 
 
@@ -560,22 +583,23 @@ def fp8_moe_permute(x, row_of, src, scale=None, xs=None, scale_s=None, stream=No
         return _under(stream, fp8_moe_permute, locals())
     T, C = _rows(x, "x")
     k, rows = _rows(row_of, "row_of")[1], src.numel()
+    on = _here(x)
     if xs is None:
         xs = torch.empty(rows, C, dtype=x.dtype, device=x.device)
         p_xs = xs.data_ptr()
     else:
-        p_xs = _given(xs, "xs", x.dtype, (rows, C))
+        p_xs = _given(xs, "xs", x.dtype, (rows, C), on)
     p_sc = p_ss = 0
     if scale is not None:
         if scale_s is None:
             scale_s = torch.empty(rows, dtype=_F32, device=x.device)
-        p_sc = _given(scale, "scale", _F32, (T,))
+        p_sc = _given(scale, "scale", _F32, (T,), on)
     if scale_s is not None:
-        p_ss = _given(scale_s, "scale_s", _F32, (rows,))
+        p_ss = _given(scale_s, "scale_s", _F32, (rows,), on)
     _check((_ready or _lib()).fp8_moe_permute(
-        _given(x, "x", x.dtype, (T, C)), p_sc, T, k, C * x.element_size(),
-        _given(row_of, "row_of", _I32, (T, k)), _given(src, "src", _I32, (rows,)), rows, p_xs, p_ss,
-        _on(x)))
+        _given(x, "x", x.dtype, (T, C), on), p_sc, T, k, C * x.element_size(),
+        _given(row_of, "row_of", _I32, (T, k), on), _given(src, "src", _I32, (rows,), on), rows, p_xs, p_ss,
+        _on(on)))
     return xs, scale_s
 
 
@@ -586,14 +610,15 @@ def fp8_moe_unpermute(ys, row_of, weights=None, y=None, stream=None) -> torch.Te
         return _under(stream, fp8_moe_unpermute, locals())
     rows, C = _rows(ys, "ys")
     T, k = _rows(row_of, "row_of")
+    on = _here(ys)
     if ys.dtype not in _OUT:
         raise TypeError(f"ys: dtype {ys.dtype}, expected bfloat16 or float32")
     if y is None:
         y = torch.empty(T, C, dtype=ys.dtype, device=ys.device)
     _check((_ready or _lib()).fp8_moe_unpermute(
-        _given(ys, "ys", ys.dtype, (rows, C)), _OUT[ys.dtype], _given(row_of, "row_of", _I32, (T, k)),
-        0 if weights is None else _given(weights, "weights", _F32, (T, k)), T, k, C, rows, _given(y, "y", ys.dtype, (T, C)),
-        _on(ys)))
+        _given(ys, "ys", ys.dtype, (rows, C), on), _OUT[ys.dtype], _given(row_of, "row_of", _I32, (T, k), on),
+        0 if weights is None else _given(weights, "weights", _F32, (T, k), on), T, k, C, rows,
+        _given(y, "y", ys.dtype, (T, C), on), _on(on)))
     return y
 
 
@@ -604,6 +629,7 @@ def fp8_moe_unpermute_bwd(dy, ys, row_of, src, weights=None, dys=None, dweights=
         return _under(stream, fp8_moe_unpermute_bwd, locals())
     rows, C = _rows(ys, "ys")
     T, k = _rows(row_of, "row_of")
+    on = _here(ys)
     if ys.dtype not in _OUT:
         raise TypeError(f"ys: dtype {ys.dtype}, expected bfloat16 or float32")
     if dys is None:
@@ -611,9 +637,9 @@ def fp8_moe_unpermute_bwd(dy, ys, row_of, src, weights=None, dys=None, dweights=
     if dweights is None and weights is not None:
         dweights = torch.empty(T, k, dtype=_F32, device=ys.device)
     _check((_ready or _lib()).fp8_moe_unpermute_bwd(
-        _given(dy, "dy", ys.dtype, (T, C)), _given(ys, "ys", ys.dtype, (rows, C)), _OUT[ys.dtype],
-        _given(row_of, "row_of", _I32, (T, k)), _given(src, "src", _I32, (rows,)),
-        0 if weights is None else _given(weights, "weights", _F32, (T, k)), T, k, C, rows,
-        _given(dys, "dys", ys.dtype, (rows, C)), 0 if dweights is None else _given(dweights, "dweights", _F32, (T, k)),
-        _on(ys)))
+        _given(dy, "dy", ys.dtype, (T, C), on), _given(ys, "ys", ys.dtype, (rows, C), on), _OUT[ys.dtype],
+        _given(row_of, "row_of", _I32, (T, k), on), _given(src, "src", _I32, (rows,), on),
+        0 if weights is None else _given(weights, "weights", _F32, (T, k), on), T, k, C, rows,
+        _given(dys, "dys", ys.dtype, (rows, C), on),
+        0 if dweights is None else _given(dweights, "dweights", _F32, (T, k), on), _on(on)))
     return dys, dweights
