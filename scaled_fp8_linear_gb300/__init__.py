@@ -164,6 +164,32 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _is_current(stream):
+    """Whether this is the current stream of the current device."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream.device_index == torch.cuda.current_device() and stream.cuda_stream == _stream(None)
+    return int(stream) == _stream(None)
+
+
+def _stream_context(stream):
+    """torch's context for a stream given as its object or as a raw handle."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _under(stream, call, args):
+    """call(**args) with the given stream as the current one.  So all that the
+    call allocates comes from this stream's memory: a block of the caller's
+    stream may still be in use by work there that this stream does not wait
+    for, however long ago its tensor was freed."""
+    args["stream"] = None
+    if _is_current(stream):
+        return call(**args)
+    with _stream_context(stream):
+        return call(**args)
+
+
 def _ptr(t, what, dtype=None, device=True):
     if t is None:
         return None
@@ -185,6 +211,8 @@ _U8 = (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
 
 def fp8_amax(x: torch.Tensor, amax: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """max |x| of a bf16 tensor into a 1-element fp32 device tensor."""
+    if stream is not None:
+        return _under(stream, fp8_amax, locals())
     if amax is None:
         amax = torch.empty(1, dtype=torch.float32, device=x.device)
     _check(lib().fp8_amax(_ptr(x, "x", torch.bfloat16), x.numel(),
@@ -223,6 +251,8 @@ def fp8_quantize(x: torch.Tensor, fmt: int, granularity: int = GRAN_TENSOR, scal
     with transpose=True the transposed block scales are in
     `scale_inv_blocks_t` (allocated here if not given) -- see
     fp8_quantize_blocks for a call that returns them."""
+    if stream is not None:
+        return _under(stream, fp8_quantize, locals())
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     rows, cols = x.shape
@@ -254,6 +284,8 @@ def fp8_quantize_counted(x: torch.Tensor, fmt: int, scale, counts=None, q=None, 
     """Per-tensor cast with fused dashboard counters.  Returns
     (q, q_t or None, amax or None, counts) where counts is a 2-element int64
     device tensor [underflow, saturated] that the call adds to."""
+    if stream is not None:
+        return _under(stream, fp8_quantize_counted, locals())
     rows, cols = x.shape
     dev = x.device
     if q is None:
@@ -276,6 +308,8 @@ def fp8_quantize_sr(x: torch.Tensor, fmt: int, scale, seed: int, offset: int = 0
                     stream=None):
     """Per-tensor cast with stochastic rounding (Philox-4x32-10 keyed by seed,
     counter offset).  Returns (q, q_t or None, amax or None)."""
+    if stream is not None:
+        return _under(stream, fp8_quantize_sr, locals())
     rows, cols = x.shape
     dev = x.device
     if q is None:
@@ -295,6 +329,8 @@ def fp8_quantize_sr(x: torch.Tensor, fmt: int, scale, seed: int, offset: int = 0
 def fp8_quantize_blocks(x: torch.Tensor, fmt: int, granularity: int, pow2: bool = False,
                         transpose: bool = False, stream=None):
     """Block cast; returns (q, scale_inv_blocks, q_t, scale_inv_blocks_t)."""
+    if stream is not None:
+        return _under(stream, fp8_quantize_blocks, locals())
     rows, cols = x.shape
     q_t = torch.empty(cols, rows, dtype=torch.uint8, device=x.device) if transpose else None
     st = None
@@ -324,6 +360,8 @@ def fp8_gemm(A: torch.Tensor, fa: int, B: torch.Tensor, fb: int, scale_inv_a, sc
              bias=None) -> torch.Tensor:
     """D = (A . B^T) with dequantisation factors (+ bias [N], bf16); A [M,K],
     B [N,K] FP8 codes, or stored [K,M] / [K,N] per `layout`."""
+    if stream is not None:
+        return _under(stream, fp8_gemm, locals())
     M, K, N = _gemm_dims(A, B, layout)
     if D is None:
         D = torch.empty(M, N, dtype=torch.bfloat16 if out == OUT_BF16 else torch.float32,
@@ -355,6 +393,8 @@ def fp8_gemm_group(g1: dict, g2: dict, stream=None):
     """Two independent GEMMs in one launch; g1, g2 hold fp8_gemm's arguments
     by name (A, fa, B, fb, scale_inv_a, scale_inv_b and optionally ga, gb,
     out, D, accumulate, bias).  Returns (D1, D2)."""
+    if stream is not None:
+        return _under(stream, fp8_gemm_group, locals())
     a1, D1 = _gemm_args(**g1)
     a2, D2 = _gemm_args(**g2)
     _check(lib().fp8_gemm_group(ctypes.byref(a1), ctypes.byref(a2), _stream(stream)))
@@ -480,6 +520,8 @@ class Fp8Linear:
     def forward(self, X: torch.Tensor, W: torch.Tensor, Y=None, stream=None,
                 bias=None) -> torch.Tensor:
         """Y = X . W^T (+ bias [N], bf16)."""
+        if stream is not None:
+            return _under(stream, Fp8Linear.forward, locals())
         if Y is None:
             Y = torch.empty(self.M, self.N, dtype=torch.bfloat16, device=X.device)
         fp8_linear_fwd(X, W, self.recipe, self.c_state, Y, None, stream, bias=bias)
@@ -491,6 +533,8 @@ class Fp8Linear:
                  stream=None, dbias=None):
         """dX, dW (+)= ...; with dbias (fp32 [N]) also the bias gradient,
         accumulated like dW."""
+        if stream is not None:
+            return _under(stream, Fp8Linear.backward, locals())
         if dX is None:
             dX = torch.empty(self.M, self.K, dtype=torch.bfloat16, device=dY.device)
         if dW is None:

@@ -22,7 +22,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import (_U8, _ptr, _raw_stream, _stream, _vp, E4M3, Fp8Error, GRAN_ROW, GRAN_TENSOR, OUT_BF16, OUT_F32,
+from . import (_U8, _ptr, _raw_stream, _stream, _under, _vp, E4M3, Fp8Error, GRAN_ROW, GRAN_TENSOR, OUT_BF16, OUT_F32,
                fp8_last_error)
 from . import lib as _base_lib
 
@@ -209,32 +209,6 @@ def _given(t, what, dtype, shape, on):
 def _on(device):
     """The handle of the current stream of the device that _here() gave."""
     return _raw_stream(device or 0) if _raw_stream is not None else _stream(None)
-
-
-def _is_current(stream):
-    """Whether this is the current stream of the current device."""
-    if isinstance(stream, torch.cuda.Stream):
-        return stream.device_index == torch.cuda.current_device() and stream.cuda_stream == _stream(None)
-    return int(stream) == _stream(None)
-
-
-def _stream_context(stream):
-    """torch's context for a stream given as its object or as a raw handle."""
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-    return torch.cuda.stream(stream)
-
-
-def _under(stream, call, args):
-    """call(**args) with the given stream as the current one.  So all that the
-    call allocates comes from this stream's memory: a block of the caller's
-    stream may still be in use by work there that this stream does not wait
-    for, however long ago its tensor was freed."""
-    args["stream"] = None
-    if _is_current(stream):
-        return call(**args)
-    with _stream_context(stream):
-        return call(**args)
 
 
 def _rows(t, what):

@@ -50,14 +50,19 @@ def world(monkeypatch):
             return make(*a, **kw)
         return call
 
-    monkeypatch.setattr(B, "_stream_context", on, raising=False)
-    monkeypatch.setattr(B, "_is_current", lambda stream: int(stream) == World.now, raising=False)
+    for module in (F, B):
+        monkeypatch.setattr(module, "_stream_context", on, raising=False)
+        monkeypatch.setattr(module, "_is_current", lambda stream: int(stream) == World.now, raising=False)
     monkeypatch.setattr(B, "_on", lambda *a: World.now)
+    monkeypatch.setattr(F, "_stream", lambda stream: World.now if stream is None else int(stream))
+    monkeypatch.setattr(F, "_ptr", lambda t, *a: None if t is None else t.data_ptr() or 16)
+    monkeypatch.setattr(F, "_lib", _Library(World.launched))
     monkeypatch.setattr(B, "_given", lambda t, what, dtype, shape, *a: t.data_ptr() or 16)
     monkeypatch.setattr(B, "_here", lambda t: 0, raising=False)
     monkeypatch.setattr(B, "_ready", _Library(World.launched))
     monkeypatch.setattr(torch, "empty", noted(torch.empty))
     monkeypatch.setattr(torch, "empty_like", noted(torch.empty_like))
+    monkeypatch.setattr(torch, "zeros", noted(torch.zeros))
     for cached in (B.fp8_act_bwd_workspace_size, B.fp8_moe_rows, B.fp8_moe_workspace_size):
         cached.cache_clear()
     yield World
@@ -66,11 +71,24 @@ def world(monkeypatch):
 
 
 def _calls():
-    t = lambda dt, *s: torch.zeros(*s, dtype=dt)
+    t = lambda dt, *s: torch.full(s, 0, dtype=dt)
     x, w, ids = t(BF, 8, 32), t(F32, 32), t(I32, 8, 2)
     one, code, off = t(F32, 1), t(U8, 8, 32), t(I32, 3)
     plan = (t(I32, 8, 2), t(I32, 64))
+    X, W = t(BF, 128, 128), t(BF, 128, 128)
+    codes = lambda: dict(A=t(U8, 8, 32), fa=0, B=t(U8, 16, 32), fb=0, scale_inv_a=one, scale_inv_b=one)
+    group = codes()
+    layer = F.Fp8Linear(128, 128, 128, F.Recipe(F.SCALING_DYNAMIC), device="cpu")
     return {
+        "linear_forward": lambda **k: layer.forward(X, W, **k),
+        "linear_backward": lambda **k: layer.backward(X, **k),
+        "amax": lambda **k: F.fp8_amax(x, **k),
+        "quantize": lambda **k: F.fp8_quantize(X, F.E4M3, F.GRAN_ROW, transpose=True, want_amax=True, **k),
+        "quantize_counted": lambda **k: F.fp8_quantize_counted(x, F.E4M3, one, transpose=True, want_amax=True, **k),
+        "quantize_sr": lambda **k: F.fp8_quantize_sr(x, F.E4M3, one, 1, transpose=True, want_amax=True, **k),
+        "quantize_blocks": lambda **k: F.fp8_quantize_blocks(X, F.E4M3, F.GRAN_1x128, transpose=True, **k),
+        "gemm": lambda **k: F.fp8_gemm(**codes(), **k),
+        "gemm_group": lambda **k: F.fp8_gemm_group(group, group, **k),
         "norm_fwd": lambda **k: F.fp8_norm_fwd(x, x, w_pre=w, want_stats=True, q_fmt=F.E4M3, q_gran=F.GRAN_ROW, **k),
         "norm_bwd": lambda **k: F.fp8_norm_bwd(x, x, t(F32, 4, 8), h=x, gate=t(BF, 1, 32), post_norm=True, w_post=w,
                                                w_pre=w, **k),
@@ -86,9 +104,15 @@ def _calls():
     }
 
 
-@pytest.mark.parametrize("name", sorted(_calls()))
+NAMES = ["act_bwd", "act_bwd_experts", "amax", "gemm", "gemm_act", "gemm_group", "linear_backward", "linear_forward",
+         "norm_bwd", "norm_fwd", "permute", "plan", "quantize", "quantize_blocks", "quantize_counted", "quantize_sr",
+         "unpermute", "unpermute_bwd"]
+
+
+@pytest.mark.parametrize("name", NAMES)
 def test_memory_comes_from_the_stream_of_the_call(world, name):
     call = _calls()[name]
+    world.allocated.clear()     # what the arguments themselves took
     call(stream=7)
     assert world.allocated and set(world.allocated) == {7}
     assert [s for _, s in world.launched] == [7]
@@ -100,9 +124,9 @@ def test_memory_comes_from_the_stream_of_the_call(world, name):
 
 
 def test_stream_given_by_position(world):
-    x = torch.zeros(8, 32, dtype=BF)
-    F.fp8_moe_plan(torch.zeros(8, 2, dtype=I32), 4, 1, None, None, None, None, None, None, 7)
-    F.fp8_moe_unpermute(x, torch.zeros(8, 2, dtype=I32), None, None, 9)
+    x, ids = torch.full((8, 32), 0, dtype=BF), torch.full((8, 2), 0, dtype=I32)
+    F.fp8_moe_plan(ids, 4, 1, None, None, None, None, None, None, 7)
+    F.fp8_moe_unpermute(x, ids, None, None, 9)
     assert [s for _, s in world.launched] == [7, 9] and set(world.allocated) == {7, 9}
 
 

@@ -116,3 +116,38 @@ def test_from_a_graph(make):
     graph.replay()
     torch.cuda.synchronize()
     assert _same(got, want)
+
+
+def _casts_and_products(seed):
+    """The linears' own calls: casts (one adds to counters that it sets to
+    zero itself) and a product."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn(4096, 2048, generator=g, device=DEV).to(BF)
+    w = torch.randint(0, 0x70, (1024, 2048), generator=g, device=DEV, dtype=torch.uint8)
+    one, inv = torch.full((1,), 300.0, device=DEV), torch.full((1,), 2.0 ** -12, device=DEV)
+
+    def call(**k):
+        q, q_t, amax, counts = F.fp8_quantize_counted(x, F.E4M3, one, transpose=True, want_amax=True, **k)
+        blocks = F.fp8_quantize_blocks(x, F.E4M3, F.GRAN_1x128, transpose=True, **k)
+        return (q, q_t, amax, counts, *blocks, F.fp8_amax(x, **k),
+                F.fp8_gemm(q, F.E4M3, w, F.E4M3, inv, inv, out=F.OUT_F32, **k))
+    return call
+
+
+def _layer(seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    layer = F.Fp8Linear(2048, 1024, 1024, F.Recipe(F.SCALING_DYNAMIC))
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV).to(BF)
+    x, w, dy = r(2048, 1024), r(1024, 1024), r(2048, 1024)
+    return lambda **k: (layer.forward(x, w, **k), *layer.backward(dy, **k))
+
+
+@pytest.mark.parametrize("make", [_casts_and_products, _layer])
+def test_the_linears_on_two_streams(make):
+    here, there = make(1), make(2)
+    want = here(), there()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = [(here(), there(stream=s)) for _ in range(6)]
+    torch.cuda.synchronize()
+    assert all(_same(a, want[0]) and _same(b, want[1]) for a, b in got)
