@@ -190,6 +190,24 @@ def _under(stream, call, args):
         return call(**args)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_devices = None   # how many there are; of one, no tensor's number is asked for (0.1 us each)
+
+
+def _here(t):
+    """The number of t's device, which has to be the current one: the library
+    launches there.  None where there is no other device."""
+    global _devices
+    if _devices is None:
+        _devices = torch.cuda.device_count()
+    if _devices == 1:
+        return None
+    n = t.get_device()
+    if n >= 0 and n != _current_device():
+        raise ValueError(f"tensors on cuda:{n}, but the current device is cuda:{_current_device()}")
+    return n
+
+
 def _ptr(t, what, dtype=None, device=True):
     if t is None:
         return None
@@ -197,6 +215,8 @@ def _ptr(t, what, dtype=None, device=True):
         raise TypeError(f"{what}: expected a tensor")
     if device and not t.is_cuda:
         raise ValueError(f"{what}: must be a CUDA tensor")
+    if device and _devices != 1:
+        _here(t)
     if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
         raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
     if not t.is_contiguous():

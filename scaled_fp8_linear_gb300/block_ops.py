@@ -22,7 +22,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import (_U8, _ptr, _raw_stream, _stream, _under, _vp, E4M3, Fp8Error, GRAN_ROW, GRAN_TENSOR, OUT_BF16, OUT_F32,
+from . import (_U8, _here, _ptr, _raw_stream, _stream, _under, _vp, E4M3, Fp8Error, GRAN_ROW, GRAN_TENSOR, OUT_BF16, OUT_F32,
                fp8_last_error)
 from . import lib as _base_lib
 
@@ -169,24 +169,6 @@ def _lib():
             getattr(L, name).restype = i
         _ready = L
     return _ready
-
-
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-_devices = None   # how many there are; of one, no tensor's number is asked for (0.1 us each)
-
-
-def _here(t):
-    """The number of t's device, which has to be the current one: the library
-    launches there.  None where there is no other device."""
-    global _devices
-    if _devices is None:
-        _devices = torch.cuda.device_count()
-    if _devices == 1:
-        return None
-    n = t.get_device()
-    if n >= 0 and n != _current_device():
-        raise ValueError(f"tensors on cuda:{n}, but the current device is cuda:{_current_device()}")
-    return n
 
 
 def _given(t, what, dtype, shape, on):

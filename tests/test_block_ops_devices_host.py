@@ -38,8 +38,10 @@ class _Library:
 @pytest.fixture(autouse=True)
 def world(monkeypatch):
     monkeypatch.setattr(B, "_ready", _Library())
-    monkeypatch.setattr(B, "_current_device", lambda: 0, raising=False)
-    monkeypatch.setattr(B, "_devices", 2, raising=False)
+    monkeypatch.setattr(F, "_lib", _Library())
+    monkeypatch.setattr(F, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(F, "_devices", 2, raising=False)
+    monkeypatch.setattr(F, "_stream", lambda stream: 0)
     monkeypatch.setattr(B, "_on", lambda *a: 0)
     cached = (B.fp8_act_bwd_workspace_size, B.fp8_moe_rows, B.fp8_moe_workspace_size)
     for c in cached:
@@ -69,6 +71,15 @@ CALLS = {
     F.fp8_moe_unpermute: (dict(ys=(BF, 64, 32), row_of=(I32, 8, 2), weights=(F32, 8, 2), y=(BF, 8, 32)), {}),
     F.fp8_moe_unpermute_bwd: (dict(dy=(BF, 8, 32), ys=(BF, 64, 32), row_of=(I32, 8, 2), src=(I32, 64),
                                    weights=(F32, 8, 2), dys=(BF, 64, 32), dweights=(F32, 8, 2)), {}),
+    F.fp8_amax: (dict(x=(BF, 8, 32), amax=(F32, 1)), {}),
+    F.fp8_update_scale: (dict(amax=(F32, 1), history=(F32, 4), pos=(I32, 1), scale=(F32, 1), scale_inv=(F32, 1)),
+                         dict(history_len=4, algo=0, fmt=0, margin=0, pow2=False)),
+    F.fp8_quantize: (dict(x=(BF, 8, 32), scale=(F32, 1), q=(U8, 8, 32), q_t=(U8, 32, 8), amax_out=(F32, 1)),
+                     dict(fmt=0)),
+    F.fp8_quantize_counted: (dict(x=(BF, 8, 32), scale=(F32, 1), counts=(torch.int64, 2), q=(U8, 8, 32)), dict(fmt=0)),
+    F.fp8_quantize_sr: (dict(x=(BF, 8, 32), scale=(F32, 1), q=(U8, 8, 32)), dict(fmt=0, seed=1)),
+    F.fp8_gemm: (dict(A=(U8, 8, 32), B=(U8, 16, 32), scale_inv_a=(F32, 1), scale_inv_b=(F32, 1), bias=(BF, 16),
+                      D=(BF, 8, 16)), dict(fa=0, fb=0)),
 }
 CASES = [(call, name) for call, (tensors, _) in CALLS.items() for name in tensors]
 
@@ -99,12 +110,12 @@ def test_all_tensors_here(call):
 
 def test_one_device_only(monkeypatch):
     """Numbers are not asked for, host tensors are refused all the same."""
-    monkeypatch.setattr(B, "_devices", 1)
+    monkeypatch.setattr(F, "_devices", 1)
     with pytest.raises(AssertionError, match="was called"):
         _run(F.fp8_norm_fwd, {"rest": 0})
     x = torch.zeros(8, 32, dtype=BF)
     with pytest.raises(ValueError, match="CUDA"):
         F.fp8_norm_fwd(x, x)
-    monkeypatch.setattr(B, "_devices", 2)
+    monkeypatch.setattr(F, "_devices", 2)
     with pytest.raises(ValueError, match="CUDA"):
         F.fp8_norm_fwd(x, x)
