@@ -1015,27 +1015,34 @@ __global__ void __launch_bounds__(256) act_bwd_kernel(const __grid_constant__ Ac
 }
 
 // dbias[e][c] (+)= the sum of expert e's row blocks' partial sums: eight slices
-// of the blocks first, then the slices, in a fixed order.
+// of the blocks first, then the slices, in a fixed order.  Four columns a
+// thread: with many experts of few rows the CTAs' number is the cost (8192 x 2048
+// gated, 256 experts, gradient and sums 44 us, 69 with one column a thread).
+constexpr int kBiasCols = 128;   // a CTA
+
 __global__ void __launch_bounds__(256)
     expert_bias_kernel(const float* part, const int32_t* first, int64_t width, float* dbias, int accumulate) {
     ptx::griddep_launch_dependents();
-    __shared__ float sums[8][32];
+    __shared__ __align__(16) float sums[8][kBiasCols];
     ptx::griddep_wait();
     const int e = blockIdx.y, slice = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;   // width is a multiple of 16
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kBiasCols, c = c0 + 4 * lane;
     const int end = first[e + 1];
-    float s = 0.0f;
-    if (c < width) {
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (c < width) {   // a multiple of 16
 #pragma unroll 4
-        for (int i = first[e] + slice; i < end; i += 8) s += part[i * width + c];
+        for (int i = first[e] + slice; i < end; i += 8) {
+            const float4 v = *reinterpret_cast<const float4*>(part + i * width + c);
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        }
     }
-    sums[slice][lane] = s;
+    *reinterpret_cast<float4*>(&sums[slice][4 * lane]) = s;
     __syncthreads();
-    if (slice == 0 && c < width) {
+    if (threadIdx.x < kBiasCols && c0 + threadIdx.x < width) {
         float t = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t += sums[i][lane];
-        float* out = dbias + e * width + c;
+        for (int i = 0; i < 8; ++i) t += sums[i][threadIdx.x];
+        float* out = dbias + e * width + c0 + threadIdx.x;
         *out = accumulate ? *out + t : t;
     }
 }
@@ -1347,8 +1354,8 @@ int fp8_act_bwd(const fp8_act_bwd_args_t* a, void* workspace, size_t workspace_b
                            a->accumulate, st);
     } else if (a->dbias && a->M) {
         const float* part = static_cast<const float*>(workspace);
-        launch_pdl(expert_bias_kernel, dim3(static_cast<unsigned>((width + 31) / 32), a->experts), dim3(256), 0,
-                   st, part, reinterpret_cast<const int32_t*>(part + row_blocks * width), width, a->dbias,
+        launch_pdl(expert_bias_kernel, dim3(static_cast<unsigned>((width + kBiasCols - 1) / kBiasCols), a->experts),
+                   dim3(256), 0, st, part, reinterpret_cast<const int32_t*>(part + row_blocks * width), width, a->dbias,
                    a->accumulate != 0 ? 1 : 0);
     } else if (a->dbias && !a->accumulate) {   // no rows: zeros
         const cudaError_t e = cudaMemsetAsync(a->dbias, 0, static_cast<size_t>(a->experts) * width * 4, st);
