@@ -164,30 +164,30 @@ def _stream(stream) -> int:
     return int(stream)
 
 
-def _is_current(stream):
-    """Whether this is the current stream of the current device."""
-    if isinstance(stream, torch.cuda.Stream):
-        return stream.device_index == torch.cuda.current_device() and stream.cuda_stream == _stream(None)
-    return int(stream) == _stream(None)
-
-
-def _stream_context(stream):
-    """torch's context for a stream given as its object or as a raw handle."""
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-    return torch.cuda.stream(stream)
+_get_stream = getattr(torch._C, "_cuda_getCurrentStream", None)
+_set_stream = getattr(torch._C, "_cuda_setStream", None)
 
 
 def _under(stream, call, args):
-    """call(**args) with the given stream as the current one.  So all that the
-    call allocates comes from this stream's memory: a block of the caller's
-    stream may still be in use by work there that this stream does not wait
-    for, however long ago its tensor was freed."""
+    """call(**args) with the given stream (torch's object or a raw handle) as
+    the current one.  So all that the call allocates comes from this stream's
+    memory: a block of the caller's stream may still be in use by work there
+    that this stream does not wait for, however long ago its tensor was freed."""
     args["stream"] = None
-    if _is_current(stream):
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    n = stream.device_index
+    if _get_stream is None or _set_stream is None or n != _current_device():
+        with torch.cuda.stream(stream):
+            return call(**args)
+    was = _get_stream(n)   # (stream id, device, type); torch.cuda.stream() would take three times as long
+    if was[0] == stream.stream_id:
         return call(**args)
-    with _stream_context(stream):
+    _set_stream(stream.stream_id, n, was[2])
+    try:
         return call(**args)
+    finally:
+        _set_stream(*was)
 
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device

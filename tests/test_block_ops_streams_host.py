@@ -2,8 +2,6 @@
 allocator hands out blocks by the stream that is current, so every tensor
 that a call allocates has to be allocated with the given stream current.  One
 from another stream's pool may still be in use by that stream's work."""
-import contextlib
-
 import pytest
 import torch
 
@@ -36,13 +34,14 @@ def world(monkeypatch):
         now, allocated, launched = 1, [], []
     World.allocated, World.launched = [], []
 
-    @contextlib.contextmanager
-    def on(stream):
-        was, World.now = World.now, int(stream)
-        try:
-            yield
-        finally:
-            World.now = was
+    class Stream:
+        device_index = 0
+
+        def __init__(self, number):
+            self.stream_id = self.cuda_stream = number
+
+    def set_stream(stream_id, device_index, device_type):
+        World.now = stream_id
 
     def noted(make):
         def call(*a, **kw):
@@ -50,9 +49,13 @@ def world(monkeypatch):
             return make(*a, **kw)
         return call
 
-    for module in (F, B):
-        monkeypatch.setattr(module, "_stream_context", on, raising=False)
-        monkeypatch.setattr(module, "_is_current", lambda stream: int(stream) == World.now, raising=False)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(F, "_get_stream", lambda device: (World.now, 0, 1), raising=False)
+    monkeypatch.setattr(F, "_set_stream", set_stream, raising=False)
+    monkeypatch.setattr(F, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(F, "_devices", 1, raising=False)
+    World.Stream = Stream
     monkeypatch.setattr(B, "_on", lambda *a: World.now)
     monkeypatch.setattr(F, "_stream", lambda stream: World.now if stream is None else int(stream))
     monkeypatch.setattr(F, "_ptr", lambda t, *a: None if t is None else t.data_ptr() or 16)
@@ -109,11 +112,12 @@ NAMES = ["act_bwd", "act_bwd_experts", "amax", "gemm", "gemm_act", "gemm_group",
          "unpermute", "unpermute_bwd"]
 
 
+@pytest.mark.parametrize("by_object", [False, True])
 @pytest.mark.parametrize("name", NAMES)
-def test_memory_comes_from_the_stream_of_the_call(world, name):
+def test_memory_comes_from_the_stream_of_the_call(world, name, by_object):
     call = _calls()[name]
     world.allocated.clear()     # what the arguments themselves took
-    call(stream=7)
+    call(stream=world.Stream(7) if by_object else 7)
     assert world.allocated and set(world.allocated) == {7}
     assert [s for _, s in world.launched] == [7]
     assert world.now == 1
