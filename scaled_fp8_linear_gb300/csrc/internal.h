@@ -16,7 +16,8 @@ namespace fp8 {
 // Launch `kernel` on `stream` with programmatic stream serialisation: it may
 // start while the previous kernel of the stream finishes, and it waits for
 // that kernel (griddepcontrol.wait) before touching global memory -- every
-// kernel of this library does.  Errors are also left for cudaGetLastError().
+// kernel of this library does, but for the second launch of a product in two
+// (gemm_act_tile_kernel on a remainder), which waits at its end.  Errors are also left for cudaGetLastError().
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t stream, Args&&... args) {

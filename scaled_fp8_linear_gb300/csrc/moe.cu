@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         }
     }
     __syncthreads();
-    // offsets: the exclusive sum of the padded totals, four experts a thread
+    // offsets: the exclusive sum of the padded totals, kPer experts a thread
     constexpr int kPer = kMaxExperts / kPlanThreads;
     int pad[kPer], sum = 0;
 #pragma unroll
@@ -618,8 +618,9 @@ __global__ void __launch_bounds__(kRowThreads)
 // read once, and the next slot's piece of ys is loaded while this one's is
 // used.  8191 tokens' 8 rows of 14 KB: 364 us (5.8 TB/s; 446 reading dy again
 // for each slot, most of it from HBM).  Two and four pieces are held to 64
-// registers, for four CTAs an SM (373 us with three), one piece to 32, for
-// eight (8192 tokens' 8 rows of 2 KB: 52 us, 62 with five).
+// registers, for four CTAs an SM (373 us with three, although four bf16 pieces
+// then spill 48 bytes), one piece to 32, for eight (8192 tokens' 8 rows of
+// 2 KB: 52 us, 62 with five).
 template <typename T, int N, int VPT>
 __global__ void __launch_bounds__(kRowThreads, VPT == 1 ? 8 : 4)
     moe_unpermute_bwd_held_kernel(const T* __restrict__ dy, const T* __restrict__ ys,

@@ -727,7 +727,8 @@ __device__ __forceinline__ void flush(const float (&acc)[VPT][8], const int (&n)
 // the gate's and the post norm's gradients.
 //
 // This kernel takes rows wider than kFastWidth (4096 x 16384: 288 us; its sums
-// spill at 64 registers a thread), the resident one below the others.
+// spill, 800 to 3712 bytes at 64 registers a thread and fewer), the resident one
+// below the others.
 template <typename S, bool VEC, bool LAYER>
 __global__ void __launch_bounds__(1024)
     norm_bwd_any_kernel(const __grid_constant__ NormBwd p) {
@@ -942,7 +943,9 @@ __global__ void __launch_bounds__(1024)
 // registers to hold a row ahead.  8192 x 4096 bf16 with both norms and a gate
 // per sequence: 67 us (6.0 TB/s) and 8 us for the sums' kernel; loads straight
 // into registers took 146.  A stage is read piece by piece as the row
-// needs it, and filled again once every thread is past its last read.
+// needs it, and filled again once every thread is past its last read.  The layer
+// norm's two more running sums spill over a CTA's rows (144 to 376 bytes at 128
+// registers; up to 616 at other widths).
 // VEC: rows in 16-byte pieces.  Others start anywhere: a copy takes the 16-byte
 // pieces around them (cut at the tensor's end, whose last elements are then
 // read from global memory), and a thread's columns are a row's threads apart.

@@ -88,7 +88,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
 // serialisation: the next kernel in the stream can start (run its prologue)
 // while this one finishes.  Every kernel therefore calls griddep_wait() before
 // its first access to global memory (it returns at once when the kernel was
-// not launched that way).  The casts and GEMMs call griddep_launch_dependents()
+// not launched that way).  The one exception is a product's remainder
+// (gemm_act.cu): the launch before it belongs to the same product, writes other
+// rows and lets its dependents start only after its own wait, so the remainder
+// runs beside it and waits at its end.  The casts and GEMMs call griddep_launch_dependents()
 // early, which lets the next kernel launch once every CTA of this one has
 // started.  The tiny kernels (scale update, zeroing, finalisers) call it only
 // after their own griddep_wait(), when the kernel before them has completed:
