@@ -171,7 +171,8 @@ def _offsets(case, seed):
 
 def _scale(amax, top, pow2):
     """top / amax, of a block of zeros 1; rounded down to a power of two."""
-    s = torch.where(amax > 0, top / amax, torch.ones_like(amax))
+    # (a number over a tensor would be a reciprocal and a product: two roundings)
+    s = torch.where(amax > 0, torch.full_like(amax, top) / amax, torch.ones_like(amax))
     return torch.ldexp(torch.ones_like(s), torch.frexp(s).exponent - 1) if pow2 else s
 
 
