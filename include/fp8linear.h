@@ -614,6 +614,125 @@ int fp8_moe_unpermute_bwd(const void* dy, const void* ys, int type, const int32_
                           const int32_t* src, const float* weights, int64_t tokens, int slots,
                           int64_t width, int64_t rows, void* dys, float* dweights, void* stream);
 
+/* -------------------------------- experts and activations in blocks of 128
+ *
+ * The block recipe ("Block-wise scaling at 128 granularity") for experts and
+ * for the activations between two products.  As everywhere, a factor is
+ * 1 / scale, a 1x128 factor belongs to 128 consecutive elements of a row, and
+ * a block's scale is fp8_quantize's: fp8_max / amax, 1 for a block that is all
+ * zero or holds a NaN or Inf, rounded down to a power of two with pow2.
+ * Rows are sorted by expert; offsets [experts + 1] (device memory) are what
+ * fp8_moe_plan writes.  Offsets outside 0..M are held to it, and one below its
+ * predecessor counts as equal to it.  Rows before offsets[0] and past
+ * offsets[experts] are neither read nor written. */
+
+/* One product per expert: for the rows m of offsets[e] .. offsets[e + 1]
+ *   D[m][n] = sum_b sa[m][b] sb[e][n/128][b] sum_{k in block b} A[m][k] B[e][n][k]
+ * every 128-deep partial sum times its factors before it is added, in FP32.
+ * The forward product, and with the transposed weight codes the dgrad.  Any
+ * offsets; experts without rows cost nothing. */
+typedef struct {
+    const uint8_t* A;      /* [M][K] codes, 16-byte aligned                   */
+    const uint8_t* B;      /* [experts][N][K] codes, 16-byte aligned          */
+    int32_t fa, fb;        /* fp8_format_t                                    */
+    int64_t M, N, K;       /* M >= 0; N, K positive multiples of 128          */
+    const float* scale_inv_a;   /* [M][K/128]                                 */
+    const float* scale_inv_b;   /* [experts][N/128][K/128]                    */
+    int32_t pow2;          /* 1: every factor is a power of two (from pow2    */
+                           /*   casts), which the tensor core applies itself; */
+                           /*   only the factors' exponents are read then     */
+    int32_t out;           /* fp8_out_t of d                                  */
+    void* d;               /* [M][N], 16-byte aligned                         */
+    const int32_t* offsets;/* [experts + 1]                                   */
+    int32_t experts;       /* 1..256                                          */
+} fp8_gemm_experts_args_t;
+
+int fp8_gemm_experts(const fp8_gemm_experts_args_t* args, void* stream);
+
+/* The experts' weight gradients, without their row counts on the host:
+ *   dW[e][n][k] (+)= sum_b sy[n][b] sx[k][b] sum_{t in block b} dYt[n][t] Xt[k][t]
+ * over the blocks b of 128 tokens of offsets[e] .. offsets[e + 1], in FP32.
+ * The offsets are multiples of 128 (fp8_moe_plan with align = 128, whose pad
+ * rows hold zeros).  An expert whose offsets are not gets NaN for its gradient
+ * and sets bit 2 of the device status word.  An expert without tokens gets
+ * zeros, or keeps dW with accumulate. */
+typedef struct {
+    const uint8_t* dY_t;   /* [N][M] codes of dY^T, 16-byte aligned           */
+    const uint8_t* X_t;    /* [K][M] codes of X^T, 16-byte aligned            */
+    int32_t f_dy, f_x;     /* fp8_format_t                                    */
+    int64_t M, N, K;       /* multiples of 128; M >= 0 tokens, N, K > 0       */
+    const float* scale_inv_dy;  /* [N][M/128]                                 */
+    const float* scale_inv_x;   /* [K][M/128]                                 */
+    int32_t pow2;          /* as in fp8_gemm_experts                          */
+    int32_t accumulate;    /* add to dW                                       */
+    float* dW;             /* [experts][N][K], 16-byte aligned                */
+    const int32_t* offsets;/* [experts + 1]                                   */
+    int32_t experts;       /* 1..256                                          */
+} fp8_wgrad_experts_args_t;
+
+int fp8_wgrad_experts(const fp8_wgrad_experts_args_t* args, void* stream);
+
+/* The activation between two products, with an 8-bit checkpoint:
+ *   h = act(z), or gated: h[m][n] = act(z[m][n]) z[m][N + n]
+ *   q:   codes of h in 1x128 blocks (the FP32 h, rounded once)
+ *   z_q: E4M3 codes of z in 1x128 blocks, all that fp8_act_block_bwd needs of
+ *        the forward: 1.03 bytes an element of z, where bf16 takes 2
+ * Each of q and z_q is optional.  With offsets only the experts' rows are read
+ * and written. */
+typedef struct {
+    int64_t M, N;          /* M >= 0; N a positive multiple of 128            */
+    int32_t act, gated;    /* fp8_act_t; 0 or 1                               */
+    const void* z;         /* bf16 [M][N or 2N], 16-byte aligned              */
+    uint8_t* q;            /* [M][N], 16-byte aligned, nullable               */
+    float* scale_inv;      /* [M][N/128], with q                              */
+    int32_t q_format;
+    int32_t pow2;          /* of both casts                                   */
+    uint8_t* z_q;          /* [M][N or 2N], 16-byte aligned, nullable         */
+    float* z_scale_inv;    /* [M][N/128 or 2N/128], with z_q                  */
+    const int32_t* offsets;/* [experts + 1], nullable                         */
+    int32_t experts;       /* 1..256, read with offsets only                  */
+} fp8_act_block_args_t;
+
+int fp8_act_block(const fp8_act_block_args_t* args, void* stream);
+
+/* Its gradient from the checkpoint z^ (codes times factors):
+ *   dz = dD act'(z^); gated: dz_gate = dD z^_up act'(z^_gate), dz_up = dD act(z^_gate)
+ *   q:   codes of dz in 1x128 blocks of its rows (the dgrad's operand)
+ *   q_t: codes of dz^T in 1x128 blocks along the tokens (the wgrad's)
+ *   h_t: codes of h^T, h = act(z^) [z^_up] as the forward had it but for the
+ *        checkpoint's rounding (the next product's wgrad operand)
+ * Each output is optional; every one is a rounding of the FP32 value.  q_t and
+ * h_t need M a multiple of 128.  With offsets only the experts' rows are read
+ * and written; in a block of 128 tokens that holds rows of experts and others,
+ * q_t and h_t hold zeros for the others. */
+typedef struct {
+    int64_t M, N;          /* N a positive multiple of 128                    */
+    int32_t act, gated;
+    const void* dD;        /* bf16 [M][N], 16-byte aligned                    */
+    const uint8_t* z_q;    /* [M][N or 2N] E4M3, as fp8_act_block wrote it    */
+    const float* z_scale_inv;
+    uint8_t* q;            /* [M][N or 2N], 16-byte aligned, nullable         */
+    float* scale_inv;      /* [M][N/128 or 2N/128], with q                    */
+    uint8_t* q_t;          /* [N or 2N][M], 16-byte aligned, nullable         */
+    float* scale_inv_t;    /* [N or 2N][M/128], with q_t                      */
+    int32_t q_format;      /* of q and q_t                                    */
+    uint8_t* h_t;          /* [N][M], 16-byte aligned, nullable               */
+    float* h_scale_inv_t;  /* [N][M/128], with h_t                            */
+    int32_t h_format;
+    int32_t pow2;          /* of all casts                                    */
+    const int32_t* offsets;/* [experts + 1], nullable                         */
+    int32_t experts;       /* 1..256, read with offsets only                  */
+} fp8_act_block_bwd_args_t;
+
+int fp8_act_block_bwd(const fp8_act_block_bwd_args_t* args, void* stream);
+
+/* A product's kept input x^ (codes in 1x128 blocks of its rows, times their
+ * factors) as its wgrad's operand: q_t [cols][rows] holds x^'s transpose in
+ * 1x128 blocks along the rows, with scale_inv_t [cols][rows/128].  rows and
+ * cols are multiples of 128, rows >= 0, cols > 0; format is both codes'. */
+int fp8_block_transpose(const uint8_t* q, const float* scale_inv, int64_t rows, int64_t cols, int format,
+                        int pow2, uint8_t* q_t, float* scale_inv_t, void* stream);
+
 /* Message of the last failing call on this host thread ("" if none). */
 const char* fp8_last_error(void);
 
@@ -622,7 +741,9 @@ const char* fp8_last_error(void);
  *   bit 1 (2): a scale update met a non-finite amax -- a NaN or Inf in a
  *              cast tensor, or still in its amax history -- and kept the
  *              previous scale ("Numerical-failure taxonomy": NaN / Inf are
- *              caught at the first step that sees them).
+ *              caught at the first step that sees them);
+ *   bit 2 (4): fp8_wgrad_experts met offsets that are no multiples of 128
+ *              and wrote NaN for those experts.
  * Synchronises the device.  Returns FP8_OK and *status = 0 when every
  * kernel finished normally. */
 int fp8_device_status(int* status, int clear);

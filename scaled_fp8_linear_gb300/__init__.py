@@ -28,7 +28,7 @@ __all__ = [
     "fp8_quantize_counted", "fp8_quantize_sr", "fp8_gemm", "fp8_gemm_group", "GemmArgsC",
     "fp8_workspace_size",
     "fp8_linear_fwd", "fp8_linear_bwd", "fp8_last_error", "fp8_device_status",
-    "check_device_status", "Fp8NumericsError", "STATUS_TIMEOUT", "STATUS_NONFINITE",
+    "check_device_status", "Fp8NumericsError", "STATUS_TIMEOUT", "STATUS_NONFINITE", "STATUS_OFFSETS",
 ]
 
 E4M3, E5M2 = 0, 1
@@ -454,17 +454,21 @@ def fp8_device_status(clear: bool = True) -> int:
 
 STATUS_TIMEOUT = 1     # bit 0 of the device status word: a bounded wait gave up
 STATUS_NONFINITE = 2   # bit 1: a scale update met a non-finite amax
+STATUS_OFFSETS = 4     # bit 2: fp8_wgrad_experts met offsets that are no multiples of 128
 
 
 def check_device_status() -> None:
     """Synchronise the device, read and clear the status word, and raise if a
     kernel reported a problem since the last read: Fp8Error with status
     FP8_ERR_TIMEOUT when a bounded wait gave up (that call's outputs are
-    incomplete), else Fp8NumericsError when a scale update met a NaN or Inf
-    (the previous scale was kept)."""
+    incomplete), ValueError when fp8_wgrad_experts met offsets that are no
+    multiples of 128 (those experts' gradients are NaN), else Fp8NumericsError
+    when a scale update met a NaN or Inf (the previous scale was kept)."""
     st = fp8_device_status(clear=True)
     if st & STATUS_TIMEOUT:
         raise Fp8Error(-5, "a kernel's bounded wait gave up; its outputs are incomplete")
+    if st & STATUS_OFFSETS:
+        raise ValueError("fp8_wgrad_experts: offsets that are no multiples of 128; those experts' gradients are NaN")
     if st & STATUS_NONFINITE:
         raise Fp8NumericsError("a scale update met a non-finite amax (NaN or Inf in a cast "
                                "tensor or its amax history); the previous scale was kept")
@@ -578,4 +582,7 @@ class Fp8Linear:
 from . import block_ops as _block_ops   # noqa: E402
 from .block_ops import *                # noqa: E402,F401,F403
 
-__all__ += _block_ops.__all__
+from . import expert_ops as _expert_ops   # noqa: E402
+from .expert_ops import *                 # noqa: E402,F401,F403
+
+__all__ += _block_ops.__all__ + _expert_ops.__all__

@@ -44,6 +44,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/fp8linear.h"
+#include "experts.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -78,6 +79,25 @@ struct GemmParams {
     int accumulate;
     int a_mn, b_mn;   // operand stored MN-major ([K x M] / [K x N]); CTA pairs, or 128 x 128 single-CTA tiles
     int group;        // CTA-pair kernel: raster group (M-blocks), see pair_group()
+    const int32_t* offsets;   // kByRows, kByTokens: [experts + 1]
+    int experts;
+};
+
+// What a block-scaled kernel's problem is: one product; one product per expert
+// over the expert's rows of A and D (B and its factors: [experts] of [N x K]);
+// or one weight gradient per expert over the expert's K (tokens), whole
+// 128-deep blocks of it (D: [experts] of [M x N]).
+enum { kDense = 0, kByRows = 1, kByTokens = 2 };
+
+// A 256-row tile of a block-scaled product.
+struct BlockTile {
+    int ya, yb;         // first row of A and of B as loaded
+    int n0;             // first column of D
+    int kb0, kb1;       // K blocks kb0 .. kb1 - 1
+    int m_end;          // rows of D from here on are not this tile's
+    int b_row;          // row of B that column 0 of D takes
+    int d_row;          // row of D that row 0 of A is
+    bool lost;          // kByTokens: offsets that are no multiples of 128, D gets NaN
 };
 
 // Eight bias values of columns n .. n+7 (n % 8 == 0) as fp32; every lane of
@@ -118,6 +138,62 @@ __device__ __forceinline__ void tile_coords_g(int tile, int num_m, int num_n, in
     const int in_g = tile - g * per_group;
     m_blk = first_m + in_g % gsize;
     n_blk = in_g / gsize;
+}
+
+// The tile of unit u.  m_tile and n_tile: its rows and columns.
+template <int MODE>
+__device__ __forceinline__ BlockTile block_tile(int u, const Units* units, const GemmParams& p, int n_tile) {
+    BlockTile t;
+    int e = 0, local = u, num_m = p.num_m;
+    if (MODE == kByRows) {
+        e = expert_of(u, units, p.experts);
+        local = u - units->first[e];
+        num_m = (units->end[e] - units->begin[e] + 255) / 256;
+    } else if (MODE == kByTokens) {
+        const int each = p.num_m * p.num_n;
+        e = u / each;
+        local = u - e * each;
+    }
+    int m_blk, n_blk;
+    tile_coords_g(local, num_m, p.num_n, p.group, m_blk, n_blk);
+    t.n0 = n_blk * n_tile;
+    t.ya = m_blk * 256;
+    t.yb = t.n0;
+    t.kb0 = 0;
+    t.kb1 = p.num_kb;
+    t.m_end = static_cast<int>(p.M);
+    t.b_row = t.d_row = 0;
+    t.lost = false;
+    if (MODE == kByRows) {
+        t.ya += units->begin[e];
+        t.m_end = units->end[e];
+        t.b_row = e * static_cast<int>(p.N);
+        t.yb += t.b_row;
+    } else if (MODE == kByTokens) {
+        t.d_row = e * static_cast<int>(p.M);
+        t.lost = ((units->begin[e] | units->end[e]) & 127) != 0;
+        t.kb0 = units->begin[e] >> 7;
+        t.kb1 = t.lost ? t.kb0 : units->end[e] >> 7;
+    }
+    return t;
+}
+
+template <int MODE>
+__device__ __forceinline__ int block_units(const Units* units, const GemmParams& p) {
+    if (MODE == kByRows) return units->first[p.experts];
+    return p.num_m * p.num_n * (MODE == kByTokens ? p.experts : 1);
+}
+
+// Fills `units` (every thread, ends with a barrier); kByTokens: reports offsets
+// that are no multiples of 128.
+template <int MODE>
+__device__ __forceinline__ void make_block_units(Units* units, const GemmParams& p) {
+    if (MODE == kDense) return;
+    const int64_t limit = MODE == kByRows ? p.M : p.K;
+    make_units(units, static_cast<int>(limit), p.offsets, p.experts, p.num_n, kAllRows, 256);
+    if (MODE == kByTokens && blockIdx.x == 0 && static_cast<int>(threadIdx.x) < p.experts &&
+        ((units->begin[threadIdx.x] | units->end[threadIdx.x]) & 127) != 0)
+        atomicOr(&g_device_status, 4u);
 }
 
 template <int BN, int STAGES>
@@ -259,10 +335,12 @@ __device__ __forceinline__ void emit_box(uint8_t* slot, const uint4 (&piece)[4],
 
 // FP32 output of one 32-column accumulator chunk of a warp's 32 rows (first
 // row m0, first column n0): v = fp32(acc * f) (+ bias), as two 16-column TMA
-// boxes through `slot`, stored or (accumulate) added.  Whole-warp call.
+// boxes through `slot`, stored or (accumulate) added at row y of D if m0 is
+// below m_end.  Whole-warp call.
 __device__ __forceinline__ void emit_f32_chunk(uint8_t* slot, const uint32_t (&r)[32],
                                                const float (&f)[32], int64_t m0, int64_t n0,
-                                               const GemmParams& p, const CUtensorMap* map) {
+                                               const GemmParams& p, const CUtensorMap* map,
+                                               int64_t m_end, int64_t y) {
     float v[32];
 #pragma unroll
     for (int e = 0; e < 32; ++e) v[e] = __fmul_rn(__uint_as_float(r[e]), f[e]);
@@ -287,7 +365,7 @@ __device__ __forceinline__ void emit_f32_chunk(uint8_t* slot, const uint32_t (&r
                                   __float_as_uint(v[16 * hb + 4 * j + 2]),
                                   __float_as_uint(v[16 * hb + 4 * j + 3]));
         const int64_t x = n0 + 16 * hb;
-        emit_box(slot, piece, map, x, m0, m0 < p.M && x < p.N, p.accumulate != 0);
+        emit_box(slot, piece, map, x, y, m0 < m_end && x < p.N, p.accumulate != 0);
     }
 }
 
@@ -717,7 +795,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                 const int64_t n0 = static_cast<int64_t>(n_blk) * TILE + c * 32;
                 float f[32];
                 chunk_factors(f, fa, n0, p);
-                if (f32) emit_f32_chunk(slot, r, f, m0, n0, p, map);
+                if (f32) emit_f32_chunk(slot, r, f, m0, n0, p, map, p.M, m0);
                 else emit_bf16_chunk(slot, r, f, m0, n0, p, map);
             }
             ptx::tc_fence_before();
@@ -818,9 +896,9 @@ struct BpCfg {
     // shared memory: operand ring, 2 KB of output staging per promotion
     // warp, per-column and per-row factors (COLSCALE only), barriers,
     // alignment slack
-    static constexpr int smem(bool colscale) {
+    static constexpr int smem(bool colscale, bool experts) {
         return STAGES * STAGE_BYTES + EPI * (2048 + (colscale ? 4 * (CW + 32) * 4 : 0)) + 256 +
-               1024;
+               (experts ? static_cast<int>(sizeof(Units)) : 0) + 1024;
     }
     static_assert(CW == 64, "a warp's columns: one 64-column slice of a 128-column factor "
                             "block, loaded as two 32-column chunks");
@@ -882,20 +960,43 @@ __device__ __forceinline__ void promote_columns(uint64_t* acc, const uint32_t* r
     }
 }
 
+// 32 columns of this thread's row m0 + lane, if the expert has it: what a box
+// that ends within another expert's rows is written by.
+__device__ __forceinline__ void store_part_row(const float (&v)[32], int64_t m0, int64_t n0, int m_end,
+                                               const GemmParams& p) {
+    const int64_t m = m0 + (threadIdx.x & 31);
+    if (m >= m_end) return;
+    if (p.out == FP8_OUT_BF16) {
+        uint4* d = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.D) + m * p.N + n0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            d[j] = make_uint4(row::pack_bf16(v[8 * j], v[8 * j + 1]), row::pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                              row::pack_bf16(v[8 * j + 4], v[8 * j + 5]),
+                              row::pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+    } else {
+        float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.D) + m * p.N + n0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    }
+}
+
 // Round one promoted 32-column chunk (16 packed pairs) plus the bias (if
 // any) and write it through the warp's staging slot: one bf16 box of 32
 // columns, or two FP32 boxes of 16 columns (added to D when accumulating).
 // Whole-warp call; m0 is the warp's first row, n0 the chunk's first column.
-__device__ __forceinline__ void emit_block_chunk(uint8_t* slot, const uint64_t* acc, int64_t m0,
-                                                 int64_t n0, const GemmParams& p,
+template <int MODE>
+__device__ __forceinline__ void emit_block_chunk(uint8_t* slot, const uint64_t* acc, const BlockTile& t,
+                                                 int64_t m0, int64_t n0, const GemmParams& p,
                                                  const CUtensorMap* map) {
+    const bool in_range = m0 < t.m_end;
+    const int64_t y = MODE == kByTokens ? t.d_row + m0 : m0;   // row of D
     float v[32];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
         v[2 * e] = __uint_as_float(static_cast<uint32_t>(acc[e]));
         v[2 * e + 1] = __uint_as_float(static_cast<uint32_t>(acc[e] >> 32));
     }
-    if (p.bias) {
+    if (MODE == kDense && p.bias) {
 #pragma unroll
         for (int j = 0; j < 32; j += 8) {
             float b[8];
@@ -903,6 +1004,10 @@ __device__ __forceinline__ void emit_block_chunk(uint8_t* slot, const uint64_t* 
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[j + e] = __fadd_rn(v[j + e], b[e]);
         }
+    }
+    if (MODE == kByRows && m0 + 32 > t.m_end) {   // the box would reach into another expert's rows
+        store_part_row(v, m0, n0, t.m_end, p);
+        return;
     }
     if (p.out == FP8_OUT_BF16) {
         uint32_t w[16];
@@ -914,7 +1019,7 @@ __device__ __forceinline__ void emit_block_chunk(uint8_t* slot, const uint64_t* 
         const uint4 piece[4] = {make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]),
                                 make_uint4(w[8], w[9], w[10], w[11]),
                                 make_uint4(w[12], w[13], w[14], w[15])};
-        emit_box(slot, piece, map, n0, m0, m0 < p.M, false);
+        emit_box(slot, piece, map, n0, y, in_range, false);
     } else {
 #pragma unroll
         for (int hb = 0; hb < 2; ++hb) {
@@ -925,12 +1030,12 @@ __device__ __forceinline__ void emit_block_chunk(uint8_t* slot, const uint64_t* 
                                       __float_as_uint(v[16 * hb + 4 * j + 1]),
                                       __float_as_uint(v[16 * hb + 4 * j + 2]),
                                       __float_as_uint(v[16 * hb + 4 * j + 3]));
-            emit_box(slot, piece, map, n0 + 16 * hb, m0, m0 < p.M, p.accumulate != 0);
+            emit_box(slot, piece, map, n0 + 16 * hb, y, in_range, p.accumulate != 0);
         }
     }
 }
 
-template <typename Cfg, bool COLSCALE>
+template <typename Cfg, bool COLSCALE, int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                            const __grid_constant__ CUtensorMap tmB,
@@ -955,6 +1060,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     uint64_t* done = tempty + NBUF;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile uint32_t* abort_flag = tmem_slot + 1;
+    Units* units = reinterpret_cast<Units*>(reinterpret_cast<uint8_t*>(full) + 256);   // experts' rows
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = ptx::cluster_ctarank();
@@ -986,8 +1092,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     ptx::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     ptx::griddep_wait();   // the previous kernel's results (operands, factors) are visible
+    make_block_units<MODE>(units, p);
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    const int num_units = p.num_m * p.num_n;
+    const int num_units = block_units<MODE>(units, p);
     const int KB = p.num_kb;
 
     if (warp < 4) {
@@ -998,11 +1105,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             int64_t issued = 0;
             bool ok = true;
             for (int u = pair; ok && u < num_units; u += npairs) {
-                int m_blk, n_blk;
-                tile_coords_g(u, p.num_m, p.num_n, p.group, m_blk, n_blk);
-                const int ya = m_blk * 256 + static_cast<int>(rank) * 128;
-                const int yb = n_blk * TN + static_cast<int>(rank) * (TN / 2);
-                for (int kb = 0; kb < KB; ++kb) {
+                const BlockTile t = block_tile<MODE>(u, units, p, TN);
+                const int ya = t.ya + static_cast<int>(rank) * 128;
+                const int yb = t.yb + static_cast<int>(rank) * (TN / 2);
+                for (int kb = t.kb0; kb < t.kb1; ++kb) {
                     if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
                     uint8_t* sa = ring + stage * STAGE_BYTES;
                     const uint32_t bar = ptx::cluster_addr(&full[stage], 0);
@@ -1035,7 +1141,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
             bool ok = true;
             for (int u = pair; ok && u < num_units; u += npairs) {
-                for (int kb = 0; kb < KB; ++kb) {
+                const BlockTile t = block_tile<MODE>(u, units, p, TN);
+                for (int kb = t.kb0; kb < t.kb1; ++kb) {
                     if (!ptx::mbar_wait(&tempty[buf], buf_phase ^ 1u, abort_flag)) { ok = false; break; }
                     if (!ptx::mbar_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
                     ptx::tc_fence_after();
@@ -1073,21 +1180,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         uint32_t buf = 0, buf_phase = 0;
         bool ok = true;
         for (int u = pair; ok && u < num_units; u += npairs) {
-            int m_blk, n_blk;
-            tile_coords_g(u, p.num_m, p.num_n, p.group, m_blk, n_blk);
-            const int64_t m0 = static_cast<int64_t>(m_blk) * 256 + rank * 128 + qd * 32;
+            const BlockTile t = block_tile<MODE>(u, units, p, TN);
+            const int64_t m0 = static_cast<int64_t>(t.ya) + rank * 128 + qd * 32;
             const int64_t m = m0 + lane;
             const int64_t m_safe = m < p.M ? m : p.M - 1;
-            const int64_t n0 = static_cast<int64_t>(n_blk) * TN + h * CW;
+            const int64_t n0 = static_cast<int64_t>(t.n0) + h * CW;
             // a warp's columns lie all inside or all outside [0, N) (N is a
             // multiple of 128, CW divides 128); outside, its factors are
             // read at column N - 1 and its columns are not stored
-            const int64_t nf = n0 < p.N ? n0 : p.N - 1;
+            const int64_t nf = t.b_row + (n0 < p.N ? n0 : p.N - 1);
             // FP32 accumulator of CW columns, as packed pairs
             uint64_t acc[CW / 2];
 #pragma unroll
             for (int e = 0; e < CW / 2; ++e) acc[e] = 0ull;
-            for (int kb0 = 0; ok && kb0 < KB; kb0 += 4) {
+            // an expert's first K block is any: groups of four stay aligned
+            for (int kb0 = MODE == kByTokens ? t.kb0 & ~3 : 0; ok && kb0 < t.kb1; kb0 += 4) {
                 // The factors of four K blocks, read at the start of the group
                 // (they hit L1; holding the next group's in registers made the
                 // loop spill): A per row; B per 128-column block, multiplied
@@ -1115,7 +1222,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (kb0 + j >= KB) break;
+                    if (kb0 + j >= t.kb1) break;
+                    if (MODE == kByTokens && kb0 + j < t.kb0) continue;
                     ok = (lane == 0) ? ptx::mbar_wait(&tfull[buf], buf_phase, abort_flag) : false;
                     ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
                     if (!ok) break;
@@ -1163,9 +1271,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                 }
             }
             if (!ok) break;
+            if (MODE == kByTokens && t.kb0 == t.kb1) {   // no tokens: zeros, or nothing to add
+                if (t.lost) {
+                    const float nan = __int_as_float(0x7FC00000);
+#pragma unroll
+                    for (int e = 0; e < CW / 2; ++e) acc[e] = pack2(nan, nan);
+                } else if (p.accumulate) {
+                    continue;
+                }
+            }
 #pragma unroll
             for (int c = 0; c < NCH; ++c)
-                if (n0 < p.N) emit_block_chunk(slot, acc + 16 * c, m0, n0 + 32 * c, p, &tmD);
+                if (n0 < p.N) emit_block_chunk<MODE>(slot, acc + 16 * c, t, m0, n0 + 32 * c, p, &tmD);
         }
         if (lane == 0) ptx::bulk_wait_group_all();   // every TMA store has completed
         __syncwarp();
@@ -1285,7 +1402,7 @@ __device__ __forceinline__ void pack_bf16_chunk(uint32_t (&pk)[16], const uint32
     }
 }
 
-template <int STAGES, int SFS>
+template <int STAGES, int SFS, int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA,
                    const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmD,
@@ -1315,6 +1432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     uint64_t* done = tempty + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile uint32_t* abort_flag = tmem_slot + 1;
+    Units* units = reinterpret_cast<Units*>(reinterpret_cast<uint8_t*>(full) + 512);   // experts' rows
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = ptx::cluster_ctarank();
@@ -1349,8 +1467,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     const uint32_t tmem_base = *tmem_slot;
     ptx::griddep_wait();   // the previous kernel's results (operands, factors) are visible
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    const int num_units = p.num_m * p.num_n;
-    const int num_slots = (p.num_kb + KPS - 1) / KPS;   // factor slots per tile
+    make_block_units<MODE>(units, p);
+    const int num_units = block_units<MODE>(units, p);
 
     if (warp == 0) {
         if (lane == 0) {
@@ -1358,11 +1476,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
             int64_t issued = 0;
             bool ok = true;
             for (int u = pair; ok && u < num_units; u += npairs) {
-                int m_blk, n_blk;
-                tile_coords_g(u, p.num_m, p.num_n, p.group, m_blk, n_blk);
-                const int ya = m_blk * TILE + static_cast<int>(rank) * HALF;
-                const int yb = n_blk * TILE + static_cast<int>(rank) * HALF;
-                for (int kb = 0; kb < p.num_kb; ++kb) {
+                const BlockTile t = block_tile<MODE>(u, units, p, TILE);
+                const int ya = t.ya + static_cast<int>(rank) * HALF;
+                const int yb = t.yb + static_cast<int>(rank) * HALF;
+                for (int kb = t.kb0; kb < t.kb1; ++kb) {
                     if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
                     uint8_t* sa = ring + stage * STAGE_BYTES;
                     const uint32_t bar = ptx::cluster_addr(&full[stage], 0);
@@ -1396,11 +1513,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
             uint32_t stage = 0, phase = 0, sfs = 0, sf_phase = 0, acc_phase = 0;
             bool ok = true;
             for (int u = pair; ok && u < num_units; u += npairs) {
+                const BlockTile t = block_tile<MODE>(u, units, p, TILE);
+                if (MODE == kByTokens && t.kb0 == t.kb1) continue;   // nothing to multiply
                 if (!ptx::mbar_wait(tempty, acc_phase ^ 1u, abort_flag)) break;
                 ptx::tc_fence_after();
-                for (int kb = 0; kb < p.num_kb; ++kb) {
+                // K blocks from a multiple of four: a factor word's four share one
+                const int base = MODE == kByTokens ? t.kb0 & ~3 : 0, last = t.kb1 - base;
+                for (int kb = t.kb0 - base; kb < last; ++kb) {
                     if (!ptx::mbar_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
-                    if ((kb % KPS) == 0 &&
+                    if (((kb % KPS) == 0 || (MODE == kByTokens && kb == t.kb0 - base)) &&
                         !ptx::mbar_wait(&sf_full[sfs], sf_phase, abort_flag)) { ok = false; break; }
                     ptx::tc_fence_after();
                     uint8_t* sa = ring + stage * STAGE_BYTES;
@@ -1414,10 +1535,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
 #pragma unroll
                     for (int k = 0; k < BK / UMMA_K; ++k)
                         ptx::mma_mxf8f6f4_pair(tmem_base, ad + (k * UMMA_K >> 4),
-                                               bd + (k * UMMA_K >> 4), id, sfa, sfb, (kb | k) != 0);
+                                               bd + (k * UMMA_K >> 4), id, sfa, sfb,
+                                               kb > t.kb0 - base || k != 0);
                     ptx::mma_commit_pair(&empty[stage], 0x3);
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                    if ((kb % KPS) == KPS - 1 || kb == p.num_kb - 1) {   // the slot's last K block
+                    if ((kb % KPS) == KPS - 1 || kb == last - 1) {   // the slot's last K block
                         ptx::mma_commit_pair(&sf_empty[sfs], 0x3);
                         if (++sfs == SFS) { sfs = 0; sf_phase ^= 1u; }
                     }
@@ -1443,15 +1565,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         // (so that the other three cannot wait on it forever) but does nothing else
         bool live = true;
         for (int u = pair; u < num_units; u += npairs) {
-            int m_blk, n_blk;
-            tile_coords_g(u, p.num_m, p.num_n, p.group, m_blk, n_blk);
-            const int64_t a0 = static_cast<int64_t>(m_blk) * TILE + rank * HALF;
-            const int64_t b0 = static_cast<int64_t>(n_blk) * TILE;
+            const BlockTile t = block_tile<MODE>(u, units, p, TILE);
+            const int64_t a0 = static_cast<int64_t>(t.ya) + rank * HALF;
+            const int64_t b0 = static_cast<int64_t>(t.n0);
+            const int base = MODE == kByTokens ? t.kb0 & ~3 : 0;
+            const int num_slots =   // factor slots of this tile
+                MODE == kByTokens && t.kb0 == t.kb1 ? 0 : (t.kb1 - base + KPS - 1) / KPS;
             for (int s2 = 0; s2 < num_slots; ++s2) {
                 uint32_t* sta = stage_a + buf * kMxStageA;
                 uint32_t* stb = stage_b + buf * kMxStageB;
                 if (live) {
-                    const int kb0 = KPS * s2 + 4 * kq;
+                    const int kb0 = base + KPS * s2 + 4 * kq;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int row = q * 32 + 8 * i + rsub;
@@ -1463,7 +1587,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
                     for (int i = 0; i < 8; ++i) {
                         const int row = q * 64 + 8 * i + rsub;
                         float f[4];
-                        mx_load4(f, p.sb, p.gb, b0 + row, p.N, kb0, p.num_kb, vec_b != 0);
+                        mx_load4(f, p.sb, p.gb, t.b_row + (b0 + row < p.N ? b0 + row : 0), t.b_row + p.N, kb0,
+                                 p.num_kb, vec_b != 0);
                         stb[kq * 264 + row] = ue8m0_word(f);
                     }
                 }
@@ -1516,10 +1641,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         for (int j = 0; j < 32; ++j) ones[j] = 1.0f;
         uint32_t acc_phase = 0;
         for (int u = pair; u < num_units; u += npairs) {
-            int m_blk, n_blk;
-            tile_coords_g(u, p.num_m, p.num_n, p.group, m_blk, n_blk);
-            const int64_t m0 = static_cast<int64_t>(m_blk) * TILE + rank * HALF + q * 32;
-            const int64_t n0 = static_cast<int64_t>(n_blk) * TILE + h * 128;
+            const BlockTile t = block_tile<MODE>(u, units, p, TILE);
+            const int64_t m0 = static_cast<int64_t>(t.ya) + rank * HALF + q * 32;
+            const int64_t n0 = static_cast<int64_t>(t.n0) + h * 128;
+            const int64_t y = MODE == kByTokens ? t.d_row + m0 : m0;   // row of D
+            if (MODE == kByTokens && t.kb0 == t.kb1) {   // no tokens: zeros, or nothing to add
+                if (!t.lost && add) continue;
+                const uint32_t w = t.lost ? 0x7FC00000u : 0u;
+                const uint4 piece[4] = {make_uint4(w, w, w, w), make_uint4(w, w, w, w),
+                                        make_uint4(w, w, w, w), make_uint4(w, w, w, w)};
+                for (int c = 0; c < 8; ++c)
+                    emit_box(stg, piece, &tmD, n0 + 16 * c, y, m0 < t.m_end && n0 + 16 * c < p.N, add);
+                continue;
+            }
             bool ok = (lane == 0) ? ptx::mbar_wait(tfull, acc_phase, abort_flag) : false;
             ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
             if (!ok) break;
@@ -1528,9 +1662,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + h * 128;
             // one staged 32-row x 64-byte box to global memory at column x
             auto emit = [&](const uint4 (&piece)[4], int64_t x) {
-                emit_box(stg, piece, &tmD, x, m0, m0 < p.M && x < p.N, add);
+                emit_box(stg, piece, &tmD, x, y, m0 < t.m_end && x < p.N, add);
             };
-            if (!f32) {
+            // the warp's rows end among another expert's: each thread stores its own
+            const bool part = MODE == kByRows && m0 < t.m_end && m0 + 32 > t.m_end;
+            if (part) {
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t r[32];
+                    ptx::tmem_ld_32x32b_x32(tbase + c * 32, r);
+                    ptx::tmem_wait_ld();
+                    float v[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+                    if (n0 + c * 32 < p.N) store_part_row(v, m0, n0 + c * 32, t.m_end, p);
+                }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::cluster_addr(tempty, 0));
+            } else if (!f32) {
                 // read and pack the 128 columns first, hand the accumulator back,
                 // then stage and store
                 uint32_t pk[4][16];
@@ -1571,7 +1721,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
                     }
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        emit_f32_chunk(stg, r[i], ones, m0, n0 + (c + i) * 32, p, &tmD);
+                        emit_f32_chunk(stg, r[i], ones, m0, n0 + (c + i) * 32, p, &tmD, t.m_end, y);
                 }
             }
             acc_phase ^= 1u;
@@ -1747,9 +1897,9 @@ int ensure_smem(Kernel k, int bytes, int kernel_id) {
 // persistent grid size); cached per device.
 int pair_clusters(const void* func, int kernel_id, int threads, int smem) {
     static std::mutex mu;
-    static int cache[64][5] = {};   // [device][kernel id]: 0 single, 1 grouped pair kernel,
+    static int cache[64][9] = {};   // [device][kernel id]: 0 single, 1 grouped pair kernel,
                                     // 2 power-of-two block kernel, 3 / 4 fp32-factor block
-                                    // kernel (row / column factors on B)
+                                    // kernel (row / column factors on B), 5-8 the experts'
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
     int uncached = 0;                            // devices past the table: computed per call
@@ -1814,87 +1964,94 @@ int pair_group(int64_t K) {
     return g;
 }
 
-// Block-scaled GEMM with power-of-two factors on the CTA-pair block-scaled
-// MMA kernel (ga, gb: FP8_GRAN_1x128 / FP8_GRAN_128x128, flag removed; K > 0).
-int launch_gemm_mx(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t N,
-                   int64_t K, int ga, const float* sa, int gb, const float* sb, const void* bias,
-                   void* D, int out, int accumulate, cudaStream_t stream) {
-    GemmParams p;
-    p.M = M; p.N = N; p.K = K;
-    p.num_m = static_cast<int>((M + 255) / 256);
-    p.num_n = static_cast<int>((N + 255) / 256);
-    p.num_kb = static_cast<int>((K + BK - 1) / BK);
-    p.fa = fa; p.fb = fb; p.ga = ga; p.gb = gb; p.sa = sa; p.sb = sb;
-    p.bias = static_cast<const __nv_bfloat16*>(bias);
-    p.D = D; p.out = out; p.accumulate = accumulate;
+// A block-scaled product (kDense), or one per expert (kByRows, kByTokens; offsets
+// [experts + 1] in device memory).  ga, gb: granularities, the flag removed.
+struct BlockProblem {
+    const uint8_t* A;
+    int fa;
+    const uint8_t* B;
+    int fb;
+    int64_t M, N, K;
+    int ga;
+    const float* sa;
+    int gb;
+    const float* sb;
+    const void* bias;
+    void* D;
+    int out, accumulate;
+    const int32_t* offsets;
+    int experts;
+};
+
+// The parameters, tensor maps and tiles of a block problem (K > 0).
+template <int MODE>
+int block_params(const BlockProblem& b, int n_tile, GemmParams& p, CUtensorMap& tmA, CUtensorMap& tmB,
+                 CUtensorMap& tmD, int64_t& tiles) {
+    p.M = b.M; p.N = b.N; p.K = b.K;
+    p.num_m = static_cast<int>((b.M + 255) / 256);
+    p.num_n = static_cast<int>((b.N + n_tile - 1) / n_tile);
+    p.num_kb = static_cast<int>((b.K + BK - 1) / BK);
+    p.fa = b.fa; p.fb = b.fb; p.ga = b.ga; p.gb = b.gb; p.sa = b.sa; p.sb = b.sb;
+    p.bias = static_cast<const __nv_bfloat16*>(b.bias);
+    p.D = b.D; p.out = b.out; p.accumulate = b.accumulate;
     p.a_mn = p.b_mn = 0;
-    p.group = pair_group(K);
+    p.group = pair_group(MODE == kByTokens ? b.K / b.experts : b.K);
+    p.offsets = b.offsets; p.experts = b.experts;
+    int st = make_kmajor_map(&tmA, b.A, b.M, b.K, BM);
+    if (st == FP8_OK) st = make_kmajor_map(&tmB, b.B, MODE == kByRows ? b.N * b.experts : b.N, b.K, n_tile / 2);
+    if (st == FP8_OK) st = make_store_map(&tmD, b.D, MODE == kByTokens ? b.M * b.experts : b.M, b.N, b.out);
+    // at most this many, however the experts' rows are cut
+    tiles = static_cast<int64_t>(p.num_m + (MODE == kByRows ? b.experts - 1 : 0)) * p.num_n *
+            (MODE == kByTokens ? b.experts : 1);
+    return st;
+}
+
+// The persistent CTA-pair kernel k over the problem's tiles.
+template <int MODE, typename Kernel>
+int launch_block(Kernel k, const BlockProblem& b, int n_tile, int threads, int smem, int smem_id, int cluster_id,
+                 cudaStream_t stream) {
+    GemmParams p;
     CUtensorMap tmA, tmB, tmD;
-    int st = make_kmajor_map(&tmA, A, M, K, BM);
+    int64_t tiles = 0;
+    int st = block_params<MODE>(b, n_tile, p, tmA, tmB, tmD, tiles);
     if (st != FP8_OK) return st;
-    if ((st = make_kmajor_map(&tmB, B, N, K, 128)) != FP8_OK) return st;
-    if ((st = make_store_map(&tmD, D, M, N, out)) != FP8_OK) return st;
-    auto k = gemm_mx_kernel<kMxStages, kMxSfSlots>;
-    if ((st = ensure_smem(k, kMxSmemBytes, 5)) != FP8_OK) return st;
-    const int64_t tiles = static_cast<int64_t>(p.num_m) * p.num_n;
-    const int64_t clusters =
-        pair_clusters(reinterpret_cast<const void*>(k), 2, kMxThreads, kMxSmemBytes);
+    if ((st = ensure_smem(k, smem, smem_id)) != FP8_OK) return st;
+    const int64_t clusters = pair_clusters(reinterpret_cast<const void*>(k), cluster_id, threads, smem);
     const int grid = static_cast<int>(2 * (tiles < clusters ? tiles : clusters));
     // factors of four K blocks as one float4: rows of a multiple of 4 floats, aligned arrays
-    const int vec_a = p.num_kb % 4 == 0 && (reinterpret_cast<uintptr_t>(sa) & 15u) == 0;
-    const int vec_b = p.num_kb % 4 == 0 && (reinterpret_cast<uintptr_t>(sb) & 15u) == 0;
-    launch_pdl(k, dim3(grid), dim3(kMxThreads), kMxSmemBytes, stream, tmA, tmB, tmD, p, vec_a, vec_b);
+    const int vec_a = p.num_kb % 4 == 0 && (reinterpret_cast<uintptr_t>(b.sa) & 15u) == 0;
+    const int vec_b = p.num_kb % 4 == 0 && (reinterpret_cast<uintptr_t>(b.sb) & 15u) == 0;
+    launch_pdl(k, dim3(grid), dim3(threads), smem, stream, tmA, tmB, tmD, p, vec_a, vec_b);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return set_error(FP8_ERR_CUDA, "GEMM launch: %s", cudaGetErrorString(e));
     return FP8_OK;
 }
 
-template <typename C, bool COLSCALE>
-int launch_block_cfg(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t N,
-                     int64_t K, int ga, const float* sa, int gb, const float* sb,
-                     const void* bias, void* D, int out, int accumulate, cudaStream_t stream) {
-    GemmParams p;
-    p.M = M; p.N = N; p.K = K;
-    p.num_m = static_cast<int>((M + 255) / 256);
-    p.num_n = static_cast<int>((N + C::TN - 1) / C::TN);
-    p.num_kb = static_cast<int>((K + BK - 1) / BK);
-    p.fa = fa; p.fb = fb; p.ga = ga; p.gb = gb; p.sa = sa; p.sb = sb;
-    p.bias = static_cast<const __nv_bfloat16*>(bias);
-    p.D = D; p.out = out; p.accumulate = accumulate;
-    p.a_mn = p.b_mn = 0;
-    p.group = pair_group(K);
-    CUtensorMap tmA, tmB, tmD;
-    int st = make_kmajor_map(&tmA, A, M, K, 128);
-    if (st != FP8_OK) return st;
-    if ((st = make_kmajor_map(&tmB, B, N, K, C::TN / 2)) != FP8_OK) return st;
-    if ((st = make_store_map(&tmD, D, M, N, out)) != FP8_OK) return st;
-    auto k = gemm_block_pair_kernel<C, COLSCALE>;
-    constexpr int SMEM = C::smem(COLSCALE);
-    if ((st = ensure_smem(k, SMEM, COLSCALE ? 3 : 1)) != FP8_OK) return st;
-    const int64_t tiles = static_cast<int64_t>(p.num_m) * p.num_n;
-    const int64_t clusters = pair_clusters(reinterpret_cast<const void*>(k), COLSCALE ? 4 : 3,
-                                           C::THREADS, SMEM);
-    const int grid = static_cast<int>(2 * (tiles < clusters ? tiles : clusters));
-    // factors of four K blocks as one float4: rows of a multiple of 4 floats, aligned arrays
-    const int vec_a = p.num_kb % 4 == 0 && (reinterpret_cast<uintptr_t>(sa) & 15u) == 0;
-    const int vec_b = p.num_kb % 4 == 0 && (reinterpret_cast<uintptr_t>(sb) & 15u) == 0;
-    launch_pdl(k, dim3(grid), dim3(C::THREADS), SMEM, stream, tmA, tmB, tmD, p, vec_a, vec_b);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return set_error(FP8_ERR_CUDA, "GEMM launch: %s", cudaGetErrorString(e));
-    return FP8_OK;
+// Power-of-two factors: the CTA-pair block-scaled MMA kernel.
+template <int MODE>
+int launch_mx(const BlockProblem& b, cudaStream_t stream) {
+    constexpr int id = MODE == kDense ? 0 : MODE == kByRows ? 1 : 2;
+    constexpr int smem_ids[3] = {5, 11, 12}, cluster_ids[3] = {2, 5, 6};
+    return launch_block<MODE>(gemm_mx_kernel<kMxStages, kMxSfSlots, MODE>, b, 256, kMxThreads,
+                              kMxSmemBytes + (MODE == kDense ? 0 : static_cast<int>(sizeof(Units))), smem_ids[id],
+                              cluster_ids[id], stream);
+}
+
+// fp32 factors: the CTA-pair promotion kernel.
+template <bool COLSCALE, int MODE>
+int launch_promote(const BlockProblem& b, cudaStream_t stream) {
+    using C = BpWide;
+    constexpr int smem_id = MODE == kDense ? (COLSCALE ? 3 : 1) : MODE == kByRows ? 13 : 14;
+    constexpr int cluster_id = MODE == kDense ? (COLSCALE ? 4 : 3) : MODE == kByRows ? 7 : 8;
+    return launch_block<MODE>(gemm_block_pair_kernel<C, COLSCALE, MODE>, b, C::TN, C::THREADS,
+                              C::smem(COLSCALE, MODE != kDense), smem_id, cluster_id, stream);
 }
 
 // Block-scaled GEMM with fp32 factors (at least one operand with 1x128 or
 // 128x128 scales; K > 0) on the CTA-pair promotion kernel (256 x 256 tiles),
 // with the per-column factor path when B has 1x128 scales.
-int launch_gemm_block(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t N,
-                      int64_t K, int ga, const float* sa, int gb, const float* sb,
-                      const void* bias, void* D, int out, int accumulate, cudaStream_t stream) {
-    const bool colscale = gb == FP8_GRAN_1x128;
-    return colscale ? launch_block_cfg<BpWide, true>(A, fa, B, fb, M, N, K, ga, sa, gb, sb, bias, D,
-                                                     out, accumulate, stream)
-                    : launch_block_cfg<BpWide, false>(A, fa, B, fb, M, N, K, ga, sa, gb, sb, bias, D,
-                                                      out, accumulate, stream);
+int launch_gemm_block(const BlockProblem& b, cudaStream_t stream) {
+    return b.gb == FP8_GRAN_1x128 ? launch_promote<true, kDense>(b, stream) : launch_promote<false, kDense>(b, stream);
 }
 
 }  // namespace
@@ -1971,11 +2128,10 @@ int launch_gemm(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, i
                        gb == FP8_GRAN_128x128;
     const bool mx = pow2 && (ga == FP8_GRAN_1x128 || ga == FP8_GRAN_128x128) &&
                     (gb == FP8_GRAN_1x128 || gb == FP8_GRAN_128x128);
-    if (mx) return launch_gemm_mx(A, fa, B, fb, M, N, K, ga, sa, gb, sb, bias, D, out, accumulate,
-                                  stream);
-    if (block)
-        return launch_gemm_block(A, fa, B, fb, M, N, K, ga, sa, gb, sb, bias, D, out, accumulate,
-                                 stream);
+    if (mx || block) {
+        const BlockProblem b{A, fa, B, fb, M, N, K, ga, sa, gb, sb, bias, D, out, accumulate, nullptr, 1};
+        return mx ? launch_mx<kDense>(b, stream) : launch_gemm_block(b, stream);
+    }
     // per-tensor and per-row scales.  A problem whose 128-row tiles fit in
     // one wave (at most one CTA per SM) runs on the single-CTA kernel (see
     // one_wave_bn); otherwise CTA pairs for every problem of at least 256 rows
@@ -2150,6 +2306,18 @@ unsigned* device_status_word() {
     const unsigned long long id_now = id != 0 ? id : current_context_id();
     if (id_now != 0) cache.emplace_back(id_now, static_cast<unsigned*>(p));
     return static_cast<unsigned*>(p);
+}
+
+int launch_gemm_by_rows(const ExpertGemm& g, cudaStream_t stream) {
+    const BlockProblem b{g.A, g.fa, g.B, g.fb, g.M, g.N, g.K, FP8_GRAN_1x128, g.sa, FP8_GRAN_128x128, g.sb,
+                         nullptr, g.D, g.out, 0, g.offsets, g.experts};
+    return g.pow2 ? launch_mx<kByRows>(b, stream) : launch_promote<false, kByRows>(b, stream);
+}
+
+int launch_gemm_by_tokens(const ExpertGemm& g, cudaStream_t stream) {
+    const BlockProblem b{g.A, g.fa, g.B, g.fb, g.M, g.N, g.K, FP8_GRAN_1x128, g.sa, FP8_GRAN_1x128, g.sb,
+                         nullptr, g.D, FP8_OUT_F32, g.accumulate, g.offsets, g.experts};
+    return g.pow2 ? launch_mx<kByTokens>(b, stream) : launch_promote<true, kByTokens>(b, stream);
 }
 
 int set_epilogue_wait_ns(uint64_t ns) {

@@ -211,8 +211,33 @@ struct GemmArgs {
 // launch_gemm calls when either problem is not a CTA-pair problem.
 int launch_gemm_group(const GemmArgs& g1, const GemmArgs& g2, cudaStream_t stream);
 
+// One block-scaled product per expert (offsets [experts + 1], device memory).
+struct ExpertGemm {
+    const uint8_t* A;
+    int fa;
+    const uint8_t* B;
+    int fb;
+    int64_t M, N, K;
+    const float* sa;
+    const float* sb;
+    void* D;
+    int out, accumulate, pow2;
+    const int32_t* offsets;
+    int experts;
+};
+
+// By rows: expert e's rows of A [M x K] (1x128 factors) and D [M x N] with its
+// B [N x K] (128x128 factors); N and K multiples of 128, M > 0.
+int launch_gemm_by_rows(const ExpertGemm& g, cudaStream_t stream);
+
+// By tokens: D[e] [M x N] (+)= the part of A [M x K] . B [N x K]^T over K from
+// offsets[e] to offsets[e + 1] (1x128 factors both), FP32; M, N, K multiples
+// of 128, K > 0.
+int launch_gemm_by_tokens(const ExpertGemm& g, cudaStream_t stream);
+
 // Device status word (bit 0: a bounded wait timed out; bit 1: a scale
-// update saw a non-finite amax).
+// update saw a non-finite amax; bit 2: offsets that are no multiples of 128
+// where tokens are the reduction).
 int read_device_status(unsigned* status, bool clear);
 
 // Sets the epilogue wait limit of the single-CTA GEMM kernel on the current

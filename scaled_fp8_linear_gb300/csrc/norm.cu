@@ -86,16 +86,6 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, float* part, int& turn) 
     return v;
 }
 
-// A row's scale from the bits of its largest magnitude, by the per-row cast's
-// rule: 1 for a row that is all zero or not finite.
-__device__ __forceinline__ float row_scale(uint32_t top, int fmt, int pow2) {
-    const float a = __uint_as_float(top);
-    if (!(a > 0.0f && a <= FLT_MAX)) return 1.0f;
-    float s = __fdiv_rn(fmt == FP8_E4M3 ? 448.0f : 57344.0f, a);
-    s = fminf(fmaxf(s, FLT_MIN), FLT_MAX);
-    return pow2 ? __uint_as_float(__float_as_uint(s) & 0xFF800000u) : s;
-}
-
 // A thread's eight elements of a piece: VEC, the 16 bytes at p (fp32: 32).
 // Otherwise, for rows that do not start on 16 bytes, the n elements at p,
 // p + step, ... (step: the threads of a row, so that a warp's loads are
@@ -301,7 +291,7 @@ __global__ void __launch_bounds__(THREADS)
     float s = 1.0f;
     if (p.q_rows || p.amax) top = row_max<WARP>(top, part, turn);
     if (p.q_rows) {
-        s = row_scale(top, p.q_fmt, p.pow2);
+        s = row::block_scale(top, p.q_fmt, p.pow2);
         if (at == 0) p.q_scale_inv[r] = __fdiv_rn(1.0f, s);
     } else {
         s = p.q_scale[0];
@@ -542,7 +532,7 @@ __global__ void __launch_bounds__(THREADS)
             }
             const uint32_t top = row_max<WARP>(row::abs_bits(m), part_max, turn_max);
             if (p.q_rows) {
-                s = row_scale(top, p.q_fmt, p.pow2);
+                s = row::block_scale(top, p.q_fmt, p.pow2);
                 if (at == 0) p.q_scale_inv[r] = __fdiv_rn(1.0f, s);
             } else if (at == 0) {
                 row::raise_amax(p.amax, top);

@@ -3,6 +3,7 @@
 // as fp32, streaming loads and stores, reductions, the FP8 cast.
 #pragma once
 
+#include <cfloat>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -172,6 +173,16 @@ __device__ __forceinline__ float max_abs(float top, float v) {
     float m;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(top), "f"(fabsf(v)));
     return m;
+}
+
+// A row's scale from the bits of its largest magnitude, by the per-row cast's
+// rule: 1 for a row that is all zero or not finite.
+__device__ __forceinline__ float block_scale(uint32_t top, int fmt, int pow2) {
+    const float a = __uint_as_float(top);
+    if (!(a > 0.0f && a <= FLT_MAX)) return 1.0f;
+    float s = __fdiv_rn(fmt == FP8_E4M3 ? 448.0f : 57344.0f, a);
+    s = fminf(fmaxf(s, FLT_MIN), FLT_MAX);
+    return pow2 ? __uint_as_float(__float_as_uint(s) & 0xFF800000u) : s;
 }
 
 // Raise *amax (fp32, non-negative) to the magnitude with these bits.  Most

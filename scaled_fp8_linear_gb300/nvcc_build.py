@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libfp8linear.so")
 SOURCES = ["quantize.cu", "gemm.cu", "api.cu", "noalloc.cu", "norm.cu", "moe.cu",
-           "gemm_act.cu"]
+           "gemm_act.cu", "experts.cu",
+           "act_block.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
