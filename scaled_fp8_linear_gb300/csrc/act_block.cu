@@ -28,8 +28,11 @@
 namespace fp8 {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 8;        // of the kernels that go by rows
 constexpr int kThreads = kWarps * 32;
+constexpr int kTileWarps = 16;   // of the kernels that go by 128 x 128 tiles
+constexpr int kTileThreads = kTileWarps * 32;
+constexpr int kTileRows = 128 / kTileWarps;
 
 // ------------------------------------------------------------------ four columns of a row
 
@@ -121,7 +124,7 @@ struct ActBlock {
 
 // R rows of one 128-column block of h a warp.
 template <int ACT, bool GATED, int R>
-__global__ void __launch_bounds__(kThreads) act_block_kernel(const __grid_constant__ ActBlock p) {
+__global__ void __launch_bounds__(kThreads, 4) act_block_kernel(const __grid_constant__ ActBlock p) {
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const int2 rows = rows_of(p.offsets, p.experts, p.M);
@@ -195,53 +198,52 @@ __global__ void __launch_bounds__(kThreads) act_block_kernel(const __grid_consta
 
 // ------------------------------------------------------------------ transposed codes of a 128 x 128 tile
 
-constexpr int kTileRows = 16;   // rows a warp: 8 warps make a tile
-
-// The codes of a lane's four columns over the warp's 16 rows: word r holds the
-// columns of row r on the way in, word 4 c + k rows 4 k .. 4 k + 3 of column c
+// The codes of a lane's four columns over the warp's 8 rows: word r holds the
+// columns of row r on the way in, word 2 c + k rows 4 k .. 4 k + 3 of column c
 // on the way out.
-__device__ __forceinline__ void turn16(uint32_t (&w)[kTileRows]) {
+__device__ __forceinline__ void turn8(uint32_t (&w)[kTileRows]) {
     uint32_t o[kTileRows];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2; ++k) {
         const uint32_t a = w[4 * k], b = w[4 * k + 1], c = w[4 * k + 2], d = w[4 * k + 3];
         const uint32_t ab = __byte_perm(a, b, 0x5140), cd = __byte_perm(c, d, 0x5140);
         const uint32_t AB = __byte_perm(a, b, 0x7362), CD = __byte_perm(c, d, 0x7362);
         o[k] = __byte_perm(ab, cd, 0x5410);
-        o[4 + k] = __byte_perm(ab, cd, 0x7632);
-        o[8 + k] = __byte_perm(AB, CD, 0x5410);
-        o[12 + k] = __byte_perm(AB, CD, 0x7632);
+        o[2 + k] = __byte_perm(ab, cd, 0x7632);
+        o[4 + k] = __byte_perm(AB, CD, 0x5410);
+        o[6 + k] = __byte_perm(AB, CD, 0x7632);
     }
 #pragma unroll
     for (int k = 0; k < kTileRows; ++k) w[k] = o[k];
 }
 
 // Puts a warp's turned codes into the tile [128 columns][128 rows]; a column's
-// eight 16-byte pieces are at piece ^ ((column >> 2) & 7), so a quarter warp's
-// writes (eight columns of four apart) and reads (one column) spread the banks.
-__device__ __forceinline__ void stage16(uint8_t* tile, const uint32_t (&w)[kTileRows], int warp, int lane) {
+// sixteen 8-byte pieces are at piece ^ ((column >> 2) & 15), so a half warp's
+// writes (sixteen columns four apart) spread over the banks.
+__device__ __forceinline__ void stage8(uint8_t* tile, const uint32_t (&w)[kTileRows], int warp, int lane) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-        *reinterpret_cast<uint4*>(tile + (4 * lane + c) * 128 + 16 * (warp ^ (lane & 7))) =
-            make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        *reinterpret_cast<uint2*>(tile + (4 * lane + c) * 128 + 8 * (warp ^ (lane & 15))) =
+            make_uint2(w[2 * c], w[2 * c + 1]);
 }
 
 // Writes the staged tile: column c's 128 codes to out + c * pitch.
 __device__ __forceinline__ void write_tile(const uint8_t* tile, uint8_t* out, int64_t pitch) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int c = i * 32 + (threadIdx.x >> 3), piece = threadIdx.x & 7;
-        *reinterpret_cast<uint4*>(out + c * pitch + 16 * piece) =
-            *reinterpret_cast<const uint4*>(tile + c * 128 + 16 * (piece ^ ((c >> 2) & 7)));
+    for (int i = 0; i < 8192 / (8 * kTileThreads); ++i) {
+        const int c = i * (kTileThreads / 8) + (threadIdx.x >> 3), piece = threadIdx.x & 7;   // 16 bytes of a column
+        const int x = (c >> 2) & 15;
+        const uint4 v = *reinterpret_cast<const uint4*>(tile + c * 128 + 16 * (piece ^ (x >> 1)));
+        *reinterpret_cast<uint4*>(out + c * pitch + 16 * piece) = x & 1 ? make_uint4(v.z, v.w, v.x, v.y) : v;
     }
 }
 
 // The scales of T tensors' 128 columns from the warps' maxima `part`
-// [8][T][128] into `scale` [T][128], and 1 / scale to inv[t] + c * pitch.
+// [16][T][128] into `scale` [T][128], and 1 / scale to inv[t] + c * pitch.
 template <int T>
 __device__ __forceinline__ void column_scales(const float* part, float* scale, float* const (&inv)[T],
                                               const int (&fmt)[T], int pow2, int64_t pitch) {
-    for (int i = threadIdx.x; i < T * 128; i += kThreads) {
+    for (int i = threadIdx.x; i < T * 128; i += kTileThreads) {
         const int t = i >> 7, c = i & 127;
         float* out = inv[0];
         int f = fmt[0];
@@ -254,7 +256,7 @@ __device__ __forceinline__ void column_scales(const float* part, float* scale, f
         if (!out) continue;   // uniform over a warp
         uint32_t m = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = max(m, row::abs_bits(part[w * T * 128 + i]));
+        for (int w = 0; w < kTileWarps; ++w) m = max(m, row::abs_bits(part[w * T * 128 + i]));
         const float s = row::block_scale(m, f, pow2);
         scale[i] = s;
         out[c * pitch] = __fdiv_rn(1.0f, s);
@@ -304,13 +306,69 @@ struct BwdRow {
     }
 };
 
+// R rows of one 128-column block of dD a warp: row codes only.
+template <int ACT, bool GATED, int R>
+__global__ void __launch_bounds__(kThreads, 4) act_block_bwd_rows_kernel(const __grid_constant__ ActBlockBwd p) {
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const int2 rows = rows_of(p.offsets, p.experts, p.M);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    const int blk = static_cast<int>(unit % p.blocks);
+    const int64_t r0 = rows.x + unit / p.blocks * R;
+    if (r0 >= rows.y) return;
+    const int64_t N = static_cast<int64_t>(p.blocks) * 128, W = GATED ? 2 * N : N;
+    const int wb = GATED ? 2 * p.blocks : p.blocks;
+    const int c = blk * 128 + lane * 4;
+    uint2 d[R];
+    uint32_t zg[R], zu[GATED ? R : 1];
+    float fg[R], fu[GATED ? R : 1];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int64_t r = r0 + i < rows.y ? r0 + i : r0;   // rows past the last are read again and not written
+        d[i] = ld8(p.d + r * N + c);
+        zg[i] = ld4(p.zq + r * W + c);
+        fg[i] = p.z_inv[r * wb + blk];
+        if (GATED) {
+            zu[i] = ld4(p.zq + r * W + N + c);
+            fu[i] = p.z_inv[r * wb + p.blocks + blk];
+        }
+    }
+    // lane 2 i + k keeps the maximum of row i's gate (k = 0) or up (1) gradient
+    BwdRow<ACT, GATED> v[R];
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        v[i].eval(d[i], zg[i], GATED ? zu[i] : 0, fg[i], GATED ? fu[i] : 0.0f);
+        const uint32_t m = row_top(v[i].dg);
+        if (lane == 2 * i) mine = m;
+        if (GATED) {
+            const uint32_t n = row_top(v[i].du);
+            if (lane == 2 * i + 1) mine = n;
+        }
+    }
+    const float s = row::block_scale(mine, p.fmt, p.pow2);
+    const int64_t mr = r0 + (lane >> 1);
+    if ((lane >> 1) < R && mr < rows.y && (GATED || !(lane & 1)))
+        p.inv[mr * wb + (lane & 1 ? p.blocks : 0) + blk] = __fdiv_rn(1.0f, s);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const f2 sg = row::all2(__shfl_sync(row::kAll, s, 2 * i));
+        const f2 su = row::all2(GATED ? __shfl_sync(row::kAll, s, 2 * i + 1) : 0.0f);
+        const int64_t r = r0 + i;
+        if (r >= rows.y) break;
+        *reinterpret_cast<uint32_t*>(p.q + r * W + c) = code4(p.fmt, v[i].dg, sg, sg);
+        if (GATED) *reinterpret_cast<uint32_t*>(p.q + r * W + N + c) = code4(p.fmt, v[i].du, su, su);
+    }
+}
+
 constexpr int kBwdSmem = 3 * 128 * 128;   // three tiles of turned codes; the maxima before them
 
-// One 128 x 128 tile of dD.  The inputs stay in registers as loaded (four bytes
-// an element) and the values are computed twice, for the maxima and for the
-// codes: held in FP32 they would take 192 registers.  COLS: with q_t or h_t.
-template <int ACT, bool GATED, bool COLS>
-__global__ void __launch_bounds__(kThreads, 2) act_block_bwd_kernel(const __grid_constant__ ActBlockBwd p) {
+// One 128 x 128 tile of dD, eight rows a warp.  The values are computed twice, for
+// the maxima and for the codes, from the inputs, which stay in registers as loaded
+// (four bytes an element): FP32 values would take three times as many.
+template <int ACT, bool GATED>
+__global__ void __launch_bounds__(kTileThreads, 2) act_block_bwd_kernel(const __grid_constant__ ActBlockBwd p) {
     ptx::griddep_launch_dependents();
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float scale[3][128];
@@ -320,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 2) act_block_bwd_kernel(const __grid
     const int64_t tile_row = blockIdx.x / p.blocks;
     const int blk = static_cast<int>(blockIdx.x - tile_row * p.blocks);
     const int64_t t0 = tile_row * 128;
-    if (t0 + 128 <= rows.x || t0 >= rows.y) return;
+    if (t0 + 128 <= rows.x || t0 >= rows.y || rows.x >= rows.y) return;
     const int64_t N = static_cast<int64_t>(p.blocks) * 128, W = GATED ? 2 * N : N;
     const int wb = GATED ? 2 * p.blocks : p.blocks;
     const int c = blk * 128 + lane * 4;
@@ -342,109 +400,96 @@ __global__ void __launch_bounds__(kThreads, 2) act_block_bwd_kernel(const __grid
             if (GATED) zu[i] = ld4(p.zq + r * W + N + c);
         }
     }
-    // lane i has row i's gate factor, lane 16 + i its up factor
+    // lane 2 i has row i's gate factor, lane 2 i + 1 its up factor
     float factor = 0.0f;
-    {
-        const int i = lane & 15;
-        if (i >= first && i < last && (GATED || lane < 16))
-            factor = p.z_inv[(r0 + i) * wb + (lane >= 16 ? p.blocks : 0) + blk];
-    }
+    const bool holds = (lane >> 1) >= first && (lane >> 1) < last && (GATED || !(lane & 1));
+    const int64_t at_factor = (r0 + (lane >> 1)) * wb + (lane & 1 ? p.blocks : 0) + blk;
+    if (holds) factor = p.z_inv[at_factor];
     float tg[4] = {}, tu[4] = {}, th[4] = {};
-    uint32_t mine = 0;   // lane i: row i's largest dz_gate, lane 16 + i: dz_up
+    uint32_t mine = 0;   // lane 2 i + k: the largest of row i's gate (k = 0) or up (1) gradient
 #pragma unroll
     for (int i = 0; i < kTileRows; ++i) {
         BwdRow<ACT, GATED> v;
-        v.eval(d[i], zg[i], GATED ? zu[i] : 0, __shfl_sync(row::kAll, factor, i),
-               GATED ? __shfl_sync(row::kAll, factor, 16 + i) : 0.0f);
+        v.eval(d[i], zg[i], GATED ? zu[i] : 0, __shfl_sync(row::kAll, factor, 2 * i),
+               GATED ? __shfl_sync(row::kAll, factor, 2 * i + 1) : 0.0f);
         if (p.q) {
             const uint32_t m = row_top(v.dg);
-            if (lane == i) mine = m;
+            if (lane == 2 * i) mine = m;
             if (GATED) {
                 const uint32_t n = row_top(v.du);
-                if (lane == 16 + i) mine = n;
+                if (lane == 2 * i + 1) mine = n;
             }
         }
-        if (COLS) {
-            if (p.qt) {
-                raise4(tg, v.dg);
-                if (GATED) raise4(tu, v.du);
-            }
-            if (p.ht) raise4(th, v.h);
+        if (p.qt) {
+            raise4(tg, v.dg);
+            if (GATED) raise4(tu, v.du);
         }
+        if (p.ht) raise4(th, v.h);
+        // the values are not kept for the second evaluation
+        asm volatile("" : "+r"(d[i].x), "+r"(d[i].y), "+r"(zg[i]));
+        if (GATED) asm volatile("" : "+r"(zu[i]));
     }
     float s_row = 1.0f;
     if (p.q) {
         s_row = row::block_scale(mine, p.fmt, p.pow2);
-        const int i = lane & 15;
-        if (i >= first && i < last && (GATED || lane < 16))
-            p.inv[(r0 + i) * wb + (lane >= 16 ? p.blocks : 0) + blk] = __fdiv_rn(1.0f, s_row);
+        if (holds) p.inv[at_factor] = __fdiv_rn(1.0f, s_row);
     }
-    f2 sg[2], su[2], sh[2];
-    if (COLS) {
-        float* part = reinterpret_cast<float*>(smem);
-        float4* mine4 = reinterpret_cast<float4*>(part + warp * 3 * 128) + lane;
-        mine4[0] = make_float4(tg[0], tg[1], tg[2], tg[3]);
-        mine4[32] = make_float4(tu[0], tu[1], tu[2], tu[3]);
-        mine4[64] = make_float4(th[0], th[1], th[2], th[3]);
-        __syncthreads();
-        const int64_t tb = p.M >> 7;
-        float* const out[3] = {
-            p.qt ? p.inv_t + static_cast<int64_t>(blk) * 128 * tb + tile_row : nullptr,
-            p.qt && GATED ? p.inv_t + (N + static_cast<int64_t>(blk) * 128) * tb + tile_row : nullptr,
-            p.ht ? p.h_inv_t + static_cast<int64_t>(blk) * 128 * tb + tile_row : nullptr};
-        const int fmt[3] = {p.fmt, p.fmt, p.h_fmt};
-        column_scales<3>(part, &scale[0][0], out, fmt, p.pow2, tb);
-        __syncthreads();
-        const float4 a = reinterpret_cast<const float4*>(scale[0])[lane], b = reinterpret_cast<const float4*>(scale[1])[lane],
-                     e = reinterpret_cast<const float4*>(scale[2])[lane];
-        sg[0] = row::mk2(a.x, a.y); sg[1] = row::mk2(a.z, a.w);
-        su[0] = row::mk2(b.x, b.y); su[1] = row::mk2(b.z, b.w);
-        sh[0] = row::mk2(e.x, e.y); sh[1] = row::mk2(e.z, e.w);
-    }
-    uint32_t wg[COLS ? kTileRows : 1], wu[COLS && GATED ? kTileRows : 1], wh[COLS ? kTileRows : 1];
+    float* part = reinterpret_cast<float*>(smem);
+    float4* mine4 = reinterpret_cast<float4*>(part + warp * 3 * 128) + lane;
+    mine4[0] = make_float4(tg[0], tg[1], tg[2], tg[3]);
+    mine4[32] = make_float4(tu[0], tu[1], tu[2], tu[3]);
+    mine4[64] = make_float4(th[0], th[1], th[2], th[3]);
+    __syncthreads();
+    const int64_t tb = p.M >> 7;
+    float* const out[3] = {p.qt ? p.inv_t + static_cast<int64_t>(blk) * 128 * tb + tile_row : nullptr,
+                           p.qt && GATED ? p.inv_t + (N + static_cast<int64_t>(blk) * 128) * tb + tile_row : nullptr,
+                           p.ht ? p.h_inv_t + static_cast<int64_t>(blk) * 128 * tb + tile_row : nullptr};
+    const int fmt[3] = {p.fmt, p.fmt, p.h_fmt};
+    column_scales<3>(part, &scale[0][0], out, fmt, p.pow2, tb);
+    __syncthreads();   // the maxima have been read: their place takes the tiles
+    const float4 a = reinterpret_cast<const float4*>(scale[0])[lane], b = reinterpret_cast<const float4*>(scale[1])[lane],
+                 e = reinterpret_cast<const float4*>(scale[2])[lane];
+    const f2 sg[2] = {row::mk2(a.x, a.y), row::mk2(a.z, a.w)}, su[2] = {row::mk2(b.x, b.y), row::mk2(b.z, b.w)};
+    const f2 sh[2] = {row::mk2(e.x, e.y), row::mk2(e.z, e.w)};
+    uint32_t wg[kTileRows], wu[kTileRows], wh[kTileRows];
 #pragma unroll
     for (int i = 0; i < kTileRows; ++i) {
         BwdRow<ACT, GATED> v;
-        v.eval(d[i], zg[i], GATED ? zu[i] : 0, __shfl_sync(row::kAll, factor, i),
-               GATED ? __shfl_sync(row::kAll, factor, 16 + i) : 0.0f);
+        v.eval(d[i], zg[i], GATED ? zu[i] : 0, __shfl_sync(row::kAll, factor, 2 * i),
+               GATED ? __shfl_sync(row::kAll, factor, 2 * i + 1) : 0.0f);
         if (p.q) {
-            const f2 a = row::all2(__shfl_sync(row::kAll, s_row, i));
-            const f2 b = row::all2(GATED ? __shfl_sync(row::kAll, s_row, 16 + i) : 0.0f);
+            const f2 a = row::all2(__shfl_sync(row::kAll, s_row, 2 * i));
+            const f2 b = row::all2(GATED ? __shfl_sync(row::kAll, s_row, 2 * i + 1) : 0.0f);
             if (i >= first && i < last) {
                 *reinterpret_cast<uint32_t*>(p.q + (r0 + i) * W + c) = code4(p.fmt, v.dg, a, a);
                 if (GATED) *reinterpret_cast<uint32_t*>(p.q + (r0 + i) * W + N + c) = code4(p.fmt, v.du, b, b);
             }
         }
-        if constexpr (COLS) {
-            if (p.qt) {
-                wg[i] = code4(p.fmt, v.dg, sg[0], sg[1]);
-                if constexpr (GATED) wu[i] = code4(p.fmt, v.du, su[0], su[1]);
-            }
-            if (p.ht) wh[i] = code4(p.h_fmt, v.h, sh[0], sh[1]);
+        if (p.qt) {
+            wg[i] = code4(p.fmt, v.dg, sg[0], sg[1]);
+            if (GATED) wu[i] = code4(p.fmt, v.du, su[0], su[1]);
+        }
+        if (p.ht) wh[i] = code4(p.h_fmt, v.h, sh[0], sh[1]);
+    }
+    if (p.qt) {
+        turn8(wg);
+        stage8(smem, wg, warp, lane);
+        if (GATED) {
+            turn8(wu);
+            stage8(smem + 128 * 128, wu, warp, lane);
         }
     }
-    if constexpr (COLS) {
-        // the maxima were read before the last barrier
-        if (p.qt) {
-            turn16(wg);
-            stage16(smem, wg, warp, lane);
-            if constexpr (GATED) {
-                turn16(wu);
-                stage16(smem + 128 * 128, wu, warp, lane);
-            }
-        }
-        if (p.ht) {
-            turn16(wh);
-            stage16(smem + 2 * 128 * 128, wh, warp, lane);
-        }
-        __syncthreads();
-        const int64_t at = static_cast<int64_t>(blk) * 128 * p.M + t0;
-        if (p.qt) {
-            write_tile(smem, p.qt + at, p.M);
-            if (GATED) write_tile(smem + 128 * 128, p.qt + N * p.M + at, p.M);
-        }
-        if (p.ht) write_tile(smem + 2 * 128 * 128, p.ht + at, p.M);
+    if (p.ht) {
+        turn8(wh);
+        stage8(smem + 2 * 128 * 128, wh, warp, lane);
     }
+    __syncthreads();
+    const int64_t at = static_cast<int64_t>(blk) * 128 * p.M + t0;
+    if (p.qt) {
+        write_tile(smem, p.qt + at, p.M);
+        if (GATED) write_tile(smem + 128 * 128, p.qt + N * p.M + at, p.M);
+    }
+    if (p.ht) write_tile(smem + 2 * 128 * 128, p.ht + at, p.M);
 }
 
 // ------------------------------------------------------------------ a kept input, transposed
@@ -460,7 +505,7 @@ struct BlockTranspose {
 };
 
 template <int FMT>
-__global__ void __launch_bounds__(kThreads, 2) block_transpose_kernel(const __grid_constant__ BlockTranspose p) {
+__global__ void __launch_bounds__(kTileThreads, 3) block_transpose_kernel(const __grid_constant__ BlockTranspose p) {
     ptx::griddep_launch_dependents();
     __shared__ __align__(16) uint8_t tile[128 * 128];   // the maxima, then the turned codes
     __shared__ __align__(16) float scale[128];
@@ -473,13 +518,12 @@ __global__ void __launch_bounds__(kThreads, 2) block_transpose_kernel(const __gr
     uint32_t w[kTileRows];
 #pragma unroll
     for (int i = 0; i < kTileRows; ++i) w[i] = ld4(p.q + (r0 + i) * cols + c);
-    float factor = lane < 16 ? p.inv[(r0 + lane) * p.blocks + blk] : 0.0f;
-    Quad v[kTileRows];
+    const float factor = lane < kTileRows ? p.inv[(r0 + lane) * p.blocks + blk] : 0.0f;
     float top[4] = {};
 #pragma unroll
     for (int i = 0; i < kTileRows; ++i) {
-        v[i] = decode4(FMT, w[i], __shfl_sync(row::kAll, factor, i));
-        raise4(top, v[i]);
+        raise4(top, decode4(FMT, w[i], __shfl_sync(row::kAll, factor, i)));
+        asm volatile("" : "+r"(w[i]));   // decoded again below
     }
     float* part = reinterpret_cast<float*>(tile);
     reinterpret_cast<float4*>(part + warp * 128)[lane] = make_float4(top[0], top[1], top[2], top[3]);
@@ -492,27 +536,37 @@ __global__ void __launch_bounds__(kThreads, 2) block_transpose_kernel(const __gr
     const float4 s = reinterpret_cast<const float4*>(scale)[lane];
     const f2 s0 = row::mk2(s.x, s.y), s1 = row::mk2(s.z, s.w);
 #pragma unroll
-    for (int i = 0; i < kTileRows; ++i) w[i] = code4(FMT, v[i], s0, s1);
-    turn16(w);
-    stage16(tile, w, warp, lane);
+    for (int i = 0; i < kTileRows; ++i)
+        w[i] = code4(FMT, decode4(FMT, w[i], __shfl_sync(row::kAll, factor, i)), s0, s1);
+    turn8(w);
+    stage8(tile, w, warp, lane);
     __syncthreads();
     write_tile(tile, p.qt + static_cast<int64_t>(blk) * 128 * p.rows + tile_row * 128, p.rows);
 }
 
 // ------------------------------------------------------------------ host side
 
+constexpr int kRows = 4;   // rows a warp where there are many
+
+// Whether kRows rows a warp still leave every SM several CTAs.
+bool many_rows(int64_t M, int64_t blocks) {
+    return M * blocks >= int64_t{kRows} * kWarps * 4 * num_sms();
+}
+
+dim3 row_grid(int64_t M, int64_t blocks, bool many) {
+    const int64_t warps = (many ? (M + kRows - 1) / kRows : M) * blocks;
+    return dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps));
+}
+
 template <int ACT>
 int launch_fwd(const ActBlock& p, bool gated, cudaStream_t st) {
-    // eight rows a warp keep enough loads in flight; fewer where that leaves SMs idle
-    const int64_t units = p.M * p.blocks;
-    const bool wide = units >= 8 * kWarps * 2 * num_sms();
-    const int64_t ctas = ((p.M + (wide ? 7 : 0)) / (wide ? 8 : 1) * p.blocks + kWarps - 1) / kWarps;
-    const dim3 grid(static_cast<unsigned>(ctas)), block(kThreads);
+    const bool many = many_rows(p.M, p.blocks);
+    const dim3 grid = row_grid(p.M, p.blocks, many), block(kThreads);
     if (gated) {
-        if (wide) launch_pdl(act_block_kernel<ACT, true, 8>, grid, block, 0, st, p);
+        if (many) launch_pdl(act_block_kernel<ACT, true, kRows>, grid, block, 0, st, p);
         else launch_pdl(act_block_kernel<ACT, true, 1>, grid, block, 0, st, p);
     } else {
-        if (wide) launch_pdl(act_block_kernel<ACT, false, 8>, grid, block, 0, st, p);
+        if (many) launch_pdl(act_block_kernel<ACT, false, kRows>, grid, block, 0, st, p);
         else launch_pdl(act_block_kernel<ACT, false, 1>, grid, block, 0, st, p);
     }
     return FP8_OK;
@@ -520,15 +574,18 @@ int launch_fwd(const ActBlock& p, bool gated, cudaStream_t st) {
 
 template <int ACT, bool GATED>
 int launch_bwd(const ActBlockBwd& p, cudaStream_t st) {
-    const dim3 grid(static_cast<unsigned>((p.M + 127) / 128 * p.blocks)), block(kThreads);
     if (!p.qt && !p.ht) {
-        launch_pdl(act_block_bwd_kernel<ACT, GATED, false>, grid, block, 0, st, p);
+        const bool many = many_rows(p.M, p.blocks);
+        const dim3 grid = row_grid(p.M, p.blocks, many), block(kThreads);
+        if (many) launch_pdl(act_block_bwd_rows_kernel<ACT, GATED, kRows>, grid, block, 0, st, p);
+        else launch_pdl(act_block_bwd_rows_kernel<ACT, GATED, 1>, grid, block, 0, st, p);
         return FP8_OK;
     }
     static host::SmemAllowance allowance;
-    const int r = host::allow_smem(act_block_bwd_kernel<ACT, GATED, true>, kBwdSmem, allowance);
+    const int r = host::allow_smem(act_block_bwd_kernel<ACT, GATED>, kBwdSmem, allowance);
     if (r != FP8_OK) return r;
-    launch_pdl(act_block_bwd_kernel<ACT, GATED, true>, grid, block, kBwdSmem, st, p);
+    const dim3 grid(static_cast<unsigned>(p.M / 128 * p.blocks)), block(kTileThreads);
+    launch_pdl(act_block_bwd_kernel<ACT, GATED>, grid, block, kBwdSmem, st, p);
     return FP8_OK;
 }
 
@@ -643,7 +700,7 @@ int fp8_block_transpose(const uint8_t* q, const float* scale_inv, int64_t rows, 
         return set_error(FP8_ERR_ALIGN, "%s: factors must be 4-byte aligned", what);
     if (rows == 0) return FP8_OK;
     const BlockTranspose p{q, scale_inv, q_t, scale_inv_t, rows, static_cast<int>(cols / 128), pow2};
-    const dim3 grid(static_cast<unsigned>(rows / 128 * p.blocks)), block(kThreads);
+    const dim3 grid(static_cast<unsigned>(rows / 128 * p.blocks)), block(kTileThreads);
     if (format == FP8_E4M3) launch_pdl(block_transpose_kernel<0>, grid, block, 0, as_stream(stream), p);
     else launch_pdl(block_transpose_kernel<1>, grid, block, 0, as_stream(stream), p);
     return launch_status(what);

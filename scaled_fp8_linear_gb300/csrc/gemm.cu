@@ -878,6 +878,14 @@ __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
 // TMEM loads (3% faster there, with fewer spills); 256 x 160 tiles with three
 // buffers and 20 promotion warps were 30% slower, and 256 x 128 tiles with
 // four buffers and 8 warps (the earlier form) 24% slower (COLSCALE: 9%).
+// Experts' factors on their way: sets of four K blocks, of the CTA's 128 rows
+// and of the tile's columns (kByTokens: 256, each its own) or 128-column blocks.
+constexpr int kFactorSets = 3;
+template <int MODE>
+constexpr int kFactorCols = MODE == kByTokens ? 256 : 2;
+template <int MODE>
+constexpr int kFactorSetBytes = (128 + kFactorCols<MODE>) * 16;
+
 template <int TN_, int EPI_, int STAGES_, int RROLE_, int RPROMO_>
 struct BpCfg {
     static constexpr int TN = TN_;
@@ -893,13 +901,21 @@ struct BpCfg {
     static constexpr int A_BYTES = 128 * BK;         // this CTA's 128 rows of A
     static constexpr int B_BYTES = (TN / 2) * BK;    // this CTA's half of the TN rows of B
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+    // output boxes and factors (floats) of a promotion warp: COLSCALE, four K
+    // blocks of its columns and rows; experts, its share of the CTA's sets
+    template <int MODE>
+    static constexpr int BOXES = MODE == kByTokens ? 2 : 1;
+    template <bool COLSCALE, int MODE>
+    static constexpr int FACTORS = MODE != kDense ? (kFactorSets * kFactorSetBytes<MODE> / 4 + EPI - 1) / EPI
+                                   : COLSCALE     ? 4 * (CW + 32)
+                                                  : 0;
     // shared memory: operand ring, 2 KB of output staging per promotion
     // warp, per-column and per-row factors (COLSCALE only), barriers,
     // alignment slack
-    static constexpr int smem(bool colscale, bool experts) {
-        return STAGES * STAGE_BYTES + EPI * (2048 + (colscale ? 4 * (CW + 32) * 4 : 0)) + 256 +
-               (experts ? static_cast<int>(sizeof(Units)) : 0) + 1024;
-    }
+    template <bool COLSCALE, int MODE>
+    static constexpr int SMEM = STAGES * STAGE_BYTES + EPI * (BOXES<MODE> * 2048 + FACTORS<COLSCALE, MODE> * 4) + 256 +
+                                (MODE != kDense ? static_cast<int>(sizeof(Units)) : 0) + 1024;
+
     static_assert(CW == 64, "a warp's columns: one 64-column slice of a 128-column factor "
                             "block, loaded as two 32-column chunks");
     static_assert(4 * 32 * RROLE + EPI * 32 * RPROMO <= THREADS * (65536 / THREADS / 8 * 8),
@@ -989,7 +1005,6 @@ __device__ __forceinline__ void emit_block_chunk(uint8_t* slot, const uint64_t* 
                                                  int64_t m0, int64_t n0, const GemmParams& p,
                                                  const CUtensorMap* map) {
     const bool in_range = m0 < t.m_end;
-    const int64_t y = MODE == kByTokens ? t.d_row + m0 : m0;   // row of D
     float v[32];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
@@ -1019,7 +1034,7 @@ __device__ __forceinline__ void emit_block_chunk(uint8_t* slot, const uint64_t* 
         const uint4 piece[4] = {make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]),
                                 make_uint4(w[8], w[9], w[10], w[11]),
                                 make_uint4(w[12], w[13], w[14], w[15])};
-        emit_box(slot, piece, map, n0, y, in_range, false);
+        emit_box(slot, piece, map, n0, m0, in_range, false);
     } else {
 #pragma unroll
         for (int hb = 0; hb < 2; ++hb) {
@@ -1030,7 +1045,185 @@ __device__ __forceinline__ void emit_block_chunk(uint8_t* slot, const uint64_t* 
                                       __float_as_uint(v[16 * hb + 4 * j + 1]),
                                       __float_as_uint(v[16 * hb + 4 * j + 2]),
                                       __float_as_uint(v[16 * hb + 4 * j + 3]));
-            emit_box(slot, piece, map, n0 + 16 * hb, y, in_range, p.accumulate != 0);
+            emit_box(slot, piece, map, n0 + 16 * hb, m0, in_range, p.accumulate != 0);
+        }
+    }
+}
+
+// ---- promotion where tokens are the reduction (kByTokens)
+//
+// Both factors differ from K block to K block, by row of D and by column: two
+// multiplications an element (512 cycles a K block, what its MMAs take).  With a
+// row a thread they would be 64 column factors a thread and K block through
+// shared memory, four cycles a load of four (it returns 512 bytes a warp): 1024
+// cycles.  So the partial sums are read in the 16 x 128 bit form, which gives a
+// thread 16 columns of four rows: 16 + 4 factors.  (All 16 warps' loads of a K
+// block take 257 cycles so, 145 in the 32 x 32 bit form, 514 in 16 x 256 bits.)
+
+__device__ __forceinline__ float ld_shared(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+
+// The factor warp: for every four K blocks of a tile, those of this CTA's 128
+// rows and of the tile's columns, copied asynchronously (0 past the last K
+// block).  One warp for all: read by the promotion warps themselves, each row's
+// 16 bytes would be a cache line looked up in four of them (experts' products
+// of 4096 x 4096 over 32768 rows: 660 us so, 545 with all factors 1).  full[s] counts
+// the 32 lanes' copies.
+template <int MODE, int TN>
+__device__ __forceinline__ void load_factors(uint32_t sets, uint64_t* full, uint64_t* empty, volatile uint32_t* abort_flag,
+                                             const Units* units, const GemmParams& p, int rank, int pair, int npairs,
+                                             int num_units, bool vec_a, bool vec_b) {
+    constexpr int COLS = kFactorCols<MODE>, STEPS = (128 + COLS + 31) / 32;
+    const int lane = threadIdx.x & 31, KB = p.num_kb;
+    uint32_t set = 0, phase = 0;
+    for (int u = pair; u < num_units; u += npairs) {
+        const BlockTile t = block_tile<MODE>(u, units, p, TN);
+        for (int kb = t.kb0 & ~3; kb < t.kb1; kb += 4) {
+            bool ok = lane == 0 ? ptx::mbar_wait(&empty[set], phase ^ 1u, abort_flag) : false;
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            if (!ok) {
+                ptx::cp_async_wait_all();
+                return;
+            }
+            const uint32_t to = sets + set * kFactorSetBytes<MODE> + lane * 16;
+#pragma unroll 1
+            for (int i = 0; i < STEPS; ++i) {   // 128 rows of A, then the columns
+                if (MODE == kByRows && i == STEPS - 1 && lane >= COLS) break;
+                // rows and columns past the matrix are read at its last ones
+                int r = min(t.ya + rank * 128 + 32 * i + lane, static_cast<int>(p.M) - 1);
+                if (i >= 4)
+                    r = MODE == kByTokens ? min(t.n0 + 32 * (i - 4) + lane, static_cast<int>(p.N) - 1)
+                                          : (t.b_row + min(t.n0 + 128 * lane, static_cast<int>(p.N) - 1)) >> 7;
+                const float* src = (i < 4 ? p.sa : p.sb) + static_cast<int64_t>(r) * KB + kb;
+                if (i < 4 ? vec_a : vec_b) {   // then KB is a multiple of four
+                    ptx::cp_async16(to + 512 * i, src, true);
+                } else {
+#pragma unroll 1
+                    for (int j = 0; j < 4; ++j)
+                        ptx::cp_async4(to + 512 * i + 4 * j, kb + j < KB ? src + j : p.sa, kb + j < KB);
+                }
+            }
+            ptx::cp_async_arrive(&full[set]);
+            if (++set == kFactorSets) { set = 0; phase ^= 1u; }
+        }
+    }
+    ptx::cp_async_wait_all();
+}
+
+// One promotion warp: 32 rows from m_off and 64 columns from n_off of every
+// tile.  slots: two boxes.  factors: the sets, from this warp's thread's first
+// column on; rows: from its first row on.  tmem: the warp's lanes and first
+// column in buffer 0.  The sums come 16 columns of 16 rows at a time, the next
+// while these are scaled and added.
+template <int NBUF, int TN>
+__device__ __forceinline__ void promote_tokens(uint8_t* slots, uint32_t cols, uint32_t rows, uint64_t* ffull,
+                                               uint64_t* fempty, uint64_t* tfull, uint64_t* tempty,
+                                               volatile uint32_t* abort_flag, const Units* units, const GemmParams& p,
+                                               const CUtensorMap* map, uint32_t tmem, int m_off, int n_off, int pair,
+                                               int npairs, int num_units) {
+    const int lane = threadIdx.x & 31, q4 = lane & 3, r8 = lane >> 2;
+    uint32_t buf = 0, buf_phase = 0, set = 0, set_phase = 0, turn = 0;
+    for (int u = pair; u < num_units; u += npairs) {
+        const BlockTile t = block_tile<kByTokens>(u, units, p, TN);
+        float2 acc[2][16];   // rows 16 hh + r8 (x) and + 8 (y); column 4 j + q4
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[hh][j] = make_float2(0.0f, 0.0f);
+        for (int base = t.kb0 & ~3; base < t.kb1; base += 4) {
+            bool ok = ptx::mbar_wait(&ffull[set], set_phase, abort_flag);   // every lane: the copies are others'
+            if (!__all_sync(0xFFFFFFFFu, ok)) return;
+            const uint32_t at = set * kFactorSetBytes<kByTokens>;
+            const int j0 = base < t.kb0 ? t.kb0 - base : 0, j1 = base + 4 < t.kb1 ? 4 : t.kb1 - base;
+#pragma unroll 1
+            for (int j = j0; j < j1; ++j) {
+                const uint32_t fc_at = cols + at + 4 * j, fr_at = rows + at + 4 * j;
+                uint64_t fr[2];   // the rows' factors
+                float fc[2][4];   // this 16-column step's factors, and the next's
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh)
+                    fr[hh] = pack2(ld_shared(fr_at + 16 * hh * 16), ld_shared(fr_at + (16 * hh + 8) * 16));
+                auto columns = [&](int c) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) fc[c & 1][i] = ld_shared(fc_at + (16 * c + 4 * i) * 16);
+                };
+                columns(0);
+                ok = lane == 0 ? ptx::mbar_wait(&tfull[buf], buf_phase, abort_flag) : false;
+                ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+                if (!ok) return;
+                __syncwarp();
+                ptx::tc_fence_after();
+                const uint32_t ta = tmem + buf * TN;
+                uint32_t r[2][8];
+                ptx::tmem_ld_16x128b_x4(ta, r[0]);
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {   // 16 columns from 16 (s / 2), 16 rows from 16 (s % 2)
+                    const int c = s >> 1, hh = s & 1;
+                    ptx::tmem_wait_ld();
+                    if (s < 7) {
+                        ptx::tmem_ld_16x128b_x4(ta + (static_cast<uint32_t>(16 * ((s + 1) & 1)) << 16) + 16 * ((s + 1) >> 1),
+                                                r[(s + 1) & 1]);
+                    } else {
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::cluster_addr(&tempty[buf], 0));
+                    }
+                    if (hh == 0 && c < 3) columns(c + 1);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint64_t v = ptx::fmul2(static_cast<uint64_t>(r[s & 1][2 * i]) |
+                                                          (static_cast<uint64_t>(r[s & 1][2 * i + 1]) << 32),
+                                                      fr[hh]);
+                        float2& a = acc[hh][4 * c + i];
+                        a.x = __fmaf_rn(__uint_as_float(static_cast<uint32_t>(v)), fc[c & 1][i], a.x);
+                        a.y = __fmaf_rn(__uint_as_float(static_cast<uint32_t>(v >> 32)), fc[c & 1][i], a.y);
+                    }
+                }
+                if (++buf == NBUF) { buf = 0; buf_phase ^= 1u; }
+            }
+            __syncwarp();   // the set has been read
+            if (lane == 0) ptx::mbar_arrive(&fempty[set]);
+            if (++set == kFactorSets) { set = 0; set_phase ^= 1u; }
+        }
+        if (t.kb0 == t.kb1) {   // no tokens: zeros, or nothing to add
+            if (t.lost) {
+                const float nan = __int_as_float(0x7FC00000);
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) acc[hh][j] = make_float2(nan, nan);
+            } else if (p.accumulate) {
+                continue;
+            }
+        }
+        const int m0 = t.ya + m_off, n0 = t.n0 + n_off;
+        if (m0 >= t.m_end || n0 >= p.N) continue;   // uniform over the warp
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {   // boxes of 32 rows x 16 columns, 64-byte swizzle
+            uint8_t* slot = slots + turn * 2048;
+            turn ^= 1u;
+            if (lane == 0) ptx::bulk_wait_group_read<1>();   // the slot's last box has been read
+            __syncwarp();
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {   // row r + 8 has row r's swizzle
+                    float* to = reinterpret_cast<float*>(slot + (16 * hh + r8) * 64 + 16 * (i ^ ((r8 >> 1) & 3)) + 4 * q4);
+                    to[0] = acc[hh][4 * b + i].x;
+                    to[8 * 16] = acc[hh][4 * b + i].y;
+                }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (p.accumulate)
+                    ptx::tma_reduce_add_2d(map, ptx::smem_u32(slot), n0 + 16 * b, t.d_row + m0);
+                else
+                    ptx::tma_store_2d(map, ptx::smem_u32(slot), n0 + 16 * b, t.d_row + m0);
+                ptx::bulk_commit_group();
+            }
         }
     }
 }
@@ -1052,14 +1245,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     uint8_t* ring = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* epi_stage = ring + STAGES * STAGE_BYTES;   // output boxes: 2 KB per epilogue warp
-    float* colf = reinterpret_cast<float*>(epi_stage + EPI * 2048);   // [warp][4][cols + 32]
-    uint64_t* full = reinterpret_cast<uint64_t*>(colf + (COLSCALE ? EPI * 4 * (Cfg::CW + 32) : 0));
+    constexpr int BOXES = Cfg::template BOXES<MODE>, FACTORS = Cfg::template FACTORS<COLSCALE, MODE>;
+    float* colf = reinterpret_cast<float*>(epi_stage + EPI * BOXES * 2048);   // [warp][FACTORS]
+    uint64_t* full = reinterpret_cast<uint64_t*>(colf + EPI * FACTORS);
     uint64_t* empty = full + STAGES;
     uint64_t* tfull = empty + STAGES;
     uint64_t* tempty = tfull + NBUF;
     uint64_t* done = tempty + NBUF;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    uint64_t* ffull = done + 1;   // experts' factor sets
+    uint64_t* fempty = ffull + kFactorSets;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fempty + kFactorSets);
     volatile uint32_t* abort_flag = tmem_slot + 1;
+    static_assert((2 * STAGES + 2 * NBUF + 1 + 2 * kFactorSets) * 8 + 8 <= 256, "the barriers' place");
     Units* units = reinterpret_cast<Units*>(reinterpret_cast<uint8_t*>(full) + 256);   // experts' rows
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1073,6 +1270,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         for (int b = 0; b < NBUF; ++b) {
             ptx::mbar_init(&tfull[b], 1);
             ptx::mbar_init(&tempty[b], 2 * EPI);   // promotion warps of both CTAs
+        }
+        if (MODE != kDense) {
+            for (int b = 0; b < kFactorSets; ++b) {
+                ptx::mbar_init(&ffull[b], 32);     // the factor warp's lanes
+                ptx::mbar_init(&fempty[b], EPI);
+            }
         }
         ptx::mbar_init(done, 1);
         *abort_flag = 0;
@@ -1164,6 +1367,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             ptx::mma_commit_pair(done, 0x1);
             ptx::mbar_wait(done, 0, &never);
         }
+    } else if (MODE != kDense && warp == 3) {
+        load_factors<MODE, TN>(ptx::smem_u32(colf), ffull, fempty, abort_flag, units, p, rank, pair, npairs, num_units,
+                         vec_a != 0, vec_b != 0);
     }
     } else {
         ptx::setmaxnreg_inc<Cfg::RPROMO>();   // each promotion warpgroup
@@ -1177,8 +1383,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         float* cf = colf + (warp - 4) * 4 * (CW + 32);
         float* rf = cf + 4 * CW;
         const uint32_t lanes = static_cast<uint32_t>(qd * 32) << 16;
-        uint32_t buf = 0, buf_phase = 0;
+        uint32_t buf = 0, buf_phase = 0, fset = 0, fset_phase = 0;
         bool ok = true;
+        if constexpr (MODE == kByTokens) {
+            static_assert(COLSCALE && CW == 64 && TN == 256, "the token path's fragments and factor sets");
+            slot = epi_stage + (warp - 4) * BOXES * 2048;
+            const uint32_t sets = ptx::smem_u32(colf);
+            promote_tokens<NBUF, TN>(slot, sets + (128 + h * CW + (lane & 3)) * 16, sets + (qd * 32 + (lane >> 2)) * 16,
+                                     ffull, fempty, tfull, tempty, abort_flag, units, p, &tmD,
+                                     tmem_base + lanes + h * CW, rank * 128 + qd * 32, h * CW, pair, npairs, num_units);
+        } else
         for (int u = pair; ok && u < num_units; u += npairs) {
             const BlockTile t = block_tile<MODE>(u, units, p, TN);
             const int64_t m0 = static_cast<int64_t>(t.ya) + rank * 128 + qd * 32;
@@ -1193,8 +1407,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             uint64_t acc[CW / 2];
 #pragma unroll
             for (int e = 0; e < CW / 2; ++e) acc[e] = 0ull;
-            // an expert's first K block is any: groups of four stay aligned
-            for (int kb0 = MODE == kByTokens ? t.kb0 & ~3 : 0; ok && kb0 < t.kb1; kb0 += 4) {
+            for (int kb0 = 0; ok && kb0 < t.kb1; kb0 += 4) {
                 // The factors of four K blocks, read at the start of the group
                 // (they hit L1; holding the next group's in registers made the
                 // loop spill): A per row; B per 128-column block, multiplied
@@ -1202,7 +1415,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                 // memory for broadcast reads (lane l writes columns n0+32c+l),
                 // with the rows' factors beside them (registers are short).
                 float fa[4], fb[4];
-                block_factors4(fa, p.sa, p.ga, m_safe, kb0, KB, vec_a != 0);
+                if constexpr (MODE == kByRows) {
+                    ok = ptx::mbar_wait(&ffull[fset], fset_phase, abort_flag);   // every lane: the copies are others'
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    const uint8_t* set = reinterpret_cast<const uint8_t*>(colf) + fset * kFactorSetBytes<MODE>;
+                    const float4 a = *reinterpret_cast<const float4*>(set + (qd * 32 + lane) * 16);
+                    const float4 b = *reinterpret_cast<const float4*>(set + (128 + (h >> 1)) * 16);
+                    fa[0] = a.x; fa[1] = a.y; fa[2] = a.z; fa[3] = a.w;
+                    fb[0] = b.x; fb[1] = b.y; fb[2] = b.z; fb[3] = b.w;
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&fempty[fset]);
+                    if (++fset == kFactorSets) { fset = 0; fset_phase ^= 1u; }
+                } else {
+                    block_factors4(fa, p.sa, p.ga, m_safe, kb0, KB, vec_a != 0);
+                }
                 if (COLSCALE) {
                     __syncwarp();   // the previous group's factors have been read
 #pragma unroll
@@ -1216,14 +1443,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                     }
                     __syncwarp();
                 } else {
-                    block_factors4(fb, p.sb, p.gb, nf, kb0, KB, vec_b != 0);
+                    if (MODE == kDense) block_factors4(fb, p.sb, p.gb, nf, kb0, KB, vec_b != 0);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) fa[j] = __fmul_rn(fa[j], fb[j]);
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (kb0 + j >= t.kb1) break;
-                    if (MODE == kByTokens && kb0 + j < t.kb0) continue;
                     ok = (lane == 0) ? ptx::mbar_wait(&tfull[buf], buf_phase, abort_flag) : false;
                     ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
                     if (!ok) break;
@@ -1271,15 +1497,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                 }
             }
             if (!ok) break;
-            if (MODE == kByTokens && t.kb0 == t.kb1) {   // no tokens: zeros, or nothing to add
-                if (t.lost) {
-                    const float nan = __int_as_float(0x7FC00000);
-#pragma unroll
-                    for (int e = 0; e < CW / 2; ++e) acc[e] = pack2(nan, nan);
-                } else if (p.accumulate) {
-                    continue;
-                }
-            }
 #pragma unroll
             for (int c = 0; c < NCH; ++c)
                 if (n0 < p.N) emit_block_chunk<MODE>(slot, acc + 16 * c, t, m0, n0 + 32 * c, p, &tmD);
@@ -2044,7 +2261,7 @@ int launch_promote(const BlockProblem& b, cudaStream_t stream) {
     constexpr int smem_id = MODE == kDense ? (COLSCALE ? 3 : 1) : MODE == kByRows ? 13 : 14;
     constexpr int cluster_id = MODE == kDense ? (COLSCALE ? 4 : 3) : MODE == kByRows ? 7 : 8;
     return launch_block<MODE>(gemm_block_pair_kernel<C, COLSCALE, MODE>, b, C::TN, C::THREADS,
-                              C::smem(COLSCALE, MODE != kDense), smem_id, cluster_id, stream);
+                              C::template SMEM<COLSCALE, MODE>, smem_id, cluster_id, stream);
 }
 
 // Block-scaled GEMM with fp32 factors (at least one operand with 1x128 or

@@ -271,6 +271,33 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
         : "r"(taddr));
 }
 
+// 16 lanes x 128 bits, four times along the columns (16 columns): of column
+// group i (4 columns), thread t receives column t % 4 of lane t / 4 in r[2i] and
+// of lane t / 4 + 8 in r[2i + 1].
+__device__ __forceinline__ void tmem_ld_16x128b_x4(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr));
+}
+
+// Asynchronous copies of 16 or 4 bytes into shared memory by the threads, with
+// zeros instead of them unless `on`; groups as committed by this thread.
+__device__ __forceinline__ void cp_async16(uint32_t smem_dst, const void* src, bool on) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(src), "r"(on ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t smem_dst, const void* src, bool on) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_dst), "l"(src), "r"(on ? 4 : 0)
+                 : "memory");
+}
+// Arrive on `bar` (counted in it beforehand) when this thread's copies so far
+// have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Warpgroup register re-allocation (every warp of the warpgroup executes the
 // same instruction): give back registers down to N per thread, or wait for
 // the block's pool to provide N per thread.
