@@ -5,8 +5,10 @@
 //   h = act(z_g) z_u,  q = codes of h,  z_q = codes of z        (1x128 blocks)
 //   dz_g = dD z_u act'(z_g),  dz_u = dD act(z_g)                (from z_q)
 //
-// A warp takes rows of one 128-column block, four columns a lane, so a row's
-// maximum is one warp reduction and a column's stays in the lane's registers
+// By rows (codes of rows only), eight lanes take a row's 128-column block, sixteen
+// columns a lane: fewest instructions an element.  By tiles of 128 x 128 (codes
+// along the tokens as well), a warp takes rows, four columns a lane: a row's
+// maximum is one warp reduction, and a column's stays in the lane's registers
 // over the rows.  Values are FP32 between the inputs and the one rounding of
 // each code.
 #include <cstdint>
@@ -107,6 +109,17 @@ __device__ __forceinline__ int2 rows_of(const int32_t* offsets, int experts, int
     return make_int2(ends[0], ends[1]);
 }
 
+// Row group (or tile row) and column block of a unit of work; units are fewer
+// than 2^31, and 64-bit divisions would take as long as ten elements' work.
+struct Place {
+    uint32_t row;
+    int blk;
+};
+__device__ __forceinline__ Place place(uint32_t unit, int blocks) {
+    const uint32_t r = unit / static_cast<uint32_t>(blocks);
+    return Place{r, static_cast<int>(unit - r * static_cast<uint32_t>(blocks))};
+}
+
 // ------------------------------------------------------------------ forward
 
 struct ActBlock {
@@ -122,77 +135,123 @@ struct ActBlock {
     int experts;
 };
 
-// R rows of one 128-column block of h a warp.
-template <int ACT, bool GATED, int R>
+// A lane's sixteen columns of a row: eight from 8 (lane % 8) and eight 64 further.
+struct Raw16 {
+    uint4 w[2];
+};
+
+__device__ __forceinline__ uint4 ld16(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ void bf16_pairs(f2 (&v)[4], const uint4& w) {
+    v[0] = row::bf2(w.x); v[1] = row::bf2(w.y); v[2] = row::bf2(w.z); v[3] = row::bf2(w.w);
+}
+
+// The largest magnitudes of a lane's sixteen bf16 in the low half of the word
+// (the bits of a bf16 order like its magnitude, NaN above all).
+__device__ __forceinline__ uint32_t top16(const Raw16& r) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        m = __vmaxu2(m, __vmaxu2(r.w[k].x & 0x7FFF7FFFu, r.w[k].y & 0x7FFF7FFFu));
+        m = __vmaxu2(m, __vmaxu2(r.w[k].z & 0x7FFF7FFFu, r.w[k].w & 0x7FFF7FFFu));
+    }
+    return max(m >> 16, m & 0xFFFFu);
+}
+
+__device__ __forceinline__ uint32_t top16(const f2 (&v)[2][4]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = row::max_abs(row::max_abs(m, row::lo2(v[k][i])), row::hi2(v[k][i]));
+    return row::abs_bits(m);
+}
+
+// The largest over eight lanes, of a word or of its two halves.
+__device__ __forceinline__ uint32_t eight_max(uint32_t m) {
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(row::kAll, m, o));
+    return m;
+}
+__device__ __forceinline__ uint32_t eight_max2(uint32_t m) {
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(row::kAll, m, o));
+    return m;
+}
+
+// Writes the codes of a lane's sixteen columns, v * s.
+__device__ __forceinline__ void put16(uint8_t* to, int fmt, const f2 (&v)[2][4], float s) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        *reinterpret_cast<uint2*>(to + 64 * k) =
+            fmt == 0 ? row::cvt8<0>(v[k], row::all2(s)) : row::cvt8<1>(v[k], row::all2(s));
+}
+
+// Four rows of one 128-column block of h a warp.  The first lanes of a row's
+// eight have the scales of its h, gate and up.
+template <int ACT, bool GATED>
 __global__ void __launch_bounds__(kThreads, 4) act_block_kernel(const __grid_constant__ ActBlock p) {
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const int2 rows = rows_of(p.offsets, p.experts, p.M);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-    const int blk = static_cast<int>(unit % p.blocks);
-    const int64_t r0 = rows.x + unit / p.blocks * R;
-    if (r0 >= rows.y) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & 7;
+    const Place at = place(blockIdx.x * kWarps + warp, p.blocks);
+    const int64_t base = rows.x + static_cast<int64_t>(at.row) * 4, r = base + (lane >> 3);
+    if (base >= rows.y) return;
     const int64_t N = static_cast<int64_t>(p.blocks) * 128, W = GATED ? 2 * N : N;
     const int wb = GATED ? 2 * p.blocks : p.blocks;   // factors a row of z
-    const int c = blk * 128 + lane * 4;
-    uint2 g[R], u[GATED ? R : 1];
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int64_t r = r0 + i;
-        g[i] = make_uint2(0, 0);
-        if (GATED) u[i] = make_uint2(0, 0);
-        if (r < rows.y) {
-            g[i] = ld8(p.z + r * W + c);
-            if (GATED) u[i] = ld8(p.z + r * W + N + c);
+    const int c = at.blk * 128 + sub * 8;
+    const bool on = r < rows.y;
+    Raw16 g = {}, u = {};
+    if (on) {
+        const __nv_bfloat16* z = p.z + r * W + c;
+        g.w[0] = ld16(z);
+        g.w[1] = ld16(z + 64);
+        if (GATED) {
+            u.w[0] = ld16(z + N);
+            u.w[1] = ld16(z + N + 64);
         }
     }
-    // lane 4 i + k keeps the maximum of row i's h (k = 0), gate (1), up (2)
-    Quad h[R];
-    uint32_t mine = 0;
+    f2 a[2][4], b[2][4], h[2][4];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const Quad a = from_bf16(g[i]);
+    for (int k = 0; k < 2; ++k) {
+        bf16_pairs(a[k], g.w[k]);
+        if (GATED) bf16_pairs(b[k], u.w[k]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            h[i].v[j] = act2<ACT>(a.v[j]);
-            if (GATED) h[i].v[j] = row::mul2(h[i].v[j], from_bf16(u[i]).v[j]);
-        }
-        if (p.q) {
-            const uint32_t m = row_top(h[i]);
-            if (lane == 4 * i) mine = m;
-        }
-        if (p.zq) {
-            const uint32_t m = row_top(a);
-            if (lane == 4 * i + 1) mine = m;
-            if (GATED) {
-                const uint32_t n = row_top(from_bf16(u[i]));
-                if (lane == 4 * i + 2) mine = n;
-            }
+        for (int j = 0; j < 4; ++j) {
+            h[k][j] = act2<ACT>(a[k][j]);
+            if (GATED) h[k][j] = row::mul2(h[k][j], b[k][j]);
         }
     }
-    const int kind = lane & 3;
-    const float s = row::block_scale(mine, kind == 0 ? p.fmt : FP8_E4M3, p.pow2);
-    const int64_t mr = r0 + (lane >> 2);
-    if ((lane >> 2) < R && mr < rows.y) {
+    uint32_t mine = eight_max(top16(h));
+    if (p.zq) {
+        uint32_t m = top16(g);
+        if (GATED) m |= top16(u) << 16;
+        m = eight_max2(m);
+        if (sub == 1) mine = m << 16;
+        if (GATED && sub == 2) mine = m & 0xFFFF0000u;
+    }
+    const float s = row::block_scale(mine, sub == 0 ? p.fmt : FP8_E4M3, p.pow2);
+    if (on && sub < 3) {
         const float f = __fdiv_rn(1.0f, s);
-        if (kind == 0 && p.q) p.inv[mr * p.blocks + blk] = f;
-        if (kind == 1 && p.zq) p.z_inv[mr * wb + blk] = f;
-        if (GATED && kind == 2 && p.zq) p.z_inv[mr * wb + p.blocks + blk] = f;
+        if (sub == 0 && p.q) p.inv[r * p.blocks + at.blk] = f;
+        if (sub == 1 && p.zq) p.z_inv[r * wb + at.blk] = f;
+        if (GATED && sub == 2 && p.zq) p.z_inv[r * wb + p.blocks + at.blk] = f;
     }
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const float sh = __shfl_sync(row::kAll, s, 4 * i), sg = __shfl_sync(row::kAll, s, 4 * i + 1);
-        const float su = GATED ? __shfl_sync(row::kAll, s, 4 * i + 2) : 0.0f;
-        const int64_t r = r0 + i;
-        if (r >= rows.y) break;
-        if (p.q) *reinterpret_cast<uint32_t*>(p.q + r * N + c) = code4(p.fmt, h[i], row::all2(sh), row::all2(sh));
-        if (p.zq) {
-            *reinterpret_cast<uint32_t*>(p.zq + r * W + c) = code4(0, from_bf16(g[i]), row::all2(sg), row::all2(sg));
-            if (GATED)
-                *reinterpret_cast<uint32_t*>(p.zq + r * W + N + c) =
-                    code4(0, from_bf16(u[i]), row::all2(su), row::all2(su));
-        }
+    const int from = lane & 24;
+    const float sh = __shfl_sync(row::kAll, s, from), sg = __shfl_sync(row::kAll, s, from + 1);
+    const float su = __shfl_sync(row::kAll, s, from + 2);
+    if (!on) return;
+    if (p.q) put16(p.q + r * N + c, p.fmt, h, sh);
+    if (p.zq) {
+        put16(p.zq + r * W + c, FP8_E4M3, a, sg);
+        if (GATED) put16(p.zq + r * W + N + c, FP8_E4M3, b, su);
     }
 }
 
@@ -280,6 +339,7 @@ struct ActBlockBwd {
     int fmt, h_fmt, pow2;
     const int32_t* offsets;
     int experts;
+    unsigned* status;
 };
 
 // What a lane reads of one row, and the values that come of it.
@@ -306,190 +366,249 @@ struct BwdRow {
     }
 };
 
-// R rows of one 128-column block of dD a warp: row codes only.
-template <int ACT, bool GATED, int R>
-__global__ void __launch_bounds__(kThreads, 4) act_block_bwd_rows_kernel(const __grid_constant__ ActBlockBwd p) {
+// Four rows of one 128-column block of dD a warp: row codes only.  The first two
+// lanes of a row's eight have the scales of its gate's (or only) and up gradient.
+template <int ACT, bool GATED>
+__global__ void __launch_bounds__(kThreads, GATED ? 4 : 5) act_block_bwd_rows_kernel(const __grid_constant__ ActBlockBwd p) {
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const int2 rows = rows_of(p.offsets, p.experts, p.M);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-    const int blk = static_cast<int>(unit % p.blocks);
-    const int64_t r0 = rows.x + unit / p.blocks * R;
-    if (r0 >= rows.y) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & 7;
+    const Place at = place(blockIdx.x * kWarps + warp, p.blocks);
+    const int64_t base = rows.x + static_cast<int64_t>(at.row) * 4, r = base + (lane >> 3);
+    if (base >= rows.y) return;
     const int64_t N = static_cast<int64_t>(p.blocks) * 128, W = GATED ? 2 * N : N;
     const int wb = GATED ? 2 * p.blocks : p.blocks;
-    const int c = blk * 128 + lane * 4;
-    uint2 d[R];
-    uint32_t zg[R], zu[GATED ? R : 1];
-    float fg[R], fu[GATED ? R : 1];
+    const int c = at.blk * 128 + sub * 8;
+    const bool on = r < rows.y;
+    Raw16 d = {};
+    uint2 zg[2] = {}, zu[2] = {};
+    float fg = 0.0f, fu = 0.0f;
+    if (on) {
+        const uint8_t* z = p.zq + r * W + c;
+        fg = p.z_inv[r * wb + at.blk];
+        if (GATED) fu = p.z_inv[r * wb + p.blocks + at.blk];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int64_t r = r0 + i < rows.y ? r0 + i : r0;   // rows past the last are read again and not written
-        d[i] = ld8(p.d + r * N + c);
-        zg[i] = ld4(p.zq + r * W + c);
-        fg[i] = p.z_inv[r * wb + blk];
-        if (GATED) {
-            zu[i] = ld4(p.zq + r * W + N + c);
-            fu[i] = p.z_inv[r * wb + p.blocks + blk];
+        for (int k = 0; k < 2; ++k) {
+            d.w[k] = ld16(p.d + r * N + c + 64 * k);
+            zg[k] = ld8(z + 64 * k);
+            if (GATED) zu[k] = ld8(z + N + 64 * k);
         }
     }
-    // lane 2 i + k keeps the maximum of row i's gate (k = 0) or up (1) gradient
-    BwdRow<ACT, GATED> v[R];
-    uint32_t mine = 0;
+    f2 dg[2][4], du[2][4];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        v[i].eval(d[i], zg[i], GATED ? zu[i] : 0, fg[i], GATED ? fu[i] : 0.0f);
-        const uint32_t m = row_top(v[i].dg);
-        if (lane == 2 * i) mine = m;
-        if (GATED) {
-            const uint32_t n = row_top(v[i].du);
-            if (lane == 2 * i + 1) mine = n;
+    for (int k = 0; k < 2; ++k) {
+        f2 D[4];
+        bf16_pairs(D, d.w[k]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const Quad z = decode4(0, h ? zg[k].y : zg[k].x, fg);
+            Quad u = zero4();
+            if (GATED) u = decode4(0, h ? zu[k].y : zu[k].x, fu);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                f2 a, g;
+                act_and_grad2<ACT>(z.v[j], a, g);
+                dg[k][2 * h + j] = row::mul2(GATED ? row::mul2(D[2 * h + j], u.v[j]) : D[2 * h + j], g);
+                if (GATED) du[k][2 * h + j] = row::mul2(D[2 * h + j], a);
+            }
         }
+    }
+    uint32_t mine = eight_max(top16(dg));
+    if constexpr (GATED) {
+        const uint32_t m = eight_max(top16(du));
+        if (sub == 1) mine = m;
     }
     const float s = row::block_scale(mine, p.fmt, p.pow2);
-    const int64_t mr = r0 + (lane >> 1);
-    if ((lane >> 1) < R && mr < rows.y && (GATED || !(lane & 1)))
-        p.inv[mr * wb + (lane & 1 ? p.blocks : 0) + blk] = __fdiv_rn(1.0f, s);
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const f2 sg = row::all2(__shfl_sync(row::kAll, s, 2 * i));
-        const f2 su = row::all2(GATED ? __shfl_sync(row::kAll, s, 2 * i + 1) : 0.0f);
-        const int64_t r = r0 + i;
-        if (r >= rows.y) break;
-        *reinterpret_cast<uint32_t*>(p.q + r * W + c) = code4(p.fmt, v[i].dg, sg, sg);
-        if (GATED) *reinterpret_cast<uint32_t*>(p.q + r * W + N + c) = code4(p.fmt, v[i].du, su, su);
-    }
+    if (on && sub < (GATED ? 2 : 1)) p.inv[r * wb + (sub ? p.blocks : 0) + at.blk] = __fdiv_rn(1.0f, s);
+    const float sg = __shfl_sync(row::kAll, s, lane & 24), su = __shfl_sync(row::kAll, s, (lane & 24) + 1);
+    if (!on) return;
+    put16(p.q + r * W + c, p.fmt, dg, sg);
+    if constexpr (GATED) put16(p.q + r * W + N + c, p.fmt, du, su);
 }
 
-constexpr int kBwdSmem = 3 * 128 * 128;   // three tiles of turned codes; the maxima before them
+// Shared memory of the tile kernel: two stages of inputs (dD, the gate's codes,
+// the up product's), the warps' column maxima, three tiles of turned codes.
+constexpr int kStageD = 128 * 128 * 2, kStageZ = 128 * 128, kStage = kStageD + 2 * kStageZ;
+constexpr int kParts = kTileWarps * 3 * 128 * 4;
+constexpr int kBwdSmem = 2 * kStage + kParts + 3 * 128 * 128 + 64 + 128;
 
-// One 128 x 128 tile of dD, eight rows a warp.  The values are computed twice, for
-// the maxima and for the codes, from the inputs, which stay in registers as loaded
-// (four bytes an element): FP32 values would take three times as many.
+// 128 x 128 tiles of dD, one CTA an SM, eight rows a warp.  A lane's values (8
+// rows, 4 columns, three numbers each: 96 registers) are computed once and wait
+// there for the rows' and the columns' scales; computed twice instead, with two
+// CTAs an SM, 32768 x 2048 gated took 200 us.  The next tile's inputs come by TMA
+// meanwhile.
 template <int ACT, bool GATED>
-__global__ void __launch_bounds__(kTileThreads, 2) act_block_bwd_kernel(const __grid_constant__ ActBlockBwd p) {
+__global__ void __launch_bounds__(kTileThreads, 1)
+    act_block_bwd_kernel(const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmZ,
+                         const __grid_constant__ ActBlockBwd p) {
     ptx::griddep_launch_dependents();
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
+    float* part = reinterpret_cast<float*>(smem + 2 * kStage);
+    uint8_t* turned = smem + 2 * kStage + kParts;
+    uint64_t* full = reinterpret_cast<uint64_t*>(turned + 3 * 128 * 128);
     __shared__ __align__(16) float scale[3][128];
+    __shared__ uint32_t abort_word;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(&full[0], 1);
+        ptx::mbar_init(&full[1], 1);
+        abort_word = 0;
+        ptx::fence_barrier_init();
+    }
     ptx::griddep_wait();
     const int2 rows = rows_of(p.offsets, p.experts, p.M);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t tile_row = blockIdx.x / p.blocks;
-    const int blk = static_cast<int>(blockIdx.x - tile_row * p.blocks);
-    const int64_t t0 = tile_row * 128;
-    if (t0 + 128 <= rows.x || t0 >= rows.y || rows.x >= rows.y) return;
-    const int64_t N = static_cast<int64_t>(p.blocks) * 128, W = GATED ? 2 * N : N;
+    __syncthreads();
+    const int64_t N = static_cast<int64_t>(p.blocks) * 128, W = GATED ? 2 * N : N, tb = p.M >> 7;
     const int wb = GATED ? 2 * p.blocks : p.blocks;
-    const int c = blk * 128 + lane * 4;
-    const int64_t r0 = t0 + warp * kTileRows;
-    // rows r0 + first .. r0 + last - 1 are the experts'
-    const int first = static_cast<int>(rows.x > r0 ? (rows.x - r0 < kTileRows ? rows.x - r0 : kTileRows) : 0);
-    const int last = static_cast<int>(rows.y > r0 ? (rows.y - r0 < kTileRows ? rows.y - r0 : kTileRows) : 0);
-    uint2 d[kTileRows];
-    uint32_t zg[kTileRows], zu[GATED ? kTileRows : 1];
+    // the tiles with rows of experts
+    const uint32_t tr0 = rows.x >> 7;
+    const uint32_t tiles = rows.y > rows.x ? ((static_cast<uint32_t>(rows.y) + 127) / 128 - tr0) * p.blocks : 0;
+    const uint32_t mine = blockIdx.x < tiles ? (tiles - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+    auto issue = [&](uint32_t k) {   // one thread: this CTA's k-th tile into stage k & 1
+        const Place at = place(blockIdx.x + k * gridDim.x, p.blocks);
+        const int x = at.blk * 128, y = static_cast<int>((tr0 + at.row) * 128);
+        uint8_t* st = smem + (k & 1) * kStage;
+        ptx::mbar_arrive_expect_tx(&full[k & 1], GATED ? kStage : kStageD + kStageZ);
+        ptx::tma_load_2d(st, &tmD, &full[k & 1], x, y);
+        ptx::tma_load_2d(st + kStageD, &tmZ, &full[k & 1], x, y);
+        if (GATED) ptx::tma_load_2d(st + kStageD + kStageZ, &tmZ, &full[k & 1], static_cast<int>(N) + x, y);
+    };
+    if (threadIdx.x == 0)
+        for (uint32_t k = 0; k < mine && k < 2; ++k) issue(k);
+    // a tile of this warp's: rows r0 + first .. r0 + last - 1 are the experts', lane
+    // 2 i has row i's gate factor, lane 2 i + 1 its up factor
+    struct Rows {
+        int64_t tile_row, r0, at_factor;
+        int blk, first, last;
+        bool holds;
+    };
+    auto rows_at = [&](uint32_t k) {
+        const Place here = place(blockIdx.x + k * gridDim.x, p.blocks);
+        Rows t;
+        t.blk = here.blk;
+        t.tile_row = tr0 + here.row;
+        t.r0 = t.tile_row * 128 + warp * kTileRows;
+        t.first = static_cast<int>(rows.x > t.r0 ? (rows.x - t.r0 < kTileRows ? rows.x - t.r0 : kTileRows) : 0);
+        t.last = static_cast<int>(rows.y > t.r0 ? (rows.y - t.r0 < kTileRows ? rows.y - t.r0 : kTileRows) : 0);
+        t.holds = (lane >> 1) >= t.first && (lane >> 1) < t.last && (GATED || !(lane & 1));
+        t.at_factor = (t.r0 + (lane >> 1)) * wb + (lane & 1 ? p.blocks : 0) + t.blk;
+        return t;
+    };
+    uint32_t k = 0;
+    auto factor_at = [&](uint32_t k) {
+        if (k >= mine) return 0.0f;
+        const Rows t = rows_at(k);
+        return t.holds ? p.z_inv[t.at_factor] : 0.0f;
+    };
+    float next_factor = factor_at(0);
+    for (; k < mine; ++k) {
+        const Rows t = rows_at(k);
+        const int64_t tile_row = t.tile_row, t0 = tile_row * 128, r0 = t.r0, at_factor = t.at_factor;
+        const int blk = t.blk, first = t.first, last = t.last, c = blk * 128 + lane * 4;
+        const bool holds = t.holds;
+        const float factor = next_factor;
+        const bool ok = ptx::mbar_wait(&full[k & 1], (k >> 1) & 1u, &abort_word);
+        const uint8_t* st = smem + (k & 1) * kStage;
+        BwdRow<ACT, GATED> v[kTileRows];
+        float tg[4] = {}, tu[4] = {}, th[4] = {};
+        uint32_t top = 0;   // lane 2 i + k: the largest of row i's gate (k = 0) or up (1) gradient
 #pragma unroll
-    for (int i = 0; i < kTileRows; ++i) {
-        d[i] = make_uint2(0, 0);
-        zg[i] = 0;
-        if (GATED) zu[i] = 0;
-        if (i >= first && i < last) {
-            const int64_t r = r0 + i;
-            d[i] = ld8(p.d + r * N + c);
-            zg[i] = ld4(p.zq + r * W + c);
-            if (GATED) zu[i] = ld4(p.zq + r * W + N + c);
+        for (int i = 0; i < kTileRows; ++i) {
+            const int at = warp * kTileRows + i;
+            uint2 d = *reinterpret_cast<const uint2*>(st + at * 256 + lane * 8);
+            uint32_t zg = *reinterpret_cast<const uint32_t*>(st + kStageD + at * 128 + lane * 4);
+            uint32_t zu = GATED ? *reinterpret_cast<const uint32_t*>(st + kStageD + kStageZ + at * 128 + lane * 4) : 0u;
+            if (i < first || i >= last) {
+                d = make_uint2(0, 0);
+                zg = zu = 0;
+            }
+            v[i].eval(d, zg, zu, __shfl_sync(row::kAll, factor, 2 * i),
+                      GATED ? __shfl_sync(row::kAll, factor, 2 * i + 1) : 0.0f);
+            if (p.q) {
+                const uint32_t m = row_top(v[i].dg);
+                if (lane == 2 * i) top = m;
+                if (GATED) {
+                    const uint32_t n = row_top(v[i].du);
+                    if (lane == 2 * i + 1) top = n;
+                }
+            }
+            if (p.qt) {
+                raise4(tg, v[i].dg);
+                if (GATED) raise4(tu, v[i].du);
+            }
+            if (p.ht) raise4(th, v[i].h);
         }
-    }
-    // lane 2 i has row i's gate factor, lane 2 i + 1 its up factor
-    float factor = 0.0f;
-    const bool holds = (lane >> 1) >= first && (lane >> 1) < last && (GATED || !(lane & 1));
-    const int64_t at_factor = (r0 + (lane >> 1)) * wb + (lane & 1 ? p.blocks : 0) + blk;
-    if (holds) factor = p.z_inv[at_factor];
-    float tg[4] = {}, tu[4] = {}, th[4] = {};
-    uint32_t mine = 0;   // lane 2 i + k: the largest of row i's gate (k = 0) or up (1) gradient
+        float4* mine4 = reinterpret_cast<float4*>(part + warp * 3 * 128) + lane;
+        mine4[0] = make_float4(tg[0], tg[1], tg[2], tg[3]);
+        mine4[32] = make_float4(tu[0], tu[1], tu[2], tu[3]);
+        mine4[64] = make_float4(th[0], th[1], th[2], th[3]);
+        // the stage has been read, the maxima are there, the last tile's codes have left `turned`
+        if (!__syncthreads_and(ok)) break;
+        if (threadIdx.x == 0 && k + 2 < mine) issue(k + 2);
+        next_factor = factor_at(k + 1);
+        float* const out[3] = {p.qt ? p.inv_t + static_cast<int64_t>(blk) * 128 * tb + tile_row : nullptr,
+                               p.qt && GATED ? p.inv_t + (N + static_cast<int64_t>(blk) * 128) * tb + tile_row : nullptr,
+                               p.ht ? p.h_inv_t + static_cast<int64_t>(blk) * 128 * tb + tile_row : nullptr};
+        const int fmt[3] = {p.fmt, p.fmt, p.h_fmt};
+        column_scales<3>(part, &scale[0][0], out, fmt, p.pow2, tb);
+        if (p.q) {   // row codes while the other warps are at the columns' scales
+            const float s_row = row::block_scale(top, p.fmt, p.pow2);
+            if (holds) p.inv[at_factor] = __fdiv_rn(1.0f, s_row);
+            uint8_t* q = p.q + r0 * W + c;
 #pragma unroll
-    for (int i = 0; i < kTileRows; ++i) {
-        BwdRow<ACT, GATED> v;
-        v.eval(d[i], zg[i], GATED ? zu[i] : 0, __shfl_sync(row::kAll, factor, 2 * i),
-               GATED ? __shfl_sync(row::kAll, factor, 2 * i + 1) : 0.0f);
-        if (p.q) {
-            const uint32_t m = row_top(v.dg);
-            if (lane == 2 * i) mine = m;
+            for (int i = 0; i < kTileRows; ++i) {
+                const f2 a = row::all2(__shfl_sync(row::kAll, s_row, 2 * i));
+                const f2 b = row::all2(GATED ? __shfl_sync(row::kAll, s_row, 2 * i + 1) : 0.0f);
+                if (i >= first && i < last) {
+                    *reinterpret_cast<uint32_t*>(q) = code4(p.fmt, v[i].dg, a, a);
+                    if (GATED) *reinterpret_cast<uint32_t*>(q + N) = code4(p.fmt, v[i].du, b, b);
+                }
+                q += W;
+            }
+        }
+        __syncthreads();
+        uint32_t w[kTileRows];
+        if (p.qt) {
+            const float4 a = reinterpret_cast<const float4*>(scale[0])[lane];
+            const f2 s0 = row::mk2(a.x, a.y), s1 = row::mk2(a.z, a.w);
+#pragma unroll
+            for (int i = 0; i < kTileRows; ++i) w[i] = code4(p.fmt, v[i].dg, s0, s1);
+            turn8(w);
+            stage8(turned, w, warp, lane);
             if (GATED) {
-                const uint32_t n = row_top(v.du);
-                if (lane == 2 * i + 1) mine = n;
-            }
-        }
-        if (p.qt) {
-            raise4(tg, v.dg);
-            if (GATED) raise4(tu, v.du);
-        }
-        if (p.ht) raise4(th, v.h);
-        // the values are not kept for the second evaluation
-        asm volatile("" : "+r"(d[i].x), "+r"(d[i].y), "+r"(zg[i]));
-        if (GATED) asm volatile("" : "+r"(zu[i]));
-    }
-    float s_row = 1.0f;
-    if (p.q) {
-        s_row = row::block_scale(mine, p.fmt, p.pow2);
-        if (holds) p.inv[at_factor] = __fdiv_rn(1.0f, s_row);
-    }
-    float* part = reinterpret_cast<float*>(smem);
-    float4* mine4 = reinterpret_cast<float4*>(part + warp * 3 * 128) + lane;
-    mine4[0] = make_float4(tg[0], tg[1], tg[2], tg[3]);
-    mine4[32] = make_float4(tu[0], tu[1], tu[2], tu[3]);
-    mine4[64] = make_float4(th[0], th[1], th[2], th[3]);
-    __syncthreads();
-    const int64_t tb = p.M >> 7;
-    float* const out[3] = {p.qt ? p.inv_t + static_cast<int64_t>(blk) * 128 * tb + tile_row : nullptr,
-                           p.qt && GATED ? p.inv_t + (N + static_cast<int64_t>(blk) * 128) * tb + tile_row : nullptr,
-                           p.ht ? p.h_inv_t + static_cast<int64_t>(blk) * 128 * tb + tile_row : nullptr};
-    const int fmt[3] = {p.fmt, p.fmt, p.h_fmt};
-    column_scales<3>(part, &scale[0][0], out, fmt, p.pow2, tb);
-    __syncthreads();   // the maxima have been read: their place takes the tiles
-    const float4 a = reinterpret_cast<const float4*>(scale[0])[lane], b = reinterpret_cast<const float4*>(scale[1])[lane],
-                 e = reinterpret_cast<const float4*>(scale[2])[lane];
-    const f2 sg[2] = {row::mk2(a.x, a.y), row::mk2(a.z, a.w)}, su[2] = {row::mk2(b.x, b.y), row::mk2(b.z, b.w)};
-    const f2 sh[2] = {row::mk2(e.x, e.y), row::mk2(e.z, e.w)};
-    uint32_t wg[kTileRows], wu[kTileRows], wh[kTileRows];
+                const float4 b = reinterpret_cast<const float4*>(scale[1])[lane];
+                const f2 u0 = row::mk2(b.x, b.y), u1 = row::mk2(b.z, b.w);
 #pragma unroll
-    for (int i = 0; i < kTileRows; ++i) {
-        BwdRow<ACT, GATED> v;
-        v.eval(d[i], zg[i], GATED ? zu[i] : 0, __shfl_sync(row::kAll, factor, 2 * i),
-               GATED ? __shfl_sync(row::kAll, factor, 2 * i + 1) : 0.0f);
-        if (p.q) {
-            const f2 a = row::all2(__shfl_sync(row::kAll, s_row, 2 * i));
-            const f2 b = row::all2(GATED ? __shfl_sync(row::kAll, s_row, 2 * i + 1) : 0.0f);
-            if (i >= first && i < last) {
-                *reinterpret_cast<uint32_t*>(p.q + (r0 + i) * W + c) = code4(p.fmt, v.dg, a, a);
-                if (GATED) *reinterpret_cast<uint32_t*>(p.q + (r0 + i) * W + N + c) = code4(p.fmt, v.du, b, b);
+                for (int i = 0; i < kTileRows; ++i) w[i] = code4(p.fmt, v[i].du, u0, u1);
+                turn8(w);
+                stage8(turned + 128 * 128, w, warp, lane);
             }
         }
+        if (p.ht) {
+            const float4 e = reinterpret_cast<const float4*>(scale[2])[lane];
+            const f2 s0 = row::mk2(e.x, e.y), s1 = row::mk2(e.z, e.w);
+#pragma unroll
+            for (int i = 0; i < kTileRows; ++i) w[i] = code4(p.h_fmt, v[i].h, s0, s1);
+            turn8(w);
+            stage8(turned + 2 * 128 * 128, w, warp, lane);
+        }
+        __syncthreads();
+        const int64_t out_at = static_cast<int64_t>(blk) * 128 * p.M + t0;
         if (p.qt) {
-            wg[i] = code4(p.fmt, v.dg, sg[0], sg[1]);
-            if (GATED) wu[i] = code4(p.fmt, v.du, su[0], su[1]);
+            write_tile(turned, p.qt + out_at, p.M);
+            if (GATED) write_tile(turned + 128 * 128, p.qt + N * p.M + out_at, p.M);
         }
-        if (p.ht) wh[i] = code4(p.h_fmt, v.h, sh[0], sh[1]);
+        if (p.ht) write_tile(turned + 2 * 128 * 128, p.ht + out_at, p.M);
     }
-    if (p.qt) {
-        turn8(wg);
-        stage8(smem, wg, warp, lane);
-        if (GATED) {
-            turn8(wu);
-            stage8(smem + 128 * 128, wu, warp, lane);
-        }
+    if (threadIdx.x == 0 && k < mine) {
+        // a wait gave up: let the copies already issued land before the CTA's
+        // shared memory is released
+        uint32_t never = 0;
+        for (uint32_t j = k; j < mine && j < k + 2; ++j) ptx::mbar_wait(&full[j & 1], (j >> 1) & 1u, &never);
+        if (p.status) atomicOr(p.status, 1u);
     }
-    if (p.ht) {
-        turn8(wh);
-        stage8(smem + 2 * 128 * 128, wh, warp, lane);
-    }
-    __syncthreads();
-    const int64_t at = static_cast<int64_t>(blk) * 128 * p.M + t0;
-    if (p.qt) {
-        write_tile(smem, p.qt + at, p.M);
-        if (GATED) write_tile(smem + 128 * 128, p.qt + N * p.M + at, p.M);
-    }
-    if (p.ht) write_tile(smem + 2 * 128 * 128, p.ht + at, p.M);
 }
 
 // ------------------------------------------------------------------ a kept input, transposed
@@ -504,88 +623,96 @@ struct BlockTranspose {
     int pow2;
 };
 
+// Two CTAs an SM walk the tiles; a tile's codes are loaded while the one before
+// it is cast, and held as codes (decoded twice).
 template <int FMT>
-__global__ void __launch_bounds__(kTileThreads, 3) block_transpose_kernel(const __grid_constant__ BlockTranspose p) {
+__global__ void __launch_bounds__(kTileThreads, 2) block_transpose_kernel(const __grid_constant__ BlockTranspose p) {
     ptx::griddep_launch_dependents();
-    __shared__ __align__(16) uint8_t tile[128 * 128];   // the maxima, then the turned codes
+    __shared__ __align__(16) uint8_t turned[128 * 128];
+    __shared__ __align__(16) float part[kTileWarps * 128];
     __shared__ __align__(16) float scale[128];
     ptx::griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t tile_row = blockIdx.x / p.blocks;
-    const int blk = static_cast<int>(blockIdx.x - tile_row * p.blocks);
-    const int64_t cols = static_cast<int64_t>(p.blocks) * 128, r0 = tile_row * 128 + warp * kTileRows;
-    const int c = blk * 128 + lane * 4;
-    uint32_t w[kTileRows];
+    const int64_t cols = static_cast<int64_t>(p.blocks) * 128, tb = p.rows >> 7;
+    const uint32_t tiles = static_cast<uint32_t>(tb) * p.blocks;
+    uint32_t next[kTileRows];
+    float next_factor = 0.0f;
+    auto load = [&](uint32_t tile) {
+        if (tile >= tiles) return;
+        const Place at = place(tile, p.blocks);
+        const int blk = at.blk;
+        const int64_t r0 = static_cast<int64_t>(at.row) * 128 + warp * kTileRows;
+        const uint8_t* q = p.q + r0 * cols + blk * 128 + lane * 4;
 #pragma unroll
-    for (int i = 0; i < kTileRows; ++i) w[i] = ld4(p.q + (r0 + i) * cols + c);
-    const float factor = lane < kTileRows ? p.inv[(r0 + lane) * p.blocks + blk] : 0.0f;
-    float top[4] = {};
+        for (int i = 0; i < kTileRows; ++i, q += cols) next[i] = ld4(q);
+        if (lane < kTileRows) next_factor = p.inv[(r0 + lane) * p.blocks + blk];
+    };
+    load(blockIdx.x);
+    for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        uint32_t w[kTileRows];
 #pragma unroll
-    for (int i = 0; i < kTileRows; ++i) {
-        raise4(top, decode4(FMT, w[i], __shfl_sync(row::kAll, factor, i)));
-        asm volatile("" : "+r"(w[i]));   // decoded again below
+        for (int i = 0; i < kTileRows; ++i) w[i] = next[i];
+        const float factor = next_factor;
+        load(tile + gridDim.x);
+        const Place here = place(tile, p.blocks);
+        const int64_t tile_row = here.row;
+        const int blk = here.blk;
+        float top[4] = {};
+#pragma unroll
+        for (int i = 0; i < kTileRows; ++i) {
+            raise4(top, decode4(FMT, w[i], __shfl_sync(row::kAll, factor, i)));
+            asm volatile("" : "+r"(w[i]));   // decoded again below
+        }
+        reinterpret_cast<float4*>(part + warp * 128)[lane] = make_float4(top[0], top[1], top[2], top[3]);
+        __syncthreads();   // also: the last tile's codes have left `turned`
+        float* const out[1] = {p.inv_t + static_cast<int64_t>(blk) * 128 * tb + tile_row};
+        const int fmt[1] = {FMT};
+        column_scales<1>(part, scale, out, fmt, p.pow2, tb);
+        __syncthreads();
+        const float4 s = reinterpret_cast<const float4*>(scale)[lane];
+        const f2 s0 = row::mk2(s.x, s.y), s1 = row::mk2(s.z, s.w);
+#pragma unroll
+        for (int i = 0; i < kTileRows; ++i)
+            w[i] = code4(FMT, decode4(FMT, w[i], __shfl_sync(row::kAll, factor, i)), s0, s1);
+        turn8(w);
+        stage8(turned, w, warp, lane);
+        __syncthreads();
+        write_tile(turned, p.qt + static_cast<int64_t>(blk) * 128 * p.rows + tile_row * 128, p.rows);
     }
-    float* part = reinterpret_cast<float*>(tile);
-    reinterpret_cast<float4*>(part + warp * 128)[lane] = make_float4(top[0], top[1], top[2], top[3]);
-    __syncthreads();
-    const int64_t tb = p.rows >> 7;
-    float* const out[1] = {p.inv_t + static_cast<int64_t>(blk) * 128 * tb + tile_row};
-    const int fmt[1] = {FMT};
-    column_scales<1>(part, scale, out, fmt, p.pow2, tb);
-    __syncthreads();
-    const float4 s = reinterpret_cast<const float4*>(scale)[lane];
-    const f2 s0 = row::mk2(s.x, s.y), s1 = row::mk2(s.z, s.w);
-#pragma unroll
-    for (int i = 0; i < kTileRows; ++i)
-        w[i] = code4(FMT, decode4(FMT, w[i], __shfl_sync(row::kAll, factor, i)), s0, s1);
-    turn8(w);
-    stage8(tile, w, warp, lane);
-    __syncthreads();
-    write_tile(tile, p.qt + static_cast<int64_t>(blk) * 128 * p.rows + tile_row * 128, p.rows);
 }
 
 // ------------------------------------------------------------------ host side
 
-constexpr int kRows = 4;   // rows a warp where there are many
-
-// Whether kRows rows a warp still leave every SM several CTAs.
-bool many_rows(int64_t M, int64_t blocks) {
-    return M * blocks >= int64_t{kRows} * kWarps * 4 * num_sms();
-}
-
-dim3 row_grid(int64_t M, int64_t blocks, bool many) {
-    const int64_t warps = (many ? (M + kRows - 1) / kRows : M) * blocks;
-    return dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps));
+// Four rows of one column block a warp.
+dim3 row_grid(int64_t M, int64_t blocks) {
+    return dim3(static_cast<unsigned>(((M + 3) / 4 * blocks + kWarps - 1) / kWarps));
 }
 
 template <int ACT>
 int launch_fwd(const ActBlock& p, bool gated, cudaStream_t st) {
-    const bool many = many_rows(p.M, p.blocks);
-    const dim3 grid = row_grid(p.M, p.blocks, many), block(kThreads);
-    if (gated) {
-        if (many) launch_pdl(act_block_kernel<ACT, true, kRows>, grid, block, 0, st, p);
-        else launch_pdl(act_block_kernel<ACT, true, 1>, grid, block, 0, st, p);
-    } else {
-        if (many) launch_pdl(act_block_kernel<ACT, false, kRows>, grid, block, 0, st, p);
-        else launch_pdl(act_block_kernel<ACT, false, 1>, grid, block, 0, st, p);
-    }
+    const dim3 grid = row_grid(p.M, p.blocks), block(kThreads);
+    if (gated) launch_pdl(act_block_kernel<ACT, true>, grid, block, 0, st, p);
+    else launch_pdl(act_block_kernel<ACT, false>, grid, block, 0, st, p);
     return FP8_OK;
 }
 
 template <int ACT, bool GATED>
 int launch_bwd(const ActBlockBwd& p, cudaStream_t st) {
     if (!p.qt && !p.ht) {
-        const bool many = many_rows(p.M, p.blocks);
-        const dim3 grid = row_grid(p.M, p.blocks, many), block(kThreads);
-        if (many) launch_pdl(act_block_bwd_rows_kernel<ACT, GATED, kRows>, grid, block, 0, st, p);
-        else launch_pdl(act_block_bwd_rows_kernel<ACT, GATED, 1>, grid, block, 0, st, p);
+        launch_pdl(act_block_bwd_rows_kernel<ACT, GATED>, row_grid(p.M, p.blocks), dim3(kThreads), 0, st, p);
         return FP8_OK;
     }
     static host::SmemAllowance allowance;
-    const int r = host::allow_smem(act_block_bwd_kernel<ACT, GATED>, kBwdSmem, allowance);
+    CUtensorMap tmD, tmZ;
+    const int64_t N = static_cast<int64_t>(p.blocks) * 128;
+    int r = make_bf16_box_map(&tmD, p.d, p.M, N, 128, 128);
+    if (r == FP8_OK) r = make_codes_box_map(&tmZ, p.zq, p.M, GATED ? 2 * N : N, 128, 128);
+    if (r == FP8_OK) r = host::allow_smem(act_block_bwd_kernel<ACT, GATED>, kBwdSmem, allowance);
     if (r != FP8_OK) return r;
-    const dim3 grid(static_cast<unsigned>(p.M / 128 * p.blocks)), block(kTileThreads);
-    launch_pdl(act_block_bwd_kernel<ACT, GATED>, grid, block, kBwdSmem, st, p);
+    const int64_t tiles = p.M / 128 * p.blocks;
+    const int sms = num_sms();
+    launch_pdl(act_block_bwd_kernel<ACT, GATED>, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)),
+               dim3(kTileThreads), kBwdSmem, st, tmD, tmZ, p);
     return FP8_OK;
 }
 
@@ -678,7 +805,7 @@ int fp8_act_block_bwd(const fp8_act_block_bwd_args_t* a, void* stream) {
     if (a->M == 0) return FP8_OK;
     const ActBlockBwd p{static_cast<const __nv_bfloat16*>(a->dD), a->z_q, a->z_scale_inv, a->q, a->scale_inv,
                         a->q_t, a->scale_inv_t, a->h_t, a->h_scale_inv_t, a->M, static_cast<int>(a->N / 128),
-                        a->q_format, a->h_format, a->pow2, a->offsets, a->experts};
+                        a->q_format, a->h_format, a->pow2, a->offsets, a->experts, device_status_word()};
     r = by_act(a->act, [&](auto act) { return launch_bwd<decltype(act)::value>(p, a->gated != 0, as_stream(stream)); });
     return r != FP8_OK ? r : launch_status(what);
 }
@@ -700,7 +827,8 @@ int fp8_block_transpose(const uint8_t* q, const float* scale_inv, int64_t rows, 
         return set_error(FP8_ERR_ALIGN, "%s: factors must be 4-byte aligned", what);
     if (rows == 0) return FP8_OK;
     const BlockTranspose p{q, scale_inv, q_t, scale_inv_t, rows, static_cast<int>(cols / 128), pow2};
-    const dim3 grid(static_cast<unsigned>(rows / 128 * p.blocks)), block(kTileThreads);
+    const int64_t tiles = rows / 128 * p.blocks, slots = 2 * static_cast<int64_t>(num_sms());
+    const dim3 grid(static_cast<unsigned>(tiles < slots ? tiles : slots)), block(kTileThreads);
     if (format == FP8_E4M3) launch_pdl(block_transpose_kernel<0>, grid, block, 0, as_stream(stream), p);
     else launch_pdl(block_transpose_kernel<1>, grid, block, 0, as_stream(stream), p);
     return launch_status(what);

@@ -388,9 +388,9 @@ int fp8_gemm_experts(const fp8_gemm_experts_args_t* a, void* stream) {
     const int64_t rows = (a->M + a->experts - 1) / a->experts;
     cudaStream_t st = as_stream(stream);
     if (rows <= 8) return launch_few<16>(g, st);
-    if (rows <= 24) return launch_few<32>(g, st);
-    if (rows <= 48) return launch_few<64>(g, st);
-    if (rows <= 96) return launch_few<128>(g, st);
+    if (rows <= 16) return launch_few<32>(g, st);
+    if (rows <= 40) return launch_few<64>(g, st);
+    if (rows <= 112) return launch_few<128>(g, st);
     r = launch_gemm_by_rows(g, st);
     return r != FP8_OK ? r : launch_status(what);
 }

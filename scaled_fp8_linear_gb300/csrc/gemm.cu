@@ -2041,23 +2041,37 @@ int make_mnmajor_map(CUtensorMap* map, const void* ptr, int64_t MN, int64_t K) {
 
 }  // namespace
 
-int make_bf16_box_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols,
-                      uint32_t box_cols, uint32_t box_rows) {
+namespace {
+
+int make_box_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, uint32_t box_cols,
+                 uint32_t box_rows, CUtensorMapDataType type, int64_t size) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return set_error(FP8_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols * size)};
     const cuuint32_t box[2] = {box_cols, box_rows};
     const cuuint32_t estr[2] = {1, 1};
-    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims,
+    const CUresult r = fn(map, type, 2, const_cast<void*>(ptr), dims,
                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
-        return set_error(FP8_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for bf16 [%lld x %lld]",
+        return set_error(FP8_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for [%lld x %lld] of %d bytes",
                          static_cast<int>(r), static_cast<long long>(rows),
-                         static_cast<long long>(cols));
+                         static_cast<long long>(cols), static_cast<int>(size));
     return FP8_OK;
+}
+
+}  // namespace
+
+int make_bf16_box_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols,
+                      uint32_t box_cols, uint32_t box_rows) {
+    return make_box_map(map, ptr, rows, cols, box_cols, box_rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2);
+}
+
+int make_codes_box_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols,
+                       uint32_t box_cols, uint32_t box_rows) {
+    return make_box_map(map, ptr, rows, cols, box_cols, box_rows, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1);
 }
 
 namespace {

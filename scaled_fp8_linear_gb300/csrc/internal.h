@@ -40,6 +40,10 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 int make_bf16_box_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols,
                       uint32_t box_cols, uint32_t box_rows);
 
+// The same of FP8 codes.
+int make_codes_box_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols,
+                       uint32_t box_cols, uint32_t box_rows);
+
 // Tensor map of a K-contiguous FP8 matrix [rows x K]: boxes of 128 bytes of K
 // by box_rows rows, 128-byte swizzle, zero fill outside the matrix.
 int make_kmajor_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t K, uint32_t box_rows);
