@@ -624,7 +624,7 @@ struct BlockTranspose {
 };
 
 // Two CTAs an SM walk the tiles; a tile's codes are loaded while the one before
-// it is cast, and held as codes (decoded twice).
+// it is cast.
 template <int FMT>
 __global__ void __launch_bounds__(kTileThreads, 2) block_transpose_kernel(const __grid_constant__ BlockTranspose p) {
     ptx::griddep_launch_dependents();
@@ -657,11 +657,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_transpose_kernel(const 
         const Place here = place(tile, p.blocks);
         const int64_t tile_row = here.row;
         const int blk = here.blk;
+        Quad v[kTileRows];
         float top[4] = {};
 #pragma unroll
         for (int i = 0; i < kTileRows; ++i) {
-            raise4(top, decode4(FMT, w[i], __shfl_sync(row::kAll, factor, i)));
-            asm volatile("" : "+r"(w[i]));   // decoded again below
+            v[i] = decode4(FMT, w[i], __shfl_sync(row::kAll, factor, i));
+            raise4(top, v[i]);
         }
         reinterpret_cast<float4*>(part + warp * 128)[lane] = make_float4(top[0], top[1], top[2], top[3]);
         __syncthreads();   // also: the last tile's codes have left `turned`
@@ -672,8 +673,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_transpose_kernel(const 
         const float4 s = reinterpret_cast<const float4*>(scale)[lane];
         const f2 s0 = row::mk2(s.x, s.y), s1 = row::mk2(s.z, s.w);
 #pragma unroll
-        for (int i = 0; i < kTileRows; ++i)
-            w[i] = code4(FMT, decode4(FMT, w[i], __shfl_sync(row::kAll, factor, i)), s0, s1);
+        for (int i = 0; i < kTileRows; ++i) w[i] = code4(FMT, v[i], s0, s1);
         turn8(w);
         stage8(turned, w, warp, lane);
         __syncthreads();
