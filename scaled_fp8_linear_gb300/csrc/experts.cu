@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(Few<TN>::THREADS, 1)
                 const FewTile t = few_tile<TN>(u, units, p);
                 const int yw = t.expert * p.N + t.n_blk * 128;
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
+                    if (!ptx::mbar_wait<true>(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
                     uint8_t* s = ring + stage * L::STAGE_BYTES;
                     ptx::mbar_arrive_expect_tx(&full[stage], L::STAGE_BYTES);
                     ptx::tma_load_2d(s, &tmW, &full[stage], kb * BK, yw);
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(Few<TN>::THREADS, 1)
             uint32_t never = 0;   // drain: the last copies into each slot have landed
             for (int s = 0; s < STAGES; ++s) {
                 if (issued <= s && issued < STAGES) break;
-                ptx::mbar_wait(&full[s], static_cast<uint32_t>(s) < stage ? phase : phase ^ 1u, &never);
+                ptx::mbar_wait<true>(&full[s], static_cast<uint32_t>(s) < stage ? phase : phase ^ 1u, &never);
             }
         }
     } else if (warp == 1) {
@@ -181,8 +181,8 @@ __global__ void __launch_bounds__(Few<TN>::THREADS, 1)
             bool ok = true;
             for (int u = u0; ok && u < num_units; u += step) {
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (!ptx::mbar_wait(&tempty[buf], buf_phase ^ 1u, abort_flag)) { ok = false; break; }
-                    if (!ptx::mbar_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
+                    if (!ptx::mbar_wait<true>(&tempty[buf], buf_phase ^ 1u, abort_flag)) { ok = false; break; }
+                    if (!ptx::mbar_wait<true>(&full[stage], phase, abort_flag)) { ok = false; break; }
                     ptx::tc_fence_after();
                     uint8_t* s = ring + stage * L::STAGE_BYTES;
                     const uint64_t wd = ptx::sdesc_kmajor_sw128(ptx::smem_u32(s));
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(Few<TN>::THREADS, 1)
             }
             uint32_t never = 0;
             ptx::mma_commit(done);
-            ptx::mbar_wait(done, 0, &never);
+            ptx::mbar_wait<true>(done, 0, &never);
         }
     } else if (warp == 3) {
         constexpr int PER = TN < 32 ? 1 : TN / 32;   // tokens a lane
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(Few<TN>::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < PER; ++i) f[i] = factors4(token(i), 0, KB, p.vec_a);
             for (int kb = 0; kb < KB; kb += 4) {
-                ok = lane == 0 ? ptx::mbar_wait(&fempty[set], phase ^ 1u, abort_flag) : false;
+                ok = lane == 0 ? ptx::mbar_wait<true>(&fempty[set], phase ^ 1u, abort_flag) : false;
                 ok = __shfl_sync(row::kAll, ok, 0);
                 if (!ok) break;
                 float* to = sets + set * (L::SET_BYTES / 4) + lane;
@@ -248,11 +248,11 @@ __global__ void __launch_bounds__(Few<TN>::THREADS, 1)
             for (int c = 0; c < CW; ++c) acc[c] = 0.0f;
             for (int kb = 0; kb < KB; ++kb) {
                 if ((kb & 3) == 0) {
-                    ok = __all_sync(row::kAll, ptx::mbar_wait(&ffull[set], set_phase, abort_flag));
+                    ok = __all_sync(row::kAll, ptx::mbar_wait<true>(&ffull[set], set_phase, abort_flag));
                     if (!ok) break;
                 }
                 const float* f = sets + set * (L::SET_BYTES / 4) + (kb & 3) * TN + c0;
-                ok = lane == 0 ? ptx::mbar_wait(&tfull[buf], buf_phase, abort_flag) : false;
+                ok = lane == 0 ? ptx::mbar_wait<true>(&tfull[buf], buf_phase, abort_flag) : false;
                 ok = __shfl_sync(row::kAll, ok, 0);
                 if (!ok) break;
                 __syncwarp();

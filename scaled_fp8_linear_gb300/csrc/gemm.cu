@@ -878,14 +878,6 @@ __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
 // TMEM loads (3% faster there, with fewer spills); 256 x 160 tiles with three
 // buffers and 20 promotion warps were 30% slower, and 256 x 128 tiles with
 // four buffers and 8 warps (the earlier form) 24% slower (COLSCALE: 9%).
-// Experts' factors on their way: sets of four K blocks, of the CTA's 128 rows
-// and of the tile's columns (kByTokens: 256, each its own) or 128-column blocks.
-constexpr int kFactorSets = 3;
-template <int MODE>
-constexpr int kFactorCols = MODE == kByTokens ? 256 : 2;
-template <int MODE>
-constexpr int kFactorSetBytes = (128 + kFactorCols<MODE>) * 16;
-
 template <int TN_, int EPI_, int STAGES_, int RROLE_, int RPROMO_>
 struct BpCfg {
     static constexpr int TN = TN_;
@@ -901,21 +893,13 @@ struct BpCfg {
     static constexpr int A_BYTES = 128 * BK;         // this CTA's 128 rows of A
     static constexpr int B_BYTES = (TN / 2) * BK;    // this CTA's half of the TN rows of B
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    // output boxes and factors (floats) of a promotion warp: COLSCALE, four K
-    // blocks of its columns and rows; experts, its share of the CTA's sets
-    template <int MODE>
-    static constexpr int BOXES = MODE == kByTokens ? 2 : 1;
-    template <bool COLSCALE, int MODE>
-    static constexpr int FACTORS = MODE != kDense ? (kFactorSets * kFactorSetBytes<MODE> / 4 + EPI - 1) / EPI
-                                   : COLSCALE     ? 4 * (CW + 32)
-                                                  : 0;
     // shared memory: operand ring, 2 KB of output staging per promotion
     // warp, per-column and per-row factors (COLSCALE only), barriers,
     // alignment slack
-    template <bool COLSCALE, int MODE>
-    static constexpr int SMEM = STAGES * STAGE_BYTES + EPI * (BOXES<MODE> * 2048 + FACTORS<COLSCALE, MODE> * 4) + 256 +
-                                (MODE != kDense ? static_cast<int>(sizeof(Units)) : 0) + 1024;
-
+    static constexpr int smem(bool colscale) {
+        return STAGES * STAGE_BYTES + EPI * (2048 + (colscale ? 4 * (CW + 32) * 4 : 0)) + 256 +
+               1024;
+    }
     static_assert(CW == 64, "a warp's columns: one 64-column slice of a 128-column factor "
                             "block, loaded as two 32-column chunks");
     static_assert(4 * 32 * RROLE + EPI * 32 * RPROMO <= THREADS * (65536 / THREADS / 8 * 8),
@@ -976,6 +960,306 @@ __device__ __forceinline__ void promote_columns(uint64_t* acc, const uint32_t* r
     }
 }
 
+// Round one promoted 32-column chunk (16 packed pairs) plus the bias (if
+// any) and write it through the warp's staging slot: one bf16 box of 32
+// columns, or two FP32 boxes of 16 columns (added to D when accumulating).
+// Whole-warp call; m0 is the warp's first row, n0 the chunk's first column.
+__device__ __forceinline__ void emit_block_chunk(uint8_t* slot, const uint64_t* acc, int64_t m0,
+                                                 int64_t n0, const GemmParams& p,
+                                                 const CUtensorMap* map) {
+    float v[32];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        v[2 * e] = __uint_as_float(static_cast<uint32_t>(acc[e]));
+        v[2 * e + 1] = __uint_as_float(static_cast<uint32_t>(acc[e] >> 32));
+    }
+    if (p.bias) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+            float b[8];
+            load_bias8(b, p.bias, n0 + j);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j + e] = __fadd_rn(v[j + e], b[e]);
+        }
+    }
+    if (p.out == FP8_OUT_BF16) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        const uint4 piece[4] = {make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]),
+                                make_uint4(w[8], w[9], w[10], w[11]),
+                                make_uint4(w[12], w[13], w[14], w[15])};
+        emit_box(slot, piece, map, n0, m0, m0 < p.M, false);
+    } else {
+#pragma unroll
+        for (int hb = 0; hb < 2; ++hb) {
+            uint4 piece[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                piece[j] = make_uint4(__float_as_uint(v[16 * hb + 4 * j]),
+                                      __float_as_uint(v[16 * hb + 4 * j + 1]),
+                                      __float_as_uint(v[16 * hb + 4 * j + 2]),
+                                      __float_as_uint(v[16 * hb + 4 * j + 3]));
+            emit_box(slot, piece, map, n0 + 16 * hb, m0, m0 < p.M, p.accumulate != 0);
+        }
+    }
+}
+
+template <typename Cfg, bool COLSCALE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
+    gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA,
+                           const __grid_constant__ CUtensorMap tmB,
+                           const __grid_constant__ CUtensorMap tmD,
+                           const __grid_constant__ GemmParams p, int vec_a, int vec_b) {
+    ptx::griddep_launch_dependents();   // the next kernel may launch now
+    constexpr int STAGES = Cfg::STAGES, NBUF = Cfg::NBUF, EPI = Cfg::EPI;
+    constexpr int A_BYTES = Cfg::A_BYTES;
+    constexpr int STAGE_BYTES = Cfg::STAGE_BYTES;
+    constexpr int TN = Cfg::TN;
+    constexpr uint32_t TMEM_COLS = 512;   // allocations are powers of two
+    static_assert(NBUF * TN <= 512, "the partial-sum buffers fit in TMEM");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* epi_stage = ring + STAGES * STAGE_BYTES;   // output boxes: 2 KB per epilogue warp
+    float* colf = reinterpret_cast<float*>(epi_stage + EPI * 2048);   // [warp][4][cols + 32]
+    uint64_t* full = reinterpret_cast<uint64_t*>(colf + (COLSCALE ? EPI * 4 * (Cfg::CW + 32) : 0));
+    uint64_t* empty = full + STAGES;
+    uint64_t* tfull = empty + STAGES;
+    uint64_t* tempty = tfull + NBUF;
+    uint64_t* done = tempty + NBUF;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_ctarank();
+    const bool leader = rank == 0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(&full[s], 1);
+            ptx::mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < NBUF; ++b) {
+            ptx::mbar_init(&tfull[b], 1);
+            ptx::mbar_init(&tempty[b], 2 * EPI);   // promotion warps of both CTAs
+        }
+        ptx::mbar_init(done, 1);
+        *abort_flag = 0;
+        ptx::fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        ptx::tma_prefetch_desc(&tmA);
+        ptx::tma_prefetch_desc(&tmB);
+        ptx::tma_prefetch_desc(&tmD);
+    }
+    if (warp == 2) {
+        ptx::tmem_alloc_pair(tmem_slot, TMEM_COLS);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before();
+    ptx::cluster_sync();   // the peer's barriers exist before any remote arrival
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    ptx::griddep_wait();   // the previous kernel's results (operands, factors) are visible
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int num_units = p.num_m * p.num_n;
+    const int KB = p.num_kb;
+
+    if (warp < 4) {
+    ptx::setmaxnreg_dec<Cfg::RROLE>();   // the whole role warpgroup
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0;
+            int64_t issued = 0;
+            bool ok = true;
+            for (int u = pair; ok && u < num_units; u += npairs) {
+                int m_blk, n_blk;
+                tile_coords_g(u, p.num_m, p.num_n, p.group, m_blk, n_blk);
+                const int ya = m_blk * 256 + static_cast<int>(rank) * 128;
+                const int yb = n_blk * TN + static_cast<int>(rank) * (TN / 2);
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
+                    uint8_t* sa = ring + stage * STAGE_BYTES;
+                    const uint32_t bar = ptx::cluster_addr(&full[stage], 0);
+                    if (leader) ptx::mbar_arrive_expect_tx(&full[stage], 2 * STAGE_BYTES);
+                    ptx::tma_load_2d_pair(sa, &tmA, bar, kb * BK, ya);
+                    ptx::tma_load_2d_pair(sa + A_BYTES, &tmB, bar, kb * BK, yb);
+                    ++issued;
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+            }
+            uint32_t never = 0;
+            if (leader) {
+                // drain: the last copies into each slot (both CTAs' bytes) have landed
+                for (int s = 0; s < STAGES; ++s) {
+                    if (issued <= s && issued < STAGES) break;
+                    const uint32_t par = (static_cast<uint32_t>(s) < stage) ? phase : (phase ^ 1u);
+                    ptx::mbar_wait(&full[s], par, &never);
+                }
+            } else if (!ok) {
+                // copies signal the peer's barriers: after an abort, give those in
+                // flight a bounded grace period to land before this CTA moves on
+                const uint64_t t0 = ptx::globaltimer();
+                while (ptx::globaltimer() - t0 < 1000000ull) {
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            const uint32_t idesc = ptx::idesc_f8f6f4(p.fa, p.fb, 256, TN);
+            uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
+            bool ok = true;
+            for (int u = pair; ok && u < num_units; u += npairs) {
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!ptx::mbar_wait(&tempty[buf], buf_phase ^ 1u, abort_flag)) { ok = false; break; }
+                    if (!ptx::mbar_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
+                    ptx::tc_fence_after();
+                    uint8_t* sa = ring + stage * STAGE_BYTES;
+                    const uint64_t ad = ptx::sdesc_kmajor_sw128(ptx::smem_u32(sa));
+                    const uint64_t bd = ptx::sdesc_kmajor_sw128(ptx::smem_u32(sa + A_BYTES));
+                    const uint32_t d = tmem_base + buf * TN;
+#pragma unroll
+                    for (int k = 0; k < BK / UMMA_K; ++k)
+                        ptx::mma_f8f6f4_pair(d, ad + (k * UMMA_K >> 4), bd + (k * UMMA_K >> 4),
+                                             idesc, k != 0);
+                    ptx::mma_commit_pair(&empty[stage], 0x3);
+                    ptx::mma_commit_pair(&tfull[buf], 0x3);
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    if (++buf == NBUF) { buf = 0; buf_phase ^= 1u; }
+                }
+            }
+            uint32_t never = 0;
+            ptx::mma_commit_pair(done, 0x1);
+            ptx::mbar_wait(done, 0, &never);
+        }
+    }
+    } else {
+        ptx::setmaxnreg_inc<Cfg::RPROMO>();   // each promotion warpgroup
+        constexpr int CW = Cfg::CW;              // columns of this warp
+        constexpr int NCH = CW / 32;             // 32-column chunks (COLSCALE factors, stores)
+        const int qd = warp & 3;                 // TMEM lane quarter of this warp
+        const int h = (warp - 4) >> 2;           // which CW-column slice of the tile
+        uint8_t* slot = epi_stage + (warp - 4) * 2048;
+        // COLSCALE: the columns' factors [4 K blocks][CW], then the rows'
+        // [4 K blocks][32 lanes]
+        float* cf = colf + (warp - 4) * 4 * (CW + 32);
+        float* rf = cf + 4 * CW;
+        const uint32_t lanes = static_cast<uint32_t>(qd * 32) << 16;
+        uint32_t buf = 0, buf_phase = 0;
+        bool ok = true;
+        for (int u = pair; ok && u < num_units; u += npairs) {
+            int m_blk, n_blk;
+            tile_coords_g(u, p.num_m, p.num_n, p.group, m_blk, n_blk);
+            const int64_t m0 = static_cast<int64_t>(m_blk) * 256 + rank * 128 + qd * 32;
+            const int64_t m = m0 + lane;
+            const int64_t m_safe = m < p.M ? m : p.M - 1;
+            const int64_t n0 = static_cast<int64_t>(n_blk) * TN + h * CW;
+            // a warp's columns lie all inside or all outside [0, N) (N is a
+            // multiple of 128, CW divides 128); outside, its factors are
+            // read at column N - 1 and its columns are not stored
+            const int64_t nf = n0 < p.N ? n0 : p.N - 1;
+            // FP32 accumulator of CW columns, as packed pairs
+            uint64_t acc[CW / 2];
+#pragma unroll
+            for (int e = 0; e < CW / 2; ++e) acc[e] = 0ull;
+            for (int kb0 = 0; ok && kb0 < KB; kb0 += 4) {
+                // The factors of four K blocks, read at the start of the group
+                // (they hit L1; holding the next group's in registers made the
+                // loop spill): A per row; B per 128-column block, multiplied
+                // into fa here, or (COLSCALE) per column, staged in shared
+                // memory for broadcast reads (lane l writes columns n0+32c+l),
+                // with the rows' factors beside them (registers are short).
+                float fa[4], fb[4];
+                block_factors4(fa, p.sa, p.ga, m_safe, kb0, KB, vec_a != 0);
+                if (COLSCALE) {
+                    __syncwarp();   // the previous group's factors have been read
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) rf[j * 32 + lane] = fa[j];
+#pragma unroll
+                    for (int c = 0; c < NCH; ++c) {
+                        block_factors4(fb, p.sb, p.gb, nf + (n0 < p.N ? 32 * c + lane : 0), kb0, KB,
+                                       vec_b != 0);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) cf[j * CW + 32 * c + lane] = fb[j];
+                    }
+                    __syncwarp();
+                } else {
+                    block_factors4(fb, p.sb, p.gb, nf, kb0, KB, vec_b != 0);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) fa[j] = __fmul_rn(fa[j], fb[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (kb0 + j >= KB) break;
+                    ok = (lane == 0) ? ptx::mbar_wait(&tfull[buf], buf_phase, abort_flag) : false;
+                    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+                    if (!ok) break;
+                    __syncwarp();
+                    ptx::tc_fence_after();
+                    const uint32_t ta = tmem_base + lanes + buf * TN + h * CW;
+                    // The warp's 64 columns as two 32-column loads, one at a
+                    // time (the accumulator takes most of the registers); the
+                    // buffer goes back once the last has landed.  Measured:
+                    // overlapping the second half's loads with the first
+                    // half's promotion (16-column loads) spilled or ran 4-46%
+                    // slower.  COLSCALE, whose factor products need more
+                    // registers, loads 16 columns at a time (3% faster).
+                    if constexpr (COLSCALE) {
+                        const float faj = rf[j * 32 + lane];
+                        const float* cfj = cf + j * CW;
+                        uint32_t r[16];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            ptx::tmem_ld_32x32b_x16(ta + 16 * c, r);
+                            ptx::tmem_wait_ld();
+                            if (c == 3) {
+                                ptx::tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0)
+                                    ptx::mbar_arrive_cluster_relaxed(ptx::cluster_addr(&tempty[buf], 0));
+                            }
+                            promote_columns<16>(acc + 8 * c, r, faj, cfj + 16 * c);
+                        }
+                    } else {
+                        const uint64_t ff = pack2(fa[j], fa[j]);
+                        uint32_t r[32];
+                        ptx::tmem_ld_32x32b_x32(ta, r);
+                        ptx::tmem_wait_ld();
+                        promote_uniform<32>(acc, r, ff);
+                        ptx::tmem_ld_32x32b_x32(ta + 32, r);
+                        ptx::tmem_wait_ld();
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            ptx::mbar_arrive_cluster_relaxed(ptx::cluster_addr(&tempty[buf], 0));
+                        promote_uniform<32>(acc + 16, r, ff);
+                    }
+                    if (++buf == NBUF) { buf = 0; buf_phase ^= 1u; }
+                }
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int c = 0; c < NCH; ++c)
+                if (n0 < p.N) emit_block_chunk(slot, acc + 16 * c, m0, n0 + 32 * c, p, &tmD);
+        }
+        if (lane == 0) ptx::bulk_wait_group_all();   // every TMA store has completed
+        __syncwarp();
+    }
+
+    ptx::tc_fence_before();
+    ptx::cluster_sync();   // the pair's MMAs, copies and remote arrivals are all done
+    if (warp == 2) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    }
+    if (threadIdx.x == 0 && *abort_flag) atomicOr(&g_device_status, 1u);
+}
+
+// ------------------------------------------ block-scaled products of experts, fp32 factors
+
 // 32 columns of this thread's row m0 + lane, if the expert has it: what a box
 // that ends within another expert's rows is written by.
 __device__ __forceinline__ void store_part_row(const float (&v)[32], int64_t m0, int64_t n0, int m_end,
@@ -996,59 +1280,13 @@ __device__ __forceinline__ void store_part_row(const float (&v)[32], int64_t m0,
     }
 }
 
-// Round one promoted 32-column chunk (16 packed pairs) plus the bias (if
-// any) and write it through the warp's staging slot: one bf16 box of 32
-// columns, or two FP32 boxes of 16 columns (added to D when accumulating).
-// Whole-warp call; m0 is the warp's first row, n0 the chunk's first column.
+// Experts' factors on their way: sets of four K blocks, of the CTA's 128 rows
+// and of the tile's columns (kByTokens: 256, each its own) or 128-column blocks.
+constexpr int kFactorSets = 3;
 template <int MODE>
-__device__ __forceinline__ void emit_block_chunk(uint8_t* slot, const uint64_t* acc, const BlockTile& t,
-                                                 int64_t m0, int64_t n0, const GemmParams& p,
-                                                 const CUtensorMap* map) {
-    const bool in_range = m0 < t.m_end;
-    float v[32];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        v[2 * e] = __uint_as_float(static_cast<uint32_t>(acc[e]));
-        v[2 * e + 1] = __uint_as_float(static_cast<uint32_t>(acc[e] >> 32));
-    }
-    if (MODE == kDense && p.bias) {
-#pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-            float b[8];
-            load_bias8(b, p.bias, n0 + j);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[j + e] = __fadd_rn(v[j + e], b[e]);
-        }
-    }
-    if (MODE == kByRows && m0 + 32 > t.m_end) {   // the box would reach into another expert's rows
-        store_part_row(v, m0, n0, t.m_end, p);
-        return;
-    }
-    if (p.out == FP8_OUT_BF16) {
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-            w[e] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        const uint4 piece[4] = {make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]),
-                                make_uint4(w[8], w[9], w[10], w[11]),
-                                make_uint4(w[12], w[13], w[14], w[15])};
-        emit_box(slot, piece, map, n0, m0, in_range, false);
-    } else {
-#pragma unroll
-        for (int hb = 0; hb < 2; ++hb) {
-            uint4 piece[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                piece[j] = make_uint4(__float_as_uint(v[16 * hb + 4 * j]),
-                                      __float_as_uint(v[16 * hb + 4 * j + 1]),
-                                      __float_as_uint(v[16 * hb + 4 * j + 2]),
-                                      __float_as_uint(v[16 * hb + 4 * j + 3]));
-            emit_box(slot, piece, map, n0 + 16 * hb, m0, in_range, p.accumulate != 0);
-        }
-    }
-}
+constexpr int kFactorCols = MODE == kByTokens ? 256 : 2;
+template <int MODE>
+constexpr int kFactorSetBytes = (128 + kFactorCols<MODE>) * 16;
 
 // ---- promotion where tokens are the reduction (kByTokens)
 //
@@ -1228,39 +1466,166 @@ __device__ __forceinline__ void promote_tokens(uint8_t* slots, uint32_t cols, ui
     }
 }
 
-template <typename Cfg, bool COLSCALE, int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
-    gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA,
-                           const __grid_constant__ CUtensorMap tmB,
-                           const __grid_constant__ CUtensorMap tmD,
-                           const __grid_constant__ GemmParams p, int vec_a, int vec_b) {
+// One product or weight gradient per expert, with fp32 factors: 256 x 256 tiles,
+// pair MMAs and two TMEM buffers as in gemm_block_pair_kernel, and a warp for the
+// factors.
+//   warp 0      TMA producer; warp 1 MMA issuer (even CTA); warp 2 TMEM;
+//   warp 3      factors; warps 4-19 promotion, 32 rows x 64 columns each.
+// What bounds it is the way of a buffer: MMA issue, completion (some 1000 cycles
+// for four MMAs that take 512), promotion (700) and the arrivals back (330) are
+// 2200 cycles for two K blocks in flight, and TMEM holds no third 256-column
+// buffer: products of 32 experts of 4096 x 4096 over 32768 rows take 570 us, 538
+// without promotion and with a quarter of the MMAs.  So the issue itself counts: by
+// rows, the whole warp runs the issue loop, so that the operands' descriptors
+// are uniform, and an elected lane issues (570 against 584 us with one lane); by
+// tokens, whose promotion is longer, one lane leaves the schedulers more (876
+// against 935).  Tried besides: each CTA its own MMAs, B by multicast (589: no
+// remote arrivals, but 48 KB a K block instead of 32 into each SM); one arrival a CTA
+// through warp 2 (608); test_wait for try_wait (level).
+// Stages: by rows four (564 us, 568 with three); by tokens three (876 against 892: shared
+// memory comes out of L1, where the factors' lines are).
+struct ExpertCfg {
+    static constexpr int TN = 256, EPI = 16, NBUF = 2, CW = 64, BOXES = 2;
+    static constexpr int THREADS = (4 + EPI) * 32;
+    static constexpr int A_BYTES = 128 * BK, STAGE_BYTES = 2 * A_BYTES;   // a CTA's half of A's rows and of B's
+    // registers of the role warps and of the promotion warps, as in BpWide
+    static constexpr int RROLE = 32, RPROMO = 112;
+    static constexpr int BAR_BYTES = 256;
+    static_assert(4 * 32 * RROLE + EPI * 32 * RPROMO <= THREADS * (65536 / THREADS / 8 * 8),
+                  "the register split fits the launch's registers");
+};
+template <int MODE>
+constexpr int kExpertStages = MODE == kByRows ? 4 : 3;
+template <int MODE>
+constexpr int kExpertSmem = kExpertStages<MODE> * ExpertCfg::STAGE_BYTES + ExpertCfg::EPI * ExpertCfg::BOXES * 2048 +
+                            kFactorSets * kFactorSetBytes<MODE> + ExpertCfg::BAR_BYTES +
+                            static_cast<int>(sizeof(Units)) + 1024;
+static_assert(kExpertSmem<kByRows> <= 227 * 1024 && kExpertSmem<kByTokens> <= 227 * 1024, "shared memory");
+
+// 32 promoted columns (16 packed pairs) of a warp's 32 rows: one bf16 box, or two
+// FP32 boxes of 16 columns, through the warp's two slots in turn; rows that end
+// among another expert's are stored by their threads.
+__device__ __forceinline__ void emit_expert_chunk(uint8_t* slots, uint32_t& turn, const uint64_t* acc, const BlockTile& t,
+                                                  int64_t m0, int64_t n0, const GemmParams& p, const CUtensorMap* map) {
+    const int lane = threadIdx.x & 31, swz = (lane >> 1) & 3;
+    float v[32];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        v[2 * e] = __uint_as_float(static_cast<uint32_t>(acc[e]));
+        v[2 * e + 1] = __uint_as_float(static_cast<uint32_t>(acc[e] >> 32));
+    }
+    if (m0 + 32 > t.m_end) {   // the box would reach into another expert's rows
+        store_part_row(v, m0, n0, t.m_end, p);
+        return;
+    }
+    const bool f32 = p.out == FP8_OUT_F32;
+#pragma unroll
+    for (int hb = 0; hb < 2; ++hb) {
+        if (hb && !f32) break;
+        uint8_t* slot = slots + turn * 2048;
+        turn ^= 1u;
+        if (lane == 0) ptx::bulk_wait_group_read<1>();   // the slot's last box has been read
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float* w = v + 16 * hb + 4 * j;
+            const uint4 piece =
+                f32 ? make_uint4(__float_as_uint(w[0]), __float_as_uint(w[1]), __float_as_uint(w[2]), __float_as_uint(w[3]))
+                    : make_uint4(row::pack_bf16(v[8 * j], v[8 * j + 1]), row::pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                                 row::pack_bf16(v[8 * j + 4], v[8 * j + 5]), row::pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+            *reinterpret_cast<uint4*>(slot + lane * 64 + 16 * (j ^ swz)) = piece;
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            ptx::tma_store_2d(map, ptx::smem_u32(slot), static_cast<int32_t>(n0 + 16 * hb), static_cast<int32_t>(m0));
+            ptx::bulk_commit_group();
+        }
+    }
+}
+
+// The promotion warp of rows m_off .. + 31 and columns n_off .. + 63 where a
+// column's factor is its 128-column block's: one factor a row and K block.
+template <int NBUF, int TN>
+__device__ __forceinline__ void promote_rows(uint8_t* slots, uint32_t col, uint32_t rows, uint64_t* ffull, uint64_t* fempty,
+                                             uint64_t* tfull, uint64_t* tempty, volatile uint32_t* abort_flag,
+                                             const Units* units, const GemmParams& p, const CUtensorMap* map, uint32_t tmem,
+                                             int m_off, int n_off, int pair, int npairs, int num_units) {
+    const int lane = threadIdx.x & 31;
+    uint32_t buf = 0, buf_phase = 0, set = 0, set_phase = 0, turn = 0;
+    for (int u = pair; u < num_units; u += npairs) {
+        uint64_t acc[32];   // 64 columns of this thread's row, as packed pairs
+#pragma unroll
+        for (int e = 0; e < 32; ++e) acc[e] = 0ull;
+        for (int base = 0; base < p.num_kb; base += 4) {
+            bool ok = ptx::mbar_wait(&ffull[set], set_phase, abort_flag);   // every lane: the copies are others'
+            if (!__all_sync(0xFFFFFFFFu, ok)) return;
+            float f[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                f[j] = __fmul_rn(ld_shared(rows + set * kFactorSetBytes<kByRows> + 4 * j),
+                                 ld_shared(col + set * kFactorSetBytes<kByRows> + 4 * j));
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&fempty[set]);
+            if (++set == kFactorSets) { set = 0; set_phase ^= 1u; }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (base + j >= p.num_kb) break;
+                ok = lane == 0 ? ptx::mbar_wait(&tfull[buf], buf_phase, abort_flag) : false;
+                ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+                if (!ok) return;
+                __syncwarp();
+                ptx::tc_fence_after();
+                const uint32_t ta = tmem + buf * TN;
+                const uint64_t ff = pack2(f[j], f[j]);
+                uint32_t r[32];
+                ptx::tmem_ld_32x32b_x32(ta, r);
+                ptx::tmem_wait_ld();
+                promote_uniform<32>(acc, r, ff);
+                ptx::tmem_ld_32x32b_x32(ta + 32, r);
+                ptx::tmem_wait_ld();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::cluster_addr(&tempty[buf], 0));
+                promote_uniform<32>(acc + 16, r, ff);
+                if (++buf == NBUF) { buf = 0; buf_phase ^= 1u; }
+            }
+        }
+        const BlockTile t = block_tile<kByRows>(u, units, p, TN);
+        const int64_t m0 = static_cast<int64_t>(t.ya) + m_off, n0 = static_cast<int64_t>(t.n0) + n_off;
+        if (m0 >= t.m_end || n0 >= p.N) continue;   // uniform over the warp
+        emit_expert_chunk(slots, turn, acc, t, m0, n0, p, map);
+        emit_expert_chunk(slots, turn, acc + 16, t, m0, n0 + 32, p, map);
+    }
+}
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ExpertCfg::THREADS, 1)
+    gemm_block_experts_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                              const __grid_constant__ CUtensorMap tmD, const __grid_constant__ GemmParams p, int vec_a,
+                              int vec_b) {
+    using C = ExpertCfg;
+    constexpr int STAGES = kExpertStages<MODE>, NBUF = C::NBUF, EPI = C::EPI, TN = C::TN;
     ptx::griddep_launch_dependents();   // the next kernel may launch now
-    constexpr int STAGES = Cfg::STAGES, NBUF = Cfg::NBUF, EPI = Cfg::EPI;
-    constexpr int A_BYTES = Cfg::A_BYTES;
-    constexpr int STAGE_BYTES = Cfg::STAGE_BYTES;
-    constexpr int TN = Cfg::TN;
-    constexpr uint32_t TMEM_COLS = 512;   // allocations are powers of two
-    static_assert(NBUF * TN <= 512, "the partial-sum buffers fit in TMEM");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint8_t* epi_stage = ring + STAGES * STAGE_BYTES;   // output boxes: 2 KB per epilogue warp
-    constexpr int BOXES = Cfg::template BOXES<MODE>, FACTORS = Cfg::template FACTORS<COLSCALE, MODE>;
-    float* colf = reinterpret_cast<float*>(epi_stage + EPI * BOXES * 2048);   // [warp][FACTORS]
-    uint64_t* full = reinterpret_cast<uint64_t*>(colf + EPI * FACTORS);
+    uint8_t* boxes = ring + STAGES * C::STAGE_BYTES;
+    uint8_t* sets = boxes + EPI * C::BOXES * 2048;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sets + kFactorSets * kFactorSetBytes<MODE>);
     uint64_t* empty = full + STAGES;
     uint64_t* tfull = empty + STAGES;
     uint64_t* tempty = tfull + NBUF;
-    uint64_t* done = tempty + NBUF;
-    uint64_t* ffull = done + 1;   // experts' factor sets
+    uint64_t* ffull = tempty + NBUF;
     uint64_t* fempty = ffull + kFactorSets;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fempty + kFactorSets);
+    uint64_t* done = fempty + kFactorSets;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile uint32_t* abort_flag = tmem_slot + 1;
-    static_assert((2 * STAGES + 2 * NBUF + 1 + 2 * kFactorSets) * 8 + 8 <= 256, "the barriers' place");
-    Units* units = reinterpret_cast<Units*>(reinterpret_cast<uint8_t*>(full) + 256);   // experts' rows
+    static_assert((2 * STAGES + 2 * NBUF + 2 * kFactorSets + 1) * 8 + 8 <= C::BAR_BYTES, "the barriers' place");
+    Units* units = reinterpret_cast<Units*>(reinterpret_cast<uint8_t*>(full) + C::BAR_BYTES);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = ptx::cluster_ctarank();
+    const int rank = static_cast<int>(ptx::cluster_ctarank());
     const bool leader = rank == 0;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -1271,53 +1636,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             ptx::mbar_init(&tfull[b], 1);
             ptx::mbar_init(&tempty[b], 2 * EPI);   // promotion warps of both CTAs
         }
-        if (MODE != kDense) {
-            for (int b = 0; b < kFactorSets; ++b) {
-                ptx::mbar_init(&ffull[b], 32);     // the factor warp's lanes
-                ptx::mbar_init(&fempty[b], EPI);
-            }
+        for (int b = 0; b < kFactorSets; ++b) {
+            ptx::mbar_init(&ffull[b], 32);   // the factor warp's lanes
+            ptx::mbar_init(&fempty[b], EPI);
         }
         ptx::mbar_init(done, 1);
         *abort_flag = 0;
         ptx::fence_barrier_init();
-    }
-    if (warp == 0 && lane == 0) {
         ptx::tma_prefetch_desc(&tmA);
         ptx::tma_prefetch_desc(&tmB);
         ptx::tma_prefetch_desc(&tmD);
     }
     if (warp == 2) {
-        ptx::tmem_alloc_pair(tmem_slot, TMEM_COLS);
+        ptx::tmem_alloc_pair(tmem_slot, 512);
         ptx::tmem_relinquish_pair();
     }
+    ptx::griddep_wait();   // the previous kernel's results (operands, factors) are visible
+    make_block_units<MODE>(units, p);
     ptx::tc_fence_before();
     ptx::cluster_sync();   // the peer's barriers exist before any remote arrival
     ptx::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    ptx::griddep_wait();   // the previous kernel's results (operands, factors) are visible
-    make_block_units<MODE>(units, p);
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     const int num_units = block_units<MODE>(units, p);
-    const int KB = p.num_kb;
 
     if (warp < 4) {
-    ptx::setmaxnreg_dec<Cfg::RROLE>();   // the whole role warpgroup
-    if (warp == 0) {
-        if (lane == 0) {
+        ptx::setmaxnreg_dec<C::RROLE>();   // the whole role warpgroup
+        if (warp == 0 && lane == 0) {
             uint32_t stage = 0, phase = 0;
             int64_t issued = 0;
             bool ok = true;
             for (int u = pair; ok && u < num_units; u += npairs) {
                 const BlockTile t = block_tile<MODE>(u, units, p, TN);
-                const int ya = t.ya + static_cast<int>(rank) * 128;
-                const int yb = t.yb + static_cast<int>(rank) * (TN / 2);
                 for (int kb = t.kb0; kb < t.kb1; ++kb) {
                     if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
-                    uint8_t* sa = ring + stage * STAGE_BYTES;
+                    uint8_t* sa = ring + stage * C::STAGE_BYTES;
                     const uint32_t bar = ptx::cluster_addr(&full[stage], 0);
-                    if (leader) ptx::mbar_arrive_expect_tx(&full[stage], 2 * STAGE_BYTES);
-                    ptx::tma_load_2d_pair(sa, &tmA, bar, kb * BK, ya);
-                    ptx::tma_load_2d_pair(sa + A_BYTES, &tmB, bar, kb * BK, yb);
+                    if (leader) ptx::mbar_arrive_expect_tx(&full[stage], 2 * C::STAGE_BYTES);
+                    ptx::tma_load_2d_pair(sa, &tmA, bar, kb * BK, t.ya + rank * 128);
+                    ptx::tma_load_2d_pair(sa + C::A_BYTES, &tmB, bar, kb * BK, t.yb + rank * 128);
                     ++issued;
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
@@ -1327,189 +1684,83 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                 // drain: the last copies into each slot (both CTAs' bytes) have landed
                 for (int s = 0; s < STAGES; ++s) {
                     if (issued <= s && issued < STAGES) break;
-                    const uint32_t par = (static_cast<uint32_t>(s) < stage) ? phase : (phase ^ 1u);
-                    ptx::mbar_wait(&full[s], par, &never);
+                    ptx::mbar_wait(&full[s], static_cast<uint32_t>(s) < stage ? phase : phase ^ 1u, &never);
                 }
             } else if (!ok) {
                 // copies signal the peer's barriers: after an abort, give those in
-                // flight a bounded grace period to land before this CTA moves on
+                // flight a bounded time to land before this CTA moves on
                 const uint64_t t0 = ptx::globaltimer();
                 while (ptx::globaltimer() - t0 < 1000000ull) {
                 }
             }
-        }
-    } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        } else if (warp == 1 && leader && (MODE == kByRows || lane == 0)) {
+            constexpr bool WARP = MODE == kByRows;   // the whole warp is here
             const uint32_t idesc = ptx::idesc_f8f6f4(p.fa, p.fb, 256, TN);
+            const uint64_t tmpl = ptx::sdesc_kmajor_sw128(0);
+            const bool one = WARP ? ptx::elect_one() : true;
+            uint32_t ring_at = ptx::smem_u32(ring), tbase = tmem_base;
+            if (WARP) {   // known to be uniform
+                ring_at = __shfl_sync(0xFFFFFFFFu, ring_at, 0);
+                tbase = __shfl_sync(0xFFFFFFFFu, tbase, 0);
+            }
             uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
             bool ok = true;
             for (int u = pair; ok && u < num_units; u += npairs) {
                 const BlockTile t = block_tile<MODE>(u, units, p, TN);
                 for (int kb = t.kb0; kb < t.kb1; ++kb) {
-                    if (!ptx::mbar_wait(&tempty[buf], buf_phase ^ 1u, abort_flag)) { ok = false; break; }
-                    if (!ptx::mbar_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
+                    const uint32_t sa = ring_at + stage * C::STAGE_BYTES;
+                    const uint64_t ad = tmpl | ((sa & 0x3FFFFu) >> 4), bd = tmpl | (((sa + C::A_BYTES) & 0x3FFFFu) >> 4);
+                    const uint32_t d = tbase + buf * TN;
+                    ok = ptx::mbar_wait(&full[stage], phase, abort_flag) &&
+                         ptx::mbar_wait(&tempty[buf], buf_phase ^ 1u, abort_flag);
+                    if (WARP) ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
                     ptx::tc_fence_after();
-                    uint8_t* sa = ring + stage * STAGE_BYTES;
-                    const uint64_t ad = ptx::sdesc_kmajor_sw128(ptx::smem_u32(sa));
-                    const uint64_t bd = ptx::sdesc_kmajor_sw128(ptx::smem_u32(sa + A_BYTES));
-                    const uint32_t d = tmem_base + buf * TN;
+                    if (one) {
 #pragma unroll
-                    for (int k = 0; k < BK / UMMA_K; ++k)
-                        ptx::mma_f8f6f4_pair(d, ad + (k * UMMA_K >> 4), bd + (k * UMMA_K >> 4),
-                                             idesc, k != 0);
-                    ptx::mma_commit_pair(&empty[stage], 0x3);
-                    ptx::mma_commit_pair(&tfull[buf], 0x3);
+                        for (int k = 0; k < BK / UMMA_K; ++k)
+                            ptx::mma_f8f6f4_pair(d, ad + (k * UMMA_K >> 4), bd + (k * UMMA_K >> 4), idesc, k != 0);
+                        ptx::mma_commit_pair(&tfull[buf], 0x3);
+                        ptx::mma_commit_pair(&empty[stage], 0x3);
+                    }
+                    if (WARP) __syncwarp();
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                     if (++buf == NBUF) { buf = 0; buf_phase ^= 1u; }
                 }
             }
-            uint32_t never = 0;
-            ptx::mma_commit_pair(done, 0x1);
-            ptx::mbar_wait(done, 0, &never);
-        }
-    } else if (MODE != kDense && warp == 3) {
-        load_factors<MODE, TN>(ptx::smem_u32(colf), ffull, fempty, abort_flag, units, p, rank, pair, npairs, num_units,
-                         vec_a != 0, vec_b != 0);
-    }
-    } else {
-        ptx::setmaxnreg_inc<Cfg::RPROMO>();   // each promotion warpgroup
-        constexpr int CW = Cfg::CW;              // columns of this warp
-        constexpr int NCH = CW / 32;             // 32-column chunks (COLSCALE factors, stores)
-        const int qd = warp & 3;                 // TMEM lane quarter of this warp
-        const int h = (warp - 4) >> 2;           // which CW-column slice of the tile
-        uint8_t* slot = epi_stage + (warp - 4) * 2048;
-        // COLSCALE: the columns' factors [4 K blocks][CW], then the rows'
-        // [4 K blocks][32 lanes]
-        float* cf = colf + (warp - 4) * 4 * (CW + 32);
-        float* rf = cf + 4 * CW;
-        const uint32_t lanes = static_cast<uint32_t>(qd * 32) << 16;
-        uint32_t buf = 0, buf_phase = 0, fset = 0, fset_phase = 0;
-        bool ok = true;
-        if constexpr (MODE == kByTokens) {
-            static_assert(COLSCALE && CW == 64 && TN == 256, "the token path's fragments and factor sets");
-            slot = epi_stage + (warp - 4) * BOXES * 2048;
-            const uint32_t sets = ptx::smem_u32(colf);
-            promote_tokens<NBUF, TN>(slot, sets + (128 + h * CW + (lane & 3)) * 16, sets + (qd * 32 + (lane >> 2)) * 16,
-                                     ffull, fempty, tfull, tempty, abort_flag, units, p, &tmD,
-                                     tmem_base + lanes + h * CW, rank * 128 + qd * 32, h * CW, pair, npairs, num_units);
-        } else
-        for (int u = pair; ok && u < num_units; u += npairs) {
-            const BlockTile t = block_tile<MODE>(u, units, p, TN);
-            const int64_t m0 = static_cast<int64_t>(t.ya) + rank * 128 + qd * 32;
-            const int64_t m = m0 + lane;
-            const int64_t m_safe = m < p.M ? m : p.M - 1;
-            const int64_t n0 = static_cast<int64_t>(t.n0) + h * CW;
-            // a warp's columns lie all inside or all outside [0, N) (N is a
-            // multiple of 128, CW divides 128); outside, its factors are
-            // read at column N - 1 and its columns are not stored
-            const int64_t nf = t.b_row + (n0 < p.N ? n0 : p.N - 1);
-            // FP32 accumulator of CW columns, as packed pairs
-            uint64_t acc[CW / 2];
-#pragma unroll
-            for (int e = 0; e < CW / 2; ++e) acc[e] = 0ull;
-            for (int kb0 = 0; ok && kb0 < t.kb1; kb0 += 4) {
-                // The factors of four K blocks, read at the start of the group
-                // (they hit L1; holding the next group's in registers made the
-                // loop spill): A per row; B per 128-column block, multiplied
-                // into fa here, or (COLSCALE) per column, staged in shared
-                // memory for broadcast reads (lane l writes columns n0+32c+l),
-                // with the rows' factors beside them (registers are short).
-                float fa[4], fb[4];
-                if constexpr (MODE == kByRows) {
-                    ok = ptx::mbar_wait(&ffull[fset], fset_phase, abort_flag);   // every lane: the copies are others'
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                    if (!ok) break;
-                    const uint8_t* set = reinterpret_cast<const uint8_t*>(colf) + fset * kFactorSetBytes<MODE>;
-                    const float4 a = *reinterpret_cast<const float4*>(set + (qd * 32 + lane) * 16);
-                    const float4 b = *reinterpret_cast<const float4*>(set + (128 + (h >> 1)) * 16);
-                    fa[0] = a.x; fa[1] = a.y; fa[2] = a.z; fa[3] = a.w;
-                    fb[0] = b.x; fb[1] = b.y; fb[2] = b.z; fb[3] = b.w;
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&fempty[fset]);
-                    if (++fset == kFactorSets) { fset = 0; fset_phase ^= 1u; }
-                } else {
-                    block_factors4(fa, p.sa, p.ga, m_safe, kb0, KB, vec_a != 0);
-                }
-                if (COLSCALE) {
-                    __syncwarp();   // the previous group's factors have been read
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) rf[j * 32 + lane] = fa[j];
-#pragma unroll
-                    for (int c = 0; c < NCH; ++c) {
-                        block_factors4(fb, p.sb, p.gb, nf + (n0 < p.N ? 32 * c + lane : 0), kb0, KB,
-                                       vec_b != 0);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) cf[j * CW + 32 * c + lane] = fb[j];
-                    }
-                    __syncwarp();
-                } else {
-                    if (MODE == kDense) block_factors4(fb, p.sb, p.gb, nf, kb0, KB, vec_b != 0);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) fa[j] = __fmul_rn(fa[j], fb[j]);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (kb0 + j >= t.kb1) break;
-                    ok = (lane == 0) ? ptx::mbar_wait(&tfull[buf], buf_phase, abort_flag) : false;
-                    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-                    if (!ok) break;
-                    __syncwarp();
-                    ptx::tc_fence_after();
-                    const uint32_t ta = tmem_base + lanes + buf * TN + h * CW;
-                    // The warp's 64 columns as two 32-column loads, one at a
-                    // time (the accumulator takes most of the registers); the
-                    // buffer goes back once the last has landed.  Measured:
-                    // overlapping the second half's loads with the first
-                    // half's promotion (16-column loads) spilled or ran 4-46%
-                    // slower.  COLSCALE, whose factor products need more
-                    // registers, loads 16 columns at a time (3% faster).
-                    if constexpr (COLSCALE) {
-                        const float faj = rf[j * 32 + lane];
-                        const float* cfj = cf + j * CW;
-                        uint32_t r[16];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            ptx::tmem_ld_32x32b_x16(ta + 16 * c, r);
-                            ptx::tmem_wait_ld();
-                            if (c == 3) {
-                                ptx::tc_fence_before();
-                                __syncwarp();
-                                if (lane == 0)
-                                    ptx::mbar_arrive_cluster_relaxed(ptx::cluster_addr(&tempty[buf], 0));
-                            }
-                            promote_columns<16>(acc + 8 * c, r, faj, cfj + 16 * c);
-                        }
-                    } else {
-                        const uint64_t ff = pack2(fa[j], fa[j]);
-                        uint32_t r[32];
-                        ptx::tmem_ld_32x32b_x32(ta, r);
-                        ptx::tmem_wait_ld();
-                        promote_uniform<32>(acc, r, ff);
-                        ptx::tmem_ld_32x32b_x32(ta + 32, r);
-                        ptx::tmem_wait_ld();
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            ptx::mbar_arrive_cluster_relaxed(ptx::cluster_addr(&tempty[buf], 0));
-                        promote_uniform<32>(acc + 16, r, ff);
-                    }
-                    if (++buf == NBUF) { buf = 0; buf_phase ^= 1u; }
-                }
+            if (one) {
+                uint32_t never = 0;
+                ptx::mma_commit_pair(done, 0x1);
+                ptx::mbar_wait(done, 0, &never);
             }
-            if (!ok) break;
-#pragma unroll
-            for (int c = 0; c < NCH; ++c)
-                if (n0 < p.N) emit_block_chunk<MODE>(slot, acc + 16 * c, t, m0, n0 + 32 * c, p, &tmD);
+            if (WARP) __syncwarp();
+        } else if (warp == 3) {
+            load_factors<MODE, TN>(ptx::smem_u32(sets), ffull, fempty, abort_flag, units, p, rank, pair, npairs, num_units,
+                                   vec_a != 0, vec_b != 0);
         }
+    } else {
+        ptx::setmaxnreg_inc<C::RPROMO>();   // each promotion warpgroup
+        const int qd = warp & 3, h = (warp - 4) >> 2;   // TMEM lanes, 64-column slice
+        uint8_t* slots = boxes + (warp - 4) * C::BOXES * 2048;
+        const uint32_t factors = ptx::smem_u32(sets);
+        const uint32_t tmem = tmem_base + (static_cast<uint32_t>(qd * 32) << 16) + h * C::CW;
+        const int m_off = rank * 128 + qd * 32, n_off = h * C::CW;
+        if constexpr (MODE == kByTokens)
+            promote_tokens<NBUF, TN>(slots, factors + (128 + n_off + (lane & 3)) * 16, factors + (qd * 32 + (lane >> 2)) * 16,
+                                     ffull, fempty, tfull, tempty, abort_flag, units, p, &tmD, tmem, m_off, n_off, pair,
+                                     npairs, num_units);
+        else
+            promote_rows<NBUF, TN>(slots, factors + (128 + (h >> 1)) * 16, factors + (qd * 32 + lane) * 16, ffull, fempty,
+                                   tfull, tempty, abort_flag, units, p, &tmD, tmem, m_off, n_off, pair, npairs, num_units);
         if (lane == 0) ptx::bulk_wait_group_all();   // every TMA store has completed
         __syncwarp();
     }
 
     ptx::tc_fence_before();
-    ptx::cluster_sync();   // the pair's MMAs, copies and remote arrivals are all done
+    ptx::cluster_sync();   // both CTAs' MMAs, copies and arrivals are done
     if (warp == 2) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc_pair(tmem_base, TMEM_COLS);
+        ptx::tmem_dealloc_pair(tmem_base, 512);
     }
     if (threadIdx.x == 0 && *abort_flag) atomicOr(&g_device_status, 1u);
 }
@@ -1697,7 +1948,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
                 const int ya = t.ya + static_cast<int>(rank) * HALF;
                 const int yb = t.yb + static_cast<int>(rank) * HALF;
                 for (int kb = t.kb0; kb < t.kb1; ++kb) {
-                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
+                    if (!ptx::mbar_wait<true>(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
                     uint8_t* sa = ring + stage * STAGE_BYTES;
                     const uint32_t bar = ptx::cluster_addr(&full[stage], 0);
                     if (leader) ptx::mbar_arrive_expect_tx(&full[stage], 2 * STAGE_BYTES);
@@ -1713,7 +1964,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
                 for (int s = 0; s < STAGES; ++s) {
                     if (issued <= s && issued < STAGES) break;
                     const uint32_t par = (static_cast<uint32_t>(s) < stage) ? phase : (phase ^ 1u);
-                    ptx::mbar_wait(&full[s], par, &never);
+                    ptx::mbar_wait<true>(&full[s], par, &never);
                 }
             } else if (!ok) {
                 // copies signal the peer's barriers: after an abort, give those in
@@ -1732,14 +1983,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
             for (int u = pair; ok && u < num_units; u += npairs) {
                 const BlockTile t = block_tile<MODE>(u, units, p, TILE);
                 if (MODE == kByTokens && t.kb0 == t.kb1) continue;   // nothing to multiply
-                if (!ptx::mbar_wait(tempty, acc_phase ^ 1u, abort_flag)) break;
+                if (!ptx::mbar_wait<true>(tempty, acc_phase ^ 1u, abort_flag)) break;
                 ptx::tc_fence_after();
                 // K blocks from a multiple of four: a factor word's four share one
                 const int base = MODE == kByTokens ? t.kb0 & ~3 : 0, last = t.kb1 - base;
                 for (int kb = t.kb0 - base; kb < last; ++kb) {
-                    if (!ptx::mbar_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
+                    if (!ptx::mbar_wait<true>(&full[stage], phase, abort_flag)) { ok = false; break; }
                     if (((kb % KPS) == 0 || (MODE == kByTokens && kb == t.kb0 - base)) &&
-                        !ptx::mbar_wait(&sf_full[sfs], sf_phase, abort_flag)) { ok = false; break; }
+                        !ptx::mbar_wait<true>(&sf_full[sfs], sf_phase, abort_flag)) { ok = false; break; }
                     ptx::tc_fence_after();
                     uint8_t* sa = ring + stage * STAGE_BYTES;
                     const uint64_t ad = ptx::sdesc_kmajor_sw128(ptx::smem_u32(sa));
@@ -1767,7 +2018,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
             }
             uint32_t never = 0;
             ptx::mma_commit_pair(done, 0x1);
-            ptx::mbar_wait(done, 0, &never);
+            ptx::mbar_wait<true>(done, 0, &never);
         }
     } else if (warp >= 4 && warp < 8) {
         // factor writers: warp 4 + q owns TMEM lanes 32q .. 32q+31.  Loads use
@@ -1824,7 +2075,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
                     for (int w = 0; w < 4; ++w)
 #pragma unroll
                         for (int c = 0; c < 8; ++c) wb[8 * w + c] = stb[w * 264 + 32 * c + lane];
-                    bool ok = (lane == 0) ? ptx::mbar_wait(&sf_empty[sfs], sf_phase ^ 1u, abort_flag)
+                    bool ok = (lane == 0) ? ptx::mbar_wait<true>(&sf_empty[sfs], sf_phase ^ 1u, abort_flag)
                                           : false;
                     ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
                     if (ok) {
@@ -1871,7 +2122,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
                     emit_box(stg, piece, &tmD, n0 + 16 * c, y, m0 < t.m_end && n0 + 16 * c < p.N, add);
                 continue;
             }
-            bool ok = (lane == 0) ? ptx::mbar_wait(tfull, acc_phase, abort_flag) : false;
+            bool ok = (lane == 0) ? ptx::mbar_wait<true>(tfull, acc_phase, abort_flag) : false;
             ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
             if (!ok) break;
             __syncwarp();
@@ -2268,21 +2519,26 @@ int launch_mx(const BlockProblem& b, cudaStream_t stream) {
                               cluster_ids[id], stream);
 }
 
-// fp32 factors: the CTA-pair promotion kernel.
-template <bool COLSCALE, int MODE>
+// fp32 factors: the CTA-pair promotion kernel, the experts' on their own.
+template <bool COLSCALE>
 int launch_promote(const BlockProblem& b, cudaStream_t stream) {
     using C = BpWide;
-    constexpr int smem_id = MODE == kDense ? (COLSCALE ? 3 : 1) : MODE == kByRows ? 13 : 14;
-    constexpr int cluster_id = MODE == kDense ? (COLSCALE ? 4 : 3) : MODE == kByRows ? 7 : 8;
-    return launch_block<MODE>(gemm_block_pair_kernel<C, COLSCALE, MODE>, b, C::TN, C::THREADS,
-                              C::template SMEM<COLSCALE, MODE>, smem_id, cluster_id, stream);
+    return launch_block<kDense>(gemm_block_pair_kernel<C, COLSCALE>, b, C::TN, C::THREADS, C::smem(COLSCALE),
+                                COLSCALE ? 3 : 1, COLSCALE ? 4 : 3, stream);
+}
+
+template <int MODE>
+int launch_promote_experts(const BlockProblem& b, cudaStream_t stream) {
+    using C = ExpertCfg;
+    return launch_block<MODE>(gemm_block_experts_kernel<MODE>, b, C::TN, C::THREADS, kExpertSmem<MODE>,
+                              MODE == kByRows ? 13 : 14, MODE == kByRows ? 7 : 8, stream);
 }
 
 // Block-scaled GEMM with fp32 factors (at least one operand with 1x128 or
 // 128x128 scales; K > 0) on the CTA-pair promotion kernel (256 x 256 tiles),
 // with the per-column factor path when B has 1x128 scales.
 int launch_gemm_block(const BlockProblem& b, cudaStream_t stream) {
-    return b.gb == FP8_GRAN_1x128 ? launch_promote<true, kDense>(b, stream) : launch_promote<false, kDense>(b, stream);
+    return b.gb == FP8_GRAN_1x128 ? launch_promote<true>(b, stream) : launch_promote<false>(b, stream);
 }
 
 }  // namespace
@@ -2542,13 +2798,13 @@ unsigned* device_status_word() {
 int launch_gemm_by_rows(const ExpertGemm& g, cudaStream_t stream) {
     const BlockProblem b{g.A, g.fa, g.B, g.fb, g.M, g.N, g.K, FP8_GRAN_1x128, g.sa, FP8_GRAN_128x128, g.sb,
                          nullptr, g.D, g.out, 0, g.offsets, g.experts};
-    return g.pow2 ? launch_mx<kByRows>(b, stream) : launch_promote<false, kByRows>(b, stream);
+    return g.pow2 ? launch_mx<kByRows>(b, stream) : launch_promote_experts<kByRows>(b, stream);
 }
 
 int launch_gemm_by_tokens(const ExpertGemm& g, cudaStream_t stream) {
     const BlockProblem b{g.A, g.fa, g.B, g.fb, g.M, g.N, g.K, FP8_GRAN_1x128, g.sa, FP8_GRAN_1x128, g.sb,
                          nullptr, g.D, FP8_OUT_F32, g.accumulate, g.offsets, g.experts};
-    return g.pow2 ? launch_mx<kByTokens>(b, stream) : launch_promote<true, kByTokens>(b, stream);
+    return g.pow2 ? launch_mx<kByTokens>(b, stream) : launch_promote_experts<kByTokens>(b, stream);
 }
 
 int set_epilogue_wait_ns(uint64_t ns) {
