@@ -10,10 +10,12 @@
 
 Everything between the tensors is a call of this package, on the device: the
 experts' row counts never come to the host in the forward pass.  The backward
-pass runs the same chain back; its weight gradients are one GEMM per expert,
-so it reads the row counts once.
+pass runs the same chain back.  ExpertBlock casts per tensor and per token; its
+weight gradients are one GEMM per expert, so it reads the row counts once.
+BlockScaledExperts casts in blocks of 128, keeps nothing but 8-bit codes of the
+experts' activations for the backward pass, and never reads the row counts.
 
-    python examples/expert_block.py [--tokens 4096] [--experts 16] ...
+    python examples/expert_block.py [--recipe block] [--tokens 4096] [--experts 16] ...
 """
 import argparse
 import math
@@ -128,6 +130,67 @@ class ExpertBlock:
         return out
 
 
+def block_codes(w, pow2):
+    """E4M3 codes of w [E, N, K] in 128x128 blocks with their factors, and transposed."""
+    parts = [F.fp8_quantize_blocks(w[e], F.E4M3, F.GRAN_128x128, pow2=pow2, transpose=True) for e in range(w.shape[0])]
+    return [torch.stack(p) for p in zip(*parts)]
+
+
+class BlockScaledExperts(ExpertBlock):
+    """The same block under the block recipe: weights in 128x128 blocks,
+    activations and gradients in 1x128 blocks.  Of the experts' activations the
+    backward pass gets the codes of the sorted inputs and of the pre-activations."""
+
+    def __init__(self, width, hidden, experts, slots, alpha=1.0, seed=0, device="cuda", pow2=False):
+        super().__init__(width, hidden, experts, slots, alpha, seed, device)
+        self.pow2 = pow2
+        self.in_q, self.in_inv, self.in_qt, self.in_inv_t = block_codes(self.w_in, pow2)
+        self.out_q, self.out_inv, self.out_qt, self.out_inv_t = block_codes(self.w_out, pow2)
+
+    def forward(self, x):
+        p2 = dict(pow2=self.pow2)
+        s = {"x": x}
+        s["pre"] = F.fp8_norm_fwd(x, w_pre=self.w_pre, want_stats=True, want_x_out=False)
+        p = torch.softmax((s["pre"].y @ self.router.t()).float(), dim=1)
+        w, ids = p.topk(self.slots, dim=1)
+        s["w"], s["ids"] = (w / w.sum(1, keepdim=True)).contiguous(), ids.int()
+        # whole blocks of 128 tokens an expert, for the weight gradients
+        rows = -(-F.fp8_moe_rows(x.shape[0], self.slots, self.experts, 128) // 128) * 128
+        s["plan"] = plan = F.fp8_moe_plan(s["ids"], self.experts, align=128, rows=rows)
+        q, inv = F.fp8_quantize_blocks(s["pre"].y, F.E4M3, F.GRAN_1x128, **p2)[:2]
+        s["xs"] = F.fp8_moe_permute(q, plan.row_of, plan.src)[0]
+        s["xs_inv"] = F.fp8_moe_permute(inv, plan.row_of, plan.src)[0]
+        z = F.fp8_gemm_experts(s["xs"], F.E4M3, self.in_q, F.E4M3, s["xs_inv"], self.in_inv, plan.offsets, **p2)
+        s["up"] = F.fp8_act_block(z, F.ACT_SILU, gated=True, keep=True, offsets=plan.offsets, **p2)
+        s["o"] = F.fp8_gemm_experts(s["up"].q, F.E4M3, self.out_q, F.E4M3, s["up"].scale_inv, self.out_inv,
+                                    plan.offsets, **p2)
+        s["b"] = F.fp8_moe_unpermute(s["o"], plan.row_of, weights=s["w"])
+        s["post"] = F.fp8_norm_fwd(x, s["b"], alpha=self.alpha, gate=self.gate, post_norm=True,
+                                   w_post=self.w_post, w_pre=self.w_next, want_stats=True)
+        return s["post"].x_out, s["post"].y, s
+
+    def backward(self, dx_out, dz, s):
+        p2 = dict(pow2=self.pow2)
+        plan, up, g = s["plan"], s["up"], {}
+        n = F.fp8_norm_bwd(dz, s["post"].x_out, s["post"].stats, dx_out=dx_out, h=s["b"],
+                           alpha=self.alpha, gate=self.gate, post_norm=True, w_post=self.w_post,
+                           w_pre=self.w_next)
+        g.update(w_next=n.dw_pre, w_post=n.dw_post, gate=n.dgate)
+        do, g["w"] = F.fp8_moe_unpermute_bwd(n.dh, s["o"], plan.row_of, plan.src, s["w"])
+        do_q, do_inv, do_t, do_inv_t = F.fp8_quantize_blocks(do, F.E5M2, F.GRAN_1x128, transpose=True, **p2)
+        dh = F.fp8_gemm_experts(do_q, F.E5M2, self.out_qt, F.E4M3, do_inv, self.out_inv_t, plan.offsets, **p2)
+        a = F.fp8_act_block_bwd(dh, up.z_q, up.z_scale_inv, F.ACT_SILU, gated=True, want_t=True, want_h_t=True,
+                                offsets=plan.offsets, **p2)
+        g["w_out"] = F.fp8_wgrad_experts(do_t, F.E5M2, a.h_t, F.E4M3, do_inv_t, a.h_scale_inv_t, plan.offsets, **p2)
+        dxs = F.fp8_gemm_experts(a.q, F.E5M2, self.in_qt, F.E4M3, a.scale_inv, self.in_inv_t, plan.offsets, **p2)
+        xs_t, xs_inv_t = F.fp8_block_transpose(s["xs"], F.E4M3, s["xs_inv"], **p2)
+        g["w_in"] = F.fp8_wgrad_experts(a.q_t, F.E5M2, xs_t, F.E4M3, a.scale_inv_t, xs_inv_t, plan.offsets, **p2)
+        dy = F.fp8_moe_unpermute(dxs, plan.row_of)
+        m = F.fp8_norm_bwd(dy, s["x"], s["pre"].stats, dx_out=n.dx, w_pre=self.w_pre)
+        g.update(x=m.dx, w_pre=m.dw_pre)
+        return g
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--tokens", type=int, default=4096)
@@ -135,8 +198,12 @@ def main():
     ap.add_argument("--hidden", type=int, default=2048)
     ap.add_argument("--experts", type=int, default=16)
     ap.add_argument("--slots", type=int, default=2)
+    ap.add_argument("--recipe", choices=["tensor", "block", "block_pow2"], default="tensor")
     a = ap.parse_args()
-    block = ExpertBlock(a.width, a.hidden, a.experts, a.slots)
+    if a.recipe == "tensor":
+        block = ExpertBlock(a.width, a.hidden, a.experts, a.slots)
+    else:
+        block = BlockScaledExperts(a.width, a.hidden, a.experts, a.slots, pow2=a.recipe == "block_pow2")
     x = torch.randn(a.tokens, a.width, device="cuda").to(torch.bfloat16)
     d = (torch.randn(a.tokens, a.width, device="cuda") * 1e-3).to(torch.bfloat16)
 
