@@ -624,7 +624,7 @@ int fp8_moe_unpermute_bwd(const void* dy, const void* ys, int type, const int32_
  * Rows are sorted by expert; offsets [experts + 1] (device memory) are what
  * fp8_moe_plan writes.  Offsets outside 0..M are held to it, and one below its
  * predecessor counts as equal to it.  Rows before offsets[0] and past
- * offsets[experts] are neither read nor written. */
+ * offsets[experts] are neither read nor written.  Outputs overlap no input. */
 
 /* One product per expert: for the rows m of offsets[e] .. offsets[e + 1]
  *   D[m][n] = sum_b sa[m][b] sb[e][n/128][b] sum_{k in block b} A[m][k] B[e][n][k]

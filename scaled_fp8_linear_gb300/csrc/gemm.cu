@@ -306,13 +306,15 @@ __device__ __forceinline__ void prefetch_row(int64_t m, int64_t n0, int width,
 // distinct banks -- and write it to global memory at (x, y) with a TMA bulk
 // store, or, with `add`, a TMA reduce-add (D += box, one FP32 add per element
 // performed by the memory system).  Whole-warp call.  The slot is reused, so
-// the previous box's store must first have read it.  in_range = false skips
-// the store (the box starts past the matrix) but keeps the group count.
+// the previous box's store must first have read it (OTHERS: boxes sent since, from
+// other slots).  in_range = false skips the store (the box starts past the
+// matrix) but keeps the group count.
+template <int OTHERS = 0>
 __device__ __forceinline__ void emit_box(uint8_t* slot, const uint4 (&piece)[4],
                                          const CUtensorMap* map, int64_t x, int64_t y,
                                          bool in_range, bool add) {
     const int lane = threadIdx.x & 31;
-    if (lane == 0) ptx::bulk_wait_group_read<0>();
+    if (lane == 0) ptx::bulk_wait_group_read<OTHERS>();
     __syncwarp();
     uint8_t* row = slot + lane * 64;
     const int swz = (lane >> 1) & 3;
@@ -1814,8 +1816,16 @@ constexpr int kMxThreads = (8 + kMxEpiWarps) * 32;
 constexpr int kMxStageA = 4 * 136;   // words per buffer: [word][128 rows + pad]
 constexpr int kMxStageB = 4 * 264;   //                   [word][256 rows + pad]
 constexpr int kMxEpiStage = 2048;     // bytes of output staging per epilogue warp: one box
-constexpr int kMxSmemBytes = kMxStages * 2 * 128 * BK + kMxEpiWarps * kMxEpiStage +
-                             2 * (kMxStageA + kMxStageB) * 4 + 512 + 1024;
+// Weight gradients of few tokens are all output (8192 tokens over 64 experts of
+// 2048 x 2048: 1 GB): four boxes a warp and four stages; else one and six.
+template <int MODE>
+constexpr int kMxBoxes = MODE == kByTokens ? 4 : 1;
+template <int MODE>
+constexpr int kMxRing = MODE == kByTokens ? 4 : kMxStages;
+template <int MODE>
+constexpr int kMxSmemBytes = kMxRing<MODE> * 2 * 128 * BK + kMxEpiWarps * kMxBoxes<MODE> * kMxEpiStage +
+                             2 * (kMxStageA + kMxStageB) * 4 + 512 + 1024 +
+                             (MODE == kDense ? 0 : static_cast<int>(sizeof(Units)));
 
 // Factors of row r (of an operand with `rows` rows) for the K blocks
 // kb0 .. kb0+3; 1.0 outside the matrix and past the last K block.  vec: the
@@ -1889,7 +1899,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     uint8_t* ring = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* epi_stage = ring + STAGES * STAGE_BYTES;   // [8 warps][2048 B], 1024-aligned
-    uint32_t* stage_a = reinterpret_cast<uint32_t*>(epi_stage + kMxEpiWarps * kMxEpiStage);  // [2][4][136]
+    constexpr int BOXES = kMxBoxes<MODE>;
+    uint32_t* stage_a = reinterpret_cast<uint32_t*>(epi_stage + kMxEpiWarps * BOXES * kMxEpiStage);  // [2][4][136]
     uint32_t* stage_b = stage_a + 2 * kMxStageA;                                  // [2][4][264]
     uint64_t* full = reinterpret_cast<uint64_t*>(stage_b + 2 * kMxStageB);
     uint64_t* empty = full + STAGES;
@@ -2101,7 +2112,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         // (32 bf16 or 16 FP32 columns), staged with the TMA's 64-byte swizzle:
         // 16-byte piece j of row r at piece j ^ ((r >> 1) & 3).
         const int q = warp & 3, h = (warp - 8) >> 2;
-        uint8_t* stg = epi_stage + (warp - 8) * kMxEpiStage;
+        uint8_t* stg = epi_stage + (warp - 8) * BOXES * kMxEpiStage;
+        uint32_t turn = 0;   // by tokens: the box of the two that is next
         const bool f32 = p.out == FP8_OUT_F32;
         const bool add = f32 && p.accumulate;
         float ones[32];   // unit factors: the block scales are applied in the MMA
@@ -2119,7 +2131,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
                 const uint4 piece[4] = {make_uint4(w, w, w, w), make_uint4(w, w, w, w),
                                         make_uint4(w, w, w, w), make_uint4(w, w, w, w)};
                 for (int c = 0; c < 8; ++c)
-                    emit_box(stg, piece, &tmD, n0 + 16 * c, y, m0 < t.m_end && n0 + 16 * c < p.N, add);
+                    emit_box<BOXES - 1>(stg + (turn + c) % BOXES * kMxEpiStage, piece, &tmD, n0 + 16 * c, y,
+                                        m0 < t.m_end && n0 + 16 * c < p.N, add);
                 continue;
             }
             bool ok = (lane == 0) ? ptx::mbar_wait<true>(tfull, acc_phase, abort_flag) : false;
@@ -2188,8 +2201,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
                         if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::cluster_addr(tempty, 0));
                     }
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        emit_f32_chunk(stg, r[i], ones, m0, n0 + (c + i) * 32, p, &tmD, t.m_end, y);
+                    for (int i = 0; i < 2; ++i) {
+                        if constexpr (MODE == kByTokens) {
+#pragma unroll
+                            for (int hb = 0; hb < 2; ++hb) {
+                                uint4 piece[4];
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    piece[j] = make_uint4(r[i][16 * hb + 4 * j], r[i][16 * hb + 4 * j + 1],
+                                                          r[i][16 * hb + 4 * j + 2], r[i][16 * hb + 4 * j + 3]);
+                                const int64_t x = n0 + (c + i) * 32 + 16 * hb;
+                                emit_box<BOXES - 1>(stg + turn * kMxEpiStage, piece, &tmD, x, y,
+                                                    m0 < t.m_end && x < p.N, add);
+                                turn = turn + 1 == BOXES ? 0 : turn + 1;
+                            }
+                        } else {
+                            emit_f32_chunk(stg, r[i], ones, m0, n0 + (c + i) * 32, p, &tmD, t.m_end, y);
+                        }
+                    }
                 }
             }
             acc_phase ^= 1u;
@@ -2514,9 +2543,8 @@ template <int MODE>
 int launch_mx(const BlockProblem& b, cudaStream_t stream) {
     constexpr int id = MODE == kDense ? 0 : MODE == kByRows ? 1 : 2;
     constexpr int smem_ids[3] = {5, 11, 12}, cluster_ids[3] = {2, 5, 6};
-    return launch_block<MODE>(gemm_mx_kernel<kMxStages, kMxSfSlots, MODE>, b, 256, kMxThreads,
-                              kMxSmemBytes + (MODE == kDense ? 0 : static_cast<int>(sizeof(Units))), smem_ids[id],
-                              cluster_ids[id], stream);
+    return launch_block<MODE>(gemm_mx_kernel<kMxRing<MODE>, kMxSfSlots, MODE>, b, 256, kMxThreads, kMxSmemBytes<MODE>,
+                              smem_ids[id], cluster_ids[id], stream);
 }
 
 // fp32 factors: the CTA-pair promotion kernel, the experts' on their own.

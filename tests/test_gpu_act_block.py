@@ -226,3 +226,11 @@ def test_transpose_of_nothing_and_of_nan():
     q[3, 7], q[:, 9] = 0x7F, 0x38
     got, inv = F.fp8_block_transpose(q, F.E4M3, torch.ones(128, 1, device=DEV))
     assert got[7, 3] == 0x7F and inv[7] == 1 and (got[9] == 0x7E).all() and inv[0] == 1 and (got[0] == 0).all()
+
+
+def test_no_rows():
+    z = lambda *s, dt=torch.uint8: torch.zeros(*s, dtype=dt, device=DEV)
+    o = F.fp8_act_block(z(0, 256, dt=BF), F.ACT_SILU, gated=True, keep=True)
+    assert o.q.shape == (0, 128) and o.z_q.shape == (0, 256) and o.z_scale_inv.shape == (0, 2)
+    b = F.fp8_act_block_bwd(z(0, 128, dt=BF), o.z_q, o.z_scale_inv, F.ACT_SILU, gated=True, want_t=True, want_h_t=True)
+    assert b.q.shape == (0, 256) and b.q_t.shape == (256, 0) and b.h_scale_inv_t.shape == (128, 0)
