@@ -62,9 +62,17 @@ __device__ __forceinline__ Quad decode4(int fmt, uint32_t w, float inv) {
 __device__ __forceinline__ Quad from_bf16(uint2 w) { return Quad{{row::bf2(w.x), row::bf2(w.y)}}; }
 
 // The four codes of q * s, the first in the low byte.
-__device__ __forceinline__ uint32_t code4(int fmt, const Quad& q, f2 s0, f2 s1) {
+template <int FMT>
+__device__ __forceinline__ uint32_t code4(const Quad& q, f2 s0, f2 s1) {
     const f2 a = row::mul2(q.v[0], s0), b = row::mul2(q.v[1], s1);
-    return row::cvt_pair(fmt, row::lo2(a), row::hi2(a)) | (row::cvt_pair(fmt, row::lo2(b), row::hi2(b)) << 16);
+    return row::cvt_pair<FMT>(row::lo2(a), row::hi2(a)) | (row::cvt_pair<FMT>(row::lo2(b), row::hi2(b)) << 16);
+}
+
+// f(std::integral_constant<int, fmt>): the format is tested once, not at every code.
+template <typename F>
+__device__ __forceinline__ void by_format(int fmt, F f) {
+    if (fmt == FP8_E4M3) f(std::integral_constant<int, FP8_E4M3>());
+    else f(std::integral_constant<int, FP8_E5M2>());
 }
 
 // The largest magnitude of a row's 128 columns, in every lane: the bits of an
@@ -507,7 +515,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const Rows t = rows_at(k);
         const int64_t tile_row = t.tile_row, t0 = tile_row * 128, r0 = t.r0, at_factor = t.at_factor;
         const int blk = t.blk, first = t.first, last = t.last, c = blk * 128 + lane * 4;
-        const bool holds = t.holds;
+        const bool holds = t.holds, whole = first == 0 && last == kTileRows;
         const float factor = next_factor;
         const bool ok = ptx::mbar_wait(&full[k & 1], (k >> 1) & 1u, &abort_word);
         const uint8_t* st = smem + (k & 1) * kStage;
@@ -520,7 +528,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             uint2 d = *reinterpret_cast<const uint2*>(st + at * 256 + lane * 8);
             uint32_t zg = *reinterpret_cast<const uint32_t*>(st + kStageD + at * 128 + lane * 4);
             uint32_t zu = GATED ? *reinterpret_cast<const uint32_t*>(st + kStageD + kStageZ + at * 128 + lane * 4) : 0u;
-            if (i < first || i >= last) {
+            if (!whole && (i < first || i >= last)) {
                 d = make_uint2(0, 0);
                 zg = zu = 0;
             }
@@ -557,43 +565,37 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const float s_row = row::block_scale(top, p.fmt, p.pow2);
             if (holds) p.inv[at_factor] = __fdiv_rn(1.0f, s_row);
             uint8_t* q = p.q + r0 * W + c;
+            by_format(p.fmt, [&](auto f) {
 #pragma unroll
-            for (int i = 0; i < kTileRows; ++i) {
-                const f2 a = row::all2(__shfl_sync(row::kAll, s_row, 2 * i));
-                const f2 b = row::all2(GATED ? __shfl_sync(row::kAll, s_row, 2 * i + 1) : 0.0f);
-                if (i >= first && i < last) {
-                    *reinterpret_cast<uint32_t*>(q) = code4(p.fmt, v[i].dg, a, a);
-                    if (GATED) *reinterpret_cast<uint32_t*>(q + N) = code4(p.fmt, v[i].du, b, b);
+                for (int i = 0; i < kTileRows; ++i) {
+                    const f2 a = row::all2(__shfl_sync(row::kAll, s_row, 2 * i));
+                    const f2 b = row::all2(GATED ? __shfl_sync(row::kAll, s_row, 2 * i + 1) : 0.0f);
+                    if (whole || (i >= first && i < last)) {
+                        *reinterpret_cast<uint32_t*>(q) = code4<f.value>(v[i].dg, a, a);
+                        if (GATED) *reinterpret_cast<uint32_t*>(q + N) = code4<f.value>(v[i].du, b, b);
+                    }
+                    q += W;
                 }
-                q += W;
-            }
+            });
         }
         __syncthreads();
-        uint32_t w[kTileRows];
-        if (p.qt) {
-            const float4 a = reinterpret_cast<const float4*>(scale[0])[lane];
+        // the codes of one tensor's columns, turned, into the tile `t`
+        auto put_columns = [&](auto f, int t, auto value) {
+            const float4 a = reinterpret_cast<const float4*>(scale[t])[lane];
             const f2 s0 = row::mk2(a.x, a.y), s1 = row::mk2(a.z, a.w);
+            uint32_t w[kTileRows];
 #pragma unroll
-            for (int i = 0; i < kTileRows; ++i) w[i] = code4(p.fmt, v[i].dg, s0, s1);
+            for (int i = 0; i < kTileRows; ++i) w[i] = code4<f.value>(value(i), s0, s1);
             turn8(w);
-            stage8(turned, w, warp, lane);
-            if (GATED) {
-                const float4 b = reinterpret_cast<const float4*>(scale[1])[lane];
-                const f2 u0 = row::mk2(b.x, b.y), u1 = row::mk2(b.z, b.w);
-#pragma unroll
-                for (int i = 0; i < kTileRows; ++i) w[i] = code4(p.fmt, v[i].du, u0, u1);
-                turn8(w);
-                stage8(turned + 128 * 128, w, warp, lane);
-            }
-        }
-        if (p.ht) {
-            const float4 e = reinterpret_cast<const float4*>(scale[2])[lane];
-            const f2 s0 = row::mk2(e.x, e.y), s1 = row::mk2(e.z, e.w);
-#pragma unroll
-            for (int i = 0; i < kTileRows; ++i) w[i] = code4(p.h_fmt, v[i].h, s0, s1);
-            turn8(w);
-            stage8(turned + 2 * 128 * 128, w, warp, lane);
-        }
+            stage8(turned + t * 128 * 128, w, warp, lane);
+        };
+        if (p.qt)
+            by_format(p.fmt, [&](auto f) {
+                put_columns(f, 0, [&](int i) -> const Quad& { return v[i].dg; });
+                if (GATED) put_columns(f, 1, [&](int i) -> const Quad& { return v[i].du; });
+            });
+        if (p.ht)
+            by_format(p.h_fmt, [&](auto f) { put_columns(f, 2, [&](int i) -> const Quad& { return v[i].h; }); });
         __syncthreads();
         const int64_t out_at = static_cast<int64_t>(blk) * 128 * p.M + t0;
         if (p.qt) {
@@ -673,7 +675,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_transpose_kernel(const 
         const float4 s = reinterpret_cast<const float4*>(scale)[lane];
         const f2 s0 = row::mk2(s.x, s.y), s1 = row::mk2(s.z, s.w);
 #pragma unroll
-        for (int i = 0; i < kTileRows; ++i) w[i] = code4(FMT, v[i], s0, s1);
+        for (int i = 0; i < kTileRows; ++i) w[i] = code4<FMT>(v[i], s0, s1);
         turn8(w);
         stage8(turned, w, warp, lane);
         __syncthreads();
