@@ -22,35 +22,44 @@ constexpr int64_t kLimit = (int64_t{1} << 31) - 1024;   // coordinates and units
 
 // ------------------------------------------------------------------ few rows an expert
 
-// Tokens of decoding or of a prompt's chunk: reading the weights is the floor,
-// and a 256-row tile would be nearly empty.  So the operands change sides: 128
-// rows of the weights are the MMA's M, TN tokens its N.  A weight tile is one
-// 128x128 block a K step, so its factor is one number, and a token's is a
-// column's.
+// Tokens of decoding or of a prompt's chunk: reading the weights is the floor.
+// 128 x 128 weight blocks against TN tokens a tile, one factor of the weights a K
+// step; the products of its token factors and that one are made once a tile.
+//   TN = 128   tokens on the MMA's M side: a promotion thread has a token and half
+//              of its columns, so one factor serves all that it adds;
+//   TN = 16    the weights on the M side, 16 tokens its N: a thread has one weight
+//              row and all 16 tokens, a factor each.  An eighth of the shared
+//              memory for tokens leaves more for weights on their way.
 //   warp 0      TMA producer (one thread): weight and token tiles into a ring;
 //   warp 1      MMA issuer: each 128-deep K block to a TMEM buffer of TN columns;
 //   warp 2      TMEM allocation;
 //   warp 3      factors: per four K blocks the products (token x weight block)
 //               of TN tokens, one group ahead;
-//   warps 4-    promotion: a weight row a thread, its sums with TN (16) or TN / 2
-//               tokens in registers, 16 partial sums on their way from TMEM while
-//               16 are added; at the tile's end a token's 32 neighbouring columns
-//               a store.
-// One CTA an SM; the ring holds 160 KB or more in flight, so that waiting for the
+//   warps 4-    promotion, 16 partial sums on their way from TMEM while 16 are
+//               added.
+// One CTA an SM; the ring holds 180 KB or more in flight, so that waiting for the
 // sums of one tile does not stop the next tile's weights.
+// Measured (and without the 256 MB that the timing left dirty in L2, some 20 us
+// less): 64 tokens to 28 of 32 experts of 4096 x 7168 147 us (823 MB read, 6.7
+// TB/s); 32 experts of 4096 x 4096 with 8 rows each 108, 24 rows 112, 64 rows
+// 116-118, 96 rows 141.  With the weights on the M side at 128 tokens the last two
+// took 142 and 171: each thread reads 64 factors from shared memory a K block, 512
+// cycles an SM.  Sixteen promotion warps instead of eight 126 for 118.  CTA pairs
+// that share the tokens, so that a quarter less goes into the SMs: level.
 constexpr int BK = 128, UMMA_K = 32;
 constexpr int kFewSets = 3;   // factor groups in flight
 
 template <int TN>
 struct Few {
-    static constexpr int EPI = TN == 16 ? 4 : 8;   // promotion warps: two a lane quarter take half of the tokens each
-    static constexpr int CW = TN * 4 / EPI;        // tokens of one
+    static constexpr bool ROWS = TN == 128;       // tokens on the M side
+    static constexpr int EPI = ROWS ? 8 : 4;      // promotion warps: two a lane quarter take half of the columns each
+    static constexpr int CW = TN * 4 / EPI;       // columns of one
     static constexpr int THREADS = (4 + EPI) * 32;
-    static constexpr int NBUF = TN <= 64 ? 4 : 512 / TN;
-    static constexpr uint32_t TMEM_COLS = NBUF * TN < 32 ? 32 : NBUF * TN;
+    static constexpr int NBUF = 4;
+    static constexpr uint32_t TMEM_COLS = NBUF * TN;
     static constexpr int W_BYTES = 128 * BK, T_BYTES = TN * BK;
     static constexpr int STAGE_BYTES = W_BYTES + T_BYTES;
-    static constexpr int STAGES = 184 * 1024 / STAGE_BYTES;
+    static constexpr int STAGES = 192 * 1024 / STAGE_BYTES;
     static constexpr int SET_BYTES = 4 * TN * 4;   // [4 K blocks][TN]
     static constexpr int BARS = 2 * STAGES + 2 * NBUF + 2 * kFewSets + 1;
     static constexpr int SMEM = STAGES * STAGE_BYTES + kFewSets * SET_BYTES + BARS * 8 + 16 +
@@ -93,6 +102,83 @@ __device__ __forceinline__ float4 factors4(const float* s, int kb, int KB, bool 
     if (vec) return *reinterpret_cast<const float4*>(s + kb);
     return make_float4(s[kb], kb + 1 < KB ? s[kb + 1] : 0.0f, kb + 2 < KB ? s[kb + 2] : 0.0f,
                        kb + 3 < KB ? s[kb + 3] : 0.0f);
+}
+
+// acc += partial sums x factors, W columns of a lane: f[c] for column c.
+// Sixteen are on their way from TMEM while sixteen are added.
+template <int W, typename Release>
+__device__ __forceinline__ void add_columns(row::f2 (&acc)[W / 2], uint32_t tmem, const float* f, Release release) {
+    uint32_t r[2][16];
+    ptx::tmem_ld_32x32b_x16(tmem, r[0]);
+#pragma unroll
+    for (int j = 0; j < W / 16; ++j) {
+        float4 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(f + 16 * j + 4 * i);
+        ptx::tmem_wait_ld();
+        if (j + 1 < W / 16) ptx::tmem_ld_32x32b_x16(tmem + 16 * (j + 1), r[(j + 1) & 1]);
+        else release();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            row::f2* a = acc + 8 * j + 2 * i;
+            const uint32_t* v = r[j & 1] + 4 * i;
+            a[0] = row::fma2(row::mk2(__uint_as_float(v[0]), __uint_as_float(v[1])), row::mk2(w[i].x, w[i].y), a[0]);
+            a[1] = row::fma2(row::mk2(__uint_as_float(v[2]), __uint_as_float(v[3])), row::mk2(w[i].z, w[i].w), a[1]);
+        }
+    }
+}
+
+// The same with one factor for all of a lane's columns.
+template <int W, typename Release>
+__device__ __forceinline__ void add_rows(row::f2 (&acc)[W / 2], uint32_t tmem, row::f2 f, Release release) {
+    uint32_t r[2][16];
+    ptx::tmem_ld_32x32b_x16(tmem, r[0]);
+#pragma unroll
+    for (int j = 0; j < W / 16; ++j) {
+        ptx::tmem_wait_ld();
+        if (j + 1 < W / 16) ptx::tmem_ld_32x32b_x16(tmem + 16 * (j + 1), r[(j + 1) & 1]);
+        else release();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t* v = r[j & 1] + 2 * i;
+            acc[8 * j + i] = row::fma2(row::mk2(__uint_as_float(v[0]), __uint_as_float(v[1])), f, acc[8 * j + i]);
+        }
+    }
+}
+
+// W neighbouring columns of one row of D, from element `at` on.
+template <int W>
+__device__ __forceinline__ void put_row(const FewParams& p, const row::f2 (&acc)[W / 2], int64_t at) {
+    if (p.out == FP8_OUT_BF16) {
+        uint4* d = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.D) + at);
+        auto pair = [](row::f2 v) { return row::pack_bf16(row::lo2(v), row::hi2(v)); };
+#pragma unroll
+        for (int i = 0; i < W / 8; ++i)
+            d[i] = make_uint4(pair(acc[4 * i]), pair(acc[4 * i + 1]), pair(acc[4 * i + 2]), pair(acc[4 * i + 3]));
+    } else {
+        float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.D) + at);
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i)
+            d[i] = make_float4(row::lo2(acc[2 * i]), row::hi2(acc[2 * i]), row::lo2(acc[2 * i + 1]),
+                               row::hi2(acc[2 * i + 1]));
+    }
+}
+
+// One column of the first `rows` of W rows of D, from element `at` on.
+template <int W>
+__device__ __forceinline__ void put_column(const FewParams& p, const row::f2 (&acc)[W / 2], int64_t at, int rows) {
+    if (p.out == FP8_OUT_BF16) {
+        __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.D) + at;
+#pragma unroll
+        for (int c = 0; c < W; ++c)
+            if (c < rows)
+                d[static_cast<int64_t>(c) * p.N] = __float2bfloat16_rn(c & 1 ? row::hi2(acc[c / 2]) : row::lo2(acc[c / 2]));
+    } else {
+        float* d = static_cast<float*>(p.D) + at;
+#pragma unroll
+        for (int c = 0; c < W; ++c)
+            if (c < rows) d[static_cast<int64_t>(c) * p.N] = c & 1 ? row::hi2(acc[c / 2]) : row::lo2(acc[c / 2]);
+    }
 }
 
 template <int TN>
@@ -176,7 +262,7 @@ __global__ void __launch_bounds__(Few<TN>::THREADS, 1)
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            const uint32_t idesc = ptx::idesc_f8f6f4(p.fb, p.fa, 128, TN);
+            const uint32_t idesc = L::ROWS ? ptx::idesc_f8f6f4(p.fa, p.fb, 128, TN) : ptx::idesc_f8f6f4(p.fb, p.fa, 128, TN);
             uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
             bool ok = true;
             for (int u = u0; ok && u < num_units; u += step) {
@@ -189,8 +275,8 @@ __global__ void __launch_bounds__(Few<TN>::THREADS, 1)
                     const uint64_t td = ptx::sdesc_kmajor_sw128(ptx::smem_u32(s + L::W_BYTES));
 #pragma unroll
                     for (int k = 0; k < BK / UMMA_K; ++k)
-                        ptx::mma_f8f6f4(tmem_base + buf * TN, wd + (k * UMMA_K >> 4), td + (k * UMMA_K >> 4), idesc,
-                                        k != 0);
+                        ptx::mma_f8f6f4(tmem_base + buf * TN, (L::ROWS ? td : wd) + (k * UMMA_K >> 4),
+                                        (L::ROWS ? wd : td) + (k * UMMA_K >> 4), idesc, k != 0);
                     ptx::mma_commit(&empty[stage]);
                     ptx::mma_commit(&tfull[buf]);
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -237,51 +323,34 @@ __global__ void __launch_bounds__(Few<TN>::THREADS, 1)
             }
         }
     } else if (warp >= 4) {
-        constexpr int CW = L::CW, STEPS = CW / 16;
-        const int c0 = (warp - 4) / 4 * CW;   // this warp's first token
-        const uint32_t tcol = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0;
+        constexpr int CW = L::CW;
+        const int quarter = warp & 3, c0 = (warp - 4) / 4 * CW;   // this warp's lanes and first column
+        const uint32_t tcol = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + c0;
+        const float* mine = sets + (L::ROWS ? quarter * 32 + lane : c0);
         uint32_t buf = 0, buf_phase = 0, set = 0, set_phase = 0;
         bool ok = true;
         for (int u = u0; u < num_units; u += step) {
-            float acc[CW];
+            row::f2 acc[CW / 2];
 #pragma unroll
-            for (int c = 0; c < CW; ++c) acc[c] = 0.0f;
+            for (int c = 0; c < CW / 2; ++c) acc[c] = 0ull;
             for (int kb = 0; kb < KB; ++kb) {
                 if ((kb & 3) == 0) {
                     ok = __all_sync(row::kAll, ptx::mbar_wait<true>(&ffull[set], set_phase, abort_flag));
                     if (!ok) break;
                 }
-                const float* f = sets + set * (L::SET_BYTES / 4) + (kb & 3) * TN + c0;
+                const float* f = mine + set * (L::SET_BYTES / 4) + (kb & 3) * TN;
                 ok = lane == 0 ? ptx::mbar_wait<true>(&tfull[buf], buf_phase, abort_flag) : false;
                 ok = __shfl_sync(row::kAll, ok, 0);
                 if (!ok) break;
                 __syncwarp();
                 ptx::tc_fence_after();
-                uint32_t r[2][16];
-                ptx::tmem_ld_32x32b_x16(tcol + buf * TN, r[0]);
-#pragma unroll
-                for (int j = 0; j < STEPS; ++j) {
-                    float4 w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(f + 16 * j + 4 * i);
-                    ptx::tmem_wait_ld();
-                    if (j + 1 < STEPS) {
-                        ptx::tmem_ld_32x32b_x16(tcol + buf * TN + 16 * (j + 1), r[(j + 1) & 1]);
-                    } else {
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(&tempty[buf]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float* a = acc + 16 * j + 4 * i;
-                        const uint32_t* v = r[j & 1] + 4 * i;
-                        a[0] = __fmaf_rn(__uint_as_float(v[0]), w[i].x, a[0]);
-                        a[1] = __fmaf_rn(__uint_as_float(v[1]), w[i].y, a[1]);
-                        a[2] = __fmaf_rn(__uint_as_float(v[2]), w[i].z, a[2]);
-                        a[3] = __fmaf_rn(__uint_as_float(v[3]), w[i].w, a[3]);
-                    }
-                }
+                auto release = [&]() {   // the buffer has been read
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&tempty[buf]);
+                };
+                if constexpr (L::ROWS) add_rows<CW>(acc, tcol + buf * TN, row::all2(*f), release);
+                else add_columns<CW>(acc, tcol + buf * TN, f, release);
                 if (++buf == NBUF) { buf = 0; buf_phase ^= 1u; }
                 if ((kb & 3) == 3 || kb == KB - 1) {
                     __syncwarp();   // the set has been read
@@ -291,18 +360,12 @@ __global__ void __launch_bounds__(Few<TN>::THREADS, 1)
             }
             if (!ok) break;
             const FewTile t = few_tile<TN>(u, units, p);
-            const int rows = t.t_end - t.t0 - c0;
-            const int64_t at = static_cast<int64_t>(t.t0 + c0) * p.N + t.n_blk * 128 + (warp & 3) * 32 + lane;
-            if (p.out == FP8_OUT_BF16) {
-                __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.D) + at;
-#pragma unroll
-                for (int c = 0; c < CW; ++c)
-                    if (c < rows) d[static_cast<int64_t>(c) * p.N] = __float2bfloat16_rn(acc[c]);
+            if constexpr (L::ROWS) {
+                const int token = t.t0 + quarter * 32 + lane;
+                if (token < t.t_end) put_row<CW>(p, acc, static_cast<int64_t>(token) * p.N + t.n_blk * 128 + c0);
             } else {
-                float* d = static_cast<float*>(p.D) + at;
-#pragma unroll
-                for (int c = 0; c < CW; ++c)
-                    if (c < rows) d[static_cast<int64_t>(c) * p.N] = acc[c];
+                const int64_t at = static_cast<int64_t>(t.t0 + c0) * p.N + t.n_blk * 128 + quarter * 32 + lane;
+                put_column<CW>(p, acc, at, t.t_end - t.t0 - c0);
             }
         }
     }
@@ -384,13 +447,16 @@ int fp8_gemm_experts(const fp8_gemm_experts_args_t* a, void* stream) {
     if (a->M == 0) return FP8_OK;
     const ExpertGemm g{a->A, a->fa, a->B, a->fb, a->M, a->N, a->K, a->scale_inv_a, a->scale_inv_b, a->d, a->out, 0,
                        a->pow2, a->offsets, a->experts};
-    // rows an expert on average: the tile that holds them
+    // By rows an expert on average (us, sizes as above).  Tiles of 16 tokens against
+    // 128: 8 rows 108 against 108, 12 rows 115 against 110, and where one in eight
+    // of 64 experts of 2048 x 7168 has a row, 36 against 44.  128 against CTA pairs of
+    // 256: fp32 factors 160 rows 179 against 191, 224 rows 214 against 213, 288 rows
+    // 252 against 249; with powers of two, which only the pairs hand to the tensor
+    // core, 64 rows 118 against 120, 80 rows 126 against 120.
     const int64_t rows = (a->M + a->experts - 1) / a->experts;
     cudaStream_t st = as_stream(stream);
     if (rows <= 8) return launch_few<16>(g, st);
-    if (rows <= 16) return launch_few<32>(g, st);
-    if (rows <= 40) return launch_few<64>(g, st);
-    if (rows <= 112) return launch_few<128>(g, st);
+    if (rows <= (a->pow2 ? 72 : 224)) return launch_few<128>(g, st);
     r = launch_gemm_by_rows(g, st);
     return r != FP8_OK ? r : launch_status(what);
 }

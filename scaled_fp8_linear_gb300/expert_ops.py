@@ -122,8 +122,12 @@ def _offsets(offsets, on):
 def _codes(t, inv, wanted, shape, inv_shape, what, dev, on):
     """Codes and their factors, the given ones or (wanted) new ones:
     (codes, factors, address, address)."""
-    if t is None and inv is None and not wanted:
-        return None, None, 0, 0
+    if t is None and inv is None:
+        if not wanted:
+            return None, None, 0, 0
+        t = torch.empty(shape, dtype=_BYTE, device=dev)
+        inv = torch.empty(inv_shape, dtype=_F32, device=dev)
+        return t, inv, t.data_ptr(), inv.data_ptr()
     if t is None:
         t = torch.empty(shape, dtype=_BYTE, device=dev)
     if inv is None:

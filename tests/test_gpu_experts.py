@@ -100,6 +100,22 @@ def test_rows_around_the_tiles(rows):
     _product(4 * rows, 256, 256, [0, rows, 2 * rows, 3 * rows, 4 * rows], seed=rows)
 
 
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("rows", [8, 9, 72, 73, 224, 225])
+def test_rows_around_the_choice_of_the_kernel(rows, pow2):
+    off = [0, rows // 2, rows // 2, 2 * rows + 3, 4 * rows]
+    _product(4 * rows, 384, 640, off, fa=1, pow2=pow2, seed=rows)
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("n", [7, 31, 256])
+def test_many_experts_of_many_rows(n, pow2):
+    g = torch.Generator().manual_seed(n)
+    M = 290 * n if n < 256 else 60000
+    cuts = torch.randint(0, M + 1, (n - 1,), generator=g).sort().values.tolist()
+    _product(M, 256, 128, [0] + cuts + [M - 1], out=F.OUT_F32, pow2=pow2, seed=n)
+
+
 def test_nan_stays_in_its_row():
     g = torch.Generator().manual_seed(3)
     for M in (40, 600):
