@@ -1483,7 +1483,8 @@ __device__ __forceinline__ void promote_tokens(uint8_t* slots, uint32_t cols, ui
 // tokens, whose promotion is longer, one lane leaves the schedulers more (876
 // against 935).  Tried besides: each CTA its own MMAs, B by multicast (589: no
 // remote arrivals, but 48 KB a K block instead of 32 into each SM); one arrival a CTA
-// through warp 2 (608); test_wait for try_wait (level).
+// through warp 2 (608); test_wait for try_wait (level); for the weight gradients
+// 128-column tiles and four buffers (949: twice the operands' way for the same FMA work).
 // Stages: by rows four (564 us, 568 with three); by tokens three (876 against 892: shared
 // memory comes out of L1, where the factors' lines are).
 struct ExpertCfg {
