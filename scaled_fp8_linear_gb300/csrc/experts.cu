@@ -2,6 +2,7 @@
 // gradients of experts: the entry points, and the kernel for few rows an expert.
 // Products of more rows and the weight gradients run on gemm.cu's CTA-pair
 // kernels.
+#include <atomic>
 #include <cstdint>
 
 #include <cuda.h>
@@ -181,7 +182,44 @@ __device__ __forceinline__ void put_column(const FewParams& p, const row::f2 (&a
     }
 }
 
+// A tile's sums over K, in parts [TN * 128 / 4] of four in each CTA's shared memory
+// (tokens on the M side: columns 4 c .. of token r at 128 c + r; else tokens 4 c ..
+// of column r): this CTA adds its share of them, in the order of the CTAs, and
+// writes it.
 template <int TN>
+__device__ __forceinline__ void join_parts(const float4* part, const FewParams& p, const FewTile& t, uint32_t rank,
+                                           uint32_t ctas) {
+    using L = Few<TN>;
+    constexpr uint32_t ALL = TN * 128 / 4;
+    const uint32_t share = ALL / ctas;
+    for (uint32_t i = rank * share + threadIdx.x; i < (rank + 1) * share; i += L::THREADS) {
+        float4 v = ptx::ld_shared_cluster_f4(ptx::cluster_addr(part + i, 0));
+        for (uint32_t c = 1; c < ctas; ++c) {
+            const float4 w = ptx::ld_shared_cluster_f4(ptx::cluster_addr(part + i, c));
+            v.x = __fadd_rn(v.x, w.x); v.y = __fadd_rn(v.y, w.y); v.z = __fadd_rn(v.z, w.z); v.w = __fadd_rn(v.w, w.w);
+        }
+        const row::f2 acc[2] = {row::mk2(v.x, v.y), row::mk2(v.z, v.w)};
+        const int r = static_cast<int>(i & 127), c4 = static_cast<int>(i >> 7) * 4;
+        if constexpr (L::ROWS) {
+            const int token = t.t0 + r;
+            const int64_t at = static_cast<int64_t>(token) * p.N + t.n_blk * 128 + c4;
+            if (token >= t.t_end) continue;
+            if (p.out == FP8_OUT_BF16)
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.D) + at) =
+                    make_uint2(row::pack_bf16(v.x, v.y), row::pack_bf16(v.z, v.w));
+            else
+                *reinterpret_cast<float4*>(static_cast<float*>(p.D) + at) = v;
+        } else {
+            const int64_t at = static_cast<int64_t>(t.t0 + c4) * p.N + t.n_blk * 128 + r;
+            put_column<4>(p, acc, at, t.t_end - t.t0 - c4);
+        }
+    }
+}
+
+// SPLIT: a cluster has one tile, each of its CTAs a range of K in groups of four
+// K blocks, joined through distributed shared memory in the CTAs' order.  For
+// products of few tiles, where the way through a tile's K is the time.
+template <int TN, bool SPLIT>
 __global__ void __launch_bounds__(Few<TN>::THREADS, 1)
     gemm_experts_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmT,
                             const __grid_constant__ FewParams p) {
@@ -234,7 +272,11 @@ __global__ void __launch_bounds__(Few<TN>::THREADS, 1)
     ptx::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const int num_units = units->first[p.experts], KB = p.num_kb;
-    const int u0 = blockIdx.x, step = gridDim.x;
+    const uint32_t ctas = SPLIT ? ptx::cluster_nctarank() : 1, rank = SPLIT ? ptx::cluster_ctarank() : 0;
+    const int u0 = static_cast<int>(blockIdx.x / ctas), step = static_cast<int>(gridDim.x / ctas);
+    const int groups = (KB + 3) / 4;
+    const int kb0 = SPLIT ? static_cast<int>(groups * rank / ctas) * 4 : 0;
+    const int kb1 = SPLIT ? min(static_cast<int>(groups * (rank + 1) / ctas) * 4, KB) : KB;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -244,7 +286,7 @@ __global__ void __launch_bounds__(Few<TN>::THREADS, 1)
             for (int u = u0; ok && u < num_units; u += step) {
                 const FewTile t = few_tile<TN>(u, units, p);
                 const int yw = t.expert * p.N + t.n_blk * 128;
-                for (int kb = 0; kb < KB; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!ptx::mbar_wait<true>(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
                     uint8_t* s = ring + stage * L::STAGE_BYTES;
                     ptx::mbar_arrive_expect_tx(&full[stage], L::STAGE_BYTES);
@@ -266,7 +308,7 @@ __global__ void __launch_bounds__(Few<TN>::THREADS, 1)
             uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
             bool ok = true;
             for (int u = u0; ok && u < num_units; u += step) {
-                for (int kb = 0; kb < KB; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!ptx::mbar_wait<true>(&tempty[buf], buf_phase ^ 1u, abort_flag)) { ok = false; break; }
                     if (!ptx::mbar_wait<true>(&full[stage], phase, abort_flag)) { ok = false; break; }
                     ptx::tc_fence_after();
@@ -297,10 +339,10 @@ __global__ void __launch_bounds__(Few<TN>::THREADS, 1)
             auto token = [&](int i) {   // tokens past the last row are read at it
                 return p.sa + static_cast<int64_t>(min(t.t0 + i * 32 + lane, p.M - 1)) * KB;
             };
-            float4 w = factors4(sw, 0, KB, p.vec_b), f[PER];
+            float4 w = factors4(sw, kb0, KB, p.vec_b), f[PER];
 #pragma unroll
-            for (int i = 0; i < PER; ++i) f[i] = factors4(token(i), 0, KB, p.vec_a);
-            for (int kb = 0; kb < KB; kb += 4) {
+            for (int i = 0; i < PER; ++i) f[i] = factors4(token(i), kb0, KB, p.vec_a);
+            for (int kb = kb0; kb < kb1; kb += 4) {
                 ok = lane == 0 ? ptx::mbar_wait<true>(&fempty[set], phase ^ 1u, abort_flag) : false;
                 ok = __shfl_sync(row::kAll, ok, 0);
                 if (!ok) break;
@@ -333,7 +375,7 @@ __global__ void __launch_bounds__(Few<TN>::THREADS, 1)
             row::f2 acc[CW / 2];
 #pragma unroll
             for (int c = 0; c < CW / 2; ++c) acc[c] = 0ull;
-            for (int kb = 0; kb < KB; ++kb) {
+            for (int kb = kb0; kb < kb1; ++kb) {
                 if ((kb & 3) == 0) {
                     ok = __all_sync(row::kAll, ptx::mbar_wait<true>(&ffull[set], set_phase, abort_flag));
                     if (!ok) break;
@@ -352,7 +394,7 @@ __global__ void __launch_bounds__(Few<TN>::THREADS, 1)
                 if constexpr (L::ROWS) add_rows<CW>(acc, tcol + buf * TN, row::all2(*f), release);
                 else add_columns<CW>(acc, tcol + buf * TN, f, release);
                 if (++buf == NBUF) { buf = 0; buf_phase ^= 1u; }
-                if ((kb & 3) == 3 || kb == KB - 1) {
+                if ((kb & 3) == 3 || kb == kb1 - 1) {
                     __syncwarp();   // the set has been read
                     if (lane == 0) ptx::mbar_arrive(&fempty[set]);
                     if (++set == kFewSets) { set = 0; set_phase ^= 1u; }
@@ -360,7 +402,13 @@ __global__ void __launch_bounds__(Few<TN>::THREADS, 1)
             }
             if (!ok) break;
             const FewTile t = few_tile<TN>(u, units, p);
-            if constexpr (L::ROWS) {
+            if constexpr (SPLIT) {   // the ring is free: its last copies have been multiplied
+                float4* to = reinterpret_cast<float4*>(ring) + c0 / 4 * 128 + quarter * 32 + lane;
+#pragma unroll
+                for (int i = 0; i < CW / 4; ++i)
+                    to[128 * i] = make_float4(row::lo2(acc[2 * i]), row::hi2(acc[2 * i]), row::lo2(acc[2 * i + 1]),
+                                              row::hi2(acc[2 * i + 1]));
+            } else if constexpr (L::ROWS) {
                 const int token = t.t0 + quarter * 32 + lane;
                 if (token < t.t_end) put_row<CW>(p, acc, static_cast<int64_t>(token) * p.N + t.n_blk * 128 + c0);
             } else {
@@ -368,6 +416,14 @@ __global__ void __launch_bounds__(Few<TN>::THREADS, 1)
                 put_column<CW>(p, acc, at, t.t_end - t.t0 - c0);
             }
         }
+    }
+    if constexpr (SPLIT) {
+        __syncwarp();
+        ptx::cluster_sync();   // every CTA's part is there
+        if (u0 < num_units)
+            join_parts<TN>(reinterpret_cast<const float4*>(ring), p, few_tile<TN>(u0, units, p), rank, ctas);
+        __syncwarp();
+        ptx::cluster_sync();   // and has been read
     }
     ptx::tc_fence_before();
     __syncthreads();
@@ -378,15 +434,44 @@ __global__ void __launch_bounds__(Few<TN>::THREADS, 1)
     if (threadIdx.x == 0 && *abort_flag && p.status) atomicOr(p.status, 1u);
 }
 
+// How many clusters of `ctas` (2, 4, 8) CTAs of the split kernel the device holds at
+// once; cached per device.  Fewer than its SMs would: a cluster is within one GPC.
+template <int TN>
+int few_clusters(int ctas) {
+    static std::atomic<int> cache[64][4] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
+    const bool known = dev >= 0 && dev < 64;   // other devices: asked at every call
+    std::atomic<int>* c = known ? &cache[dev][ctas / 4 + 1] : nullptr;
+    int n = known ? c->load(std::memory_order_relaxed) : 0;
+    if (n) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas * 1024));
+    cfg.blockDim = dim3(Few<TN>::THREADS);
+    cfg.dynamicSmemBytes = Few<TN>::SMEM;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, gemm_experts_few_kernel<TN, true>, &cfg) != cudaSuccess || n <= 0) {
+        (void)cudaGetLastError();
+        n = num_sms() / (2 * ctas);
+    }
+    if (known) c->store(n, std::memory_order_relaxed);
+    return n;
+}
+
 template <int TN>
 int launch_few(const ExpertGemm& g, cudaStream_t stream) {
     using L = Few<TN>;
     CUtensorMap tmW, tmT;
     int r = make_kmajor_map(&tmW, g.B, g.N * g.experts, g.K, 128);
     if (r == FP8_OK) r = make_kmajor_map(&tmT, g.A, g.M, g.K, TN);
-    static host::SmemAllowance allowance;
-    auto k = gemm_experts_few_kernel<TN>;
-    if (r == FP8_OK) r = host::allow_smem(k, L::SMEM, allowance);
+    static host::SmemAllowance whole, split;
+    if (r == FP8_OK) r = host::allow_smem(gemm_experts_few_kernel<TN, false>, L::SMEM, whole);
+    if (r == FP8_OK) r = host::allow_smem(gemm_experts_few_kernel<TN, true>, L::SMEM, split);
     if (r != FP8_OK) return r;
     FewParams p{};
     p.M = static_cast<int>(g.M); p.N = static_cast<int>(g.N);
@@ -398,10 +483,21 @@ int launch_few(const ExpertGemm& g, cudaStream_t stream) {
     p.status = device_status_word();
     // at most this many tiles, however the rows are cut
     const int64_t busy = g.M < g.experts ? g.M : g.experts;
-    const int64_t tiles = ((g.M - busy) / TN + busy) * p.num_n;
-    const int sms = num_sms();
-    launch_pdl(k, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(L::THREADS), L::SMEM, stream, tmW, tmT,
-               p);
+    const int64_t tiles = ((g.M - busy) / TN + busy) * p.num_n, sms = num_sms();
+    // As many CTAs a tile as groups of K blocks and all tiles' clusters at once allow.
+    // (us with a launch's and a cold cache's 10, one CTA against 8, 4 or 2: 1 row of
+    // 128 x 7168 28 against 13; 100 rows of 1024 x 7168 30 against 18, 16 of 2048 x
+    // 7168 30 against 19, 64 of 4096 x 4096 22 against 18.  In two rounds 16 tiles of
+    // 8 CTAs take 28.)
+    const int groups = (p.num_kb + 3) / 4;
+    int ctas = 8;
+    while (ctas > 1 && (groups < ctas || tiles * ctas > sms || tiles > few_clusters<TN>(ctas))) ctas /= 2;
+    if (ctas > 1)
+        launch_pdl_cluster(gemm_experts_few_kernel<TN, true>, dim3(static_cast<unsigned>(tiles * ctas)), dim3(L::THREADS),
+                           L::SMEM, ctas, stream, tmW, tmT, p);
+    else
+        launch_pdl(gemm_experts_few_kernel<TN, false>, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)),
+                   dim3(L::THREADS), L::SMEM, stream, tmW, tmT, p);
     return host::launch_status("fp8_gemm_experts");
 }
 

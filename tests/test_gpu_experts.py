@@ -107,6 +107,29 @@ def test_rows_around_the_choice_of_the_kernel(rows, pow2):
     _product(4 * rows, 384, 640, off, fa=1, pow2=pow2, seed=rows)
 
 
+@pytest.mark.parametrize("out", [F.OUT_BF16, F.OUT_F32])
+@pytest.mark.parametrize("K", [128, 512, 640, 1152, 2048, 4224, 7168])
+@pytest.mark.parametrize("M,N,off", [
+    (1, 128, [0, 1]), (3, 384, [0, 1, 1, 3]), (16, 1024, [0, 16]), (17, 256, [0, 0, 17]), (9, 128, [2, 2, 7]),
+    (40, 128, [0, 40]), (129, 512, [0, 129]), (200, 256, [3, 100, 199]), (30, 256, [0, 0, 0])])
+def test_few_tiles_with_a_long_reduction(M, N, K, off, out):
+    """K cut into ranges, and groups of four K blocks that do not divide evenly."""
+    _product(M, N, K, off, fa=1, out=out, seed=K + M)
+    if K == 7168:
+        _product(M, N, K, off, out=out, exact=False, seed=M)
+
+
+def test_equal_calls_give_equal_bits_when_k_is_cut():
+    g = torch.Generator().manual_seed(9)
+    for M in (5, 70):
+        a, b = E.any_codes(g, 0, M, 7168).to(DEV), E.any_codes(g, 0, 2, 256, 7168).to(DEV)
+        sa, sb = (torch.rand(M, 56, generator=g) + 0.1).to(DEV), (torch.rand(2, 2, 56, generator=g) + 0.1).to(DEV)
+        off = _i32([0, M // 2, M])
+        first = F.fp8_gemm_experts(a, 0, b, 0, sa, sb, off, out=F.OUT_F32)
+        for _ in range(20):
+            assert torch.equal(F.fp8_gemm_experts(a, 0, b, 0, sa, sb, off, out=F.OUT_F32), first)
+
+
 @pytest.mark.parametrize("pow2", [False, True])
 @pytest.mark.parametrize("n", [7, 31, 256])
 def test_many_experts_of_many_rows(n, pow2):
