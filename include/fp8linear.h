@@ -639,8 +639,8 @@ typedef struct {
     const float* scale_inv_a;   /* [M][K/128]                                 */
     const float* scale_inv_b;   /* [experts][N/128][K/128]                    */
     int32_t pow2;          /* 1: every factor is a power of two (from pow2    */
-                           /*   casts), which the tensor core applies itself; */
-                           /*   only the factors' exponents are read then     */
+                           /*   casts), which the tensor core may apply: it   */
+                           /*   reads only the factors' exponents             */
     int32_t out;           /* fp8_out_t of d                                  */
     void* d;               /* [M][N], 16-byte aligned                         */
     const int32_t* offsets;/* [experts + 1]                                   */

@@ -463,6 +463,12 @@ int few_clusters(int ctas) {
     return n;
 }
 
+// How many tiles of tn tokens there are at most, however the rows are cut.
+int64_t most_tiles(const ExpertGemm& g, int tn) {
+    const int64_t busy = g.M < g.experts ? g.M : g.experts;
+    return ((g.M - busy) / tn + busy) * (g.N / 128);
+}
+
 template <int TN>
 int launch_few(const ExpertGemm& g, cudaStream_t stream) {
     using L = Few<TN>;
@@ -481,9 +487,7 @@ int launch_few(const ExpertGemm& g, cudaStream_t stream) {
     p.vec_a = p.num_kb % 4 == 0 && host::aligned(g.sa, 16);
     p.vec_b = p.num_kb % 4 == 0 && host::aligned(g.sb, 16);
     p.status = device_status_word();
-    // at most this many tiles, however the rows are cut
-    const int64_t busy = g.M < g.experts ? g.M : g.experts;
-    const int64_t tiles = ((g.M - busy) / TN + busy) * p.num_n, sms = num_sms();
+    const int64_t tiles = most_tiles(g, TN), sms = num_sms();
     // As many CTAs a tile as groups of K blocks and all tiles' clusters at once allow.
     // (us with a launch's and a cold cache's 10, one CTA against 8, 4 or 2: 1 row of
     // 128 x 7168 28 against 13; 100 rows of 1024 x 7168 30 against 18, 16 of 2048 x
@@ -548,11 +552,14 @@ int fp8_gemm_experts(const fp8_gemm_experts_args_t* a, void* stream) {
     // of 64 experts of 2048 x 7168 has a row, 36 against 44.  128 against CTA pairs of
     // 256: fp32 factors 160 rows 179 against 191, 224 rows 214 against 213, 288 rows
     // 252 against 249; with powers of two, which only the pairs hand to the tensor
-    // core, 64 rows 118 against 120, 80 rows 126 against 120.
+    // core, 64 rows 118 against 120, 80 rows 126 against 120.  And tiles of 128 that
+    // all run at once, of which the pairs would be half or a quarter of the CTAs: 300
+    // rows of 1024 x 7168 20 against 42 (powers of two 32), 1000 rows of 2048 x 7168 32
+    // against 42 (34), 2000 rows of 1024 x 2048 17 against 22 (22).
     const int64_t rows = (a->M + a->experts - 1) / a->experts;
     cudaStream_t st = as_stream(stream);
     if (rows <= 8) return launch_few<16>(g, st);
-    if (rows <= (a->pow2 ? 72 : 224)) return launch_few<128>(g, st);
+    if (rows <= (a->pow2 ? 72 : 224) || most_tiles(g, 128) <= num_sms()) return launch_few<128>(g, st);
     r = launch_gemm_by_rows(g, st);
     return r != FP8_OK ? r : launch_status(what);
 }

@@ -85,6 +85,41 @@ def test_products_of_any_codes(M, off, fa, fb, pow2):
     _product(M, 384, 896, off, fa, fb, out=F.OUT_F32, pow2=pow2, exact=False, seed=1)
 
 
+# more rows an expert and more tiles than the kernels of few rows take
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("out", [F.OUT_BF16, F.OUT_F32])
+@pytest.mark.parametrize("K,off", [
+    (128, [0, 3000]),
+    (384, [5, 700, 700, 1411, 2990]),            # rows of no expert before and after
+    (640, [0, 1500, 1400, 4000]),                # falling, and past the rows
+    (256, [-5, 256, 512, 813, 941, 1069, 1070, 2222]),
+    (2176, [0, 1, 130, 3000]),
+    (256, [0, 0, 0, 0]),                         # no rows at all
+    (512, [2999, 2999, 3000]),
+])
+def test_products_of_many_tiles(K, off, out, pow2):
+    _product(3000, 1152, K, off, out=out, pow2=pow2)
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("fa,fb", [(0, 0), (1, 0), (0, 1), (1, 1)])
+def test_products_of_many_tiles_of_any_codes(fa, fb, pow2):
+    _product(2700, 1280, 896, [0, 601, 1300, 2600], fa, fb, out=F.OUT_F32, pow2=pow2, exact=False, seed=1)
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+def test_nan_stays_in_its_row_among_many_tiles(pow2):
+    g = torch.Generator().manual_seed(3)
+    M, N = 3000, 1152
+    a, b = E.exact_codes(g, 0, M, 256), E.exact_codes(g, 0, 2, N, 256)
+    sa, sb = E.exact_factors(g, M, 2), E.exact_factors(g, 2, N // 128, 2)
+    a[11, 5] = a[1400, 200] = 0x7F
+    got = F.fp8_gemm_experts(a.to(DEV), 0, b.to(DEV), 0, sa.to(DEV), sb.to(DEV), _i32([0, 1300, M]), pow2=pow2).cpu()
+    nan = torch.zeros(M, dtype=torch.bool)
+    nan[[11, 1400]] = True
+    assert torch.isnan(got[nan]).all() and not torch.isnan(got[~nan]).any()
+
+
 @pytest.mark.parametrize("M,rows", [(200, 3), (4096, 100), (6000, 2000)])
 def test_many_experts(M, rows):
     g = torch.Generator().manual_seed(rows)
@@ -117,6 +152,13 @@ def test_few_tiles_with_a_long_reduction(M, N, K, off, out):
     _product(M, N, K, off, fa=1, out=out, seed=K + M)
     if K == 7168:
         _product(M, N, K, off, out=out, exact=False, seed=M)
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("M,N,off", [(300, 256, [0, 300]), (1000, 384, [0, 450, 450, 1000]),
+                                     (4800, 512, [0, 4799]), (5000, 512, [0, 4999])])   # 148 and 160 tiles of 128 rows
+def test_many_rows_in_few_tiles(M, N, off, pow2):
+    _product(M, N, 1152, off, fb=1, pow2=pow2, seed=M)
 
 
 def test_equal_calls_give_equal_bits_when_k_is_cut():
