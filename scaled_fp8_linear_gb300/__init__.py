@@ -457,21 +457,31 @@ STATUS_NONFINITE = 2   # bit 1: a scale update met a non-finite amax
 STATUS_OFFSETS = 4     # bit 2: fp8_wgrad_experts met offsets that are no multiples of 128
 
 
+# bit, error, what it says; by how much a report spoils
+_REPORTS = (
+    (STATUS_TIMEOUT, lambda m: Fp8Error(-5, m), "a kernel's bounded wait gave up; its outputs are incomplete"),
+    (STATUS_OFFSETS, ValueError,
+     "fp8_wgrad_experts: offsets that are no multiples of 128; those experts' gradients are NaN"),
+    (STATUS_NONFINITE, Fp8NumericsError, "a scale update met a non-finite amax (NaN or Inf in a cast "
+                                         "tensor or its amax history); the previous scale was kept"),
+)
+
+
 def check_device_status() -> None:
     """Synchronise the device, read and clear the status word, and raise if a
     kernel reported a problem since the last read: Fp8Error with status
     FP8_ERR_TIMEOUT when a bounded wait gave up (that call's outputs are
-    incomplete), ValueError when fp8_wgrad_experts met offsets that are no
+    incomplete), else ValueError when fp8_wgrad_experts met offsets that are no
     multiples of 128 (those experts' gradients are NaN), else Fp8NumericsError
-    when a scale update met a NaN or Inf (the previous scale was kept)."""
+    when a scale update met a NaN or Inf (the previous scale was kept).  Where
+    several were reported the exception is the first one's and its message names
+    all; its device_status is the word that was read."""
     st = fp8_device_status(clear=True)
-    if st & STATUS_TIMEOUT:
-        raise Fp8Error(-5, "a kernel's bounded wait gave up; its outputs are incomplete")
-    if st & STATUS_OFFSETS:
-        raise ValueError("fp8_wgrad_experts: offsets that are no multiples of 128; those experts' gradients are NaN")
-    if st & STATUS_NONFINITE:
-        raise Fp8NumericsError("a scale update met a non-finite amax (NaN or Inf in a cast "
-                               "tensor or its amax history); the previous scale was kept")
+    met = [(error, says) for bit, error, says in _REPORTS if st & bit]
+    if met:
+        e = met[0][0]("; also: ".join(says for _, says in met))
+        e.device_status = st
+        raise e
 
 
 # ------------------------------------------------------------- layer object
@@ -486,9 +496,10 @@ class Fp8Linear:
     codes for K-major backward GEMMs; by default (False) the backward reads
     the codes as stored (MN-major) and no copy is made.  The block-wise and
     per-row recipes always keep them (their transposed codes differ).
-    check_status: after every forward / backward, synchronise and raise
-    (check_device_status) if a kernel timed out or a scale update met a
-    non-finite amax -- off by default, since it waits for the device."""
+    check_status: after every forward / backward, synchronise and raise what
+    check_device_status raises, above all if a kernel timed out or a scale
+    update met a non-finite amax -- off by default, since it waits for the
+    device."""
 
     def __init__(self, M: int, N: int, K: int, recipe: Recipe | None = None, device="cuda",
                  sr_seed: int = 0, transposes: bool = False, check_status: bool = False):
