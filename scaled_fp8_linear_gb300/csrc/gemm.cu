@@ -149,7 +149,7 @@ __device__ __forceinline__ void tile_coords_g(int tile, int num_m, int num_n, in
     n_blk = in_g / gsize;
 }
 
-// The tile of unit u.  m_tile and n_tile: its rows and columns.
+// The tile of unit u: 256 rows by n_tile columns.
 template <int MODE>
 __device__ __forceinline__ BlockTile block_tile(int u, const Units* units, const GemmParams& p, int n_tile) {
     BlockTile t;
@@ -1482,15 +1482,17 @@ __device__ __forceinline__ void promote_tokens(uint8_t* slots, uint32_t cols, ui
 // factors.
 //   warp 0      TMA producer; warp 1 MMA issuer (even CTA); warp 2 TMEM;
 //   warp 3      factors; warps 4-19 promotion, 32 rows x 64 columns each.
-// What bounds it is the way of a buffer: MMA issue, completion (some 1000 cycles
-// for four MMAs that take 512), promotion (700) and the arrivals back (330) are
-// 2200 cycles for two K blocks in flight, and TMEM holds no third 256-column
-// buffer: products of 32 experts of 4096 x 4096 over 32768 rows take 570 us, 538
-// without promotion and with a quarter of the MMAs.  So the issue itself counts: by
+// What bounds it is not established.  By rows, a K block takes a pair some 1200
+// cycles, its MMAs 512.  Two K blocks are in flight (TMEM holds no third 256-column
+// buffer), and a buffer's way is long: issue to completion some 1000 cycles,
+// promotion 700, the arrivals back 330.  But products of 32 experts of 4096 x 4096
+// over 32768 rows take 570 us with all of it and 538 without promotion and with a
+// quarter of the MMAs, so neither is most of it; nor are the operands alone, which
+// the power-of-two kernel takes at 3030 TFLOP/s.  The issue counts: by
 // rows, the whole warp runs the issue loop, so that the operands' descriptors
 // are uniform, and an elected lane issues (570 against 584 us with one lane); by
-// tokens, whose promotion is longer, one lane leaves the schedulers more (876
-// against 935).  Tried besides: each CTA its own MMAs, B by multicast (589: no
+// tokens, where a K block takes some 2000 cycles, one lane leaves the schedulers more
+// (876 against 935).  Tried besides: each CTA its own MMAs, B by multicast (589: no
 // remote arrivals, but 48 KB a K block instead of 32 into each SM); one arrival a CTA
 // through warp 2 (608); test_wait for try_wait (level); for the weight gradients
 // 128-column tiles and four buffers (949: twice the operands' way for the same FMA work).
@@ -1828,8 +1830,9 @@ constexpr int kMxThreads = (8 + kMxEpiWarps) * 32;
 constexpr int kMxStageA = 4 * 136;   // words per buffer: [word][128 rows + pad]
 constexpr int kMxStageB = 4 * 264;   //                   [word][256 rows + pad]
 constexpr int kMxEpiStage = 2048;     // bytes of output staging per epilogue warp: one box
-// Weight gradients of few tokens are all output (8192 tokens over 64 experts of
-// 2048 x 2048: 1 GB): four boxes a warp and four stages; else one and six.
+// Weight gradients of few tokens are mostly output (8192 tokens over 64 experts of
+// 2048 x 2048: 1 GB, 223-240 us; a plain fill of it 140): four boxes a warp and four
+// stages; else one and six.
 template <int MODE>
 constexpr int kMxBoxes = MODE == kByTokens ? 4 : 1;
 template <int MODE>
@@ -2126,7 +2129,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         // 16-byte piece j of row r at piece j ^ ((r >> 1) & 3).
         const int q = warp & 3, h = (warp - 8) >> 2;
         uint8_t* stg = epi_stage + (warp - 8) * BOXES * kMxEpiStage;
-        uint32_t turn = 0;   // by tokens: the box of the two that is next
+        uint32_t turn = 0;   // by tokens: the box that is next
         const bool f32 = p.out == FP8_OUT_F32;
         const bool add = f32 && p.accumulate;
         float ones[32];   // unit factors: the block scales are applied in the MMA
